@@ -102,7 +102,10 @@ def load():
         if not os.path.exists(path):
             raise RuntimeError(f"libgdn_gb300.so is not built ({path}); run "
                                "`python -c 'import __graft_entry__ as g; g.build()'` first")
-        _LIB = _declare(ctypes.CDLL(path))
+        from . import _mixer
+        lib = _declare(ctypes.CDLL(path))
+        _mixer.declare(lib)
+        _LIB = lib
     return _LIB
 
 

@@ -10,12 +10,15 @@
 #include <string>
 
 #include "../../include/gdn.h"
+#include "api_util.h"
 #include "internal.h"
 
 namespace {
-
 thread_local std::string g_last_error;
 thread_local int g_test_injection = 0;
+}  // namespace
+
+namespace gdn {
 
 gdn_status fail(gdn_status s, const char* fmt, ...) {
     char buf[512];
@@ -36,9 +39,15 @@ gdn_status cuda_fail(cudaError_t e, const char* what) {
     return fail(GDN_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
 }
 
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+}  // namespace gdn
 
-bool dtype_ok(gdn_dtype d) { return d == GDN_F32 || d == GDN_BF16; }
+namespace {
+
+using gdn::aligned;
+using gdn::cuda_fail;
+using gdn::dtype_ok;
+using gdn::fail;
+using gdn::ok;
 
 gdn_status check_chunk(const gdn::ChunkArgs& a, gdn_dtype dtype, gdn_dtype o_dtype, int output_final_state,
                        const char* fn) {

@@ -484,6 +484,166 @@ gdn_status gdn_chunk_bwd_workspace_size(int per_channel, int B, int T, int H, in
 #define GDN_TEST_FWD_ONE_STAGE 3
 gdn_status gdn_test_inject(int what);
 
+/* ======================================================================================
+ * Operators around the delta rule: the sequence-mixing layer's short convolution, the norm
+ * (and rotation) of its query and key heads, and the gated linear recurrence, the diagonal
+ * mixer that layers of the same model use beside it.
+ *
+ * Beyond the conventions above:
+ *   - Inputs that a model cuts out of a wider projection need not be contiguous: their rows
+ *     may lie ld_* (or *_stride) elements apart, each row itself being contiguous.  Outputs
+ *     are contiguous.
+ *   - Gradients of tokens have the type of their tensor (rounded once, to nearest even);
+ *     gradients of parameters are fp32.  All arithmetic is fp32.  Sums over tokens are taken
+ *     in a fixed order, so that a call's results are the same from run to run.
+ *   - cu_seqlens packs sequences as in gdn_chunk_fwd (B must be 1; zero-length sequences are
+ *     allowed; offsets are clamped into [0, T]).
+ *   - A workspace, where a call takes one, follows the rules of gdn_chunk_fwd_ws.
+ *   - T = 0 is allowed: final states are the initial ones and parameter gradients are zero.
+ * ====================================================================================== */
+
+/*
+ * glr_scan_fwd -- gated linear recurrence over whole sequences, per channel c:
+ *
+ *     h_t = a_t h_{t-1} + u_t,   o_t = h_t,
+ *     log a_t = g_t, or -exp(A_log[c]) softplus(g_t + dt_bias[c]) when A_log is given,
+ *     u_t = s_t sigma(i_t) x_t   (sigma(i_t) is 1 without in_gate),
+ *     s_t = sqrt(1 - a_t^2) with normalize (the state keeps the input's variance), else 1.
+ *
+ *   x            [B, T, D]   dtype, rows ld_x apart
+ *   g            [B, T, D]   g_dtype (fp32, or bf16 with bf16 inputs), rows ld_g apart; log a <= 0
+ *                            (-inf forgets everything), or raw logits when A_log is given
+ *   in_gate      [B, T, D]   dtype, rows ld_i apart, or NULL
+ *   A_log, dt_bias  [D] fp32, or NULL; dt_bias needs A_log
+ *   initial_state   [N, D] fp32, or NULL for zeros;  final_state [N, D] fp32, or NULL
+ *   o            [B, T, D]   dtype (output)
+ *   checkpoints  [B, ceil(T / 64), D] fp32, or NULL (output): the state before tokens 0, 64,
+ *                128, ... of every row (of no meaning where such a token starts a sequence), for
+ *                glr_scan_bwd with the same inputs
+ *   workspace    glr_workspace_size(0, ...) bytes
+ * The bounded waits of the kernel are reported by gdn_device_status.
+ */
+gdn_status glr_scan_fwd(const void* x, const void* g, const void* in_gate, const float* A_log, const float* dt_bias,
+                        int normalize, const float* initial_state, float* final_state, const int32_t* cu_seqlens,
+                        int n_seqs, void* o, float* checkpoints, int B, int T, int D, int64_t ld_x, int64_t ld_g,
+                        int64_t ld_i, gdn_dtype dtype, gdn_dtype g_dtype, void* workspace, size_t workspace_bytes,
+                        void* stream);
+
+/*
+ * glr_scan_bwd -- gradients of L = sum <grad_o, o> + sum <grad_final_state, final state> through
+ * glr_scan_fwd, from the forward's inputs.
+ *   grad_o            [B, T, D] dtype;  grad_final_state [N, D] fp32 or NULL (zero)
+ *   checkpoints       those of the forward, or NULL (they are computed again)
+ *   grad_x, grad_in_gate  [B, T, D] dtype;  grad_g [B, T, D] g_dtype (of the raw logits with A_log)
+ *   grad_initial_state    [N, D] fp32, or NULL
+ *   grad_A_log        [D] fp32, required with A_log;  grad_dt_bias [D] fp32 or NULL (needs dt_bias)
+ *   workspace         glr_workspace_size(1, ...) bytes
+ * Where log a = 0 the derivative of s = sqrt(1 - a^2) does not exist; it is taken as 0 there.
+ */
+gdn_status glr_scan_bwd(const void* x, const void* g, const void* in_gate, const float* A_log, const float* dt_bias,
+                        int normalize, const float* initial_state, const void* grad_o, const float* grad_final_state,
+                        const int32_t* cu_seqlens, int n_seqs, const float* checkpoints, void* grad_x, void* grad_g,
+                        void* grad_in_gate, float* grad_initial_state, float* grad_A_log, float* grad_dt_bias, int B,
+                        int T, int D, int64_t ld_x, int64_t ld_g, int64_t ld_i, gdn_dtype dtype, gdn_dtype g_dtype,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of glr_scan_fwd (backward = 0) or glr_scan_bwd; n_seqs is 0 without cu_seqlens. */
+gdn_status glr_workspace_size(int backward, int B, int T, int D, int n_seqs, size_t* bytes);
+
+/*
+ * glr_step -- one decode token of the gated linear recurrence for N sequences.
+ *   x, g, in_gate [N, D] (rows ld_* apart), o [N, D] dtype; state, state_out [N, D] fp32.
+ * state_out may be state (updated in place) or a buffer of its own (state is kept).
+ */
+gdn_status glr_step(const void* x, const void* g, const void* in_gate, const float* A_log, const float* dt_bias,
+                    int normalize, const float* state, float* state_out, void* o, int N, int D, int64_t ld_x,
+                    int64_t ld_g, int64_t ld_i, gdn_dtype dtype, gdn_dtype g_dtype, void* stream);
+
+typedef enum gdn_norm {
+    GDN_NORM_RMS = 0,   /* x / sqrt(mean x^2 + eps) */
+    GDN_NORM_L2 = 1     /* x / sqrt(sum x^2 + eps): the unit-norm queries and keys of the delta rule */
+} gdn_norm;
+
+/*
+ * gdn_qk_norm_fwd -- norm of every query and key head, with the position rotation in the same pass:
+ *     y = weight * x / sqrt(c sum x^2 + eps),   c = 1/d (RMS) or 1 (L2),
+ * then the first rotary_dim channels of y turn by the angles of the token's position p:
+ *     (y_i, y_j) <- (y_i cos - y_j sin, y_j cos + y_i sin),
+ * with (i, j) = (m, m + rotary_dim/2), or (2m, 2m + 1) when interleaved, and cos[p, m], sin[p, m].
+ *   q [n_tokens, H_q, d], k [n_tokens, H_k, d]  dtype, with token and head strides in elements
+ *   q_weight, k_weight   [d] fp32, or NULL (ones)
+ *   eps                  > 0 (a head of zeros stays zero)
+ *   cos, sin             [n_pos, rotary_dim / 2] fp32; not read when rotary_dim is 0
+ *   positions            [n_tokens] int32 device, clamped into [0, n_pos); NULL: the token's index
+ *                        modulo T (sequences of T tokens, T <= n_pos)
+ *   q_out, k_out         contiguous, dtype
+ *   sizes                1 <= d <= 256, rotary_dim even, 0..d
+ */
+gdn_status gdn_qk_norm_fwd(const void* q, const void* k, const float* q_weight, const float* k_weight, gdn_norm norm,
+                           float eps, const float* cos, const float* sin, int n_pos, int rotary_dim, int interleaved,
+                           const int32_t* positions, void* q_out, void* k_out, int64_t n_tokens, int T, int H_q,
+                           int H_k, int d, int64_t q_token_stride, int64_t q_head_stride, int64_t k_token_stride,
+                           int64_t k_head_stride, gdn_dtype dtype, void* stream);
+
+/*
+ * gdn_qk_norm_bwd -- gradients through gdn_qk_norm_fwd, from its inputs and the gradients of its
+ * outputs (contiguous, dtype).  grad_q, grad_k: contiguous, dtype.  grad_q_weight, grad_k_weight:
+ * [d] fp32 sums over tokens and heads, required with their weight.  The rotation table has no gradient.
+ *   workspace  gdn_qk_norm_workspace_size bytes
+ */
+gdn_status gdn_qk_norm_bwd(const void* q, const void* k, const void* grad_q_out, const void* grad_k_out,
+                           const float* q_weight, const float* k_weight, gdn_norm norm, float eps, const float* cos,
+                           const float* sin, int n_pos, int rotary_dim, int interleaved, const int32_t* positions,
+                           void* grad_q, void* grad_k, float* grad_q_weight, float* grad_k_weight, int64_t n_tokens,
+                           int T, int H_q, int H_k, int d, int64_t q_token_stride, int64_t q_head_stride,
+                           int64_t k_token_stride, int64_t k_head_stride, gdn_dtype dtype, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of gdn_qk_norm_bwd. */
+gdn_status gdn_qk_norm_workspace_size(int64_t n_tokens, int H_q, int H_k, int d, size_t* bytes);
+
+typedef enum gdn_activation {
+    GDN_ACT_NONE = 0,
+    GDN_ACT_SILU = 1    /* p sigma(p) */
+} gdn_activation;
+
+/*
+ * gdn_short_conv_fwd -- causal depthwise convolution over W = 2, 3 or 4 tokens, with its activation:
+ *     p_t = bias + sum_j weight[c, j] x_{t - W + 1 + j},   y_t = silu(p_t) or p_t.
+ * Inputs before a sequence's first token are its initial state, or zero.
+ *   x        [B, T, D] dtype, rows ld_x apart;  y [B, T, D] dtype
+ *   weight   [D, W] fp32;  bias [D] fp32 or NULL
+ *   initial_state, final_state  [N, W - 1, D] dtype or NULL: the last W - 1 inputs, oldest first
+ */
+gdn_status gdn_short_conv_fwd(const void* x, const float* weight, const float* bias, gdn_activation activation,
+                              const void* initial_state, void* final_state, const int32_t* cu_seqlens, int n_seqs,
+                              void* y, int B, int T, int D, int W, int64_t ld_x, gdn_dtype dtype, void* stream);
+
+/*
+ * gdn_short_conv_bwd -- gradients through gdn_short_conv_fwd, from its inputs (p is formed again).
+ *   grad_y [B, T, D] dtype;  grad_final_state [N, W - 1, D] dtype or NULL (zero)
+ *   grad_x [B, T, D] dtype;  grad_weight [D, W] fp32;  grad_bias [D] fp32 or NULL (needs bias)
+ *   grad_initial_state [N, W - 1, D] dtype or NULL
+ *   workspace  gdn_short_conv_workspace_size bytes
+ */
+gdn_status gdn_short_conv_bwd(const void* x, const float* weight, const float* bias, gdn_activation activation,
+                              const void* initial_state, const void* grad_y, const void* grad_final_state,
+                              const int32_t* cu_seqlens, int n_seqs, void* grad_x, float* grad_weight,
+                              float* grad_bias, void* grad_initial_state, int B, int T, int D, int W, int64_t ld_x,
+                              gdn_dtype dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of gdn_short_conv_bwd. */
+gdn_status gdn_short_conv_workspace_size(int B, int T, int D, int W, size_t* bytes);
+
+/*
+ * gdn_short_conv_step -- one decode token of the convolution for N sequences.
+ *   x [N, D] (rows ld_x apart), y [N, D]; state, state_out [N, W - 1, D], all dtype.
+ * The state moves up by one token; state_out may be state or a buffer of its own.
+ */
+gdn_status gdn_short_conv_step(const void* x, const float* weight, const float* bias, gdn_activation activation,
+                               const void* state, void* state_out, void* y, int N, int D, int W, int64_t ld_x,
+                               gdn_dtype dtype, void* stream);
+
 /* Message for the calling thread's last non-OK status ("" if none). */
 const char* gdn_last_error(void);
 
