@@ -12,6 +12,7 @@
 #include "../../include/gdn.h"
 #include "api_util.h"
 #include "internal.h"
+#include "mixer.h"
 
 namespace {
 thread_local std::string g_last_error;
@@ -556,7 +557,7 @@ gdn_status gdn_chunk_bwd_workspace_size(int per_channel, int B, int T, int H, in
 
 gdn_status gdn_test_inject(int what) {
     if (what != 0 && what != GDN_TEST_BWD_RECORD_STALL && what != GDN_TEST_FWD_RECORD_STALL &&
-        what != GDN_TEST_FWD_ONE_STAGE)
+        what != GDN_TEST_FWD_ONE_STAGE && what != GDN_TEST_GLR_STALL)
         return fail(GDN_ERR_INVALID_ARG, "gdn_test_inject: unknown injection %d", what);
     g_test_injection = what;
     return ok();
@@ -565,18 +566,21 @@ gdn_status gdn_test_inject(int what) {
 const char* gdn_last_error(void) { return g_last_error.c_str(); }
 
 gdn_status gdn_device_status(int clear) {
-    unsigned tp = 0, gt = 0, bw = 0, d2 = 0;
+    unsigned tp = 0, gt = 0, bw = 0, d2 = 0, lr = 0, lb = 0;
     cudaError_t e = gdn::tp_read_and_clear_status(&tp, clear != 0);
     if (e == cudaSuccess) e = gdn::gt_read_and_clear_status(&gt, clear != 0);
     if (e == cudaSuccess) e = gdn::d256_read_and_clear_status(&d2, clear != 0);
     gt |= d2;   // the scalar-gate forward at either head size
     if (e == cudaSuccess) e = gdn::bwd_read_and_clear_status(&bw, clear != 0);
+    if (e == cudaSuccess) e = gdn::glr_read_and_clear_status(&lr, clear != 0);
+    if (e == cudaSuccess) e = gdn::glr_bwd_read_and_clear_status(&lb, clear != 0);
+    lr |= lb;
     if (e != cudaSuccess) return cuda_fail(e, "gdn_device_status");
     const unsigned nf = gdn::kStatusNonfinite;
-    if (((tp | gt) & ~nf) != 0 || bw != 0)
+    if (((tp | gt) & ~nf) != 0 || bw != 0 || lr != 0)
         return fail(GDN_ERR_TIMEOUT,
                     "gdn_device_status: a kernel gave up a bounded wait (per-channel forward 0x%x, scalar-gate forward "
-                    "0x%x, backward 0x%x)", tp, gt, bw);
+                    "0x%x, backward 0x%x, linear recurrence 0x%x)", tp, gt, bw, lr);
     if (((tp | gt) & nf) != 0)
         return fail(GDN_ERR_NONFINITE,
                     "gdn_device_status: a chunk forward wrote a non-finite value to o or the final state (an fp16 "

@@ -35,10 +35,14 @@ struct GlrArgs {
     int B, T, D;
     int64_t ldx, ldg, ldi;
     int bf16, g_bf16;       // element types: x, gi, o, dO, dx, di; g, dg
+    int test_stall;         // test of the bounded waits: the first tile of every row keeps its map to itself
     __host__ __device__ int N() const { return cu ? n_seqs : B; }
 };
 constexpr int kGlrTile = 64;   // tokens between checkpoints
 size_t glr_workspace_bytes(const GlrArgs& a, bool backward);
+bool glr_vector(const GlrArgs& a, int V);      // rows can be read and written V channels at a time
+cudaError_t glr_read_and_clear_status(unsigned* value, bool clear);
+cudaError_t glr_bwd_read_and_clear_status(unsigned* value, bool clear);
 cudaError_t launch_glr_fwd(const GlrArgs& a, cudaStream_t s);
 cudaError_t launch_glr_bwd(const GlrArgs& a, cudaStream_t s);
 

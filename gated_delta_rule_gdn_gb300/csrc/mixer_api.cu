@@ -7,6 +7,7 @@
 
 #include "../../include/gdn.h"
 #include "api_util.h"
+#include "internal.h"
 #include "mixer.h"
 
 namespace {
@@ -30,6 +31,8 @@ gdn_status check_sizes(const char* fn, int B, int T, int D, const int32_t* cu, i
                     (long long)kMaxRows);
     if ((int64_t)B * (T > 0 ? T : 1) > (int64_t(1) << 37) / D || (cu && (int64_t)n_seqs > (int64_t(1) << 37) / D))
         return fail(GDN_ERR_UNSUPPORTED, "%s: a tensor has more than 2^37 elements", fn);
+    if ((int64_t)B * (T / 64 + 1) > ((int64_t(1) << 31) - 1) / (D / 32 + 1))     // one block per 64 tokens x 32 channels
+        return fail(GDN_ERR_UNSUPPORTED, "%s: B=%d T=%d D=%d needs more than 2^31 blocks", fn, B, T, D);
     if (cu) {
         if (B != 1) return fail(GDN_ERR_INVALID_ARG, "%s: cu_seqlens needs B == 1 (got B=%d)", fn, B);
         if (n_seqs < 1) return fail(GDN_ERR_INVALID_ARG, "%s: cu_seqlens needs n_seqs >= 1 (got %d)", fn, n_seqs);
@@ -202,6 +205,7 @@ gdn_status glr_scan_fwd(const void* x, const void* g, const void* in_gate, const
     Workspace ws;
     GDN_TRY(ws.get(fn, workspace, workspace_bytes, gdn::glr_workspace_bytes(a, false), static_cast<cudaStream_t>(stream)));
     a.ws = ws.ptr;
+    a.test_stall = gdn::take_test_injection(GDN_TEST_GLR_STALL);
     return finish(fn, gdn::launch_glr_fwd(a, ws.s), ws);
 }
 

@@ -482,6 +482,12 @@ gdn_status gdn_chunk_bwd_workspace_size(int per_channel, int B, int T, int H, in
  */
 #define GDN_TEST_FWD_RECORD_STALL 2
 #define GDN_TEST_FWD_ONE_STAGE 3
+/*
+ * GDN_TEST_GLR_STALL: the next glr_scan_fwd keeps the first tile of every row from the tiles after
+ * it, so their bounded waits give up (once, after 2 s; the other blocks then leave at once),
+ * gdn_device_status reports GDN_ERR_TIMEOUT and that call's outputs are unspecified.
+ */
+#define GDN_TEST_GLR_STALL 4
 gdn_status gdn_test_inject(int what);
 
 /* ======================================================================================
