@@ -1,7 +1,8 @@
 // Per-element mathematics of the gated linear recurrence h_t = a_t h_{t-1} + u_t.
 //   log a = g, or -exp(A_log) softplus(g + dt_bias);   u = s sigma(i) x,   s = sqrt(1 - a^2) or 1.
 // Written so that nothing cancels: a and a - 1 come from one polynomial, 1 - a^2 is -(a - 1)(2 + (a - 1)), softplus is
-// max(z, 0) + log1p(exp(-|z|)), and sigma' is formed from exp(-|z|).
+// max(z, 0) + log1p(exp(-|z|)).  The scans spend about as long on these as on their memory traffic, so each is kept to
+// as few instructions as its accuracy allows; the polynomials are minimax fits (Remez exchange) of this file's own.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -9,57 +10,63 @@
 namespace gdn {
 namespace glr {
 
-// a = exp(x) and e = exp(x) - 1.  x = k ln 2 + r, |r| <= ln 2 / 2, with ln 2 split in two parts (Cody and Waite); p =
-// exp(r) - 1 by the series up to r^7 / 7! (the next term is below 2^-25 of p); a = 2^k + 2^k p, e = (2^k - 1) + 2^k p.
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Single-instruction approximations (relative error about 2^-22), flushing what is below 2^-126 to zero, and maxima that
+// keep NaN.
+__device__ __forceinline__ float ex2(float x) { float y; asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x)); return y; }
+__device__ __forceinline__ float rcp(float x) { float y; asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x)); return y; }
+__device__ __forceinline__ float rsq(float x) { float y; asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x)); return y; }
+__device__ __forceinline__ float root(float x) { float y; asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x)); return y; }
+__device__ __forceinline__ float max_nan(float x, float y) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float min_nan(float x, float y) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+    return r;
+}
+
+// a = exp(x) and e = exp(x) - 1 for x <= 88.  x = k ln 2 + r, |r| <= ln 2 / 2, with ln 2 split in two parts (Cody and
+// Waite); p = exp(r) - 1 = r + r^2 Q(r), off by less than 2^-28; a = 2^k + 2^k p, e = (2^k - 1) + 2^k p.
 // Rounding a once matters: a memory of n tokens multiplies a one-sided error of a by n (a decay taken from expf was off
-// by 4e-5 after 10^4 tokens).  Below 2^-125 the decay is 0.
+// by 4e-5 after 10^4 tokens).  Below -88 (where 2^k becomes 0) the decay is exactly 0.
+// x is brought to -88 in place: log a times a gradient that holds a factor a is then 0 there, not NaN.
 struct Decay { float a, e; };
-__device__ __forceinline__ Decay decay(float x) {
-    const float c = x < -87.f ? -87.f : (x > 88.f ? 88.f : x);      // (keeps NaN)
-    const float t = fmaf(c, 1.4426950408889634f, 12582912.f);       // k in the low bits of 1.5 * 2^23 + k
+__device__ __forceinline__ Decay decay(float& x) {
+    x = max_nan(x, -88.f);
+    const float t = fmaf(x, kLog2e, 12582912.f);                    // k in the low bits of 1.5 * 2^23 + k
     const float k = t - 12582912.f;
-    const float r = fmaf(k, 2.1219444e-4f, fmaf(k, -0.693359375f, c));
-    float q = fmaf(r, 1.f / 5040.f, 1.f / 720.f);
-    q = fmaf(q, r, 1.f / 120.f);
-    q = fmaf(q, r, 1.f / 24.f);
-    q = fmaf(q, r, 1.f / 6.f);
+    const float r = fmaf(k, 2.1219444e-4f, fmaf(k, -0.693359375f, x));
+    float q = fmaf(r, 1.3950337e-3f, 8.3688218e-3f);
+    q = fmaf(q, r, 4.1666210e-2f);
+    q = fmaf(q, r, 1.6666520e-1f);
     q = fmaf(q, r, 0.5f);
     const float p = fmaf(r * r, q, r);
     const float sc = __int_as_float((__float_as_int(t) << 23) + 0x3f800000);
-    Decay d;
-    d.a = fmaf(sc, p, sc);
-    d.e = fmaf(sc, p, sc - 1.f);
-    if (x < -87.f) d = {0.f, -1.f};
-    return d;
+    return {fmaf(sc, p, sc), fmaf(sc, p, sc - 1.f)};
 }
 
-// exp(-|z|) carries both softplus and sigma
-struct Tail { float z, q; };
-__device__ __forceinline__ Tail tail(float z) { return {z, expf(-fabsf(z))}; }
+// exp(-|z|) carries both softplus and sigma.  log1p(q) = q P(q) on [0, 1], off by less than 2^-25 of itself.
+__device__ __forceinline__ float tail(float z) { return ex2(fabsf(z) * -kLog2e); }
+__device__ __forceinline__ float softplus(float z, float q) {
+    float s = fmaf(q, 5.3840620e-3f, -3.0110965e-2f);
+    s = fmaf(s, q, 7.9210736e-2f);
+    s = fmaf(s, q, -1.3746622e-1f);
+    s = fmaf(s, q, 1.9145116e-1f);
+    s = fmaf(s, q, -2.4852946e-1f);
+    s = fmaf(s, q, 3.3320343e-1f);
+    s = fmaf(s, q, -4.9999553e-1f);
+    s = fmaf(s, q, 1.f);
+    return fmaf(s, q, fmaxf(z, 0.f));
+}
+__device__ __forceinline__ float sigmoid(float z, float q) { return (z < 0.f ? q : 1.f) * rcp(1.f + q); }
+__device__ __forceinline__ float sigmoid(float z) { return rcp(1.f + ex2(z * -kLog2e)); }
 
-// log1p(q) = 2 atanh(w), w = q / (2 + q) <= 1/3, by the odd series up to w^13 (the next term is below 2^-25 of it)
-__device__ __forceinline__ float softplus(const Tail& t) {
-    const float w = __fdividef(t.q, 2.f + t.q), v = w * w;
-    float s = fmaf(v, 2.f / 13.f, 2.f / 11.f);
-    s = fmaf(s, v, 2.f / 9.f);
-    s = fmaf(s, v, 2.f / 7.f);
-    s = fmaf(s, v, 2.f / 5.f);
-    s = fmaf(s, v, 2.f / 3.f);
-    return fmaxf(t.z, 0.f) + fmaf(w * v, s, 2.f * w);
-}
-__device__ __forceinline__ float sigmoid(const Tail& t) { return __fdividef(t.z < 0.f ? t.q : 1.f, 1.f + t.q); }
-__device__ __forceinline__ float sigmoid_slope(const Tail& t) {
-    const float r = __fdividef(1.f, 1.f + t.q);
-    return t.q * r * r;
-}
-
-__device__ __forceinline__ float root(float x) {
-    float y;
-    asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-// the input factor sqrt(1 - a^2)
-__device__ __forceinline__ float input_factor(const Decay& d) { return root(fmaxf(-d.e * (2.f + d.e), 0.f)); }
+// 1 - a^2 (0 for a decay above 1), the square of the input factor
+__device__ __forceinline__ float input_power(const Decay& d) { return fmaxf(-d.e * (2.f + d.e), 0.f); }
 
 }  // namespace glr
 }  // namespace gdn

@@ -15,169 +15,215 @@ using mix::Vec;
 
 __device__ unsigned g_glr_status;   // bit 0: a block gave up a bounded wait
 
-// one block per tile of 64 tokens x 32 V channels
-template <typename Tx, typename Tg, int V>
-__global__ void __launch_bounds__(kWarps * 32)
-glr_fwd_kernel(const GlrArgs a, const Exchange x, int publish) {
-    constexpr int W = 32 * V;
-    __shared__ float sA[kWarps][W], sH[kWarps][W], s_carry[W];
-    __shared__ int s_start[kTile], s_end[kTile];
-    __shared__ unsigned s_id;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    unsigned id = blockIdx.x;
+template <typename Tx, typename Tg, int LANES, int V, bool PACKED>
+__global__ void __launch_bounds__(kThreads, LANES * V <= 64 ? 3 : 2)
+glr_fwd_kernel(const GlrArgs a, const Exchange x, const int publish) {
+    using At = Place<LANES, V>;
+    constexpr int W = At::W, R = At::kRuns, L = At::L;
+    extern __shared__ __align__(16) unsigned char s_raw[];
+    __shared__ float sA[R][W], sH[R][W];
+    __shared__ int s_start[2][kTile], s_end[2][kTile];
+    __shared__ unsigned s_next;
+    const int tid = threadIdx.x, run = tid / LANES, lane = tid % LANES;
+    auto* bg = reinterpret_cast<Vec<Tg, V>*>(s_raw) + tid;                    // [L][256] each
+    auto* bx = reinterpret_cast<Vec<Tx, V>*>(s_raw + L * kThreads * sizeof(Vec<Tg, V>)) + tid;
+    auto* bi = bx + L * kThreads;
+
+    At at;
+    const auto fetch = [&](int id) {
+        at.set(x, a, id, false);
+        const Tg* g = static_cast<const Tg*>(a.g) + at.row * a.ldg + at.c;
+        const Tx* xp = static_cast<const Tx*>(a.x) + at.row * a.ldx + at.c;
+        const Tx* ip = static_cast<const Tx*>(a.gi) + at.row * a.ldi + at.c;
+        const int n = at.live ? at.count : 0;
+#pragma unroll
+        for (int j = 0; j < L; ++j) {
+            copy_async(bg + j * kThreads, j < n ? g : static_cast<const Tg*>(a.g), j < n);
+            copy_async(bx + j * kThreads, j < n ? xp : static_cast<const Tx*>(a.x), j < n);
+            if (a.gi) copy_async(bi + j * kThreads, j < n ? ip : static_cast<const Tx*>(a.gi), j < n);
+            g += a.ldg;
+            xp += a.ldx;
+            ip += a.ldi;
+        }
+    };
+    unsigned ticket = 0;
+    int id = blockIdx.x;
     if (x.tiles > 1) {
-        if (tid == 0) s_id = atomicAdd(x.ticket, 1u);
+        if (tid == 0) s_next = atomicAdd(x.ticket, 1u) + 1u;
         __syncthreads();
-        id = s_id;
+        id = (int)s_next;
+        if (tid == 0) ticket = atomicAdd(x.ticket, 1u) + 1u;
+        __syncthreads();
     }
-    const int p = id / x.chains, chain = id % x.chains, cols = x.chains / a.B;
-    const int b = chain / cols, c0 = (chain % cols) * W, c = c0 + lane * V;
-    const int t0 = p * kTile + warp * kRun;
-    const bool live = c < a.D;
-    const size_t row0 = (size_t)b * a.T;
+    if (id < x.total) {
+        fetch(id);
+        if (PACKED && tid < kTile) sequence_marks(a, at.p, s_start[0], s_end[0]);
+    }
+    if (PACKED) __syncthreads();
 
-    // the run's inputs
-    Vec<Tg, V> g[kRun];
-    Vec<Tx, V> xv[kRun], gi[kRun];
+    for (int k = 0; id < x.total; k ^= 1) {
+        const At now = at;
+        // which tokens of the run start a sequence
+        unsigned starts = 0;
+        if (PACKED) {
 #pragma unroll
-    for (int j = 0; j < kRun; ++j) {
-        const bool in = live && t0 + j < a.T;
-        if (in) g[j].load(static_cast<const Tg*>(a.g) + (row0 + t0 + j) * a.ldg + c); else g[j].zero();
-        if (in) xv[j].load(static_cast<const Tx*>(a.x) + (row0 + t0 + j) * a.ldx + c); else xv[j].zero();
-        if (a.gi) {
-            if (in) gi[j].load(static_cast<const Tx*>(a.gi) + (row0 + t0 + j) * a.ldi + c); else gi[j].zero();
+            for (int j = 0; j < L; ++j) starts |= (s_start[k][run * L + j] >= 0 ? 1u : 0u) << j;
         }
-    }
-    // packed sequences: the one that starts at each token of the tile, and the one that ends there
-    if (a.cu && tid < kTile) {
-        const int t = p * kTile + tid;
-        int starts = -1, ends = -1;
-        if (t < a.T) {
-            const mix::Span s = mix::span_of(a.cu, a.n_seqs, a.T, t);
-            if (s.first == t) starts = s.n;
-            if (s.end == t + 1) ends = s.n;
-        }
-        s_start[tid] = starts;
-        s_end[tid] = ends;
-    }
-    if (a.cu) __syncthreads();
-    const unsigned starts = a.cu ? __ballot_sync(~0u, lane < kRun && s_start[warp * kRun + (lane & (kRun - 1))] >= 0) : 0;
-
-    float al[kRun][V], u[kRun][V];
+        float al[L][V], u[L][V];
+        copies_done();
 #pragma unroll
-    for (int j = 0; j < kRun; ++j)
+        for (int j = 0; j < L; ++j) {
+            const Vec<Tg, V> g = bg[j * kThreads];
+            const Vec<Tx, V> xv = bx[j * kThreads];
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            al[j][v] = g[j].get(v);
-            u[j][v] = xv[j].get(v);
-        }
-    if (a.A_log) {
-        Channel ch[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) ch[v] = live ? channel(a.A_log, a.dt_bias, c + v) : Channel{0.f, 0.f};
-#pragma unroll
-        for (int j = 0; j < kRun; ++j)
-#pragma unroll
-            for (int v = 0; v < V; ++v) al[j][v] = ch[v].neg_eA * softplus(tail(al[j][v] + ch[v].dt));
-    }
-    if (a.gi) {
-#pragma unroll
-        for (int j = 0; j < kRun; ++j)
-#pragma unroll
-            for (int v = 0; v < V; ++v) u[j][v] *= sigmoid(tail(gi[j].get(v)));
-    }
-#pragma unroll
-    for (int j = 0; j < kRun; ++j)
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const Decay d = decay(al[j][v]);
-            if (a.normalize) u[j][v] *= input_factor(d);
-            al[j][v] = t0 + j < a.T ? d.a : 1.f;         // past the row's end the state stays
-        }
-
-    // the run's map
-    float A[V], H[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        A[v] = 1.f;
-        H[v] = 0.f;
-    }
-#pragma unroll
-    for (int j = 0; j < kRun; ++j) {
-        const bool starts_here = (starts >> j) & 1;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            if (starts_here) {
-                const int n = s_start[warp * kRun + j];
-                if (a.h0 && live) u[j][v] = fmaf(al[j][v], a.h0[(size_t)n * a.D + c + v], u[j][v]);
-                H[v] = u[j][v];
-            } else {
-                H[v] = fmaf(al[j][v], H[v], u[j][v]);
-                A[v] *= al[j][v];
+            for (int v = 0; v < V; ++v) {
+                al[j][v] = g.get(v);
+                u[j][v] = xv.get(v);
             }
         }
-    }
+        if (a.gi) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        sA[warp][lane * V + v] = starts ? -1.f : A[v];
-        sH[warp][lane * V + v] = H[v];
-    }
-    __syncthreads();
-
-    // the tile's map, and the state that enters it
-    float tA = 1.f, tH = 0.f, first = 0.f;
-    if (tid < W) {
+            for (int j = 0; j < L; ++j) {
+                const Vec<Tx, V> gi = bi[j * kThreads];
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            tH = apply(sA[w][tid], sH[w][tid], tH);
-            tA = both(tA, sA[w][tid]);
+                for (int v = 0; v < V; ++v) u[j][v] *= sigmoid(gi.get(v));
+            }
         }
-        if (p < kGroup && !a.cu && a.h0 && c0 + tid < a.D) first = a.h0[(size_t)b * a.D + c0 + tid];
-    }
-    const float carry = carry_in(x, W, p, chain, tA, tH, first, publish || p > 0, &g_glr_status);
-    if (tid < W) {
-        s_carry[tid] = carry;
-        if (a.ckpt && c0 + tid < a.D && p * kTile < a.T)
-            a.ckpt[((size_t)b * x.tiles + p) * a.D + c0 + tid] = carry;
-    }
-    __syncthreads();
+        if (a.A_log) {
+            Channel ch[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) ch[v] = now.live ? channel(a.A_log, a.dt_bias, now.c + v) : Channel{0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < L; ++j)
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    const float z = al[j][v] + ch[v].dt;
+                    al[j][v] = ch[v].neg_eA * softplus(z, tail(z));
+                }
+        } else {
+#pragma unroll
+            for (int j = 0; j < L; ++j)
+#pragma unroll
+                for (int v = 0; v < V; ++v) al[j][v] = min_nan(al[j][v], 88.f);
+        }
+#pragma unroll
+        for (int j = 0; j < L; ++j)
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const Decay d = decay(al[j][v]);
+                if (a.normalize) u[j][v] *= root(input_power(d));
+                al[j][v] = d.a;
+            }
+        if (now.count < L) {                     // past the row's end the state stays
+#pragma unroll
+            for (int j = 0; j < L; ++j)
+#pragma unroll
+                for (int v = 0; v < V; ++v) al[j][v] = j < now.count ? al[j][v] : 1.f;
+        }
 
-    // the states
-    float h[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) h[v] = s_carry[lane * V + v];
-    for (int w = 0; w < warp; ++w)
-#pragma unroll
-        for (int v = 0; v < V; ++v) h[v] = apply(sA[w][lane * V + v], sH[w][lane * V + v], h[v]);
-#pragma unroll
-    for (int j = 0; j < kRun; ++j) {
-        const bool starts_here = (starts >> j) & 1;
-        Vec<Tx, V> o;
+        // the run's map
+        float A[V], H[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            h[v] = starts_here ? u[j][v] : fmaf(al[j][v], h[v], u[j][v]);
-            o.set(v, h[v]);
+            A[v] = al[0][v];
+            H[v] = u[0][v];
         }
-        if (a.o && live && t0 + j < a.T) o.store(static_cast<Tx*>(a.o) + (row0 + t0 + j) * a.D + c);
-        if (a.cu && a.hT && live) {
-            const int n = s_end[warp * kRun + j];
-            if (n >= 0)
+        if (PACKED && starts) {
 #pragma unroll
-                for (int v = 0; v < V; ++v) a.hT[(size_t)n * a.D + c + v] = h[v];
+            for (int j = 0; j < L; ++j) {
+                const bool here = (starts >> j) & 1;
+                if (here && a.h0 && now.live) {
+                    const float* h0 = a.h0 + (size_t)s_start[k][run * L + j] * a.D + now.c;
+#pragma unroll
+                    for (int v = 0; v < V; ++v) u[j][v] = fmaf(al[j][v], h0[v], u[j][v]);
+                }
+#pragma unroll
+                for (int v = 0; v < V; ++v) H[v] = here || j == 0 ? u[j][v] : fmaf(al[j][v], H[v], u[j][v]);
+            }
+#pragma unroll
+            for (int v = 0; v < V; ++v) A[v] = -1.f;
+        } else {
+#pragma unroll
+            for (int j = 1; j < L; ++j)
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    H[v] = fmaf(al[j][v], H[v], u[j][v]);
+                    A[v] *= al[j][v];
+                }
         }
-    }
-    if (!a.hT || !live) return;
-    if (!a.cu) {
-        if (p == x.tiles - 1 && warp == kWarps - 1)
 #pragma unroll
-            for (int v = 0; v < V; ++v) a.hT[(size_t)b * a.D + c + v] = h[v];
-    } else {
-        // empty sequences end as they began; the row's tiles share them
-        for (int n = p * kWarps + warp; n < a.n_seqs; n += x.tiles * kWarps) {
-            if (mix::clamp_off(a.cu[n + 1], a.T) > mix::clamp_off(a.cu[n], a.T)) continue;
-#pragma unroll
-            for (int v = 0; v < V; ++v) a.hT[(size_t)n * a.D + c + v] = a.h0 ? a.h0[(size_t)n * a.D + c + v] : 0.f;
+        for (int v = 0; v < V; ++v) {
+            sA[run][lane * V + v] = A[v];
+            sH[run][lane * V + v] = H[v];
         }
+        if (x.tiles > 1) {
+            if (tid == 0) s_next = ticket;
+        }
+        __syncthreads();
+        const int next = x.tiles > 1 ? (int)s_next : id + (int)gridDim.x;
+        if (next < x.total) {                    // the buffer is free: the next tile's inputs on the way
+            fetch(next);
+            if (PACKED && tid < kTile) sequence_marks(a, at.p, s_start[k ^ 1], s_end[k ^ 1]);
+            if (x.tiles > 1 && tid == 0) ticket = atomicAdd(x.ticket, 1u) + 1u;
+        }
+
+        // the state that enters the tile, and each of its runs
+        if (tid < W) {
+            const int c = now.c0 + tid;
+            float tA = 1.f, tH = 0.f, h = 0.f;
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                tH = apply(sA[r][tid], sH[r][tid], tH);
+                tA = both(tA, sA[r][tid]);
+            }
+            if (!PACKED && now.p < kGroup && a.h0 && c < a.D) h = a.h0[(size_t)now.b * a.D + c];
+            h = carry_in(x, W, now.p, now.chain, tid, tA, tH, h, publish || now.p > 0, &g_glr_status);
+            if (a.ckpt && c < a.D && now.p * kTile < a.T) a.ckpt[((size_t)now.b * x.tiles + now.p) * a.D + c] = h;
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const float H = sH[r][tid];
+                sH[r][tid] = h;
+                h = apply(sA[r][tid], H, h);
+            }
+        }
+        __syncthreads();
+
+        float h[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) h[v] = sH[run][lane * V + v];
+        Tx* op = static_cast<Tx*>(a.o) + now.row * a.D + now.c;
+        const int n = now.live && a.o ? now.count : 0;
+#pragma unroll
+        for (int j = 0; j < L; ++j) {
+            Vec<Tx, V> o;
+            const bool here = PACKED && ((starts >> j) & 1);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                h[v] = here ? u[j][v] : fmaf(al[j][v], h[v], u[j][v]);
+                o.set(v, h[v]);
+            }
+            if (j < n) o.store(op);
+            op += a.D;
+            if (PACKED && a.hT && now.live) {
+                const int m = s_end[k][run * L + j];
+                if (m >= 0)
+#pragma unroll
+                    for (int v = 0; v < V; ++v) a.hT[(size_t)m * a.D + now.c + v] = h[v];
+            }
+        }
+        if (!PACKED && a.hT && now.live && now.p == x.tiles - 1 && run == R - 1)
+#pragma unroll
+            for (int v = 0; v < V; ++v) a.hT[(size_t)now.b * a.D + now.c + v] = h[v];
+        if (PACKED && a.hT && now.live) {
+            // empty sequences end as they began; the row's tiles share them
+            for (int m = now.p * R + run; m < a.n_seqs; m += x.tiles * R) {
+                if (mix::clamp_off(a.cu[m + 1], a.T) > mix::clamp_off(a.cu[m], a.T)) continue;
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    a.hT[(size_t)m * a.D + now.c + v] = a.h0 ? a.h0[(size_t)m * a.D + now.c + v] : 0.f;
+            }
+        }
+        id = next;
     }
 }
 
@@ -189,35 +235,60 @@ __global__ void glr_step_kernel(const GlrStepArgs a) {
     if (n >= a.N) return;
     const float g = mix::ld(static_cast<const Tg*>(a.g) + n * a.ldg + c);
     const Channel ch = channel(a.A_log, a.dt_bias, c);
-    const Decay d = decay(a.A_log ? ch.neg_eA * softplus(tail(g + ch.dt)) : g);
+    float la = a.A_log ? ch.neg_eA * softplus(g + ch.dt, tail(g + ch.dt)) : min_nan(g, 88.f);
+    const Decay d = decay(la);
     float u = mix::ld(static_cast<const Tx*>(a.x) + n * a.ldx + c);
-    if (a.normalize) u *= input_factor(d);
-    if (a.gi) u *= sigmoid(tail(mix::ld(static_cast<const Tx*>(a.gi) + n * a.ldi + c)));
+    if (a.normalize) u *= root(input_power(d));
+    if (a.gi) u *= sigmoid(mix::ld(static_cast<const Tx*>(a.gi) + n * a.ldi + c));
     const float h = fmaf(d.a, a.h[n * a.D + c], u);
     a.h_out[n * a.D + c] = h;
     mix::st(static_cast<Tx*>(a.o) + n * a.D + c, h);
 }
 
-template <typename Tx, typename Tg, int V>
-cudaError_t fwd(const GlrArgs& a, bool stall, cudaStream_t s) {
-    const Layout l = layout(a.B, a.T, a.D, 32 * V);
+template <typename Tx, typename Tg, int LANES, int V, bool PACKED>
+cudaError_t fwd(const GlrArgs& a, cudaStream_t s) {
+    using At = Place<LANES, V>;
+    const Layout l = layout(a.B, a.T, a.D, At::W);
     const Exchange x = exchange(l, a.ws);
-    if (l.flag_bytes) {
-        const cudaError_t e = cudaMemsetAsync(a.ws, 0, l.flag_bytes, s);
+    if (l.bytes) {
+        const cudaError_t e = cudaMemsetAsync(a.ws, 0xff, l.bytes, s);
         if (e != cudaSuccess) return e;
     }
-    glr_fwd_kernel<Tx, Tg, V><<<(unsigned)l.tiles * l.chains, kWarps * 32, 0, s>>>(a, x, stall ? 0 : 1);
+    const auto kernel = glr_fwd_kernel<Tx, Tg, LANES, V, PACKED>;
+    const size_t smem = (size_t)At::L * kThreads * V * (sizeof(Tg) + 2 * sizeof(Tx));
+    static const Residency res = residency(reinterpret_cast<const void*>(kernel), smem);
+    if (res.error != cudaSuccess) return res.error;
+    kernel<<<x.total < res.blocks ? x.total : res.blocks, kThreads, smem, s>>>(a, x, a.test_stall ? 0 : 1);
     return cudaGetLastError();
 }
 
+template <typename Tx, typename Tg, int LANES, int V>
+cudaError_t fwd_packed(const GlrArgs& a, cudaStream_t s) {
+    return a.cu ? fwd<Tx, Tg, LANES, V, true>(a, s) : fwd<Tx, Tg, LANES, V, false>(a, s);
+}
+
 template <typename Tx, typename Tg>
-cudaError_t fwd_wide(const GlrArgs& a, bool stall, cudaStream_t s) {
-    if (glr_vector(a, 4)) return fwd<Tx, Tg, 4>(a, stall, s);
-    if (glr_vector(a, 2)) return fwd<Tx, Tg, 2>(a, stall, s);
-    return fwd<Tx, Tg, 1>(a, stall, s);
+cudaError_t fwd_wide(const GlrArgs& a, cudaStream_t s) {
+    if (glr_vector(a, 4)) return fwd_packed<Tx, Tg, 16, 4>(a, s);
+    if (glr_vector(a, 2)) return fwd_packed<Tx, Tg, 32, 2>(a, s);
+    return fwd_packed<Tx, Tg, 32, 1>(a, s);
 }
 
 }  // namespace
+
+// Blocks that are resident at once on the whole device (persistent kernels launch no more).
+namespace glr {
+Residency residency(const void* kernel, size_t smem) {
+    Residency r{cudaSuccess, 0};
+    int dev = 0, sms = 0, per = 0;
+    r.error = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (r.error == cudaSuccess) r.error = cudaGetDevice(&dev);
+    if (r.error == cudaSuccess) r.error = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (r.error == cudaSuccess) r.error = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, kThreads, smem);
+    r.blocks = sms * (per > 0 ? per : 1);
+    return r;
+}
+}  // namespace glr
 
 // Whether rows can be read and written V channels at a time.
 bool glr_vector(const GlrArgs& a, int V) {
@@ -228,9 +299,8 @@ bool glr_vector(const GlrArgs& a, int V) {
 }
 
 cudaError_t launch_glr_fwd(const GlrArgs& a, cudaStream_t s) {
-    const bool stall = a.test_stall;
-    if (!a.bf16) return fwd_wide<float, float>(a, stall, s);
-    return a.g_bf16 ? fwd_wide<bf16, bf16>(a, stall, s) : fwd_wide<bf16, float>(a, stall, s);
+    if (!a.bf16) return fwd_wide<float, float>(a, s);
+    return a.g_bf16 ? fwd_wide<bf16, bf16>(a, s) : fwd_wide<bf16, float>(a, s);
 }
 
 cudaError_t launch_glr_step(const GlrStepArgs& a, cudaStream_t s) {

@@ -1,17 +1,21 @@
-// Shared parts of the gated linear recurrence's scans (glr_scan.cu, glr_scan_bwd.cu): the tiling, and the carry of a
-// tile from the tiles before it.
+// Shared parts of the gated linear recurrence's scans (glr_scan.cu, glr_scan_bwd.cu): the tiling, the input buffer, and
+// the carry of a tile from the tiles before it.
 //
-// A row of T tokens is cut into tiles of 64 tokens x 32 V channels, a block each; a warp takes 8 consecutive tokens of
-// the tile, a lane V channels, and holds them in registers.  The recurrence over a run of tokens is the map
-// h -> A h + H; a run in which a sequence starts (backward: ends) forgets h altogether, which is written A = -1 (decays
-// are never negative), so that a state that is not a number stays in its own sequence.
+// A row of T tokens is cut into tiles of 64 tokens x W = LANES * V channels.  A block of 256 threads takes one tile after
+// another; LANES threads side by side read V channels each, and so the block has 256 / LANES runs of LANES / 4 consecutive
+// tokens, each held in the registers of its threads.  The recurrence over a run of tokens is the map h -> A h + H; a run
+// in which a sequence starts (backward: ends) forgets h altogether, which is written A = -1 (decays are never negative),
+// so that a state that is not a number stays in its own sequence.
 //
 // The carry into tile p (in scan order) is, in a fixed association whatever the timing, so that results do not change
 // from run to run:
 //   the state at the start of its group of kGroup tiles, then the maps of the group's tiles before it, composed first.
 // A tile publishes its map as soon as it has it; the last of a group publishes the next group's starting state.  So the
-// serial chain of a row is T / (64 kGroup) hops, and each byte of the inputs is read once.  Tiles take tickets in scan
-// order, so every tile that a block waits for has been started before it; waits are bounded all the same.
+// serial chain of a row is T / (64 kGroup) hops, and each byte of the inputs is read once.  A map is one 8-byte word and a
+// state one 4-byte word, which are their own flags: the workspace starts as all ones, which no published word is.
+// Blocks take tickets for tiles in scan order, one ahead, to have the next tile's inputs on the way while the carry of the
+// current one is worked out.  The smallest tile that is not done is always the current one of its block, so waiting ends;
+// waits are bounded all the same.
 #pragma once
 
 #include "glr_math.cuh"
@@ -21,138 +25,177 @@
 namespace gdn {
 namespace glr {
 
-constexpr int kWarps = 8, kRun = 8;              // a warp's run of tokens
-constexpr int kTile = kWarps * kRun;
-static_assert(kTile == kGlrTile, "checkpoints are tile entries");
+constexpr int kThreads = 256;
+constexpr int kTile = kGlrTile;                  // checkpoints are tile entries
 constexpr int kGroup = 16;
+constexpr unsigned kEmpty = 0xffffffffu;
 constexpr unsigned long long kWaitNs = 2000000000ull;
 
-// Workspace of one scan: [ticket, gave-up flag, map flags [chains][tiles], state flags [chains][groups]] zeroed before
-// the launch, then the maps and the states.
+struct Residency { cudaError_t error; int blocks; };
+Residency residency(const void* kernel, size_t smem);
+
+// Workspace of one scan, set to all ones before the launch.
 struct Exchange {
-    unsigned* ticket;
-    unsigned* gave_up;
-    unsigned* map_flag;
-    unsigned* state_flag;
-    float2* map;            // [tiles][chains][width]
-    float* state;           // [groups][chains][width]
-    int tiles, groups, chains;
+    unsigned* ticket;       // the last ticket taken (all ones: none)
+    unsigned* gave_up;      // 0 once a block gave up a wait
+    unsigned long long* map;    // [tiles][chains][W]: A in the low half, H in the high half
+    unsigned* state;        // [groups][chains][W]
+    int tiles, chains, total;
 };
 
 struct Layout {
-    size_t flag_bytes, map_off, state_off, bytes;
-    int tiles, groups, chains;
+    size_t state_off, bytes;
+    int tiles, chains;
 };
 inline Layout layout(int B, int T, int D, int width) {
     Layout l;
     l.tiles = T > kTile ? (T + kTile - 1) / kTile : 1;
-    l.groups = (l.tiles + kGroup - 1) / kGroup;
     l.chains = B * ((D + width - 1) / width);
     if (l.tiles == 1) {                          // nothing to exchange
-        l.flag_bytes = l.map_off = l.state_off = l.bytes = 0;
+        l.state_off = l.bytes = 0;
         return l;
     }
-    const auto up = [](size_t v) { return (v + 255) / 256 * 256; };
-    l.flag_bytes = up((2 + (size_t)l.chains * (l.tiles + l.groups)) * sizeof(unsigned));
-    l.map_off = l.flag_bytes;
-    l.state_off = up(l.map_off + (size_t)l.tiles * l.chains * width * sizeof(float2));
-    l.bytes = up(l.state_off + (size_t)l.groups * l.chains * width * sizeof(float));
+    const size_t groups = (l.tiles + kGroup - 1) / kGroup, row = (size_t)l.chains * width;
+    l.state_off = 256 + l.tiles * row * sizeof(unsigned long long);
+    l.bytes = (l.state_off + groups * row * sizeof(unsigned) + 255) / 256 * 256;
     return l;
 }
 inline Exchange exchange(const Layout& l, void* ws) {
     Exchange x{};
     char* p = static_cast<char*>(ws);
-    x.tiles = l.tiles; x.groups = l.groups; x.chains = l.chains;
+    x.tiles = l.tiles;
+    x.chains = l.chains;
+    x.total = l.tiles * l.chains;
     if (l.tiles == 1) return x;
     x.ticket = reinterpret_cast<unsigned*>(p);
     x.gave_up = x.ticket + 1;
-    x.map_flag = x.ticket + 2;
-    x.state_flag = x.map_flag + (size_t)l.chains * l.tiles;
-    x.map = reinterpret_cast<float2*>(p + l.map_off);
-    x.state = reinterpret_cast<float*>(p + l.state_off);
+    x.map = reinterpret_cast<unsigned long long*>(p + 256);
+    x.state = reinterpret_cast<unsigned*>(p + l.state_off);
     return x;
 }
 
 __device__ __forceinline__ float apply(float A, float H, float h) { return A < 0.f ? H : fmaf(A, h, H); }
 __device__ __forceinline__ float both(float A1, float A2) { return A1 < 0.f || A2 < 0.f ? -1.f : A1 * A2; }
 
-__device__ __forceinline__ unsigned load_acquire(const unsigned* p) {
-    unsigned v;
-    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+__device__ __forceinline__ unsigned long long load_word(const unsigned long long* p) {
+    unsigned long long v;
+    asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
     return v;
 }
-__device__ __forceinline__ void store_release(unsigned* p, unsigned v) {
-    asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+__device__ __forceinline__ unsigned load_word(const unsigned* p) {
+    unsigned v;
+    asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
 }
-// Wait until *p is set.  Gives up after kWaitNs, or soon after another block has; the call's outputs are then
-// unspecified and *status says so.
-__device__ __forceinline__ void wait_flag(const unsigned* p, unsigned* gave_up, unsigned* status) {
-    if (load_acquire(p)) return;
-    unsigned long long t0, t;
-    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t0));
-    while (true) {
-        for (int i = 0; i < 64; ++i)
-            if (load_acquire(p)) return;
-        asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
-        if (t - t0 > kWaitNs || load_acquire(gave_up)) {
-            atomicExch(gave_up, 1u);
-            atomicOr(status, 1u);
-            return;
-        }
-    }
+__device__ __forceinline__ void store_word(unsigned long long* p, unsigned long long v) {
+    asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(p), "l"(v) : "memory");
+}
+__device__ __forceinline__ void store_word(unsigned* p, unsigned v) {
+    asm volatile("st.relaxed.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+__device__ __forceinline__ unsigned full(float v) {           // a float's bits, which are never kEmpty
+    const unsigned b = __float_as_uint(v);
+    return b == kEmpty ? 0x7fffffffu : b;
 }
 
-// The carry into tile p of a chain.  Called by the whole block; threads below `width` pass their channel's map (A, H)
-// of the tile and the state `first` before tile 0 of the row, and get the carry.
-__device__ __forceinline__ float carry_in(const Exchange& x, int width, int p, int chain, float A, float H, float first,
-                                          bool publish, unsigned* status) {
-    const int tid = threadIdx.x, start = p / kGroup * kGroup, group = p / kGroup;
-    const bool more = p + 1 < x.tiles, closes = more && p + 1 == start + kGroup;
-    const size_t at = (size_t)chain * width + tid, row = (size_t)x.chains * width;
-    if (more && !closes) {
-        if (tid < width) __stcg(&x.map[p * row + at], make_float2(A, H));
-        __syncthreads();
-        if (tid == 0 && publish) {
-            __threadfence();
-            store_release(&x.map_flag[(size_t)chain * x.tiles + p], 1u);
-        }
-    }
-    float cA = 1.f, cH = 0.f;
-    if (p > start) {
-        if (tid < p - start) wait_flag(&x.map_flag[(size_t)chain * x.tiles + start + tid], x.gave_up, status);
-        __syncthreads();
-        if (tid < width) {
-            float2 m[kGroup - 1];
+// The carry into tile p of a chain, for one channel: called by the W threads that have the channels' maps (A, H) of the
+// tile and the state `first` before tile 0 of the row.
+__device__ __forceinline__ float carry_in(const Exchange& x, int W, int p, int chain, int ch, float A, float H,
+                                          float first, bool publish, unsigned* status) {
+    const int group = p / kGroup, start = group * kGroup, n = p - start;
+    const bool more = p + 1 < x.tiles, closes = more && n + 1 == kGroup;
+    const size_t row = (size_t)x.chains * W, at = (size_t)chain * W + ch;
+    if (more && !closes && publish) store_word(x.map + p * row + at, (unsigned long long)full(H) << 32 | full(A));
+    if (p == 0) return first;
+    unsigned long long m[kGroup - 1];
+    unsigned st = group > 0 ? kEmpty : 0u;
 #pragma unroll
-            for (int j = 0; j < kGroup - 1; ++j)
-                m[j] = start + j < p ? __ldcg(&x.map[(start + j) * row + at]) : make_float2(1.f, 0.f);
+    for (int j = 0; j < kGroup - 1; ++j) m[j] = j < n ? ~0ull : 0x3f800000ull;       // (the identity: A = 1, H = 0)
+    unsigned long long t0 = 0;
+    for (int round = 0;; ++round) {
+        bool ok = true;
+        if (st == kEmpty) st = load_word(x.state + group * row + at);
 #pragma unroll
-            for (int j = 0; j < kGroup - 1; ++j) {
-                cH = apply(m[j].x, m[j].y, cH);
-                cA = both(cA, m[j].x);
+        for (int j = 0; j < kGroup - 1; ++j)
+            if ((unsigned)m[j] == kEmpty) m[j] = load_word(x.map + (start + j) * row + at);
+#pragma unroll
+        for (int j = 0; j < kGroup - 1; ++j) ok = ok && (unsigned)m[j] != kEmpty;
+        if (ok && st != kEmpty) break;
+        if ((round & 63) == 63) {
+            unsigned long long t;
+            asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+            if (t0 == 0) t0 = t;
+            if (t - t0 > kWaitNs || load_word(x.gave_up) == 0u) {
+                store_word(x.gave_up, 0u);
+                atomicOr(status, 1u);
+                break;                            // the outputs are now unspecified
             }
         }
     }
-    if (group > 0) {
-        if (tid == 0) wait_flag(&x.state_flag[(size_t)chain * x.groups + group], x.gave_up, status);
-        __syncthreads();
-        if (tid < width) first = __ldcg(&x.state[group * row + at]);
+    float cA = 1.f, cH = 0.f;
+#pragma unroll
+    for (int j = 0; j < kGroup - 1; ++j) {
+        const float a = __uint_as_float((unsigned)m[j]), h = __uint_as_float((unsigned)(m[j] >> 32));
+        cH = apply(a, h, cH);
+        cA = both(cA, a);
     }
-    const float carry = apply(cA, cH, first);
-    if (closes) {
-        if (tid < width) __stcg(&x.state[(group + 1) * row + at], apply(A, H, carry));
-        __syncthreads();
-        if (tid == 0 && publish) {
-            __threadfence();
-            store_release(&x.state_flag[(size_t)chain * x.groups + group + 1], 1u);
-        }
-    }
+    const float carry = apply(cA, cH, group > 0 ? __uint_as_float(st) : first);
+    if (closes && publish) store_word(x.state + (group + 1) * row + at, full(apply(A, H, carry)));
     return carry;
 }
 
 struct Channel { float neg_eA, dt; };   // -exp(A_log) (0: g is log a) and dt_bias of a channel
 __device__ __forceinline__ Channel channel(const float* A_log, const float* dt_bias, int c) {
     return {A_log ? -expf(A_log[c]) : 0.f, dt_bias ? dt_bias[c] : 0.f};
+}
+
+// Copy V elements into shared memory without waiting (or zeros); the copying thread alone reads them.
+template <typename T, int V>
+__device__ __forceinline__ void copy_async(mix::Vec<T, V>* dst, const T* src, bool in) {
+    constexpr int N = sizeof(T) * V;
+    if constexpr (N >= 4) {
+        const unsigned d = static_cast<unsigned>(__cvta_generic_to_shared(dst));
+        const int size = in ? N : 0;
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(d), "l"(src), "n"(N), "r"(size) : "memory");
+    } else {                                     // (two bytes: no asynchronous form)
+        if (in) dst->load(src); else dst->zero();
+    }
+}
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// A block's place in its current tile.
+template <int LANES, int V>
+struct Place {
+    static constexpr int W = LANES * V, kRuns = kThreads / LANES, L = kTile / kRuns;
+    int p, chain, b, c0, c, t0;      // tile in the row, chain, batch row, the block's and the thread's first channel,
+    int count;                       // the run's first token, and its tokens inside the row
+    bool live;                       // the thread's channels exist
+    size_t row;                      // the run's first row in [B T]
+    __device__ __forceinline__ void set(const Exchange& x, const GlrArgs& a, int id, bool reverse) {
+        const int q = id / x.chains, cols = x.chains / a.B;
+        chain = id - q * x.chains;
+        p = reverse ? x.tiles - 1 - q : q;
+        b = chain / cols;
+        c0 = (chain - b * cols) * W;
+        c = c0 + (int)(threadIdx.x % LANES) * V;
+        t0 = p * kTile + (int)(threadIdx.x / LANES) * L;
+        live = c < a.D;
+        count = min(max(a.T - t0, 0), L);
+        row = (size_t)b * a.T + t0;
+    }
+};
+
+// Packed sequences: which one starts, and which ends, at each token of tile p (-1: none).  Called by threads 0..63.
+__device__ __forceinline__ void sequence_marks(const GlrArgs& a, int p, int* starts, int* ends) {
+    const int t = p * kTile + threadIdx.x;
+    int s = -1, e = -1;
+    if (t < a.T) {
+        const mix::Span sp = mix::span_of(a.cu, a.n_seqs, a.T, t);
+        if (sp.first == t) s = sp.n;
+        if (sp.end == t + 1) e = sp.n;
+    }
+    starts[threadIdx.x] = s;
+    ends[threadIdx.x] = e;
 }
 
 }  // namespace glr

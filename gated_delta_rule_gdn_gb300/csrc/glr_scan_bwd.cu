@@ -19,256 +19,315 @@ __device__ unsigned g_glr_bwd_status;   // bit 0: a block gave up a bounded wait
 
 struct BwdSpace { void* scan; float* part; };
 
-template <typename Tx, typename Tg, int V>
-__global__ void __launch_bounds__(kWarps * 32)
+template <typename Tx, typename Tg, int LANES, int V, bool PACKED>
+__global__ void __launch_bounds__(kThreads, 2)
 glr_bwd_kernel(const GlrArgs a, const Exchange x, float* part) {
-    constexpr int W = 32 * V;
-    __shared__ float sA[kWarps][W], sH[kWarps][W], sG[kWarps][W], s_carry[W], s_state[W];
-    __shared__ int s_start[kTile], s_end[kTile];
-    __shared__ unsigned s_id;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    unsigned id = blockIdx.x;
+    using At = Place<LANES, V>;
+    constexpr int W = At::W, R = At::kRuns, L = At::L;
+    static_assert(2 * W <= kThreads, "one thread a channel for each direction");
+    extern __shared__ __align__(16) unsigned char s_raw[];
+    __shared__ float sA[R][W], sH[R][W], sG[R][W];
+    __shared__ unsigned char s_any[R];           // bit 0: a sequence starts in the run; bit 1: one ends
+    __shared__ int s_start[2][kTile], s_end[2][kTile];
+    __shared__ unsigned s_next;
+    const int tid = threadIdx.x, run = tid / LANES, lane = tid % LANES;
+    auto* bg = reinterpret_cast<Vec<Tg, V>*>(s_raw) + tid;                    // [L][256] each
+    auto* bx = reinterpret_cast<Vec<Tx, V>*>(s_raw + L * kThreads * sizeof(Vec<Tg, V>)) + tid;
+    auto* bi = bx + L * kThreads;
+    auto* bo = bi + L * kThreads;
+
+    At at;
+    const auto fetch = [&](int id) {
+        at.set(x, a, id, true);
+        const Tg* g = static_cast<const Tg*>(a.g) + at.row * a.ldg + at.c;
+        const Tx* xp = static_cast<const Tx*>(a.x) + at.row * a.ldx + at.c;
+        const Tx* ip = static_cast<const Tx*>(a.gi) + at.row * a.ldi + at.c;
+        const Tx* op = static_cast<const Tx*>(a.dO) + at.row * a.D + at.c;
+        const int n = at.live ? at.count : 0;
+#pragma unroll
+        for (int j = 0; j < L; ++j) {
+            copy_async(bg + j * kThreads, j < n ? g : static_cast<const Tg*>(a.g), j < n);
+            copy_async(bx + j * kThreads, j < n ? xp : static_cast<const Tx*>(a.x), j < n);
+            if (a.gi) copy_async(bi + j * kThreads, j < n ? ip : static_cast<const Tx*>(a.gi), j < n);
+            copy_async(bo + j * kThreads, j < n ? op : static_cast<const Tx*>(a.dO), j < n);
+            g += a.ldg;
+            xp += a.ldx;
+            ip += a.ldi;
+            op += a.D;
+        }
+    };
+    // the state that enters the tile, for the threads that run the states through it (tid - W is their channel)
+    const auto entry_state = [&]() {
+        const int c = at.c0 + tid - W;
+        if (tid < W || tid >= 2 * W || c >= a.D || at.p * kTile >= a.T) return 0.f;
+        if (at.p > 0 || PACKED) return a.ckpt[((size_t)at.b * x.tiles + at.p) * a.D + c];
+        return a.h0 ? a.h0[(size_t)at.b * a.D + c] : 0.f;
+    };
+    unsigned ticket = 0;
+    int id = blockIdx.x;
     if (x.tiles > 1) {
-        if (tid == 0) s_id = atomicAdd(x.ticket, 1u);
+        if (tid == 0) s_next = atomicAdd(x.ticket, 1u) + 1u;
         __syncthreads();
-        id = s_id;
+        id = (int)s_next;
+        if (tid == 0) ticket = atomicAdd(x.ticket, 1u) + 1u;
+        __syncthreads();
     }
-    const int q = id / x.chains, p = x.tiles - 1 - q, chain = id % x.chains, cols = x.chains / a.B;
-    const int b = chain / cols, c0 = (chain % cols) * W, c = c0 + lane * V;
-    const int t0 = p * kTile + warp * kRun;
-    const bool live = c < a.D;
-    const size_t row0 = (size_t)b * a.T;
+    float entry = 0.f;
+    if (id < x.total) {
+        fetch(id);
+        entry = entry_state();
+        if (PACKED && tid < kTile) sequence_marks(a, at.p, s_start[0], s_end[0]);
+    }
+    if (PACKED) __syncthreads();
 
-    Vec<Tg, V> g[kRun];
-    Vec<Tx, V> xv[kRun], gi[kRun], dO[kRun];
+    for (int k = 0; id < x.total; k ^= 1) {
+        const At now = at;
+        unsigned starts = 0, ends = 0;
+        if (PACKED) {
 #pragma unroll
-    for (int j = 0; j < kRun; ++j) {
-        const bool in = live && t0 + j < a.T;
-        if (in) g[j].load(static_cast<const Tg*>(a.g) + (row0 + t0 + j) * a.ldg + c); else g[j].zero();
-        if (in) xv[j].load(static_cast<const Tx*>(a.x) + (row0 + t0 + j) * a.ldx + c); else xv[j].zero();
-        if (in && a.gi) gi[j].load(static_cast<const Tx*>(a.gi) + (row0 + t0 + j) * a.ldi + c); else gi[j].zero();
-        if (in) dO[j].load(static_cast<const Tx*>(a.dO) + (row0 + t0 + j) * a.D + c); else dO[j].zero();
-    }
-    if (a.cu && tid < kTile) {
-        const int t = p * kTile + tid;
-        int starts = -1, ends = -1;
-        if (t < a.T) {
-            const mix::Span s = mix::span_of(a.cu, a.n_seqs, a.T, t);
-            if (s.first == t) starts = s.n;
-            if (s.end == t + 1) ends = s.n;
-        }
-        s_start[tid] = starts;
-        s_end[tid] = ends;
-    }
-    if (tid < W) {                               // the state that enters the tile
-        float h = 0.f;
-        if (c0 + tid < a.D && p * kTile < a.T) {
-            if (p > 0 || a.cu) h = a.ckpt[((size_t)b * x.tiles + p) * a.D + c0 + tid];
-            else if (a.h0) h = a.h0[(size_t)b * a.D + c0 + tid];
-        }
-        s_state[tid] = h;
-    }
-    __syncthreads();
-    unsigned starts = 0, ends = 0;
-    if (a.cu) {
-        starts = __ballot_sync(~0u, lane < kRun && s_start[warp * kRun + (lane & (kRun - 1))] >= 0);
-        ends = __ballot_sync(~0u, lane < kRun && s_end[warp * kRun + (lane & (kRun - 1))] >= 0);
-    }
-    Channel ch[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) ch[v] = live ? channel(a.A_log, a.dt_bias, c + v) : Channel{0.f, 0.f};
-
-    // decays, the run's forward map (A, H) and backward map (A, G)
-    float al[kRun][V], u[kRun][V];
-#pragma unroll
-    for (int j = 0; j < kRun; ++j)
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const float z = g[j].get(v);
-            const Decay d = decay(a.A_log ? ch[v].neg_eA * softplus(tail(z + ch[v].dt)) : z);
-            float w = xv[j].get(v);
-            if (a.gi) w *= sigmoid(tail(gi[j].get(v)));
-            if (a.normalize) w *= input_factor(d);
-            u[j][v] = w;
-            al[j][v] = t0 + j < a.T ? d.a : 1.f;
-        }
-    float A[V], H[V], G[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        A[v] = 1.f;
-        H[v] = 0.f;
-        G[v] = 0.f;
-    }
-#pragma unroll
-    for (int j = 0; j < kRun; ++j) {
-        const bool here = (starts >> j) & 1;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            if (here) {
-                const int n = s_start[warp * kRun + j];
-                if (a.h0 && live) u[j][v] = fmaf(al[j][v], a.h0[(size_t)n * a.D + c + v], u[j][v]);
-                H[v] = u[j][v];
-            } else {
-                H[v] = fmaf(al[j][v], H[v], u[j][v]);
-            }
-            A[v] *= al[j][v];
-        }
-    }
-#pragma unroll
-    for (int j = kRun - 1; j >= 0; --j) {
-        const bool here = (ends >> j) & 1;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            float D = dO[j].get(v);
-            if (here) {
-                const int n = s_end[warp * kRun + j];
-                if (a.dhT && live) D += a.dhT[(size_t)n * a.D + c + v];
-            } else {
-                D += G[v];
-            }
-            G[v] = al[j][v] * D;
-        }
-    }
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        // one A serves both maps: the signs tell where each forgets
-        sA[warp][lane * V + v] = A[v];
-        sH[warp][lane * V + v] = H[v];
-        sG[warp][lane * V + v] = G[v];
-    }
-    __shared__ unsigned char s_starts[kWarps], s_ends[kWarps];
-    if (lane == 0) {
-        s_starts[warp] = starts != 0;
-        s_ends[warp] = ends != 0;
-    }
-    __syncthreads();
-    float tA = 1.f, tG = 0.f, last = 0.f;
-    if (tid < W) {
-#pragma unroll
-        for (int w = kWarps - 1; w >= 0; --w) {
-            const float wA = s_ends[w] ? -1.f : sA[w][tid];
-            tG = apply(wA, sG[w][tid], tG);
-            tA = both(tA, wA);
-        }
-        if (q < kGroup && !a.cu && a.dhT && c0 + tid < a.D) last = a.dhT[(size_t)b * a.D + c0 + tid];
-    }
-    const float carry = carry_in(x, W, q, chain, tA, tG, last, true, &g_glr_bwd_status);
-    if (tid < W) s_carry[tid] = carry;
-    __syncthreads();
-
-    // h_{t-1} of every token (in place of u), then the gradients from the last token to the first
-    float h[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) h[v] = s_state[lane * V + v];
-    for (int w = 0; w < warp; ++w)
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-            h[v] = apply(s_starts[w] ? -1.f : sA[w][lane * V + v], sH[w][lane * V + v], h[v]);
-#pragma unroll
-    for (int j = 0; j < kRun; ++j) {
-        const bool here = (starts >> j) & 1;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const float uj = u[j][v];
-            if (here) {
-                const int n = s_start[warp * kRun + j];
-                u[j][v] = a.h0 && live ? a.h0[(size_t)n * a.D + c + v] : 0.f;
-                h[v] = uj;
-            } else {
-                u[j][v] = h[v];
-                h[v] = fmaf(al[j][v], h[v], uj);
+            for (int j = 0; j < L; ++j) {
+                starts |= (s_start[k][run * L + j] >= 0 ? 1u : 0u) << j;
+                ends |= (s_end[k][run * L + j] >= 0 ? 1u : 0u) << j;
             }
         }
-    }
+        // the decay, the input u, and the factors of the gradients:
+        //   dx = D w, di = dx y, dla = D (a h_{t-1} - m), dg = dla w3, dA_log = sum dla la
+        //   w = s sigma(i), y = x (1 - sigma(i)), m = sigma(i) x a^2 / s, w3 = dla/dg
+        float al[L][V], u[L][V], w[L][V], y[L][V], m[L][V], w3[L][V], la[L][V], dO[L][V];
+        copies_done();
 #pragma unroll
-    for (int v = 0; v < V; ++v) G[v] = s_carry[lane * V + v];
-    for (int w = kWarps - 1; w > warp; --w)
+        for (int j = 0; j < L; ++j) {
+            const Vec<Tg, V> g = bg[j * kThreads];
+            const Vec<Tx, V> xv = bx[j * kThreads], ov = bo[j * kThreads];
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-            G[v] = apply(s_ends[w] ? -1.f : sA[w][lane * V + v], sG[w][lane * V + v], G[v]);
-    float pA[V], pdt[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) pA[v] = pdt[v] = 0.f;
-#pragma unroll
-    for (int j = kRun - 1; j >= 0; --j) {
-        const bool here = (ends >> j) & 1, in = live && t0 + j < a.T;
-        Vec<Tx, V> dx, di;
-        Vec<Tg, V> dg;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            float D = dO[j].get(v);
-            if (here) {
-                const int n = s_end[warp * kRun + j];
-                if (a.dhT && live) D += a.dhT[(size_t)n * a.D + c + v];
-            } else {
-                D += G[v];
-            }
-            G[v] = al[j][v] * D;
-            const float z = g[j].get(v), xe = xv[j].get(v);
-            const Tail tz = tail(z + ch[v].dt), ti = tail(gi[j].get(v));
-            const float la = a.A_log ? ch[v].neg_eA * softplus(tz) : z;
-            const float si = a.gi ? sigmoid(ti) : 1.f;
-            float s = 1.f, dla = G[v] * u[j][v];
-            if (a.normalize) {
-                const Decay d = decay(la);
-                s = input_factor(d);
-                // ds/dlog a = -a^2 / s, taken as 0 where s = 0 (log a = 0: the derivative does not exist there)
-                if (s > 0.f) dla -= D * si * xe * __fdividef(d.a * d.a, s);
-            }
-            const float du = D * s;
-            dx.set(v, du * si);
-            if (a.gi) di.set(v, du * xe * sigmoid_slope(ti));
-            const float dz = a.A_log ? dla * ch[v].neg_eA * sigmoid(tz) : dla;
-            dg.set(v, dz);
-            if (in) {
-                if (dla != 0.f) pA[v] = fmaf(dla, la, pA[v]);     // (0 where log a is infinite)
-                pdt[v] += dz;
+            for (int v = 0; v < V; ++v) {
+                la[j][v] = g.get(v);
+                u[j][v] = xv.get(v);
+                dO[j][v] = ov.get(v);
+                w[j][v] = w3[j][v] = 1.f;
+                y[j][v] = m[j][v] = 0.f;
             }
         }
-        if (in) {
-            dx.store(static_cast<Tx*>(a.dx) + (row0 + t0 + j) * a.D + c);
-            dg.store(static_cast<Tg*>(a.dg) + (row0 + t0 + j) * a.D + c);
-            if (a.gi) di.store(static_cast<Tx*>(a.di) + (row0 + t0 + j) * a.D + c);
-        }
-        if (a.cu && a.dh0 && live) {
-            const int n = s_start[warp * kRun + j];
-            if (n >= 0)
+        if (a.gi) {
 #pragma unroll
-                for (int v = 0; v < V; ++v) a.dh0[(size_t)n * a.D + c + v] = G[v];
-        }
-    }
-    if (a.dh0 && live) {
-        if (!a.cu) {
-            if (p == 0 && warp == 0)
+            for (int j = 0; j < L; ++j) {
+                const Vec<Tx, V> gi = bi[j * kThreads];
 #pragma unroll
-                for (int v = 0; v < V; ++v) a.dh0[(size_t)b * a.D + c + v] = G[v];
+                for (int v = 0; v < V; ++v) {
+                    // 1 - sigma(i) = e sigma(i) with e = exp(-i), kept finite
+                    const float e = ex2(max_nan(gi.get(v), -80.f) * -kLog2e), si = rcp(1.f + e);
+                    w[j][v] = si;
+                    u[j][v] *= si;
+                    y[j][v] = u[j][v] * e;
+                }
+            }
+        }
+        if (a.A_log) {
+            Channel ch[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) ch[v] = now.live ? channel(a.A_log, a.dt_bias, now.c + v) : Channel{0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < L; ++j)
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    const float z = la[j][v] + ch[v].dt, e = tail(z);
+                    la[j][v] = ch[v].neg_eA * softplus(z, e);
+                    w3[j][v] = ch[v].neg_eA * sigmoid(z, e);
+                }
         } else {
-            for (int n = p * kWarps + warp; n < a.n_seqs; n += x.tiles * kWarps) {
-                if (mix::clamp_off(a.cu[n + 1], a.T) > mix::clamp_off(a.cu[n], a.T)) continue;
+#pragma unroll
+            for (int j = 0; j < L; ++j)
+#pragma unroll
+                for (int v = 0; v < V; ++v) la[j][v] = min_nan(la[j][v], 88.f);
+        }
+#pragma unroll
+        for (int j = 0; j < L; ++j)
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const Decay d = decay(la[j][v]);
+                if (a.normalize) {
+                    // ds/dlog a = -a^2 / s, taken as 0 where s = 0 (log a = 0: the derivative does not exist there)
+                    const float s2 = input_power(d), rs = s2 > 0.f ? rsq(s2) : 0.f, s = s2 * rs;
+                    m[j][v] = u[j][v] * (d.a * d.a) * rs;
+                    u[j][v] *= s;
+                    w[j][v] *= s;
+                }
+                al[j][v] = d.a;
+            }
+        if (now.count < L) {                     // past the row's end state and gradient stay
+#pragma unroll
+            for (int j = 0; j < L; ++j)
+#pragma unroll
+                for (int v = 0; v < V; ++v) al[j][v] = j < now.count ? al[j][v] : 1.f;
+        }
+        if (PACKED && (starts | ends) && now.live) {
+            // what enters at a sequence's first token, and at its last
+#pragma unroll
+            for (int j = 0; j < L; ++j) {
+                if (((starts >> j) & 1) && a.h0)
+#pragma unroll
+                    for (int v = 0; v < V; ++v)
+                        u[j][v] = fmaf(al[j][v], a.h0[(size_t)s_start[k][run * L + j] * a.D + now.c + v], u[j][v]);
+                if (((ends >> j) & 1) && a.dhT)
+#pragma unroll
+                    for (int v = 0; v < V; ++v) dO[j][v] += a.dhT[(size_t)s_end[k][run * L + j] * a.D + now.c + v];
+            }
+        }
+
+        // the run's maps: (A, H) of the state, (A, G) of the gradient; one A serves both
+        float A[V], H[V], G[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            A[v] = 1.f;
+            H[v] = G[v] = 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < L; ++j) {
+            const int r = L - 1 - j;
+            const bool start = PACKED && ((starts >> j) & 1), end = PACKED && ((ends >> r) & 1);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                H[v] = start ? u[j][v] : fmaf(al[j][v], H[v], u[j][v]);
+                G[v] = al[r][v] * (end ? dO[r][v] : dO[r][v] + G[v]);
+                A[v] *= al[j][v];
+            }
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            sA[run][lane * V + v] = A[v];
+            sH[run][lane * V + v] = H[v];
+            sG[run][lane * V + v] = G[v];
+        }
+        if (PACKED && lane == 0) s_any[run] = (starts ? 1 : 0) | (ends ? 2 : 0);
+        const float enter = entry;
+        if (x.tiles > 1 && tid == 0) s_next = ticket;
+        __syncthreads();
+        const int next = x.tiles > 1 ? (int)s_next : id + (int)gridDim.x;
+        if (next < x.total) {                    // the buffer is free: the next tile's inputs on the way
+            fetch(next);
+            entry = entry_state();
+            if (PACKED && tid < kTile) sequence_marks(a, at.p, s_start[k ^ 1], s_end[k ^ 1]);
+            if (x.tiles > 1 && tid == 0) ticket = atomicAdd(x.ticket, 1u) + 1u;
+        }
+        if (tid < W) {                           // the gradient that enters the tile from behind, and each of its runs
+            const int c = now.c0 + tid;
+            const auto run_A = [&](int r) { return PACKED && (s_any[r] & 2) ? -1.f : sA[r][tid]; };
+            float tA = 1.f, tG = 0.f, G = 0.f;
+#pragma unroll
+            for (int r = R - 1; r >= 0; --r) {
+                tG = apply(run_A(r), sG[r][tid], tG);
+                tA = both(tA, run_A(r));
+            }
+            const int q = x.tiles - 1 - now.p;
+            if (!PACKED && q < kGroup && a.dhT && c < a.D) G = a.dhT[(size_t)now.b * a.D + c];
+            G = carry_in(x, W, q, now.chain, tid, tA, tG, G, true, &g_glr_bwd_status);
+#pragma unroll
+            for (int r = R - 1; r >= 0; --r) {
+                const float rG = sG[r][tid];
+                sG[r][tid] = G;
+                G = apply(run_A(r), rG, G);
+            }
+        } else if (tid < 2 * W) {                // the states that enter the runs
+            const int c = tid - W;
+            float h = enter;
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const float rA = PACKED && (s_any[r] & 1) ? -1.f : sA[r][c], rH = sH[r][c];
+                sH[r][c] = h;
+                h = apply(rA, rH, h);
+            }
+        }
+        __syncthreads();
+
+        // h_{t-1} of every token in place of u, then the gradients from the last token to the first
+        float h[V], pA[V], pdt[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            h[v] = sH[run][lane * V + v];
+            G[v] = sG[run][lane * V + v];
+            pA[v] = pdt[v] = 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < L; ++j) {
+            const bool start = PACKED && ((starts >> j) & 1);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float uj = u[j][v];
+                u[j][v] = h[v];
+                if (start) {
+                    u[j][v] = a.h0 && now.live ? a.h0[(size_t)s_start[k][run * L + j] * a.D + now.c + v] : 0.f;
+                    h[v] = uj;
+                } else {
+                    h[v] = fmaf(al[j][v], h[v], uj);
+                }
+            }
+        }
+        Tx* dx_p = static_cast<Tx*>(a.dx) + (now.row + L) * a.D + now.c;
+        Tx* di_p = static_cast<Tx*>(a.di) + (now.row + L) * a.D + now.c;
+        Tg* dg_p = static_cast<Tg*>(a.dg) + (now.row + L) * a.D + now.c;
+        const int n = now.live ? now.count : 0;
+#pragma unroll
+        for (int j = L - 1; j >= 0; --j) {
+            const bool end = PACKED && ((ends >> j) & 1);
+            Vec<Tx, V> dx, di;
+            Vec<Tg, V> dg;
+            dx_p -= a.D;
+            di_p -= a.D;
+            dg_p -= a.D;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float D = end ? dO[j][v] : dO[j][v] + G[v];
+                G[v] = al[j][v] * D;
+                const float dla = D * fmaf(al[j][v], u[j][v], -m[j][v]), dw = D * w[j][v], dz = dla * w3[j][v];
+                dx.set(v, dw);
+                di.set(v, dw * y[j][v]);
+                dg.set(v, dz);
+                if (j < n) {
+                    pA[v] = fmaf(dla, la[j][v], pA[v]);
+                    pdt[v] += dz;
+                }
+            }
+            if (j < n) {
+                dx.store(dx_p);
+                dg.store(dg_p);
+                if (a.gi) di.store(di_p);
+            }
+            if (PACKED && a.dh0 && now.live) {
+                const int s = s_start[k][run * L + j];
+                if (s >= 0)
+#pragma unroll
+                    for (int v = 0; v < V; ++v) a.dh0[(size_t)s * a.D + now.c + v] = G[v];
+            }
+        }
+        if (!PACKED && a.dh0 && now.live && now.p == 0 && run == 0)
+#pragma unroll
+            for (int v = 0; v < V; ++v) a.dh0[(size_t)now.b * a.D + now.c + v] = G[v];
+        if (PACKED && a.dh0 && now.live) {
+            for (int s = now.p * R + run; s < a.n_seqs; s += x.tiles * R) {
+                if (mix::clamp_off(a.cu[s + 1], a.T) > mix::clamp_off(a.cu[s], a.T)) continue;
 #pragma unroll
                 for (int v = 0; v < V; ++v)
-                    a.dh0[(size_t)n * a.D + c + v] = a.dhT ? a.dhT[(size_t)n * a.D + c + v] : 0.f;
+                    a.dh0[(size_t)s * a.D + now.c + v] = a.dhT ? a.dhT[(size_t)s * a.D + now.c + v] : 0.f;
             }
         }
-    }
-    if (!a.dA) return;
-    __syncthreads();
+        if (a.dA) {                              // the tile's sums, runs in order
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        sA[warp][lane * V + v] = pA[v];
-        sG[warp][lane * V + v] = pdt[v];
-    }
-    __syncthreads();
-    if (tid < W && c0 + tid < a.D) {
-        float s = 0.f, d = 0.f;
+            for (int v = 0; v < V; ++v) {
+                sA[run][lane * V + v] = pA[v];
+                sG[run][lane * V + v] = pdt[v];  // (each thread overwrites what it alone has read)
+            }
+            __syncthreads();
+            if (tid < 2 * W && now.c0 + tid % W < a.D) {
+                const float(*src)[W] = tid < W ? sA : sG;
+                float s = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            s += sA[w][tid];
-            d += sG[w][tid];
+                for (int r = 0; r < R; ++r) s += src[r][tid % W];
+                const size_t rows = (size_t)a.B * x.tiles, r = (size_t)now.b * x.tiles + now.p;
+                part[((tid < W ? 0 : rows) + r) * a.D + now.c0 + tid % W] = s;
+            }
+            __syncthreads();
         }
-        const size_t rows = (size_t)a.B * x.tiles, r = (size_t)b * x.tiles + p;
-        part[r * a.D + c0 + tid] = s;
-        part[(rows + r) * a.D + c0 + tid] = d;
+        id = next;
     }
 }
 
@@ -296,23 +355,34 @@ __global__ void __launch_bounds__(256) glr_param_kernel(const float* part, int r
     }
 }
 
-template <typename Tx, typename Tg, int V>
+template <typename Tx, typename Tg, int LANES, int V, bool PACKED>
 cudaError_t bwd(const GlrArgs& a, const BwdSpace& sp, cudaStream_t s) {
-    const Layout l = layout(a.B, a.T, a.D, 32 * V);
+    using At = Place<LANES, V>;
+    const Layout l = layout(a.B, a.T, a.D, At::W);
     const Exchange x = exchange(l, sp.scan);
-    if (l.flag_bytes) {
-        const cudaError_t e = cudaMemsetAsync(sp.scan, 0, l.flag_bytes, s);
+    if (l.bytes) {
+        const cudaError_t e = cudaMemsetAsync(sp.scan, 0xff, l.bytes, s);
         if (e != cudaSuccess) return e;
     }
-    glr_bwd_kernel<Tx, Tg, V><<<(unsigned)l.tiles * l.chains, kWarps * 32, 0, s>>>(a, x, sp.part);
+    const auto kernel = glr_bwd_kernel<Tx, Tg, LANES, V, PACKED>;
+    const size_t smem = (size_t)At::L * kThreads * V * (sizeof(Tg) + 3 * sizeof(Tx));
+    static const Residency res = residency(reinterpret_cast<const void*>(kernel), smem);
+    if (res.error != cudaSuccess) return res.error;
+    kernel<<<x.total < res.blocks ? x.total : res.blocks, kThreads, smem, s>>>(a, x, sp.part);
     if (a.dA)
         glr_param_kernel<<<dim3((a.D + 31) / 32, 2), 256, 0, s>>>(sp.part, a.B * l.tiles, a.D, a.dA, a.ddt);
     return cudaGetLastError();
 }
 
+template <typename Tx, typename Tg, int LANES, int V>
+cudaError_t bwd_packed(const GlrArgs& a, const BwdSpace& sp, cudaStream_t s) {
+    return a.cu ? bwd<Tx, Tg, LANES, V, true>(a, sp, s) : bwd<Tx, Tg, LANES, V, false>(a, sp, s);
+}
+
 template <typename Tx, typename Tg>
 cudaError_t bwd_wide(const GlrArgs& a, const BwdSpace& sp, cudaStream_t s) {
-    return glr_vector(a, 2) ? bwd<Tx, Tg, 2>(a, sp, s) : bwd<Tx, Tg, 1>(a, sp, s);
+    if (glr_vector(a, 2)) return bwd_packed<Tx, Tg, 16, 2>(a, sp, s);
+    return bwd_packed<Tx, Tg, 32, 1>(a, sp, s);
 }
 
 // The backward's workspace: the scan's exchange, the partial sums of the parameters, and the checkpoints that the
@@ -325,8 +395,8 @@ size_t part_bytes(const GlrArgs& a) { return up(2 * (size_t)a.B * tiles_of(a) * 
 
 size_t glr_workspace_bytes(const GlrArgs& a, bool backward) {
     size_t scan = 0;
-    for (int V = 1; V <= 4; V *= 2) {
-        const size_t n = layout(a.B, a.T, a.D, 32 * V).bytes;
+    for (int width = 32; width <= 64; width *= 2) {
+        const size_t n = layout(a.B, a.T, a.D, width).bytes;
         scan = n > scan ? n : scan;
     }
     if (!backward) return scan;
