@@ -3,6 +3,12 @@
 //   the first `rot` channels of y turn by the angles of the token's position: pairs (i, i + rot/2), or (2i, 2i + 1)
 //   interleaved.
 // Backward: dy = the output's gradient turned back, dw = sum dy x r, e = w dy, dx = r (e - c r^2 x sum(x e)).
+// Bound by HBM: every head is read once and written once (backward: read with its gradient, written once).
+//
+// Vector kernels: G neighbouring lanes hold a head, 8 channels each, and a group of lanes takes `kHeads` heads of one
+// token, so that the token's angles are read once for them and their loads are under way together.  The rotation's
+// partner is in the same lane (interleaved), or in the lane rot/16 away.  Heads whose size, rotation or alignment does
+// not go in steps of 8 channels take the scalar kernels, a warp per head.
 
 #include <type_traits>
 
@@ -16,10 +22,215 @@ using mix::bf16;
 using mix::ld;
 using mix::st;
 
-__device__ __forceinline__ float warp_sum(float v) {
-    for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+constexpr int kMaxD = 256, kThreads = 256, kHeads = 4, E = 8;
+
+__device__ __forceinline__ int position(const QkNormArgs& a, int64_t tok) {
+    const int p = a.pos ? a.pos[tok] : (int)((unsigned)tok % (unsigned)a.T);    // (tokens times heads fit 31 bits)
+    return min(max(p, 0), a.n_pos - 1);
+}
+
+template <int G>
+__device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+    for (int m = G / 2; m > 0; m >>= 1) v += __shfl_xor_sync(~0u, v, m, G);
     return v;
 }
+
+// 8 channels in 16-byte accesses
+template <typename T> struct Eight;
+template <> struct Eight<bf16> {
+    mix::Vec<bf16, 8> v;
+    __device__ __forceinline__ void load(const bf16* p) { v.load(p); }
+    __device__ __forceinline__ void zero() { v.zero(); }
+    __device__ __forceinline__ float get(int i) const { return v.get(i); }
+    __device__ __forceinline__ void set(int i, float x) { v.set(i, x); }
+    __device__ __forceinline__ void store(bf16* p) const { v.store(p); }
+};
+template <> struct Eight<float> {
+    mix::Vec<float, 4> v[2];
+    __device__ __forceinline__ void load(const float* p) { v[0].load(p); v[1].load(p + 4); }
+    __device__ __forceinline__ void zero() { v[0].zero(); v[1].zero(); }
+    __device__ __forceinline__ float get(int i) const { return v[i / 4].get(i % 4); }
+    __device__ __forceinline__ void set(int i, float x) { v[i / 4].set(i % 4, x); }
+    __device__ __forceinline__ void store(float* p) const { v[0].store(p); v[1].store(p + 4); }
+};
+
+enum Rotation { kNone, kHalves, kInterleaved };
+
+// The angles of a lane's channels at position p (cos = 1, sin = 0 past the rotated ones), with the sign that the forward
+// rotation gives the partner's term in `sin` for halves.
+template <int ROT>
+struct Angles {
+    float c[ROT == kInterleaved ? E / 2 : E], s[ROT == kInterleaved ? E / 2 : E];
+    int partner;
+    __device__ __forceinline__ void load(const QkNormArgs& a, int p, int lane) {
+        const int j = lane * E, half = a.rot / 2;
+        constexpr int N = ROT == kInterleaved ? E / 2 : E;
+        const bool in = j < a.rot;
+        const bool low = j < half;
+        const int at = ROT == kInterleaved ? j / 2 : (low ? j : j - half);
+        partner = in ? (low ? lane + half / E : lane - half / E) : lane;
+        const float* cp = a.cos + (int64_t)p * half + at;
+        const float* sp = a.sin + (int64_t)p * half + at;
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+            const float4 x = in ? *reinterpret_cast<const float4*>(cp + i) : make_float4(1.f, 1.f, 1.f, 1.f);
+            const float4 y = in ? *reinterpret_cast<const float4*>(sp + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+            c[i] = x.x; c[i + 1] = x.y; c[i + 2] = x.z; c[i + 3] = x.w;
+            s[i] = y.x; s[i + 1] = y.y; s[i + 2] = y.z; s[i + 3] = y.w;
+        }
+        if (ROT == kHalves && low)
+#pragma unroll
+            for (int i = 0; i < N; ++i) s[i] = -s[i];
+    }
+    // turn y forward (sign = 1) or back (sign = -1)
+    template <int G>
+    __device__ __forceinline__ void turn(float (&y)[E], float sign) const {
+        if (ROT == kHalves) {
+            // a lane past the rotated channels is its own partner, with sin = 0
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                const float o = __shfl_sync(~0u, y[i], partner, G);
+                y[i] = s[i] == 0.f ? y[i] * c[i] : fmaf(y[i], c[i], sign * s[i] * o);
+            }
+        } else if (ROT == kInterleaved) {
+#pragma unroll
+            for (int i = 0; i < E / 2; ++i) {
+                const float u = y[2 * i], v = y[2 * i + 1];
+                y[2 * i] = fmaf(u, c[i], -sign * s[i] * v);
+                y[2 * i + 1] = fmaf(v, c[i], sign * s[i] * u);
+            }
+        }
+    }
+};
+
+// a group's share of the work: kHeads heads (of q's, then k's) of a token
+template <int G>
+struct Share {
+    int64_t tok;
+    int head0, lane;
+    bool in;                          // the lane's channels exist
+    __device__ __forceinline__ Share(const QkNormArgs& a, unsigned item, unsigned parts) {
+        const unsigned t = item / parts;
+        tok = t;
+        head0 = (int)(item - t * parts) * kHeads;
+        lane = threadIdx.x % G;
+        in = lane * E < a.d;
+    }
+};
+
+template <typename T, int G, int ROT>
+__global__ void __launch_bounds__(kThreads) qk_fwd_kernel(const QkNormArgs a, const int parts) {
+    const unsigned item = blockIdx.x * (kThreads / G) + threadIdx.x / G;
+    const Share<G> w(a, min(item, (unsigned)(a.n * parts - 1)), parts);      // (the last block repeats the last share)
+    const int heads = a.H[0] + a.H[1], j0 = w.lane * E;
+    Eight<T> x[kHeads];
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i) {
+        const int hh = w.head0 + i, k = hh >= a.H[0], h = k ? hh - a.H[0] : hh;
+        if (w.in && hh < heads)
+            x[i].load(static_cast<const T*>(a.in[k]) + w.tok * a.tok_stride[k] + h * a.head_stride[k] + j0);
+        else
+            x[i].zero();
+    }
+    Angles<ROT> ang;
+    if (ROT != kNone) ang.load(a, position(a, w.tok), w.lane);
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i) {
+        const int hh = w.head0 + i, k = hh >= a.H[0], h = k ? hh - a.H[0] : hh;
+        float y[E], ss = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            y[e] = x[i].get(e);
+            ss = fmaf(y[e], y[e], ss);
+        }
+        const float r = rsqrtf(fmaf(a.c, group_sum<G>(ss), a.eps));
+        const float* wt = k ? a.w[1] : a.w[0];
+#pragma unroll
+        for (int e = 0; e < E; ++e) y[e] *= r;
+        if (wt && w.in)
+#pragma unroll
+            for (int e = 0; e < E; ++e) y[e] *= wt[j0 + e];
+        ang.template turn<G>(y, 1.f);
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[i].set(e, y[e]);
+        if (w.in && hh < heads) x[i].store(static_cast<T*>(a.out[k]) + (w.tok * a.H[k] + h) * a.d + j0);
+    }
+}
+
+// persistent blocks: the weight gradients of a block's heads stay in registers and leave as one row of partial sums
+template <typename T, int G, int ROT>
+__global__ void __launch_bounds__(kThreads) qk_bwd_kernel(const QkNormArgs a, const int parts, float* part) {
+    constexpr int kGroups = kThreads / G;
+    __shared__ float sw[2][kGroups][G * E];
+    const int heads = a.H[0] + a.H[1];
+    float acc[2][E] = {};
+    const int64_t items = a.n * parts;
+    for (int64_t base = (int64_t)blockIdx.x * kGroups; base < items; base += (int64_t)gridDim.x * kGroups) {
+        const int64_t item = base + threadIdx.x / G;
+        const bool real = item < items;
+        const Share<G> w(a, (unsigned)(real ? item : items - 1), parts);
+        const int j0 = w.lane * E;
+        Eight<T> x[kHeads], dz[kHeads];
+#pragma unroll
+        for (int i = 0; i < kHeads; ++i) {
+            const int hh = w.head0 + i, k = hh >= a.H[0], h = k ? hh - a.H[0] : hh;
+            if (w.in && real && hh < heads) {
+                x[i].load(static_cast<const T*>(a.in[k]) + w.tok * a.tok_stride[k] + h * a.head_stride[k] + j0);
+                dz[i].load(static_cast<const T*>(a.dout[k]) + (w.tok * a.H[k] + h) * a.d + j0);
+            } else {
+                x[i].zero();
+                dz[i].zero();
+            }
+        }
+        Angles<ROT> ang;
+        if (ROT != kNone) ang.load(a, position(a, w.tok), w.lane);
+#pragma unroll
+        for (int i = 0; i < kHeads; ++i) {
+            const int hh = w.head0 + i, k = hh >= a.H[0], h = k ? hh - a.H[0] : hh;
+            float e[E], ss = 0.f, xe = 0.f;
+#pragma unroll
+            for (int c = 0; c < E; ++c) {
+                e[c] = dz[i].get(c);
+                ss = fmaf(x[i].get(c), x[i].get(c), ss);
+            }
+            ang.template turn<G>(e, -1.f);
+            const float r = rsqrtf(fmaf(a.c, group_sum<G>(ss), a.eps));
+            const float* wt = k ? a.w[1] : a.w[0];
+            if (wt && w.in) {
+#pragma unroll
+                for (int c = 0; c < E; ++c) {
+                    const float t = e[c] * x[i].get(c) * r;
+                    if (k) acc[1][c] += t; else acc[0][c] += t;
+                    e[c] *= wt[j0 + c];
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < E; ++c) xe = fmaf(x[i].get(c), e[c], xe);
+            xe = group_sum<G>(xe) * a.c * r * r;
+#pragma unroll
+            for (int c = 0; c < E; ++c) x[i].set(c, r * fmaf(-x[i].get(c), xe, e[c]));
+            if (w.in && real && hh < heads) x[i].store(static_cast<T*>(a.out[k]) + (w.tok * a.H[k] + h) * a.d + j0);
+        }
+    }
+    if (!part) return;
+    const int g = threadIdx.x / G, lane = threadIdx.x % G;
+#pragma unroll
+    for (int c = 0; c < E; ++c) {
+        sw[0][g][lane * E + c] = acc[0][c];
+        sw[1][g][lane * E + c] = acc[1][c];
+    }
+    __syncthreads();
+    for (int j = threadIdx.x; j < 2 * a.d; j += kThreads) {
+        float s = 0.f;
+        for (int i = 0; i < kGroups; ++i) s += sw[j / a.d][i][j % a.d];
+        part[(size_t)blockIdx.x * 2 * a.d + j] = s;
+    }
+}
+
+// ---------------------------------------------------------------------------- any size and alignment: a warp per head
+
+constexpr int kWarps = kThreads / 32;
 
 // partner channel, its sign in the forward rotation, and the angle index of rotated channel j
 __device__ __forceinline__ void pair_of(const QkNormArgs& a, int j, int* other, float* sign, int* angle) {
@@ -35,58 +246,58 @@ __device__ __forceinline__ void pair_of(const QkNormArgs& a, int j, int* other, 
     }
 }
 
-constexpr int kMaxD = 256, kWarps = 4;
-
-__device__ __forceinline__ int position(const QkNormArgs& a, int64_t tok) {
-    const int p = a.pos ? a.pos[tok] : (int)(tok % a.T);
-    return min(max(p, 0), a.n_pos - 1);
-}
-
-// one warp per (token, head)
 template <typename T>
-__global__ void qk_fwd_kernel(const QkNormArgs a) {
+__global__ void __launch_bounds__(kThreads) qk_fwd_any_kernel(const QkNormArgs a) {
     __shared__ float buf[kWarps][kMaxD];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t id = (int64_t)blockIdx.x * kWarps + warp;
     const int heads = a.H[0] + a.H[1];
-    const int64_t tok = id / heads;
-    const int hh = (int)(id % heads), which = hh >= a.H[0], h = which ? hh - a.H[0] : hh;
+    const int64_t tok = (unsigned)id / (unsigned)heads;
+    const int hh = (int)((unsigned)id % (unsigned)heads), which = hh >= a.H[0], h = which ? hh - a.H[0] : hh;
     if (tok >= a.n) return;
     const T* x = static_cast<const T*>(a.in[which]) + tok * a.tok_stride[which] + h * a.head_stride[which];
     T* y = static_cast<T*>(a.out[which]) + (tok * a.H[which] + h) * a.d;
-    float ss = 0.f;
-    for (int j = lane; j < a.d; j += 32) {
-        const float v = ld(x + j);
-        ss = fmaf(v, v, ss);
+    float v[kMaxD / 32], ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < kMaxD / 32; ++i) {
+        const int j = lane + 32 * i;
+        v[i] = j < a.d ? ld(x + j) : 0.f;
+        ss = fmaf(v[i], v[i], ss);
     }
-    const float r = rsqrtf(fmaf(a.c, warp_sum(ss), a.eps));
-    for (int j = lane; j < a.d; j += 32) buf[warp][j] = ld(x + j) * r * (a.w[which] ? a.w[which][j] : 1.f);
+    const float r = rsqrtf(fmaf(a.c, group_sum<32>(ss), a.eps));
+#pragma unroll
+    for (int i = 0; i < kMaxD / 32; ++i) {
+        const int j = lane + 32 * i;
+        if (j < a.d) buf[warp][j] = v[i] * r * (a.w[which] ? a.w[which][j] : 1.f);
+    }
     __syncwarp();
     const int p = a.rot ? position(a, tok) : 0;
-    for (int j = lane; j < a.d; j += 32) {
-        float v = buf[warp][j];
+#pragma unroll
+    for (int i = 0; i < kMaxD / 32; ++i) {
+        const int j = lane + 32 * i;
+        if (j >= a.d) continue;
+        float u = buf[warp][j];
         if (j < a.rot) {
             int o, k;
             float sg;
             pair_of(a, j, &o, &sg, &k);
             const int64_t at = (int64_t)p * (a.rot >> 1) + k;
-            v = v * a.cos[at] + sg * buf[warp][o] * a.sin[at];
+            u = u * a.cos[at] + sg * buf[warp][o] * a.sin[at];
         }
-        st(y + j, v);
+        st(y + j, u);
     }
 }
 
-// one warp per (token, head); the block's weight gradients go to a partial row each
 template <typename T>
-__global__ void qk_bwd_kernel(const QkNormArgs a, float* part) {
+__global__ void __launch_bounds__(kThreads) qk_bwd_any_kernel(const QkNormArgs a, float* part) {
     __shared__ float buf[kWarps][kMaxD];
-    __shared__ float dw[2][kMaxD];
+    __shared__ float dw[2][kWarps][kMaxD];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int heads = a.H[0] + a.H[1];
     float acc[2][kMaxD / 32] = {};
     for (int64_t id = (int64_t)blockIdx.x * kWarps + warp; id < a.n * heads; id += (int64_t)gridDim.x * kWarps) {
-        const int64_t tok = id / heads;
-        const int hh = (int)(id % heads), which = hh >= a.H[0], h = which ? hh - a.H[0] : hh;
+        const int64_t tok = (unsigned)id / (unsigned)heads;
+        const int hh = (int)((unsigned)id % (unsigned)heads), which = hh >= a.H[0], h = which ? hh - a.H[0] : hh;
         const T* x = static_cast<const T*>(a.in[which]) + tok * a.tok_stride[which] + h * a.head_stride[which];
         const T* dz = static_cast<const T*>(a.dout[which]) + (tok * a.H[which] + h) * a.d;
         T* dx = static_cast<T*>(a.out[which]) + (tok * a.H[which] + h) * a.d;
@@ -112,71 +323,128 @@ __global__ void qk_bwd_kernel(const QkNormArgs a, float* part) {
             ss = fmaf(xv[i], xv[i], ss);
             e[i] = v;
         }
-        const float r = rsqrtf(fmaf(a.c, warp_sum(ss), a.eps));
+        const float r = rsqrtf(fmaf(a.c, group_sum<32>(ss), a.eps));
 #pragma unroll
         for (int i = 0; i < kMaxD / 32; ++i) {
             const int j = lane + 32 * i;
             if (j >= a.d) continue;
-            if (which) acc[1][i] += e[i] * xv[i] * r; else acc[0][i] += e[i] * xv[i] * r;
+            const float t = e[i] * xv[i] * r;
+            if (which) acc[1][i] += t; else acc[0][i] += t;
             if (a.w[which]) e[i] *= a.w[which][j];
             xe = fmaf(xv[i], e[i], xe);
         }
-        xe = warp_sum(xe) * a.c * r * r;
+        xe = group_sum<32>(xe) * a.c * r * r;
 #pragma unroll
         for (int i = 0; i < kMaxD / 32; ++i) {
             const int j = lane + 32 * i;
             if (j < a.d) st(dx + j, r * (e[i] - xv[i] * xe));
         }
     }
-    for (int w = 0; w < kWarps; ++w) {     // warps in turn: a fixed order
-        if (warp == w)
+    if (!part) return;
 #pragma unroll
-            for (int i = 0; i < kMaxD / 32; ++i)
-                for (int k = 0; k < 2; ++k) {
-                    const int j = lane + 32 * i;
-                    dw[k][j] = (w ? dw[k][j] : 0.f) + acc[k][i];
-                }
-        __syncthreads();
+    for (int i = 0; i < kMaxD / 32; ++i) {
+        dw[0][warp][lane + 32 * i] = acc[0][i];
+        dw[1][warp][lane + 32 * i] = acc[1][i];
     }
-    for (int j = threadIdx.x; j < 2 * a.d; j += blockDim.x)
-        part[(size_t)blockIdx.x * 2 * a.d + j] = dw[j / a.d][j % a.d];
+    __syncthreads();
+    for (int j = threadIdx.x; j < 2 * a.d; j += kThreads) {
+        float s = 0.f;
+        for (int i = 0; i < kWarps; ++i) s += dw[j / a.d][i][j % a.d];
+        part[(size_t)blockIdx.x * 2 * a.d + j] = s;
+    }
 }
 
-__global__ void qk_dw_kernel(const float* part, int rows, int d, float* dwq, float* dwk) {
-    const int j = blockIdx.x * blockDim.x + threadIdx.x;
-    if (j >= 2 * d) return;
-    float s = 0.f;
-    for (int r = 0; r < rows; ++r) s += part[(size_t)r * 2 * d + j];
-    float* out = j < d ? dwq : dwk;
-    if (out) out[j % d] = s;
+// column sums of part [rows][2 d]: 8 columns a block, 32 row lanes, joined in order
+__global__ void __launch_bounds__(256) qk_dw_kernel(const float* part, int rows, int d, float* dwq, float* dwk) {
+    __shared__ float s[32][9];
+    const int c = threadIdx.x % 8, w = threadIdx.x / 8, j = blockIdx.x * 8 + c;
+    float acc = 0.f;
+    if (j < 2 * d)
+#pragma unroll 4
+        for (int r = w; r < rows; r += 32) acc += part[(size_t)r * 2 * d + j];
+    s[w][c] = acc;
+    __syncthreads();
+    if (w == 0 && j < 2 * d) {
+        float t = 0.f;
+        for (int i = 0; i < 32; ++i) t += s[i][c];
+        float* out = j < d ? dwq : dwk;
+        if (out) out[j < d ? j : j - d] = t;
+    }
 }
 
-int bwd_blocks(const QkNormArgs& a) {
-    const int64_t rows = a.n * (a.H[0] + a.H[1]);
-    const int64_t want = (rows + kWarps - 1) / kWarps;
-    return (int)(want < 152 * 8 ? want : 152 * 8);
+// Whether the vector kernels apply: everything in steps of 8 channels, on 16-byte addresses.
+bool vector_ok(const QkNormArgs& a, bool backward) {
+    const auto al = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
+    if (a.d % E) return false;
+    if (a.rot > 0 && (a.interleaved ? a.rot % E != 0 : a.rot % (2 * E) != 0)) return false;
+    if (a.rot > 0 && (!al(a.cos) || !al(a.sin) || (a.rot / 2) % 4)) return false;
+    for (int i = 0; i < 2; ++i) {
+        if (a.tok_stride[i] % E || a.head_stride[i] % E || !al(a.in[i]) || !al(a.out[i])) return false;
+        if (backward && !al(a.dout[i])) return false;
+    }
+    return true;
+}
+
+constexpr int kBwdBlocks = 152 * 4;
+int64_t groups_per_block(int d) { return d <= 64 ? 32 : d <= 128 ? 16 : 8; }
+int parts_of(const QkNormArgs& a) { return (a.H[0] + a.H[1] + kHeads - 1) / kHeads; }
+
+// f(group size, rotation) as compile-time constants
+template <typename F>
+void by_shape(const QkNormArgs& a, F f) {
+    const auto rot = [&](auto g) {
+        if (a.rot == 0) f(g, std::integral_constant<int, kNone>{});
+        else if (a.interleaved) f(g, std::integral_constant<int, kInterleaved>{});
+        else f(g, std::integral_constant<int, kHalves>{});
+    };
+    if (a.d <= 64) rot(std::integral_constant<int, 8>{});
+    else if (a.d <= 128) rot(std::integral_constant<int, 16>{});
+    else rot(std::integral_constant<int, 32>{});
+}
+
+template <typename T>
+cudaError_t fwd(const QkNormArgs& a, cudaStream_t s) {
+    if (vector_ok(a, false)) {
+        const int parts = parts_of(a);
+        by_shape(a, [&](auto g, auto rot) {
+            const int64_t per = kThreads / g.value;
+            qk_fwd_kernel<T, g.value, rot.value><<<(unsigned)((a.n * parts + per - 1) / per), kThreads, 0, s>>>(a, parts);
+        });
+    } else {
+        const int64_t rows = a.n * (a.H[0] + a.H[1]);
+        qk_fwd_any_kernel<T><<<(unsigned)((rows + kWarps - 1) / kWarps), kThreads, 0, s>>>(a);
+    }
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t bwd(const QkNormArgs& a, cudaStream_t s) {
+    const bool weights = a.dw[0] || a.dw[1];
+    float* part = weights ? static_cast<float*>(a.ws) : nullptr;
+    int blocks = 0;                            // none without tokens: the weight gradients are then zero
+    if (a.n > 0 && vector_ok(a, true)) {
+        const int parts = parts_of(a);
+        const int64_t per = groups_per_block(a.d), want = (a.n * parts + per - 1) / per;
+        blocks = (int)(want < kBwdBlocks ? want : kBwdBlocks);
+        by_shape(a, [&](auto g, auto rot) {
+            qk_bwd_kernel<T, g.value, rot.value><<<blocks, kThreads, 0, s>>>(a, parts, part);
+        });
+    } else if (a.n > 0) {
+        const int64_t want = (a.n * (a.H[0] + a.H[1]) + kWarps - 1) / kWarps;
+        blocks = (int)(want < kBwdBlocks ? want : kBwdBlocks);
+        qk_bwd_any_kernel<T><<<blocks, kThreads, 0, s>>>(a, part);
+    }
+    if (weights) qk_dw_kernel<<<(2 * a.d + 7) / 8, 256, 0, s>>>(part, blocks, a.d, a.dw[0], a.dw[1]);
+    return cudaGetLastError();
 }
 
 }  // namespace
 
-size_t qk_norm_workspace_bytes(const QkNormArgs& a) { return (size_t)bwd_blocks(a) * 2 * a.d * sizeof(float); }
-
-cudaError_t launch_qk_norm_fwd(const QkNormArgs& a, cudaStream_t s) {
-    const int64_t rows = a.n * (a.H[0] + a.H[1]);
-    const unsigned blocks = (unsigned)((rows + kWarps - 1) / kWarps);
-    if (a.bf16) qk_fwd_kernel<bf16><<<blocks, kWarps * 32, 0, s>>>(a);
-    else qk_fwd_kernel<float><<<blocks, kWarps * 32, 0, s>>>(a);
-    return cudaGetLastError();
+size_t qk_norm_workspace_bytes(const QkNormArgs& a) {
+    const int64_t want = (a.n * (a.H[0] + a.H[1]) + 7) / 8;          // at least the blocks of either kernel
+    return (size_t)(want < kBwdBlocks ? want : kBwdBlocks) * 2 * a.d * sizeof(float);
 }
-
-cudaError_t launch_qk_norm_bwd(const QkNormArgs& a, cudaStream_t s) {
-    const int blocks = bwd_blocks(a);          // 0 without tokens: the weight gradients are then zero
-    float* part = static_cast<float*>(a.ws);
-    if (blocks == 0) {}
-    else if (a.bf16) qk_bwd_kernel<bf16><<<blocks, kWarps * 32, 0, s>>>(a, part);
-    else qk_bwd_kernel<float><<<blocks, kWarps * 32, 0, s>>>(a, part);
-    if (a.dw[0] || a.dw[1]) qk_dw_kernel<<<(2 * a.d + 127) / 128, 128, 0, s>>>(part, blocks, a.d, a.dw[0], a.dw[1]);
-    return cudaGetLastError();
-}
+cudaError_t launch_qk_norm_fwd(const QkNormArgs& a, cudaStream_t s) { return a.bf16 ? fwd<bf16>(a, s) : fwd<float>(a, s); }
+cudaError_t launch_qk_norm_bwd(const QkNormArgs& a, cudaStream_t s) { return a.bf16 ? bwd<bf16>(a, s) : bwd<float>(a, s); }
 
 }  // namespace gdn

@@ -2,6 +2,15 @@
 //   p_t = b + sum_j w_j x_{t - W + 1 + j},  y_t = silu(p_t) or p_t; inputs before a sequence's first token are its
 //   initial state (its last W - 1 inputs, oldest first) or zero.
 // Backward: ds = dy silu'(p), dx_t = sum_j w_j ds_{t + W - 1 - j}, dw_j = sum_t ds_t x_{t - W + 1 + j}, db = sum ds.
+// Bound by HBM: x is read once and y written once (backward: x and dy read once, dx written once).
+//
+// A thread walks a run of tokens of V neighbouring channels with the last W inputs in registers, a warp 32 V channels;
+// the W - 1 tokens around a run that its neighbours walk too come out of L2.  The backward walks W - 1 tokens further, for
+// the ds that its last tokens need, and keeps its sums of dw and db in registers; a block adds up its 8 runs and a second
+// kernel the blocks, in order.  Rows of sequence states (the final state, the initial state's gradient) are formed by
+// blocks of their own at the end of the grid.
+
+#include <type_traits>
 
 #include "mixer.h"
 #include "mixer_common.cuh"
@@ -10,189 +19,443 @@ namespace gdn {
 namespace {
 
 using mix::bf16;
-using mix::ld;
-using mix::st;
+using mix::Vec;
 
-// the input at place `at` of sequence n (negative: the initial state), channel c
-template <typename T>
-__device__ __forceinline__ float input(const ConvArgs& a, int64_t row0, int n, int at, int c) {
-    if (at >= 0) return ld(static_cast<const T*>(a.x) + (row0 + at) * a.ldx + c);
-    return a.h0 ? ld(static_cast<const T*>(a.h0) + ((int64_t)n * (a.W - 1) + at + a.W - 1) * a.D + c) : 0.f;
+constexpr int kWarps = 8, kRun = 32, kAhead = 8;
+
+__device__ __forceinline__ float ex2(float x) { float y; asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x)); return y; }
+__device__ __forceinline__ float rcp(float x) { float y; asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x)); return y; }
+// p sigma(p), and its derivative sigma (1 + p (1 - sigma)).  exp(-p) is kept finite, so that p sigma(p) of a large
+// negative p is a tiny number, not 0 times infinity; 1 - sigma = exp(-p) sigma.
+__device__ __forceinline__ float silu(float p) {
+    const float s = rcp(1.f + ex2(fminf(p * -1.4426950408889634f, 126.f)));
+    return p * s;
+}
+__device__ __forceinline__ float silu_slope(float p) {
+    const float e = ex2(fminf(p * -1.4426950408889634f, 126.f)), s = rcp(1.f + e);
+    return s * fmaf(p, e * s, 1.f);
 }
 
-template <typename T>
-__device__ __forceinline__ float pre(const ConvArgs& a, int64_t row0, int n, int at, int c) {
-    float p = a.b ? a.b[c] : 0.f;
-    for (int j = 0; j < a.W; ++j) p = fmaf(a.w[(size_t)c * a.W + j], input<T>(a, row0, n, at - a.W + 1 + j, c), p);
-    return p;
-}
-__device__ __forceinline__ float act(const ConvArgs& a, float p) { return a.silu ? p / (1.f + expf(-p)) : p; }
-
-// the gradient of p at place `at` < len
-template <typename T>
-__device__ __forceinline__ float grad_pre(const ConvArgs& a, int64_t row0, int n, int at, int c) {
-    const float dy = ld(static_cast<const T*>(a.dy) + (row0 + at) * a.D + c);
-    if (!a.silu) return dy;
-    const float p = pre<T>(a, row0, n, at, c), sg = 1.f / (1.f + expf(-p));
-    return dy * sg * (1.f + p * (1.f - sg));
+// A sequence: its number, and its first token and one past its last in the batch row.
+struct Seq { int n, first, end; };
+template <bool PACKED>
+__device__ __forceinline__ Seq sequence_at(const ConvArgs& a, int b, int t) {
+    if (!PACKED) return {b, 0, a.T};
+    const mix::Span s = mix::span_of(a.cu, a.n_seqs, a.T, t);
+    return {s.n, s.first, s.end};
 }
 
-// the gradient of the input at place `at` (negative: the initial state's)
-template <typename T>
-__device__ __forceinline__ float grad_in(const ConvArgs& a, int64_t row0, int n, int len, int at, int c) {
-    float s = 0.f;
-    for (int j = 0; j < a.W; ++j) {
-        const int t = at + a.W - 1 - j;
-        if (t >= 0 && t < len) s = fmaf(a.w[(size_t)c * a.W + j], grad_pre<T>(a, row0, n, t, c), s);
+template <typename T, int V>
+__device__ __forceinline__ void load_row(float (&d)[V], const T* p, bool in) {
+    Vec<T, V> r;
+    if (in) r.load(p); else r.zero();
+#pragma unroll
+    for (int v = 0; v < V; ++v) d[v] = r.get(v);
+}
+// the input at place `at` of sequence s (negative: out of its initial state)
+template <typename T, int V>
+__device__ __forceinline__ void load_input(float (&d)[V], const ConvArgs& a, const Seq& s, size_t row0, int at, int c) {
+    if (at >= 0) load_row<T, V>(d, static_cast<const T*>(a.x) + (row0 + s.first + at) * a.ldx + c, true);
+    else load_row<T, V>(d, static_cast<const T*>(a.h0) + ((size_t)s.n * (a.W - 1) + at + a.W - 1) * a.D + c, a.h0 != nullptr);
+}
+
+template <int W, int V>
+struct Taps {
+    float w[W][V], b[V];
+    __device__ __forceinline__ void load(const ConvArgs& a, int c, bool live) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+#pragma unroll
+            for (int j = 0; j < W; ++j) w[j][v] = live ? a.w[(size_t)(c + v) * W + j] : 0.f;
+            b[v] = live && a.b ? a.b[c + v] : 0.f;
+        }
     }
-    const int tail = at - (len - (a.W - 1));        // its place in the final state
-    if (a.dhT && tail >= 0) s += ld(static_cast<const T*>(a.dhT) + ((int64_t)n * (a.W - 1) + tail) * a.D + c);
-    return s;
-}
+};
 
-__device__ __forceinline__ void token(const ConvArgs& a, int64_t r, int64_t* row0, int* n, int* at, int* len) {
-    const int b = (int)(r / a.T), t = (int)(r % a.T);
+// rows [N, W - 1] of the final states (forward) or of the initial states' gradients (backward), a warp each
+template <typename T, int W, int V, bool BACKWARD>
+__device__ __forceinline__ void state_row(const ConvArgs& a, int64_t r, int c) {
+    const int n = (int)(r / (W - 1)), j = (int)(r % (W - 1));
+    Seq s{n, 0, a.T};
+    size_t row0 = (size_t)n * a.T;
     if (a.cu) {
-        const mix::Span s = mix::span_of(a.cu, a.n_seqs, a.T, t);
-        *row0 = s.first;
-        *n = s.n;
-        *at = t - s.first;
-        *len = s.end - s.first;
+        s.first = mix::clamp_off(a.cu[n], a.T);
+        s.end = max(mix::clamp_off(a.cu[n + 1], a.T), s.first);
+        row0 = 0;
+    }
+    const int len = s.end - s.first;
+    Vec<T, V> o;
+    if constexpr (!BACKWARD) {
+        float d[V];
+        load_input<T, V>(d, a, s, row0, len - (W - 1) + j, c);
+#pragma unroll
+        for (int v = 0; v < V; ++v) o.set(v, d[v]);
+        o.store(static_cast<T*>(a.hT) + r * a.D + c);
     } else {
-        *row0 = (int64_t)b * a.T;
-        *n = b;
-        *at = t;
-        *len = a.T;
+        // the input at place j - (W - 1) is tap j - t of token t
+        Taps<W, V> k;
+        k.load(a, c, true);
+        float g[V] = {};
+#pragma unroll
+        for (int t = 0; t < W - 1; ++t) {
+            if (t > j || t >= len) break;
+            float p[V], dy[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) p[v] = k.b[v];
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                float x[V];
+                load_input<T, V>(x, a, s, row0, t - (W - 1) + i, c);
+#pragma unroll
+                for (int v = 0; v < V; ++v) p[v] = fmaf(k.w[i][v], x[v], p[v]);
+            }
+            load_row<T, V>(dy, static_cast<const T*>(a.dy) + (row0 + s.first + t) * a.D + c, true);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float ds = a.silu ? dy[v] * silu_slope(p[v]) : dy[v];
+                float w = 0.f;
+#pragma unroll
+                for (int i = 0; i < W; ++i) w = i == j - t ? k.w[i][v] : w;
+                g[v] = fmaf(w, ds, g[v]);
+            }
+        }
+        const int tail = j - len;                 // its place in the final state of a sequence shorter than that
+        if (a.dhT && tail >= 0) {
+            float d[V];
+            load_row<T, V>(d, static_cast<const T*>(a.dhT) + ((size_t)n * (W - 1) + tail) * a.D + c, true);
+#pragma unroll
+            for (int v = 0; v < V; ++v) g[v] += d[v];
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) o.set(v, g[v]);
+        o.store(static_cast<T*>(a.dh0) + r * a.D + c);
     }
 }
-__device__ __forceinline__ void sequence(const ConvArgs& a, int n, int64_t* row0, int* len) {
-    *row0 = a.cu ? mix::clamp_off(a.cu[n], a.T) : (int64_t)n * a.T;
-    *len = a.cu ? max(mix::clamp_off(a.cu[n + 1], a.T) - (int)*row0, 0) : a.T;
+
+// The grid: for every 32 V channels, the blocks of 8 runs of each batch row, then those of 8 state rows.
+struct Grid { int cols, run_blocks, state_blocks; };
+Grid grid_of(const ConvArgs& a, int V, bool states) {
+    const int runs = (a.T + kRun - 1) / kRun;
+    const int64_t rows = (int64_t)a.N() * (a.W - 1);
+    return {(a.D + 32 * V - 1) / (32 * V), (runs + kWarps - 1) / kWarps, states ? (int)((rows + kWarps - 1) / kWarps) : 0};
 }
 
-template <typename T>
-__global__ void conv_fwd_kernel(const ConvArgs a) {
-    const int64_t id = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, r = id / a.D;
-    const int c = (int)(id % a.D);
-    if (r >= (int64_t)a.B * a.T) return;
-    int64_t row0;
-    int n, at, len;
-    token(a, r, &row0, &n, &at, &len);
-    st(static_cast<T*>(a.y) + r * a.D + c, act(a, pre<T>(a, row0, n, at, c)));
-}
-
-// the last W - 1 inputs of every sequence (forward), and the gradients of the initial ones (backward)
-template <typename T>
-__global__ void conv_state_kernel(const ConvArgs a) {
-    const int64_t id = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, r = id / a.D;
-    const int c = (int)(id % a.D);
-    if (r >= (int64_t)a.N() * (a.W - 1)) return;
-    const int n = (int)(r / (a.W - 1)), j = (int)(r % (a.W - 1));
-    int64_t row0;
-    int len;
-    sequence(a, n, &row0, &len);
-    if (a.hT) st(static_cast<T*>(a.hT) + r * a.D + c, input<T>(a, row0, n, len - (a.W - 1) + j, c));
-    if (a.dh0) st(static_cast<T*>(a.dh0) + r * a.D + c, grad_in<T>(a, row0, n, len, j - (a.W - 1), c));
-}
-
-template <typename T>
-__global__ void conv_bwd_kernel(const ConvArgs a) {
-    const int64_t id = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, r = id / a.D;
-    const int c = (int)(id % a.D);
-    if (r >= (int64_t)a.B * a.T) return;
-    int64_t row0;
-    int n, at, len;
-    token(a, r, &row0, &n, &at, &len);
-    st(static_cast<T*>(a.dx) + r * a.D + c, grad_in<T>(a, row0, n, len, at, c));
-}
-
-constexpr int kRowsPerPart = 128;
-
-// weight gradients of kRowsPerPart tokens of a channel: [W] then the bias's
-template <typename T>
-__global__ void conv_dw_kernel(const ConvArgs a, float* part) {
-    const int c = blockIdx.x * blockDim.x + threadIdx.x;
+template <typename T, int W, int V, bool PACKED>
+__global__ void __launch_bounds__(kWarps * 32) conv_fwd_kernel(const ConvArgs a, const Grid g) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int c = ((int)(blockIdx.x % g.cols) * 32 + lane) * V;
+    const int64_t block = blockIdx.x / g.cols;
     if (c >= a.D) return;
-    float s[5] = {};
-    const int64_t lo = (int64_t)blockIdx.y * kRowsPerPart, rows = (int64_t)a.B * a.T;
-    for (int64_t r = lo; r < min(lo + kRowsPerPart, rows); ++r) {
-        int64_t row0;
-        int n, at, len;
-        token(a, r, &row0, &n, &at, &len);
-        const float g = grad_pre<T>(a, row0, n, at, c);
-        for (int j = 0; j < a.W; ++j) s[j] = fmaf(g, input<T>(a, row0, n, at - a.W + 1 + j, c), s[j]);
-        s[4] += g;
+    if (block >= (int64_t)a.B * g.run_blocks) {
+        const int64_t r = (block - (int64_t)a.B * g.run_blocks) * kWarps + warp;
+        if (r < (int64_t)a.N() * (W - 1)) state_row<T, W, V, false>(a, r, c);
+        return;
     }
-    for (int j = 0; j < 5; ++j) part[((size_t)blockIdx.y * 5 + j) * a.D + c] = s[j];
+    const int b = (int)(block / g.run_blocks), t0 = ((int)(block % g.run_blocks) * kWarps + warp) * kRun;
+    const int t1 = min(t0 + kRun, a.T);
+    if (t0 >= t1) return;
+    const size_t row0 = (size_t)b * a.T;
+    const T* x = static_cast<const T*>(a.x) + (row0 + t0) * a.ldx + c;
+    T* y = static_cast<T*>(a.y) + (row0 + t0) * a.D + c;
+    Vec<T, V> nx[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+        if (t0 + i < t1) nx[i].load(x + i * a.ldx); else nx[i].zero();
+    Taps<W, V> k;
+    k.load(a, c, true);
+    Seq s = sequence_at<PACKED>(a, b, t0);
+    float win[W - 1][V];                          // the last W - 1 inputs, oldest first
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) load_input<T, V>(win[j], a, s, row0, t0 - s.first - (W - 1) + j, c);
+    for (int t = t0; t < t1; t += kAhead) {
+        Vec<T, V> cur[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) cur[i] = nx[i];
+        x += kAhead * a.ldx;
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (t + kAhead + i < t1) nx[i].load(x + i * a.ldx);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            if (t + i >= t1) break;
+            if (PACKED && t + i >= s.end) {
+                s = sequence_at<true>(a, b, t + i);
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j) load_input<T, V>(win[j], a, s, row0, j - (W - 1), c);
+            }
+            Vec<T, V> o;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float xv = cur[i].get(v);
+                float p = k.b[v];
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j) p = fmaf(k.w[j][v], win[j][v], p);
+                p = fmaf(k.w[W - 1][v], xv, p);
+                o.set(v, a.silu ? silu(p) : p);
+#pragma unroll
+                for (int j = 0; j < W - 2; ++j) win[j][v] = win[j + 1][v];
+                win[W - 2][v] = xv;
+            }
+            o.store(y);
+            y += a.D;
+        }
+    }
 }
 
-__global__ void conv_param_kernel(const ConvArgs a, const float* part, int parts) {
-    const int c = blockIdx.x * blockDim.x + threadIdx.x;
-    if (c >= a.D) return;
-    float s[5] = {};
-    for (int k = 0; k < parts; ++k)
-        for (int j = 0; j < 5; ++j) s[j] += part[((size_t)k * 5 + j) * a.D + c];
-    for (int j = 0; j < a.W; ++j) a.dw[(size_t)c * a.W + j] = s[j];
-    if (a.db) a.db[c] = s[4];
+template <typename T, int W, int V, bool PACKED>
+__global__ void __launch_bounds__(kWarps * 32) conv_bwd_kernel(const ConvArgs a, const Grid g, float* part) {
+    __shared__ float sum[kWarps][W + 1][32 * V];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int c = ((int)(blockIdx.x % g.cols) * 32 + lane) * V;
+    const bool live = c < a.D;
+    const int64_t block = blockIdx.x / g.cols;
+    if (block >= (int64_t)a.B * g.run_blocks) {
+        const int64_t r = (block - (int64_t)a.B * g.run_blocks) * kWarps + warp;
+        if (live && r < (int64_t)a.N() * (W - 1)) state_row<T, W, V, true>(a, r, c);
+        return;
+    }
+    const int b = (int)(block / g.run_blocks), t0 = ((int)(block % g.run_blocks) * kWarps + warp) * kRun;
+    const int t1 = live ? min(t0 + kRun, a.T) : t0;            // the run's tokens
+    const int t2 = min(t1 + W - 1, a.T);                       // and those whose ds they need
+    const size_t row0 = (size_t)b * a.T;
+    float dw[W + 1][V];                                        // the taps', then the bias's
+#pragma unroll
+    for (int j = 0; j <= W; ++j)
+#pragma unroll
+        for (int v = 0; v < V; ++v) dw[j][v] = 0.f;
+    if (t0 < t1) {
+        const T* x = static_cast<const T*>(a.x) + (row0 + t0) * a.ldx + c;
+        const T* dy = static_cast<const T*>(a.dy) + (row0 + t0) * a.D + c;
+        T* dx = static_cast<T*>(a.dx) + (row0 + t0) * a.D + c;
+        constexpr int kNext = kAhead / 2;
+        Vec<T, V> nx[kNext], ny[kNext];
+#pragma unroll
+        for (int i = 0; i < kNext; ++i) {
+            if (t0 + i < t2) nx[i].load(x + i * a.ldx); else nx[i].zero();
+            if (t0 + i < t2) ny[i].load(dy + i * a.D); else ny[i].zero();
+        }
+        Taps<W, V> k;
+        k.load(a, c, true);
+        Seq s = sequence_at<PACKED>(a, b, t0);
+        float win[W - 1][V], ds[W - 1][V];                     // the last W - 1 inputs and ds, oldest first
+        Seq own[W - 1];                                        // the sequences of the last W - 1 tokens
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) {
+            load_input<T, V>(win[j], a, s, row0, t0 - s.first - (W - 1) + j, c);
+            own[j] = s;
+#pragma unroll
+            for (int v = 0; v < V; ++v) ds[j][v] = 0.f;
+        }
+        // token t brings ds_t; dx of token t - (W - 1) is then complete (past the row's end ds is 0)
+        for (int t = t0; t < t1 + W - 1; t += kNext) {
+            Vec<T, V> cx[kNext], cy[kNext];
+#pragma unroll
+            for (int i = 0; i < kNext; ++i) {
+                cx[i] = nx[i];
+                cy[i] = ny[i];
+            }
+            x += kNext * a.ldx;
+            dy += kNext * (size_t)a.D;
+#pragma unroll
+            for (int i = 0; i < kNext; ++i) {
+                if (t + kNext + i < t2) nx[i].load(x + i * a.ldx); else nx[i].zero();
+                if (t + kNext + i < t2) ny[i].load(dy + i * a.D); else ny[i].zero();
+            }
+#pragma unroll
+            for (int i = 0; i < kNext; ++i) {
+                const int now = t + i, out = now - (W - 1);
+                if (now >= t1 + W - 1) break;
+                if (PACKED && now >= s.end && now < a.T) {
+                    s = sequence_at<true>(a, b, now);
+#pragma unroll
+                    for (int j = 0; j < W - 1; ++j) load_input<T, V>(win[j], a, s, row0, j - (W - 1), c);
+                }
+                // tokens from here on that belong to another sequence do not reach token `out`
+                const int reach = PACKED ? own[0].end - out : a.T - out;       // ds at out .. out + reach - 1 count
+                float d[V], gx[V];
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    const float xv = cx[i].get(v);
+                    float p = k.b[v];
+#pragma unroll
+                    for (int j = 0; j < W - 1; ++j) p = fmaf(k.w[j][v], win[j][v], p);
+                    p = fmaf(k.w[W - 1][v], xv, p);
+                    d[v] = cy[i].get(v);
+                    if (a.silu) d[v] *= silu_slope(p);
+                    if (now >= a.T) d[v] = 0.f;
+                    if (now < t1) {
+#pragma unroll
+                        for (int j = 0; j < W - 1; ++j) dw[j][v] = fmaf(d[v], win[j][v], dw[j][v]);
+                        dw[W - 1][v] = fmaf(d[v], xv, dw[W - 1][v]);
+                        dw[W][v] += d[v];
+                    }
+#pragma unroll
+                    for (int j = 0; j < W - 2; ++j) win[j][v] = win[j + 1][v];
+                    win[W - 2][v] = xv;
+                    // tap W - 1 - i of token out + i; the newest ds has tap 0
+                    gx[v] = k.w[W - 1][v] * ds[0][v];
+#pragma unroll
+                    for (int m = 1; m < W - 1; ++m)
+                        gx[v] = !PACKED || m < reach ? fmaf(k.w[W - 1 - m][v], ds[m][v], gx[v]) : gx[v];
+                    gx[v] = !PACKED || W - 1 < reach ? fmaf(k.w[0][v], d[v], gx[v]) : gx[v];
+#pragma unroll
+                    for (int j = 0; j < W - 2; ++j) ds[j][v] = ds[j + 1][v];
+                    ds[W - 2][v] = d[v];
+                }
+                if (out >= t0) {
+                    const int tail = W - 1 - reach;            // its place in its sequence's final state
+                    if (a.dhT && tail >= 0) {
+                        float e[V];
+                        load_row<T, V>(e, static_cast<const T*>(a.dhT) + ((size_t)own[0].n * (W - 1) + tail) * a.D + c, true);
+#pragma unroll
+                        for (int v = 0; v < V; ++v) gx[v] += e[v];
+                    }
+                    Vec<T, V> o;
+#pragma unroll
+                    for (int v = 0; v < V; ++v) o.set(v, gx[v]);
+                    o.store(dx);
+                    dx += a.D;
+                }
+                if (PACKED) {
+#pragma unroll
+                    for (int j = 0; j < W - 2; ++j) own[j] = own[j + 1];
+                    own[W - 2] = s;
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j <= W; ++j)
+#pragma unroll
+        for (int v = 0; v < V; ++v) sum[warp][j][lane * V + v] = dw[j][v];
+    __syncthreads();
+    // part [W + 1][blocks][D]
+    const int64_t rows = (int64_t)a.B * g.run_blocks;
+    for (int i = threadIdx.x; i < (W + 1) * 32 * V; i += kWarps * 32) {
+        const int j = i / (32 * V), lc = i % (32 * V), cc = (int)(blockIdx.x % g.cols) * 32 * V + lc;
+        if (cc >= a.D) continue;
+        float t = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) t += sum[w][j][lc];
+        part[(j * rows + block) * a.D + cc] = t;
+    }
 }
 
-template <typename T>
-__global__ void conv_step_kernel(const ConvArgs a, const T* state, T* out) {
-    const int64_t id = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, n = id / a.D;
-    const int c = (int)(id % a.D);
+// sums over the blocks: 32 channels a block, 8 row lanes, joined in order; blockIdx.y is the tap, or W for the bias
+__global__ void __launch_bounds__(256) conv_param_kernel(const float* part, int64_t rows, int D, int W, float* dw, float* db) {
+    __shared__ float s[8][32];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, c = blockIdx.x * 32 + lane, j = blockIdx.y;
+    if (j == W && !db) return;
+    float acc = 0.f;
+    if (c < D)
+#pragma unroll 4
+        for (int64_t r = w; r < rows; r += 8) acc += part[(j * rows + r) * D + c];
+    s[w][lane] = acc;
+    __syncthreads();
+    if (w == 0 && c < D) {
+        float t = 0.f;
+        for (int i = 0; i < 8; ++i) t += s[i][lane];
+        if (j < W) dw[(size_t)c * W + j] = t; else db[c] = t;
+    }
+}
+
+template <typename T, int W, int V>
+__global__ void __launch_bounds__(128) conv_step_kernel(const ConvArgs a, const T* state, T* out) {
+    const int64_t id = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    const int cols = a.D / V;
+    const int64_t n = id / cols;
+    const int c = (int)(id - n * cols) * V;
     if (n >= a.B) return;
-    const T* h = state + n * (a.W - 1) * a.D + c;
-    T* o = out + n * (a.W - 1) * a.D + c;
-    const T x = static_cast<const T*>(a.x)[n * a.ldx + c];
-    float p = a.b ? a.b[c] : 0.f;
-    for (int j = 0; j < a.W - 1; ++j) {
-        const T v = h[(int64_t)j * a.D];
-        p = fmaf(a.w[(size_t)c * a.W + j], ld(&v), p);
-        if (j > 0) o[(int64_t)(j - 1) * a.D] = v;
+    const T* h = state + n * (W - 1) * a.D + c;
+    T* o = out + n * (W - 1) * a.D + c;
+    Vec<T, V> win[W], y;
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) win[j].load(h + (int64_t)j * a.D);
+    win[W - 1].load(static_cast<const T*>(a.x) + n * a.ldx + c);
+    Taps<W, V> k;
+    k.load(a, c, true);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        float p = k.b[v];
+#pragma unroll
+        for (int j = 0; j < W; ++j) p = fmaf(k.w[j][v], win[j].get(v), p);
+        y.set(v, a.silu ? silu(p) : p);
     }
-    p = fmaf(a.w[(size_t)c * a.W + a.W - 1], ld(&x), p);
-    o[(int64_t)(a.W - 2) * a.D] = x;
-    st(static_cast<T*>(a.y) + n * a.D + c, act(a, p));
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) win[j + 1].store(o + (int64_t)j * a.D);
+    y.store(static_cast<T*>(a.y) + n * a.D + c);
 }
 
-// (grid.y of the weight gradients: up to 65,535 parts, 8M tokens; mixer_api.cu refuses more)
-unsigned blocks_for(int64_t n) { return (unsigned)((n + 127) / 128); }
-int parts_of(const ConvArgs& a) { return (int)(((int64_t)a.B * a.T + kRowsPerPart - 1) / kRowsPerPart); }
-
-template <typename T>
-cudaError_t fwd(const ConvArgs& a, cudaStream_t s) {
-    const int64_t rows = (int64_t)a.B * a.T;
-    if (rows > 0) conv_fwd_kernel<T><<<blocks_for(rows * a.D), 128, 0, s>>>(a);
-    if (a.hT) conv_state_kernel<T><<<blocks_for((int64_t)a.N() * (a.W - 1) * a.D), 128, 0, s>>>(a);
-    return cudaGetLastError();
+// Whether rows can be accessed V channels at a time.
+bool vector_ok(const ConvArgs& a, int V, const void* state = nullptr, const void* state_out = nullptr) {
+    const size_t bytes = V * (a.bf16 ? 2 : 4);
+    const auto al = [&](const void* p) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; };
+    return a.D % V == 0 && a.ldx % V == 0 && al(a.x) && al(a.h0) && al(a.hT) && al(a.y) && al(a.dy) && al(a.dhT) &&
+           al(a.dx) && al(a.dh0) && al(state) && al(state_out);
 }
-
-template <typename T>
-cudaError_t bwd(const ConvArgs& a, cudaStream_t s) {
-    const int64_t rows = (int64_t)a.B * a.T;
-    float* part = static_cast<float*>(a.ws);
-    if (rows > 0) {
-        conv_bwd_kernel<T><<<blocks_for(rows * a.D), 128, 0, s>>>(a);
-        conv_dw_kernel<T><<<dim3((a.D + 127) / 128, parts_of(a)), 128, 0, s>>>(a, part);
-    }
-    conv_param_kernel<<<(a.D + 127) / 128, 128, 0, s>>>(a, part, parts_of(a));
-    if (a.dh0) conv_state_kernel<T><<<blocks_for((int64_t)a.N() * (a.W - 1) * a.D), 128, 0, s>>>(a);
-    return cudaGetLastError();
+template <typename F>
+void by_width(int W, F f) {
+    if (W == 2) f(std::integral_constant<int, 2>{});
+    else if (W == 3) f(std::integral_constant<int, 3>{});
+    else f(std::integral_constant<int, 4>{});
+}
+template <typename F>
+void by_type(const ConvArgs& a, bool wide, F f) {
+    const auto vec = [&](auto* t) {
+        if (wide) f(t, std::integral_constant<int, 4>{});
+        else f(t, std::integral_constant<int, 1>{});
+    };
+    if (a.bf16) vec((bf16*)nullptr);
+    else vec((float*)nullptr);
 }
 
 }  // namespace
 
-size_t conv_workspace_bytes(const ConvArgs& a) { return (size_t)parts_of(a) * 5 * a.D * sizeof(float); }
-cudaError_t launch_conv_fwd(const ConvArgs& a, cudaStream_t s) { return a.bf16 ? fwd<bf16>(a, s) : fwd<float>(a, s); }
-cudaError_t launch_conv_bwd(const ConvArgs& a, cudaStream_t s) { return a.bf16 ? bwd<bf16>(a, s) : bwd<float>(a, s); }
+size_t conv_workspace_bytes(const ConvArgs& a) {
+    return (size_t)a.B * grid_of(a, 1, false).run_blocks * (a.W + 1) * a.D * sizeof(float);
+}
+
+cudaError_t launch_conv_fwd(const ConvArgs& a, cudaStream_t s) {
+    by_width(a.W, [&](auto w) {
+        by_type(a, vector_ok(a, 4), [&](auto* t, auto v) {
+            using T = std::remove_pointer_t<decltype(t)>;
+            const Grid g = grid_of(a, v.value, a.hT != nullptr);
+            const unsigned blocks = (unsigned)(g.cols * ((int64_t)a.B * g.run_blocks + g.state_blocks));
+            if (blocks == 0) return;
+            if (a.cu) conv_fwd_kernel<T, w.value, v.value, true><<<blocks, kWarps * 32, 0, s>>>(a, g);
+            else conv_fwd_kernel<T, w.value, v.value, false><<<blocks, kWarps * 32, 0, s>>>(a, g);
+        });
+    });
+    return cudaGetLastError();
+}
+
+cudaError_t launch_conv_bwd(const ConvArgs& a, cudaStream_t s) {
+    float* part = static_cast<float*>(a.ws);
+    int64_t rows = 0;
+    by_width(a.W, [&](auto w) {
+        by_type(a, vector_ok(a, 4), [&](auto* t, auto v) {
+            using T = std::remove_pointer_t<decltype(t)>;
+            const Grid g = grid_of(a, v.value, a.dh0 != nullptr);
+            rows = (int64_t)a.B * g.run_blocks;
+            const unsigned blocks = (unsigned)(g.cols * (rows + g.state_blocks));
+            if (blocks == 0) return;
+            if (a.cu) conv_bwd_kernel<T, w.value, v.value, true><<<blocks, kWarps * 32, 0, s>>>(a, g, part);
+            else conv_bwd_kernel<T, w.value, v.value, false><<<blocks, kWarps * 32, 0, s>>>(a, g, part);
+        });
+    });
+    conv_param_kernel<<<dim3((a.D + 31) / 32, a.W + 1), 256, 0, s>>>(part, rows, a.D, a.W, a.dw, a.db);
+    return cudaGetLastError();
+}
 
 cudaError_t launch_conv_step(const ConvArgs& a, const void* state, void* state_out, cudaStream_t s) {
-    const unsigned blocks = blocks_for((int64_t)a.B * a.D);
-    if (a.bf16)
-        conv_step_kernel<bf16><<<blocks, 128, 0, s>>>(a, static_cast<const bf16*>(state), static_cast<bf16*>(state_out));
-    else
-        conv_step_kernel<float><<<blocks, 128, 0, s>>>(a, static_cast<const float*>(state),
-                                                       static_cast<float*>(state_out));
+    by_width(a.W, [&](auto w) {
+        by_type(a, vector_ok(a, 4, state, state_out), [&](auto* t, auto v) {
+            using T = std::remove_pointer_t<decltype(t)>;
+            const int64_t threads = (int64_t)a.B * (a.D / v.value);
+            conv_step_kernel<T, w.value, v.value><<<(unsigned)((threads + 127) / 128), 128, 0, s>>>(
+                a, static_cast<const T*>(state), static_cast<T*>(state_out));
+        });
+    });
     return cudaGetLastError();
 }
 
