@@ -38,13 +38,14 @@ glr_fwd_kernel(const GlrArgs a, const Exchange x, const int publish) {
         const int n = at.live ? at.count : 0;
 #pragma unroll
         for (int j = 0; j < L; ++j) {
-            copy_async(bg + j * kThreads, j < n ? g : static_cast<const Tg*>(a.g), j < n);
-            copy_async(bx + j * kThreads, j < n ? xp : static_cast<const Tx*>(a.x), j < n);
-            if (a.gi) copy_async(bi + j * kThreads, j < n ? ip : static_cast<const Tx*>(a.gi), j < n);
+            mix::copy_async(bg + j * kThreads, j < n ? g : static_cast<const Tg*>(a.g), j < n);
+            mix::copy_async(bx + j * kThreads, j < n ? xp : static_cast<const Tx*>(a.x), j < n);
+            if (a.gi) mix::copy_async(bi + j * kThreads, j < n ? ip : static_cast<const Tx*>(a.gi), j < n);
             g += a.ldg;
             xp += a.ldx;
             ip += a.ldi;
         }
+        mix::copies_close();
     };
     unsigned ticket = 0;
     int id = blockIdx.x;
@@ -70,7 +71,7 @@ glr_fwd_kernel(const GlrArgs a, const Exchange x, const int publish) {
             for (int j = 0; j < L; ++j) starts |= (s_start[k][run * L + j] >= 0 ? 1u : 0u) << j;
         }
         float al[L][V], u[L][V];
-        copies_done();
+        mix::copies_wait<0>();
 #pragma unroll
         for (int j = 0; j < L; ++j) {
             const Vec<Tg, V> g = bg[j * kThreads];

@@ -149,20 +149,6 @@ __device__ __forceinline__ Channel channel(const float* A_log, const float* dt_b
     return {A_log ? -expf(A_log[c]) : 0.f, dt_bias ? dt_bias[c] : 0.f};
 }
 
-// Copy V elements into shared memory without waiting (or zeros); the copying thread alone reads them.
-template <typename T, int V>
-__device__ __forceinline__ void copy_async(mix::Vec<T, V>* dst, const T* src, bool in) {
-    constexpr int N = sizeof(T) * V;
-    if constexpr (N >= 4) {
-        const unsigned d = static_cast<unsigned>(__cvta_generic_to_shared(dst));
-        const int size = in ? N : 0;
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(d), "l"(src), "n"(N), "r"(size) : "memory");
-    } else {                                     // (two bytes: no asynchronous form)
-        if (in) dst->load(src); else dst->zero();
-    }
-}
-__device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-
 // A block's place in its current tile.
 template <int LANES, int V>
 struct Place {

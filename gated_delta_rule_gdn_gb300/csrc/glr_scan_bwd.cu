@@ -46,15 +46,16 @@ glr_bwd_kernel(const GlrArgs a, const Exchange x, float* part) {
         const int n = at.live ? at.count : 0;
 #pragma unroll
         for (int j = 0; j < L; ++j) {
-            copy_async(bg + j * kThreads, j < n ? g : static_cast<const Tg*>(a.g), j < n);
-            copy_async(bx + j * kThreads, j < n ? xp : static_cast<const Tx*>(a.x), j < n);
-            if (a.gi) copy_async(bi + j * kThreads, j < n ? ip : static_cast<const Tx*>(a.gi), j < n);
-            copy_async(bo + j * kThreads, j < n ? op : static_cast<const Tx*>(a.dO), j < n);
+            mix::copy_async(bg + j * kThreads, j < n ? g : static_cast<const Tg*>(a.g), j < n);
+            mix::copy_async(bx + j * kThreads, j < n ? xp : static_cast<const Tx*>(a.x), j < n);
+            if (a.gi) mix::copy_async(bi + j * kThreads, j < n ? ip : static_cast<const Tx*>(a.gi), j < n);
+            mix::copy_async(bo + j * kThreads, j < n ? op : static_cast<const Tx*>(a.dO), j < n);
             g += a.ldg;
             xp += a.ldx;
             ip += a.ldi;
             op += a.D;
         }
+        mix::copies_close();
     };
     // the state that enters the tile, for the threads that run the states through it (tid - W is their channel)
     const auto entry_state = [&]() {
@@ -94,7 +95,7 @@ glr_bwd_kernel(const GlrArgs a, const Exchange x, float* part) {
         //   dx = D w, di = dx y, dla = D (a h_{t-1} - m), dg = dla w3, dA_log = sum dla la
         //   w = s sigma(i), y = x (1 - sigma(i)), m = sigma(i) x a^2 / s, w3 = dla/dg
         float al[L][V], u[L][V], w[L][V], y[L][V], m[L][V], w3[L][V], la[L][V], dO[L][V];
-        copies_done();
+        mix::copies_wait<0>();
 #pragma unroll
         for (int j = 0; j < L; ++j) {
             const Vec<Tg, V> g = bg[j * kThreads];

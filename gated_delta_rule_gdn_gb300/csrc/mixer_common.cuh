@@ -42,6 +42,55 @@ __device__ __forceinline__ void of_f32(bf16* d, float x) { *d = __float2bfloat16
 template <typename T, int N> __device__ __forceinline__ float Vec<T, N>::get(int i) const { return to_f32(e[i]); }
 template <typename T, int N> __device__ __forceinline__ void Vec<T, N>::set(int i, float x) { of_f32(&e[i], x); }
 
+// d = a * b + c (and d = a * b) over N floats, two to an instruction where N is even.
+template <int N>
+__device__ __forceinline__ void fma_row(float (&d)[N], const float (&a)[N], const float (&b)[N], const float (&c)[N]) {
+    if constexpr (N % 2 == 0) {
+#pragma unroll
+        for (int i = 0; i < N; i += 2)
+            asm("{\n\t.reg .b64 x, y, z;\n\t"
+                "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+                "fma.rn.f32x2 z, x, y, z;\n\tmov.b64 {%0, %1}, z;\n\t}"
+                : "=f"(d[i]), "=f"(d[i + 1])
+                : "f"(a[i]), "f"(a[i + 1]), "f"(b[i]), "f"(b[i + 1]), "f"(c[i]), "f"(c[i + 1]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) d[i] = fmaf(a[i], b[i], c[i]);
+    }
+}
+template <int N>
+__device__ __forceinline__ void mul_row(float (&d)[N], const float (&a)[N], const float (&b)[N]) {
+    if constexpr (N % 2 == 0) {
+#pragma unroll
+        for (int i = 0; i < N; i += 2)
+            asm("{\n\t.reg .b64 x, y;\n\t"
+                "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+                "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+                : "=f"(d[i]), "=f"(d[i + 1])
+                : "f"(a[i]), "f"(a[i + 1]), "f"(b[i]), "f"(b[i + 1]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) d[i] = a[i] * b[i];
+    }
+}
+
+// Copy V elements into shared memory without waiting (or zeros); the copying thread alone reads them.
+template <typename T, int V>
+__device__ __forceinline__ void copy_async(Vec<T, V>* dst, const T* src, bool in) {
+    constexpr int N = sizeof(T) * V;
+    if constexpr (N >= 4) {
+        const unsigned d = static_cast<unsigned>(__cvta_generic_to_shared(dst));
+        const int size = in ? N : 0;
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(d), "l"(src), "n"(N), "r"(size) : "memory");
+    } else {                                     // (two bytes: no asynchronous form)
+        if (in) dst->load(src); else dst->zero();
+    }
+}
+__device__ __forceinline__ void copies_close() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// wait until at most N of the closed groups are under way
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
 // Packed sequences: the one that token t belongs to, with its first token and one past its last.  Every offset is
 // clamped into [0, T], and the answer always satisfies 0 <= first <= t < end <= T, so a malformed array cannot lead
 // an access outside the tensors.

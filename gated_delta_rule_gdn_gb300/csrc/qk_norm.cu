@@ -87,11 +87,11 @@ struct Angles {
     template <int G>
     __device__ __forceinline__ void turn(float (&y)[E], float sign) const {
         if (ROT == kHalves) {
-            // a lane past the rotated channels is its own partner, with sin = 0
+            // a lane past the rotated channels is its own partner, with cos = 1 and sin = 0
 #pragma unroll
             for (int i = 0; i < E; ++i) {
                 const float o = __shfl_sync(~0u, y[i], partner, G);
-                y[i] = s[i] == 0.f ? y[i] * c[i] : fmaf(y[i], c[i], sign * s[i] * o);
+                y[i] = fmaf(sign * s[i], o, y[i] * c[i]);
             }
         } else if (ROT == kInterleaved) {
 #pragma unroll
@@ -104,113 +104,121 @@ struct Angles {
     }
 };
 
-// a group's share of the work: kHeads heads (of q's, then k's) of a token
-template <int G>
+// A group's share of the work: kHeads heads of q, or of k, of one token.  The token's shares are those of q, then of k.
+struct Shares { unsigned of_q, all; };
+template <typename T, int G>
 struct Share {
-    int64_t tok;
-    int head0, lane;
+    unsigned tok;
+    int which, count, j0;             // tensor, heads, the lane's first channel
+    const T* x;                       // the lane's channels of the first head in the input, and the same in contiguous
+    size_t at;                        // tensors
     bool in;                          // the lane's channels exist
-    __device__ __forceinline__ Share(const QkNormArgs& a, unsigned item, unsigned parts) {
-        const unsigned t = item / parts;
-        tok = t;
-        head0 = (int)(item - t * parts) * kHeads;
-        lane = threadIdx.x % G;
-        in = lane * E < a.d;
+    int64_t step;                     // between the input's heads
+    __device__ __forceinline__ Share(const QkNormArgs& a, const Shares& sh, unsigned item) {
+        tok = item / sh.all;
+        unsigned part = item - tok * sh.all;
+        which = part >= sh.of_q;
+        if (which) part -= sh.of_q;
+        const int h = (int)part * kHeads, H = which ? a.H[1] : a.H[0];
+        count = min(H - h, kHeads);
+        j0 = (int)(threadIdx.x % G) * E;
+        in = j0 < a.d;
+        step = which ? a.head_stride[1] : a.head_stride[0];
+        x = static_cast<const T*>(which ? a.in[1] : a.in[0]) + (int64_t)tok * (which ? a.tok_stride[1] : a.tok_stride[0]) +
+            h * step + j0;
+        at = ((size_t)tok * H + h) * a.d + j0;
     }
 };
 
 template <typename T, int G, int ROT>
-__global__ void __launch_bounds__(kThreads) qk_fwd_kernel(const QkNormArgs a, const int parts) {
+__global__ void __launch_bounds__(kThreads) qk_fwd_kernel(const QkNormArgs a, const Shares sh, const unsigned items) {
     const unsigned item = blockIdx.x * (kThreads / G) + threadIdx.x / G;
-    const Share<G> w(a, min(item, (unsigned)(a.n * parts - 1)), parts);      // (the last block repeats the last share)
-    const int heads = a.H[0] + a.H[1], j0 = w.lane * E;
+    const Share<T, G> w(a, sh, min(item, items - 1));            // (the last block repeats the last share)
     Eight<T> x[kHeads];
 #pragma unroll
-    for (int i = 0; i < kHeads; ++i) {
-        const int hh = w.head0 + i, k = hh >= a.H[0], h = k ? hh - a.H[0] : hh;
-        if (w.in && hh < heads)
-            x[i].load(static_cast<const T*>(a.in[k]) + w.tok * a.tok_stride[k] + h * a.head_stride[k] + j0);
-        else
-            x[i].zero();
-    }
+    for (int i = 0; i < kHeads; ++i)
+        if (w.in && i < w.count) x[i].load(w.x + i * w.step); else x[i].zero();
     Angles<ROT> ang;
-    if (ROT != kNone) ang.load(a, position(a, w.tok), w.lane);
+    if (ROT != kNone) ang.load(a, position(a, w.tok), (int)threadIdx.x % G);
+    const float* wt = w.which ? a.w[1] : a.w[0];
+    float weight[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) weight[e] = wt && w.in ? wt[w.j0 + e] : 1.f;
+    T* y = static_cast<T*>(w.which ? a.out[1] : a.out[0]) + w.at;
 #pragma unroll
     for (int i = 0; i < kHeads; ++i) {
-        const int hh = w.head0 + i, k = hh >= a.H[0], h = k ? hh - a.H[0] : hh;
-        float y[E], ss = 0.f;
+        float v[E], ss = 0.f;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            y[e] = x[i].get(e);
-            ss = fmaf(y[e], y[e], ss);
+            v[e] = x[i].get(e);
+            ss = fmaf(v[e], v[e], ss);
         }
         const float r = rsqrtf(fmaf(a.c, group_sum<G>(ss), a.eps));
-        const float* wt = k ? a.w[1] : a.w[0];
 #pragma unroll
-        for (int e = 0; e < E; ++e) y[e] *= r;
-        if (wt && w.in)
+        for (int e = 0; e < E; ++e) v[e] *= r * weight[e];
+        ang.template turn<G>(v, 1.f);
 #pragma unroll
-            for (int e = 0; e < E; ++e) y[e] *= wt[j0 + e];
-        ang.template turn<G>(y, 1.f);
-#pragma unroll
-        for (int e = 0; e < E; ++e) x[i].set(e, y[e]);
-        if (w.in && hh < heads) x[i].store(static_cast<T*>(a.out[k]) + (w.tok * a.H[k] + h) * a.d + j0);
+        for (int e = 0; e < E; ++e) x[i].set(e, v[e]);
+        if (w.in && i < w.count) x[i].store(y);
+        y += a.d;
     }
 }
 
 // persistent blocks: the weight gradients of a block's heads stay in registers and leave as one row of partial sums
 template <typename T, int G, int ROT>
-__global__ void __launch_bounds__(kThreads) qk_bwd_kernel(const QkNormArgs a, const int parts, float* part) {
+__global__ void __launch_bounds__(kThreads, 2) qk_bwd_kernel(const QkNormArgs a, const Shares sh, const unsigned items,
+                                                             float* part) {
     constexpr int kGroups = kThreads / G;
     __shared__ float sw[2][kGroups][G * E];
-    const int heads = a.H[0] + a.H[1];
     float acc[2][E] = {};
-    const int64_t items = a.n * parts;
-    for (int64_t base = (int64_t)blockIdx.x * kGroups; base < items; base += (int64_t)gridDim.x * kGroups) {
-        const int64_t item = base + threadIdx.x / G;
-        const bool real = item < items;
-        const Share<G> w(a, (unsigned)(real ? item : items - 1), parts);
-        const int j0 = w.lane * E;
+    for (unsigned base = blockIdx.x * kGroups; base < items; base += gridDim.x * kGroups) {
+        const unsigned item = base + threadIdx.x / G;
+        const Share<T, G> w(a, sh, min(item, items - 1));
+        const int count = item < items && w.in ? w.count : 0;
         Eight<T> x[kHeads], dz[kHeads];
+        const T* dp = static_cast<const T*>(w.which ? a.dout[1] : a.dout[0]) + w.at;
 #pragma unroll
         for (int i = 0; i < kHeads; ++i) {
-            const int hh = w.head0 + i, k = hh >= a.H[0], h = k ? hh - a.H[0] : hh;
-            if (w.in && real && hh < heads) {
-                x[i].load(static_cast<const T*>(a.in[k]) + w.tok * a.tok_stride[k] + h * a.head_stride[k] + j0);
-                dz[i].load(static_cast<const T*>(a.dout[k]) + (w.tok * a.H[k] + h) * a.d + j0);
-            } else {
-                x[i].zero();
-                dz[i].zero();
-            }
+            if (i < count) x[i].load(w.x + i * w.step); else x[i].zero();
+            if (i < count) dz[i].load(dp + (size_t)i * a.d); else dz[i].zero();
         }
         Angles<ROT> ang;
-        if (ROT != kNone) ang.load(a, position(a, w.tok), w.lane);
+        if (ROT != kNone) ang.load(a, position(a, w.tok), (int)threadIdx.x % G);
+        const float* wt = w.which ? a.w[1] : a.w[0];
+        T* out = static_cast<T*>(w.which ? a.out[1] : a.out[0]) + w.at;
+        float sum[E] = {};
 #pragma unroll
         for (int i = 0; i < kHeads; ++i) {
-            const int hh = w.head0 + i, k = hh >= a.H[0], h = k ? hh - a.H[0] : hh;
-            float e[E], ss = 0.f, xe = 0.f;
+            float e[E], v[E], ss = 0.f, xe = 0.f;
 #pragma unroll
             for (int c = 0; c < E; ++c) {
                 e[c] = dz[i].get(c);
-                ss = fmaf(x[i].get(c), x[i].get(c), ss);
+                v[c] = x[i].get(c);
+                ss = fmaf(v[c], v[c], ss);
             }
             ang.template turn<G>(e, -1.f);
             const float r = rsqrtf(fmaf(a.c, group_sum<G>(ss), a.eps));
-            const float* wt = k ? a.w[1] : a.w[0];
-            if (wt && w.in) {
+#pragma unroll
+            for (int c = 0; c < E; ++c) v[c] *= r;
+            if (wt) {
 #pragma unroll
                 for (int c = 0; c < E; ++c) {
-                    const float t = e[c] * x[i].get(c) * r;
-                    if (k) acc[1][c] += t; else acc[0][c] += t;
-                    e[c] *= wt[j0 + c];
+                    sum[c] = fmaf(e[c], v[c], sum[c]);
+                    e[c] *= w.in ? wt[w.j0 + c] : 0.f;
                 }
             }
 #pragma unroll
-            for (int c = 0; c < E; ++c) xe = fmaf(x[i].get(c), e[c], xe);
-            xe = group_sum<G>(xe) * a.c * r * r;
+            for (int c = 0; c < E; ++c) xe = fmaf(v[c], e[c], xe);
+            xe = group_sum<G>(xe) * a.c;
 #pragma unroll
-            for (int c = 0; c < E; ++c) x[i].set(c, r * fmaf(-x[i].get(c), xe, e[c]));
-            if (w.in && real && hh < heads) x[i].store(static_cast<T*>(a.out[k]) + (w.tok * a.H[k] + h) * a.d + j0);
+            for (int c = 0; c < E; ++c) x[i].set(c, r * fmaf(-v[c], xe, e[c]));
+            if (i < count) x[i].store(out);
+            out += a.d;
+        }
+#pragma unroll
+        for (int c = 0; c < E; ++c) {
+            acc[0][c] += w.which ? 0.f : sum[c];
+            acc[1][c] += w.which ? sum[c] : 0.f;
         }
     }
     if (!part) return;
@@ -387,7 +395,10 @@ bool vector_ok(const QkNormArgs& a, bool backward) {
 
 constexpr int kBwdBlocks = 152 * 4;
 int64_t groups_per_block(int d) { return d <= 64 ? 32 : d <= 128 ? 16 : 8; }
-int parts_of(const QkNormArgs& a) { return (a.H[0] + a.H[1] + kHeads - 1) / kHeads; }
+Shares shares_of(const QkNormArgs& a) {
+    const unsigned q = (a.H[0] + kHeads - 1) / kHeads, k = (a.H[1] + kHeads - 1) / kHeads;
+    return {q, q + k};
+}
 
 // f(group size, rotation) as compile-time constants
 template <typename F>
@@ -405,10 +416,11 @@ void by_shape(const QkNormArgs& a, F f) {
 template <typename T>
 cudaError_t fwd(const QkNormArgs& a, cudaStream_t s) {
     if (vector_ok(a, false)) {
-        const int parts = parts_of(a);
+        const Shares sh = shares_of(a);
+        const unsigned items = (unsigned)(a.n * sh.all);         // (at most tokens times heads, which fits)
         by_shape(a, [&](auto g, auto rot) {
-            const int64_t per = kThreads / g.value;
-            qk_fwd_kernel<T, g.value, rot.value><<<(unsigned)((a.n * parts + per - 1) / per), kThreads, 0, s>>>(a, parts);
+            const unsigned per = kThreads / g.value;
+            qk_fwd_kernel<T, g.value, rot.value><<<(items + per - 1) / per, kThreads, 0, s>>>(a, sh, items);
         });
     } else {
         const int64_t rows = a.n * (a.H[0] + a.H[1]);
@@ -423,11 +435,12 @@ cudaError_t bwd(const QkNormArgs& a, cudaStream_t s) {
     float* part = weights ? static_cast<float*>(a.ws) : nullptr;
     int blocks = 0;                            // none without tokens: the weight gradients are then zero
     if (a.n > 0 && vector_ok(a, true)) {
-        const int parts = parts_of(a);
-        const int64_t per = groups_per_block(a.d), want = (a.n * parts + per - 1) / per;
+        const Shares sh = shares_of(a);
+        const unsigned items = (unsigned)(a.n * sh.all);
+        const int64_t per = groups_per_block(a.d), want = (items + per - 1) / per;
         blocks = (int)(want < kBwdBlocks ? want : kBwdBlocks);
         by_shape(a, [&](auto g, auto rot) {
-            qk_bwd_kernel<T, g.value, rot.value><<<blocks, kThreads, 0, s>>>(a, parts, part);
+            qk_bwd_kernel<T, g.value, rot.value><<<blocks, kThreads, 0, s>>>(a, sh, items, part);
         });
     } else if (a.n > 0) {
         const int64_t want = (a.n * (a.H[0] + a.H[1]) + kWarps - 1) / kWarps;

@@ -21,7 +21,9 @@ namespace {
 using mix::bf16;
 using mix::Vec;
 
-constexpr int kWarps = 8, kRun = 32, kAhead = 8;
+// A thread's inputs come through a ring of its own in shared memory, kRing tokens deep, kChunk tokens a copy group.
+constexpr int kWarps = 8, kRun = 32, kChunk = 4, kRing = 16, kThreads = kWarps * 32;
+static_assert(kRing % kChunk == 0 && kRun % kChunk == 0, "whole groups");
 
 __device__ __forceinline__ float ex2(float x) { float y; asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x)); return y; }
 __device__ __forceinline__ float rcp(float x) { float y; asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x)); return y; }
@@ -141,7 +143,9 @@ Grid grid_of(const ConvArgs& a, int V, bool states) {
 }
 
 template <typename T, int W, int V, bool PACKED>
-__global__ void __launch_bounds__(kWarps * 32) conv_fwd_kernel(const ConvArgs a, const Grid g) {
+__global__ void __launch_bounds__(kThreads) conv_fwd_kernel(const ConvArgs a, const Grid g) {
+    extern __shared__ __align__(16) unsigned char s_raw[];
+    auto* ring = reinterpret_cast<Vec<T, V>*>(s_raw) + threadIdx.x;           // [kRing][256]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int c = ((int)(blockIdx.x % g.cols) * 32 + lane) * V;
     const int64_t block = blockIdx.x / g.cols;
@@ -157,54 +161,63 @@ __global__ void __launch_bounds__(kWarps * 32) conv_fwd_kernel(const ConvArgs a,
     const size_t row0 = (size_t)b * a.T;
     const T* x = static_cast<const T*>(a.x) + (row0 + t0) * a.ldx + c;
     T* y = static_cast<T*>(a.y) + (row0 + t0) * a.D + c;
-    Vec<T, V> nx[kAhead];
+    // copy group m brings tokens t0 + m kChunk ...
+    const auto fetch = [&](int t, int slot) {
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i)
-        if (t0 + i < t1) nx[i].load(x + i * a.ldx); else nx[i].zero();
+        for (int i = 0; i < kChunk; ++i) {
+            const bool in = t + i < t1;
+            mix::copy_async(ring + (slot + i) * kThreads, in ? x : static_cast<const T*>(a.x), in);
+            x += a.ldx;
+        }
+        mix::copies_close();
+    };
+#pragma unroll
+    for (int m = 0; m < kRing; m += kChunk) fetch(t0 + m, m);
     Taps<W, V> k;
     k.load(a, c, true);
     Seq s = sequence_at<PACKED>(a, b, t0);
     float win[W - 1][V];                          // the last W - 1 inputs, oldest first
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) load_input<T, V>(win[j], a, s, row0, t0 - s.first - (W - 1) + j, c);
-    for (int t = t0; t < t1; t += kAhead) {
-        Vec<T, V> cur[kAhead];
+    int slot = 0;
+    for (int t = t0; t < t1; t += kChunk) {
+        mix::copies_wait<kRing / kChunk - 1>();
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) cur[i] = nx[i];
-        x += kAhead * a.ldx;
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i)
-            if (t + kAhead + i < t1) nx[i].load(x + i * a.ldx);
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
+        for (int i = 0; i < kChunk; ++i) {
             if (t + i >= t1) break;
             if (PACKED && t + i >= s.end) {
                 s = sequence_at<true>(a, b, t + i);
 #pragma unroll
                 for (int j = 0; j < W - 1; ++j) load_input<T, V>(win[j], a, s, row0, j - (W - 1), c);
             }
+            const Vec<T, V> cur = ring[(slot + i) * kThreads];
+            float xv[V], p[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) xv[v] = cur.get(v);
+            mix::fma_row(p, k.w[W - 1], xv, k.b);
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j) mix::fma_row(p, k.w[j], win[j], p);
             Vec<T, V> o;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const float xv = cur[i].get(v);
-                float p = k.b[v];
-#pragma unroll
-                for (int j = 0; j < W - 1; ++j) p = fmaf(k.w[j][v], win[j][v], p);
-                p = fmaf(k.w[W - 1][v], xv, p);
-                o.set(v, a.silu ? silu(p) : p);
+                o.set(v, a.silu ? silu(p[v]) : p[v]);
 #pragma unroll
                 for (int j = 0; j < W - 2; ++j) win[j][v] = win[j + 1][v];
-                win[W - 2][v] = xv;
+                win[W - 2][v] = xv[v];
             }
             o.store(y);
             y += a.D;
         }
+        fetch(t + kRing, slot);
+        slot = slot + kChunk == kRing ? 0 : slot + kChunk;
     }
 }
 
 template <typename T, int W, int V, bool PACKED>
-__global__ void __launch_bounds__(kWarps * 32) conv_bwd_kernel(const ConvArgs a, const Grid g, float* part) {
-    __shared__ float sum[kWarps][W + 1][32 * V];
+__global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(const ConvArgs a, const Grid g, float* part) {
+    extern __shared__ __align__(16) unsigned char s_raw[];
+    auto* rx = reinterpret_cast<Vec<T, V>*>(s_raw) + threadIdx.x;             // [kRing][256] each
+    auto* ry = rx + kRing * kThreads;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int c = ((int)(blockIdx.x % g.cols) * 32 + lane) * V;
     const bool live = c < a.D;
@@ -227,42 +240,38 @@ __global__ void __launch_bounds__(kWarps * 32) conv_bwd_kernel(const ConvArgs a,
         const T* x = static_cast<const T*>(a.x) + (row0 + t0) * a.ldx + c;
         const T* dy = static_cast<const T*>(a.dy) + (row0 + t0) * a.D + c;
         T* dx = static_cast<T*>(a.dx) + (row0 + t0) * a.D + c;
-        constexpr int kNext = kAhead / 2;
-        Vec<T, V> nx[kNext], ny[kNext];
+        const auto fetch = [&](int t, int slot) {
 #pragma unroll
-        for (int i = 0; i < kNext; ++i) {
-            if (t0 + i < t2) nx[i].load(x + i * a.ldx); else nx[i].zero();
-            if (t0 + i < t2) ny[i].load(dy + i * a.D); else ny[i].zero();
-        }
+            for (int i = 0; i < kChunk; ++i) {
+                const bool in = t + i < t2;
+                mix::copy_async(rx + (slot + i) * kThreads, in ? x : static_cast<const T*>(a.x), in);
+                mix::copy_async(ry + (slot + i) * kThreads, in ? dy : static_cast<const T*>(a.dy), in);
+                x += a.ldx;
+                dy += a.D;
+            }
+            mix::copies_close();
+        };
+#pragma unroll
+        for (int m = 0; m < kRing; m += kChunk) fetch(t0 + m, m);
         Taps<W, V> k;
         k.load(a, c, true);
         Seq s = sequence_at<PACKED>(a, b, t0);
         float win[W - 1][V], ds[W - 1][V];                     // the last W - 1 inputs and ds, oldest first
-        Seq own[W - 1];                                        // the sequences of the last W - 1 tokens
+        int end[W - 1], own[W - 1];                            // the sequences of the last W - 1 tokens
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) {
             load_input<T, V>(win[j], a, s, row0, t0 - s.first - (W - 1) + j, c);
-            own[j] = s;
+            end[j] = s.end;
+            own[j] = s.n;
 #pragma unroll
             for (int v = 0; v < V; ++v) ds[j][v] = 0.f;
         }
         // token t brings ds_t; dx of token t - (W - 1) is then complete (past the row's end ds is 0)
-        for (int t = t0; t < t1 + W - 1; t += kNext) {
-            Vec<T, V> cx[kNext], cy[kNext];
+        int slot = 0;
+        for (int t = t0; t < t1 + W - 1; t += kChunk) {
+            mix::copies_wait<kRing / kChunk - 1>();
 #pragma unroll
-            for (int i = 0; i < kNext; ++i) {
-                cx[i] = nx[i];
-                cy[i] = ny[i];
-            }
-            x += kNext * a.ldx;
-            dy += kNext * (size_t)a.D;
-#pragma unroll
-            for (int i = 0; i < kNext; ++i) {
-                if (t + kNext + i < t2) nx[i].load(x + i * a.ldx); else nx[i].zero();
-                if (t + kNext + i < t2) ny[i].load(dy + i * a.D); else ny[i].zero();
-            }
-#pragma unroll
-            for (int i = 0; i < kNext; ++i) {
+            for (int i = 0; i < kChunk; ++i) {
                 const int now = t + i, out = now - (W - 1);
                 if (now >= t1 + W - 1) break;
                 if (PACKED && now >= s.end && now < a.T) {
@@ -270,43 +279,50 @@ __global__ void __launch_bounds__(kWarps * 32) conv_bwd_kernel(const ConvArgs a,
 #pragma unroll
                     for (int j = 0; j < W - 1; ++j) load_input<T, V>(win[j], a, s, row0, j - (W - 1), c);
                 }
-                // tokens from here on that belong to another sequence do not reach token `out`
-                const int reach = PACKED ? own[0].end - out : a.T - out;       // ds at out .. out + reach - 1 count
-                float d[V], gx[V];
+                const Vec<T, V> cx = rx[(slot + i) * kThreads], cy = ry[(slot + i) * kThreads];
+                float xv[V], p[V], d[V];
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    const float xv = cx[i].get(v);
-                    float p = k.b[v];
+                    xv[v] = cx.get(v);
+                    d[v] = cy.get(v);
+                }
+                if (a.silu) {
+                    mix::fma_row(p, k.w[W - 1], xv, k.b);
 #pragma unroll
-                    for (int j = 0; j < W - 1; ++j) p = fmaf(k.w[j][v], win[j][v], p);
-                    p = fmaf(k.w[W - 1][v], xv, p);
-                    d[v] = cy[i].get(v);
-                    if (a.silu) d[v] *= silu_slope(p);
-                    if (now >= a.T) d[v] = 0.f;
-                    if (now < t1) {
+                    for (int j = 0; j < W - 1; ++j) mix::fma_row(p, k.w[j], win[j], p);
 #pragma unroll
-                        for (int j = 0; j < W - 1; ++j) dw[j][v] = fmaf(d[v], win[j][v], dw[j][v]);
-                        dw[W - 1][v] = fmaf(d[v], xv, dw[W - 1][v]);
-                        dw[W][v] += d[v];
-                    }
+                    for (int v = 0; v < V; ++v) p[v] = silu_slope(p[v]);
+                    mix::mul_row(d, d, p);
+                }
+                if (now >= a.T)
 #pragma unroll
-                    for (int j = 0; j < W - 2; ++j) win[j][v] = win[j + 1][v];
-                    win[W - 2][v] = xv;
-                    // tap W - 1 - i of token out + i; the newest ds has tap 0
-                    gx[v] = k.w[W - 1][v] * ds[0][v];
+                    for (int v = 0; v < V; ++v) d[v] = 0.f;
+                if (now < t1) {
 #pragma unroll
-                    for (int m = 1; m < W - 1; ++m)
-                        gx[v] = !PACKED || m < reach ? fmaf(k.w[W - 1 - m][v], ds[m][v], gx[v]) : gx[v];
-                    gx[v] = !PACKED || W - 1 < reach ? fmaf(k.w[0][v], d[v], gx[v]) : gx[v];
+                    for (int j = 0; j < W - 1; ++j) mix::fma_row(dw[j], d, win[j], dw[j]);
+                    mix::fma_row(dw[W - 1], d, xv, dw[W - 1]);
 #pragma unroll
-                    for (int j = 0; j < W - 2; ++j) ds[j][v] = ds[j + 1][v];
-                    ds[W - 2][v] = d[v];
+                    for (int v = 0; v < V; ++v) dw[W][v] += d[v];
                 }
                 if (out >= t0) {
+                    // ds at out .. out + reach - 1 belong to the token's sequence; that of out + m meets tap W - 1 - m
+                    const int reach = (PACKED ? end[0] : a.T) - out;
+                    float gx[V];
+                    mix::mul_row(gx, k.w[W - 1], ds[0]);
+                    if (!PACKED || reach >= W) {
+#pragma unroll
+                        for (int m = 1; m < W - 1; ++m) mix::fma_row(gx, k.w[W - 1 - m], ds[m], gx);
+                        mix::fma_row(gx, k.w[0], d, gx);
+                    } else {
+#pragma unroll
+                        for (int m = 1; m < W - 1; ++m)
+                            if (m < reach) mix::fma_row(gx, k.w[W - 1 - m], ds[m], gx);
+                    }
                     const int tail = W - 1 - reach;            // its place in its sequence's final state
                     if (a.dhT && tail >= 0) {
                         float e[V];
-                        load_row<T, V>(e, static_cast<const T*>(a.dhT) + ((size_t)own[0].n * (W - 1) + tail) * a.D + c, true);
+                        const int n = PACKED ? own[0] : b;
+                        load_row<T, V>(e, static_cast<const T*>(a.dhT) + ((size_t)n * (W - 1) + tail) * a.D + c, true);
 #pragma unroll
                         for (int v = 0; v < V; ++v) gx[v] += e[v];
                     }
@@ -316,14 +332,31 @@ __global__ void __launch_bounds__(kWarps * 32) conv_bwd_kernel(const ConvArgs a,
                     o.store(dx);
                     dx += a.D;
                 }
-                if (PACKED) {
 #pragma unroll
-                    for (int j = 0; j < W - 2; ++j) own[j] = own[j + 1];
-                    own[W - 2] = s;
+                for (int j = 0; j < W - 2; ++j) {
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        win[j][v] = win[j + 1][v];
+                        ds[j][v] = ds[j + 1][v];
+                    }
+                    end[j] = end[j + 1];
+                    own[j] = own[j + 1];
                 }
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    win[W - 2][v] = xv[v];
+                    ds[W - 2][v] = d[v];
+                }
+                end[W - 2] = s.end;
+                own[W - 2] = s.n;
             }
+            fetch(t + kRing, slot);
+            slot = slot + kChunk == kRing ? 0 : slot + kChunk;
         }
     }
+    mix::copies_wait<0>();
+    __syncthreads();
+    auto& sum = *reinterpret_cast<float(*)[kWarps][W + 1][32 * V]>(s_raw);     // (the rings are done with)
 #pragma unroll
     for (int j = 0; j <= W; ++j)
 #pragma unroll
@@ -393,6 +426,10 @@ bool vector_ok(const ConvArgs& a, int V, const void* state = nullptr, const void
     return a.D % V == 0 && a.ldx % V == 0 && al(a.x) && al(a.h0) && al(a.hT) && al(a.y) && al(a.dy) && al(a.dhT) &&
            al(a.dx) && al(a.dh0) && al(state) && al(state_out);
 }
+cudaError_t allow_smem(const void* kernel, size_t bytes) {
+    return bytes > 48 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes)
+                             : cudaSuccess;
+}
 template <typename F>
 void by_width(int W, F f) {
     if (W == 2) f(std::integral_constant<int, 2>{});
@@ -416,22 +453,26 @@ size_t conv_workspace_bytes(const ConvArgs& a) {
 }
 
 cudaError_t launch_conv_fwd(const ConvArgs& a, cudaStream_t s) {
+    cudaError_t e = cudaSuccess;
     by_width(a.W, [&](auto w) {
         by_type(a, vector_ok(a, 4), [&](auto* t, auto v) {
             using T = std::remove_pointer_t<decltype(t)>;
             const Grid g = grid_of(a, v.value, a.hT != nullptr);
             const unsigned blocks = (unsigned)(g.cols * ((int64_t)a.B * g.run_blocks + g.state_blocks));
             if (blocks == 0) return;
-            if (a.cu) conv_fwd_kernel<T, w.value, v.value, true><<<blocks, kWarps * 32, 0, s>>>(a, g);
-            else conv_fwd_kernel<T, w.value, v.value, false><<<blocks, kWarps * 32, 0, s>>>(a, g);
+            const size_t smem = (size_t)kRing * kThreads * v.value * sizeof(T);
+            const auto kernel = a.cu ? conv_fwd_kernel<T, w.value, v.value, true> : conv_fwd_kernel<T, w.value, v.value, false>;
+            e = allow_smem(reinterpret_cast<const void*>(kernel), smem);
+            if (e == cudaSuccess) kernel<<<blocks, kThreads, smem, s>>>(a, g);
         });
     });
-    return cudaGetLastError();
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 cudaError_t launch_conv_bwd(const ConvArgs& a, cudaStream_t s) {
     float* part = static_cast<float*>(a.ws);
     int64_t rows = 0;
+    cudaError_t e = cudaSuccess;
     by_width(a.W, [&](auto w) {
         by_type(a, vector_ok(a, 4), [&](auto* t, auto v) {
             using T = std::remove_pointer_t<decltype(t)>;
@@ -439,10 +480,15 @@ cudaError_t launch_conv_bwd(const ConvArgs& a, cudaStream_t s) {
             rows = (int64_t)a.B * g.run_blocks;
             const unsigned blocks = (unsigned)(g.cols * (rows + g.state_blocks));
             if (blocks == 0) return;
-            if (a.cu) conv_bwd_kernel<T, w.value, v.value, true><<<blocks, kWarps * 32, 0, s>>>(a, g, part);
-            else conv_bwd_kernel<T, w.value, v.value, false><<<blocks, kWarps * 32, 0, s>>>(a, g, part);
+            const size_t rings = 2 * (size_t)kRing * kThreads * v.value * sizeof(T);
+            const size_t sums = (size_t)kWarps * (w.value + 1) * 32 * v.value * sizeof(float);
+            const size_t smem = rings > sums ? rings : sums;
+            const auto kernel = a.cu ? conv_bwd_kernel<T, w.value, v.value, true> : conv_bwd_kernel<T, w.value, v.value, false>;
+            e = allow_smem(reinterpret_cast<const void*>(kernel), smem);
+            if (e == cudaSuccess) kernel<<<blocks, kThreads, smem, s>>>(a, g, part);
         });
     });
+    if (e != cudaSuccess) return e;
     conv_param_kernel<<<dim3((a.D + 31) / 32, a.W + 1), 256, 0, s>>>(part, rows, a.D, a.W, a.dw, a.db);
     return cudaGetLastError();
 }
