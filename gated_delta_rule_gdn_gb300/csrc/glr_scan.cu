@@ -16,62 +16,110 @@ using mix::Vec;
 __device__ unsigned g_glr_status;   // bit 0: a block gave up a bounded wait
 
 template <typename Tx, typename Tg, int LANES, int V, bool PACKED>
-__global__ void __launch_bounds__(kThreads, LANES * V <= 64 ? 3 : 2)
+__global__ void __launch_bounds__(kBlock, 2)
 glr_fwd_kernel(const GlrArgs a, const Exchange x, const int publish) {
-    using At = Place<LANES, V>;
-    constexpr int W = At::W, R = At::kRuns, L = At::L;
+    using S = Shape<LANES, V>;
+    constexpr int W = S::W, R = S::R, L = S::L;
+    static_assert(W <= kCarryThreads, "a carry thread for every channel");
     extern __shared__ __align__(16) unsigned char s_raw[];
-    __shared__ float sA[R][W], sH[R][W];
-    __shared__ int s_start[2][kTile], s_end[2][kTile];
-    __shared__ unsigned s_next;
-    const int tid = threadIdx.x, run = tid / LANES, lane = tid % LANES;
-    auto* bg = reinterpret_cast<Vec<Tg, V>*>(s_raw) + tid;                    // [L][256] each
-    auto* bx = reinterpret_cast<Vec<Tx, V>*>(s_raw + L * kThreads * sizeof(Vec<Tg, V>)) + tid;
-    auto* bi = bx + L * kThreads;
+    __shared__ float sA[2][R][W], sH[2][R][W];
+    __shared__ int s_start[PACKED ? kPlaces : 1][kTile], s_end[PACKED ? kPlaces : 1][kTile];
+    __shared__ Tile s_tile[kPlaces];
+    const int tid = threadIdx.x;
 
-    At at;
-    const auto fetch = [&](int id) {
-        at.set(x, a, id, false);
-        const Tg* g = static_cast<const Tg*>(a.g) + at.row * a.ldg + at.c;
-        const Tx* xp = static_cast<const Tx*>(a.x) + at.row * a.ldx + at.c;
-        const Tx* ip = static_cast<const Tx*>(a.gi) + at.row * a.ldi + at.c;
-        const int n = at.live ? at.count : 0;
+    if (tid >= kThreads) {                       // the carry threads
+        const int ch = tid - kThreads;
+        Tickets tickets(x);
+        unsigned ticket = 0;
+        if (ch == 0) {
+            for (int i = 0; i < 3; ++i) s_tile[i] = tile_of(x, a, W, tickets.take(), false);
+            ticket = tickets.take();
+        }
+        __syncwarp();
+        bar_sync(kMaps);                         // (places are read below by all carry threads: meet once)
+        if (PACKED)
+            for (int i = 0; i < 3; ++i)
+                if (s_tile[i].chain >= 0) sequence_marks(a, s_tile[i].p, ch, s_start[i], s_end[i]);
+        __syncthreads();
+        for (int i = 0; s_tile[i % kPlaces].chain >= 0; ++i) {
+            const Tile t = s_tile[i % kPlaces];
+            const int k = i & 1, ahead = (i + 3) % kPlaces;
+            if (ch == 0) {
+                s_tile[ahead] = tile_of(x, a, W, ticket, false);
+                ticket = tickets.take();
+            }
+            float first = 0.f;
+            if (!PACKED && ch < W && t.p < kGroup && a.h0 && t.c0 + ch < a.D) first = a.h0[(size_t)t.b * a.D + t.c0 + ch];
+            bar_sync(kMaps + k);
+            if (ch < W) {
+                float A = 1.f, H = 0.f;
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    H = apply(sA[k][r][ch], sH[k][r][ch], H);
+                    A = both(A, sA[k][r][ch]);
+                }
+                if (publish || t.p > 0) hand_map(x, W, t.p, t.chain, ch, A, H);
+                float h = carry_in(x, W, t.p, t.chain, ch, first, &g_glr_status);
+                hand_state(x, W, t.p, t.chain, ch, apply(A, H, h));
+                if (a.ckpt && t.c0 + ch < a.D && t.p * kTile < a.T)
+                    a.ckpt[((size_t)t.b * x.tiles + t.p) * a.D + t.c0 + ch] = h;
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const float rH = sH[k][r][ch];
+                    sH[k][r][ch] = h;
+                    h = apply(sA[k][r][ch], rH, h);
+                }
+            }
+            if (PACKED && s_tile[ahead].chain >= 0) sequence_marks(a, s_tile[ahead].p, ch, s_start[ahead], s_end[ahead]);
+            bar_arrive(kCarry + k);
+        }
+        return;
+    }
+
+    // the compute threads
+    const int run = tid / LANES, lane = tid % LANES, arrays = a.gi ? 3 : 2;
+    const int bytes = L * kThreads * (int)(sizeof(Vec<Tg, V>) + (arrays - 1) * sizeof(Vec<Tx, V>));
+    const auto buf_g = [&](int k) { return reinterpret_cast<Vec<Tg, V>*>(s_raw + k * bytes) + tid; };   // [L][256] each
+    const auto buf_x = [&](int k) {
+        return reinterpret_cast<Vec<Tx, V>*>(s_raw + k * bytes + L * kThreads * sizeof(Vec<Tg, V>)) + tid;
+    };
+    const auto fetch = [&](int i) {
+        const Tile t = s_tile[i % kPlaces];
+        const int c = t.c0 + lane * V, t0 = t.p * kTile + run * L;
+        const int n = t.chain >= 0 && c < a.D ? min(a.T - t0, L) : 0;
+        const size_t row = (size_t)t.b * a.T + t0;
+        const Tg* g = static_cast<const Tg*>(a.g) + row * a.ldg + c;
+        const Tx* xp = static_cast<const Tx*>(a.x) + row * a.ldx + c;
+        const Tx* ip = static_cast<const Tx*>(a.gi) + row * a.ldi + c;
+        Vec<Tg, V>* bg = buf_g(i & 1);
+        Vec<Tx, V>* bx = buf_x(i & 1);
 #pragma unroll
         for (int j = 0; j < L; ++j) {
             mix::copy_async(bg + j * kThreads, j < n ? g : static_cast<const Tg*>(a.g), j < n);
             mix::copy_async(bx + j * kThreads, j < n ? xp : static_cast<const Tx*>(a.x), j < n);
-            if (a.gi) mix::copy_async(bi + j * kThreads, j < n ? ip : static_cast<const Tx*>(a.gi), j < n);
+            if (a.gi) mix::copy_async(bx + (L + j) * kThreads, j < n ? ip : static_cast<const Tx*>(a.gi), j < n);
             g += a.ldg;
             xp += a.ldx;
             ip += a.ldi;
         }
         mix::copies_close();
     };
-    unsigned ticket = 0;
-    int id = blockIdx.x;
-    if (x.tiles > 1) {
-        if (tid == 0) s_next = atomicAdd(x.ticket, 1u) + 1u;
-        __syncthreads();
-        id = (int)s_next;
-        if (tid == 0) ticket = atomicAdd(x.ticket, 1u) + 1u;
-        __syncthreads();
-    }
-    if (id < x.total) {
-        fetch(id);
-        if (PACKED && tid < kTile) sequence_marks(a, at.p, s_start[0], s_end[0]);
-    }
-    if (PACKED) __syncthreads();
-
-    for (int k = 0; id < x.total; k ^= 1) {
-        const At now = at;
-        // which tokens of the run start a sequence
-        unsigned starts = 0;
+    const auto run_starts = [&](int i) {         // which tokens of the run start a sequence
+        unsigned m = 0;
         if (PACKED) {
 #pragma unroll
-            for (int j = 0; j < L; ++j) starts |= (s_start[k][run * L + j] >= 0 ? 1u : 0u) << j;
+            for (int j = 0; j < L; ++j) m |= (s_start[i % kPlaces][run * L + j] >= 0 ? 1u : 0u) << j;
         }
-        float al[L][V], u[L][V];
-        mix::copies_wait<0>();
+        return m;
+    };
+
+    // stage one: decays and inputs of the run, and its map
+    const auto maps = [&](int i, float (&al)[L][V], float (&u)[L][V]) {
+        const Tile t = s_tile[i % kPlaces];
+        const int c = t.c0 + lane * V, count = a.T - (t.p * kTile + run * L);
+        const bool live = c < a.D;
+        const Vec<Tg, V>* bg = buf_g(i & 1);
+        const Vec<Tx, V>* bx = buf_x(i & 1);
 #pragma unroll
         for (int j = 0; j < L; ++j) {
             const Vec<Tg, V> g = bg[j * kThreads];
@@ -85,7 +133,7 @@ glr_fwd_kernel(const GlrArgs a, const Exchange x, const int publish) {
         if (a.gi) {
 #pragma unroll
             for (int j = 0; j < L; ++j) {
-                const Vec<Tx, V> gi = bi[j * kThreads];
+                const Vec<Tx, V> gi = bx[(L + j) * kThreads];
 #pragma unroll
                 for (int v = 0; v < V; ++v) u[j][v] *= sigmoid(gi.get(v));
             }
@@ -93,7 +141,7 @@ glr_fwd_kernel(const GlrArgs a, const Exchange x, const int publish) {
         if (a.A_log) {
             Channel ch[V];
 #pragma unroll
-            for (int v = 0; v < V; ++v) ch[v] = now.live ? channel(a.A_log, a.dt_bias, now.c + v) : Channel{0.f, 0.f};
+            for (int v = 0; v < V; ++v) ch[v] = live ? channel(a.A_log, a.dt_bias, c + v) : Channel{0.f, 0.f};
 #pragma unroll
             for (int j = 0; j < L; ++j)
 #pragma unroll
@@ -115,26 +163,20 @@ glr_fwd_kernel(const GlrArgs a, const Exchange x, const int publish) {
                 if (a.normalize) u[j][v] *= root(input_power(d));
                 al[j][v] = d.a;
             }
-        if (now.count < L) {                     // past the row's end the state stays
+        if (count < L) {                         // past the row's end the state stays
 #pragma unroll
             for (int j = 0; j < L; ++j)
 #pragma unroll
-                for (int v = 0; v < V; ++v) al[j][v] = j < now.count ? al[j][v] : 1.f;
+                for (int v = 0; v < V; ++v) al[j][v] = j < count ? al[j][v] : 1.f;
         }
-
-        // the run's map
+        const unsigned starts = run_starts(i);
         float A[V], H[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            A[v] = al[0][v];
-            H[v] = u[0][v];
-        }
         if (PACKED && starts) {
 #pragma unroll
             for (int j = 0; j < L; ++j) {
                 const bool here = (starts >> j) & 1;
-                if (here && a.h0 && now.live) {
-                    const float* h0 = a.h0 + (size_t)s_start[k][run * L + j] * a.D + now.c;
+                if (here && a.h0 && live) {
+                    const float* h0 = a.h0 + (size_t)s_start[i % kPlaces][run * L + j] * a.D + c;
 #pragma unroll
                     for (int v = 0; v < V; ++v) u[j][v] = fmaf(al[j][v], h0[v], u[j][v]);
                 }
@@ -145,55 +187,32 @@ glr_fwd_kernel(const GlrArgs a, const Exchange x, const int publish) {
             for (int v = 0; v < V; ++v) A[v] = -1.f;
         } else {
 #pragma unroll
-            for (int j = 1; j < L; ++j)
+            for (int j = 0; j < L; ++j)
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    H[v] = fmaf(al[j][v], H[v], u[j][v]);
-                    A[v] *= al[j][v];
+                    H[v] = j == 0 ? u[j][v] : fmaf(al[j][v], H[v], u[j][v]);
+                    A[v] = j == 0 ? al[j][v] : A[v] * al[j][v];
                 }
         }
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            sA[run][lane * V + v] = A[v];
-            sH[run][lane * V + v] = H[v];
+            sA[i & 1][run][lane * V + v] = A[v];
+            sH[i & 1][run][lane * V + v] = H[v];
         }
-        if (x.tiles > 1) {
-            if (tid == 0) s_next = ticket;
-        }
-        __syncthreads();
-        const int next = x.tiles > 1 ? (int)s_next : id + (int)gridDim.x;
-        if (next < x.total) {                    // the buffer is free: the next tile's inputs on the way
-            fetch(next);
-            if (PACKED && tid < kTile) sequence_marks(a, at.p, s_start[k ^ 1], s_end[k ^ 1]);
-            if (x.tiles > 1 && tid == 0) ticket = atomicAdd(x.ticket, 1u) + 1u;
-        }
+        bar_arrive(kMaps + (i & 1));
+    };
 
-        // the state that enters the tile, and each of its runs
-        if (tid < W) {
-            const int c = now.c0 + tid;
-            float tA = 1.f, tH = 0.f, h = 0.f;
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                tH = apply(sA[r][tid], sH[r][tid], tH);
-                tA = both(tA, sA[r][tid]);
-            }
-            if (!PACKED && now.p < kGroup && a.h0 && c < a.D) h = a.h0[(size_t)now.b * a.D + c];
-            h = carry_in(x, W, now.p, now.chain, tid, tA, tH, h, publish || now.p > 0, &g_glr_status);
-            if (a.ckpt && c < a.D && now.p * kTile < a.T) a.ckpt[((size_t)now.b * x.tiles + now.p) * a.D + c] = h;
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const float H = sH[r][tid];
-                sH[r][tid] = h;
-                h = apply(sA[r][tid], H, h);
-            }
-        }
-        __syncthreads();
-
+    // stage two: the states
+    const auto states = [&](int i, const float (&al)[L][V], const float (&u)[L][V]) {
+        const Tile t = s_tile[i % kPlaces];
+        const int c = t.c0 + lane * V, t0 = t.p * kTile + run * L;
+        const bool live = c < a.D;
+        const unsigned starts = run_starts(i);
         float h[V];
 #pragma unroll
-        for (int v = 0; v < V; ++v) h[v] = sH[run][lane * V + v];
-        Tx* op = static_cast<Tx*>(a.o) + now.row * a.D + now.c;
-        const int n = now.live && a.o ? now.count : 0;
+        for (int v = 0; v < V; ++v) h[v] = sH[i & 1][run][lane * V + v];
+        Tx* op = static_cast<Tx*>(a.o) + ((size_t)t.b * a.T + t0) * a.D + c;
+        const int n = live && a.o ? a.T - t0 : 0;
 #pragma unroll
         for (int j = 0; j < L; ++j) {
             Vec<Tx, V> o;
@@ -205,26 +224,46 @@ glr_fwd_kernel(const GlrArgs a, const Exchange x, const int publish) {
             }
             if (j < n) o.store(op);
             op += a.D;
-            if (PACKED && a.hT && now.live) {
-                const int m = s_end[k][run * L + j];
+            if (PACKED && a.hT && live) {
+                const int m = s_end[i % kPlaces][run * L + j];
                 if (m >= 0)
 #pragma unroll
-                    for (int v = 0; v < V; ++v) a.hT[(size_t)m * a.D + now.c + v] = h[v];
+                    for (int v = 0; v < V; ++v) a.hT[(size_t)m * a.D + c + v] = h[v];
             }
         }
-        if (!PACKED && a.hT && now.live && now.p == x.tiles - 1 && run == R - 1)
+        if (!PACKED && a.hT && live && t.p == x.tiles - 1 && run == R - 1)
 #pragma unroll
-            for (int v = 0; v < V; ++v) a.hT[(size_t)now.b * a.D + now.c + v] = h[v];
-        if (PACKED && a.hT && now.live) {
+            for (int v = 0; v < V; ++v) a.hT[(size_t)t.b * a.D + c + v] = h[v];
+        if (PACKED && a.hT && live) {
             // empty sequences end as they began; the row's tiles share them
-            for (int m = now.p * R + run; m < a.n_seqs; m += x.tiles * R) {
+            for (int m = t.p * R + run; m < a.n_seqs; m += x.tiles * R) {
                 if (mix::clamp_off(a.cu[m + 1], a.T) > mix::clamp_off(a.cu[m], a.T)) continue;
 #pragma unroll
-                for (int v = 0; v < V; ++v)
-                    a.hT[(size_t)m * a.D + now.c + v] = a.h0 ? a.h0[(size_t)m * a.D + now.c + v] : 0.f;
+                for (int v = 0; v < V; ++v) a.hT[(size_t)m * a.D + c + v] = a.h0 ? a.h0[(size_t)m * a.D + c + v] : 0.f;
             }
         }
-        id = next;
+    };
+
+    bar_arrive(kMaps);
+    __syncthreads();
+    fetch(0);
+    fetch(1);
+    float al0[L][V], u0[L][V], al1[L][V], u1[L][V];
+    const auto step = [&](int i, float (&al)[L][V], float (&u)[L][V], const float (&al_p)[L][V], const float (&u_p)[L][V]) {
+        const bool more = s_tile[i % kPlaces].chain >= 0;
+        if (more) {
+            mix::copies_wait<1>();
+            maps(i, al, u);
+        }
+        if (i > 0) bar_sync(kCarry + ((i - 1) & 1));
+        if (more) fetch(i + 2);
+        if (i > 0) states(i - 1, al_p, u_p);
+        return more;
+    };
+    if (s_tile[0].chain < 0) return;
+    for (int i = 0;; i += 2) {
+        if (!step(i, al0, u0, al1, u1)) break;
+        if (!step(i + 1, al1, u1, al0, u0)) break;
     }
 }
 
@@ -248,18 +287,19 @@ __global__ void glr_step_kernel(const GlrStepArgs a) {
 
 template <typename Tx, typename Tg, int LANES, int V, bool PACKED>
 cudaError_t fwd(const GlrArgs& a, cudaStream_t s) {
-    using At = Place<LANES, V>;
-    const Layout l = layout(a.B, a.T, a.D, At::W);
+    using S = Shape<LANES, V>;
+    const Layout l = layout(a.B, a.T, a.D, S::W);
     const Exchange x = exchange(l, a.ws);
     if (l.bytes) {
         const cudaError_t e = cudaMemsetAsync(a.ws, 0xff, l.bytes, s);
         if (e != cudaSuccess) return e;
     }
     const auto kernel = glr_fwd_kernel<Tx, Tg, LANES, V, PACKED>;
-    const size_t smem = (size_t)At::L * kThreads * V * (sizeof(Tg) + 2 * sizeof(Tx));
-    static const Residency res = residency(reinterpret_cast<const void*>(kernel), smem);
-    if (res.error != cudaSuccess) return res.error;
-    kernel<<<x.total < res.blocks ? x.total : res.blocks, kThreads, smem, s>>>(a, x, a.test_stall ? 0 : 1);
+    const int smem = 2 * S::L * kThreads * V * (int)(sizeof(Tg) + (a.gi ? 2 : 1) * sizeof(Tx));
+    static Residency res[2];                     // without and with the input gate
+    const int blocks = res[a.gi != nullptr].get(reinterpret_cast<const void*>(kernel), smem);
+    if (blocks == 0) return cudaGetLastError();
+    kernel<<<x.total < blocks ? x.total : blocks, kBlock, smem, s>>>(a, x, a.test_stall ? 0 : 1);
     return cudaGetLastError();
 }
 
@@ -277,17 +317,20 @@ cudaError_t fwd_wide(const GlrArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-// Blocks that are resident at once on the whole device (persistent kernels launch no more).
 namespace glr {
-Residency residency(const void* kernel, size_t smem) {
-    Residency r{cudaSuccess, 0};
-    int dev = 0, sms = 0, per = 0;
-    r.error = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (r.error == cudaSuccess) r.error = cudaGetDevice(&dev);
-    if (r.error == cudaSuccess) r.error = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (r.error == cudaSuccess) r.error = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, kThreads, smem);
-    r.blocks = sms * (per > 0 ? per : 1);
-    return r;
+int Residency::get(const void* kernel, int smem) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev >= kDevices) return 0;
+    int n = blocks[dev].load(std::memory_order_relaxed);
+    if (n > 0) return n;
+    int sms = 0, per = 0;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamicSmem) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, kBlock, smem) != cudaSuccess)
+        return 0;
+    n = sms * (per > 0 ? per : 1);
+    blocks[dev].store(n, std::memory_order_relaxed);
+    return n;
 }
 }  // namespace glr
 

@@ -1,8 +1,8 @@
 // Shared parts of the gated linear recurrence's scans (glr_scan.cu, glr_scan_bwd.cu): the tiling, the input buffer, and
 // the carry of a tile from the tiles before it.
 //
-// A row of T tokens is cut into tiles of 64 tokens x W = LANES * V channels.  A block of 256 threads takes one tile after
-// another; LANES threads side by side read V channels each, and so the block has 256 / LANES runs of LANES / 4 consecutive
+// A row of T tokens is cut into tiles of 64 tokens x W = LANES * V channels.  A block takes one tile after another with 256
+// compute threads; LANES threads side by side read V channels each, and so it has 256 / LANES runs of LANES / 4 consecutive
 // tokens, each held in the registers of its threads.  The recurrence over a run of tokens is the map h -> A h + H; a run
 // in which a sequence starts (backward: ends) forgets h altogether, which is written A = -1 (decays are never negative),
 // so that a state that is not a number stays in its own sequence.
@@ -13,10 +13,11 @@
 // A tile publishes its map as soon as it has it; the last of a group publishes the next group's starting state.  So the
 // serial chain of a row is T / (64 kGroup) hops, and each byte of the inputs is read once.  A map is one 8-byte word and a
 // state one 4-byte word, which are their own flags: the workspace starts as all ones, which no published word is.
-// Blocks take tickets for tiles in scan order, one ahead, to have the next tile's inputs on the way while the carry of the
-// current one is worked out.  The smallest tile that is not done is always the current one of its block, so waiting ends;
-// waits are bounded all the same.
+// Blocks take tickets for tiles in scan order, a few ahead, and go through their tiles in that order.  All that the smallest
+// tile without a carry waits for is therefore done or under way, and waiting ends; waits are bounded all the same.
 #pragma once
+
+#include <atomic>
 
 #include "glr_math.cuh"
 #include "mixer.h"
@@ -31,8 +32,13 @@ constexpr int kGroup = 16;
 constexpr unsigned kEmpty = 0xffffffffu;
 constexpr unsigned long long kWaitNs = 2000000000ull;
 
-struct Residency { cudaError_t error; int blocks; };
-Residency residency(const void* kernel, size_t smem);
+// How many blocks of a kernel with this much dynamic shared memory the device holds at once (persistent kernels launch no
+// more), asked once per device; 0 if a query failed.
+constexpr int kDevices = 64, kMaxDynamicSmem = 200 * 1024;
+struct Residency {
+    std::atomic<int> blocks[kDevices]{};
+    int get(const void* kernel, int smem);
+};
 
 // Workspace of one scan, set to all ones before the launch.
 struct Exchange {
@@ -98,15 +104,21 @@ __device__ __forceinline__ unsigned full(float v) {           // a float's bits,
     return b == kEmpty ? 0x7fffffffu : b;
 }
 
-// The carry into tile p of a chain, for one channel: called by the W threads that have the channels' maps (A, H) of the
-// tile and the state `first` before tile 0 of the row.
-__device__ __forceinline__ float carry_in(const Exchange& x, int W, int p, int chain, int ch, float A, float H,
-                                          float first, bool publish, unsigned* status) {
+// Hand over a tile's map, for one channel (the last tile of a group hands over the state after it instead).
+__device__ __forceinline__ bool closes_group(const Exchange& x, int p) { return p + 1 < x.tiles && p % kGroup == kGroup - 1; }
+__device__ __forceinline__ void hand_map(const Exchange& x, int W, int p, int chain, int ch, float A, float H) {
+    if (p + 1 < x.tiles && !closes_group(x, p))
+        store_word(x.map + ((size_t)p * x.chains + chain) * W + ch, (unsigned long long)full(H) << 32 | full(A));
+}
+__device__ __forceinline__ void hand_state(const Exchange& x, int W, int p, int chain, int ch, float h) {
+    if (closes_group(x, p)) store_word(x.state + ((size_t)(p / kGroup + 1) * x.chains + chain) * W + ch, full(h));
+}
+
+// The carry into tile p of a chain, for one channel; `first` is the state before tile 0 of the row.
+__device__ __forceinline__ float carry_in(const Exchange& x, int W, int p, int chain, int ch, float first, unsigned* status) {
     const int group = p / kGroup, start = group * kGroup, n = p - start;
-    const bool more = p + 1 < x.tiles, closes = more && n + 1 == kGroup;
-    const size_t row = (size_t)x.chains * W, at = (size_t)chain * W + ch;
-    if (more && !closes && publish) store_word(x.map + p * row + at, (unsigned long long)full(H) << 32 | full(A));
     if (p == 0) return first;
+    const size_t row = (size_t)x.chains * W, at = (size_t)chain * W + ch;
     unsigned long long m[kGroup - 1];
     unsigned st = group > 0 ? kEmpty : 0u;
 #pragma unroll
@@ -139,9 +151,7 @@ __device__ __forceinline__ float carry_in(const Exchange& x, int W, int p, int c
         cH = apply(a, h, cH);
         cA = both(cA, a);
     }
-    const float carry = apply(cA, cH, group > 0 ? __uint_as_float(st) : first);
-    if (closes && publish) store_word(x.state + (group + 1) * row + at, full(apply(A, H, carry)));
-    return carry;
+    return apply(cA, cH, group > 0 ? __uint_as_float(st) : first);
 }
 
 struct Channel { float neg_eA, dt; };   // -exp(A_log) (0: g is log a) and dt_bias of a channel
@@ -149,39 +159,53 @@ __device__ __forceinline__ Channel channel(const float* A_log, const float* dt_b
     return {A_log ? -expf(A_log[c]) : 0.f, dt_bias ? dt_bias[c] : 0.f};
 }
 
-// A block's place in its current tile.
+// The block's division of work.  Its 256 compute threads take a tile in two stages: the maps of their runs (stage one), and
+// with the states that enter the runs the outputs (stage two).  Stage two of a tile comes after stage one of the next, so
+// that the carry, which kCarryThreads threads of their own work out in between, has that long to arrive.  Two more
+// tiles' inputs are on the way meanwhile.  Per tile i the two sides meet at two barriers, each of one parity of i:
+//   MAPS   the compute threads have left their runs' maps in shared memory;
+//   CARRY  the carry threads have left the runs' entering states there, and tile i + 3's place in the ring of places.
+constexpr int kCarryThreads = 64, kBlock = kThreads + kCarryThreads, kPlaces = 8;
+__device__ __forceinline__ void bar_arrive(int id) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "n"(kBlock) : "memory"); }
+__device__ __forceinline__ void bar_sync(int id) { asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(kBlock) : "memory"); }
+constexpr int kMaps = 1, kCarry = 3;
+
 template <int LANES, int V>
-struct Place {
-    static constexpr int W = LANES * V, kRuns = kThreads / LANES, L = kTile / kRuns;
-    int p, chain, b, c0, c, t0;      // tile in the row, chain, batch row, the block's and the thread's first channel,
-    int count;                       // the run's first token, and its tokens inside the row
-    bool live;                       // the thread's channels exist
-    size_t row;                      // the run's first row in [B T]
-    __device__ __forceinline__ void set(const Exchange& x, const GlrArgs& a, int id, bool reverse) {
-        const int q = id / x.chains, cols = x.chains / a.B;
-        chain = id - q * x.chains;
-        p = reverse ? x.tiles - 1 - q : q;
-        b = chain / cols;
-        c0 = (chain - b * cols) * W;
-        c = c0 + (int)(threadIdx.x % LANES) * V;
-        t0 = p * kTile + (int)(threadIdx.x / LANES) * L;
-        live = c < a.D;
-        count = min(max(a.T - t0, 0), L);
-        row = (size_t)b * a.T + t0;
+struct Shape {
+    static constexpr int W = LANES * V, R = kThreads / LANES, L = kTile / R;
+};
+
+// A tile: its place in the row, batch row, first channel and chain (chain < 0: there is none).
+struct Tile { int p, b, c0, chain; };
+__device__ __forceinline__ Tile tile_of(const Exchange& x, const GlrArgs& a, int W, unsigned id, bool reverse) {
+    if (id >= (unsigned)x.total) return {0, 0, 0, -1};
+    const int q = id / x.chains, chain = id - q * x.chains, cols = x.chains / a.B, b = chain / cols;
+    return {reverse ? x.tiles - 1 - q : q, b, (chain - b * cols) * W, chain};
+}
+// Rows with a single tile need no tickets: blocks stride over the chains.
+struct Tickets {
+    unsigned* counter;
+    unsigned next;
+    __device__ __forceinline__ explicit Tickets(const Exchange& x) : counter(x.ticket), next(blockIdx.x) {}
+    __device__ __forceinline__ unsigned take() {
+        if (counter) return atomicAdd(counter, 1u) + 1u;
+        const unsigned t = next;
+        next += gridDim.x;
+        return t;
     }
 };
 
-// Packed sequences: which one starts, and which ends, at each token of tile p (-1: none).  Called by threads 0..63.
-__device__ __forceinline__ void sequence_marks(const GlrArgs& a, int p, int* starts, int* ends) {
-    const int t = p * kTile + threadIdx.x;
+// Packed sequences: which one starts, and which ends, at token i of tile p (-1: none).
+__device__ __forceinline__ void sequence_marks(const GlrArgs& a, int p, int i, int* starts, int* ends) {
+    const int t = p * kTile + i;
     int s = -1, e = -1;
     if (t < a.T) {
         const mix::Span sp = mix::span_of(a.cu, a.n_seqs, a.T, t);
         if (sp.first == t) s = sp.n;
         if (sp.end == t + 1) e = sp.n;
     }
-    starts[threadIdx.x] = s;
-    ends[threadIdx.x] = e;
+    starts[i] = s;
+    ends[i] = e;
 }
 
 }  // namespace glr

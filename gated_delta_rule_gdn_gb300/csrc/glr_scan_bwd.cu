@@ -19,37 +19,129 @@ __device__ unsigned g_glr_bwd_status;   // bit 0: a block gave up a bounded wait
 
 struct BwdSpace { void* scan; float* part; };
 
-template <typename Tx, typename Tg, int LANES, int V, bool PACKED>
-__global__ void __launch_bounds__(kThreads, 2)
-glr_bwd_kernel(const GlrArgs a, const Exchange x, float* part) {
-    using At = Place<LANES, V>;
-    constexpr int W = At::W, R = At::kRuns, L = At::L;
-    static_assert(2 * W <= kThreads, "one thread a channel for each direction");
-    extern __shared__ __align__(16) unsigned char s_raw[];
-    __shared__ float sA[R][W], sH[R][W], sG[R][W];
-    __shared__ unsigned char s_any[R];           // bit 0: a sequence starts in the run; bit 1: one ends
-    __shared__ int s_start[2][kTile], s_end[2][kTile];
-    __shared__ unsigned s_next;
-    const int tid = threadIdx.x, run = tid / LANES, lane = tid % LANES;
-    auto* bg = reinterpret_cast<Vec<Tg, V>*>(s_raw) + tid;                    // [L][256] each
-    auto* bx = reinterpret_cast<Vec<Tx, V>*>(s_raw + L * kThreads * sizeof(Vec<Tg, V>)) + tid;
-    auto* bi = bx + L * kThreads;
-    auto* bo = bi + L * kThreads;
+// Stage one keeps the decay (as a and as a - 1), log a and the input u of a tile's elements in registers; its raw inputs
+// stay in shared memory until stage two, which first runs the gradient D through the run from behind, then the state from
+// the front, and forms each token's gradients on the way.
+constexpr int kBuffers = 3;
 
-    At at;
-    const auto fetch = [&](int id) {
-        at.set(x, a, id, true);
-        const Tg* g = static_cast<const Tg*>(a.g) + at.row * a.ldg + at.c;
-        const Tx* xp = static_cast<const Tx*>(a.x) + at.row * a.ldx + at.c;
-        const Tx* ip = static_cast<const Tx*>(a.gi) + at.row * a.ldi + at.c;
-        const Tx* op = static_cast<const Tx*>(a.dO) + at.row * a.D + at.c;
-        const int n = at.live ? at.count : 0;
+template <typename Tx, typename Tg, int LANES, int V, bool PACKED>
+__global__ void __launch_bounds__(kBlock, 2)
+glr_bwd_kernel(const GlrArgs a, const Exchange x, float* part) {
+    using S = Shape<LANES, V>;
+    constexpr int W = S::W, R = S::R, L = S::L;
+    static_assert(2 * W <= kCarryThreads, "a carry thread for every channel and direction");
+    extern __shared__ __align__(16) unsigned char s_raw[];
+    __shared__ float sA[2][R][W], sH[2][R][W], sG[2][R][W], s_sum[2][2][R][W];
+    __shared__ unsigned char s_any[2][R];        // bit 0: a sequence starts in the run; bit 1: one ends
+    __shared__ int s_start[PACKED ? kPlaces : 1][kTile], s_end[PACKED ? kPlaces : 1][kTile];
+    __shared__ Tile s_tile[kPlaces];
+    const int tid = threadIdx.x;
+
+    if (tid >= kThreads) {                       // the carry threads: the gradient's, the state's
+        const int ch = (tid - kThreads) % W, side = (tid - kThreads) / W;
+        Tickets tickets(x);
+        unsigned ticket = 0;
+        if (tid == kThreads) {
+            for (int i = 0; i < 3; ++i) s_tile[i] = tile_of(x, a, W, tickets.take(), true);
+            ticket = tickets.take();
+        }
+        __syncwarp();
+        bar_sync(kMaps);
+        if (PACKED)
+            for (int i = 0; i < 3; ++i)
+                if (s_tile[i].chain >= 0) sequence_marks(a, s_tile[i].p, tid - kThreads, s_start[i], s_end[i]);
+        __syncthreads();
+        // the sums of tile i over its runs, in order
+        const auto sums = [&](int i) {
+            const Tile t = s_tile[i % kPlaces];
+            if (side > 1 || t.c0 + ch >= a.D) return;
+            float s = 0.f;
+#pragma unroll
+            for (int r = 0; r < R; ++r) s += s_sum[i & 1][side][r][ch];
+            const size_t rows = (size_t)a.B * x.tiles, r = (size_t)t.b * x.tiles + t.p;
+            part[((side ? rows : 0) + r) * a.D + t.c0 + ch] = s;
+        };
+        int i = 0;
+        for (; s_tile[i % kPlaces].chain >= 0; ++i) {
+            const Tile t = s_tile[i % kPlaces];
+            const int k = i & 1, ahead = (i + 3) % kPlaces, q = x.tiles - 1 - t.p;
+            if (tid == kThreads) {
+                s_tile[ahead] = tile_of(x, a, W, ticket, true);
+                ticket = tickets.take();
+            }
+            // what enters the tile: the state from its checkpoint, the gradient behind the row's last token
+            const bool live = t.c0 + ch < a.D;
+            float enter = 0.f;
+            if (side == 0) {
+                if (!PACKED && q < kGroup && a.dhT && live) enter = a.dhT[(size_t)t.b * a.D + t.c0 + ch];
+            } else if (side == 1 && live && t.p * kTile < a.T) {
+                if (t.p > 0 || PACKED) enter = a.ckpt[((size_t)t.b * x.tiles + t.p) * a.D + t.c0 + ch];
+                else if (a.h0) enter = a.h0[(size_t)t.b * a.D + t.c0 + ch];
+            }
+            bar_sync(kMaps + k);
+            if (side == 0) {
+                const auto run_A = [&](int r) { return PACKED && (s_any[k][r] & 2) ? -1.f : sA[k][r][ch]; };
+                float A = 1.f, G = 0.f;
+#pragma unroll
+                for (int r = R - 1; r >= 0; --r) {
+                    G = apply(run_A(r), sG[k][r][ch], G);
+                    A = both(A, run_A(r));
+                }
+                hand_map(x, W, q, t.chain, ch, A, G);
+                float g = carry_in(x, W, q, t.chain, ch, enter, &g_glr_bwd_status);
+                hand_state(x, W, q, t.chain, ch, apply(A, G, g));
+#pragma unroll
+                for (int r = R - 1; r >= 0; --r) {
+                    const float rG = sG[k][r][ch];
+                    sG[k][r][ch] = g;
+                    g = apply(run_A(r), rG, g);
+                }
+            } else if (side == 1) {
+                float h = enter;
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const float rA = PACKED && (s_any[k][r] & 1) ? -1.f : sA[k][r][ch], rH = sH[k][r][ch];
+                    sH[k][r][ch] = h;
+                    h = apply(rA, rH, h);
+                }
+            }
+            if (a.dA && i >= 2) sums(i - 2);     // (stage two of tile i - 2 came before the maps of tile i)
+            if (PACKED && s_tile[ahead].chain >= 0)
+                sequence_marks(a, s_tile[ahead].p, tid - kThreads, s_start[ahead], s_end[ahead]);
+            bar_arrive(kCarry + k);
+        }
+        if (a.dA && i > 0) {
+            bar_sync(kMaps + (i & 1));           // the compute threads are through
+            if (i >= 2) sums(i - 2);
+            sums(i - 1);
+        }
+        return;
+    }
+
+    // the compute threads
+    const int run = tid / LANES, lane = tid % LANES, arrays = a.gi ? 4 : 3;
+    const int bytes = L * kThreads * (int)(sizeof(Vec<Tg, V>) + (arrays - 1) * sizeof(Vec<Tx, V>));
+    const auto buf_g = [&](int i) { return reinterpret_cast<Vec<Tg, V>*>(s_raw + i % kBuffers * bytes) + tid; };
+    const auto buf_x = [&](int i) {              // x, dO, and the input gate's logits: [L][256] each
+        return reinterpret_cast<Vec<Tx, V>*>(s_raw + i % kBuffers * bytes + L * kThreads * sizeof(Vec<Tg, V>)) + tid;
+    };
+    const auto fetch = [&](int i) {
+        const Tile t = s_tile[i % kPlaces];
+        const int c = t.c0 + lane * V, t0 = t.p * kTile + run * L;
+        const int n = t.chain >= 0 && c < a.D ? min(a.T - t0, L) : 0;
+        const size_t row = (size_t)t.b * a.T + t0;
+        const Tg* g = static_cast<const Tg*>(a.g) + row * a.ldg + c;
+        const Tx* xp = static_cast<const Tx*>(a.x) + row * a.ldx + c;
+        const Tx* ip = static_cast<const Tx*>(a.gi) + row * a.ldi + c;
+        const Tx* op = static_cast<const Tx*>(a.dO) + row * a.D + c;
+        Vec<Tg, V>* bg = buf_g(i);
+        Vec<Tx, V>* bx = buf_x(i);
 #pragma unroll
         for (int j = 0; j < L; ++j) {
             mix::copy_async(bg + j * kThreads, j < n ? g : static_cast<const Tg*>(a.g), j < n);
             mix::copy_async(bx + j * kThreads, j < n ? xp : static_cast<const Tx*>(a.x), j < n);
-            if (a.gi) mix::copy_async(bi + j * kThreads, j < n ? ip : static_cast<const Tx*>(a.gi), j < n);
-            mix::copy_async(bo + j * kThreads, j < n ? op : static_cast<const Tx*>(a.dO), j < n);
+            mix::copy_async(bx + (L + j) * kThreads, j < n ? op : static_cast<const Tx*>(a.dO), j < n);
+            if (a.gi) mix::copy_async(bx + (2 * L + j) * kThreads, j < n ? ip : static_cast<const Tx*>(a.gi), j < n);
             g += a.ldg;
             xp += a.ldx;
             ip += a.ldi;
@@ -57,125 +149,84 @@ glr_bwd_kernel(const GlrArgs a, const Exchange x, float* part) {
         }
         mix::copies_close();
     };
-    // the state that enters the tile, for the threads that run the states through it (tid - W is their channel)
-    const auto entry_state = [&]() {
-        const int c = at.c0 + tid - W;
-        if (tid < W || tid >= 2 * W || c >= a.D || at.p * kTile >= a.T) return 0.f;
-        if (at.p > 0 || PACKED) return a.ckpt[((size_t)at.b * x.tiles + at.p) * a.D + c];
-        return a.h0 ? a.h0[(size_t)at.b * a.D + c] : 0.f;
-    };
-    unsigned ticket = 0;
-    int id = blockIdx.x;
-    if (x.tiles > 1) {
-        if (tid == 0) s_next = atomicAdd(x.ticket, 1u) + 1u;
-        __syncthreads();
-        id = (int)s_next;
-        if (tid == 0) ticket = atomicAdd(x.ticket, 1u) + 1u;
-        __syncthreads();
-    }
-    float entry = 0.f;
-    if (id < x.total) {
-        fetch(id);
-        entry = entry_state();
-        if (PACKED && tid < kTile) sequence_marks(a, at.p, s_start[0], s_end[0]);
-    }
-    if (PACKED) __syncthreads();
-
-    for (int k = 0; id < x.total; k ^= 1) {
-        const At now = at;
-        unsigned starts = 0, ends = 0;
+    struct Held { float al[L][V], e[L][V], la[L][V], u[L][V]; };
+    const auto marks = [&](int i, unsigned* starts, unsigned* ends) {
+        *starts = *ends = 0;
         if (PACKED) {
 #pragma unroll
             for (int j = 0; j < L; ++j) {
-                starts |= (s_start[k][run * L + j] >= 0 ? 1u : 0u) << j;
-                ends |= (s_end[k][run * L + j] >= 0 ? 1u : 0u) << j;
+                *starts |= (s_start[i % kPlaces][run * L + j] >= 0 ? 1u : 0u) << j;
+                *ends |= (s_end[i % kPlaces][run * L + j] >= 0 ? 1u : 0u) << j;
             }
         }
-        // the decay, the input u, and the factors of the gradients:
-        //   dx = D w, di = dx y, dla = D (a h_{t-1} - m), dg = dla w3, dA_log = sum dla la
-        //   w = s sigma(i), y = x (1 - sigma(i)), m = sigma(i) x a^2 / s, w3 = dla/dg
-        float al[L][V], u[L][V], w[L][V], y[L][V], m[L][V], w3[L][V], la[L][V], dO[L][V];
-        mix::copies_wait<0>();
+    };
+    // dO, with what enters behind a sequence's last token
+    const auto grad_o = [&](int i, int j, int c, bool end, float (&d)[V]) {
+        const Vec<Tx, V> o = buf_x(i)[(L + j) * kThreads];
+#pragma unroll
+        for (int v = 0; v < V; ++v) d[v] = o.get(v);
+        if (PACKED && end && a.dhT && c < a.D)
+#pragma unroll
+            for (int v = 0; v < V; ++v) d[v] += a.dhT[(size_t)s_end[i % kPlaces][run * L + j] * a.D + c + v];
+    };
+
+    // stage one: decays and inputs of the run, and its maps: (A, H) of the state, (A, G) of the gradient
+    const auto maps = [&](int i, Held& q) {
+        const Tile t = s_tile[i % kPlaces];
+        const int c = t.c0 + lane * V, count = a.T - (t.p * kTile + run * L);
+        const bool live = c < a.D;
 #pragma unroll
         for (int j = 0; j < L; ++j) {
-            const Vec<Tg, V> g = bg[j * kThreads];
-            const Vec<Tx, V> xv = bx[j * kThreads], ov = bo[j * kThreads];
+            const Vec<Tg, V> g = buf_g(i)[j * kThreads];
+            const Vec<Tx, V> xv = buf_x(i)[j * kThreads];
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                la[j][v] = g.get(v);
-                u[j][v] = xv.get(v);
-                dO[j][v] = ov.get(v);
-                w[j][v] = w3[j][v] = 1.f;
-                y[j][v] = m[j][v] = 0.f;
+                q.la[j][v] = g.get(v);
+                q.u[j][v] = xv.get(v);
             }
         }
         if (a.gi) {
 #pragma unroll
             for (int j = 0; j < L; ++j) {
-                const Vec<Tx, V> gi = bi[j * kThreads];
+                const Vec<Tx, V> gi = buf_x(i)[(2 * L + j) * kThreads];
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    // 1 - sigma(i) = e sigma(i) with e = exp(-i), kept finite
-                    const float e = ex2(max_nan(gi.get(v), -80.f) * -kLog2e), si = rcp(1.f + e);
-                    w[j][v] = si;
-                    u[j][v] *= si;
-                    y[j][v] = u[j][v] * e;
-                }
+                for (int v = 0; v < V; ++v) q.u[j][v] *= sigmoid(gi.get(v));
             }
         }
         if (a.A_log) {
             Channel ch[V];
 #pragma unroll
-            for (int v = 0; v < V; ++v) ch[v] = now.live ? channel(a.A_log, a.dt_bias, now.c + v) : Channel{0.f, 0.f};
+            for (int v = 0; v < V; ++v) ch[v] = live ? channel(a.A_log, a.dt_bias, c + v) : Channel{0.f, 0.f};
 #pragma unroll
             for (int j = 0; j < L; ++j)
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    const float z = la[j][v] + ch[v].dt, e = tail(z);
-                    la[j][v] = ch[v].neg_eA * softplus(z, e);
-                    w3[j][v] = ch[v].neg_eA * sigmoid(z, e);
+                    const float z = q.la[j][v] + ch[v].dt;
+                    q.la[j][v] = ch[v].neg_eA * softplus(z, tail(z));
                 }
         } else {
 #pragma unroll
             for (int j = 0; j < L; ++j)
 #pragma unroll
-                for (int v = 0; v < V; ++v) la[j][v] = min_nan(la[j][v], 88.f);
+                for (int v = 0; v < V; ++v) q.la[j][v] = min_nan(q.la[j][v], 88.f);
         }
 #pragma unroll
         for (int j = 0; j < L; ++j)
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const Decay d = decay(la[j][v]);
-                if (a.normalize) {
-                    // ds/dlog a = -a^2 / s, taken as 0 where s = 0 (log a = 0: the derivative does not exist there)
-                    const float s2 = input_power(d), rs = s2 > 0.f ? rsq(s2) : 0.f, s = s2 * rs;
-                    m[j][v] = u[j][v] * (d.a * d.a) * rs;
-                    u[j][v] *= s;
-                    w[j][v] *= s;
-                }
-                al[j][v] = d.a;
+                const Decay d = decay(q.la[j][v]);
+                q.al[j][v] = d.a;
+                q.e[j][v] = d.e;
+                if (a.normalize) q.u[j][v] *= root(input_power(d));
             }
-        if (now.count < L) {                     // past the row's end state and gradient stay
+        if (count < L) {                         // past the row's end state and gradient stay
 #pragma unroll
             for (int j = 0; j < L; ++j)
 #pragma unroll
-                for (int v = 0; v < V; ++v) al[j][v] = j < now.count ? al[j][v] : 1.f;
+                for (int v = 0; v < V; ++v) q.al[j][v] = j < count ? q.al[j][v] : 1.f;
         }
-        if (PACKED && (starts | ends) && now.live) {
-            // what enters at a sequence's first token, and at its last
-#pragma unroll
-            for (int j = 0; j < L; ++j) {
-                if (((starts >> j) & 1) && a.h0)
-#pragma unroll
-                    for (int v = 0; v < V; ++v)
-                        u[j][v] = fmaf(al[j][v], a.h0[(size_t)s_start[k][run * L + j] * a.D + now.c + v], u[j][v]);
-                if (((ends >> j) & 1) && a.dhT)
-#pragma unroll
-                    for (int v = 0; v < V; ++v) dO[j][v] += a.dhT[(size_t)s_end[k][run * L + j] * a.D + now.c + v];
-            }
-        }
-
-        // the run's maps: (A, H) of the state, (A, G) of the gradient; one A serves both
+        unsigned starts, ends;
+        marks(i, &starts, &ends);
         float A[V], H[V], G[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -184,151 +235,189 @@ glr_bwd_kernel(const GlrArgs a, const Exchange x, float* part) {
         }
 #pragma unroll
         for (int j = 0; j < L; ++j) {
-            const int r = L - 1 - j;
-            const bool start = PACKED && ((starts >> j) & 1), end = PACKED && ((ends >> r) & 1);
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                H[v] = start ? u[j][v] : fmaf(al[j][v], H[v], u[j][v]);
-                G[v] = al[r][v] * (end ? dO[r][v] : dO[r][v] + G[v]);
-                A[v] *= al[j][v];
-            }
-        }
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            sA[run][lane * V + v] = A[v];
-            sH[run][lane * V + v] = H[v];
-            sG[run][lane * V + v] = G[v];
-        }
-        if (PACKED && lane == 0) s_any[run] = (starts ? 1 : 0) | (ends ? 2 : 0);
-        const float enter = entry;
-        if (x.tiles > 1 && tid == 0) s_next = ticket;
-        __syncthreads();
-        const int next = x.tiles > 1 ? (int)s_next : id + (int)gridDim.x;
-        if (next < x.total) {                    // the buffer is free: the next tile's inputs on the way
-            fetch(next);
-            entry = entry_state();
-            if (PACKED && tid < kTile) sequence_marks(a, at.p, s_start[k ^ 1], s_end[k ^ 1]);
-            if (x.tiles > 1 && tid == 0) ticket = atomicAdd(x.ticket, 1u) + 1u;
-        }
-        if (tid < W) {                           // the gradient that enters the tile from behind, and each of its runs
-            const int c = now.c0 + tid;
-            const auto run_A = [&](int r) { return PACKED && (s_any[r] & 2) ? -1.f : sA[r][tid]; };
-            float tA = 1.f, tG = 0.f, G = 0.f;
-#pragma unroll
-            for (int r = R - 1; r >= 0; --r) {
-                tG = apply(run_A(r), sG[r][tid], tG);
-                tA = both(tA, run_A(r));
-            }
-            const int q = x.tiles - 1 - now.p;
-            if (!PACKED && q < kGroup && a.dhT && c < a.D) G = a.dhT[(size_t)now.b * a.D + c];
-            G = carry_in(x, W, q, now.chain, tid, tA, tG, G, true, &g_glr_bwd_status);
-#pragma unroll
-            for (int r = R - 1; r >= 0; --r) {
-                const float rG = sG[r][tid];
-                sG[r][tid] = G;
-                G = apply(run_A(r), rG, G);
-            }
-        } else if (tid < 2 * W) {                // the states that enter the runs
-            const int c = tid - W;
-            float h = enter;
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const float rA = PACKED && (s_any[r] & 1) ? -1.f : sA[r][c], rH = sH[r][c];
-                sH[r][c] = h;
-                h = apply(rA, rH, h);
-            }
-        }
-        __syncthreads();
-
-        // h_{t-1} of every token in place of u, then the gradients from the last token to the first
-        float h[V], pA[V], pdt[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            h[v] = sH[run][lane * V + v];
-            G[v] = sG[run][lane * V + v];
-            pA[v] = pdt[v] = 0.f;
-        }
-#pragma unroll
-        for (int j = 0; j < L; ++j) {
             const bool start = PACKED && ((starts >> j) & 1);
+            if (start && a.h0 && live)
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    q.u[j][v] = fmaf(q.al[j][v], a.h0[(size_t)s_start[i % kPlaces][run * L + j] * a.D + c + v], q.u[j][v]);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const float uj = u[j][v];
-                u[j][v] = h[v];
-                if (start) {
-                    u[j][v] = a.h0 && now.live ? a.h0[(size_t)s_start[k][run * L + j] * a.D + now.c + v] : 0.f;
-                    h[v] = uj;
-                } else {
-                    h[v] = fmaf(al[j][v], h[v], uj);
-                }
+                H[v] = start ? q.u[j][v] : fmaf(q.al[j][v], H[v], q.u[j][v]);
+                A[v] *= q.al[j][v];
             }
         }
-        Tx* dx_p = static_cast<Tx*>(a.dx) + (now.row + L) * a.D + now.c;
-        Tx* di_p = static_cast<Tx*>(a.di) + (now.row + L) * a.D + now.c;
-        Tg* dg_p = static_cast<Tg*>(a.dg) + (now.row + L) * a.D + now.c;
-        const int n = now.live ? now.count : 0;
 #pragma unroll
         for (int j = L - 1; j >= 0; --j) {
             const bool end = PACKED && ((ends >> j) & 1);
-            Vec<Tx, V> dx, di;
-            Vec<Tg, V> dg;
-            dx_p -= a.D;
-            di_p -= a.D;
-            dg_p -= a.D;
+            float d[V];
+            grad_o(i, j, c, end, d);
+#pragma unroll
+            for (int v = 0; v < V; ++v) G[v] = q.al[j][v] * (end ? d[v] : d[v] + G[v]);
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            sA[i & 1][run][lane * V + v] = A[v];
+            sH[i & 1][run][lane * V + v] = H[v];
+            sG[i & 1][run][lane * V + v] = G[v];
+        }
+        if (PACKED && lane == 0) s_any[i & 1][run] = (starts ? 1 : 0) | (ends ? 2 : 0);
+        bar_arrive(kMaps + (i & 1));
+    };
+
+    // stage two: with h_{t-1}, and D the gradient of h_t,
+    //   dx = D s sigma(i), di = dx x (1 - sigma(i)), dla = D (a h_{t-1} - sigma(i) x a^2 / s), dg = dla dlog a/dg
+    const auto gradients = [&](int i, const Held& q) {
+        const Tile t = s_tile[i % kPlaces];
+        const int c = t.c0 + lane * V, t0 = t.p * kTile + run * L;
+        const bool live = c < a.D;
+        const int n = live ? a.T - t0 : 0;
+        unsigned starts, ends;
+        marks(i, &starts, &ends);
+        float D[L][V], G[V], h[V], pA[V], pdt[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            G[v] = sG[i & 1][run][lane * V + v];
+            h[v] = sH[i & 1][run][lane * V + v];
+            pA[v] = pdt[v] = 0.f;
+        }
+#pragma unroll
+        for (int j = L - 1; j >= 0; --j) {
+            const bool end = PACKED && ((ends >> j) & 1);
+            grad_o(i, j, c, end, D[j]);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const float D = end ? dO[j][v] : dO[j][v] + G[v];
-                G[v] = al[j][v] * D;
-                const float dla = D * fmaf(al[j][v], u[j][v], -m[j][v]), dw = D * w[j][v], dz = dla * w3[j][v];
-                dx.set(v, dw);
-                di.set(v, dw * y[j][v]);
-                dg.set(v, dz);
-                if (j < n) {
-                    pA[v] = fmaf(dla, la[j][v], pA[v]);
-                    pdt[v] += dz;
+                if (!end) D[j][v] += G[v];
+                G[v] = q.al[j][v] * D[j][v];
+            }
+            if (PACKED && a.dh0 && live) {
+                const int s = s_start[i % kPlaces][run * L + j];
+                if (s >= 0)
+#pragma unroll
+                    for (int v = 0; v < V; ++v) a.dh0[(size_t)s * a.D + c + v] = G[v];
+            }
+        }
+        Channel ch[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) ch[v] = live ? channel(a.A_log, a.dt_bias, c + v) : Channel{0.f, 0.f};
+        const size_t at = ((size_t)t.b * a.T + t0) * a.D + c;
+        Tx* dx_p = static_cast<Tx*>(a.dx) + at;
+        Tx* di_p = static_cast<Tx*>(a.di) + at;
+        Tg* dg_p = static_cast<Tg*>(a.dg) + at;
+#pragma unroll
+        for (int j = 0; j < L; ++j) {
+            const bool start = PACKED && ((starts >> j) & 1);
+            float hp[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                hp[v] = h[v];
+                h[v] = start ? q.u[j][v] : fmaf(q.al[j][v], h[v], q.u[j][v]);
+            }
+            if (start)
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    hp[v] = a.h0 && live ? a.h0[(size_t)s_start[i % kPlaces][run * L + j] * a.D + c + v] : 0.f;
+            const Vec<Tx, V> xv = buf_x(i)[j * kThreads];
+            float w[V], y[V], xs[V], dla[V], dz[V];   // s sigma(i), x (1 - sigma(i)), x sigma(i)
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                xs[v] = xv.get(v);
+                w[v] = 1.f;
+                y[v] = 0.f;
+            }
+            if (a.gi) {
+                const Vec<Tx, V> gi = buf_x(i)[(2 * L + j) * kThreads];
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    // 1 - sigma(i) = exp(-i) sigma(i), with exp(-i) kept finite
+                    const float f = ex2(max_nan(gi.get(v), -80.f) * -kLog2e);
+                    w[v] = rcp(1.f + f);
+                    xs[v] *= w[v];
+                    y[v] = xs[v] * f;
                 }
+            }
+#pragma unroll
+            for (int v = 0; v < V; ++v) dla[v] = q.al[j][v] * hp[v];
+            if (a.normalize) {
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    // ds/dlog a = -a^2 / s, taken as 0 where s = 0 (log a = 0: the derivative does not exist there)
+                    const float s2 = input_power({q.al[j][v], q.e[j][v]}), rs = s2 > 0.f ? rsq(s2) : 0.f;
+                    w[v] *= s2 * rs;
+                    dla[v] = fmaf(-xs[v] * rs, q.al[j][v] * q.al[j][v], dla[v]);
+                }
+            }
+#pragma unroll
+            for (int v = 0; v < V; ++v) dz[v] = dla[v] *= D[j][v];
+            if (a.A_log) {
+                const Vec<Tg, V> g = buf_g(i)[j * kThreads];
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    const float z = g.get(v) + ch[v].dt;
+                    dz[v] *= ch[v].neg_eA * sigmoid(z, tail(z));
+                    if (j < n) {
+                        pA[v] = fmaf(dla[v], q.la[j][v], pA[v]);
+                        pdt[v] += dz[v];
+                    }
+                }
+            }
+            Vec<Tx, V> dx, di;
+            Vec<Tg, V> dg;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float d = D[j][v] * w[v];
+                dx.set(v, d);
+                di.set(v, d * y[v]);
+                dg.set(v, dz[v]);
             }
             if (j < n) {
                 dx.store(dx_p);
                 dg.store(dg_p);
                 if (a.gi) di.store(di_p);
             }
-            if (PACKED && a.dh0 && now.live) {
-                const int s = s_start[k][run * L + j];
-                if (s >= 0)
-#pragma unroll
-                    for (int v = 0; v < V; ++v) a.dh0[(size_t)s * a.D + now.c + v] = G[v];
-            }
+            dx_p += a.D;
+            di_p += a.D;
+            dg_p += a.D;
         }
-        if (!PACKED && a.dh0 && now.live && now.p == 0 && run == 0)
+        if (!PACKED && a.dh0 && live && t.p == 0 && run == 0)
 #pragma unroll
-            for (int v = 0; v < V; ++v) a.dh0[(size_t)now.b * a.D + now.c + v] = G[v];
-        if (PACKED && a.dh0 && now.live) {
-            for (int s = now.p * R + run; s < a.n_seqs; s += x.tiles * R) {
+            for (int v = 0; v < V; ++v) a.dh0[(size_t)t.b * a.D + c + v] = G[v];
+        if (PACKED && a.dh0 && live) {
+            // empty sequences: what enters behind leaves in front; the row's tiles share them
+            for (int s = t.p * R + run; s < a.n_seqs; s += x.tiles * R) {
                 if (mix::clamp_off(a.cu[s + 1], a.T) > mix::clamp_off(a.cu[s], a.T)) continue;
 #pragma unroll
-                for (int v = 0; v < V; ++v)
-                    a.dh0[(size_t)s * a.D + now.c + v] = a.dhT ? a.dhT[(size_t)s * a.D + now.c + v] : 0.f;
+                for (int v = 0; v < V; ++v) a.dh0[(size_t)s * a.D + c + v] = a.dhT ? a.dhT[(size_t)s * a.D + c + v] : 0.f;
             }
         }
-        if (a.dA) {                              // the tile's sums, runs in order
+        if (a.dA)
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                sA[run][lane * V + v] = pA[v];
-                sG[run][lane * V + v] = pdt[v];  // (each thread overwrites what it alone has read)
+                s_sum[i & 1][0][run][lane * V + v] = pA[v];
+                s_sum[i & 1][1][run][lane * V + v] = pdt[v];
             }
-            __syncthreads();
-            if (tid < 2 * W && now.c0 + tid % W < a.D) {
-                const float(*src)[W] = tid < W ? sA : sG;
-                float s = 0.f;
-#pragma unroll
-                for (int r = 0; r < R; ++r) s += src[r][tid % W];
-                const size_t rows = (size_t)a.B * x.tiles, r = (size_t)now.b * x.tiles + now.p;
-                part[((tid < W ? 0 : rows) + r) * a.D + now.c0 + tid % W] = s;
-            }
-            __syncthreads();
+    };
+
+    bar_arrive(kMaps);
+    __syncthreads();
+    if (s_tile[0].chain < 0) return;
+    fetch(0);
+    fetch(1);
+    Held q0, q1;
+    const auto step = [&](int i, Held& q, const Held& before) {
+        const bool more = s_tile[i % kPlaces].chain >= 0;
+        if (more) {
+            mix::copies_wait<1>();
+            maps(i, q);
         }
-        id = next;
+        if (i > 0) bar_sync(kCarry + ((i - 1) & 1));
+        if (i > 0) gradients(i - 1, before);
+        if (more) fetch(i + 2);                  // (into the buffer of tile i - 1)
+        else if (a.dA) bar_arrive(kMaps + (i & 1));
+        return more;
+    };
+    for (int i = 0;; i += 2) {
+        if (!step(i, q0, q1)) break;
+        if (!step(i + 1, q1, q0)) break;
     }
 }
 
@@ -358,18 +447,19 @@ __global__ void __launch_bounds__(256) glr_param_kernel(const float* part, int r
 
 template <typename Tx, typename Tg, int LANES, int V, bool PACKED>
 cudaError_t bwd(const GlrArgs& a, const BwdSpace& sp, cudaStream_t s) {
-    using At = Place<LANES, V>;
-    const Layout l = layout(a.B, a.T, a.D, At::W);
+    using S = Shape<LANES, V>;
+    const Layout l = layout(a.B, a.T, a.D, S::W);
     const Exchange x = exchange(l, sp.scan);
     if (l.bytes) {
         const cudaError_t e = cudaMemsetAsync(sp.scan, 0xff, l.bytes, s);
         if (e != cudaSuccess) return e;
     }
     const auto kernel = glr_bwd_kernel<Tx, Tg, LANES, V, PACKED>;
-    const size_t smem = (size_t)At::L * kThreads * V * (sizeof(Tg) + 3 * sizeof(Tx));
-    static const Residency res = residency(reinterpret_cast<const void*>(kernel), smem);
-    if (res.error != cudaSuccess) return res.error;
-    kernel<<<x.total < res.blocks ? x.total : res.blocks, kThreads, smem, s>>>(a, x, sp.part);
+    const int smem = kBuffers * S::L * kThreads * V * (int)(sizeof(Tg) + (a.gi ? 3 : 2) * sizeof(Tx));
+    static Residency res[2];                     // without and with the input gate
+    const int blocks = res[a.gi != nullptr].get(reinterpret_cast<const void*>(kernel), smem);
+    if (blocks == 0) return cudaGetLastError();
+    kernel<<<x.total < blocks ? x.total : blocks, kBlock, smem, s>>>(a, x, sp.part);
     if (a.dA)
         glr_param_kernel<<<dim3((a.D + 31) / 32, 2), 256, 0, s>>>(sp.part, a.B * l.tiles, a.D, a.dA, a.ddt);
     return cudaGetLastError();
