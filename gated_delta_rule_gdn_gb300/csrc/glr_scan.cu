@@ -5,6 +5,7 @@
 #include <type_traits>
 
 #include "glr_scan.cuh"
+#include "internal.h"
 
 namespace gdn {
 namespace {
@@ -15,11 +16,10 @@ using mix::Vec;
 
 __device__ unsigned g_glr_status;   // bit 0: a block gave up a bounded wait
 
-template <typename Tx, typename Tg, int LANES, int V, bool PACKED>
-__global__ void __launch_bounds__(kBlock, 2)
+template <typename Tx, typename Tg, typename S, bool PACKED>
+__global__ void __launch_bounds__(S::kBlock, 2)
 glr_fwd_kernel(const GlrArgs a, const Exchange x, const int publish) {
-    using S = Shape<LANES, V>;
-    constexpr int W = S::W, R = S::R, L = S::L;
+    constexpr int LANES = S::LANES, V = S::V, W = S::W, R = S::R, L = S::L, kThreads = S::kThreads;
     static_assert(W <= kCarryThreads, "a carry thread for every channel");
     extern __shared__ __align__(16) unsigned char s_raw[];
     __shared__ float sA[2][R][W], sH[2][R][W];
@@ -36,7 +36,7 @@ glr_fwd_kernel(const GlrArgs a, const Exchange x, const int publish) {
             ticket = tickets.take();
         }
         __syncwarp();
-        bar_sync(kMaps);                         // (places are read below by all carry threads: meet once)
+        S::sync(kMaps);                         // (places are read below by all carry threads: meet once)
         if (PACKED)
             for (int i = 0; i < 3; ++i)
                 if (s_tile[i].chain >= 0) sequence_marks(a, s_tile[i].p, ch, s_start[i], s_end[i]);
@@ -50,28 +50,28 @@ glr_fwd_kernel(const GlrArgs a, const Exchange x, const int publish) {
             }
             float first = 0.f;
             if (!PACKED && ch < W && t.p < kGroup && a.h0 && t.c0 + ch < a.D) first = a.h0[(size_t)t.b * a.D + t.c0 + ch];
-            bar_sync(kMaps + k);
+            S::sync(kMaps + k);
             if (ch < W) {
                 float A = 1.f, H = 0.f;
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
-                    H = apply(sA[k][r][ch], sH[k][r][ch], H);
-                    A = both(A, sA[k][r][ch]);
+                    H = apply<PACKED>(sA[k][r][ch], sH[k][r][ch], H);
+                    A = both<PACKED>(A, sA[k][r][ch]);
                 }
                 if (publish || t.p > 0) hand_map(x, W, t.p, t.chain, ch, A, H);
-                float h = carry_in(x, W, t.p, t.chain, ch, first, &g_glr_status);
-                hand_state(x, W, t.p, t.chain, ch, apply(A, H, h));
+                float h = carry_in<PACKED>(x, W, t.p, t.chain, ch, first, &g_glr_status);
+                hand_state(x, W, t.p, t.chain, ch, apply<PACKED>(A, H, h));
                 if (a.ckpt && t.c0 + ch < a.D && t.p * kTile < a.T)
                     a.ckpt[((size_t)t.b * x.tiles + t.p) * a.D + t.c0 + ch] = h;
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
                     const float rH = sH[k][r][ch];
                     sH[k][r][ch] = h;
-                    h = apply(sA[k][r][ch], rH, h);
+                    h = apply<PACKED>(sA[k][r][ch], rH, h);
                 }
             }
+            S::arrive(kCarry + k);
             if (PACKED && s_tile[ahead].chain >= 0) sequence_marks(a, s_tile[ahead].p, ch, s_start[ahead], s_end[ahead]);
-            bar_arrive(kCarry + k);
         }
         return;
     }
@@ -79,7 +79,7 @@ glr_fwd_kernel(const GlrArgs a, const Exchange x, const int publish) {
     // the compute threads
     const int run = tid / LANES, lane = tid % LANES, arrays = a.gi ? 3 : 2;
     const int bytes = L * kThreads * (int)(sizeof(Vec<Tg, V>) + (arrays - 1) * sizeof(Vec<Tx, V>));
-    const auto buf_g = [&](int k) { return reinterpret_cast<Vec<Tg, V>*>(s_raw + k * bytes) + tid; };   // [L][256] each
+    const auto buf_g = [&](int k) { return reinterpret_cast<Vec<Tg, V>*>(s_raw + k * bytes) + tid; };   // [L][kThreads] each
     const auto buf_x = [&](int k) {
         return reinterpret_cast<Vec<Tx, V>*>(s_raw + k * bytes + L * kThreads * sizeof(Vec<Tg, V>)) + tid;
     };
@@ -93,8 +93,21 @@ glr_fwd_kernel(const GlrArgs a, const Exchange x, const int publish) {
         const Tx* ip = static_cast<const Tx*>(a.gi) + row * a.ldi + c;
         Vec<Tg, V>* bg = buf_g(i & 1);
         Vec<Tx, V>* bx = buf_x(i & 1);
+        if (n == L) {
 #pragma unroll
-        for (int j = 0; j < L; ++j) {
+            for (int j = 0; j < L; ++j) {
+                mix::copy_async(bg + j * kThreads, g, true);
+                mix::copy_async(bx + j * kThreads, xp, true);
+                if (a.gi) mix::copy_async(bx + (L + j) * kThreads, ip, true);
+                g += a.ldg;
+                xp += a.ldx;
+                ip += a.ldi;
+            }
+            mix::copies_close();
+            return;
+        }
+#pragma unroll 1
+        for (int j = 0; j < L; ++j) {            // the row's end, or no channels
             mix::copy_async(bg + j * kThreads, j < n ? g : static_cast<const Tg*>(a.g), j < n);
             mix::copy_async(bx + j * kThreads, j < n ? xp : static_cast<const Tx*>(a.x), j < n);
             if (a.gi) mix::copy_async(bx + (L + j) * kThreads, j < n ? ip : static_cast<const Tx*>(a.gi), j < n);
@@ -199,7 +212,7 @@ glr_fwd_kernel(const GlrArgs a, const Exchange x, const int publish) {
             sA[i & 1][run][lane * V + v] = A[v];
             sH[i & 1][run][lane * V + v] = H[v];
         }
-        bar_arrive(kMaps + (i & 1));
+        S::arrive(kMaps + (i & 1));
     };
 
     // stage two: the states
@@ -244,26 +257,29 @@ glr_fwd_kernel(const GlrArgs a, const Exchange x, const int publish) {
         }
     };
 
-    bar_arrive(kMaps);
+    S::arrive(kMaps);
     __syncthreads();
+    if (s_tile[0].chain < 0) return;
     fetch(0);
     fetch(1);
-    float al0[L][V], u0[L][V], al1[L][V], u1[L][V];
-    const auto step = [&](int i, float (&al)[L][V], float (&u)[L][V], const float (&al_p)[L][V], const float (&u_p)[L][V]) {
+    float al[L][V], u[L][V], al_p[L][V], u_p[L][V];           // the current tile's, and the one's before it
+    for (int i = 0;; ++i) {
         const bool more = s_tile[i % kPlaces].chain >= 0;
         if (more) {
             mix::copies_wait<1>();
             maps(i, al, u);
         }
-        if (i > 0) bar_sync(kCarry + ((i - 1) & 1));
+        if (i > 0) S::sync(kCarry + ((i - 1) & 1));
         if (more) fetch(i + 2);
         if (i > 0) states(i - 1, al_p, u_p);
-        return more;
-    };
-    if (s_tile[0].chain < 0) return;
-    for (int i = 0;; i += 2) {
-        if (!step(i, al0, u0, al1, u1)) break;
-        if (!step(i + 1, al1, u1, al0, u0)) break;
+        if (!more) break;
+#pragma unroll
+        for (int j = 0; j < L; ++j)
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                al_p[j][v] = al[j][v];
+                u_p[j][v] = u[j][v];
+            }
     }
 }
 
@@ -285,48 +301,50 @@ __global__ void glr_step_kernel(const GlrStepArgs a) {
     mix::st(static_cast<Tx*>(a.o) + n * a.D + c, h);
 }
 
-template <typename Tx, typename Tg, int LANES, int V, bool PACKED>
+template <typename Tx, typename Tg, typename S, bool PACKED>
 cudaError_t fwd(const GlrArgs& a, cudaStream_t s) {
-    using S = Shape<LANES, V>;
     const Layout l = layout(a.B, a.T, a.D, S::W);
     const Exchange x = exchange(l, a.ws);
     if (l.bytes) {
         const cudaError_t e = cudaMemsetAsync(a.ws, 0xff, l.bytes, s);
         if (e != cudaSuccess) return e;
     }
-    const auto kernel = glr_fwd_kernel<Tx, Tg, LANES, V, PACKED>;
-    const int smem = 2 * S::L * kThreads * V * (int)(sizeof(Tg) + (a.gi ? 2 : 1) * sizeof(Tx));
+    const auto kernel = glr_fwd_kernel<Tx, Tg, S, PACKED>;
+    const int smem = 2 * S::L * S::kThreads * S::V * (int)(sizeof(Tg) + (a.gi ? 2 : 1) * sizeof(Tx));
     static Residency res[2];                     // without and with the input gate
-    const int blocks = res[a.gi != nullptr].get(reinterpret_cast<const void*>(kernel), smem);
+    const int blocks = res[a.gi != nullptr].get(reinterpret_cast<const void*>(kernel), S::kBlock, smem);
     if (blocks == 0) return cudaGetLastError();
-    kernel<<<x.total < blocks ? x.total : blocks, kBlock, smem, s>>>(a, x, a.test_stall ? 0 : 1);
+    kernel<<<x.total < blocks ? x.total : blocks, S::kBlock, smem, s>>>(a, x, a.test_stall ? 0 : 1);
     return cudaGetLastError();
 }
 
-template <typename Tx, typename Tg, int LANES, int V>
+template <typename Tx, typename Tg, typename S>
 cudaError_t fwd_packed(const GlrArgs& a, cudaStream_t s) {
-    return a.cu ? fwd<Tx, Tg, LANES, V, true>(a, s) : fwd<Tx, Tg, LANES, V, false>(a, s);
+    return a.cu ? fwd<Tx, Tg, S, true>(a, s) : fwd<Tx, Tg, S, false>(a, s);
 }
 
 template <typename Tx, typename Tg>
 cudaError_t fwd_wide(const GlrArgs& a, cudaStream_t s) {
-    if (glr_vector(a, 4)) return fwd_packed<Tx, Tg, 16, 4>(a, s);
-    if (glr_vector(a, 2)) return fwd_packed<Tx, Tg, 32, 2>(a, s);
-    return fwd_packed<Tx, Tg, 32, 1>(a, s);
+    if (glr_vector(a, 4)) return fwd_packed<Tx, Tg, Shape<16, 4, 8>>(a, s);
+    if (glr_vector(a, 2)) return fwd_packed<Tx, Tg, Shape<32, 2, 8>>(a, s);
+    return fwd_packed<Tx, Tg, Shape<32, 1, 8>>(a, s);
 }
 
 }  // namespace
 
 namespace glr {
-int Residency::get(const void* kernel, int smem) {
+int Residency::get(const void* kernel, int threads, int smem) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev >= kDevices) return 0;
     int n = blocks[dev].load(std::memory_order_relaxed);
     if (n > 0) return n;
     int sms = 0, per = 0;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamicSmem) != cudaSuccess ||
+    cudaFuncAttributes attr{};
+    if (cudaFuncGetAttributes(&attr, kernel) != cudaSuccess ||
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)(kMaxSmemPerBlock - attr.sharedSizeBytes)) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, kBlock, smem) != cudaSuccess)
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, threads, smem) != cudaSuccess)
         return 0;
     n = sms * (per > 0 ? per : 1);
     blocks[dev].store(n, std::memory_order_relaxed);

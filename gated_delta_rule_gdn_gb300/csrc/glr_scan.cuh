@@ -1,9 +1,8 @@
 // Shared parts of the gated linear recurrence's scans (glr_scan.cu, glr_scan_bwd.cu): the tiling, the input buffer, and
 // the carry of a tile from the tiles before it.
 //
-// A row of T tokens is cut into tiles of 64 tokens x W = LANES * V channels.  A block takes one tile after another with 256
-// compute threads; LANES threads side by side read V channels each, and so it has 256 / LANES runs of LANES / 4 consecutive
-// tokens, each held in the registers of its threads.  The recurrence over a run of tokens is the map h -> A h + H; a run
+// A row of T tokens is cut into tiles of 64 tokens x W = LANES * V channels.  A block takes one tile after another; LANES
+// threads side by side read V channels each and L consecutive tokens, a run, and 64 / L such rows of threads take the tile.  The recurrence over a run of tokens is the map h -> A h + H; a run
 // in which a sequence starts (backward: ends) forgets h altogether, which is written A = -1 (decays are never negative),
 // so that a state that is not a number stays in its own sequence.
 //
@@ -26,7 +25,6 @@
 namespace gdn {
 namespace glr {
 
-constexpr int kThreads = 256;
 constexpr int kTile = kGlrTile;                  // checkpoints are tile entries
 constexpr int kGroup = 16;
 constexpr unsigned kEmpty = 0xffffffffu;
@@ -34,10 +32,10 @@ constexpr unsigned long long kWaitNs = 2000000000ull;
 
 // How many blocks of a kernel with this much dynamic shared memory the device holds at once (persistent kernels launch no
 // more), asked once per device; 0 if a query failed.
-constexpr int kDevices = 64, kMaxDynamicSmem = 200 * 1024;
+constexpr int kDevices = 64;
 struct Residency {
     std::atomic<int> blocks[kDevices]{};
-    int get(const void* kernel, int smem);
+    int get(const void* kernel, int threads, int smem);
 };
 
 // Workspace of one scan, set to all ones before the launch.
@@ -80,8 +78,13 @@ inline Exchange exchange(const Layout& l, void* ws) {
     return x;
 }
 
-__device__ __forceinline__ float apply(float A, float H, float h) { return A < 0.f ? H : fmaf(A, h, H); }
-__device__ __forceinline__ float both(float A1, float A2) { return A1 < 0.f || A2 < 0.f ? -1.f : A1 * A2; }
+// Maps applied and composed; without packed sequences none forgets.
+template <bool PACKED>
+__device__ __forceinline__ float apply(float A, float H, float h) { return PACKED && A < 0.f ? H : fmaf(A, h, H); }
+template <bool PACKED>
+__device__ __forceinline__ float both(float A1, float A2) {
+    return PACKED && (A1 < 0.f || A2 < 0.f) ? -1.f : A1 * A2;
+}
 
 __device__ __forceinline__ unsigned long long load_word(const unsigned long long* p) {
     unsigned long long v;
@@ -115,6 +118,7 @@ __device__ __forceinline__ void hand_state(const Exchange& x, int W, int p, int 
 }
 
 // The carry into tile p of a chain, for one channel; `first` is the state before tile 0 of the row.
+template <bool PACKED>
 __device__ __forceinline__ float carry_in(const Exchange& x, int W, int p, int chain, int ch, float first, unsigned* status) {
     const int group = p / kGroup, start = group * kGroup, n = p - start;
     if (p == 0) return first;
@@ -148,10 +152,10 @@ __device__ __forceinline__ float carry_in(const Exchange& x, int W, int p, int c
 #pragma unroll
     for (int j = 0; j < kGroup - 1; ++j) {
         const float a = __uint_as_float((unsigned)m[j]), h = __uint_as_float((unsigned)(m[j] >> 32));
-        cH = apply(a, h, cH);
-        cA = both(cA, a);
+        cH = apply<PACKED>(a, h, cH);
+        cA = both<PACKED>(cA, a);
     }
-    return apply(cA, cH, group > 0 ? __uint_as_float(st) : first);
+    return apply<PACKED>(cA, cH, group > 0 ? __uint_as_float(st) : first);
 }
 
 struct Channel { float neg_eA, dt; };   // -exp(A_log) (0: g is log a) and dt_bias of a channel
@@ -159,20 +163,26 @@ __device__ __forceinline__ Channel channel(const float* A_log, const float* dt_b
     return {A_log ? -expf(A_log[c]) : 0.f, dt_bias ? dt_bias[c] : 0.f};
 }
 
-// The block's division of work.  Its 256 compute threads take a tile in two stages: the maps of their runs (stage one), and
+// The block's division of work.  Its compute threads take a tile in two stages: the maps of their runs (stage one), and
 // with the states that enter the runs the outputs (stage two).  Stage two of a tile comes after stage one of the next, so
 // that the carry, which kCarryThreads threads of their own work out in between, has that long to arrive.  Two more
 // tiles' inputs are on the way meanwhile.  Per tile i the two sides meet at two barriers, each of one parity of i:
 //   MAPS   the compute threads have left their runs' maps in shared memory;
 //   CARRY  the carry threads have left the runs' entering states there, and tile i + 3's place in the ring of places.
-constexpr int kCarryThreads = 64, kBlock = kThreads + kCarryThreads, kPlaces = 8;
-__device__ __forceinline__ void bar_arrive(int id) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "n"(kBlock) : "memory"); }
-__device__ __forceinline__ void bar_sync(int id) { asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(kBlock) : "memory"); }
+// (Its sequence marks follow, in time for CARRY of tile i + 1.)
+constexpr int kCarryThreads = 64, kPlaces = 8;
 constexpr int kMaps = 1, kCarry = 3;
 
-template <int LANES, int V>
+template <int LANES_, int V_, int L_>
 struct Shape {
-    static constexpr int W = LANES * V, R = kThreads / LANES, L = kTile / R;
+    static constexpr int LANES = LANES_, V = V_, L = L_, W = LANES * V, R = kTile / L;
+    static constexpr int kThreads = LANES * R, kBlock = kThreads + kCarryThreads;      // compute threads, all threads
+    static __device__ __forceinline__ void arrive(int id) {
+        asm volatile("bar.arrive %0, %1;" ::"r"(id), "n"(kBlock) : "memory");
+    }
+    static __device__ __forceinline__ void sync(int id) {
+        asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(kBlock) : "memory");
+    }
 };
 
 // A tile: its place in the row, batch row, first channel and chain (chain < 0: there is none).

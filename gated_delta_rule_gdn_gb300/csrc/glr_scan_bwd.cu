@@ -24,14 +24,13 @@ struct BwdSpace { void* scan; float* part; };
 // the front, and forms each token's gradients on the way.
 constexpr int kBuffers = 3;
 
-template <typename Tx, typename Tg, int LANES, int V, bool PACKED>
-__global__ void __launch_bounds__(kBlock, 2)
+template <typename Tx, typename Tg, typename S, bool PACKED>
+__global__ void __launch_bounds__(S::kBlock, 2)
 glr_bwd_kernel(const GlrArgs a, const Exchange x, float* part) {
-    using S = Shape<LANES, V>;
-    constexpr int W = S::W, R = S::R, L = S::L;
+    constexpr int LANES = S::LANES, V = S::V, W = S::W, R = S::R, L = S::L, kThreads = S::kThreads;
     static_assert(2 * W <= kCarryThreads, "a carry thread for every channel and direction");
     extern __shared__ __align__(16) unsigned char s_raw[];
-    __shared__ float sA[2][R][W], sH[2][R][W], sG[2][R][W], s_sum[2][2][R][W];
+    __shared__ float sA[2][R][W], sH[2][R][W], sG[2][R][W], s_sum[3][2][R][W];
     __shared__ unsigned char s_any[2][R];        // bit 0: a sequence starts in the run; bit 1: one ends
     __shared__ int s_start[PACKED ? kPlaces : 1][kTile], s_end[PACKED ? kPlaces : 1][kTile];
     __shared__ Tile s_tile[kPlaces];
@@ -46,7 +45,7 @@ glr_bwd_kernel(const GlrArgs a, const Exchange x, float* part) {
             ticket = tickets.take();
         }
         __syncwarp();
-        bar_sync(kMaps);
+        S::sync(kMaps);
         if (PACKED)
             for (int i = 0; i < 3; ++i)
                 if (s_tile[i].chain >= 0) sequence_marks(a, s_tile[i].p, tid - kThreads, s_start[i], s_end[i]);
@@ -57,7 +56,7 @@ glr_bwd_kernel(const GlrArgs a, const Exchange x, float* part) {
             if (side > 1 || t.c0 + ch >= a.D) return;
             float s = 0.f;
 #pragma unroll
-            for (int r = 0; r < R; ++r) s += s_sum[i & 1][side][r][ch];
+            for (int r = 0; r < R; ++r) s += s_sum[i % 3][side][r][ch];
             const size_t rows = (size_t)a.B * x.tiles, r = (size_t)t.b * x.tiles + t.p;
             part[((side ? rows : 0) + r) * a.D + t.c0 + ch] = s;
         };
@@ -78,23 +77,23 @@ glr_bwd_kernel(const GlrArgs a, const Exchange x, float* part) {
                 if (t.p > 0 || PACKED) enter = a.ckpt[((size_t)t.b * x.tiles + t.p) * a.D + t.c0 + ch];
                 else if (a.h0) enter = a.h0[(size_t)t.b * a.D + t.c0 + ch];
             }
-            bar_sync(kMaps + k);
+            S::sync(kMaps + k);
             if (side == 0) {
                 const auto run_A = [&](int r) { return PACKED && (s_any[k][r] & 2) ? -1.f : sA[k][r][ch]; };
                 float A = 1.f, G = 0.f;
 #pragma unroll
                 for (int r = R - 1; r >= 0; --r) {
-                    G = apply(run_A(r), sG[k][r][ch], G);
-                    A = both(A, run_A(r));
+                    G = apply<PACKED>(run_A(r), sG[k][r][ch], G);
+                    A = both<PACKED>(A, run_A(r));
                 }
                 hand_map(x, W, q, t.chain, ch, A, G);
-                float g = carry_in(x, W, q, t.chain, ch, enter, &g_glr_bwd_status);
-                hand_state(x, W, q, t.chain, ch, apply(A, G, g));
+                float g = carry_in<PACKED>(x, W, q, t.chain, ch, enter, &g_glr_bwd_status);
+                hand_state(x, W, q, t.chain, ch, apply<PACKED>(A, G, g));
 #pragma unroll
                 for (int r = R - 1; r >= 0; --r) {
                     const float rG = sG[k][r][ch];
                     sG[k][r][ch] = g;
-                    g = apply(run_A(r), rG, g);
+                    g = apply<PACKED>(run_A(r), rG, g);
                 }
             } else if (side == 1) {
                 float h = enter;
@@ -102,16 +101,16 @@ glr_bwd_kernel(const GlrArgs a, const Exchange x, float* part) {
                 for (int r = 0; r < R; ++r) {
                     const float rA = PACKED && (s_any[k][r] & 1) ? -1.f : sA[k][r][ch], rH = sH[k][r][ch];
                     sH[k][r][ch] = h;
-                    h = apply(rA, rH, h);
+                    h = apply<PACKED>(rA, rH, h);
                 }
             }
+            S::arrive(kCarry + k);
             if (a.dA && i >= 2) sums(i - 2);     // (stage two of tile i - 2 came before the maps of tile i)
             if (PACKED && s_tile[ahead].chain >= 0)
                 sequence_marks(a, s_tile[ahead].p, tid - kThreads, s_start[ahead], s_end[ahead]);
-            bar_arrive(kCarry + k);
         }
         if (a.dA && i > 0) {
-            bar_sync(kMaps + (i & 1));           // the compute threads are through
+            S::sync(kMaps + (i & 1));           // the compute threads are through
             if (i >= 2) sums(i - 2);
             sums(i - 1);
         }
@@ -122,7 +121,7 @@ glr_bwd_kernel(const GlrArgs a, const Exchange x, float* part) {
     const int run = tid / LANES, lane = tid % LANES, arrays = a.gi ? 4 : 3;
     const int bytes = L * kThreads * (int)(sizeof(Vec<Tg, V>) + (arrays - 1) * sizeof(Vec<Tx, V>));
     const auto buf_g = [&](int i) { return reinterpret_cast<Vec<Tg, V>*>(s_raw + i % kBuffers * bytes) + tid; };
-    const auto buf_x = [&](int i) {              // x, dO, and the input gate's logits: [L][256] each
+    const auto buf_x = [&](int i) {              // x, dO, and the input gate's logits: [L][kThreads] each
         return reinterpret_cast<Vec<Tx, V>*>(s_raw + i % kBuffers * bytes + L * kThreads * sizeof(Vec<Tg, V>)) + tid;
     };
     const auto fetch = [&](int i) {
@@ -136,8 +135,23 @@ glr_bwd_kernel(const GlrArgs a, const Exchange x, float* part) {
         const Tx* op = static_cast<const Tx*>(a.dO) + row * a.D + c;
         Vec<Tg, V>* bg = buf_g(i);
         Vec<Tx, V>* bx = buf_x(i);
+        if (n == L) {
 #pragma unroll
-        for (int j = 0; j < L; ++j) {
+            for (int j = 0; j < L; ++j) {
+                mix::copy_async(bg + j * kThreads, g, true);
+                mix::copy_async(bx + j * kThreads, xp, true);
+                mix::copy_async(bx + (L + j) * kThreads, op, true);
+                if (a.gi) mix::copy_async(bx + (2 * L + j) * kThreads, ip, true);
+                op += a.D;
+                g += a.ldg;
+                xp += a.ldx;
+                ip += a.ldi;
+            }
+            mix::copies_close();
+            return;
+        }
+#pragma unroll 1
+        for (int j = 0; j < L; ++j) {            // the row's end, or no channels
             mix::copy_async(bg + j * kThreads, j < n ? g : static_cast<const Tg*>(a.g), j < n);
             mix::copy_async(bx + j * kThreads, j < n ? xp : static_cast<const Tx*>(a.x), j < n);
             mix::copy_async(bx + (L + j) * kThreads, j < n ? op : static_cast<const Tx*>(a.dO), j < n);
@@ -261,7 +275,7 @@ glr_bwd_kernel(const GlrArgs a, const Exchange x, float* part) {
             sG[i & 1][run][lane * V + v] = G[v];
         }
         if (PACKED && lane == 0) s_any[i & 1][run] = (starts ? 1 : 0) | (ends ? 2 : 0);
-        bar_arrive(kMaps + (i & 1));
+        S::arrive(kMaps + (i & 1));
     };
 
     // stage two: with h_{t-1}, and D the gradient of h_t,
@@ -392,32 +406,33 @@ glr_bwd_kernel(const GlrArgs a, const Exchange x, float* part) {
         if (a.dA)
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                s_sum[i & 1][0][run][lane * V + v] = pA[v];
-                s_sum[i & 1][1][run][lane * V + v] = pdt[v];
+                s_sum[i % 3][0][run][lane * V + v] = pA[v];
+                s_sum[i % 3][1][run][lane * V + v] = pdt[v];
             }
     };
 
-    bar_arrive(kMaps);
+    S::arrive(kMaps);
     __syncthreads();
     if (s_tile[0].chain < 0) return;
     fetch(0);
     fetch(1);
-    Held q0, q1;
-    const auto step = [&](int i, Held& q, const Held& before) {
+    Held q, before;                              // the current tile's, and the one's before it
+    for (int i = 0;; ++i) {
         const bool more = s_tile[i % kPlaces].chain >= 0;
         if (more) {
             mix::copies_wait<1>();
             maps(i, q);
         }
-        if (i > 0) bar_sync(kCarry + ((i - 1) & 1));
-        if (i > 0) gradients(i - 1, before);
-        if (more) fetch(i + 2);                  // (into the buffer of tile i - 1)
-        else if (a.dA) bar_arrive(kMaps + (i & 1));
-        return more;
-    };
-    for (int i = 0;; i += 2) {
-        if (!step(i, q0, q1)) break;
-        if (!step(i + 1, q1, q0)) break;
+        if (i > 0) {
+            S::sync(kCarry + ((i - 1) & 1));
+            gradients(i - 1, before);
+        }
+        if (!more) {
+            if (a.dA) S::arrive(kMaps + (i & 1));
+            break;
+        }
+        fetch(i + 2);                            // (into the buffer of tile i - 1)
+        before = q;
     }
 }
 
@@ -445,35 +460,34 @@ __global__ void __launch_bounds__(256) glr_param_kernel(const float* part, int r
     }
 }
 
-template <typename Tx, typename Tg, int LANES, int V, bool PACKED>
+template <typename Tx, typename Tg, typename S, bool PACKED>
 cudaError_t bwd(const GlrArgs& a, const BwdSpace& sp, cudaStream_t s) {
-    using S = Shape<LANES, V>;
     const Layout l = layout(a.B, a.T, a.D, S::W);
     const Exchange x = exchange(l, sp.scan);
     if (l.bytes) {
         const cudaError_t e = cudaMemsetAsync(sp.scan, 0xff, l.bytes, s);
         if (e != cudaSuccess) return e;
     }
-    const auto kernel = glr_bwd_kernel<Tx, Tg, LANES, V, PACKED>;
-    const int smem = kBuffers * S::L * kThreads * V * (int)(sizeof(Tg) + (a.gi ? 3 : 2) * sizeof(Tx));
+    const auto kernel = glr_bwd_kernel<Tx, Tg, S, PACKED>;
+    const int smem = kBuffers * S::L * S::kThreads * S::V * (int)(sizeof(Tg) + (a.gi ? 3 : 2) * sizeof(Tx));
     static Residency res[2];                     // without and with the input gate
-    const int blocks = res[a.gi != nullptr].get(reinterpret_cast<const void*>(kernel), smem);
+    const int blocks = res[a.gi != nullptr].get(reinterpret_cast<const void*>(kernel), S::kBlock, smem);
     if (blocks == 0) return cudaGetLastError();
-    kernel<<<x.total < blocks ? x.total : blocks, kBlock, smem, s>>>(a, x, sp.part);
+    kernel<<<x.total < blocks ? x.total : blocks, S::kBlock, smem, s>>>(a, x, sp.part);
     if (a.dA)
         glr_param_kernel<<<dim3((a.D + 31) / 32, 2), 256, 0, s>>>(sp.part, a.B * l.tiles, a.D, a.dA, a.ddt);
     return cudaGetLastError();
 }
 
-template <typename Tx, typename Tg, int LANES, int V>
+template <typename Tx, typename Tg, typename S>
 cudaError_t bwd_packed(const GlrArgs& a, const BwdSpace& sp, cudaStream_t s) {
-    return a.cu ? bwd<Tx, Tg, LANES, V, true>(a, sp, s) : bwd<Tx, Tg, LANES, V, false>(a, sp, s);
+    return a.cu ? bwd<Tx, Tg, S, true>(a, sp, s) : bwd<Tx, Tg, S, false>(a, sp, s);
 }
 
 template <typename Tx, typename Tg>
 cudaError_t bwd_wide(const GlrArgs& a, const BwdSpace& sp, cudaStream_t s) {
-    if (glr_vector(a, 2)) return bwd_packed<Tx, Tg, 16, 2>(a, sp, s);
-    return bwd_packed<Tx, Tg, 32, 1>(a, sp, s);
+    if (glr_vector(a, 2)) return bwd_packed<Tx, Tg, Shape<16, 2, 4>>(a, sp, s);
+    return bwd_packed<Tx, Tg, Shape<32, 1, 8>>(a, sp, s);
 }
 
 // The backward's workspace: the scan's exchange, the partial sums of the parameters, and the checkpoints that the
