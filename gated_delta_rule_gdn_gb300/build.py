@@ -2,26 +2,33 @@
 
 Each translation unit under csrc/ compiles to an object in parallel; the
 objects link into gated_delta_rule_gdn_gb300/libgdn_gb300.so.  There is no
-cmake and no torch extension machinery: the library is plain C ABI.
+cmake and no torch extension machinery: the library is plain C ABI.  The
+Python extension module csrc/torch_binding.cpp (tensor checks and allocation
+for some entry points) compiles beside them with the host compiler against
+torch's headers, into gated_delta_rule_gdn_gb300/_native.so.
 
 Environment knobs:
   GDN_NVCC          nvcc to use (default: nvcc on PATH, else /usr/local/cuda/bin/nvcc)
+  GDN_CXX           host compiler of the extension module (default: g++ on PATH)
   GDN_PTXAS_VERBOSE=1  pass -Xptxas -v (registers, spills, shared memory per kernel)
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(os.path.dirname(PKG), "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgdn_gb300.so")
+NATIVE = os.path.join(PKG, "_native.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -36,15 +43,26 @@ def _sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
+def _native_command(out: str) -> list:
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    include = os.path.join(torch, "include")
+    return [os.environ.get("GDN_CXX") or shutil.which("g++") or "c++", "-O1", "-std=c++20", "-fPIC", "-shared",
+            "-I", include, "-I", os.path.join(include, "torch", "csrc", "api", "include"),
+            "-I", os.path.join(cuda, "include"), "-I", sysconfig.get_paths()["include"],
+            os.path.join(CSRC, "torch_binding.cpp"), "-o", out, "-L", os.path.join(torch, "lib"),
+            "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python"]
+
+
 def _deps():
-    return _sources() + sorted(glob.glob(os.path.join(CSRC, "*.h"))) + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) \
+    return _sources() + sorted(glob.glob(os.path.join(CSRC, "*.cpp"))) + sorted(glob.glob(os.path.join(CSRC, "*.h"))) + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) \
         + sorted(glob.glob(os.path.join(INCLUDE, "*.h"))) + [os.path.abspath(__file__)]
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(NATIVE):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(NATIVE))
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
@@ -58,27 +76,37 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if os.environ.get("GDN_PTXAS_VERBOSE") == "1":
         flags += ["-Xptxas", "-v"]
 
-    def compile_one(src: str) -> str:
-        obj = os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")
-        cmd = [nvcc] + flags + ["-c", src, "-o", obj]
+    def run(cmd, what: str):
         if verbose:
             print(" ".join(cmd), file=sys.stderr)
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0 or (verbose and r.stderr):
             sys.stderr.write(r.stderr)
         if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed on {os.path.basename(src)}")
+            raise RuntimeError(f"compilation failed on {what}")
+
+    def compile_one(src: str) -> str:
+        obj = os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")
+        run([nvcc] + flags + ["-c", src, "-o", obj], os.path.basename(src))
         return obj
 
+    def compile_native() -> str:
+        out = NATIVE + f".tmp{os.getpid()}"
+        run(_native_command(out), "torch_binding.cpp")
+        return out
+
     srcs = _sources()
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 4))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 4))) as ex:
+        native = ex.submit(compile_native)
         objs = list(ex.map(compile_one, srcs))
+        native = native.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc] + ARCH + ["-shared", "-o", tmp] + objs
     if verbose:
         print(" ".join(cmd), file=sys.stderr)
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIB)
+    os.replace(native, NATIVE)
     return LIB
 
 

@@ -325,7 +325,7 @@ cudaError_t fwd_packed(const GlrArgs& a, cudaStream_t s) {
 
 template <typename Tx, typename Tg>
 cudaError_t fwd_wide(const GlrArgs& a, cudaStream_t s) {
-    if (glr_vector(a, 4)) return fwd_packed<Tx, Tg, Shape<16, 4, 8>>(a, s);
+    if (glr_vector(a, 4)) return fwd_packed<Tx, Tg, Shape<16, 4, 4>>(a, s);
     if (glr_vector(a, 2)) return fwd_packed<Tx, Tg, Shape<32, 2, 8>>(a, s);
     return fwd_packed<Tx, Tg, Shape<32, 1, 8>>(a, s);
 }

@@ -163,10 +163,10 @@ def test_binding_refuses_wrong_tensors(lib):
         gdn.glr_scan_fwd(None, x)
 
 
-def test_row_spacing():
+def test_row_spacing(lib):
     """The one row stride that a strided view has, or the refusal of a view that has none."""
     base = torch.zeros(4, 6, 20)
-    rows = lambda t: _mixer._rows(t, "t", t.shape, t.dtype, base)[1]     # noqa: E731
+    rows = lambda t: _mixer.native().spacing(t)[0]     # noqa: E731
     assert rows(base) == 20
     assert rows(base[..., 3:11]) == 20
     assert rows(base[:, :1, :5]) == 120           # one token of every row
@@ -176,7 +176,25 @@ def test_row_spacing():
                 base[:, :1].expand(4, 6, 20)):
         with pytest.raises(ValueError):
             rows(bad)
+    heads = lambda t: _mixer.native().spacing(t, heads=True)     # noqa: E731
     q = torch.zeros(4, 6, 10 * 16)[..., 32:96].unflatten(-1, (4, 16))
-    assert _mixer._heads(q, "q", q.shape[:-2], 16, q.dtype, base)[1:] == (4, 160, 16)
+    assert heads(q) == (160, 16)
+    assert heads(q[:, :, 1:2]) == (160, 16)       # a single head
     with pytest.raises(ValueError):
-        _mixer._heads(q.transpose(1, 2), "q", (4, 4), 16, q.dtype, base)
+        heads(q.transpose(1, 2))
+    with pytest.raises(ValueError):
+        heads(q[..., :1, :].expand(4, 6, 4, 16))
+
+
+def test_binding_arguments(lib):
+    x = torch.zeros(1, 4, 8)
+    for bad in (lambda: gdn.glr_scan_fwd(), lambda: gdn.glr_scan_fwd(x), lambda: gdn.glr_scan_fwd(x, x, what=1),
+                lambda: gdn.glr_scan_fwd(x, x, x=x), lambda: gdn.glr_step(*([x] * 30)), lambda: gdn.glr_scan_fwd(3, x),
+                lambda: _mixer.native().spacing(None)):
+        with pytest.raises(TypeError):
+            bad()
+    with pytest.raises(AttributeError):
+        gdn.no_such_entry
+    import inspect
+    for name in _mixer.ENTRIES:
+        assert name in gdn.__all__ and "stream" in inspect.signature(getattr(gdn, name)).parameters
