@@ -5,10 +5,10 @@
 // Backward: dy = the output's gradient turned back, dw = sum dy x r, e = w dy, dx = r (e - c r^2 x sum(x e)).
 // Bound by HBM: every head is read once and written once (backward: read with its gradient, written once).
 //
-// Vector kernels: G neighbouring lanes hold a head, 8 channels each, and a group of lanes takes `kHeads` heads of one
+// Vector kernels: G neighbouring lanes hold a head, E = 8 or 4 channels each, and a group of lanes takes `kHeads` heads of one
 // token, so that the token's angles are read once for them and their loads are under way together.  The rotation's
-// partner is in the same lane (interleaved), or in the lane rot/16 away.  Heads whose size, rotation or alignment does
-// not go in steps of 8 channels take the scalar kernels, a warp per head.
+// partner is in the same lane (interleaved), or in the lane rot / 2E away.  Heads whose size, rotation or alignment
+// does not go in steps of 4 channels take the scalar kernels, a warp per head.
 
 #include <type_traits>
 
@@ -22,7 +22,7 @@ using mix::bf16;
 using mix::ld;
 using mix::st;
 
-constexpr int kMaxD = 256, kThreads = 256, kHeads = 4, E = 8;
+constexpr int kMaxD = 256, kThreads = 256, kHeads = 4;
 
 __device__ __forceinline__ int position(const QkNormArgs& a, int64_t tok) {
     const int p = a.pos ? a.pos[tok] : (int)((unsigned)tok % (unsigned)a.T);    // (tokens times heads fit 31 bits)
@@ -36,30 +36,32 @@ __device__ __forceinline__ float group_sum(float v) {
     return v;
 }
 
-// 8 channels in 16-byte accesses
-template <typename T> struct Eight;
-template <> struct Eight<bf16> {
-    mix::Vec<bf16, 8> v;
-    __device__ __forceinline__ void load(const bf16* p) { v.load(p); }
-    __device__ __forceinline__ void zero() { v.zero(); }
-    __device__ __forceinline__ float get(int i) const { return v.get(i); }
-    __device__ __forceinline__ void set(int i, float x) { v.set(i, x); }
-    __device__ __forceinline__ void store(bf16* p) const { v.store(p); }
-};
-template <> struct Eight<float> {
-    mix::Vec<float, 4> v[2];
-    __device__ __forceinline__ void load(const float* p) { v[0].load(p); v[1].load(p + 4); }
-    __device__ __forceinline__ void zero() { v[0].zero(); v[1].zero(); }
-    __device__ __forceinline__ float get(int i) const { return v[i / 4].get(i % 4); }
-    __device__ __forceinline__ void set(int i, float x) { v[i / 4].set(i % 4, x); }
-    __device__ __forceinline__ void store(float* p) const { v[0].store(p); v[1].store(p + 4); }
+// E channels in accesses of at most 16 bytes
+template <typename T, int E>
+struct Chunk {
+    static constexpr int N = sizeof(T) * E > 16 ? 16 / sizeof(T) : E;
+    mix::Vec<T, N> v[E / N];
+    __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+        for (int i = 0; i < E / N; ++i) v[i].load(p + i * N);
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < E / N; ++i) v[i].zero();
+    }
+    __device__ __forceinline__ float get(int i) const { return v[i / N].get(i % N); }
+    __device__ __forceinline__ void set(int i, float x) { v[i / N].set(i % N, x); }
+    __device__ __forceinline__ void store(T* p) const {
+#pragma unroll
+        for (int i = 0; i < E / N; ++i) v[i].store(p + i * N);
+    }
 };
 
 enum Rotation { kNone, kHalves, kInterleaved };
 
 // The angles of a lane's channels at position p (cos = 1, sin = 0 past the rotated ones), with the sign that the forward
 // rotation gives the partner's term in `sin` for halves.
-template <int ROT>
+template <int E, int ROT>
 struct Angles {
     float c[ROT == kInterleaved ? E / 2 : E], s[ROT == kInterleaved ? E / 2 : E];
     int partner;
@@ -72,12 +74,13 @@ struct Angles {
         partner = in ? (low ? lane + half / E : lane - half / E) : lane;
         const float* cp = a.cos + (int64_t)p * half + at;
         const float* sp = a.sin + (int64_t)p * half + at;
+        Chunk<float, N> x, y;
+        if (in) x.load(cp);
+        if (in) y.load(sp);
 #pragma unroll
-        for (int i = 0; i < N; i += 4) {
-            const float4 x = in ? *reinterpret_cast<const float4*>(cp + i) : make_float4(1.f, 1.f, 1.f, 1.f);
-            const float4 y = in ? *reinterpret_cast<const float4*>(sp + i) : make_float4(0.f, 0.f, 0.f, 0.f);
-            c[i] = x.x; c[i + 1] = x.y; c[i + 2] = x.z; c[i + 3] = x.w;
-            s[i] = y.x; s[i + 1] = y.y; s[i + 2] = y.z; s[i + 3] = y.w;
+        for (int i = 0; i < N; ++i) {
+            c[i] = in ? x.get(i) : 1.f;
+            s[i] = in ? y.get(i) : 0.f;
         }
         if (ROT == kHalves && low)
 #pragma unroll
@@ -106,7 +109,7 @@ struct Angles {
 
 // A group's share of the work: kHeads heads of q, or of k, of one token.  The token's shares are those of q, then of k.
 struct Shares { unsigned of_q, all; };
-template <typename T, int G>
+template <typename T, int E, int G>
 struct Share {
     unsigned tok;
     int which, count, j0;             // tensor, heads, the lane's first channel
@@ -130,15 +133,15 @@ struct Share {
     }
 };
 
-template <typename T, int G, int ROT>
+template <typename T, int E, int G, int ROT>
 __global__ void __launch_bounds__(kThreads) qk_fwd_kernel(const QkNormArgs a, const Shares sh, const unsigned items) {
     const unsigned item = blockIdx.x * (kThreads / G) + threadIdx.x / G;
-    const Share<T, G> w(a, sh, min(item, items - 1));            // (the last block repeats the last share)
-    Eight<T> x[kHeads];
+    const Share<T, E, G> w(a, sh, min(item, items - 1));            // (the last block repeats the last share)
+    Chunk<T, E> x[kHeads];
 #pragma unroll
     for (int i = 0; i < kHeads; ++i)
         if (w.in && i < w.count) x[i].load(w.x + i * w.step); else x[i].zero();
-    Angles<ROT> ang;
+    Angles<E, ROT> ang;
     if (ROT != kNone) ang.load(a, position(a, w.tok), (int)threadIdx.x % G);
     const float* wt = w.which ? a.w[1] : a.w[0];
     float weight[E];
@@ -165,7 +168,7 @@ __global__ void __launch_bounds__(kThreads) qk_fwd_kernel(const QkNormArgs a, co
 }
 
 // persistent blocks: the weight gradients of a block's heads stay in registers and leave as one row of partial sums
-template <typename T, int G, int ROT>
+template <typename T, int E, int G, int ROT>
 __global__ void __launch_bounds__(kThreads, 2) qk_bwd_kernel(const QkNormArgs a, const Shares sh, const unsigned items,
                                                              float* part) {
     constexpr int kGroups = kThreads / G;
@@ -173,16 +176,16 @@ __global__ void __launch_bounds__(kThreads, 2) qk_bwd_kernel(const QkNormArgs a,
     float acc[2][E] = {};
     for (unsigned base = blockIdx.x * kGroups; base < items; base += gridDim.x * kGroups) {
         const unsigned item = base + threadIdx.x / G;
-        const Share<T, G> w(a, sh, min(item, items - 1));
+        const Share<T, E, G> w(a, sh, min(item, items - 1));
         const int count = item < items && w.in ? w.count : 0;
-        Eight<T> x[kHeads], dz[kHeads];
+        Chunk<T, E> x[kHeads], dz[kHeads];
         const T* dp = static_cast<const T*>(w.which ? a.dout[1] : a.dout[0]) + w.at;
 #pragma unroll
         for (int i = 0; i < kHeads; ++i) {
             if (i < count) x[i].load(w.x + i * w.step); else x[i].zero();
             if (i < count) dz[i].load(dp + (size_t)i * a.d); else dz[i].zero();
         }
-        Angles<ROT> ang;
+        Angles<E, ROT> ang;
         if (ROT != kNone) ang.load(a, position(a, w.tok), (int)threadIdx.x % G);
         const float* wt = w.which ? a.w[1] : a.w[0];
         T* out = static_cast<T*>(w.which ? a.out[1] : a.out[0]) + w.at;
@@ -380,47 +383,55 @@ __global__ void __launch_bounds__(256) qk_dw_kernel(const float* part, int rows,
     }
 }
 
-// Whether the vector kernels apply: everything in steps of 8 channels, on 16-byte addresses.
-bool vector_ok(const QkNormArgs& a, bool backward) {
-    const auto al = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
-    if (a.d % E) return false;
-    if (a.rot > 0 && (a.interleaved ? a.rot % E != 0 : a.rot % (2 * E) != 0)) return false;
-    if (a.rot > 0 && (!al(a.cos) || !al(a.sin) || (a.rot / 2) % 4)) return false;
-    for (int i = 0; i < 2; ++i) {
-        if (a.tok_stride[i] % E || a.head_stride[i] % E || !al(a.in[i]) || !al(a.out[i])) return false;
-        if (backward && !al(a.dout[i])) return false;
+// The channels a lane takes in the vector kernels: 8 or 4, whichever everything goes in steps of, or 0 if neither.
+int channels_a_lane(const QkNormArgs& a, bool backward) {
+    for (int E = 8; E >= 4; E /= 2) {
+        const size_t size = (a.bf16 ? 2 : 4) * E, bytes = size < 16 ? size : 16;
+        const size_t table = a.interleaved ? 2 * E : (E < 4 ? E : 4) * 4;
+        const auto al = [](const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; };
+        bool ok = a.d % E == 0 && a.d <= 32 * E;
+        if (a.rot > 0)
+            ok = ok && (a.interleaved ? a.rot % E == 0 : a.rot % (2 * E) == 0) && al(a.cos, table < 16 ? table : 16) &&
+                 al(a.sin, table < 16 ? table : 16);
+        for (int i = 0; i < 2; ++i)
+            ok = ok && a.tok_stride[i] % E == 0 && a.head_stride[i] % E == 0 && al(a.in[i], bytes) && al(a.out[i], bytes) &&
+                 (!backward || al(a.dout[i], bytes));
+        if (ok) return E;
     }
-    return true;
+    return 0;
 }
 
-constexpr int kBwdBlocks = 152 * 4;
-int64_t groups_per_block(int d) { return d <= 64 ? 32 : d <= 128 ? 16 : 8; }
+constexpr int kBwdBlocks = 152 * 2;
 Shares shares_of(const QkNormArgs& a) {
     const unsigned q = (a.H[0] + kHeads - 1) / kHeads, k = (a.H[1] + kHeads - 1) / kHeads;
     return {q, q + k};
 }
 
-// f(group size, rotation) as compile-time constants
+// f(channels a lane, group size, rotation) as compile-time constants
 template <typename F>
-void by_shape(const QkNormArgs& a, F f) {
-    const auto rot = [&](auto g) {
-        if (a.rot == 0) f(g, std::integral_constant<int, kNone>{});
-        else if (a.interleaved) f(g, std::integral_constant<int, kInterleaved>{});
-        else f(g, std::integral_constant<int, kHalves>{});
+void by_shape(const QkNormArgs& a, int E, F f) {
+    const auto rot = [&](auto e, auto g) {
+        if (a.rot == 0) f(e, g, std::integral_constant<int, kNone>{});
+        else if (a.interleaved) f(e, g, std::integral_constant<int, kInterleaved>{});
+        else f(e, g, std::integral_constant<int, kHalves>{});
     };
-    if (a.d <= 64) rot(std::integral_constant<int, 8>{});
-    else if (a.d <= 128) rot(std::integral_constant<int, 16>{});
-    else rot(std::integral_constant<int, 32>{});
+    using std::integral_constant;
+    if (E == 4) {
+        if (a.d <= 64) rot(integral_constant<int, 4>{}, integral_constant<int, 16>{});
+        else rot(integral_constant<int, 4>{}, integral_constant<int, 32>{});
+    } else if (a.d <= 64) rot(integral_constant<int, 8>{}, integral_constant<int, 8>{});
+    else if (a.d <= 128) rot(integral_constant<int, 8>{}, integral_constant<int, 16>{});
+    else rot(integral_constant<int, 8>{}, integral_constant<int, 32>{});
 }
 
 template <typename T>
 cudaError_t fwd(const QkNormArgs& a, cudaStream_t s) {
-    if (vector_ok(a, false)) {
+    if (const int E = channels_a_lane(a, false)) {
         const Shares sh = shares_of(a);
         const unsigned items = (unsigned)(a.n * sh.all);         // (at most tokens times heads, which fits)
-        by_shape(a, [&](auto g, auto rot) {
+        by_shape(a, E, [&](auto e, auto g, auto rot) {
             const unsigned per = kThreads / g.value;
-            qk_fwd_kernel<T, g.value, rot.value><<<(items + per - 1) / per, kThreads, 0, s>>>(a, sh, items);
+            qk_fwd_kernel<T, e.value, g.value, rot.value><<<(items + per - 1) / per, kThreads, 0, s>>>(a, sh, items);
         });
     } else {
         const int64_t rows = a.n * (a.H[0] + a.H[1]);
@@ -434,13 +445,14 @@ cudaError_t bwd(const QkNormArgs& a, cudaStream_t s) {
     const bool weights = a.dw[0] || a.dw[1];
     float* part = weights ? static_cast<float*>(a.ws) : nullptr;
     int blocks = 0;                            // none without tokens: the weight gradients are then zero
-    if (a.n > 0 && vector_ok(a, true)) {
+    const int E = a.n > 0 ? channels_a_lane(a, true) : 0;
+    if (E > 0) {
         const Shares sh = shares_of(a);
         const unsigned items = (unsigned)(a.n * sh.all);
-        const int64_t per = groups_per_block(a.d), want = (items + per - 1) / per;
-        blocks = (int)(want < kBwdBlocks ? want : kBwdBlocks);
-        by_shape(a, [&](auto g, auto rot) {
-            qk_bwd_kernel<T, g.value, rot.value><<<blocks, kThreads, 0, s>>>(a, sh, items, part);
+        by_shape(a, E, [&](auto e, auto g, auto rot) {
+            const unsigned per = kThreads / g.value, want = (items + per - 1) / per;
+            blocks = (int)(want < kBwdBlocks ? want : kBwdBlocks);
+            qk_bwd_kernel<T, e.value, g.value, rot.value><<<blocks, kThreads, 0, s>>>(a, sh, items, part);
         });
     } else if (a.n > 0) {
         const int64_t want = (a.n * (a.H[0] + a.H[1]) + kWarps - 1) / kWarps;

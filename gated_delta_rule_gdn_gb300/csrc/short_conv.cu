@@ -65,6 +65,21 @@ template <int W, int V>
 struct Taps {
     float w[W][V], b[V];
     __device__ __forceinline__ void load(const ConvArgs& a, int c, bool live) {
+        if (V == 4 && live && reinterpret_cast<uintptr_t>(a.w) % 16 == 0) {       // the channels' taps lie together
+            float t[4 * W];
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                const float4 q = reinterpret_cast<const float4*>(a.w + (size_t)c * W)[i];
+                t[4 * i] = q.x; t[4 * i + 1] = q.y; t[4 * i + 2] = q.z; t[4 * i + 3] = q.w;
+            }
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+#pragma unroll
+                for (int j = 0; j < W; ++j) w[j][v] = t[(v * W + j) % (4 * W)];
+                b[v] = a.b ? a.b[c + v] : 0.f;
+            }
+            return;
+        }
 #pragma unroll
         for (int v = 0; v < V; ++v) {
 #pragma unroll
@@ -392,31 +407,41 @@ __global__ void __launch_bounds__(256) conv_param_kernel(const float* part, int6
     }
 }
 
+// a thread takes V channels of up to `per` sequences, whose loads are under way together
+constexpr int kStepSeqs = 4;
 template <typename T, int W, int V>
-__global__ void __launch_bounds__(128) conv_step_kernel(const ConvArgs a, const T* state, T* out) {
+__global__ void __launch_bounds__(128) conv_step_kernel(const ConvArgs a, const T* state, T* out, const int per) {
     const int64_t id = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     const int cols = a.D / V;
-    const int64_t n = id / cols;
-    const int c = (int)(id - n * cols) * V;
-    if (n >= a.B) return;
-    const T* h = state + n * (W - 1) * a.D + c;
-    T* o = out + n * (W - 1) * a.D + c;
-    Vec<T, V> win[W], y;
+    const int64_t n0 = id / cols * per;
+    const int c = (int)(id % cols) * V;
+    if (n0 >= a.B) return;
+    const int count = (int)min((int64_t)per, a.B - n0);
+    Vec<T, V> win[kStepSeqs][W];
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) win[j].load(h + (int64_t)j * a.D);
-    win[W - 1].load(static_cast<const T*>(a.x) + n * a.ldx + c);
+    for (int i = 0; i < kStepSeqs; ++i) {
+        if (i >= count) break;
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) win[i][j].load(state + ((n0 + i) * (W - 1) + j) * a.D + c);
+        win[i][W - 1].load(static_cast<const T*>(a.x) + (n0 + i) * a.ldx + c);
+    }
     Taps<W, V> k;
     k.load(a, c, true);
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        float p = k.b[v];
+    for (int i = 0; i < kStepSeqs; ++i) {
+        if (i >= count) break;
+        Vec<T, V> y;
 #pragma unroll
-        for (int j = 0; j < W; ++j) p = fmaf(k.w[j][v], win[j].get(v), p);
-        y.set(v, a.silu ? silu(p) : p);
+        for (int v = 0; v < V; ++v) {
+            float p = k.b[v];
+#pragma unroll
+            for (int j = 0; j < W; ++j) p = fmaf(k.w[j][v], win[i][j].get(v), p);
+            y.set(v, a.silu ? silu(p) : p);
+        }
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) win[i][j + 1].store(out + ((n0 + i) * (W - 1) + j) * a.D + c);
+        y.store(static_cast<T*>(a.y) + (n0 + i) * a.D + c);
     }
-#pragma unroll
-    for (int j = 0; j < W - 1; ++j) win[j + 1].store(o + (int64_t)j * a.D);
-    y.store(static_cast<T*>(a.y) + n * a.D + c);
 }
 
 // Whether rows can be accessed V channels at a time.
@@ -497,9 +522,12 @@ cudaError_t launch_conv_step(const ConvArgs& a, const void* state, void* state_o
     by_width(a.W, [&](auto w) {
         by_type(a, vector_ok(a, 4, state, state_out), [&](auto* t, auto v) {
             using T = std::remove_pointer_t<decltype(t)>;
-            const int64_t threads = (int64_t)a.B * (a.D / v.value);
+            // several sequences a thread once there are threads for every SM without (152 x 2048)
+            const int64_t cols = a.D / v.value;
+            const int per = (int64_t)a.B * cols > 152 * 2048 ? kStepSeqs : 1;
+            const int64_t threads = (a.B + per - 1) / per * cols;
             conv_step_kernel<T, w.value, v.value><<<(unsigned)((threads + 127) / 128), 128, 0, s>>>(
-                a, static_cast<const T*>(state), static_cast<T*>(state_out));
+                a, static_cast<const T*>(state), static_cast<T*>(state_out), per);
         });
     });
     return cudaGetLastError();
