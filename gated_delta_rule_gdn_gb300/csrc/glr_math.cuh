@@ -29,15 +29,27 @@ __device__ __forceinline__ float min_nan(float x, float y) {
     return r;
 }
 
+// Two fp32 numbers to an instruction (the pair in one 64-bit register).
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 pack(float x, float y) { f2 r; asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y)); return r; }
+__device__ __forceinline__ f2 both_of(float x) { return pack(x, x); }
+__device__ __forceinline__ void unpack(f2 r, float& x, float& y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(r)); }
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) { f2 r; asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c)); return r; }
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) { f2 r; asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b)); return r; }
+__device__ __forceinline__ f2 add2(f2 a, f2 b) { f2 r; asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b)); return r; }
+
 // a = exp(x) and e = exp(x) - 1 for x <= 88.  x = k ln 2 + r, |r| <= ln 2 / 2, with ln 2 split in two parts (Cody and
 // Waite); p = exp(r) - 1 = r + r^2 Q(r), off by less than 2^-28; a = 2^k + 2^k p, e = (2^k - 1) + 2^k p.
 // Rounding a once matters: a memory of n tokens multiplies a one-sided error of a by n (a decay taken from expf was off
 // by 4e-5 after 10^4 tokens).  Below -88 (where 2^k becomes 0) the decay is exactly 0.
 // x is brought to -88 in place: log a times a gradient that holds a factor a is then 0 there, not NaN.
 struct Decay { float a, e; };
+__device__ __forceinline__ float power_of_two(float t) {           // 2^k, k in the low bits of t = 1.5 * 2^23 + k
+    return __int_as_float((__float_as_int(t) << 23) + 0x3f800000);
+}
 __device__ __forceinline__ Decay decay(float& x) {
     x = max_nan(x, -88.f);
-    const float t = fmaf(x, kLog2e, 12582912.f);                    // k in the low bits of 1.5 * 2^23 + k
+    const float t = fmaf(x, kLog2e, 12582912.f);
     const float k = t - 12582912.f;
     const float r = fmaf(k, 2.1219444e-4f, fmaf(k, -0.693359375f, x));
     float q = fmaf(r, 1.3950337e-3f, 8.3688218e-3f);
@@ -45,8 +57,24 @@ __device__ __forceinline__ Decay decay(float& x) {
     q = fmaf(q, r, 1.6666520e-1f);
     q = fmaf(q, r, 0.5f);
     const float p = fmaf(r * r, q, r);
-    const float sc = __int_as_float((__float_as_int(t) << 23) + 0x3f800000);
+    const float sc = power_of_two(t);
     return {fmaf(sc, p, sc), fmaf(sc, p, sc - 1.f)};
+}
+__device__ __forceinline__ void decay(float& x0, float& x1, Decay& d0, Decay& d1) {
+    x0 = max_nan(x0, -88.f);
+    x1 = max_nan(x1, -88.f);
+    const f2 x = pack(x0, x1), t = fma2(x, both_of(kLog2e), both_of(12582912.f)), k = add2(t, both_of(-12582912.f));
+    const f2 r = fma2(k, both_of(2.1219444e-4f), fma2(k, both_of(-0.693359375f), x));
+    f2 q = fma2(r, both_of(1.3950337e-3f), both_of(8.3688218e-3f));
+    q = fma2(q, r, both_of(4.1666210e-2f));
+    q = fma2(q, r, both_of(1.6666520e-1f));
+    q = fma2(q, r, both_of(0.5f));
+    const f2 p = fma2(mul2(r, r), q, r);
+    float t0, t1;
+    unpack(t, t0, t1);
+    const f2 sc = pack(power_of_two(t0), power_of_two(t1));
+    unpack(fma2(sc, p, sc), d0.a, d1.a);
+    unpack(fma2(sc, p, add2(sc, both_of(-1.f))), d0.e, d1.e);
 }
 
 // exp(-|z|) carries both softplus and sigma.  log1p(q) = q P(q) on [0, 1], off by less than 2^-25 of itself.
@@ -61,6 +89,19 @@ __device__ __forceinline__ float softplus(float z, float q) {
     s = fmaf(s, q, -4.9999553e-1f);
     s = fmaf(s, q, 1.f);
     return fmaf(s, q, fmaxf(z, 0.f));
+}
+// of two logits, times nA
+__device__ __forceinline__ void softplus(float z0, float z1, float nA0, float nA1, float& r0, float& r1) {
+    const f2 q = pack(tail(z0), tail(z1));
+    f2 s = fma2(q, both_of(5.3840620e-3f), both_of(-3.0110965e-2f));
+    s = fma2(s, q, both_of(7.9210736e-2f));
+    s = fma2(s, q, both_of(-1.3746622e-1f));
+    s = fma2(s, q, both_of(1.9145116e-1f));
+    s = fma2(s, q, both_of(-2.4852946e-1f));
+    s = fma2(s, q, both_of(3.3320343e-1f));
+    s = fma2(s, q, both_of(-4.9999553e-1f));
+    s = fma2(s, q, both_of(1.f));
+    unpack(mul2(fma2(s, q, pack(fmaxf(z0, 0.f), fmaxf(z1, 0.f))), pack(nA0, nA1)), r0, r1);
 }
 __device__ __forceinline__ float sigmoid(float z, float q) { return (z < 0.f ? q : 1.f) * rcp(1.f + q); }
 __device__ __forceinline__ float sigmoid(float z) { return rcp(1.f + ex2(z * -kLog2e)); }

@@ -24,11 +24,17 @@ glr_fwd_kernel(const GlrArgs a, const Exchange x, const int publish) {
     extern __shared__ __align__(16) unsigned char s_raw[];
     __shared__ float sA[2][R][W], sH[2][R][W];
     __shared__ int s_start[PACKED ? kPlaces : 1][kTile], s_end[PACKED ? kPlaces : 1][kTile];
+    __shared__ bool s_marked[kPlaces][2];        // whether either half of a tile's tokens has a mark
     __shared__ Tile s_tile[kPlaces];
     const int tid = threadIdx.x;
 
     if (tid >= kThreads) {                       // the carry threads
         const int ch = tid - kThreads;
+        const auto mark = [&](int slot) {
+            if (!PACKED || s_tile[slot].chain < 0) return;
+            const bool any = sequence_marks(a, s_tile[slot].p, ch, s_start[slot], s_end[slot]);
+            if (ch % 32 == 0) s_marked[slot][ch / 32] = any;
+        };
         Tickets tickets(x);
         unsigned ticket = 0;
         if (ch == 0) {
@@ -37,9 +43,7 @@ glr_fwd_kernel(const GlrArgs a, const Exchange x, const int publish) {
         }
         __syncwarp();
         S::sync(kMaps);                         // (places are read below by all carry threads: meet once)
-        if (PACKED)
-            for (int i = 0; i < 3; ++i)
-                if (s_tile[i].chain >= 0) sequence_marks(a, s_tile[i].p, ch, s_start[i], s_end[i]);
+        for (int i = 0; i < 3; ++i) mark(i);
         __syncthreads();
         for (int i = 0; s_tile[i % kPlaces].chain >= 0; ++i) {
             const Tile t = s_tile[i % kPlaces];
@@ -49,29 +53,48 @@ glr_fwd_kernel(const GlrArgs a, const Exchange x, const int publish) {
                 ticket = tickets.take();
             }
             float first = 0.f;
-            if (!PACKED && ch < W && t.p < kGroup && a.h0 && t.c0 + ch < a.D) first = a.h0[(size_t)t.b * a.D + t.c0 + ch];
+            if (!PACKED && ch < W && t.p < x.group && a.h0 && t.c0 + ch < a.D) first = a.h0[(size_t)t.b * a.D + t.c0 + ch];
             S::sync(kMaps + k);
             if (ch < W) {
+                // (a tile without marks forgets nothing inside)
+                const bool marked = PACKED && (s_marked[i % kPlaces][0] || s_marked[i % kPlaces][1]);
                 float A = 1.f, H = 0.f;
+                if (marked) {
 #pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    H = apply<PACKED>(sA[k][r][ch], sH[k][r][ch], H);
-                    A = both<PACKED>(A, sA[k][r][ch]);
+                    for (int r = 0; r < R; ++r) {
+                        H = apply<true>(sA[k][r][ch], sH[k][r][ch], H);
+                        A = both<true>(A, sA[k][r][ch]);
+                    }
+                } else {
+#pragma unroll
+                    for (int r = 0; r < R; ++r) {
+                        H = fmaf(sA[k][r][ch], H, sH[k][r][ch]);
+                        A *= sA[k][r][ch];
+                    }
                 }
                 if (publish || t.p > 0) hand_map(x, W, t.p, t.chain, ch, A, H);
                 float h = carry_in<PACKED>(x, W, t.p, t.chain, ch, first, &g_glr_status);
                 hand_state(x, W, t.p, t.chain, ch, apply<PACKED>(A, H, h));
                 if (a.ckpt && t.c0 + ch < a.D && t.p * kTile < a.T)
                     a.ckpt[((size_t)t.b * x.tiles + t.p) * a.D + t.c0 + ch] = h;
+                if (marked) {
 #pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    const float rH = sH[k][r][ch];
-                    sH[k][r][ch] = h;
-                    h = apply<PACKED>(sA[k][r][ch], rH, h);
+                    for (int r = 0; r < R; ++r) {
+                        const float rH = sH[k][r][ch];
+                        sH[k][r][ch] = h;
+                        h = apply<true>(sA[k][r][ch], rH, h);
+                    }
+                } else {
+#pragma unroll
+                    for (int r = 0; r < R; ++r) {
+                        const float rH = sH[k][r][ch];
+                        sH[k][r][ch] = h;
+                        h = fmaf(sA[k][r][ch], h, rH);
+                    }
                 }
             }
             S::arrive(kCarry + k);
-            if (PACKED && s_tile[ahead].chain >= 0) sequence_marks(a, s_tile[ahead].p, ch, s_start[ahead], s_end[ahead]);
+            mark(ahead);
         }
         return;
     }
@@ -119,10 +142,8 @@ glr_fwd_kernel(const GlrArgs a, const Exchange x, const int publish) {
     };
     const auto run_starts = [&](int i) {         // which tokens of the run start a sequence
         unsigned m = 0;
-        if (PACKED) {
 #pragma unroll
-            for (int j = 0; j < L; ++j) m |= (s_start[i % kPlaces][run * L + j] >= 0 ? 1u : 0u) << j;
-        }
+        for (int j = 0; j < L; ++j) m |= (s_start[i % kPlaces][run * L + j] >= 0 ? 1u : 0u) << j;
         return m;
     };
 
@@ -151,39 +172,19 @@ glr_fwd_kernel(const GlrArgs a, const Exchange x, const int publish) {
                 for (int v = 0; v < V; ++v) u[j][v] *= sigmoid(gi.get(v));
             }
         }
-        if (a.A_log) {
-            Channel ch[V];
-#pragma unroll
-            for (int v = 0; v < V; ++v) ch[v] = live ? channel(a.A_log, a.dt_bias, c + v) : Channel{0.f, 0.f};
-#pragma unroll
-            for (int j = 0; j < L; ++j)
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    const float z = al[j][v] + ch[v].dt;
-                    al[j][v] = ch[v].neg_eA * softplus(z, tail(z));
-                }
-        } else {
-#pragma unroll
-            for (int j = 0; j < L; ++j)
-#pragma unroll
-                for (int v = 0; v < V; ++v) al[j][v] = min_nan(al[j][v], 88.f);
-        }
-#pragma unroll
-        for (int j = 0; j < L; ++j)
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const Decay d = decay(al[j][v]);
-                if (a.normalize) u[j][v] *= root(input_power(d));
-                al[j][v] = d.a;
-            }
+        log_decays<L, V>(a, c, live, al);
+        decays<L, V>(al, [&](int j, int v, const Decay& d) {
+            if (a.normalize) u[j][v] *= root(input_power(d));
+            al[j][v] = d.a;
+        });
         if (count < L) {                         // past the row's end the state stays
 #pragma unroll
             for (int j = 0; j < L; ++j)
 #pragma unroll
                 for (int v = 0; v < V; ++v) al[j][v] = j < count ? al[j][v] : 1.f;
         }
-        const unsigned starts = run_starts(i);
         float A[V], H[V];
+        const unsigned starts = PACKED && (s_marked[i % kPlaces][0] || s_marked[i % kPlaces][1]) ? run_starts(i) : 0;
         if (PACKED && starts) {
 #pragma unroll
             for (int j = 0; j < L; ++j) {
@@ -220,28 +221,40 @@ glr_fwd_kernel(const GlrArgs a, const Exchange x, const int publish) {
         const Tile t = s_tile[i % kPlaces];
         const int c = t.c0 + lane * V, t0 = t.p * kTile + run * L;
         const bool live = c < a.D;
-        const unsigned starts = run_starts(i);
         float h[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) h[v] = sH[i & 1][run][lane * V + v];
         Tx* op = static_cast<Tx*>(a.o) + ((size_t)t.b * a.T + t0) * a.D + c;
         const int n = live && a.o ? a.T - t0 : 0;
+        if (PACKED && (s_marked[i % kPlaces][0] || s_marked[i % kPlaces][1])) {
+            const unsigned starts = run_starts(i);
 #pragma unroll
-        for (int j = 0; j < L; ++j) {
-            Vec<Tx, V> o;
-            const bool here = PACKED && ((starts >> j) & 1);
+            for (int j = 0; j < L; ++j) {
+                Vec<Tx, V> o;
+                const bool here = (starts >> j) & 1;
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                h[v] = here ? u[j][v] : fmaf(al[j][v], h[v], u[j][v]);
-                o.set(v, h[v]);
-            }
-            if (j < n) o.store(op);
-            op += a.D;
-            if (PACKED && a.hT && live) {
+                for (int v = 0; v < V; ++v) {
+                    h[v] = here ? u[j][v] : fmaf(al[j][v], h[v], u[j][v]);
+                    o.set(v, h[v]);
+                }
+                if (j < n) o.store(op);
+                op += a.D;
                 const int m = s_end[i % kPlaces][run * L + j];
-                if (m >= 0)
+                if (a.hT && live && m >= 0)
 #pragma unroll
                     for (int v = 0; v < V; ++v) a.hT[(size_t)m * a.D + c + v] = h[v];
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < L; ++j) {
+                Vec<Tx, V> o;
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    h[v] = fmaf(al[j][v], h[v], u[j][v]);
+                    o.set(v, h[v]);
+                }
+                if (j < n) o.store(op);
+                op += a.D;
             }
         }
         if (!PACKED && a.hT && live && t.p == x.tiles - 1 && run == R - 1)

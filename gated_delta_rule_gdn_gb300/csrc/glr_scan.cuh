@@ -8,9 +8,9 @@
 //
 // The carry into tile p (in scan order) is, in a fixed association whatever the timing, so that results do not change
 // from run to run:
-//   the state at the start of its group of kGroup tiles, then the maps of the group's tiles before it, composed first.
+//   the state at the start of its group of tiles, then the maps of the group's tiles before it, composed first.
 // A tile publishes its map as soon as it has it; the last of a group publishes the next group's starting state.  So the
-// serial chain of a row is T / (64 kGroup) hops, and each byte of the inputs is read once.  A map is one 8-byte word and a
+// serial chain of a row is T / 64 / (tiles a group) hops, and each byte of the inputs is read once.  A map is one 8-byte word and a
 // state one 4-byte word, which are their own flags: the workspace starts as all ones, which no published word is.
 // Blocks take tickets for tiles in scan order, a few ahead, and go through their tiles in that order.  All that the smallest
 // tile without a carry waits for is therefore done or under way, and waiting ends; waits are bounded all the same.
@@ -26,7 +26,7 @@ namespace gdn {
 namespace glr {
 
 constexpr int kTile = kGlrTile;                  // checkpoints are tile entries
-constexpr int kGroup = 16;
+constexpr int kMostGroup = 16;
 constexpr unsigned kEmpty = 0xffffffffu;
 constexpr unsigned long long kWaitNs = 2000000000ull;
 
@@ -44,22 +44,26 @@ struct Exchange {
     unsigned* gave_up;      // 0 once a block gave up a wait
     unsigned long long* map;    // [tiles][chains][W]: A in the low half, H in the high half
     unsigned* state;        // [groups][chains][W]
-    int tiles, chains, total;
+    int tiles, chains, total, group;
 };
 
 struct Layout {
     size_t state_off, bytes;
-    int tiles, chains;
+    int tiles, chains, group;
 };
 inline Layout layout(int B, int T, int D, int width) {
     Layout l;
     l.tiles = T > kTile ? (T + kTile - 1) / kTile : 1;
     l.chains = B * ((D + width - 1) / width);
+    // Tiles a group: 16 halve the serial hops of a row, 8 halve the maps that a carry takes in.  With 4 chains (65,536 tokens x
+    // 250 channels) the hops count: 79 us with 16, 103 with 8; with 32 to 256 chains the maps: 229 and 219 us backward
+    // (B4 T4096 D2048), 2.78 and 2.28 ms (65,536 packed tokens x 4096 channels).
+    l.group = l.chains >= 16 ? 8 : kMostGroup;
     if (l.tiles == 1) {                          // nothing to exchange
         l.state_off = l.bytes = 0;
         return l;
     }
-    const size_t groups = (l.tiles + kGroup - 1) / kGroup, row = (size_t)l.chains * width;
+    const size_t groups = (l.tiles + l.group - 1) / l.group, row = (size_t)l.chains * width;
     l.state_off = 256 + l.tiles * row * sizeof(unsigned long long);
     l.bytes = (l.state_off + groups * row * sizeof(unsigned) + 255) / 256 * 256;
     return l;
@@ -70,6 +74,7 @@ inline Exchange exchange(const Layout& l, void* ws) {
     x.tiles = l.tiles;
     x.chains = l.chains;
     x.total = l.tiles * l.chains;
+    x.group = l.group;
     if (l.tiles == 1) return x;
     x.ticket = reinterpret_cast<unsigned*>(p);
     x.gave_up = x.ticket + 1;
@@ -108,52 +113,57 @@ __device__ __forceinline__ unsigned full(float v) {           // a float's bits,
 }
 
 // Hand over a tile's map, for one channel (the last tile of a group hands over the state after it instead).
-__device__ __forceinline__ bool closes_group(const Exchange& x, int p) { return p + 1 < x.tiles && p % kGroup == kGroup - 1; }
+__device__ __forceinline__ bool closes_group(const Exchange& x, int p) { return p + 1 < x.tiles && p % x.group == x.group - 1; }
 __device__ __forceinline__ void hand_map(const Exchange& x, int W, int p, int chain, int ch, float A, float H) {
     if (p + 1 < x.tiles && !closes_group(x, p))
         store_word(x.map + ((size_t)p * x.chains + chain) * W + ch, (unsigned long long)full(H) << 32 | full(A));
 }
 __device__ __forceinline__ void hand_state(const Exchange& x, int W, int p, int chain, int ch, float h) {
-    if (closes_group(x, p)) store_word(x.state + ((size_t)(p / kGroup + 1) * x.chains + chain) * W + ch, full(h));
+    if (closes_group(x, p)) store_word(x.state + ((size_t)(p / x.group + 1) * x.chains + chain) * W + ch, full(h));
 }
 
 // The carry into tile p of a chain, for one channel; `first` is the state before tile 0 of the row.
 template <bool PACKED>
 __device__ __forceinline__ float carry_in(const Exchange& x, int W, int p, int chain, int ch, float first, unsigned* status) {
-    const int group = p / kGroup, start = group * kGroup, n = p - start;
+    const int group = p / x.group, start = group * x.group, n = p - start;
     if (p == 0) return first;
     const size_t row = (size_t)x.chains * W, at = (size_t)chain * W + ch;
-    unsigned long long m[kGroup - 1];
-    unsigned st = group > 0 ? kEmpty : 0u;
-#pragma unroll
-    for (int j = 0; j < kGroup - 1; ++j) m[j] = j < n ? ~0ull : 0x3f800000ull;       // (the identity: A = 1, H = 0)
+    unsigned st = group > 0 ? load_word(x.state + group * row + at) : 0u;
+    float cA = 1.f, cH = 0.f;
     unsigned long long t0 = 0;
-    for (int round = 0;; ++round) {
-        bool ok = true;
-        if (st == kEmpty) st = load_word(x.state + group * row + at);
+    constexpr int kHalf = kMostGroup / 2;
+#pragma unroll 1
+    for (int base = 0; base < kMostGroup && (base < n || base == 0); base += kHalf) {
+        unsigned long long m[kHalf];
 #pragma unroll
-        for (int j = 0; j < kGroup - 1; ++j)
-            if ((unsigned)m[j] == kEmpty) m[j] = load_word(x.map + (start + j) * row + at);
+        for (int j = 0; j < kHalf; ++j) m[j] = base + j < n ? ~0ull : 0x3f800000ull;       // (the identity: A = 1, H = 0)
+        for (int round = 0;; ++round) {
+            bool ok = true;
 #pragma unroll
-        for (int j = 0; j < kGroup - 1; ++j) ok = ok && (unsigned)m[j] != kEmpty;
-        if (ok && st != kEmpty) break;
-        if ((round & 63) == 63) {
-            unsigned long long t;
-            asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
-            if (t0 == 0) t0 = t;
-            if (t - t0 > kWaitNs || load_word(x.gave_up) == 0u) {
-                store_word(x.gave_up, 0u);
-                atomicOr(status, 1u);
-                break;                            // the outputs are now unspecified
+            for (int j = 0; j < kHalf; ++j)
+                if ((unsigned)m[j] == kEmpty) m[j] = load_word(x.map + (start + base + j) * row + at);
+            if (st == kEmpty) st = load_word(x.state + group * row + at);
+#pragma unroll
+            for (int j = 0; j < kHalf; ++j) ok = ok && (unsigned)m[j] != kEmpty;
+            // (the state is waited for with the last of the maps)
+            if (ok && (st != kEmpty || base + kHalf < n)) break;
+            if ((round & 63) == 63) {
+                unsigned long long t;
+                asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+                if (t0 == 0) t0 = t;
+                if (t - t0 > kWaitNs || load_word(x.gave_up) == 0u) {
+                    store_word(x.gave_up, 0u);
+                    atomicOr(status, 1u);
+                    break;                        // the outputs are now unspecified
+                }
             }
         }
-    }
-    float cA = 1.f, cH = 0.f;
 #pragma unroll
-    for (int j = 0; j < kGroup - 1; ++j) {
-        const float a = __uint_as_float((unsigned)m[j]), h = __uint_as_float((unsigned)(m[j] >> 32));
-        cH = apply<PACKED>(a, h, cH);
-        cA = both<PACKED>(cA, a);
+        for (int j = 0; j < kHalf; ++j) {
+            const float a = __uint_as_float((unsigned)m[j]), h = __uint_as_float((unsigned)(m[j] >> 32));
+            cH = apply<PACKED>(a, h, cH);
+            cA = both<PACKED>(cA, a);
+        }
     }
     return apply<PACKED>(cA, cH, group > 0 ? __uint_as_float(st) : first);
 }
@@ -161,6 +171,54 @@ __device__ __forceinline__ float carry_in(const Exchange& x, int W, int p, int c
 struct Channel { float neg_eA, dt; };   // -exp(A_log) (0: g is log a) and dt_bias of a channel
 __device__ __forceinline__ Channel channel(const float* A_log, const float* dt_bias, int c) {
     return {A_log ? -expf(A_log[c]) : 0.f, dt_bias ? dt_bias[c] : 0.f};
+}
+
+// log a of a run's gates, in place.
+template <int L, int V>
+__device__ __forceinline__ void log_decays(const GlrArgs& a, int c, bool live, float (&la)[L][V]) {
+    if (a.A_log) {
+        Channel ch[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) ch[v] = live ? channel(a.A_log, a.dt_bias, c + v) : Channel{0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < L; ++j) {
+            if constexpr (V % 2 == 0) {
+#pragma unroll
+                for (int v = 0; v < V; v += 2)
+                    softplus(la[j][v] + ch[v].dt, la[j][v + 1] + ch[v + 1].dt, ch[v].neg_eA, ch[v + 1].neg_eA, la[j][v], la[j][v + 1]);
+            } else {
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    const float z = la[j][v] + ch[v].dt;
+                    la[j][v] = ch[v].neg_eA * softplus(z, tail(z));
+                }
+            }
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < L; ++j)
+#pragma unroll
+            for (int v = 0; v < V; ++v) la[j][v] = min_nan(la[j][v], 88.f);
+    }
+}
+// f(j, v, decay) for every element of a run.
+template <int L, int V, typename F>
+__device__ __forceinline__ void decays(float (&la)[L][V], F f) {
+#pragma unroll
+    for (int j = 0; j < L; ++j) {
+        if constexpr (V % 2 == 0) {
+#pragma unroll
+            for (int v = 0; v < V; v += 2) {
+                Decay d0, d1;
+                decay(la[j][v], la[j][v + 1], d0, d1);
+                f(j, v, d0);
+                f(j, v + 1, d1);
+            }
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v) f(j, v, decay(la[j][v]));
+        }
+    }
 }
 
 // The block's division of work.  Its compute threads take a tile in two stages: the maps of their runs (stage one), and
@@ -206,7 +264,8 @@ struct Tickets {
 };
 
 // Packed sequences: which one starts, and which ends, at token i of tile p (-1: none).
-__device__ __forceinline__ void sequence_marks(const GlrArgs& a, int p, int i, int* starts, int* ends) {
+// Returns, in every lane, whether there is any among the warp's.
+__device__ __forceinline__ bool sequence_marks(const GlrArgs& a, int p, int i, int* starts, int* ends) {
     const int t = p * kTile + i;
     int s = -1, e = -1;
     if (t < a.T) {
@@ -216,6 +275,7 @@ __device__ __forceinline__ void sequence_marks(const GlrArgs& a, int p, int i, i
     }
     starts[i] = s;
     ends[i] = e;
+    return __any_sync(~0u, s >= 0 || e >= 0);
 }
 
 }  // namespace glr

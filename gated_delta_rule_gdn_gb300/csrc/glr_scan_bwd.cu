@@ -6,6 +6,8 @@
 // the three gradients written once.  The per-channel sums of A_log and dt_bias leave the block as a row of partial sums
 // that a second kernel adds in order.
 
+#include <type_traits>
+
 #include "glr_scan.cuh"
 
 namespace gdn {
@@ -33,11 +35,18 @@ glr_bwd_kernel(const GlrArgs a, const Exchange x, float* part) {
     __shared__ float sA[2][R][W], sH[2][R][W], sG[2][R][W], s_sum[3][2][R][W];
     __shared__ unsigned char s_any[2][R];        // bit 0: a sequence starts in the run; bit 1: one ends
     __shared__ int s_start[PACKED ? kPlaces : 1][kTile], s_end[PACKED ? kPlaces : 1][kTile];
+    __shared__ bool s_marked[kPlaces][2];        // whether either half of a tile's tokens has a mark
     __shared__ Tile s_tile[kPlaces];
     const int tid = threadIdx.x;
+    const auto marked = [&](int i) { return PACKED && (s_marked[i % kPlaces][0] || s_marked[i % kPlaces][1]); };
 
     if (tid >= kThreads) {                       // the carry threads: the gradient's, the state's
         const int ch = (tid - kThreads) % W, side = (tid - kThreads) / W;
+        const auto mark = [&](int slot) {
+            if (!PACKED || s_tile[slot].chain < 0) return;
+            const bool any = sequence_marks(a, s_tile[slot].p, tid - kThreads, s_start[slot], s_end[slot]);
+            if (tid % 32 == 0) s_marked[slot][(tid - kThreads) / 32] = any;
+        };
         Tickets tickets(x);
         unsigned ticket = 0;
         if (tid == kThreads) {
@@ -46,9 +55,7 @@ glr_bwd_kernel(const GlrArgs a, const Exchange x, float* part) {
         }
         __syncwarp();
         S::sync(kMaps);
-        if (PACKED)
-            for (int i = 0; i < 3; ++i)
-                if (s_tile[i].chain >= 0) sequence_marks(a, s_tile[i].p, tid - kThreads, s_start[i], s_end[i]);
+        for (int i = 0; i < 3; ++i) mark(i);
         __syncthreads();
         // the sums of tile i over its runs, in order
         const auto sums = [&](int i) {
@@ -72,42 +79,46 @@ glr_bwd_kernel(const GlrArgs a, const Exchange x, float* part) {
             const bool live = t.c0 + ch < a.D;
             float enter = 0.f;
             if (side == 0) {
-                if (!PACKED && q < kGroup && a.dhT && live) enter = a.dhT[(size_t)t.b * a.D + t.c0 + ch];
+                if (!PACKED && q < x.group && a.dhT && live) enter = a.dhT[(size_t)t.b * a.D + t.c0 + ch];
             } else if (side == 1 && live && t.p * kTile < a.T) {
                 if (t.p > 0 || PACKED) enter = a.ckpt[((size_t)t.b * x.tiles + t.p) * a.D + t.c0 + ch];
                 else if (a.h0) enter = a.h0[(size_t)t.b * a.D + t.c0 + ch];
             }
             S::sync(kMaps + k);
-            if (side == 0) {
-                const auto run_A = [&](int r) { return PACKED && (s_any[k][r] & 2) ? -1.f : sA[k][r][ch]; };
-                float A = 1.f, G = 0.f;
+            // (a tile without marks forgets nothing inside)
+            const auto work = [&](auto marks) {
+                constexpr bool M = decltype(marks)::value;
+                if (side == 0) {
+                    const auto run_A = [&](int r) { return M && (s_any[k][r] & 2) ? -1.f : sA[k][r][ch]; };
+                    float A = 1.f, G = 0.f;
 #pragma unroll
-                for (int r = R - 1; r >= 0; --r) {
-                    G = apply<PACKED>(run_A(r), sG[k][r][ch], G);
-                    A = both<PACKED>(A, run_A(r));
-                }
-                hand_map(x, W, q, t.chain, ch, A, G);
-                float g = carry_in<PACKED>(x, W, q, t.chain, ch, enter, &g_glr_bwd_status);
-                hand_state(x, W, q, t.chain, ch, apply<PACKED>(A, G, g));
+                    for (int r = R - 1; r >= 0; --r) {
+                        G = apply<M>(run_A(r), sG[k][r][ch], G);
+                        A = both<M>(A, run_A(r));
+                    }
+                    hand_map(x, W, q, t.chain, ch, A, G);
+                    float g = carry_in<PACKED>(x, W, q, t.chain, ch, enter, &g_glr_bwd_status);
+                    hand_state(x, W, q, t.chain, ch, apply<PACKED>(A, G, g));
 #pragma unroll
-                for (int r = R - 1; r >= 0; --r) {
-                    const float rG = sG[k][r][ch];
-                    sG[k][r][ch] = g;
-                    g = apply<PACKED>(run_A(r), rG, g);
-                }
-            } else if (side == 1) {
-                float h = enter;
+                    for (int r = R - 1; r >= 0; --r) {
+                        const float rG = sG[k][r][ch];
+                        sG[k][r][ch] = g;
+                        g = apply<M>(run_A(r), rG, g);
+                    }
+                } else if (side == 1) {
+                    float h = enter;
 #pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    const float rA = PACKED && (s_any[k][r] & 1) ? -1.f : sA[k][r][ch], rH = sH[k][r][ch];
-                    sH[k][r][ch] = h;
-                    h = apply<PACKED>(rA, rH, h);
+                    for (int r = 0; r < R; ++r) {
+                        const float rA = M && (s_any[k][r] & 1) ? -1.f : sA[k][r][ch], rH = sH[k][r][ch];
+                        sH[k][r][ch] = h;
+                        h = apply<M>(rA, rH, h);
+                    }
                 }
-            }
+            };
+            if (marked(i)) work(std::bool_constant<PACKED>{}); else work(std::false_type{});
             S::arrive(kCarry + k);
             if (a.dA && i >= 2) sums(i - 2);     // (stage two of tile i - 2 came before the maps of tile i)
-            if (PACKED && s_tile[ahead].chain >= 0)
-                sequence_marks(a, s_tile[ahead].p, tid - kThreads, s_start[ahead], s_end[ahead]);
+            mark(ahead);
         }
         if (a.dA && i > 0) {
             S::sync(kMaps + (i & 1));           // the compute threads are through
@@ -166,12 +177,10 @@ glr_bwd_kernel(const GlrArgs a, const Exchange x, float* part) {
     struct Held { float al[L][V], e[L][V], la[L][V], u[L][V]; };
     const auto marks = [&](int i, unsigned* starts, unsigned* ends) {
         *starts = *ends = 0;
-        if (PACKED) {
 #pragma unroll
-            for (int j = 0; j < L; ++j) {
-                *starts |= (s_start[i % kPlaces][run * L + j] >= 0 ? 1u : 0u) << j;
-                *ends |= (s_end[i % kPlaces][run * L + j] >= 0 ? 1u : 0u) << j;
-            }
+        for (int j = 0; j < L; ++j) {
+            *starts |= (s_start[i % kPlaces][run * L + j] >= 0 ? 1u : 0u) << j;
+            *ends |= (s_end[i % kPlaces][run * L + j] >= 0 ? 1u : 0u) << j;
         }
     };
     // dO, with what enters behind a sequence's last token
@@ -179,13 +188,14 @@ glr_bwd_kernel(const GlrArgs a, const Exchange x, float* part) {
         const Vec<Tx, V> o = buf_x(i)[(L + j) * kThreads];
 #pragma unroll
         for (int v = 0; v < V; ++v) d[v] = o.get(v);
-        if (PACKED && end && a.dhT && c < a.D)
+        if (end && a.dhT && c < a.D)
 #pragma unroll
             for (int v = 0; v < V; ++v) d[v] += a.dhT[(size_t)s_end[i % kPlaces][run * L + j] * a.D + c + v];
     };
 
     // stage one: decays and inputs of the run, and its maps: (A, H) of the state, (A, G) of the gradient
-    const auto maps = [&](int i, Held& q) {
+    const auto maps = [&](int i, Held& q, auto marks_here) {
+        constexpr bool M = decltype(marks_here)::value;
         const Tile t = s_tile[i % kPlaces];
         const int c = t.c0 + lane * V, count = a.T - (t.p * kTile + run * L);
         const bool live = c < a.D;
@@ -207,40 +217,20 @@ glr_bwd_kernel(const GlrArgs a, const Exchange x, float* part) {
                 for (int v = 0; v < V; ++v) q.u[j][v] *= sigmoid(gi.get(v));
             }
         }
-        if (a.A_log) {
-            Channel ch[V];
-#pragma unroll
-            for (int v = 0; v < V; ++v) ch[v] = live ? channel(a.A_log, a.dt_bias, c + v) : Channel{0.f, 0.f};
-#pragma unroll
-            for (int j = 0; j < L; ++j)
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    const float z = q.la[j][v] + ch[v].dt;
-                    q.la[j][v] = ch[v].neg_eA * softplus(z, tail(z));
-                }
-        } else {
-#pragma unroll
-            for (int j = 0; j < L; ++j)
-#pragma unroll
-                for (int v = 0; v < V; ++v) q.la[j][v] = min_nan(q.la[j][v], 88.f);
-        }
-#pragma unroll
-        for (int j = 0; j < L; ++j)
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const Decay d = decay(q.la[j][v]);
-                q.al[j][v] = d.a;
-                q.e[j][v] = d.e;
-                if (a.normalize) q.u[j][v] *= root(input_power(d));
-            }
+        log_decays<L, V>(a, c, live, q.la);
+        decays<L, V>(q.la, [&](int j, int v, const Decay& d) {
+            q.al[j][v] = d.a;
+            q.e[j][v] = d.e;
+            if (a.normalize) q.u[j][v] *= root(input_power(d));
+        });
         if (count < L) {                         // past the row's end state and gradient stay
 #pragma unroll
             for (int j = 0; j < L; ++j)
 #pragma unroll
                 for (int v = 0; v < V; ++v) q.al[j][v] = j < count ? q.al[j][v] : 1.f;
         }
-        unsigned starts, ends;
-        marks(i, &starts, &ends);
+        unsigned starts = 0, ends = 0;
+        if (M) marks(i, &starts, &ends);
         float A[V], H[V], G[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -249,7 +239,7 @@ glr_bwd_kernel(const GlrArgs a, const Exchange x, float* part) {
         }
 #pragma unroll
         for (int j = 0; j < L; ++j) {
-            const bool start = PACKED && ((starts >> j) & 1);
+            const bool start = M && ((starts >> j) & 1);
             if (start && a.h0 && live)
 #pragma unroll
                 for (int v = 0; v < V; ++v)
@@ -262,7 +252,7 @@ glr_bwd_kernel(const GlrArgs a, const Exchange x, float* part) {
         }
 #pragma unroll
         for (int j = L - 1; j >= 0; --j) {
-            const bool end = PACKED && ((ends >> j) & 1);
+            const bool end = M && ((ends >> j) & 1);
             float d[V];
             grad_o(i, j, c, end, d);
 #pragma unroll
@@ -280,13 +270,14 @@ glr_bwd_kernel(const GlrArgs a, const Exchange x, float* part) {
 
     // stage two: with h_{t-1}, and D the gradient of h_t,
     //   dx = D s sigma(i), di = dx x (1 - sigma(i)), dla = D (a h_{t-1} - sigma(i) x a^2 / s), dg = dla dlog a/dg
-    const auto gradients = [&](int i, const Held& q) {
+    const auto gradients = [&](int i, const Held& q, auto marks_here) {
+        constexpr bool M = decltype(marks_here)::value;
         const Tile t = s_tile[i % kPlaces];
         const int c = t.c0 + lane * V, t0 = t.p * kTile + run * L;
         const bool live = c < a.D;
         const int n = live ? a.T - t0 : 0;
-        unsigned starts, ends;
-        marks(i, &starts, &ends);
+        unsigned starts = 0, ends = 0;
+        if (M) marks(i, &starts, &ends);
         float D[L][V], G[V], h[V], pA[V], pdt[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -296,14 +287,14 @@ glr_bwd_kernel(const GlrArgs a, const Exchange x, float* part) {
         }
 #pragma unroll
         for (int j = L - 1; j >= 0; --j) {
-            const bool end = PACKED && ((ends >> j) & 1);
+            const bool end = M && ((ends >> j) & 1);
             grad_o(i, j, c, end, D[j]);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 if (!end) D[j][v] += G[v];
                 G[v] = q.al[j][v] * D[j][v];
             }
-            if (PACKED && a.dh0 && live) {
+            if (M && a.dh0 && live) {
                 const int s = s_start[i % kPlaces][run * L + j];
                 if (s >= 0)
 #pragma unroll
@@ -319,7 +310,7 @@ glr_bwd_kernel(const GlrArgs a, const Exchange x, float* part) {
         Tg* dg_p = static_cast<Tg*>(a.dg) + at;
 #pragma unroll
         for (int j = 0; j < L; ++j) {
-            const bool start = PACKED && ((starts >> j) & 1);
+            const bool start = M && ((starts >> j) & 1);
             float hp[V];
 #pragma unroll
             for (int v = 0; v < V; ++v) {
@@ -421,11 +412,12 @@ glr_bwd_kernel(const GlrArgs a, const Exchange x, float* part) {
         const bool more = s_tile[i % kPlaces].chain >= 0;
         if (more) {
             mix::copies_wait<1>();
-            maps(i, q);
+            if (marked(i)) maps(i, q, std::bool_constant<PACKED>{}); else maps(i, q, std::false_type{});
         }
         if (i > 0) {
             S::sync(kCarry + ((i - 1) & 1));
-            gradients(i - 1, before);
+            if (marked(i - 1)) gradients(i - 1, before, std::bool_constant<PACKED>{});
+            else gradients(i - 1, before, std::false_type{});
         }
         if (!more) {
             if (a.dA) S::arrive(kMaps + (i & 1));
