@@ -53,7 +53,7 @@ glr_fwd_kernel(const GlrArgs a, const Exchange x, const int publish) {
                 ticket = tickets.take();
             }
             float first = 0.f;
-            if (!PACKED && ch < W && t.p < x.group && a.h0 && t.c0 + ch < a.D) first = a.h0[(size_t)t.b * a.D + t.c0 + ch];
+            if (!PACKED && ch < W && t.p < kSpan && a.h0 && t.c0 + ch < a.D) first = a.h0[(size_t)t.b * a.D + t.c0 + ch];
             S::sync(kMaps + k);
             if (ch < W) {
                 // (a tile without marks forgets nothing inside)
@@ -72,9 +72,7 @@ glr_fwd_kernel(const GlrArgs a, const Exchange x, const int publish) {
                         A *= sA[k][r][ch];
                     }
                 }
-                if (publish || t.p > 0) hand_map(x, W, t.p, t.chain, ch, A, H);
-                float h = carry_in<PACKED>(x, W, t.p, t.chain, ch, first, &g_glr_status);
-                hand_state(x, W, t.p, t.chain, ch, apply<PACKED>(A, H, h));
+                float h = carry_in<PACKED>(x, W, t.p, t.chain, ch, A, H, first, publish || t.p > 0, &g_glr_status);
                 if (a.ckpt && t.c0 + ch < a.D && t.p * kTile < a.T)
                     a.ckpt[((size_t)t.b * x.tiles + t.p) * a.D + t.c0 + ch] = h;
                 if (marked) {

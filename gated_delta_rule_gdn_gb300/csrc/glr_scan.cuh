@@ -7,11 +7,12 @@
 // so that a state that is not a number stays in its own sequence.
 //
 // The carry into tile p (in scan order) is, in a fixed association whatever the timing, so that results do not change
-// from run to run:
-//   the state at the start of its group of tiles, then the maps of the group's tiles before it, composed first.
-// A tile publishes its map as soon as it has it; the last of a group publishes the next group's starting state.  So the
-// serial chain of a row is T / 64 / (tiles a group) hops, and each byte of the inputs is read once.  A map is one 8-byte word and a
-// state one 4-byte word, which are their own flags: the workspace starts as all ones, which no published word is.
+// from run to run: the state at the start of its block of 64 tiles, then the maps of the block's groups of 8 tiles before
+// its own, then the maps of its group's tiles before it.  A tile publishes its map as soon as it has it; the last of a
+// group the group's map as soon as it has the other seven; the last of a block the next block's starting state.  So the
+// serial chain of a row is T / 4096 hops, a carry takes in at most 14 maps, and each byte of the inputs is read once.  A map
+// is one 8-byte word and a state one 4-byte word, which are their own flags: the workspace starts as all ones, which no
+// published word is.
 // Blocks take tickets for tiles in scan order, a few ahead, and go through their tiles in that order.  All that the smallest
 // tile without a carry waits for is therefore done or under way, and waiting ends; waits are bounded all the same.
 #pragma once
@@ -26,7 +27,7 @@ namespace gdn {
 namespace glr {
 
 constexpr int kTile = kGlrTile;                  // checkpoints are tile entries
-constexpr int kMostGroup = 16;
+constexpr int kGroup = 8, kSpan = kGroup * kGroup;      // tiles a group, and a block of groups
 constexpr unsigned kEmpty = 0xffffffffu;
 constexpr unsigned long long kWaitNs = 2000000000ull;
 
@@ -42,30 +43,29 @@ struct Residency {
 struct Exchange {
     unsigned* ticket;       // the last ticket taken (all ones: none)
     unsigned* gave_up;      // 0 once a block gave up a wait
-    unsigned long long* map;    // [tiles][chains][W]: A in the low half, H in the high half
-    unsigned* state;        // [groups][chains][W]
-    int tiles, chains, total, group;
+    unsigned long long* map;        // [tiles][chains][W]: A in the low half, H in the high half
+    unsigned long long* group_map;  // [groups][chains][W]
+    unsigned* state;                // [blocks of groups][chains][W]
+    int tiles, chains, total;
 };
 
 struct Layout {
-    size_t state_off, bytes;
-    int tiles, chains, group;
+    size_t group_off, state_off, bytes;
+    int tiles, chains;
 };
 inline Layout layout(int B, int T, int D, int width) {
     Layout l;
     l.tiles = T > kTile ? (T + kTile - 1) / kTile : 1;
     l.chains = B * ((D + width - 1) / width);
-    // Tiles a group: 16 halve the serial hops of a row, 8 halve the maps that a carry takes in.  With 4 chains (65,536 tokens x
-    // 250 channels) the hops count: 79 us with 16, 103 with 8; with 32 to 256 chains the maps: 229 and 219 us backward
-    // (B4 T4096 D2048), 2.78 and 2.28 ms (65,536 packed tokens x 4096 channels).
-    l.group = l.chains >= 16 ? 8 : kMostGroup;
     if (l.tiles == 1) {                          // nothing to exchange
-        l.state_off = l.bytes = 0;
+        l.group_off = l.state_off = l.bytes = 0;
         return l;
     }
-    const size_t groups = (l.tiles + l.group - 1) / l.group, row = (size_t)l.chains * width;
-    l.state_off = 256 + l.tiles * row * sizeof(unsigned long long);
-    l.bytes = (l.state_off + groups * row * sizeof(unsigned) + 255) / 256 * 256;
+    const size_t groups = (l.tiles + kGroup - 1) / kGroup, spans = (l.tiles + kSpan - 1) / kSpan;
+    const size_t row = (size_t)l.chains * width;
+    l.group_off = 256 + l.tiles * row * sizeof(unsigned long long);
+    l.state_off = l.group_off + groups * row * sizeof(unsigned long long);
+    l.bytes = (l.state_off + spans * row * sizeof(unsigned) + 255) / 256 * 256;
     return l;
 }
 inline Exchange exchange(const Layout& l, void* ws) {
@@ -74,11 +74,11 @@ inline Exchange exchange(const Layout& l, void* ws) {
     x.tiles = l.tiles;
     x.chains = l.chains;
     x.total = l.tiles * l.chains;
-    x.group = l.group;
     if (l.tiles == 1) return x;
     x.ticket = reinterpret_cast<unsigned*>(p);
     x.gave_up = x.ticket + 1;
     x.map = reinterpret_cast<unsigned long long*>(p + 256);
+    x.group_map = reinterpret_cast<unsigned long long*>(p + l.group_off);
     x.state = reinterpret_cast<unsigned*>(p + l.state_off);
     return x;
 }
@@ -112,60 +112,82 @@ __device__ __forceinline__ unsigned full(float v) {           // a float's bits,
     return b == kEmpty ? 0x7fffffffu : b;
 }
 
-// Hand over a tile's map, for one channel (the last tile of a group hands over the state after it instead).
-__device__ __forceinline__ bool closes_group(const Exchange& x, int p) { return p + 1 < x.tiles && p % x.group == x.group - 1; }
-__device__ __forceinline__ void hand_map(const Exchange& x, int W, int p, int chain, int ch, float A, float H) {
-    if (p + 1 < x.tiles && !closes_group(x, p))
-        store_word(x.map + ((size_t)p * x.chains + chain) * W + ch, (unsigned long long)full(H) << 32 | full(A));
+__device__ __forceinline__ unsigned long long word_of(float A, float H) { return (unsigned long long)full(H) << 32 | full(A); }
+constexpr unsigned long long kIdentity = 0x3f800000ull;       // A = 1, H = 0
+
+// Load those of the first n (<= 7) words of a column that are still empty; whether all are there now.
+__device__ __forceinline__ bool gather(unsigned long long (&m)[kGroup - 1], const unsigned long long* p, size_t step) {
+#pragma unroll
+    for (int j = 0; j < kGroup - 1; ++j)
+        if ((unsigned)m[j] == kEmpty) m[j] = load_word(p + j * step);
+    bool ok = true;
+#pragma unroll
+    for (int j = 0; j < kGroup - 1; ++j) ok = ok && (unsigned)m[j] != kEmpty;
+    return ok;
 }
-__device__ __forceinline__ void hand_state(const Exchange& x, int W, int p, int chain, int ch, float h) {
-    if (closes_group(x, p)) store_word(x.state + ((size_t)(p / x.group + 1) * x.chains + chain) * W + ch, full(h));
+template <bool PACKED>
+__device__ __forceinline__ void compose(const unsigned long long (&m)[kGroup - 1], float& A, float& H) {
+    A = 1.f;
+    H = 0.f;
+#pragma unroll
+    for (int j = 0; j < kGroup - 1; ++j) {
+        const float a = __uint_as_float((unsigned)m[j]);
+        H = apply<PACKED>(a, __uint_as_float((unsigned)(m[j] >> 32)), H);
+        A = both<PACKED>(A, a);
+    }
 }
 
-// The carry into tile p of a chain, for one channel; `first` is the state before tile 0 of the row.
-template <bool PACKED>
-__device__ __forceinline__ float carry_in(const Exchange& x, int W, int p, int chain, int ch, float first, unsigned* status) {
-    const int group = p / x.group, start = group * x.group, n = p - start;
-    if (p == 0) return first;
-    const size_t row = (size_t)x.chains * W, at = (size_t)chain * W + ch;
-    unsigned st = group > 0 ? load_word(x.state + group * row + at) : 0u;
-    float cA = 1.f, cH = 0.f;
+// Time out of a wait, looked at once in 64 rounds: true if the block gives up (its outputs are then unspecified).
+struct Patience {
     unsigned long long t0 = 0;
-    constexpr int kHalf = kMostGroup / 2;
-#pragma unroll 1
-    for (int base = 0; base < kMostGroup && (base < n || base == 0); base += kHalf) {
-        unsigned long long m[kHalf];
-#pragma unroll
-        for (int j = 0; j < kHalf; ++j) m[j] = base + j < n ? ~0ull : 0x3f800000ull;       // (the identity: A = 1, H = 0)
-        for (int round = 0;; ++round) {
-            bool ok = true;
-#pragma unroll
-            for (int j = 0; j < kHalf; ++j)
-                if ((unsigned)m[j] == kEmpty) m[j] = load_word(x.map + (start + base + j) * row + at);
-            if (st == kEmpty) st = load_word(x.state + group * row + at);
-#pragma unroll
-            for (int j = 0; j < kHalf; ++j) ok = ok && (unsigned)m[j] != kEmpty;
-            // (the state is waited for with the last of the maps)
-            if (ok && (st != kEmpty || base + kHalf < n)) break;
-            if ((round & 63) == 63) {
-                unsigned long long t;
-                asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
-                if (t0 == 0) t0 = t;
-                if (t - t0 > kWaitNs || load_word(x.gave_up) == 0u) {
-                    store_word(x.gave_up, 0u);
-                    atomicOr(status, 1u);
-                    break;                        // the outputs are now unspecified
-                }
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < kHalf; ++j) {
-            const float a = __uint_as_float((unsigned)m[j]), h = __uint_as_float((unsigned)(m[j] >> 32));
-            cH = apply<PACKED>(a, h, cH);
-            cA = both<PACKED>(cA, a);
-        }
+    int round = 0;
+    __device__ __forceinline__ bool over(const Exchange& x, unsigned* status) {
+        if ((++round & 63) != 0) return false;
+        unsigned long long t;
+        asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+        if (t0 == 0) t0 = t;
+        if (t - t0 <= kWaitNs && load_word(x.gave_up) != 0u) return false;
+        store_word(x.gave_up, 0u);
+        atomicOr(status, 1u);
+        return true;
     }
-    return apply<PACKED>(cA, cH, group > 0 ? __uint_as_float(st) : first);
+};
+
+// Hand over the map (A, H) of tile p of a chain, for one channel, and get the carry into it; `first` is the state before
+// tile 0 of the row.
+template <bool PACKED>
+__device__ __forceinline__ float carry_in(const Exchange& x, int W, int p, int chain, int ch, float A, float H, float first,
+                                          bool publish, unsigned* status) {
+    const size_t row = (size_t)x.chains * W, at = (size_t)chain * W + ch;
+    const int in_group = p % kGroup, group = p / kGroup, in_span = group % kGroup, span = p / kSpan;
+    const bool more = p + 1 < x.tiles, last = in_group == kGroup - 1;
+    if (more && !last && publish) store_word(x.map + p * row + at, word_of(A, H));
+    unsigned long long m[kGroup - 1], g[kGroup - 1];
+#pragma unroll
+    for (int j = 0; j < kGroup - 1; ++j) {
+        m[j] = j < in_group ? ~0ull : kIdentity;
+        g[j] = j < in_span ? ~0ull : kIdentity;
+    }
+    const unsigned long long* mp = x.map + (size_t)(p - in_group) * row + at;
+    const unsigned long long* gp = x.group_map + (size_t)(group - in_span) * row + at;
+    unsigned st = span > 0 ? load_word(x.state + span * row + at) : 0u;
+    gather(g, gp, row);
+    Patience wait;
+    while (!gather(m, mp, row))
+        if (wait.over(x, status)) break;
+    float mA, mH;
+    compose<PACKED>(m, mA, mH);
+    if (more && last && in_span != kGroup - 1)
+        store_word(x.group_map + (size_t)group * row + at, word_of(both<PACKED>(mA, A), apply<PACKED>(A, H, mH)));
+    while (!gather(g, gp, row) || st == kEmpty) {
+        if (st == kEmpty) st = load_word(x.state + span * row + at);
+        if (wait.over(x, status)) break;
+    }
+    float gA, gH;
+    compose<PACKED>(g, gA, gH);
+    const float carry = apply<PACKED>(mA, mH, apply<PACKED>(gA, gH, span > 0 ? __uint_as_float(st) : first));
+    if (more && p % kSpan == kSpan - 1) store_word(x.state + (size_t)(span + 1) * row + at, full(apply<PACKED>(A, H, carry)));
+    return carry;
 }
 
 struct Channel { float neg_eA, dt; };   // -exp(A_log) (0: g is log a) and dt_bias of a channel

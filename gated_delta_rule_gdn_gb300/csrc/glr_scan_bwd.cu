@@ -79,7 +79,7 @@ glr_bwd_kernel(const GlrArgs a, const Exchange x, float* part) {
             const bool live = t.c0 + ch < a.D;
             float enter = 0.f;
             if (side == 0) {
-                if (!PACKED && q < x.group && a.dhT && live) enter = a.dhT[(size_t)t.b * a.D + t.c0 + ch];
+                if (!PACKED && q < kSpan && a.dhT && live) enter = a.dhT[(size_t)t.b * a.D + t.c0 + ch];
             } else if (side == 1 && live && t.p * kTile < a.T) {
                 if (t.p > 0 || PACKED) enter = a.ckpt[((size_t)t.b * x.tiles + t.p) * a.D + t.c0 + ch];
                 else if (a.h0) enter = a.h0[(size_t)t.b * a.D + t.c0 + ch];
@@ -96,9 +96,7 @@ glr_bwd_kernel(const GlrArgs a, const Exchange x, float* part) {
                         G = apply<M>(run_A(r), sG[k][r][ch], G);
                         A = both<M>(A, run_A(r));
                     }
-                    hand_map(x, W, q, t.chain, ch, A, G);
-                    float g = carry_in<PACKED>(x, W, q, t.chain, ch, enter, &g_glr_bwd_status);
-                    hand_state(x, W, q, t.chain, ch, apply<PACKED>(A, G, g));
+                    float g = carry_in<PACKED>(x, W, q, t.chain, ch, A, G, enter, true, &g_glr_bwd_status);
 #pragma unroll
                     for (int r = R - 1; r >= 0; --r) {
                         const float rG = sG[k][r][ch];
