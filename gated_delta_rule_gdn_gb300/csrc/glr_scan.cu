@@ -25,25 +25,27 @@ glr_fwd_kernel(const GlrArgs a, const Exchange x, const int publish) {
     __shared__ float sA[2][R][W], sH[2][R][W];
     __shared__ int s_start[PACKED ? kPlaces : 1][kTile], s_end[PACKED ? kPlaces : 1][kTile];
     __shared__ bool s_marked[kPlaces][2];        // whether either half of a tile's tokens has a mark
+    __shared__ __align__(16) Channel s_chan[kPlaces][W];
     __shared__ Tile s_tile[kPlaces];
     const int tid = threadIdx.x;
 
     if (tid >= kThreads) {                       // the carry threads
         const int ch = tid - kThreads;
-        const auto mark = [&](int slot) {
-            if (!PACKED || s_tile[slot].chain < 0) return;
+        const auto prepare = [&](int slot) {      // a place's channels and marks
+            if (s_tile[slot].chain < 0) return;
+            const int pc = tid - kThreads, c = s_tile[slot].c0 + pc;
+            if (a.A_log && pc < W && c < a.D) s_chan[slot][pc] = channel(a.A_log, a.dt_bias, c);
+            if (!PACKED) return;
             const bool any = sequence_marks(a, s_tile[slot].p, ch, s_start[slot], s_end[slot]);
             if (ch % 32 == 0) s_marked[slot][ch / 32] = any;
         };
         Tickets tickets(x);
         unsigned ticket = 0;
-        if (ch == 0) {
-            for (int i = 0; i < 3; ++i) s_tile[i] = tile_of(x, a, W, tickets.take(), false);
-            ticket = tickets.take();
-        }
+        first_tiles(x, a, W, false, tickets, s_tile, ch == 0, [] { __syncthreads(); });
+        if (ch == 0) ticket = tickets.take();
         __syncwarp();
         S::sync(kMaps);                         // (places are read below by all carry threads: meet once)
-        for (int i = 0; i < 3; ++i) mark(i);
+        for (int i = 0; i < 3; ++i) prepare(i);
         __syncthreads();
         for (int i = 0; s_tile[i % kPlaces].chain >= 0; ++i) {
             const Tile t = s_tile[i % kPlaces];
@@ -92,7 +94,7 @@ glr_fwd_kernel(const GlrArgs a, const Exchange x, const int publish) {
                 }
             }
             S::arrive(kCarry + k);
-            mark(ahead);
+            prepare(ahead);
         }
         return;
     }
@@ -170,7 +172,7 @@ glr_fwd_kernel(const GlrArgs a, const Exchange x, const int publish) {
                 for (int v = 0; v < V; ++v) u[j][v] *= sigmoid(gi.get(v));
             }
         }
-        log_decays<L, V>(a, c, live, al);
+        log_decays<L, V>(a, s_chan[i % kPlaces] + lane * V, al);
         decays<L, V>(al, [&](int j, int v, const Decay& d) {
             if (a.normalize) u[j][v] *= root(input_power(d));
             al[j][v] = d.a;
@@ -268,10 +270,11 @@ glr_fwd_kernel(const GlrArgs a, const Exchange x, const int publish) {
         }
     };
 
+    __syncthreads();
+    fetch(0);
     S::arrive(kMaps);
     __syncthreads();
     if (s_tile[0].chain < 0) return;
-    fetch(0);
     fetch(1);
     float al[L][V], u[L][V], al_p[L][V], u_p[L][V];           // the current tile's, and the one's before it
     for (int i = 0;; ++i) {
@@ -336,7 +339,7 @@ cudaError_t fwd_packed(const GlrArgs& a, cudaStream_t s) {
 
 template <typename Tx, typename Tg>
 cudaError_t fwd_wide(const GlrArgs& a, cudaStream_t s) {
-    if (glr_vector(a, 4)) return fwd_packed<Tx, Tg, Shape<16, 4, 4>>(a, s);
+    if (glr_vector(a, 4)) return fwd_packed<Tx, Tg, Shape<16, 4, 8>>(a, s);
     if (glr_vector(a, 2)) return fwd_packed<Tx, Tg, Shape<32, 2, 8>>(a, s);
     return fwd_packed<Tx, Tg, Shape<32, 1, 8>>(a, s);
 }

@@ -195,13 +195,13 @@ __device__ __forceinline__ Channel channel(const float* A_log, const float* dt_b
     return {A_log ? -expf(A_log[c]) : 0.f, dt_bias ? dt_bias[c] : 0.f};
 }
 
-// log a of a run's gates, in place.
+// log a of a run's gates, in place; `chan` the parameters of its channels.
 template <int L, int V>
-__device__ __forceinline__ void log_decays(const GlrArgs& a, int c, bool live, float (&la)[L][V]) {
+__device__ __forceinline__ void log_decays(const GlrArgs& a, const Channel* chan, float (&la)[L][V]) {
     if (a.A_log) {
         Channel ch[V];
 #pragma unroll
-        for (int v = 0; v < V; ++v) ch[v] = live ? channel(a.A_log, a.dt_bias, c + v) : Channel{0.f, 0.f};
+        for (int v = 0; v < V; ++v) ch[v] = chan[v];
 #pragma unroll
         for (int j = 0; j < L; ++j) {
             if constexpr (V % 2 == 0) {
@@ -249,7 +249,7 @@ __device__ __forceinline__ void decays(float (&la)[L][V], F f) {
 // tiles' inputs are on the way meanwhile.  Per tile i the two sides meet at two barriers, each of one parity of i:
 //   MAPS   the compute threads have left their runs' maps in shared memory;
 //   CARRY  the carry threads have left the runs' entering states there, and tile i + 3's place in the ring of places.
-// (Its sequence marks follow, in time for CARRY of tile i + 1.)
+// (Its channels' parameters and sequence marks follow, in time for CARRY of tile i + 1.)
 constexpr int kCarryThreads = 64, kPlaces = 8;
 constexpr int kMaps = 1, kCarry = 3;
 
@@ -284,6 +284,17 @@ struct Tickets {
         return t;
     }
 };
+// A block's first three tiles, one ticket after the other, so that every block has its first before any has its second:
+// blocks that take several at once have neighbouring tiles at different places in their queues, and wait for each other's
+// queues (65,536 tokens x 250 channels: 1.2 ms with three at once, 87 us so).
+template <typename Meet>
+__device__ __forceinline__ void first_tiles(const Exchange& x, const GlrArgs& a, int W, bool reverse, Tickets& tickets,
+                                            Tile* tile, bool leader, Meet meet) {
+    if (leader) tile[0] = tile_of(x, a, W, tickets.take(), reverse);
+    meet();
+    if (leader)
+        for (int i = 1; i < 3; ++i) tile[i] = tile_of(x, a, W, tickets.take(), reverse);
+}
 
 // Packed sequences: which one starts, and which ends, at token i of tile p (-1: none).
 // Returns, in every lane, whether there is any among the warp's.

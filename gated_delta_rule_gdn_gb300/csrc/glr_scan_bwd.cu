@@ -36,26 +36,28 @@ glr_bwd_kernel(const GlrArgs a, const Exchange x, float* part) {
     __shared__ unsigned char s_any[2][R];        // bit 0: a sequence starts in the run; bit 1: one ends
     __shared__ int s_start[PACKED ? kPlaces : 1][kTile], s_end[PACKED ? kPlaces : 1][kTile];
     __shared__ bool s_marked[kPlaces][2];        // whether either half of a tile's tokens has a mark
+    __shared__ __align__(16) Channel s_chan[kPlaces][W];
     __shared__ Tile s_tile[kPlaces];
     const int tid = threadIdx.x;
     const auto marked = [&](int i) { return PACKED && (s_marked[i % kPlaces][0] || s_marked[i % kPlaces][1]); };
 
     if (tid >= kThreads) {                       // the carry threads: the gradient's, the state's
         const int ch = (tid - kThreads) % W, side = (tid - kThreads) / W;
-        const auto mark = [&](int slot) {
-            if (!PACKED || s_tile[slot].chain < 0) return;
+        const auto prepare = [&](int slot) {      // a place's channels and marks
+            if (s_tile[slot].chain < 0) return;
+            const int pc = tid - kThreads, c = s_tile[slot].c0 + pc;
+            if (a.A_log && pc < W && c < a.D) s_chan[slot][pc] = channel(a.A_log, a.dt_bias, c);
+            if (!PACKED) return;
             const bool any = sequence_marks(a, s_tile[slot].p, tid - kThreads, s_start[slot], s_end[slot]);
             if (tid % 32 == 0) s_marked[slot][(tid - kThreads) / 32] = any;
         };
         Tickets tickets(x);
         unsigned ticket = 0;
-        if (tid == kThreads) {
-            for (int i = 0; i < 3; ++i) s_tile[i] = tile_of(x, a, W, tickets.take(), true);
-            ticket = tickets.take();
-        }
+        first_tiles(x, a, W, true, tickets, s_tile, tid == kThreads, [] { __syncthreads(); });
+        if (tid == kThreads) ticket = tickets.take();
         __syncwarp();
         S::sync(kMaps);
-        for (int i = 0; i < 3; ++i) mark(i);
+        for (int i = 0; i < 3; ++i) prepare(i);
         __syncthreads();
         // the sums of tile i over its runs, in order
         const auto sums = [&](int i) {
@@ -116,7 +118,7 @@ glr_bwd_kernel(const GlrArgs a, const Exchange x, float* part) {
             if (marked(i)) work(std::bool_constant<PACKED>{}); else work(std::false_type{});
             S::arrive(kCarry + k);
             if (a.dA && i >= 2) sums(i - 2);     // (stage two of tile i - 2 came before the maps of tile i)
-            mark(ahead);
+            prepare(ahead);
         }
         if (a.dA && i > 0) {
             S::sync(kMaps + (i & 1));           // the compute threads are through
@@ -215,7 +217,7 @@ glr_bwd_kernel(const GlrArgs a, const Exchange x, float* part) {
                 for (int v = 0; v < V; ++v) q.u[j][v] *= sigmoid(gi.get(v));
             }
         }
-        log_decays<L, V>(a, c, live, q.la);
+        log_decays<L, V>(a, s_chan[i % kPlaces] + lane * V, q.la);
         decays<L, V>(q.la, [&](int j, int v, const Decay& d) {
             q.al[j][v] = d.a;
             q.e[j][v] = d.e;
@@ -301,7 +303,7 @@ glr_bwd_kernel(const GlrArgs a, const Exchange x, float* part) {
         }
         Channel ch[V];
 #pragma unroll
-        for (int v = 0; v < V; ++v) ch[v] = live ? channel(a.A_log, a.dt_bias, c + v) : Channel{0.f, 0.f};
+        for (int v = 0; v < V; ++v) ch[v] = s_chan[i % kPlaces][lane * V + v];
         const size_t at = ((size_t)t.b * a.T + t0) * a.D + c;
         Tx* dx_p = static_cast<Tx*>(a.dx) + at;
         Tx* di_p = static_cast<Tx*>(a.di) + at;
@@ -400,10 +402,11 @@ glr_bwd_kernel(const GlrArgs a, const Exchange x, float* part) {
             }
     };
 
+    __syncthreads();
+    fetch(0);
     S::arrive(kMaps);
     __syncthreads();
     if (s_tile[0].chain < 0) return;
-    fetch(0);
     fetch(1);
     Held q, before;                              // the current tile's, and the one's before it
     for (int i = 0;; ++i) {
