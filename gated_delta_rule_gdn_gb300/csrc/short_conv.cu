@@ -21,9 +21,10 @@ namespace {
 using mix::bf16;
 using mix::Vec;
 
-// A thread's inputs come through a ring of its own in shared memory, kRing tokens deep, kChunk tokens a copy group.
-constexpr int kWarps = 8, kRun = 32, kChunk = 4, kRing = 16, kThreads = kWarps * 32;
-static_assert(kRing % kChunk == 0 && kRun % kChunk == 0, "whole groups");
+// A thread's inputs come through a ring of its own in shared memory, kRing tokens deep, kChunk tokens a copy group: 16
+// tokens forward; 8 backward, where two rings of 16 leave room for one block less in fp32 (52 and 70 us, B2 T4096 D2048).
+constexpr int kWarps = 8, kChunk = 4, kFwdRing = 16, kBwdRing = 8, kThreads = kWarps * 32;
+static_assert(kFwdRing % kChunk == 0 && kBwdRing % kChunk == 0, "whole groups");
 
 __device__ __forceinline__ float ex2(float x) { float y; asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x)); return y; }
 __device__ __forceinline__ float rcp(float x) { float y; asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x)); return y; }
@@ -150,15 +151,24 @@ __device__ __forceinline__ void state_row(const ConvArgs& a, int64_t r, int c) {
 }
 
 // The grid: for every 32 V channels, the blocks of 8 runs of each batch row, then those of 8 state rows.
-struct Grid { int cols, run_blocks, state_blocks; };
+struct Grid { int cols, run, run_blocks, state_blocks; };
+// Tokens a run: as many as leave 32 warps of 128 channels for each of 152 SMs, since a run's neighbourhood is walked twice
+// (65,536 packed tokens x 4096 channels: forward 185 us with 32 tokens and 172 with 64, backward 408 and 351; 128 gain
+// nothing), and 16 where there are few.
+int run_of(const ConvArgs& a) {
+    for (int run = 64; run > 16; run /= 2)
+        if ((int64_t)a.B * ((a.T + run - 1) / run) * ((a.D + 127) / 128) >= 152 * 32) return run;
+    return 16;
+}
 Grid grid_of(const ConvArgs& a, int V, bool states) {
-    const int runs = (a.T + kRun - 1) / kRun;
+    const int run = run_of(a), runs = (a.T + run - 1) / run;
     const int64_t rows = (int64_t)a.N() * (a.W - 1);
-    return {(a.D + 32 * V - 1) / (32 * V), (runs + kWarps - 1) / kWarps, states ? (int)((rows + kWarps - 1) / kWarps) : 0};
+    return {(a.D + 32 * V - 1) / (32 * V), run, (runs + kWarps - 1) / kWarps, states ? (int)((rows + kWarps - 1) / kWarps) : 0};
 }
 
 template <typename T, int W, int V, bool PACKED>
 __global__ void __launch_bounds__(kThreads) conv_fwd_kernel(const ConvArgs a, const Grid g) {
+    constexpr int kRing = kFwdRing;
     extern __shared__ __align__(16) unsigned char s_raw[];
     auto* ring = reinterpret_cast<Vec<T, V>*>(s_raw) + threadIdx.x;           // [kRing][256]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -170,66 +180,75 @@ __global__ void __launch_bounds__(kThreads) conv_fwd_kernel(const ConvArgs a, co
         if (r < (int64_t)a.N() * (W - 1)) state_row<T, W, V, false>(a, r, c);
         return;
     }
-    const int b = (int)(block / g.run_blocks), t0 = ((int)(block % g.run_blocks) * kWarps + warp) * kRun;
-    const int t1 = min(t0 + kRun, a.T);
+    const int b = (int)(block / g.run_blocks), t0 = ((int)(block % g.run_blocks) * kWarps + warp) * g.run;
+    const int t1 = min(t0 + g.run, a.T);
     if (t0 >= t1) return;
     const size_t row0 = (size_t)b * a.T;
     const T* x = static_cast<const T*>(a.x) + (row0 + t0) * a.ldx + c;
     T* y = static_cast<T*>(a.y) + (row0 + t0) * a.D + c;
-    // copy group m brings tokens t0 + m kChunk ...
-    const auto fetch = [&](int t, int slot) {
-#pragma unroll
-        for (int i = 0; i < kChunk; ++i) {
-            const bool in = t + i < t1;
-            mix::copy_async(ring + (slot + i) * kThreads, in ? x : static_cast<const T*>(a.x), in);
-            x += a.ldx;
-        }
-        mix::copies_close();
-    };
-#pragma unroll
-    for (int m = 0; m < kRing; m += kChunk) fetch(t0 + m, m);
-    Taps<W, V> k;
-    k.load(a, c, true);
     Seq s = sequence_at<PACKED>(a, b, t0);
     float win[W - 1][V];                          // the last W - 1 inputs, oldest first
+    Taps<W, V> k;
+    // CLEAN: a whole run of one sequence, nothing to look out for
+    const auto walk = [&](auto clean) {
+        constexpr bool CLEAN = decltype(clean)::value;
+        const auto fetch = [&](int t, int slot) {
+            if (t < t1) {
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) load_input<T, V>(win[j], a, s, row0, t0 - s.first - (W - 1) + j, c);
-    int slot = 0;
-    for (int t = t0; t < t1; t += kChunk) {
-        mix::copies_wait<kRing / kChunk - 1>();
-#pragma unroll
-        for (int i = 0; i < kChunk; ++i) {
-            if (t + i >= t1) break;
-            if (PACKED && t + i >= s.end) {
-                s = sequence_at<true>(a, b, t + i);
-#pragma unroll
-                for (int j = 0; j < W - 1; ++j) load_input<T, V>(win[j], a, s, row0, j - (W - 1), c);
+                for (int i = 0; i < kChunk; ++i) {
+                    const bool in = CLEAN || t + i < t1;
+                    mix::copy_async(ring + (slot + i) * kThreads, in ? x : static_cast<const T*>(a.x), in);
+                    x += a.ldx;
+                }
             }
-            const Vec<T, V> cur = ring[(slot + i) * kThreads];
-            float xv[V], p[V];
+            mix::copies_close();
+        };
 #pragma unroll
-            for (int v = 0; v < V; ++v) xv[v] = cur.get(v);
-            mix::fma_row(p, k.w[W - 1], xv, k.b);
+        for (int m = 0; m < kRing; m += kChunk) fetch(t0 + m, m);
+        k.load(a, c, true);
 #pragma unroll
-            for (int j = 0; j < W - 1; ++j) mix::fma_row(p, k.w[j], win[j], p);
-            Vec<T, V> o;
+        for (int j = 0; j < W - 1; ++j) load_input<T, V>(win[j], a, s, row0, t0 - s.first - (W - 1) + j, c);
+        int slot = 0;
+#pragma unroll 1
+        for (int t = t0; t < t1; t += kChunk) {
+            mix::copies_wait<kRing / kChunk - 1>();
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                o.set(v, a.silu ? silu(p[v]) : p[v]);
+            for (int i = 0; i < kChunk; ++i) {
+                if (!CLEAN && t + i >= t1) break;
+                if (!CLEAN && PACKED && t + i >= s.end) {
+                    s = sequence_at<true>(a, b, t + i);
 #pragma unroll
-                for (int j = 0; j < W - 2; ++j) win[j][v] = win[j + 1][v];
-                win[W - 2][v] = xv[v];
+                    for (int j = 0; j < W - 1; ++j) load_input<T, V>(win[j], a, s, row0, j - (W - 1), c);
+                }
+                const Vec<T, V> cur = ring[(slot + i) * kThreads];
+                float xv[V], p[V];
+#pragma unroll
+                for (int v = 0; v < V; ++v) xv[v] = cur.get(v);
+                mix::fma_row(p, k.w[W - 1], xv, k.b);
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j) mix::fma_row(p, k.w[j], win[j], p);
+                Vec<T, V> o;
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    o.set(v, a.silu ? silu(p[v]) : p[v]);
+#pragma unroll
+                    for (int j = 0; j < W - 2; ++j) win[j][v] = win[j + 1][v];
+                    win[W - 2][v] = xv[v];
+                }
+                o.store(y);
+                y += a.D;
             }
-            o.store(y);
-            y += a.D;
+            fetch(t + kRing, slot);
+            slot = slot + kChunk == kRing ? 0 : slot + kChunk;
         }
-        fetch(t + kRing, slot);
-        slot = slot + kChunk == kRing ? 0 : slot + kChunk;
-    }
+    };
+    if (t0 + g.run <= (PACKED ? min(s.end, a.T) : a.T)) walk(std::true_type{});
+    else walk(std::false_type{});
 }
 
 template <typename T, int W, int V, bool PACKED>
 __global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(const ConvArgs a, const Grid g, float* part) {
+    constexpr int kRing = kBwdRing;
     extern __shared__ __align__(16) unsigned char s_raw[];
     auto* rx = reinterpret_cast<Vec<T, V>*>(s_raw) + threadIdx.x;             // [kRing][256] each
     auto* ry = rx + kRing * kThreads;
@@ -242,8 +261,8 @@ __global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(const ConvArgs a,
         if (live && r < (int64_t)a.N() * (W - 1)) state_row<T, W, V, true>(a, r, c);
         return;
     }
-    const int b = (int)(block / g.run_blocks), t0 = ((int)(block % g.run_blocks) * kWarps + warp) * kRun;
-    const int t1 = live ? min(t0 + kRun, a.T) : t0;            // the run's tokens
+    const int b = (int)(block / g.run_blocks), t0 = ((int)(block % g.run_blocks) * kWarps + warp) * g.run;
+    const int t1 = live ? min(t0 + g.run, a.T) : t0;            // the run's tokens
     const int t2 = min(t1 + W - 1, a.T);                       // and those whose ds they need
     const size_t row0 = (size_t)b * a.T;
     float dw[W + 1][V];                                        // the taps', then the bias's
@@ -255,51 +274,54 @@ __global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(const ConvArgs a,
         const T* x = static_cast<const T*>(a.x) + (row0 + t0) * a.ldx + c;
         const T* dy = static_cast<const T*>(a.dy) + (row0 + t0) * a.D + c;
         T* dx = static_cast<T*>(a.dx) + (row0 + t0) * a.D + c;
-        const auto fetch = [&](int t, int slot) {
-#pragma unroll
-            for (int i = 0; i < kChunk; ++i) {
-                const bool in = t + i < t2;
-                mix::copy_async(rx + (slot + i) * kThreads, in ? x : static_cast<const T*>(a.x), in);
-                mix::copy_async(ry + (slot + i) * kThreads, in ? dy : static_cast<const T*>(a.dy), in);
-                x += a.ldx;
-                dy += a.D;
-            }
-            mix::copies_close();
-        };
-#pragma unroll
-        for (int m = 0; m < kRing; m += kChunk) fetch(t0 + m, m);
         Taps<W, V> k;
-        k.load(a, c, true);
         Seq s = sequence_at<PACKED>(a, b, t0);
         float win[W - 1][V], ds[W - 1][V];                     // the last W - 1 inputs and ds, oldest first
         int end[W - 1], own[W - 1];                            // the sequences of the last W - 1 tokens
+        // CLEAN: a whole run of one sequence, and the tokens behind it that it needs too
+        const auto walk = [&](auto clean) {
+            constexpr bool CLEAN = decltype(clean)::value;
+            const auto fetch = [&](int t, int slot) {
+                if (t < t2) {
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j) {
-            load_input<T, V>(win[j], a, s, row0, t0 - s.first - (W - 1) + j, c);
-            end[j] = s.end;
-            own[j] = s.n;
+                    for (int i = 0; i < kChunk; ++i) {
+                        const bool in = t + i < t2;
+                        mix::copy_async(rx + (slot + i) * kThreads, in ? x : static_cast<const T*>(a.x), in);
+                        mix::copy_async(ry + (slot + i) * kThreads, in ? dy : static_cast<const T*>(a.dy), in);
+                        x += a.ldx;
+                        dy += a.D;
+                    }
+                }
+                mix::copies_close();
+            };
 #pragma unroll
-            for (int v = 0; v < V; ++v) ds[j][v] = 0.f;
-        }
-        // token t brings ds_t; dx of token t - (W - 1) is then complete (past the row's end ds is 0)
-        int slot = 0;
-        for (int t = t0; t < t1 + W - 1; t += kChunk) {
-            mix::copies_wait<kRing / kChunk - 1>();
+            for (int m = 0; m < kRing; m += kChunk) fetch(t0 + m, m);
+            k.load(a, c, true);
 #pragma unroll
-            for (int i = 0; i < kChunk; ++i) {
-                const int now = t + i, out = now - (W - 1);
-                if (now >= t1 + W - 1) break;
-                if (PACKED && now >= s.end && now < a.T) {
+            for (int j = 0; j < W - 1; ++j) {
+                load_input<T, V>(win[j], a, s, row0, t0 - s.first - (W - 1) + j, c);
+                end[j] = s.end;
+                own[j] = s.n;
+#pragma unroll
+                for (int v = 0; v < V; ++v) ds[j][v] = 0.f;
+            }
+            // Token `now` brings ds; dx of token now - (W - 1) is then complete.  INSIDE: the token is of the run (else
+            // one behind it, whose ds the run's last tokens need; past the row's end ds is 0).
+            const auto token = [&](int now, int at, auto inside) {
+                constexpr bool INSIDE = decltype(inside)::value;
+                const int out = now - (W - 1);
+                if (!CLEAN && PACKED && now >= s.end && now < a.T) {
                     s = sequence_at<true>(a, b, now);
 #pragma unroll
                     for (int j = 0; j < W - 1; ++j) load_input<T, V>(win[j], a, s, row0, j - (W - 1), c);
                 }
-                const Vec<T, V> cx = rx[(slot + i) * kThreads], cy = ry[(slot + i) * kThreads];
                 float xv[V], p[V], d[V];
+                const bool there = CLEAN || now < t2;          // (what is not was not copied)
+                const Vec<T, V> cx = rx[at * kThreads], cy = ry[at * kThreads];
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    xv[v] = cx.get(v);
-                    d[v] = cy.get(v);
+                    xv[v] = there ? cx.get(v) : 0.f;
+                    d[v] = there ? cy.get(v) : 0.f;
                 }
                 if (a.silu) {
                     mix::fma_row(p, k.w[W - 1], xv, k.b);
@@ -309,10 +331,10 @@ __global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(const ConvArgs a,
                     for (int v = 0; v < V; ++v) p[v] = silu_slope(p[v]);
                     mix::mul_row(d, d, p);
                 }
-                if (now >= a.T)
+                if (!CLEAN && now >= a.T)
 #pragma unroll
                     for (int v = 0; v < V; ++v) d[v] = 0.f;
-                if (now < t1) {
+                if (INSIDE) {
 #pragma unroll
                     for (int j = 0; j < W - 1; ++j) mix::fma_row(dw[j], d, win[j], dw[j]);
                     mix::fma_row(dw[W - 1], d, xv, dw[W - 1]);
@@ -321,10 +343,10 @@ __global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(const ConvArgs a,
                 }
                 if (out >= t0) {
                     // ds at out .. out + reach - 1 belong to the token's sequence; that of out + m meets tap W - 1 - m
-                    const int reach = (PACKED ? end[0] : a.T) - out;
+                    const int reach = CLEAN ? W : (PACKED ? end[0] : a.T) - out;
                     float gx[V];
                     mix::mul_row(gx, k.w[W - 1], ds[0]);
-                    if (!PACKED || reach >= W) {
+                    if (CLEAN || !PACKED || reach >= W) {
 #pragma unroll
                         for (int m = 1; m < W - 1; ++m) mix::fma_row(gx, k.w[W - 1 - m], ds[m], gx);
                         mix::fma_row(gx, k.w[0], d, gx);
@@ -334,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(const ConvArgs a,
                             if (m < reach) mix::fma_row(gx, k.w[W - 1 - m], ds[m], gx);
                     }
                     const int tail = W - 1 - reach;            // its place in its sequence's final state
-                    if (a.dhT && tail >= 0) {
+                    if (!CLEAN && a.dhT && tail >= 0) {
                         float e[V];
                         const int n = PACKED ? own[0] : b;
                         load_row<T, V>(e, static_cast<const T*>(a.dhT) + ((size_t)n * (W - 1) + tail) * a.D + c, true);
@@ -364,10 +386,30 @@ __global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(const ConvArgs a,
                 }
                 end[W - 2] = s.end;
                 own[W - 2] = s.n;
+            };
+            int slot = 0, t = t0;
+#pragma unroll 1
+            for (; CLEAN ? t < t1 : t + kChunk <= t1; t += kChunk) {
+                mix::copies_wait<kRing / kChunk - 1>();
+#pragma unroll
+                for (int i = 0; i < kChunk; ++i) token(t + i, slot + i, std::true_type{});
+                fetch(t + kRing, slot);
+                slot = slot + kChunk == kRing ? 0 : slot + kChunk;
             }
-            fetch(t + kRing, slot);
-            slot = slot + kChunk == kRing ? 0 : slot + kChunk;
-        }
+            mix::copies_wait<0>();
+#pragma unroll 1
+            for (; t < t1; ++t) {                              // (a row's end inside a group)
+                token(t, slot, std::true_type{});
+                slot = slot + 1 == kRing ? 0 : slot + 1;
+            }
+#pragma unroll 1
+            for (; t < t1 + W - 1; ++t) {
+                token(t, slot, std::false_type{});
+                slot = slot + 1 == kRing ? 0 : slot + 1;
+            }
+        };
+        if (t0 + g.run + W <= (PACKED ? min(s.end, a.T) : a.T)) walk(std::true_type{});
+        else walk(std::false_type{});
     }
     mix::copies_wait<0>();
     __syncthreads();
@@ -485,7 +527,7 @@ cudaError_t launch_conv_fwd(const ConvArgs& a, cudaStream_t s) {
             const Grid g = grid_of(a, v.value, a.hT != nullptr);
             const unsigned blocks = (unsigned)(g.cols * ((int64_t)a.B * g.run_blocks + g.state_blocks));
             if (blocks == 0) return;
-            const size_t smem = (size_t)kRing * kThreads * v.value * sizeof(T);
+            const size_t smem = (size_t)kFwdRing * kThreads * v.value * sizeof(T);
             const auto kernel = a.cu ? conv_fwd_kernel<T, w.value, v.value, true> : conv_fwd_kernel<T, w.value, v.value, false>;
             e = allow_smem(reinterpret_cast<const void*>(kernel), smem);
             if (e == cudaSuccess) kernel<<<blocks, kThreads, smem, s>>>(a, g);
@@ -505,7 +547,7 @@ cudaError_t launch_conv_bwd(const ConvArgs& a, cudaStream_t s) {
             rows = (int64_t)a.B * g.run_blocks;
             const unsigned blocks = (unsigned)(g.cols * (rows + g.state_blocks));
             if (blocks == 0) return;
-            const size_t rings = 2 * (size_t)kRing * kThreads * v.value * sizeof(T);
+            const size_t rings = 2 * (size_t)kBwdRing * kThreads * v.value * sizeof(T);
             const size_t sums = (size_t)kWarps * (w.value + 1) * 32 * v.value * sizeof(float);
             const size_t smem = rings > sums ? rings : sums;
             const auto kernel = a.cu ? conv_bwd_kernel<T, w.value, v.value, true> : conv_bwd_kernel<T, w.value, v.value, false>;
