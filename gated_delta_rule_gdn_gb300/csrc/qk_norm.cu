@@ -5,8 +5,9 @@
 // Backward: dy = the output's gradient turned back, dw = sum dy x r, e = w dy, dx = r (e - c r^2 x sum(x e)).
 // Bound by HBM: every head is read once and written once (backward: read with its gradient, written once).
 //
-// Vector kernels: G neighbouring lanes hold a head, E = 8 or 4 channels each, and a group of lanes takes `kHeads` heads of one
-// token, so that the token's angles are read once for them and their loads are under way together.  The rotation's
+// Vector kernels: G neighbouring lanes hold a head, E = 8 or 4 channels each, and a group of lanes takes N heads of one token,
+// so that the token's angles are read once for them.  Blocks are persistent; each thread's inputs of the next shares come
+// through kSlots slots of its own in shared memory, so that loads are under way all the time.  The rotation's
 // partner is in the same lane (interleaved), or in the lane rot / 2E away.  Heads whose size, rotation or alignment
 // does not go in steps of 4 channels take the scalar kernels, a warp per head.
 
@@ -22,7 +23,7 @@ using mix::bf16;
 using mix::ld;
 using mix::st;
 
-constexpr int kMaxD = 256, kThreads = 256, kHeads = 4;
+constexpr int kMaxD = 256, kThreads = 256;
 
 __device__ __forceinline__ int position(const QkNormArgs& a, int64_t tok) {
     const int p = a.pos ? a.pos[tok] : (int)((unsigned)tok % (unsigned)a.T);    // (tokens times heads fit 31 bits)
@@ -39,8 +40,9 @@ __device__ __forceinline__ float group_sum(float v) {
 // E channels in accesses of at most 16 bytes
 template <typename T, int E>
 struct Chunk {
-    static constexpr int N = sizeof(T) * E > 16 ? 16 / sizeof(T) : E;
-    mix::Vec<T, N> v[E / N];
+    static constexpr int N = sizeof(T) * E > 16 ? 16 / sizeof(T) : E, kParts = E / N;
+    using Part = mix::Vec<T, N>;
+    Part v[kParts];
     __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
         for (int i = 0; i < E / N; ++i) v[i].load(p + i * N);
@@ -107,117 +109,169 @@ struct Angles {
     }
 };
 
-// A group's share of the work: kHeads heads of q, or of k, of one token.  The token's shares are those of q, then of k.
+// A group's share of the work: up to N heads of q, or of k, of one token.  The token's shares are those of q, then of k.
 struct Shares { unsigned of_q, all; };
-template <typename T, int E, int G>
+template <typename T, int E, int G, int N>
 struct Share {
     unsigned tok;
     int which, count, j0;             // tensor, heads, the lane's first channel
     const T* x;                       // the lane's channels of the first head in the input, and the same in contiguous
     size_t at;                        // tensors
-    bool in;                          // the lane's channels exist
     int64_t step;                     // between the input's heads
-    __device__ __forceinline__ Share(const QkNormArgs& a, const Shares& sh, unsigned item) {
+    // (a share past the last has no heads)
+    __device__ __forceinline__ Share(const QkNormArgs& a, const Shares& sh, unsigned item, unsigned items) {
+        const bool real = item < items;
+        if (!real) item = items - 1;
         tok = item / sh.all;
         unsigned part = item - tok * sh.all;
         which = part >= sh.of_q;
         if (which) part -= sh.of_q;
-        const int h = (int)part * kHeads, H = which ? a.H[1] : a.H[0];
-        count = min(H - h, kHeads);
+        const int h = (int)part * N, H = which ? a.H[1] : a.H[0];
         j0 = (int)(threadIdx.x % G) * E;
-        in = j0 < a.d;
+        count = real && j0 < a.d ? min(H - h, N) : 0;
         step = which ? a.head_stride[1] : a.head_stride[0];
         x = static_cast<const T*>(which ? a.in[1] : a.in[0]) + (int64_t)tok * (which ? a.tok_stride[1] : a.tok_stride[0]) +
             h * step + j0;
         at = ((size_t)tok * H + h) * a.d + j0;
     }
 };
-
-template <typename T, int E, int G, int ROT>
-__global__ void __launch_bounds__(kThreads) qk_fwd_kernel(const QkNormArgs a, const Shares sh, const unsigned items) {
-    const unsigned item = blockIdx.x * (kThreads / G) + threadIdx.x / G;
-    const Share<T, E, G> w(a, sh, min(item, items - 1));            // (the last block repeats the last share)
-    Chunk<T, E> x[kHeads];
+template <typename T, int E>
+__device__ __forceinline__ void copy_chunk(Chunk<T, E>* dst, int pitch, const T* src, bool in, const void* any) {
 #pragma unroll
-    for (int i = 0; i < kHeads; ++i)
-        if (w.in && i < w.count) x[i].load(w.x + i * w.step); else x[i].zero();
-    Angles<E, ROT> ang;
-    if (ROT != kNone) ang.load(a, position(a, w.tok), (int)threadIdx.x % G);
-    const float* wt = w.which ? a.w[1] : a.w[0];
-    float weight[E];
+    for (int i = 0; i < Chunk<T, E>::kParts; ++i)
+        mix::copy_async(reinterpret_cast<typename Chunk<T, E>::Part*>(dst) + i * pitch,
+                        in ? src + i * Chunk<T, E>::N : static_cast<const T*>(any), in);
+}
+template <typename T, int E>
+__device__ __forceinline__ Chunk<T, E> read_chunk(const Chunk<T, E>* src, int pitch) {
+    Chunk<T, E> c;
 #pragma unroll
-    for (int e = 0; e < E; ++e) weight[e] = wt && w.in ? wt[w.j0 + e] : 1.f;
-    T* y = static_cast<T*>(w.which ? a.out[1] : a.out[0]) + w.at;
-#pragma unroll
-    for (int i = 0; i < kHeads; ++i) {
-        float v[E], ss = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            v[e] = x[i].get(e);
-            ss = fmaf(v[e], v[e], ss);
-        }
-        const float r = rsqrtf(fmaf(a.c, group_sum<G>(ss), a.eps));
-#pragma unroll
-        for (int e = 0; e < E; ++e) v[e] *= r * weight[e];
-        ang.template turn<G>(v, 1.f);
-#pragma unroll
-        for (int e = 0; e < E; ++e) x[i].set(e, v[e]);
-        if (w.in && i < w.count) x[i].store(y);
-        y += a.d;
-    }
+    for (int i = 0; i < Chunk<T, E>::kParts; ++i) c.v[i] = reinterpret_cast<const typename Chunk<T, E>::Part*>(src)[i * pitch];
+    return c;
 }
 
-// persistent blocks: the weight gradients of a block's heads stay in registers and leave as one row of partial sums
-template <typename T, int E, int G, int ROT>
-__global__ void __launch_bounds__(kThreads, 2) qk_bwd_kernel(const QkNormArgs a, const Shares sh, const unsigned items,
-                                                             float* part) {
-    constexpr int kGroups = kThreads / G;
-    __shared__ float sw[2][kGroups][G * E];
-    float acc[2][E] = {};
-    for (unsigned base = blockIdx.x * kGroups; base < items; base += gridDim.x * kGroups) {
-        const unsigned item = base + threadIdx.x / G;
-        const Share<T, E, G> w(a, sh, min(item, items - 1));
-        const int count = item < items && w.in ? w.count : 0;
-        Chunk<T, E> x[kHeads], dz[kHeads];
-        const T* dp = static_cast<const T*>(w.which ? a.dout[1] : a.dout[0]) + w.at;
+// Without rotation there is little to wait for but the heads: a block for every share is then faster than persistent ones
+// (16,384 tokens x 32 heads of 128: 43 and 52 us); with it the angles' latency is worth hiding (16,384 tokens x 40 heads: 78 us
+// with a block for every share, 68 us so).
+template <int ROT> constexpr int kSlots = ROT == kNone ? 1 : 2;
+constexpr int kBwdSlots = 2;
+
+template <typename T, int E, int G, int ROT, int N>
+__global__ void __launch_bounds__(kThreads) qk_fwd_kernel(const QkNormArgs a, const Shares sh, const unsigned items) {
+    using C = Chunk<T, E>;
+    constexpr unsigned kGroups = kThreads / G;
+    extern __shared__ __align__(16) unsigned char s_raw[];
+    auto* buf = reinterpret_cast<typename C::Part*>(s_raw) + threadIdx.x;     // [slots][N][parts][256]
+    const auto slot = [&](int k, int i) { return reinterpret_cast<C*>(buf + ((k * N + i) * C::kParts) * kThreads); };
+    const unsigned stride = gridDim.x * kGroups, first = blockIdx.x * kGroups + threadIdx.x / G;
+    const auto fetch = [&](unsigned item, int k) {
+        const Share<T, E, G, N> w(a, sh, item, items);
 #pragma unroll
-        for (int i = 0; i < kHeads; ++i) {
-            if (i < count) x[i].load(w.x + i * w.step); else x[i].zero();
-            if (i < count) dz[i].load(dp + (size_t)i * a.d); else dz[i].zero();
-        }
+        for (int i = 0; i < N; ++i) copy_chunk<T, E>(slot(k, i), kThreads, w.x + i * w.step, i < w.count, a.in[0]);
+        mix::copies_close();
+    };
+#pragma unroll
+    for (int k = 0; k < kSlots<ROT>; ++k) fetch(first + k * stride, k);
+    int k = 0;
+    // (all groups of a block go round as often as its first)
+    for (unsigned item = first, base = blockIdx.x * kGroups; base < items; item += stride, base += stride) {
+        const Share<T, E, G, N> w(a, sh, item, items);
         Angles<E, ROT> ang;
         if (ROT != kNone) ang.load(a, position(a, w.tok), (int)threadIdx.x % G);
         const float* wt = w.which ? a.w[1] : a.w[0];
-        T* out = static_cast<T*>(w.which ? a.out[1] : a.out[0]) + w.at;
-        float sum[E] = {};
+        float weight[E];
 #pragma unroll
-        for (int i = 0; i < kHeads; ++i) {
+        for (int e = 0; e < E; ++e) weight[e] = wt && w.count > 0 ? wt[w.j0 + e] : 1.f;
+        T* y = static_cast<T*>(w.which ? a.out[1] : a.out[0]) + w.at;
+        mix::copies_wait<kSlots<ROT> - 1>();
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            C x = read_chunk<T, E>(slot(k, i), kThreads);
+            float v[E], ss = 0.f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                v[e] = x.get(e);
+                ss = fmaf(v[e], v[e], ss);
+            }
+            const float r = rsqrtf(fmaf(a.c, group_sum<G>(ss), a.eps));
+#pragma unroll
+            for (int e = 0; e < E; ++e) v[e] *= r * weight[e];
+            ang.template turn<G>(v, 1.f);
+#pragma unroll
+            for (int e = 0; e < E; ++e) x.set(e, v[e]);
+            if (i < w.count) x.store(y);
+            y += a.d;
+        }
+        fetch(item + kSlots<ROT> * stride, k);
+        k = k + 1 == kSlots<ROT> ? 0 : k + 1;
+    }
+}
+
+// The weight gradients of a block's heads stay in registers and leave as one row of partial sums.
+template <typename T, int E, int G, int ROT, int N>
+__global__ void __launch_bounds__(kThreads, 2) qk_bwd_kernel(const QkNormArgs a, const Shares sh, const unsigned items,
+                                                             float* part) {
+    using C = Chunk<T, E>;
+    constexpr unsigned kGroups = kThreads / G;
+    extern __shared__ __align__(16) unsigned char s_raw[];
+    auto* buf = reinterpret_cast<typename C::Part*>(s_raw) + threadIdx.x;     // [kBwdSlots][N][x, dz][parts][256]
+    const auto slot = [&](int k, int i, int z) {
+        return reinterpret_cast<C*>(buf + (((k * N + i) * 2 + z) * C::kParts) * kThreads);
+    };
+    const unsigned stride = gridDim.x * kGroups, first = blockIdx.x * kGroups + threadIdx.x / G;
+    const auto fetch = [&](unsigned item, int k) {
+        const Share<T, E, G, N> w(a, sh, item, items);
+        const T* dp = static_cast<const T*>(w.which ? a.dout[1] : a.dout[0]) + w.at;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            copy_chunk<T, E>(slot(k, i, 0), kThreads, w.x + i * w.step, i < w.count, a.in[0]);
+            copy_chunk<T, E>(slot(k, i, 1), kThreads, dp + (size_t)i * a.d, i < w.count, a.in[0]);
+        }
+        mix::copies_close();
+    };
+#pragma unroll
+    for (int k = 0; k < kBwdSlots; ++k) fetch(first + k * stride, k);
+    float acc[2][E] = {};
+    int k = 0;
+    for (unsigned item = first, base = blockIdx.x * kGroups; base < items; item += stride, base += stride) {
+        const Share<T, E, G, N> w(a, sh, item, items);
+        Angles<E, ROT> ang;
+        if (ROT != kNone) ang.load(a, position(a, w.tok), (int)threadIdx.x % G);
+        const float* wt = w.which ? a.w[1] : a.w[0];
+        float weight[E], sum[E] = {};
+#pragma unroll
+        for (int e = 0; e < E; ++e) weight[e] = wt && w.count > 0 ? wt[w.j0 + e] : 1.f;
+        T* out = static_cast<T*>(w.which ? a.out[1] : a.out[0]) + w.at;
+        mix::copies_wait<kBwdSlots - 1>();
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            C x = read_chunk<T, E>(slot(k, i, 0), kThreads);
+            const C dz = read_chunk<T, E>(slot(k, i, 1), kThreads);
             float e[E], v[E], ss = 0.f, xe = 0.f;
 #pragma unroll
             for (int c = 0; c < E; ++c) {
-                e[c] = dz[i].get(c);
-                v[c] = x[i].get(c);
+                e[c] = dz.get(c);
+                v[c] = x.get(c);
                 ss = fmaf(v[c], v[c], ss);
             }
             ang.template turn<G>(e, -1.f);
             const float r = rsqrtf(fmaf(a.c, group_sum<G>(ss), a.eps));
 #pragma unroll
-            for (int c = 0; c < E; ++c) v[c] *= r;
-            if (wt) {
-#pragma unroll
-                for (int c = 0; c < E; ++c) {
-                    sum[c] = fmaf(e[c], v[c], sum[c]);
-                    e[c] *= w.in ? wt[w.j0 + c] : 0.f;
-                }
+            for (int c = 0; c < E; ++c) {
+                v[c] *= r;
+                sum[c] = fmaf(e[c], v[c], sum[c]);
+                e[c] *= weight[c];
+                xe = fmaf(v[c], e[c], xe);
             }
-#pragma unroll
-            for (int c = 0; c < E; ++c) xe = fmaf(v[c], e[c], xe);
             xe = group_sum<G>(xe) * a.c;
 #pragma unroll
-            for (int c = 0; c < E; ++c) x[i].set(c, r * fmaf(-v[c], xe, e[c]));
-            if (i < count) x[i].store(out);
+            for (int c = 0; c < E; ++c) x.set(c, r * fmaf(-v[c], xe, e[c]));
+            if (i < w.count) x.store(out);
             out += a.d;
         }
+        fetch(item + kBwdSlots * stride, k);
+        k = k + 1 == kBwdSlots ? 0 : k + 1;
+        // (heads that a share does not have were copied as zeros and add nothing)
 #pragma unroll
         for (int c = 0; c < E; ++c) {
             acc[0][c] += w.which ? 0.f : sum[c];
@@ -225,6 +279,9 @@ __global__ void __launch_bounds__(kThreads, 2) qk_bwd_kernel(const QkNormArgs a,
         }
     }
     if (!part) return;
+    mix::copies_wait<0>();
+    __syncthreads();
+    auto& sw = *reinterpret_cast<float(*)[2][kGroups][G * E]>(s_raw);         // (the slots are done with)
     const int g = threadIdx.x / G, lane = threadIdx.x % G;
 #pragma unroll
     for (int c = 0; c < E; ++c) {
@@ -234,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 2) qk_bwd_kernel(const QkNormArgs a,
     __syncthreads();
     for (int j = threadIdx.x; j < 2 * a.d; j += kThreads) {
         float s = 0.f;
-        for (int i = 0; i < kGroups; ++i) s += sw[j / a.d][i][j % a.d];
+        for (unsigned i = 0; i < kGroups; ++i) s += sw[j / a.d][i][j % a.d];
         part[(size_t)blockIdx.x * 2 * a.d + j] = s;
     }
 }
@@ -401,11 +458,17 @@ int channels_a_lane(const QkNormArgs& a, bool backward) {
     return 0;
 }
 
-constexpr int kBwdBlocks = 152 * 2;
-Shares shares_of(const QkNormArgs& a) {
-    const unsigned q = (a.H[0] + kHeads - 1) / kHeads, k = (a.H[1] + kHeads - 1) / kHeads;
+constexpr unsigned kFwdBlocks = 152 * 4, kBwdBlocks = 152 * 2;
+Shares shares_of(const QkNormArgs& a, int N) {
+    const unsigned q = (a.H[0] + N - 1) / N, k = (a.H[1] + N - 1) / N;
     return {q, q + k};
 }
+cudaError_t allow_smem(const void* kernel, size_t bytes) {
+    return bytes > 48 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes)
+                             : cudaSuccess;
+}
+constexpr int kFwdHeads = 4;
+template <typename T> constexpr int kBwdHeads = sizeof(T) == 2 ? 4 : 2;       // (two inputs, 64 KB of slots a block)
 
 // f(channels a lane, group size, rotation) as compile-time constants
 template <typename F>
@@ -427,12 +490,17 @@ void by_shape(const QkNormArgs& a, int E, F f) {
 template <typename T>
 cudaError_t fwd(const QkNormArgs& a, cudaStream_t s) {
     if (const int E = channels_a_lane(a, false)) {
-        const Shares sh = shares_of(a);
+        const Shares sh = shares_of(a, kFwdHeads);
         const unsigned items = (unsigned)(a.n * sh.all);         // (at most tokens times heads, which fits)
+        cudaError_t err = cudaSuccess;
         by_shape(a, E, [&](auto e, auto g, auto rot) {
-            const unsigned per = kThreads / g.value;
-            qk_fwd_kernel<T, e.value, g.value, rot.value><<<(items + per - 1) / per, kThreads, 0, s>>>(a, sh, items);
+            const unsigned per = kThreads / g.value, want = (items + per - 1) / per;
+            const auto kernel = qk_fwd_kernel<T, e.value, g.value, rot.value, kFwdHeads>;
+            const size_t smem = (size_t)kSlots<rot.value> * kFwdHeads * kThreads * e.value * sizeof(T);
+            err = allow_smem(reinterpret_cast<const void*>(kernel), smem);
+            if (err == cudaSuccess) kernel<<<rot.value == kNone || want < kFwdBlocks ? want : kFwdBlocks, kThreads, smem, s>>>(a, sh, items);
         });
+        if (err != cudaSuccess) return err;
     } else {
         const int64_t rows = a.n * (a.H[0] + a.H[1]);
         qk_fwd_any_kernel<T><<<(unsigned)((rows + kWarps - 1) / kWarps), kThreads, 0, s>>>(a);
@@ -447,16 +515,23 @@ cudaError_t bwd(const QkNormArgs& a, cudaStream_t s) {
     int blocks = 0;                            // none without tokens: the weight gradients are then zero
     const int E = a.n > 0 ? channels_a_lane(a, true) : 0;
     if (E > 0) {
-        const Shares sh = shares_of(a);
+        constexpr int N = kBwdHeads<T>;
+        const Shares sh = shares_of(a, N);
         const unsigned items = (unsigned)(a.n * sh.all);
+        cudaError_t err = cudaSuccess;
         by_shape(a, E, [&](auto e, auto g, auto rot) {
             const unsigned per = kThreads / g.value, want = (items + per - 1) / per;
             blocks = (int)(want < kBwdBlocks ? want : kBwdBlocks);
-            qk_bwd_kernel<T, e.value, g.value, rot.value><<<blocks, kThreads, 0, s>>>(a, sh, items, part);
+            const auto kernel = qk_bwd_kernel<T, e.value, g.value, rot.value, N>;
+            const size_t slots = 2 * (size_t)kBwdSlots * N * kThreads * e.value * sizeof(T);
+            const size_t sums = 2 * (size_t)kThreads * e.value * sizeof(float), smem = slots > sums ? slots : sums;
+            err = allow_smem(reinterpret_cast<const void*>(kernel), smem);
+            if (err == cudaSuccess) kernel<<<blocks, kThreads, smem, s>>>(a, sh, items, part);
         });
+        if (err != cudaSuccess) return err;
     } else if (a.n > 0) {
         const int64_t want = (a.n * (a.H[0] + a.H[1]) + kWarps - 1) / kWarps;
-        blocks = (int)(want < kBwdBlocks ? want : kBwdBlocks);
+        blocks = (int)(want < (int64_t)kBwdBlocks ? want : (int64_t)kBwdBlocks);
         qk_bwd_any_kernel<T><<<blocks, kThreads, 0, s>>>(a, part);
     }
     if (weights) qk_dw_kernel<<<(2 * a.d + 7) / 8, 256, 0, s>>>(part, blocks, a.d, a.dw[0], a.dw[1]);
@@ -467,7 +542,7 @@ cudaError_t bwd(const QkNormArgs& a, cudaStream_t s) {
 
 size_t qk_norm_workspace_bytes(const QkNormArgs& a) {
     const int64_t want = (a.n * (a.H[0] + a.H[1]) + 7) / 8;          // at least the blocks of either kernel
-    return (size_t)(want < kBwdBlocks ? want : kBwdBlocks) * 2 * a.d * sizeof(float);
+    return (size_t)(want < (int64_t)kBwdBlocks ? want : (int64_t)kBwdBlocks) * 2 * a.d * sizeof(float);
 }
 cudaError_t launch_qk_norm_fwd(const QkNormArgs& a, cudaStream_t s) { return a.bf16 ? fwd<bf16>(a, s) : fwd<float>(a, s); }
 cudaError_t launch_qk_norm_bwd(const QkNormArgs& a, cudaStream_t s) { return a.bf16 ? bwd<bf16>(a, s) : bwd<float>(a, s); }

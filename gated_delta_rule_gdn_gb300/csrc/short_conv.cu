@@ -359,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(const ConvArgs a,
                     if (!CLEAN && a.dhT && tail >= 0) {
                         float e[V];
                         const int n = PACKED ? own[0] : b;
-                        load_row<T, V>(e, static_cast<const T*>(a.dhT) + ((size_t)n * (W - 1) + tail) * a.D + c, true);
+                        load_row<T, V>(e, static_cast<const T*>(a.dhT) + ((int64_t)n * (W - 1) + tail) * a.D + c, true);
 #pragma unroll
                         for (int v = 0; v < V; ++v) gx[v] += e[v];
                     }
