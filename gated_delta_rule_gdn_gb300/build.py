@@ -51,7 +51,7 @@ def _native_command(out: str) -> list:
             "-I", include, "-I", os.path.join(include, "torch", "csrc", "api", "include"),
             "-I", os.path.join(cuda, "include"), "-I", sysconfig.get_paths()["include"],
             os.path.join(CSRC, "torch_binding.cpp"), "-o", out, "-L", os.path.join(torch, "lib"),
-            "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python"]
+            "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch", "-ltorch_python"]
 
 
 def _deps():

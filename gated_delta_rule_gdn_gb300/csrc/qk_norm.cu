@@ -469,6 +469,12 @@ cudaError_t allow_smem(const void* kernel, size_t bytes) {
 }
 constexpr int kFwdHeads = 4;
 template <typename T> constexpr int kBwdHeads = sizeof(T) == 2 ? 4 : 2;       // (two inputs, 64 KB of slots a block)
+// Heads a share: as above, or one where neither tensor has as many as half of that.
+template <int N, typename F>
+void by_heads(const QkNormArgs& a, F f) {
+    if (2 * a.H[0] <= N && 2 * a.H[1] <= N) f(std::integral_constant<int, 1>{});
+    else f(std::integral_constant<int, N>{});
+}
 
 // f(channels a lane, group size, rotation) as compile-time constants
 template <typename F>
@@ -490,15 +496,18 @@ void by_shape(const QkNormArgs& a, int E, F f) {
 template <typename T>
 cudaError_t fwd(const QkNormArgs& a, cudaStream_t s) {
     if (const int E = channels_a_lane(a, false)) {
-        const Shares sh = shares_of(a, kFwdHeads);
-        const unsigned items = (unsigned)(a.n * sh.all);         // (at most tokens times heads, which fits)
         cudaError_t err = cudaSuccess;
-        by_shape(a, E, [&](auto e, auto g, auto rot) {
-            const unsigned per = kThreads / g.value, want = (items + per - 1) / per;
-            const auto kernel = qk_fwd_kernel<T, e.value, g.value, rot.value, kFwdHeads>;
-            const size_t smem = (size_t)kSlots<rot.value> * kFwdHeads * kThreads * e.value * sizeof(T);
-            err = allow_smem(reinterpret_cast<const void*>(kernel), smem);
-            if (err == cudaSuccess) kernel<<<rot.value == kNone || want < kFwdBlocks ? want : kFwdBlocks, kThreads, smem, s>>>(a, sh, items);
+        by_heads<kFwdHeads>(a, [&](auto heads) {
+            const Shares sh = shares_of(a, heads.value);
+            const unsigned items = (unsigned)(a.n * sh.all);     // (at most tokens times heads, which fits)
+            by_shape(a, E, [&](auto e, auto g, auto rot) {
+                const unsigned per = kThreads / g.value, want = (items + per - 1) / per;
+                const auto kernel = qk_fwd_kernel<T, e.value, g.value, rot.value, heads.value>;
+                const size_t smem = (size_t)kSlots<rot.value> * heads.value * kThreads * e.value * sizeof(T);
+                err = allow_smem(reinterpret_cast<const void*>(kernel), smem);
+                if (err == cudaSuccess)
+                    kernel<<<rot.value == kNone || want < kFwdBlocks ? want : kFwdBlocks, kThreads, smem, s>>>(a, sh, items);
+            });
         });
         if (err != cudaSuccess) return err;
     } else {
@@ -515,18 +524,19 @@ cudaError_t bwd(const QkNormArgs& a, cudaStream_t s) {
     int blocks = 0;                            // none without tokens: the weight gradients are then zero
     const int E = a.n > 0 ? channels_a_lane(a, true) : 0;
     if (E > 0) {
-        constexpr int N = kBwdHeads<T>;
-        const Shares sh = shares_of(a, N);
-        const unsigned items = (unsigned)(a.n * sh.all);
         cudaError_t err = cudaSuccess;
-        by_shape(a, E, [&](auto e, auto g, auto rot) {
-            const unsigned per = kThreads / g.value, want = (items + per - 1) / per;
-            blocks = (int)(want < kBwdBlocks ? want : kBwdBlocks);
-            const auto kernel = qk_bwd_kernel<T, e.value, g.value, rot.value, N>;
-            const size_t slots = 2 * (size_t)kBwdSlots * N * kThreads * e.value * sizeof(T);
-            const size_t sums = 2 * (size_t)kThreads * e.value * sizeof(float), smem = slots > sums ? slots : sums;
-            err = allow_smem(reinterpret_cast<const void*>(kernel), smem);
-            if (err == cudaSuccess) kernel<<<blocks, kThreads, smem, s>>>(a, sh, items, part);
+        by_heads<kBwdHeads<T>>(a, [&](auto heads) {
+            const Shares sh = shares_of(a, heads.value);
+            const unsigned items = (unsigned)(a.n * sh.all);
+            by_shape(a, E, [&](auto e, auto g, auto rot) {
+                const unsigned per = kThreads / g.value, want = (items + per - 1) / per;
+                blocks = (int)(want < kBwdBlocks ? want : kBwdBlocks);
+                const auto kernel = qk_bwd_kernel<T, e.value, g.value, rot.value, heads.value>;
+                const size_t slots = 2 * (size_t)kBwdSlots * heads.value * kThreads * e.value * sizeof(T);
+                const size_t sums = 2 * (size_t)kThreads * e.value * sizeof(float), smem = slots > sums ? slots : sums;
+                err = allow_smem(reinterpret_cast<const void*>(kernel), smem);
+                if (err == cudaSuccess) kernel<<<blocks, kThreads, smem, s>>>(a, sh, items, part);
+            });
         });
         if (err != cudaSuccess) return err;
     } else if (a.n > 0) {

@@ -150,8 +150,8 @@ __device__ __forceinline__ void state_row(const ConvArgs& a, int64_t r, int c) {
     }
 }
 
-// The grid: for every 32 V channels, the blocks of 8 runs of each batch row, then those of 8 state rows.
-struct Grid { int cols, run, run_blocks, state_blocks; };
+// The grid: for every 32 V channels, the blocks of 8 runs (of whatever batch rows), then those of 8 state rows.
+struct Grid { int cols, run, runs, run_blocks, state_blocks; };      // runs: of a batch row
 // Tokens a run: as many as leave 32 warps of 128 channels for each of 152 SMs, since a run's neighbourhood is walked twice
 // (65,536 packed tokens x 4096 channels: forward 185 us with 32 tokens and 172 with 64, backward 408 and 351; 128 gain
 // nothing), and 16 where there are few.
@@ -163,7 +163,8 @@ int run_of(const ConvArgs& a) {
 Grid grid_of(const ConvArgs& a, int V, bool states) {
     const int run = run_of(a), runs = (a.T + run - 1) / run;
     const int64_t rows = (int64_t)a.N() * (a.W - 1);
-    return {(a.D + 32 * V - 1) / (32 * V), run, (runs + kWarps - 1) / kWarps, states ? (int)((rows + kWarps - 1) / kWarps) : 0};
+    return {(a.D + 32 * V - 1) / (32 * V), run, runs, (int)(((int64_t)a.B * runs + kWarps - 1) / kWarps),
+            states ? (int)((rows + kWarps - 1) / kWarps) : 0};
 }
 
 template <typename T, int W, int V, bool PACKED>
@@ -175,12 +176,14 @@ __global__ void __launch_bounds__(kThreads) conv_fwd_kernel(const ConvArgs a, co
     const int c = ((int)(blockIdx.x % g.cols) * 32 + lane) * V;
     const int64_t block = blockIdx.x / g.cols;
     if (c >= a.D) return;
-    if (block >= (int64_t)a.B * g.run_blocks) {
-        const int64_t r = (block - (int64_t)a.B * g.run_blocks) * kWarps + warp;
+    if (block >= (int64_t)g.run_blocks) {
+        const int64_t r = (block - (int64_t)g.run_blocks) * kWarps + warp;
         if (r < (int64_t)a.N() * (W - 1)) state_row<T, W, V, false>(a, r, c);
         return;
     }
-    const int b = (int)(block / g.run_blocks), t0 = ((int)(block % g.run_blocks) * kWarps + warp) * g.run;
+    const int64_t r = block * kWarps + warp;
+    if (r >= (int64_t)a.B * g.runs) return;
+    const int b = (int)(r / g.runs), t0 = (int)(r % g.runs) * g.run;
     const int t1 = min(t0 + g.run, a.T);
     if (t0 >= t1) return;
     const size_t row0 = (size_t)b * a.T;
@@ -256,12 +259,14 @@ __global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(const ConvArgs a,
     const int c = ((int)(blockIdx.x % g.cols) * 32 + lane) * V;
     const bool live = c < a.D;
     const int64_t block = blockIdx.x / g.cols;
-    if (block >= (int64_t)a.B * g.run_blocks) {
-        const int64_t r = (block - (int64_t)a.B * g.run_blocks) * kWarps + warp;
+    if (block >= (int64_t)g.run_blocks) {
+        const int64_t r = (block - (int64_t)g.run_blocks) * kWarps + warp;
         if (live && r < (int64_t)a.N() * (W - 1)) state_row<T, W, V, true>(a, r, c);
         return;
     }
-    const int b = (int)(block / g.run_blocks), t0 = ((int)(block % g.run_blocks) * kWarps + warp) * g.run;
+    const int64_t r = block * kWarps + warp;
+    const bool run_there = r < (int64_t)a.B * g.runs;
+    const int b = run_there ? (int)(r / g.runs) : 0, t0 = run_there ? (int)(r % g.runs) * g.run : a.T;
     const int t1 = live ? min(t0 + g.run, a.T) : t0;            // the run's tokens
     const int t2 = min(t1 + W - 1, a.T);                       // and those whose ds they need
     const size_t row0 = (size_t)b * a.T;
@@ -420,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(const ConvArgs a,
         for (int v = 0; v < V; ++v) sum[warp][j][lane * V + v] = dw[j][v];
     __syncthreads();
     // part [W + 1][blocks][D]
-    const int64_t rows = (int64_t)a.B * g.run_blocks;
+    const int64_t rows = (int64_t)g.run_blocks;
     for (int i = threadIdx.x; i < (W + 1) * 32 * V; i += kWarps * 32) {
         const int j = i / (32 * V), lc = i % (32 * V), cc = (int)(blockIdx.x % g.cols) * 32 * V + lc;
         if (cc >= a.D) continue;
@@ -516,7 +521,7 @@ void by_type(const ConvArgs& a, bool wide, F f) {
 }  // namespace
 
 size_t conv_workspace_bytes(const ConvArgs& a) {
-    return (size_t)a.B * grid_of(a, 1, false).run_blocks * (a.W + 1) * a.D * sizeof(float);
+    return (size_t)grid_of(a, 1, false).run_blocks * (a.W + 1) * a.D * sizeof(float);
 }
 
 cudaError_t launch_conv_fwd(const ConvArgs& a, cudaStream_t s) {
@@ -525,7 +530,7 @@ cudaError_t launch_conv_fwd(const ConvArgs& a, cudaStream_t s) {
         by_type(a, vector_ok(a, 4), [&](auto* t, auto v) {
             using T = std::remove_pointer_t<decltype(t)>;
             const Grid g = grid_of(a, v.value, a.hT != nullptr);
-            const unsigned blocks = (unsigned)(g.cols * ((int64_t)a.B * g.run_blocks + g.state_blocks));
+            const unsigned blocks = (unsigned)(g.cols * ((int64_t)g.run_blocks + g.state_blocks));
             if (blocks == 0) return;
             const size_t smem = (size_t)kFwdRing * kThreads * v.value * sizeof(T);
             const auto kernel = a.cu ? conv_fwd_kernel<T, w.value, v.value, true> : conv_fwd_kernel<T, w.value, v.value, false>;
@@ -544,7 +549,7 @@ cudaError_t launch_conv_bwd(const ConvArgs& a, cudaStream_t s) {
         by_type(a, vector_ok(a, 4), [&](auto* t, auto v) {
             using T = std::remove_pointer_t<decltype(t)>;
             const Grid g = grid_of(a, v.value, a.dh0 != nullptr);
-            rows = (int64_t)a.B * g.run_blocks;
+            rows = (int64_t)g.run_blocks;
             const unsigned blocks = (unsigned)(g.cols * (rows + g.state_blocks));
             if (blocks == 0) return;
             const size_t rings = 2 * (size_t)kBwdRing * kThreads * v.value * sizeof(T);

@@ -8,6 +8,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -15,6 +16,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstring>
+#include <optional>
 #include <string>
 #include <vector>
 
@@ -218,7 +220,7 @@ struct OnStream {
 };
 
 at::Tensor empty(at::IntArrayRef shape, at::ScalarType type, const at::Tensor& like) {
-    return at::empty(shape, at::TensorOptions().dtype(type).device(like.device()));
+    return at::detail::empty_cuda(shape, type, like.device(), std::nullopt);
 }
 // The caller's output buffer, or a new one; `keep` holds it.
 void* output(PyObject* o, const char* name, at::IntArrayRef shape, at::ScalarType type, const at::Tensor& like, at::Tensor& keep) {
