@@ -201,12 +201,15 @@ glr_fwd_kernel(const GlrArgs a, const Exchange x, const int publish) {
             for (int v = 0; v < V; ++v) A[v] = -1.f;
         } else {
 #pragma unroll
-            for (int j = 0; j < L; ++j)
+            for (int v = 0; v < V; ++v) {
+                H[v] = u[0][v];
+                A[v] = al[0][v];
+            }
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    H[v] = j == 0 ? u[j][v] : fmaf(al[j][v], H[v], u[j][v]);
-                    A[v] = j == 0 ? al[j][v] : A[v] * al[j][v];
-                }
+            for (int j = 1; j < L; ++j) {
+                mix::fma_row(H, al[j], H, u[j]);
+                mix::mul_row(A, A, al[j]);
+            }
         }
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -248,11 +251,9 @@ glr_fwd_kernel(const GlrArgs a, const Exchange x, const int publish) {
 #pragma unroll
             for (int j = 0; j < L; ++j) {
                 Vec<Tx, V> o;
+                mix::fma_row(h, al[j], h, u[j]);
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    h[v] = fmaf(al[j][v], h[v], u[j][v]);
-                    o.set(v, h[v]);
-                }
+                for (int v = 0; v < V; ++v) o.set(v, h[v]);
                 if (j < n) o.store(op);
                 op += a.D;
             }

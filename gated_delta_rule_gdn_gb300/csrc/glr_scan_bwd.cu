@@ -244,19 +244,21 @@ glr_bwd_kernel(const GlrArgs a, const Exchange x, float* part) {
 #pragma unroll
                 for (int v = 0; v < V; ++v)
                     q.u[j][v] = fmaf(q.al[j][v], a.h0[(size_t)s_start[i % kPlaces][run * L + j] * a.D + c + v], q.u[j][v]);
+            if (start) {
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                H[v] = start ? q.u[j][v] : fmaf(q.al[j][v], H[v], q.u[j][v]);
-                A[v] *= q.al[j][v];
+                for (int v = 0; v < V; ++v) H[v] = q.u[j][v];
+            } else {
+                mix::fma_row(H, q.al[j], H, q.u[j]);
             }
+            mix::mul_row(A, A, q.al[j]);
         }
 #pragma unroll
         for (int j = L - 1; j >= 0; --j) {
             const bool end = M && ((ends >> j) & 1);
             float d[V];
             grad_o(i, j, c, end, d);
-#pragma unroll
-            for (int v = 0; v < V; ++v) G[v] = q.al[j][v] * (end ? d[v] : d[v] + G[v]);
+            if (!end) mix::add_row(d, d, G);
+            mix::mul_row(G, q.al[j], d);
         }
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -289,11 +291,8 @@ glr_bwd_kernel(const GlrArgs a, const Exchange x, float* part) {
         for (int j = L - 1; j >= 0; --j) {
             const bool end = M && ((ends >> j) & 1);
             grad_o(i, j, c, end, D[j]);
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                if (!end) D[j][v] += G[v];
-                G[v] = q.al[j][v] * D[j][v];
-            }
+            if (!end) mix::add_row(D[j], D[j], G);
+            mix::mul_row(G, q.al[j], D[j]);
             if (M && a.dh0 && live) {
                 const int s = s_start[i % kPlaces][run * L + j];
                 if (s >= 0)
@@ -313,14 +312,15 @@ glr_bwd_kernel(const GlrArgs a, const Exchange x, float* part) {
             const bool start = M && ((starts >> j) & 1);
             float hp[V];
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                hp[v] = h[v];
-                h[v] = start ? q.u[j][v] : fmaf(q.al[j][v], h[v], q.u[j][v]);
-            }
-            if (start)
+            for (int v = 0; v < V; ++v) hp[v] = h[v];
+            if (!start) {
+                mix::fma_row(h, q.al[j], h, q.u[j]);
+            } else
 #pragma unroll
-                for (int v = 0; v < V; ++v)
+                for (int v = 0; v < V; ++v) {
+                    h[v] = q.u[j][v];
                     hp[v] = a.h0 && live ? a.h0[(size_t)s_start[i % kPlaces][run * L + j] * a.D + c + v] : 0.f;
+                }
             const Vec<Tx, V> xv = buf_x(i)[j * kThreads];
             float w[V], y[V], xs[V], dla[V], dz[V];   // s sigma(i), x (1 - sigma(i)), x sigma(i)
 #pragma unroll
@@ -331,47 +331,57 @@ glr_bwd_kernel(const GlrArgs a, const Exchange x, float* part) {
             }
             if (a.gi) {
                 const Vec<Tx, V> gi = buf_x(i)[(2 * L + j) * kThreads];
+                float f[V];
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
                     // 1 - sigma(i) = exp(-i) sigma(i), with exp(-i) kept finite
-                    const float f = ex2(max_nan(gi.get(v), -80.f) * -kLog2e);
-                    w[v] = rcp(1.f + f);
-                    xs[v] *= w[v];
-                    y[v] = xs[v] * f;
+                    f[v] = ex2(max_nan(gi.get(v), -80.f) * -kLog2e);
+                    w[v] = rcp(1.f + f[v]);
                 }
+                mix::mul_row(xs, xs, w);
+                mix::mul_row(y, xs, f);
             }
-#pragma unroll
-            for (int v = 0; v < V; ++v) dla[v] = q.al[j][v] * hp[v];
+            mix::mul_row(dla, q.al[j], hp);
             if (a.normalize) {
+                float s[V], m[V], sq[V];
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
                     // ds/dlog a = -a^2 / s, taken as 0 where s = 0 (log a = 0: the derivative does not exist there)
                     const float s2 = input_power({q.al[j][v], q.e[j][v]}), rs = s2 > 0.f ? rsq(s2) : 0.f;
-                    w[v] *= s2 * rs;
-                    dla[v] = fmaf(-xs[v] * rs, q.al[j][v] * q.al[j][v], dla[v]);
+                    s[v] = s2 * rs;
+                    m[v] = -rs;
                 }
+                mix::mul_row(w, w, s);
+                mix::mul_row(m, m, xs);
+                mix::mul_row(sq, q.al[j], q.al[j]);
+                mix::fma_row(dla, m, sq, dla);
             }
+            mix::mul_row(dla, dla, D[j]);
 #pragma unroll
-            for (int v = 0; v < V; ++v) dz[v] = dla[v] *= D[j][v];
+            for (int v = 0; v < V; ++v) dz[v] = dla[v];
             if (a.A_log) {
                 const Vec<Tg, V> g = buf_g(i)[j * kThreads];
+                float t[V];
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
                     const float z = g.get(v) + ch[v].dt;
-                    dz[v] *= ch[v].neg_eA * sigmoid(z, tail(z));
-                    if (j < n) {
-                        pA[v] = fmaf(dla[v], q.la[j][v], pA[v]);
-                        pdt[v] += dz[v];
-                    }
+                    t[v] = ch[v].neg_eA * sigmoid(z, tail(z));
+                }
+                mix::mul_row(dz, dz, t);
+                if (j < n) {
+                    mix::fma_row(pA, dla, q.la[j], pA);
+                    mix::add_row(pdt, pdt, dz);
                 }
             }
+            float dw[V], dy[V];
+            mix::mul_row(dw, D[j], w);
+            mix::mul_row(dy, dw, y);
             Vec<Tx, V> dx, di;
             Vec<Tg, V> dg;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const float d = D[j][v] * w[v];
-                dx.set(v, d);
-                di.set(v, d * y[v]);
+                dx.set(v, dw[v]);
+                di.set(v, dy[v]);
                 dg.set(v, dz[v]);
             }
             if (j < n) {

@@ -74,6 +74,22 @@ __device__ __forceinline__ void mul_row(float (&d)[N], const float (&a)[N], cons
     }
 }
 
+template <int N>
+__device__ __forceinline__ void add_row(float (&d)[N], const float (&a)[N], const float (&b)[N]) {
+    if constexpr (N % 2 == 0) {
+#pragma unroll
+        for (int i = 0; i < N; i += 2)
+            asm("{\n\t.reg .b64 x, y;\n\t"
+                "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+                "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+                : "=f"(d[i]), "=f"(d[i + 1])
+                : "f"(a[i]), "f"(a[i + 1]), "f"(b[i]), "f"(b[i + 1]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) d[i] = a[i] + b[i];
+    }
+}
+
 // Copy V elements into shared memory without waiting (or zeros); the copying thread alone reads them.
 template <typename T, int V>
 __device__ __forceinline__ void copy_async(Vec<T, V>* dst, const T* src, bool in) {
