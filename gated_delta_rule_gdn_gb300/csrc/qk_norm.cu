@@ -448,7 +448,7 @@ __global__ void __launch_bounds__(256) qk_dw_kernel(const float* part, int rows,
 }
 
 // The channels a lane takes in the vector kernels: 8 or 4, whichever everything goes in steps of, or 0 if neither (twice 16,384
-// tokens x 32 heads of 128 in bf16: forward 78 us, 103, and 263 with the scalar kernel; backward 169 us, 196, and 463).
+// tokens x 32 heads of 128 in bf16: forward 78 us, 104, and 250 with the scalar kernel; backward 168 to 178, 188 to 198, and 464).
 int channels_a_lane(const QkNormArgs& a, bool backward) {
     for (int E = 8; E >= 4; E /= 2) {
         const size_t size = (a.bf16 ? 2 : 4) * E, bytes = size < 16 ? size : 16;

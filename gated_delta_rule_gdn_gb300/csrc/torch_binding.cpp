@@ -1,7 +1,7 @@
 // Python binding of the operators around the delta rule (module _native): checks torch tensors, allocates outputs and
 // workspaces through torch, and calls the C ABI on torch's current stream.
 //
-// Marshalling only, like _binding.py, but without its interpreter time: a decode step's kernel takes 2 us, its checks in
+// Marshalling only, like _binding.py, but without its interpreter time: a decode step's kernel takes 1.6 us, its checks in
 // Python took 14 us.  The entry points of libgdn_gb300.so are handed over as addresses by init(), so this module links
 // against torch alone.  Every entry turns C++ exceptions into Python ones.
 
