@@ -31,6 +31,7 @@ glr_fwd_kernel(const GlrArgs a, const Exchange x, const int publish) {
     __shared__ __align__(16) Channel s_chan[kPlaces][W];
     __shared__ Tile s_tile[kPlaces];
     const int tid = threadIdx.x;
+    cleared();
 
     if (tid >= kThreads) {                       // the carry threads
         const int ch = tid - kThreads;
@@ -301,6 +302,12 @@ glr_fwd_kernel(const GlrArgs a, const Exchange x, const int publish) {
     }
 }
 
+__global__ void __launch_bounds__(256) glr_clear_kernel(uint4* p, size_t n) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (size_t)gridDim.x * 256)
+        p[i] = make_uint4(kEmpty, kEmpty, kEmpty, kEmpty);
+}
+
 template <typename Tx, typename Tg>
 __global__ void glr_step_kernel(const GlrStepArgs a) {
     const int64_t id = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
@@ -324,7 +331,7 @@ cudaError_t fwd(const GlrArgs& a, cudaStream_t s) {
     const Layout l = layout(a.B, a.T, a.D, S::W);
     const Exchange x = exchange(l, a.ws);
     if (l.bytes) {
-        const cudaError_t e = cudaMemsetAsync(a.ws, 0xff, l.bytes, s);
+        const cudaError_t e = clear(a.ws, l.bytes, s);
         if (e != cudaSuccess) return e;
     }
     const auto kernel = glr_fwd_kernel<Tx, Tg, S, PACKED>;
@@ -332,8 +339,7 @@ cudaError_t fwd(const GlrArgs& a, cudaStream_t s) {
     static Residency res[2];                     // without and with the input gate
     const int blocks = res[a.gi != nullptr].get(reinterpret_cast<const void*>(kernel), S::kBlock, smem);
     if (blocks == 0) return cudaGetLastError();
-    kernel<<<x.total < blocks ? x.total : blocks, S::kBlock, smem, s>>>(a, x, a.test_stall ? 0 : 1);
-    return cudaGetLastError();
+    return launch_scan(kernel, x.total < blocks ? x.total : blocks, S::kBlock, smem, l.bytes > 0, s, a, x, a.test_stall ? 0 : 1);
 }
 
 template <typename Tx, typename Tg, typename S>
@@ -351,6 +357,12 @@ cudaError_t fwd_wide(const GlrArgs& a, cudaStream_t s) {
 }  // namespace
 
 namespace glr {
+cudaError_t clear(void* ws, size_t bytes, cudaStream_t s) {
+    const size_t n = bytes / sizeof(uint4), blocks = (n + 1023) / 1024, most = 152 * 8;
+    glr_clear_kernel<<<(unsigned)(blocks < most ? blocks : most), 256, 0, s>>>(static_cast<uint4*>(ws), n);
+    return cudaGetLastError();
+}
+
 int Residency::get(const void* kernel, int threads, int smem) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev >= kDevices) return 0;

@@ -42,6 +42,7 @@ glr_bwd_kernel(const GlrArgs a, const Exchange x, float* part) {
     __shared__ __align__(16) Channel s_chan[kPlaces][W];
     __shared__ Tile s_tile[kPlaces];
     const int tid = threadIdx.x;
+    cleared();
     const auto marked = [&](int i) { return PACKED && (s_marked[i % kPlaces][0] || s_marked[i % kPlaces][1]); };
 
     if (tid >= kThreads) {                       // the carry threads: the gradient's, the state's
@@ -471,7 +472,7 @@ cudaError_t bwd(const GlrArgs& a, const BwdSpace& sp, cudaStream_t s) {
     const Layout l = layout(a.B, a.T, a.D, S::W);
     const Exchange x = exchange(l, sp.scan);
     if (l.bytes) {
-        const cudaError_t e = cudaMemsetAsync(sp.scan, 0xff, l.bytes, s);
+        const cudaError_t e = clear(sp.scan, l.bytes, s);
         if (e != cudaSuccess) return e;
     }
     const auto kernel = glr_bwd_kernel<Tx, Tg, S, PACKED>;
@@ -479,7 +480,8 @@ cudaError_t bwd(const GlrArgs& a, const BwdSpace& sp, cudaStream_t s) {
     static Residency res[2];                     // without and with the input gate
     const int blocks = res[a.gi != nullptr].get(reinterpret_cast<const void*>(kernel), S::kBlock, smem);
     if (blocks == 0) return cudaGetLastError();
-    kernel<<<x.total < blocks ? x.total : blocks, S::kBlock, smem, s>>>(a, x, sp.part);
+    const cudaError_t e = launch_scan(kernel, x.total < blocks ? x.total : blocks, S::kBlock, smem, l.bytes > 0, s, a, x, sp.part);
+    if (e != cudaSuccess) return e;
     if (a.dA)
         glr_param_kernel<<<dim3((a.D + 31) / 32, 2), 256, 0, s>>>(sp.part, a.B * l.tiles, a.D, a.dA, a.ddt);
     return cudaGetLastError();
