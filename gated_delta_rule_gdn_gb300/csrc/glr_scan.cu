@@ -31,7 +31,7 @@ glr_fwd_kernel(const GlrArgs a, const Exchange x, const int publish) {
     __shared__ __align__(16) Channel s_chan[kPlaces][W];
     __shared__ Tile s_tile[kPlaces];
     const int tid = threadIdx.x;
-    cleared();
+    mix::wait_behind();                          // for the clearing
 
     if (tid >= kThreads) {                       // the carry threads
         const int ch = tid - kThreads;
@@ -303,7 +303,7 @@ glr_fwd_kernel(const GlrArgs a, const Exchange x, const int publish) {
 }
 
 __global__ void __launch_bounds__(256) glr_clear_kernel(uint4* p, size_t n) {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    mix::let_next();
     for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (size_t)gridDim.x * 256)
         p[i] = make_uint4(kEmpty, kEmpty, kEmpty, kEmpty);
 }
@@ -339,7 +339,8 @@ cudaError_t fwd(const GlrArgs& a, cudaStream_t s) {
     static Residency res[2];                     // without and with the input gate
     const int blocks = res[a.gi != nullptr].get(reinterpret_cast<const void*>(kernel), S::kBlock, smem);
     if (blocks == 0) return cudaGetLastError();
-    return launch_scan(kernel, x.total < blocks ? x.total : blocks, S::kBlock, smem, l.bytes > 0, s, a, x, a.test_stall ? 0 : 1);
+    return mix::launch_behind(kernel, x.total < blocks ? x.total : blocks, S::kBlock, smem, l.bytes > 0, s, a, x,
+                              a.test_stall ? 0 : 1);
 }
 
 template <typename Tx, typename Tg, typename S>

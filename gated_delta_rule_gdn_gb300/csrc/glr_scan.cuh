@@ -40,26 +40,11 @@ struct Residency {
     int get(const void* kernel, int threads, int smem);
 };
 
-// Launch a scan behind the clearing of its workspace.  The clearing starts after all earlier work of the stream; the scan's
+// A scan is launched behind the clearing of its workspace (mix::launch_behind).  The clearing starts after all earlier work of the stream; the scan's
 // blocks start while it runs, and touch memory only after their wait for it (against a memset before the scan: 1000 tokens x
 // 2048 channels 14.7 us and 17.5, B4 T4096 D2048 86 and 89 forward, 199 and 203 backward, 65,536 packed tokens x 4096 763 and 755
 // forward, 1613 and 1619 backward).
-__device__ __forceinline__ void cleared() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 cudaError_t clear(void* ws, size_t bytes, cudaStream_t s);       // bytes in steps of 256, ws on a 256-byte boundary
-template <typename... P, typename... Q>
-cudaError_t launch_scan(void (*kernel)(P...), int blocks, int threads, int smem, bool behind_clear, cudaStream_t s, Q... args) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(blocks);
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = behind_clear ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
 
 // Workspace of one scan, set to all ones before the launch.
 struct Exchange {

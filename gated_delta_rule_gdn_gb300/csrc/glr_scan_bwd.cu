@@ -42,7 +42,8 @@ glr_bwd_kernel(const GlrArgs a, const Exchange x, float* part) {
     __shared__ __align__(16) Channel s_chan[kPlaces][W];
     __shared__ Tile s_tile[kPlaces];
     const int tid = threadIdx.x;
-    cleared();
+    mix::wait_behind();                          // for the clearing
+    mix::let_next();
     const auto marked = [&](int i) { return PACKED && (s_marked[i % kPlaces][0] || s_marked[i % kPlaces][1]); };
 
     if (tid >= kThreads) {                       // the carry threads: the gradient's, the state's
@@ -450,6 +451,7 @@ __global__ void __launch_bounds__(256) glr_param_kernel(const float* part, int r
     const float* src = part + (size_t)blockIdx.y * rows * D;
     float* out = blockIdx.y ? ddt : dA;
     if (!out) return;
+    mix::wait_behind();
     float acc[4] = {};
     if (c < D) {
         int r = w;
@@ -480,11 +482,11 @@ cudaError_t bwd(const GlrArgs& a, const BwdSpace& sp, cudaStream_t s) {
     static Residency res[2];                     // without and with the input gate
     const int blocks = res[a.gi != nullptr].get(reinterpret_cast<const void*>(kernel), S::kBlock, smem);
     if (blocks == 0) return cudaGetLastError();
-    const cudaError_t e = launch_scan(kernel, x.total < blocks ? x.total : blocks, S::kBlock, smem, l.bytes > 0, s, a, x, sp.part);
-    if (e != cudaSuccess) return e;
-    if (a.dA)
-        glr_param_kernel<<<dim3((a.D + 31) / 32, 2), 256, 0, s>>>(sp.part, a.B * l.tiles, a.D, a.dA, a.ddt);
-    return cudaGetLastError();
+    const cudaError_t e = mix::launch_behind(kernel, x.total < blocks ? x.total : blocks, S::kBlock, smem, l.bytes > 0, s, a, x,
+                                             sp.part);
+    if (e != cudaSuccess || !a.dA) return e;
+    return mix::launch_behind(glr_param_kernel, dim3((a.D + 31) / 32, 2), 256, 0, true, s, sp.part, a.B * l.tiles, a.D, a.dA,
+                              a.ddt);
 }
 
 template <typename Tx, typename Tg, typename S>

@@ -10,6 +10,28 @@ namespace mix {
 
 using bf16 = __nv_bfloat16;
 
+// A kernel launched behind another of the same call: its blocks may start once all of the first's have come to let_next(),
+// and touch memory only after wait_behind(), which waits for the first to end with its writes visible.  (Sums of parameter
+// gradients, forward and backward, against ordinary launches: convolution of 1000 tokens x 4096 channels 22.7 us and 25.1,
+// recurrence 1000 x 2048 41.7 and 43.5, B4 T4096 D2048 277 and 280, norm of 16,384 tokens x 40 heads 172.7 and 174.0.)
+__device__ __forceinline__ void let_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_behind() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// (`behind` false: an ordinary launch)
+template <typename... P, typename... Q>
+cudaError_t launch_behind(void (*kernel)(P...), dim3 blocks, int threads, size_t smem, bool behind, cudaStream_t s, Q... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = blocks;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = behind ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 __device__ __forceinline__ float ld(const float* p) { return *p; }
 __device__ __forceinline__ float ld(const bf16* p) { return __bfloat162float(*p); }
 __device__ __forceinline__ void st(float* p, float x) { *p = x; }

@@ -216,6 +216,7 @@ __global__ void __launch_bounds__(kThreads, 2) qk_bwd_kernel(const QkNormArgs a,
                                                              float* part) {
     using C = Chunk<T, E>;
     constexpr unsigned kGroups = kThreads / G;
+    mix::let_next();
     extern __shared__ __align__(16) unsigned char s_raw[];
     auto* buf = reinterpret_cast<typename C::Part*>(s_raw) + threadIdx.x;     // [kBwdSlots][N][x, dz][parts][256]
     const auto slot = [&](int k, int i, int z) {
@@ -363,6 +364,7 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads, 3) qk_bwd_any_kernel(const QkNormArgs a, float* part) {
     __shared__ float buf[kWarps][kMaxD];
     __shared__ float dw[2][kWarps][kMaxD];
+    mix::let_next();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int heads = a.H[0] + a.H[1];
     float acc[2][kMaxD / 32] = {};
@@ -433,6 +435,7 @@ __global__ void __launch_bounds__(kThreads, 3) qk_bwd_any_kernel(const QkNormArg
 __global__ void __launch_bounds__(256) qk_dw_kernel(const float* part, int rows, int d, float* dwq, float* dwk) {
     __shared__ float s[32][9];
     const int c = threadIdx.x % 8, w = threadIdx.x / 8, j = blockIdx.x * 8 + c;
+    mix::wait_behind();
     float acc = 0.f;
     if (j < 2 * d)
 #pragma unroll 4
@@ -552,8 +555,9 @@ cudaError_t bwd(const QkNormArgs& a, cudaStream_t s) {
         blocks = (int)(want < (int64_t)kAnyBlocks ? want : (int64_t)kAnyBlocks);
         qk_bwd_any_kernel<T><<<blocks, kThreads, 0, s>>>(a, part);
     }
-    if (weights) qk_dw_kernel<<<(2 * a.d + 7) / 8, 256, 0, s>>>(part, blocks, a.d, a.dw[0], a.dw[1]);
-    return cudaGetLastError();
+    const cudaError_t err = cudaGetLastError();
+    if (err != cudaSuccess || !weights) return err;
+    return mix::launch_behind(qk_dw_kernel, (2 * a.d + 7) / 8, 256, 0, blocks > 0, s, part, blocks, a.d, a.dw[0], a.dw[1]);
 }
 
 }  // namespace

@@ -254,6 +254,7 @@ __global__ void __launch_bounds__(kThreads) conv_fwd_kernel(const ConvArgs a, co
 template <typename T, int W, int V, bool PACKED>
 __global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(const ConvArgs a, const Grid g, float* part) {
     constexpr int kRing = kBwdRing;
+    mix::let_next();
     extern __shared__ __align__(16) unsigned char s_raw[];
     auto* rx = reinterpret_cast<Vec<T, V>*>(s_raw) + threadIdx.x;             // [kRing][256] each
     auto* ry = rx + kRing * kThreads;
@@ -443,6 +444,7 @@ __global__ void __launch_bounds__(256) conv_param_kernel(const float* part, int6
     __shared__ float s[8][32];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, c = blockIdx.x * 32 + lane, j = blockIdx.y;
     if (j == W && !db) return;
+    mix::wait_behind();
     float acc = 0.f;
     if (c < D)
 #pragma unroll 4
@@ -563,9 +565,10 @@ cudaError_t launch_conv_bwd(const ConvArgs& a, cudaStream_t s) {
             if (e == cudaSuccess) kernel<<<blocks, kThreads, smem, s>>>(a, g, part);
         });
     });
+    if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    conv_param_kernel<<<dim3((a.D + 31) / 32, a.W + 1), 256, 0, s>>>(part, rows, a.D, a.W, a.dw, a.db);
-    return cudaGetLastError();
+    return mix::launch_behind(conv_param_kernel, dim3((a.D + 31) / 32, a.W + 1), 256, 0, rows > 0, s, part, rows, a.D, a.W, a.dw,
+                              a.db);
 }
 
 cudaError_t launch_conv_step(const ConvArgs& a, const void* state, void* state_out, cudaStream_t s) {
