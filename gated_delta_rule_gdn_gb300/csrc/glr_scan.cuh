@@ -40,10 +40,10 @@ struct Residency {
     int get(const void* kernel, int threads, int smem);
 };
 
-// A scan is launched behind the clearing of its workspace (mix::launch_behind).  The clearing starts after all earlier work of the stream; the scan's
-// blocks start while it runs, and touch memory only after their wait for it (against a memset before the scan: 1000 tokens x
-// 2048 channels 14.7 us and 17.5, B4 T4096 D2048 86 and 89 forward, 199 and 203 backward, 65,536 packed tokens x 4096 763 and 755
-// forward, 1613 and 1619 backward).
+// A scan is launched behind the clearing of its workspace (mix::launch_behind).  The clearing starts after all earlier
+// work of the stream; the scan's blocks start while it runs, and touch memory only after their wait for it (against a memset
+// before the scan: 1000 tokens x 2048 channels 14.7 us and 17.5, B4 T4096 D2048 86 and 89 forward, 199 and 203 backward,
+// 65,536 packed tokens x 4096 channels 763 and 755 forward, 1613 and 1619 backward).
 cudaError_t clear(void* ws, size_t bytes, cudaStream_t s);       // bytes in steps of 256, ws on a 256-byte boundary
 
 // Workspace of one scan, set to all ones before the launch.
@@ -293,7 +293,7 @@ struct Tickets {
 };
 // A block's first three tiles, one ticket after the other, so that every block has its first before any has its second:
 // blocks that take several at once have neighbouring tiles at different places in their queues, and wait for each other's
-// queues (65,536 tokens x 250 channels: 1.2 ms with three at once, 87 us so; 76 us with what came after).
+// queues (65,536 tokens x 250 channels: 1.2 ms with three at once, 87 us so; 73 us with what came after).
 template <typename Meet>
 __device__ __forceinline__ void first_tiles(const Exchange& x, const GlrArgs& a, int W, bool reverse, Tickets& tickets,
                                             Tile* tile, bool leader, Meet meet) {
