@@ -30,15 +30,13 @@ static_assert(kFwdRing % kChunk == 0 && kBwdRing % kChunk == 0, "whole groups");
 
 __device__ __forceinline__ float ex2(float x) { float y; asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x)); return y; }
 __device__ __forceinline__ float rcp(float x) { float y; asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x)); return y; }
-// p sigma(p), and its derivative sigma (1 + p (1 - sigma)).  exp(-p) is kept finite, so that p sigma(p) of a large
-// negative p is a tiny number, not 0 times infinity; 1 - sigma = exp(-p) sigma.
-__device__ __forceinline__ float silu(float p) {
-    const float s = rcp(1.f + ex2(fminf(p * -1.4426950408889634f, 126.f)));
-    return p * s;
-}
+// p sigma(p), and its derivative sigma (1 + p (1 - sigma)), sigma = 1 / (1 + exp(-p)).  Where sigma is below 2^-126 (p < -87.3)
+// it is 0, and so are both, for any finite p: what is dropped is less than 2^-119.  1 - sigma = exp(-p) sigma, with exp(-p) kept
+// finite so that it is 0 there, not infinity times 0.  (Both keep NaN, and give it for -infinity, where the formulas do.)
+__device__ __forceinline__ float silu(float p) { return p * rcp(1.f + ex2(p * -1.4426950408889634f)); }
 __device__ __forceinline__ float silu_slope(float p) {
-    const float e = ex2(fminf(p * -1.4426950408889634f, 126.f)), s = rcp(1.f + e);
-    return s * fmaf(p, e * s, 1.f);
+    const float e = ex2(p * -1.4426950408889634f), s = rcp(1.f + e);
+    return s * fmaf(p, fminf(e, 3.402823466e38f) * s, 1.f);
 }
 
 // A sequence: its number, and its first token and one past its last in the batch row.
