@@ -339,9 +339,11 @@ glr_bwd_kernel(const GlrArgs a, const Exchange x, float* part) {
                 float f[V];
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    // 1 - sigma(i) = exp(-i) sigma(i), with exp(-i) kept finite
-                    f[v] = ex2(max_nan(gi.get(v), -80.f) * -kLog2e);
-                    w[v] = rcp(1.f + f[v]);
+                    // 1 - sigma(i) = exp(-i) sigma(i), with exp(-i) kept finite for that product: a shut gate's sigma is 0
+                    // here as it is forward, whatever the input behind it
+                    const float e = ex2(gi.get(v) * -kLog2e);
+                    w[v] = rcp(1.f + e);
+                    f[v] = fminf(e, 3.402823466e38f);
                 }
                 mix::mul_row(xs, xs, w);
                 mix::mul_row(y, xs, f);

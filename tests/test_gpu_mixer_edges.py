@@ -67,3 +67,45 @@ def test_convolution_silu_of_any_argument(dtype, count):
     each(db, want["db"], "db", rel, flushed)
     each(dh0, want["dh0"], "dh0", rel, flushed)
     each(dw, want["dw"], "dw", np.stack([rel, rel], 1), np.stack([flushed, flushed * np.abs(p).clip(max=104)], 1))
+
+
+# ------------------------------------------------------------------------------------------- gated linear recurrence
+
+def glr_one_token(x, g, i, h0, A_log=None, dt_bias=None, normalize=False):
+    """One token of one sequence, forward, step and backward with gradients of ones: (got, want), and the magnitudes
+    that dg and dA_log are sums of."""
+    row = lambda t: None if t is None else t[None, None]     # noqa: E731
+    kw = dict(in_gate=row(i), A_log=A_log, dt_bias=dt_bias, normalize=normalize, initial_state=h0[None])
+    ref = dict(i=f64(row(i)), A_log=f64(A_log), dt_bias=f64(dt_bias), normalize=normalize, h0=f64(h0[None]))
+    one, x, g = torch.ones_like(row(x)), row(x), row(g)
+    o, hT = gdn.glr_scan_fwd(x, g, output_final_state=True, **kw)
+    state = h0[None].clone()
+    gdn.glr_step(x[0], g[0], state, in_gate=None if i is None else i[None], A_log=A_log, dt_bias=dt_bias, normalize=normalize)
+    got = dict(zip(("dx", "dg", "di", "dh0", "dA_log", "ddt_bias"), gdn.glr_scan_bwd(x, g, one, **kw)), hT=hT, step=state)
+    want = R.glr_bwd(f64(x), f64(g), f64(one), **ref)
+    want["hT"] = want["step"] = R.glr_fwd(f64(x), f64(g), **ref)[1]
+    return got, want
+
+
+@pytest.mark.parametrize("normalize", [False, True])
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("count", [64, 63])
+def test_recurrence_closed_input_gate(dtype, normalize, count):
+    """Inputs of any finite size behind an input gate that is shut: nothing of them comes through, either way."""
+    low = float(torch.finfo(dtype).min)
+    gates = [-float("inf"), low, -1e30, -1e4, -200.0, -100.0, -60.0, -20.0]
+    values = [low, -low, 1e30, -1e20, 1e10, -1.0, 1.0, 0.0]
+    i, x = (torch.tensor(v, dtype=dtype).cuda()[:count] for v in zip(*[(a, b) for a in gates for b in values]))
+    gen = torch.Generator().manual_seed(3)
+    h0 = torch.randn(count, generator=gen).cuda()
+    g = (-torch.rand(count, generator=gen) - 0.1).cuda()
+    got, want = glr_one_token(x, g, i, h0, normalize=normalize)
+    z = np.abs(f64(i)).clip(max=104)
+    # what a sigma that counts as 0 leaves out; a^2 / s < 3 for these decays; a sum is off by what its larger part is
+    rel, lost = (z + 16) * 2.0 ** -22, np.where(z > 87, np.abs(f64(x)) * TINY, 0)
+    m, h = np.abs(f64(x)) * R.sigmoid(f64(i)), np.abs(f64(h0))
+    for n in ("hT", "step"):
+        each(got[n], want[n], n, 2.0 ** -20, m * rel + lost + h * 2.0 ** -20)
+    each(got["dx"], want["dx"], "dx", rel, TINY)
+    each(got["di"], want["di"], "di", rel, 2 * lost + TINY)
+    each(got["dg"], want["dg"], "dg", 2.0 ** -20, 3 * (m * rel + lost) + h * 2.0 ** -20)
