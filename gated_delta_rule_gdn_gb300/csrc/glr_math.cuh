@@ -106,8 +106,29 @@ __device__ __forceinline__ void softplus(float z0, float z1, float nA0, float nA
 __device__ __forceinline__ float sigmoid(float z, float q) { return (z < 0.f ? q : 1.f) * rcp(1.f + q); }
 __device__ __forceinline__ float sigmoid(float z) { return rcp(1.f + ex2(z * -kLog2e)); }
 
-// 1 - a^2 (0 for a decay above 1), the square of the input factor
-__device__ __forceinline__ float input_power(const Decay& d) { return fmaxf(-d.e * (2.f + d.e), 0.f); }
+// The input factor s = sqrt(1 - a^2) (0 for a decay above 1).  A log a that is a subnormal number leaves 1 - a^2 one too, while
+// s (about 1e-20) and 1 / s are not; so 1 - a^2 is taken times 2^64, past the flushing of the approximations, and s times 2^32.
+// Two elements to an instruction where there are two (65,536 packed tokens x 4096 channels forward: 749 us; one by one 823).
+constexpr float kFactor = 0x1p32f;
+__device__ __forceinline__ void input_powers(float* power, const Decay& d) {      // 2^64 (1 - a^2) = -2^64 e (2 + e)
+    power[0] = fmaxf(d.e * fmaf(d.e, -kFactor * kFactor, -2.f * kFactor * kFactor), 0.f);
+}
+__device__ __forceinline__ void input_powers(float* power, const Decay& d0, const Decay& d1) {
+    const f2 e = pack(d0.e, d1.e);
+    unpack(mul2(e, fma2(e, both_of(-kFactor * kFactor), both_of(-2.f * kFactor * kFactor))), power[0], power[1]);
+    power[0] = fmaxf(power[0], 0.f);
+    power[1] = fmaxf(power[1], 0.f);
+}
+// u times s
+template <int N>
+__device__ __forceinline__ void times_factors(float* u, const float* power) {
+    if constexpr (N == 2) {
+        const f2 s = mul2(pack(root(power[0]), root(power[1])), both_of(1.f / kFactor));
+        unpack(mul2(pack(u[0], u[1]), s), u[0], u[1]);
+    } else {
+        u[0] *= root(power[0]) * (1.f / kFactor);
+    }
+}
 
 }  // namespace glr
 }  // namespace gdn

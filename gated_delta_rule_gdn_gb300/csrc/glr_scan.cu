@@ -178,9 +178,13 @@ glr_fwd_kernel(const GlrArgs a, const Exchange x, const int publish) {
             }
         }
         log_decays<L, V>(a, s_chan[i % kPlaces] + lane * V, al);
-        decays<L, V>(al, [&](int j, int v, const Decay& d) {
-            if (a.normalize) u[j][v] *= root(input_power(d));
-            al[j][v] = d.a;
+        decays<L, V>(al, [&](int j, int v, const auto&... d) {
+            if (a.normalize) {
+                float power[sizeof...(d)];
+                input_powers(power, d...);
+                times_factors<sizeof...(d)>(&u[j][v], power);
+            }
+            ((al[j][v++] = d.a), ...);
         });
         if (count < L) {                         // past the row's end the state stays
 #pragma unroll
@@ -320,7 +324,11 @@ __global__ void glr_step_kernel(const GlrStepArgs a) {
     float la = a.A_log ? ch.neg_eA * softplus(g + ch.dt, tail(g + ch.dt)) : min_nan(g, 88.f);
     const Decay d = decay(la);
     float u = mix::ld(static_cast<const Tx*>(a.x) + n * a.ldx + c);
-    if (a.normalize) u *= root(input_power(d));
+    if (a.normalize) {
+        float power;
+        input_powers(&power, d);
+        times_factors<1>(&u, &power);
+    }
     if (a.gi) u *= sigmoid(mix::ld(static_cast<const Tx*>(a.gi) + n * a.ldi + c));
     const float h = fmaf(d.a, a.h[n * a.D + c], u);
     a.h_out[n * a.D + c] = h;

@@ -230,7 +230,7 @@ __device__ __forceinline__ void log_decays(const GlrArgs& a, const Channel* chan
             for (int v = 0; v < V; ++v) la[j][v] = min_nan(la[j][v], 88.f);
     }
 }
-// f(j, v, decay) for every element of a run.
+// f(j, v, decay of element v, of element v + 1) for every pair of a run, or f(j, v, decay) for every element if V is odd.
 template <int L, int V, typename F>
 __device__ __forceinline__ void decays(float (&la)[L][V], F f) {
 #pragma unroll
@@ -240,8 +240,7 @@ __device__ __forceinline__ void decays(float (&la)[L][V], F f) {
             for (int v = 0; v < V; v += 2) {
                 Decay d0, d1;
                 decay(la[j][v], la[j][v + 1], d0, d1);
-                f(j, v, d0);
-                f(j, v + 1, d1);
+                f(j, v, d0, d1);
             }
         } else {
 #pragma unroll

@@ -24,7 +24,7 @@ __device__ unsigned g_glr_bwd_status;   // bit 0: a block gave up a bounded wait
 
 struct BwdSpace { void* scan; float* part; };
 
-// Stage one keeps the decay (as a and as a - 1), log a and the input u of a tile's elements in registers; its raw inputs
+// Stage one keeps the decay, 1 - a^2, log a and the input u of a tile's elements in registers; its raw inputs
 // stay in shared memory until stage two, which first runs the gradient D through the run from behind, then the state from
 // the front, and forms each token's gradients on the way.
 constexpr int kBuffers = 3;
@@ -179,7 +179,7 @@ glr_bwd_kernel(const GlrArgs a, const Exchange x, float* part) {
         }
         mix::copies_close();
     };
-    struct Held { float al[L][V], e[L][V], la[L][V], u[L][V]; };
+    struct Held { float al[L][V], power[L][V], la[L][V], u[L][V]; };
     const auto marks = [&](int i, unsigned* starts, unsigned* ends) {
         *starts = *ends = 0;
 #pragma unroll
@@ -223,10 +223,12 @@ glr_bwd_kernel(const GlrArgs a, const Exchange x, float* part) {
             }
         }
         log_decays<L, V>(a, s_chan[i % kPlaces] + lane * V, q.la);
-        decays<L, V>(q.la, [&](int j, int v, const Decay& d) {
-            q.al[j][v] = d.a;
-            q.e[j][v] = d.e;
-            if (a.normalize) q.u[j][v] *= root(input_power(d));
+        decays<L, V>(q.la, [&](int j, int v, const auto&... d) {
+            if (a.normalize) {
+                input_powers(&q.power[j][v], d...);
+                times_factors<sizeof...(d)>(&q.u[j][v], &q.power[j][v]);
+            }
+            ((q.al[j][v++] = d.a), ...);
         });
         if (count < L) {                         // past the row's end state and gradient stay
 #pragma unroll
@@ -350,14 +352,17 @@ glr_bwd_kernel(const GlrArgs a, const Exchange x, float* part) {
             }
             mix::mul_row(dla, q.al[j], hp);
             if (a.normalize) {
-                float s[V], m[V], sq[V];
+                float s[V], m[V], sq[V], down[V], up[V];
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
                     // ds/dlog a = -a^2 / s, taken as 0 where s = 0 (log a = 0: the derivative does not exist there)
-                    const float s2 = input_power({q.al[j][v], q.e[j][v]}), rs = s2 > 0.f ? rsq(s2) : 0.f;
-                    s[v] = s2 * rs;
-                    m[v] = -rs;
+                    m[v] = q.power[j][v] > 0.f ? rsq(q.power[j][v]) : 0.f;
+                    down[v] = 1.f / kFactor;
+                    up[v] = -kFactor;
                 }
+                mix::mul_row(s, q.power[j], m);
+                mix::mul_row(s, s, down);
+                mix::mul_row(m, m, up);
                 mix::mul_row(w, w, s);
                 mix::mul_row(m, m, xs);
                 mix::mul_row(sq, q.al[j], q.al[j]);

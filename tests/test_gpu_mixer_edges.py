@@ -109,3 +109,27 @@ def test_recurrence_closed_input_gate(dtype, normalize, count):
     each(got["dx"], want["dx"], "dx", rel, TINY)
     each(got["di"], want["di"], "di", rel, 2 * lost + TINY)
     each(got["dg"], want["dg"], "dg", 2.0 ** -20, 3 * (m * rel + lost) + h * 2.0 ** -20)
+
+
+@pytest.mark.parametrize("count", [32, 31])
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_recurrence_decay_next_to_one(dtype, count):
+    """Log decays that are subnormal numbers: s = sqrt(1 - a^2) is about 1e-20, far inside the range of fp32, and so are
+    1 / s and the gradients that have it as a factor."""
+    gen = torch.Generator().manual_seed(4)
+    x, i = ((torch.randn(count, generator=gen) + 0.1).to(dtype).cuda() for _ in range(2))
+    h0 = torch.zeros(count, device="cuda")                # (next to a state of order one nothing of s would show)
+    la = -torch.logspace(-43, -37, 32, dtype=torch.float64)[:count]
+    got, want = glr_one_token(x, la.float().cuda(), i, h0, normalize=True)
+    rel = (np.abs(f64(i)) + 32) * 2.0 ** -22
+    for n in ("hT", "step", "dx", "di", "dg"):
+        each(got[n], want[n], n, rel)
+    # the same out of logits: softplus(z) = exp(z) is a normal number, times exp(A_log) it is not.  Products that are
+    # subnormal are rounded in steps of 2^-149
+    z = torch.linspace(-87, -80, 32)[:count].cuda()
+    A = torch.full((count,), -7.0, device="cuda")
+    got, want = glr_one_token(x, z, i, h0, A, torch.zeros_like(A), normalize=True)
+    small = np.exp(f64(A) + f64(z))
+    rel = (np.abs(f64(i)) + np.abs(f64(z)) + 32) * 2.0 ** -22 + 2 * 2.0 ** -149 / small
+    for n in ("hT", "step", "dx", "di", "dA_log", "dg", "ddt_bias"):
+        each(got[n], want[n], n, rel)
