@@ -326,8 +326,9 @@ gdn_status gdn_qk_norm_bwd(const void* q, const void* k, const void* grad_q_out,
         if (a.w[i]) GDN_TRY(need(fn, name, a.dw[i], 4));
         else if (a.dw[i]) return fail(GDN_ERR_INVALID_ARG, "%s: %s is given without its weight", fn, name);
     }
+    const size_t bytes = a.dw[0] || a.dw[1] ? gdn::qk_norm_workspace_bytes(a) : 0;     // (for the weights' gradients alone)
     Workspace ws;
-    GDN_TRY(ws.get(fn, workspace, workspace_bytes, gdn::qk_norm_workspace_bytes(a), static_cast<cudaStream_t>(stream)));
+    GDN_TRY(ws.get(fn, workspace, workspace_bytes, bytes, static_cast<cudaStream_t>(stream)));
     a.ws = ws.ptr;
     return finish(fn, gdn::launch_qk_norm_bwd(a, ws.s), ws);
 }

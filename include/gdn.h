@@ -595,7 +595,7 @@ gdn_status gdn_qk_norm_fwd(const void* q, const void* k, const float* q_weight, 
  * gdn_qk_norm_bwd -- gradients through gdn_qk_norm_fwd, from its inputs and the gradients of its
  * outputs (contiguous, dtype).  grad_q, grad_k: contiguous, dtype.  grad_q_weight, grad_k_weight:
  * [d] fp32 sums over tokens and heads, required with their weight.  The rotation table has no gradient.
- *   workspace  gdn_qk_norm_workspace_size bytes
+ *   workspace  gdn_qk_norm_workspace_size bytes; none is needed without weights
  */
 gdn_status gdn_qk_norm_bwd(const void* q, const void* k, const void* grad_q_out, const void* grad_k_out,
                            const float* q_weight, const float* k_weight, gdn_norm norm, float eps, const float* cos,

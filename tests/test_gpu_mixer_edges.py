@@ -7,6 +7,8 @@ Tolerances, from the arithmetic (z the argument of an exponential, u = 2^-24 the
 * sigma(z) below 2^-126 may count as 0: it is then off by less than 2^-126, times whatever multiplies it.
 * A result in bf16 adds its unit roundoff 2^-8.
 """
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -133,3 +135,46 @@ def test_recurrence_decay_next_to_one(dtype, count):
     rel = (np.abs(f64(i)) + np.abs(f64(z)) + 32) * 2.0 ** -22 + 2 * 2.0 ** -149 / small
     for n in ("hT", "step", "dx", "di", "dA_log", "dg", "ddt_bias"):
         each(got[n], want[n], n, rel)
+
+
+# ----------------------------------------------------------------------------------------------- query/key head norm
+
+class Pool:
+    """The device's default memory pool, which cudaMallocAsync takes from: the most that was in use since reset()."""
+    HIGH = 8                                              # CU_MEMPOOL_ATTR_USED_MEM_HIGH
+
+    def __init__(self):
+        self.cuda, self.pool = ctypes.CDLL("libcuda.so.1"), ctypes.c_void_p()
+        assert self.cuda.cuDeviceGetDefaultMemPool(ctypes.byref(self.pool), torch.cuda.current_device()) == 0
+
+    def reset(self):
+        torch.cuda.synchronize()
+        assert self.cuda.cuMemPoolSetAttribute(self.pool, self.HIGH, ctypes.byref(ctypes.c_uint64(0))) == 0
+        return self.high()
+
+    def high(self):
+        torch.cuda.synchronize()
+        v = ctypes.c_uint64(0)
+        assert self.cuda.cuMemPoolGetAttribute(self.pool, self.HIGH, ctypes.byref(v)) == 0
+        return v.value
+
+
+def test_head_norm_without_weights_takes_no_workspace():
+    """Only the weights' gradients need one: without weights neither the binding nor the C ABI allocates any."""
+    q, k = torch.randn(2, 300, 4, 128, device="cuda"), torch.randn(2, 300, 2, 128, device="cuda")
+    w = torch.ones(128, device="cuda")
+    lib, pool, out = gdn.load(), Pool(), [torch.empty_like(q), torch.empty_like(k), torch.empty_like(w), torch.empty_like(w)]
+    want = gdn.gdn_qk_norm_bwd(q, k, q, k, norm="l2")     # (builds what a first call builds)
+    before = pool.reset()
+    assert all(torch.equal(a, b) for a, b in zip(gdn.gdn_qk_norm_bwd(q, k, q, k, norm="l2")[:2], want))
+    assert pool.high() == before
+
+    def call(weight):
+        p = [t.data_ptr() for t in (q, k, q, k)] + [w.data_ptr() if weight else None] * 2
+        o = [t.data_ptr() for t in out[:2]] + [out[2 + i].data_ptr() if weight else None for i in (0, 1)]
+        assert lib.gdn_qk_norm_bwd(*p, 1, 1e-6, None, None, 0, 0, 0, None, *o, 600, 300, 4, 2, 128, 512, 128, 256, 128, 0,
+                                   None, 0, torch.cuda.current_stream().cuda_stream) == 0
+        return pool.high()
+    assert call(False) == before
+    assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
+    assert call(True) > before                            # with weights the C ABI allocates for itself
