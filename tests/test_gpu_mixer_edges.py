@@ -139,6 +139,32 @@ def test_recurrence_decay_next_to_one(dtype, count):
 
 # ----------------------------------------------------------------------------------------------- query/key head norm
 
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("d", [128, 100, 127])            # eight channels a lane, four, and a warp per head
+def test_head_norm_infinities_next_to_the_rotation(dtype, d, interleaved):
+    """An infinite channel that does not turn stays where it is; its neighbours are what they were."""
+    gen = torch.Generator().manual_seed(5)
+    q, k, dq, dk = (torch.randn(2, 5, h, d, generator=gen).to(dtype).cuda() for h in (3, 2, 3, 2))
+    ang = torch.rand(5, 24, generator=gen).cuda()
+    w = (torch.rand(d, generator=gen) + 0.5).cuda()
+    kw = dict(cos=ang.cos(), sin=ang.sin(), interleaved=interleaved)
+    bad = [50, 97]
+    other = [c for c in range(d) if c not in bad]
+    up = w.clone()
+    up[bad] = float("inf")
+    for x, y, z in zip((q, k), gdn.gdn_qk_norm_fwd(q, k, q_weight=w, k_weight=w, **kw),
+                       gdn.gdn_qk_norm_fwd(q, k, q_weight=up, k_weight=up, **kw)):
+        assert torch.equal(z[..., other], y[..., other])
+        assert torch.equal(z[..., bad].float(), torch.copysign(torch.full_like(x[..., bad].float(), float("inf")), x[..., bad].float()))
+    _, _, wq, wk = gdn.gdn_qk_norm_bwd(q, k, dq, dk, q_weight=w, k_weight=w, **kw)
+    dq[0, 1, 2, bad], dk[1, 3, 0, bad] = float("inf"), float("inf")
+    _, _, vq, vk = gdn.gdn_qk_norm_bwd(q, k, dq, dk, q_weight=w, k_weight=w, **kw)
+    for v, was, x in ((vq, wq, q[0, 1, 2, bad]), (vk, wk, k[1, 3, 0, bad])):
+        assert torch.equal(v[other], was[other])
+        assert torch.equal(v[bad], torch.copysign(torch.full((2,), float("inf"), device="cuda"), x.float()))
+
+
 class Pool:
     """The device's default memory pool, which cudaMallocAsync takes from: the most that was in use since reset()."""
     HIGH = 8                                              # CU_MEMPOOL_ATTR_USED_MEM_HIGH
