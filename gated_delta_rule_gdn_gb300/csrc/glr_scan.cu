@@ -346,8 +346,9 @@ cudaError_t fwd(const GlrArgs& a, cudaStream_t s) {
     const auto kernel = glr_fwd_kernel<Tx, Tg, S, PACKED>;
     const int smem = 2 * S::L * S::kThreads * S::V * (int)(sizeof(Tg) + (a.gi ? 2 : 1) * sizeof(Tx));
     static Residency res[2];                     // without and with the input gate
-    const int blocks = res[a.gi != nullptr].get(reinterpret_cast<const void*>(kernel), S::kBlock, smem);
-    if (blocks == 0) return cudaGetLastError();
+    int blocks = 0;
+    const cudaError_t e = res[a.gi != nullptr].get(reinterpret_cast<const void*>(kernel), S::kBlock, smem, &blocks);
+    if (e != cudaSuccess) return e;
     return mix::launch_behind(kernel, x.total < blocks ? x.total : blocks, S::kBlock, smem, l.bytes > 0, s, a, x,
                               a.test_stall ? 0 : 1);
 }
@@ -371,24 +372,6 @@ cudaError_t clear(void* ws, size_t bytes, cudaStream_t s) {
     const size_t n = bytes / sizeof(uint4), blocks = (n + 1023) / 1024, most = 152 * 8;
     glr_clear_kernel<<<(unsigned)(blocks < most ? blocks : most), 256, 0, s>>>(static_cast<uint4*>(ws), n);
     return cudaGetLastError();
-}
-
-int Residency::get(const void* kernel, int threads, int smem) {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev >= kDevices) return 0;
-    int n = blocks[dev].load(std::memory_order_relaxed);
-    if (n > 0) return n;
-    int sms = 0, per = 0;
-    cudaFuncAttributes attr{};
-    if (cudaFuncGetAttributes(&attr, kernel) != cudaSuccess ||
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)(kMaxSmemPerBlock - attr.sharedSizeBytes)) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, threads, smem) != cudaSuccess)
-        return 0;
-    n = sms * (per > 0 ? per : 1);
-    blocks[dev].store(n, std::memory_order_relaxed);
-    return n;
 }
 }  // namespace glr
 

@@ -18,11 +18,10 @@
 // tile without a carry waits for is therefore done or under way, and waiting ends; waits are bounded all the same.
 #pragma once
 
-#include <atomic>
-
 #include "glr_math.cuh"
 #include "mixer.h"
 #include "mixer_common.cuh"
+#include "residency.h"
 
 namespace gdn {
 namespace glr {
@@ -31,14 +30,6 @@ constexpr int kTile = kGlrTile;                  // checkpoints are tile entries
 constexpr int kGroup = 8, kSpan = kGroup * kGroup;      // tiles a group, and a block of groups
 constexpr unsigned kEmpty = 0xffffffffu;
 constexpr unsigned long long kWaitNs = 2000000000ull;
-
-// How many blocks of a kernel with this much dynamic shared memory the device holds at once (persistent kernels launch no
-// more), asked once per device; 0 if a query failed.
-constexpr int kDevices = 64;
-struct Residency {
-    std::atomic<int> blocks[kDevices]{};
-    int get(const void* kernel, int threads, int smem);
-};
 
 // A scan is launched behind the clearing of its workspace (mix::launch_behind).  The clearing starts after all earlier
 // work of the stream; the scan's blocks start while it runs, and touch memory only after their wait for it (against a memset

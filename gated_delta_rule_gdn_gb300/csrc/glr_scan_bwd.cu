@@ -487,10 +487,10 @@ cudaError_t bwd(const GlrArgs& a, const BwdSpace& sp, cudaStream_t s) {
     const auto kernel = glr_bwd_kernel<Tx, Tg, S, PACKED>;
     const int smem = kBuffers * S::L * S::kThreads * S::V * (int)(sizeof(Tg) + (a.gi ? 3 : 2) * sizeof(Tx));
     static Residency res[2];                     // without and with the input gate
-    const int blocks = res[a.gi != nullptr].get(reinterpret_cast<const void*>(kernel), S::kBlock, smem);
-    if (blocks == 0) return cudaGetLastError();
-    const cudaError_t e = mix::launch_behind(kernel, x.total < blocks ? x.total : blocks, S::kBlock, smem, l.bytes > 0, s, a, x,
-                                             sp.part);
+    int blocks = 0;
+    cudaError_t e = res[a.gi != nullptr].get(reinterpret_cast<const void*>(kernel), S::kBlock, smem, &blocks);
+    if (e != cudaSuccess) return e;
+    e = mix::launch_behind(kernel, x.total < blocks ? x.total : blocks, S::kBlock, smem, l.bytes > 0, s, a, x, sp.part);
     if (e != cudaSuccess || !a.dA) return e;
     return mix::launch_behind(glr_param_kernel, dim3((a.D + 31) / 32, 2), 256, 0, true, s, sp.part, a.B * l.tiles, a.D, a.dA,
                               a.ddt);

@@ -1,0 +1,59 @@
+"""Host side of the operators around the delta rule.  No GPU is needed."""
+import os
+import shutil
+import subprocess
+
+import pytest
+
+from gated_delta_rule_gdn_gb300 import build
+
+# A runtime whose calls succeed, but for the one named in FAIL; the current device is DEVICE.
+RUNTIME = r'''
+#include "residency.h"
+#include <cstdio>
+#include <cstdlib>
+#include <cstring>
+static const char* fail;
+static int device, asked;
+static cudaError_t answer(const char* name) { return fail && !strcmp(fail, name) ? cudaErrorInvalidValue : cudaSuccess; }
+extern "C" {
+cudaError_t cudaGetDevice(int* d) { *d = device; return answer("device"); }
+cudaError_t cudaFuncGetAttributes(cudaFuncAttributes* a, const void*) { a->sharedSizeBytes = 1024; return answer("attributes"); }
+cudaError_t cudaFuncSetAttribute(const void*, cudaFuncAttribute, int v) { return v == 226 * 1024 ? answer("shared") : cudaErrorUnknown; }
+cudaError_t cudaDeviceGetAttribute(int* v, cudaDeviceAttr, int d) { *v = 152; return d == device ? answer("sms") : cudaErrorUnknown; }
+cudaError_t cudaOccupancyMaxActiveBlocksPerMultiprocessor(int* n, const void*, int, size_t) { ++asked; *n = 2; return answer("occupancy"); }
+}
+int main(int argc, char** argv) {
+    device = atoi(argv[1]);
+    fail = argc > 2 ? argv[2] : nullptr;
+    static gdn::Residency r;
+    int a = 0, b = 0;
+    const cudaError_t e = r.get(&r, 192, 1000, &a), f = r.get(&r, 192, 1000, &b);
+    printf("%d %d %d %d %d\n", (int)e, (int)f, a, b, asked);
+}
+'''
+
+
+@pytest.fixture(scope="module")
+def residency(tmp_path_factory):
+    d = tmp_path_factory.mktemp("residency")
+    (d / "main.cpp").write_text(RUNTIME)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(build._nvcc())))
+    subprocess.run([shutil.which("g++") or "c++", "-std=c++17", "-I", os.path.join(cuda, "include"), "-I", build.CSRC,
+                    "-I", build.INCLUDE, "-x", "c++", os.path.join(build.CSRC, "residency.cu"), str(d / "main.cpp"),
+                    "-o", str(d / "run")], check=True)
+    return lambda *args: [int(v) for v in subprocess.run([str(d / "run"), *map(str, args)], check=True, capture_output=True,
+                                                         text=True).stdout.split()]
+
+
+@pytest.mark.parametrize("device", [0, 63, 64, 1000])
+def test_resident_blocks_of_any_device(residency, device):
+    first, second, a, b, asked = residency(device)
+    assert (first, second, a, b) == (0, 0, 304, 304)
+    assert asked == (1 if device < 64 else 2)
+
+
+@pytest.mark.parametrize("what", ["device", "attributes", "shared", "sms", "occupancy"])
+@pytest.mark.parametrize("device", [0, 64])
+def test_a_failed_query_is_an_error(residency, device, what):
+    assert residency(device, what)[:2] == [1, 1]
