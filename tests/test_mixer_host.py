@@ -3,8 +3,11 @@ import os
 import shutil
 import subprocess
 
+import numpy as np
 import pytest
 
+import mixer_reference as R
+import mixer_reference_flat as F
 from gated_delta_rule_gdn_gb300 import build
 
 # A runtime whose calls succeed, but for the one named in FAIL; the current device is DEVICE.
@@ -57,3 +60,23 @@ def test_resident_blocks_of_any_device(residency, device):
 @pytest.mark.parametrize("device", [0, 64])
 def test_a_failed_query_is_an_error(residency, device, what):
     assert residency(device, what)[:2] == [1, 1]
+
+
+@pytest.mark.parametrize("W", [2, 3, 4])
+@pytest.mark.parametrize("cu", [None, [0, 0, 1, 3, 6, 6, 20, 22]])
+@pytest.mark.parametrize("silu,given", [(True, True), (False, False)])
+def test_flat_convolution_reference(W, cu, silu, given):
+    """The whole-array reference against the one that goes token by token (sums of up to 22 terms in 64 bits)."""
+    rng = np.random.default_rng(W)
+    B, T, D = (1, 22, 3) if cu else (2, 11, 3)
+    N = len(cu) - 1 if cu else B
+    x, dy, w, b = rng.normal(size=(B, T, D)), rng.normal(size=(B, T, D)), rng.normal(size=(D, W)), rng.normal(size=D)
+    h0, dhT = rng.normal(size=(2, N, W - 1, D)) if given else (None, None)
+    got = F.conv(x, w, dy, b, silu, h0, dhT, cu)
+    y, hT = R.conv_fwd(x, w, b, silu, h0, cu)
+    want = dict(R.conv_bwd(x, w, dy, b, silu, h0, dhT, cu), y=y, hT=hT)
+    mags = want.pop("abs")
+    for name, v in want.items():
+        assert np.allclose(got[name], v, rtol=1e-13, atol=1e-13), name
+    for name, v in mags.items():
+        assert np.allclose(got["abs"][name], v, rtol=1e-13), name
