@@ -37,6 +37,7 @@ gdn_status ok() {
 }
 
 gdn_status cuda_fail(cudaError_t e, const char* what) {
+    (void)cudaGetLastError();   // reported here: the next call's launch checks must not find it
     return fail(GDN_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
 }
 

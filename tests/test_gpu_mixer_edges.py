@@ -204,3 +204,20 @@ def test_head_norm_without_weights_takes_no_workspace():
     assert call(False) == before
     assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
     assert call(True) > before                            # with weights the C ABI allocates for itself
+
+
+# --------------------------------------------------------------------------------------------------------- errors
+
+def test_a_failed_call_does_not_fail_the_next():
+    """A request whose workspace no device can hold ends with the allocation's error, and the call after it is all right."""
+    lib = gdn.load()
+    total = torch.cuda.get_device_properties(0).total_memory
+    B, T, H = 1 << 17, 1, 120
+    assert gdn.workspace_size(False, B, T, H, 128, 128, 64, BF) > 1.5 * total     # (so nothing is launched)
+    x, h = torch.ones(2, 64, device="cuda"), torch.zeros(2, 64, device="cuda")
+    p = x.data_ptr()
+    assert lib.gdn_chunk_fwd(p, p, p, p, p, 1.0, None, 0, None, None, 0, p, B, T, H, 128, 128, 64, 1, 0,
+                             torch.cuda.current_stream().cuda_stream) == 3
+    assert "gdn_chunk_fwd" in gdn.last_error()
+    o = gdn.glr_step(x, -x, h)
+    assert torch.equal(o, x) and torch.equal(h, x)
