@@ -15,7 +15,6 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
-#include <cstring>
 #include <optional>
 #include <string>
 #include <vector>
@@ -85,15 +84,17 @@ struct Args {
                 at = 0;
                 while (at < n && PyUnicode_Compare(s.names[at], name) != 0) ++at;
             }
-            if (at == n)
-                raise(PyExc_TypeError, std::string(s.fn) + "() got an unexpected keyword argument '" + PyUnicode_AsUTF8(name) + "'");
-            if (at < nargs)
-                raise(PyExc_TypeError, std::string(s.fn) + "() got multiple values for argument '" + PyUnicode_AsUTF8(name) + "'");
+            // (a name may be text that has no UTF-8 form: %U prints any)
+            if (at == n) PyErr_Format(PyExc_TypeError, "%s() got an unexpected keyword argument '%U'", s.fn, name);
+            else if (at < nargs) PyErr_Format(PyExc_TypeError, "%s() got multiple values for argument '%U'", s.fn, name);
+            if (at == n || at < nargs) throw Raised{};
             v[at] = args[nargs + i];
         }
         for (int i = 0; i < s.required; ++i)
-            if (!v[i])
-                raise(PyExc_TypeError, std::string(s.fn) + "() missing argument '" + PyUnicode_AsUTF8(s.names[i]) + "'");
+            if (!v[i]) {
+                PyErr_Format(PyExc_TypeError, "%s() missing argument '%U'", s.fn, s.names[i]);
+                throw Raised{};
+            }
         for (int i = 0; i < n; ++i)
             if (v[i] == Py_None) v[i] = nullptr;
     }
@@ -432,9 +433,9 @@ struct Qk {
         wk = dense_f32(v[1], "k_weight", {d}, qx);
         norm = GDN_NORM_RMS;
         if (v[2]) {
-            const char* s = PyUnicode_Check(v[2]) ? PyUnicode_AsUTF8(v[2]) : nullptr;
-            if (s && !std::strcmp(s, "l2")) norm = GDN_NORM_L2;
-            else if (!s || std::strcmp(s, "rms")) value_error("norm must be 'rms' or 'l2'");
+            const auto is = [&](const char* n) { return PyUnicode_CompareWithASCIIString(v[2], n) == 0; };
+            if (!PyUnicode_Check(v[2]) || (!is("rms") && !is("l2"))) value_error("norm must be 'rms' or 'l2'");
+            if (is("l2")) norm = GDN_NORM_L2;
         }
         eps = 1e-6f;
         if (v[3]) {
