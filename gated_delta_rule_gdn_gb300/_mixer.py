@@ -59,6 +59,9 @@ def native():
         if not os.path.exists(path):
             raise RuntimeError(f"the binding is not built ({path}); run "
                                "`python -c 'import __graft_entry__ as g; g.build()'` first")
+        if not _build.native_current():
+            raise RuntimeError(f"the binding ({path}) was built with another torch or Python; run "
+                               "`python -c 'import __graft_entry__ as g; g.build()'` again")
         loader = importlib.machinery.ExtensionFileLoader("_native", path)
         module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_native", loader))
         loader.exec_module(module)

@@ -5,7 +5,9 @@ objects link into gated_delta_rule_gdn_gb300/libgdn_gb300.so.  There is no
 cmake and no torch extension machinery: the library is plain C ABI.  The
 Python extension module csrc/torch_binding.cpp (tensor checks and allocation
 for some entry points) compiles beside them with the host compiler against
-torch's headers, into gated_delta_rule_gdn_gb300/_native.so.
+torch's headers, into gated_delta_rule_gdn_gb300/_native.so.  It fits the
+torch and the Python it was built with alone, so a stamp beside the objects
+names them, and another torch or Python means another build.
 
 Environment knobs:
   GDN_NVCC          nvcc to use (default: nvcc on PATH, else /usr/local/cuda/bin/nvcc)
@@ -18,6 +20,7 @@ import concurrent.futures as cf
 import glob
 import importlib.util
 import os
+import platform
 import shutil
 import subprocess
 import sys
@@ -29,6 +32,7 @@ INCLUDE = os.path.join(os.path.dirname(PKG), "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgdn_gb300.so")
 NATIVE = os.path.join(PKG, "_native.so")
+STAMP = os.path.join(BUILD, "native.stamp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -43,8 +47,27 @@ def _sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
+def _torch_dir() -> str:
+    return os.path.dirname(importlib.util.find_spec("torch").origin)
+
+
+def _native_stamp() -> str:
+    """What the extension module depends on besides its source: the torch (its version file names the build) and the Python."""
+    with open(os.path.join(_torch_dir(), "version.py"), encoding="utf-8") as f:
+        return "\n".join([_torch_dir(), f.read(), sys.version, platform.machine()])
+
+
+def native_current() -> bool:
+    """Whether the extension module was built with the torch and the Python that are here."""
+    try:
+        with open(STAMP, encoding="utf-8") as f:
+            return os.path.exists(NATIVE) and f.read() == _native_stamp()
+    except OSError:
+        return False
+
+
 def _native_command(out: str) -> list:
-    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    torch = _torch_dir()
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
     include = os.path.join(torch, "include")
     return [os.environ.get("GDN_CXX") or shutil.which("g++") or "c++", "-O1", "-std=c++20", "-fPIC", "-shared",
@@ -60,7 +83,7 @@ def _deps():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(NATIVE):
+    if not os.path.exists(LIB) or not native_current():
         return False
     t = min(os.path.getmtime(LIB), os.path.getmtime(NATIVE))
     return all(os.path.getmtime(p) <= t for p in _deps())
@@ -95,7 +118,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         run(_native_command(out), "torch_binding.cpp")
         return out
 
-    srcs = _sources()
+    srcs, stamp = _sources(), _native_stamp()
     with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 4))) as ex:
         native = ex.submit(compile_native)
         objs = list(ex.map(compile_one, srcs))
@@ -107,6 +130,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIB)
     os.replace(native, NATIVE)
+    with open(STAMP + f".tmp{os.getpid()}", "w", encoding="utf-8") as f:
+        f.write(stamp)
+    os.replace(f.name, STAMP)
     return LIB
 
 

@@ -8,7 +8,7 @@ import pytest
 
 import mixer_reference as R
 import mixer_reference_flat as F
-from gated_delta_rule_gdn_gb300 import build
+from gated_delta_rule_gdn_gb300 import _mixer, build
 
 # A runtime whose calls succeed, but for the one named in FAIL; the current device is DEVICE.
 RUNTIME = r'''
@@ -80,3 +80,24 @@ def test_flat_convolution_reference(W, cu, silu, given):
         assert np.allclose(got[name], v, rtol=1e-13, atol=1e-13), name
     for name, v in mags.items():
         assert np.allclose(got["abs"][name], v, rtol=1e-13), name
+
+
+@pytest.mark.parametrize("change", ["torch", "python", "place", "gone"])
+def test_another_torch_or_python_means_another_build(change, monkeypatch, tmp_path):
+    """The extension module is of one torch and one Python: with another it is neither up to date nor loaded."""
+    build.build()
+    assert build.up_to_date() and build.native_current()
+    version = open(os.path.join(build._torch_dir(), "version.py"), encoding="utf-8").read()
+    if change in ("torch", "place"):
+        (tmp_path / "version.py").write_text(version + ("git_version = 'another'\n" if change == "torch" else ""))
+        monkeypatch.setattr(build, "_torch_dir", lambda: str(tmp_path))
+    elif change == "python":
+        monkeypatch.setattr(build.sys, "version", "3.99.0")
+    else:
+        monkeypatch.setattr(build, "STAMP", str(tmp_path / "no.stamp"))
+    assert not build.native_current() and not build.up_to_date()
+    monkeypatch.setattr(_mixer, "_NATIVE", None)
+    with pytest.raises(RuntimeError, match="another torch or Python"):
+        _mixer.native()
+    monkeypatch.undo()
+    assert build.up_to_date() and _mixer.native()
