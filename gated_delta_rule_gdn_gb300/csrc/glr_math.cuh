@@ -2,7 +2,8 @@
 //   log a = g, or -exp(A_log) softplus(g + dt_bias);   u = s sigma(i) x,   s = sqrt(1 - a^2) or 1.
 // Written so that nothing cancels: a and a - 1 come from one polynomial, 1 - a^2 is -(a - 1)(2 + (a - 1)), softplus is
 // max(z, 0) + log1p(exp(-|z|)).  The scans spend about as long on these as on their memory traffic, so each is kept to
-// as few instructions as its accuracy allows; the polynomials are minimax fits (Remez exchange) of this file's own.
+// as few instructions as its accuracy allows; the polynomials are minimax fits (Remez exchange) of this file's own;
+// the bounds stated with them are of the fp32 coefficients as they stand here, before the rounding of the evaluation.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -39,7 +40,7 @@ __device__ __forceinline__ f2 mul2(f2 a, f2 b) { f2 r; asm("mul.rn.f32x2 %0, %1,
 __device__ __forceinline__ f2 add2(f2 a, f2 b) { f2 r; asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b)); return r; }
 
 // a = exp(x) and e = exp(x) - 1 for x <= 88.  x = k ln 2 + r, |r| <= ln 2 / 2, with ln 2 split in two parts (Cody and
-// Waite); p = exp(r) - 1 = r + r^2 Q(r), off by less than 2^-28; a = 2^k + 2^k p, e = (2^k - 1) + 2^k p.
+// Waite); p = exp(r) - 1 = r + r^2 Q(r), off by less than 2^-27.7; a = 2^k + 2^k p, e = (2^k - 1) + 2^k p.
 // Rounding a once matters: a memory of n tokens multiplies a one-sided error of a by n (a decay taken from expf was off
 // by 4e-5 after 10^4 tokens).  Below -88 (where 2^k becomes 0) the decay is exactly 0.
 // x is brought to -88 in place: log a times a gradient that holds a factor a is then 0 there, not NaN.
@@ -77,7 +78,7 @@ __device__ __forceinline__ void decay(float& x0, float& x1, Decay& d0, Decay& d1
     unpack(fma2(sc, p, add2(sc, both_of(-1.f))), d0.e, d1.e);
 }
 
-// exp(-|z|) carries both softplus and sigma.  log1p(q) = q P(q) on [0, 1], off by less than 2^-25 of itself.
+// exp(-|z|) carries both softplus and sigma.  log1p(q) = q P(q) on [0, 1], off by less than 2^-23.9 of itself.
 __device__ __forceinline__ float tail(float z) { return ex2(fabsf(z) * -kLog2e); }
 __device__ __forceinline__ float softplus(float z, float q) {
     float s = fmaf(q, 5.3840620e-3f, -3.0110965e-2f);

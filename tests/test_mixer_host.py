@@ -1,5 +1,6 @@
 """Host side of the operators around the delta rule.  No GPU is needed."""
 import os
+import re
 import shutil
 import subprocess
 
@@ -101,3 +102,39 @@ def test_another_torch_or_python_means_another_build(change, monkeypatch, tmp_pa
         _mixer.native()
     monkeypatch.undo()
     assert build.up_to_date() and _mixer.native()
+
+
+def _coefficients(function):
+    """The decimal constants of one function of glr_math.cuh, as the fp32 numbers they become."""
+    text = open(os.path.join(build.CSRC, "glr_math.cuh")).read()
+    body = text[text.index(function):]
+    return [float(np.float32(c)) for c in re.findall(r"-?\d+\.\d*(?:e[-+]?\d+)?(?=f\b)", body[:body.index("\n}")])]
+
+
+def _stated(which):
+    """The bound that a comment of glr_math.cuh gives behind these words."""
+    text = open(os.path.join(build.CSRC, "glr_math.cuh")).read()
+    return 2.0 ** -float(re.search(r"off by less than 2\^-([\d.]*\d)", text[text.index(which):]).group(1))
+
+
+def test_polynomial_of_the_decay():
+    """The bound that the comment states, for the coefficients in 64 bits; both forms have the same ones."""
+    one, two = _coefficients("Decay decay(float& x) {"), _coefficients("void decay(float& x0, float& x1, Decay& d0, Decay& d1) {")
+    assert one[3:10] == two[4:11] and one[9] == 0.5
+    low, high = one[3], one[4]                            # ln 2 = -(high + low), high with zeros behind
+    assert abs(-high - low - np.log(2)) < 2.0 ** -36 and (high * 2 ** 9).is_integer()
+    r = np.linspace(-0.5 * np.log(2), 0.5 * np.log(2), 2_000_001)
+    q = np.zeros_like(r)
+    for c in one[5:10]:
+        q = q * r + c
+    assert np.abs(r + r * r * q - np.expm1(r)).max() < _stated("p = exp(r) - 1")
+
+
+def test_polynomial_of_softplus():
+    one, two = _coefficients("float softplus(float z, float q) {"), _coefficients("void softplus(float z0")
+    q = np.linspace(2.0 ** -30, 1, 2_000_001)
+    p = np.zeros_like(q)
+    for c in one[:9]:
+        p = p * q + c
+    assert one[:9] == two[:9]
+    assert np.abs(q * p / np.log1p(q) - 1).max() < _stated("log1p(q) = q P(q)")
