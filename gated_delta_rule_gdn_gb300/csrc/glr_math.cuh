@@ -79,7 +79,13 @@ __device__ __forceinline__ void decay(float& x0, float& x1, Decay& d0, Decay& d1
 }
 
 // exp(-|z|) carries both softplus and sigma.  log1p(q) = q P(q) on [0, 1], off by less than 2^-23.9 of itself.
-__device__ __forceinline__ float tail(float z) { return ex2(fabsf(z) * -kLog2e); }
+// It is the square of its root, which is a normal number down to z = -174: a subnormal exp(-|z|) still makes 1 - a^2 and the
+// gates' gradients what they are.
+__device__ __forceinline__ float tail_root(float z) { return ex2(fabsf(z) * (-0.5f * kLog2e)); }
+__device__ __forceinline__ float tail(float z) {
+    const float h = tail_root(z);
+    return h * h;
+}
 __device__ __forceinline__ float softplus(float z, float q) {
     float s = fmaf(q, 5.3840620e-3f, -3.0110965e-2f);
     s = fmaf(s, q, 7.9210736e-2f);
@@ -93,7 +99,7 @@ __device__ __forceinline__ float softplus(float z, float q) {
 }
 // of two logits, times nA
 __device__ __forceinline__ void softplus(float z0, float z1, float nA0, float nA1, float& r0, float& r1) {
-    const f2 q = pack(tail(z0), tail(z1));
+    const f2 h = pack(tail_root(z0), tail_root(z1)), q = mul2(h, h);
     f2 s = fma2(q, both_of(5.3840620e-3f), both_of(-3.0110965e-2f));
     s = fma2(s, q, both_of(7.9210736e-2f));
     s = fma2(s, q, both_of(-1.3746622e-1f));

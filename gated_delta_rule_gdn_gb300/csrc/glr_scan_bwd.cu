@@ -373,12 +373,15 @@ glr_bwd_kernel(const GlrArgs a, const Exchange x, float* part) {
             for (int v = 0; v < V; ++v) dz[v] = dla[v];
             if (a.A_log) {
                 const Vec<Tg, V> g = buf_g(i)[j * kThreads];
-                float t[V];
+                float t[V], z[V], ez[V];
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    const float z = g.get(v) + ch[v].dt;
-                    t[v] = ch[v].neg_eA * sigmoid(z, tail(z));
+                    z[v] = g.get(v) + ch[v].dt;
+                    ez[v] = tail_root(z[v]);
                 }
+                mix::mul_row(ez, ez, ez);
+#pragma unroll
+                for (int v = 0; v < V; ++v) t[v] = ch[v].neg_eA * sigmoid(z[v], ez[v]);
                 mix::mul_row(dz, dz, t);
                 if (j < n) {
                     mix::fma_row(pA, dla, q.la[j], pA);

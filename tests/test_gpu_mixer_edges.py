@@ -137,6 +137,21 @@ def test_recurrence_decay_next_to_one(dtype, count):
         each(got[n], want[n], n, rel)
 
 
+@pytest.mark.parametrize("count", [32, 31])
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_recurrence_decay_logits_far_below_zero(dtype, count):
+    """softplus(z) = exp(z) as a subnormal number, in steps of 2^-149, which the input factor (about 1e-19) still shows."""
+    gen = torch.Generator().manual_seed(6)
+    x, i = ((torch.randn(count, generator=gen) + 0.1).to(dtype).cuda() for _ in range(2))
+    h0, z = torch.zeros(count, device="cuda"), torch.linspace(-98, -86, 32)[:count].cuda()
+    A = torch.full((count,), 1.0, device="cuda")
+    got, want = glr_one_token(x, z, i, h0, A, torch.zeros_like(A), normalize=True)
+    small = np.exp(f64(z))
+    rel = (np.abs(f64(i)) + np.abs(f64(z)) + 32) * 2.0 ** -22 + 2 * 2.0 ** -149 / small
+    for n in ("hT", "step", "dx", "di", "dA_log", "dg", "ddt_bias"):
+        each(got[n], want[n], n, rel)
+
+
 # ----------------------------------------------------------------------------------------------- query/key head norm
 
 @pytest.mark.parametrize("interleaved", [False, True])
