@@ -5,7 +5,8 @@ The entry points themselves are in the extension module _native (csrc/torch_bind
 allocates outputs and workspaces, and calls the C ABI; see their docstrings.  Inputs may be cut out of a wider projection
 (their rows must be contiguous and evenly spaced); outputs are contiguous.  Calls run on the current stream, or on
 ``stream``; with ``stream`` their outputs and workspaces are allocated on it too, so that the allocator does not hand
-their memory to other streams while the call runs.
+their memory to other streams while the call runs.  Inputs, and buffers that are handed in, are the caller's to have ready
+on that stream and to keep until its work is done, as for any torch operation on a stream that is not the tensors' own.
 """
 from __future__ import annotations
 
