@@ -1,9 +1,8 @@
 // Gated linear recurrence: scan forward, and the decode step.
 //   h_t = a_t h_{t-1} + u_t,  o_t = h_t;  see glr_math.cuh for a and u, glr_scan.cuh for the tiling and the carry.
 // x, g and in_gate are read once and o is written once (268 MB for B4 T4096 D2048 in bf16, 40 us at the copy rate).  Measured
-// 87 us with both activations and the normalisation (without them 74 us of 89, before the scan started behind its
-// clearing): at 60 instructions an element and 2.3 instructions a cycle the kernel is bound by issue and by the latency
-// of 12 warps an SM, not by HBM.  The shape of a block (16 lanes x 4 channels x 8 tokens, 32 elements a thread in
+// 82 us with both activations and the normalisation, 61 with the normalisation alone, 131 in fp32 (537 MB): at 60 instructions
+// an element and about 2 instructions a cycle the kernel is bound by issue and by the latency of 12 warps an SM, not by HBM.  The shape of a block (16 lanes x 4 channels x 8 tokens, 32 elements a thread in
 // registers) trades warps for instructions: runs of 4 tokens, 95 us.
 
 #include <type_traits>
@@ -376,7 +375,7 @@ cudaError_t clear(void* ws, size_t bytes, cudaStream_t s) {
 }  // namespace glr
 
 // Whether rows can be read and written V channels at a time.  The widest access that everything is aligned to is taken
-// (B4 T4096 D2048 in bf16: forward 87, 99 and 140 us with 4, 2 and 1; backward 197 us with 2, 250 with 1).
+// (B4 T4096 D2048 in bf16: after a flush of L2: forward 87, 102 and 142 us with 4, 2 and 1; backward 199 us with 2, 258 with 1).
 bool glr_vector(const GlrArgs& a, int V) {
     const size_t es = a.bf16 ? 2 : 4, gs = a.g_bf16 ? 2 : 4;
     const auto ok = [V](const void* p, size_t size) { return reinterpret_cast<uintptr_t>(p) % (V * size) == 0; };

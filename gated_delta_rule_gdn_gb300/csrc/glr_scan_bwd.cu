@@ -5,7 +5,7 @@
 // the same recurrence; G is carried between tiles in reverse (glr_scan.cuh).  So x, g, in_gate and dO are read once and
 // the three gradients written once.  The per-channel sums of A_log and dt_bias leave the block as a row of partial sums
 // that a second kernel adds in order.
-// 470 MB for B4 T4096 D2048 in bf16, 69 us at the copy rate; measured 197 us.  Bound by issue: 160 instructions an element
+// 470 MB for B4 T4096 D2048 in bf16, 69 us at the copy rate; measured 197 us.  In fp32 279 us (939 MB). Bound by issue: 159 instructions an element
 // (8 special functions, two polynomials, five products of stage two) at 2.3 to 2.6 a cycle.  Keeping all seven factors of the
 // gradients from stage one, instead of forming them again in stage two, took 314 us: one tile at a time in registers.
 

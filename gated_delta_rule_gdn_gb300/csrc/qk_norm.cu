@@ -4,9 +4,9 @@
 //   interleaved.
 // Backward: dy = the output's gradient turned back, dw = sum dy x r, e = w dy, dx = r (e - c r^2 x sum(x e)).
 // Bound by HBM: every head is read once and written once (backward: read with its gradient, written once).  Measured: 16,384
-// tokens x 32 heads of 128 in bf16 without rotation 43.7 us (268 MB, 90 % of the copy rate); 16,384 tokens x 40 heads, half of
-// each rotated, 66 us forward (336 MB, 75 %) and 107 us backward (503 MB, 69 %), where the shuffles and the angles' latency
-// show.
+// tokens x 32 heads of 128 in bf16 without rotation 43.7 us forward (268 MB, 90 % of the copy rate) and 68 us backward (403 MB,
+// 88 %); 16,384 tokens x 40 heads, half of each rotated, 65 us forward (336 MB, 76 %) and 107 us backward (503 MB, 69 %), where
+// the shuffles and the angles' latency show, in fp32 127 (78 %) and 167 us (89 %).
 //
 // Vector kernels: G neighbouring lanes hold a head, E = 8 or 4 channels each, and a group of lanes takes N heads of one token,
 // so that the token's angles are read once for them.  Blocks are persistent; each thread's inputs of the next shares come
@@ -453,7 +453,7 @@ __global__ void __launch_bounds__(256) qk_dw_kernel(const float* part, int rows,
 }
 
 // The channels a lane takes in the vector kernels: 8 or 4, whichever everything goes in steps of, or 0 if neither (twice 16,384
-// tokens x 32 heads of 128 in bf16: forward 78 us, 104, and 250 with the scalar kernel; backward 168 to 178, 188 to 198, and 464).
+// tokens x 32 heads of 128 in bf16: forward 78 us, 103, and 250 with the scalar kernel; backward 109, 134 and 400).
 int channels_a_lane(const QkNormArgs& a, bool backward) {
     for (int E = 8; E >= 4; E /= 2) {
         const size_t size = (a.bf16 ? 2 : 4) * E, bytes = size < 16 ? size : 16;

@@ -3,8 +3,9 @@
 //   initial state (its last W - 1 inputs, oldest first) or zero.
 // Backward: ds = dy silu'(p), dx_t = sum_j w_j ds_{t + W - 1 - j}, dw_j = sum_t ds_t x_{t - W + 1 + j}, db = sum ds.
 // Bound by HBM: x is read once and y written once (backward: x and dy read once, dx written once).  Measured in bf16, width 4
-// with silu: 16,384 tokens x 6144 channels 69.8 us (403 MB, 85 % of the copy rate); 65,536 packed tokens x 4096 channels 172 us
-// forward (1.07 GB, 92 %) and 343 us backward (1.61 GB, 69 %; 29 instructions an element and 16 warps an SM show there).
+// with silu: 16,384 tokens x 6144 channels 69 us (403 MB, 86 % of the copy rate), in fp32 128 us (93 %) and 197 us backward (91 %);
+// 65,536 packed tokens x 4096 channels 166 us forward (1.07 GB, 95 %) and 341 us backward (1.61 GB, 70 %; 29 instructions an element
+// and 16 warps an SM show there).
 //
 // A thread walks a run of tokens of V neighbouring channels with the last W inputs in registers, a warp 32 V channels;
 // the W - 1 tokens around a run that its neighbours walk too come out of L2.  The backward walks W - 1 tokens further, for
@@ -493,8 +494,8 @@ __global__ void __launch_bounds__(128) conv_step_kernel(const ConvArgs a, const 
     }
 }
 
-// Whether rows can be accessed V channels at a time (4 where they can, else 1: 16,384 tokens x 2048 channels 33 us and 49 us
-// forward, 65 and 103 us backward).
+// Whether rows can be accessed V channels at a time (4 where they can, else 1: 16,384 tokens x 2048 channels 31 us and 50 us
+// forward, 64 and 99 us backward).
 bool vector_ok(const ConvArgs& a, int V, const void* state = nullptr, const void* state_out = nullptr) {
     const size_t bytes = V * (a.bf16 ? 2 : 4);
     const auto al = [&](const void* p) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; };

@@ -578,7 +578,8 @@ typedef enum gdn_norm {
  * with (i, j) = (m, m + rotary_dim/2), or (2m, 2m + 1) when interleaved, and cos[p, m], sin[p, m].
  *   q [n_tokens, H_q, d], k [n_tokens, H_k, d]  dtype, with token and head strides in elements
  *   q_weight, k_weight   [d] fp32, or NULL (ones)
- *   eps                  > 0 (a head of zeros stays zero)
+ *   eps                  > 0 (a head of zeros stays zero; one whose sum of squares is past the range of fp32, so with
+ *                        entries beyond about 1e19, comes out as zeros)
  *   cos, sin             [n_pos, rotary_dim / 2] fp32; not read when rotary_dim is 0
  *   positions            [n_tokens] int32 device, clamped into [0, n_pos); NULL: the token's index
  *                        modulo T (sequences of T tokens, T <= n_pos)
