@@ -1,5 +1,5 @@
-"""Binding of the operators around the delta rule: the gated linear recurrence, the query/key head norm with rotation, and
-the short causal convolution.
+"""Binding of the operators around the delta rule (the gated linear recurrence, the query/key head norm with rotation, the
+short causal convolution) and beside it (linear attention with a decay for each head, the paged key-value cache).
 
 The entry points themselves are in the extension module _native (csrc/torch_binding.cpp), which checks the tensors,
 allocates outputs and workspaces, and calls the C ABI; see their docstrings.  Inputs may be cut out of a wider projection
@@ -19,8 +19,10 @@ from . import build as _build
 from ._binding import _check, load
 
 ENTRIES = ("glr_scan_fwd", "glr_scan_bwd", "glr_step", "gdn_qk_norm_fwd", "gdn_qk_norm_bwd", "gdn_short_conv_fwd",
-           "gdn_short_conv_bwd", "gdn_short_conv_step")
-_SIZES = ("glr_workspace_size", "gdn_qk_norm_workspace_size", "gdn_short_conv_workspace_size")
+           "gdn_short_conv_bwd", "gdn_short_conv_step", "lin_chunk_fwd", "lin_chunk_bwd", "lin_recurrent_step", "paged_append",
+           "paged_attn_step")
+_SIZES = ("glr_workspace_size", "gdn_qk_norm_workspace_size", "gdn_short_conv_workspace_size", "lin_workspace_size",
+          "paged_attn_workspace_size")
 
 _NATIVE = None
 
@@ -43,6 +45,13 @@ def declare(lib):
         "gdn_short_conv_bwd": [vp] * 3 + [i, vp, vp, vp, vp, i, vp, vp, vp, vp, i, i, i, i, i64, i, vp, sz, vp],
         "gdn_short_conv_workspace_size": [i, i, i, i, szp],
         "gdn_short_conv_step": [vp] * 3 + [i, vp, vp, vp, i, i, i, i64, i, vp],
+        "lin_chunk_fwd": [vp] * 4 + [i, fp, vp, vp, vp, i, vp] + [i] * 6 + [i64] * 6 + [i, i, vp, sz, vp],
+        "lin_chunk_bwd": [vp] * 4 + [i, fp] + [vp] * 4 + [i] + [vp] * 5 + [i] * 6 + [i64] * 6 + [i, i, vp, sz, vp],
+        "lin_workspace_size": [i] * 8 + [szp],
+        "lin_recurrent_step": [vp] * 4 + [i, fp, vp, vp, vp] + [i] * 5 + [i64] * 6 + [i, vp],
+        "paged_append": [vp] * 7 + [i, i, i, vp, i64, i] + [i64] * 6 + [vp],
+        "paged_attn_step": [vp, vp, fp, vp, vp, i, i64, i64, vp, sz, vp],
+        "paged_attn_workspace_size": [i] * 6 + [szp],
     }.items():
         f = getattr(lib, name)
         f.restype, f.argtypes = i, args
@@ -89,4 +98,18 @@ def short_conv_workspace_size(B: int, T: int, D: int, W: int) -> int:
     """Device workspace bytes of gdn_short_conv_bwd (C ABI gdn_short_conv_workspace_size)."""
     out = ctypes.c_size_t(0)
     _check(load().gdn_short_conv_workspace_size(B, T, D, W, ctypes.byref(out)))
+    return out.value
+
+
+def lin_workspace_size(B: int, T: int, H_k: int, H: int, d_k: int, d_v: int, n_seqs: int = 0, backward: bool = False) -> int:
+    """Device workspace bytes of lin_chunk_fwd, or lin_chunk_bwd (C ABI lin_workspace_size)."""
+    out = ctypes.c_size_t(0)
+    _check(load().lin_workspace_size(int(backward), B, T, H_k, H, d_k, d_v, n_seqs, ctypes.byref(out)))
+    return out.value
+
+
+def paged_attn_workspace_size(N: int, H_q: int, H_k: int, d: int, max_pages: int, page_size: int) -> int:
+    """Device workspace bytes of paged_attn_step (C ABI paged_attn_workspace_size)."""
+    out = ctypes.c_size_t(0)
+    _check(load().paged_attn_workspace_size(N, H_q, H_k, d, max_pages, page_size, ctypes.byref(out)))
     return out.value

@@ -1,0 +1,248 @@
+// C ABI of linear attention with a decay for each head (declared in include/gdn.h): argument checks, workspaces, dispatch.
+
+#include "lin.h"
+
+#include "internal.h"
+#include "mixer_check.h"
+
+namespace {
+
+using gdn::LinTok;
+using gdn::LinWalk;
+
+struct Sizes {
+    int B, T, Hk, H, dk, dv;
+    const int32_t* cu;
+    int n_seqs;
+    int N() const { return cu ? n_seqs : B; }
+    int64_t rows() const { return (int64_t)B * T; }
+    int group() const { return H / Hk; }
+};
+
+gdn_status check_sizes(const char* fn, const Sizes& z, gdn_dtype dtype, gdn_algo algo) {
+    if (!dtype_ok(dtype)) return fail(GDN_ERR_INVALID_ARG, "%s: unknown dtype %d", fn, (int)dtype);
+    if (algo != GDN_ALGO_AUTO && algo != GDN_ALGO_GENERIC && algo != GDN_ALGO_TCGEN05)
+        return fail(GDN_ERR_INVALID_ARG, "%s: algo must be GDN_ALGO_AUTO, _GENERIC or _TCGEN05 (got %d)", fn, (int)algo);
+    if (z.B < 1 || z.T < 0 || z.Hk < 1 || z.H < 1 || z.dk < 1 || z.dv < 1)
+        return fail(GDN_ERR_INVALID_ARG, "%s: need B, H_k, H, d_k, d_v >= 1 and T >= 0 (got %d, %d, %d, %d, %d, %d)", fn, z.B,
+                    z.Hk, z.H, z.dk, z.dv, z.T);
+    if (z.H % z.Hk)
+        return fail(GDN_ERR_INVALID_ARG, "%s: H=%d value heads are no multiple of H_k=%d key heads", fn, z.H, z.Hk);
+    if (z.dk > 256 || z.dv > 256)
+        return fail(GDN_ERR_UNSUPPORTED, "%s: head sizes must be 1..256 (got d_k=%d, d_v=%d)", fn, z.dk, z.dv);
+    if (z.rows() > kMaxRows)
+        return fail(GDN_ERR_UNSUPPORTED, "%s: B * T = %lld tokens is more than %lld", fn, (long long)z.rows(), (long long)kMaxRows);
+    if (z.cu || z.n_seqs) {
+        if (z.B != 1) return fail(GDN_ERR_INVALID_ARG, "%s: cu_seqlens needs B == 1 (got B=%d)", fn, z.B);
+        if (z.n_seqs < 1) return fail(GDN_ERR_INVALID_ARG, "%s: cu_seqlens needs n_seqs >= 1 (got %d)", fn, z.n_seqs);
+        if (!aligned(z.cu, 4)) return fail(GDN_ERR_INVALID_ARG, "%s: cu_seqlens is not 4-byte aligned", fn);
+    }
+    if (algo == GDN_ALGO_TCGEN05) return fail(GDN_ERR_UNSUPPORTED, "%s: the tensor-core path does not take this request", fn);
+    const int64_t most = (int64_t(1) << 31) - 1;       // blocks of a launch
+    if ((int64_t)z.N() > most / (8 * (int64_t)z.H) || gdn::lin_span_slots(z.rows(), z.N()) > most / z.H)
+        return fail(GDN_ERR_UNSUPPORTED, "%s: %d sequences of %d heads need more than 2^31 blocks", fn, z.N(), z.H);
+    if (z.rows() * z.H > (int64_t(1) << 40) / 256)
+        return fail(GDN_ERR_UNSUPPORTED, "%s: tokens times heads is more than 2^32", fn);
+    return GDN_OK;
+}
+
+gdn_status check_strides(const char* fn, const char* name, const LinTok& t, int d) {
+    if (t.tok < d || t.head < d || t.tok > (int64_t(1) << 31) || t.head > (int64_t(1) << 31))
+        return fail(GDN_ERR_INVALID_ARG, "%s: the token and head strides of %s must be %d..2^31 elements (got %lld, %lld)", fn,
+                    name, d, (long long)t.tok, (long long)t.head);
+    return GDN_OK;
+}
+
+LinWalk walk(const Sizes& z, const LinTok& a, const LinTok& b, const LinTok& c, int da, int dc, const float* g, int g_per_head,
+             gdn_dtype dtype) {
+    LinWalk w{};
+    w.a = a; w.b = b; w.c = c; w.da = da; w.dc = dc;
+    w.g = g;
+    w.g_tok = g_per_head ? 0 : z.H;
+    w.g_head = 1;
+    w.cu = z.cu; w.n_seqs = z.n_seqs; w.B = z.B; w.T = z.T; w.H = z.H;
+    w.bf16 = dtype == GDN_BF16;
+    return w;
+}
+void state(LinWalk& w, const float* in, float* out, int rows_step, int cols_step) {
+    w.s_in = in; w.s_out = out; w.s_r = rows_step; w.s_c = cols_step;
+}
+
+// Parts of the backward's workspace, each a multiple of 256 bytes (for either walk: which one it is goes by the buffers too).
+struct BwdParts {
+    size_t plus, minus, spans, anchors, part, group, bytes;
+    explicit BwdParts(const Sizes& z) {
+        size_t at = 0;
+        auto take = [&](size_t n) {
+            const size_t here = at;
+            at += (n + 255) / 256 * 256;
+            return here;
+        };
+        const size_t slots = (size_t)gdn::lin_span_slots(z.rows(), z.N()), heads = (size_t)z.H;
+        const size_t blocks = (size_t)gdn::lin_blocks(z.dk, false);
+        const size_t span = gdn::lin_span_floats(z.dv, z.dk, false), tc = gdn::lin_span_floats(z.dv, z.dk, true);
+        plus = take(4 * blocks * heads * (size_t)z.rows());
+        minus = take(4 * blocks * heads * (size_t)z.rows());
+        spans = take(4 * slots * heads * (span > tc ? span : tc));
+        anchors = take(4 * slots * heads * blocks);
+        part = take(8 * slots * heads);
+        group = take(z.group() > 1 ? 4 * (size_t)z.rows() * heads * (size_t)z.dk : 0);
+        bytes = at;
+    }
+};
+
+}  // namespace
+
+extern "C" {
+
+gdn_status lin_workspace_size(int backward, int B, int T, int H_k, int H, int d_k, int d_v, int n_seqs, size_t* bytes) {
+    const char* fn = "lin_workspace_size";
+    if (!bytes) return fail(GDN_ERR_INVALID_ARG, "%s: bytes is NULL", fn);
+    if (n_seqs < 0) return fail(GDN_ERR_INVALID_ARG, "%s: n_seqs must be >= 0 (got %d)", fn, n_seqs);
+    const Sizes z{B, T, H_k, H, d_k, d_v, n_seqs > 0 ? reinterpret_cast<const int32_t*>(uintptr_t(1) << 20) : nullptr, n_seqs};
+    GDN_TRY(check_sizes(fn, z, GDN_F32, GDN_ALGO_AUTO));
+    *bytes = backward ? BwdParts(z).bytes : 0;
+    return ok();
+}
+
+gdn_status lin_chunk_fwd(const void* q, const void* k, const void* v, const float* g, int g_per_head, float scale,
+                         const float* initial_state, float* final_state, const int32_t* cu_seqlens, int n_seqs, void* o,
+                         int B, int T, int H_k, int H, int d_k, int d_v, int64_t q_token_stride, int64_t q_head_stride,
+                         int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
+                         gdn_dtype dtype, gdn_algo algo, void* workspace, size_t workspace_bytes, void* stream) {
+    const char* fn = "lin_chunk_fwd";
+    const Sizes z{B, T, H_k, H, d_k, d_v, cu_seqlens, cu_seqlens ? n_seqs : 0};
+    GDN_TRY(check_sizes(fn, z, dtype, algo));
+    const size_t es = size_of(dtype);
+    const LinTok tq{q, q_token_stride, q_head_stride, z.group()}, tk{k, k_token_stride, k_head_stride, z.group()};
+    const LinTok tv{v, v_token_stride, v_head_stride, 1};
+    GDN_TRY(check_strides(fn, "q", tq, d_k));
+    GDN_TRY(check_strides(fn, "k", tk, d_k));
+    GDN_TRY(check_strides(fn, "v", tv, d_v));
+    if (T > 0) {
+        GDN_TRY(need(fn, "q", q, es));
+        GDN_TRY(need(fn, "k", k, es));
+        GDN_TRY(need(fn, "v", v, es));
+        GDN_TRY(need(fn, "g", g, 4));
+        GDN_TRY(need(fn, "o", o, es));
+    }
+    GDN_TRY(may(fn, "initial_state", initial_state, 4));
+    GDN_TRY(may(fn, "final_state", final_state, 4));
+    LinWalk w = walk(z, tq, tk, tv, d_k, d_v, g, g_per_head, dtype);
+    w.s_intra = w.s_inter = scale;
+    w.s_state = 1.f;
+    state(w, initial_state, final_state, d_v, 1);
+    w.out = o;
+    w.out_f32 = dtype == GDN_F32;
+    Workspace ws;
+    GDN_TRY(ws.get(fn, workspace, workspace_bytes, 0, static_cast<cudaStream_t>(stream)));
+    return finish(fn, gdn::launch_lin_walk_generic(w, ws.s), ws);
+}
+
+gdn_status lin_chunk_bwd(const void* q, const void* k, const void* v, const float* g, int g_per_head, float scale,
+                         const float* initial_state, const void* grad_o, const float* grad_final_state,
+                         const int32_t* cu_seqlens, int n_seqs, void* grad_q, void* grad_k, void* grad_v, float* grad_g,
+                         float* grad_initial_state, int B, int T, int H_k, int H, int d_k, int d_v, int64_t q_token_stride,
+                         int64_t q_head_stride, int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
+                         int64_t v_head_stride, gdn_dtype dtype, gdn_algo algo, void* workspace, size_t workspace_bytes,
+                         void* stream) {
+    const char* fn = "lin_chunk_bwd";
+    const Sizes z{B, T, H_k, H, d_k, d_v, cu_seqlens, cu_seqlens ? n_seqs : 0};
+    GDN_TRY(check_sizes(fn, z, dtype, algo));
+    const size_t es = size_of(dtype);
+    const int group = z.group();
+    const LinTok tq{q, q_token_stride, q_head_stride, group}, tk{k, k_token_stride, k_head_stride, group};
+    const LinTok tv{v, v_token_stride, v_head_stride, 1}, to{grad_o, (int64_t)H * d_v, d_v, 1};
+    GDN_TRY(check_strides(fn, "q", tq, d_k));
+    GDN_TRY(check_strides(fn, "k", tk, d_k));
+    GDN_TRY(check_strides(fn, "v", tv, d_v));
+    if (T > 0) {
+        GDN_TRY(need(fn, "q", q, es));
+        GDN_TRY(need(fn, "k", k, es));
+        GDN_TRY(need(fn, "v", v, es));
+        GDN_TRY(need(fn, "g", g, 4));
+        GDN_TRY(need(fn, "grad_o", grad_o, es));
+        GDN_TRY(need(fn, "grad_q", grad_q, es));
+        GDN_TRY(need(fn, "grad_k", grad_k, es));
+        GDN_TRY(need(fn, "grad_v", grad_v, es));
+    }
+    if (T > 0 || g_per_head) GDN_TRY(need(fn, "grad_g", grad_g, 4));
+    GDN_TRY(may(fn, "initial_state", initial_state, 4));
+    GDN_TRY(may(fn, "grad_final_state", grad_final_state, 4));
+    GDN_TRY(may(fn, "grad_initial_state", grad_initial_state, 4));
+    const BwdParts parts(z);
+    Workspace ws;
+    GDN_TRY(ws.get(fn, workspace, workspace_bytes, parts.bytes, static_cast<cudaStream_t>(stream)));
+    char* base = static_cast<char*>(ws.ptr);
+    auto part = [&](size_t at) { return reinterpret_cast<float*>(base + at); };
+
+    // dq, with the states at the spans' ends on the way
+    LinWalk w = walk(z, to, tv, tk, d_v, d_k, g, g_per_head, dtype);
+    w.s_intra = w.s_inter = scale;
+    w.s_state = 1.f;
+    state(w, initial_state, nullptr, 1, d_v);
+    w.out = group > 1 ? part(parts.group) : grad_q;
+    w.out_f32 = group > 1 || dtype == GDN_F32;
+    w.x = tq;
+    w.dots = part(parts.plus);
+    w.spans = part(parts.spans);
+    cudaError_t e = gdn::launch_lin_walk_generic(w, ws.s);
+    if (e == cudaSuccess && group > 1)
+        e = gdn::launch_lin_group_sum(part(parts.group), grad_q, w.bf16, z.rows(), H_k, group, d_k, ws.s);
+    // dk, from the last token to the first, with the states' inner products
+    w = walk(z, tv, to, tq, d_v, d_k, g, g_per_head, dtype);
+    w.rev = 1;
+    w.s_intra = w.s_state = scale;
+    w.s_inter = 1.f;
+    state(w, grad_final_state, nullptr, 1, d_v);
+    w.out = group > 1 ? part(parts.group) : grad_k;
+    w.out_f32 = group > 1 || dtype == GDN_F32;
+    w.x = tk;
+    w.dots = part(parts.minus);
+    w.spans = part(parts.spans);
+    w.anchors = part(parts.anchors);
+    if (e == cudaSuccess) e = gdn::launch_lin_walk_generic(w, ws.s);
+    if (e == cudaSuccess && group > 1)
+        e = gdn::launch_lin_group_sum(part(parts.group), grad_k, w.bf16, z.rows(), H_k, group, d_k, ws.s);
+    const int blocks = gdn::lin_blocks(d_k, false);
+    // dv, and the gradient of the initial state
+    w = walk(z, tk, tq, to, d_k, d_v, g, g_per_head, dtype);
+    w.rev = 1;
+    w.s_intra = w.s_state = scale;
+    w.s_inter = 1.f;
+    state(w, grad_final_state, grad_initial_state, d_v, 1);
+    w.out = grad_v;
+    w.out_f32 = dtype == GDN_F32;
+    if (e == cudaSuccess) e = gdn::launch_lin_walk_generic(w, ws.s);
+    gdn::LinDg d{part(parts.plus), part(parts.minus), part(parts.anchors), blocks, blocks, grad_g, g_per_head != 0,
+                 reinterpret_cast<double*>(base + parts.part), z.cu, z.n_seqs, B, T, H};
+    if (e == cudaSuccess) e = gdn::launch_lin_dg(d, ws.s);
+    return finish(fn, e, ws);
+}
+
+gdn_status lin_recurrent_step(const void* q, const void* k, const void* v, const float* g, int g_per_head, float scale,
+                              const float* state, float* state_out, void* o, int N, int H_k, int H, int d_k, int d_v,
+                              int64_t q_token_stride, int64_t q_head_stride, int64_t k_token_stride, int64_t k_head_stride,
+                              int64_t v_token_stride, int64_t v_head_stride, gdn_dtype dtype, void* stream) {
+    const char* fn = "lin_recurrent_step";
+    const Sizes z{N, 1, H_k, H, d_k, d_v, nullptr, 0};
+    GDN_TRY(check_sizes(fn, z, dtype, GDN_ALGO_AUTO));
+    const size_t es = size_of(dtype);
+    const LinTok tq{q, q_token_stride, q_head_stride, z.group()}, tk{k, k_token_stride, k_head_stride, z.group()};
+    const LinTok tv{v, v_token_stride, v_head_stride, 1};
+    GDN_TRY(check_strides(fn, "q", tq, d_k));
+    GDN_TRY(check_strides(fn, "k", tk, d_k));
+    GDN_TRY(check_strides(fn, "v", tv, d_v));
+    GDN_TRY(need(fn, "q", q, es));
+    GDN_TRY(need(fn, "k", k, es));
+    GDN_TRY(need(fn, "v", v, es));
+    GDN_TRY(need(fn, "g", g, 4));
+    GDN_TRY(need(fn, "state", state, 4));
+    GDN_TRY(need(fn, "state_out", state_out, 4));
+    GDN_TRY(need(fn, "o", o, es));
+    gdn::LinStepArgs a{tq, tk, tv, g, g_per_head ? 0 : (int64_t)H, 1, scale, state, state_out, o, N, H, d_k, d_v, dtype == GDN_BF16};
+    const cudaError_t e = gdn::launch_lin_step(a, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ok() : cuda_fail(e, fn);
+}
+
+}  // extern "C"

@@ -1,0 +1,262 @@
+// Linear attention with a decay for each head: the generic walk (fp32 arithmetic, any head size up to 256, fp32 or bf16
+// tokens), and the sums behind the walks of the backward pass.
+//
+// One block of threads walks one (sequence, value head, 32 columns of c) in chunks of 32 tokens, with the state in shared
+// memory.  A chunk: the 32 x 32 triangle of decayed products a_i . b_j, the outputs (row i: a_i S and the triangle's row), then
+// the state.  The triangle is a loop bound, not a factor, so a value that is not a number reaches no token it should not.
+// It is bound by shared-memory reads (two to three for each multiply-add of the triangle).
+
+#include "internal.h"
+#include "lin_common.cuh"
+
+namespace gdn {
+namespace {
+
+using mix::bf16;
+constexpr int CH = 32, COLS = kLinGenericCols, THREADS = 256;
+
+template <typename T>
+__global__ void __launch_bounds__(THREADS) lin_walk_kernel(const LinWalk w) {
+    extern __shared__ float sh[];
+    const int da = w.da, lda = da | 1;                 // (odd: rows read at one column hit different banks)
+    float* S = sh;                                     // [da][COLS]
+    float* As = S + da * COLS;                         // [CH][lda]
+    float* Bs = As + CH * lda;                         // [CH][lda]
+    float* Cs = Bs + CH * lda;                         // [CH][COLS]
+    float* P = Cs + CH * COLS;                         // [CH][CH + 1]
+    __shared__ double G[CH];
+    __shared__ float rowf[CH], colf[CH], whole_s, red[THREADS / 32];
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int blocks = (w.dc + COLS - 1) / COLS;
+    const int64_t unit = blockIdx.x;
+    const int blk = (int)(unit % blocks), h = (int)(unit / blocks % w.H);
+    const int n = lin::by_length(w.cu, w.n_seqs, w.T, (int)(unit / blocks / w.H));
+    int64_t first;
+    int len;
+    lin::sequence(w.cu, w.T, n, first, len);
+    const int c0 = blk * COLS, cols = min(COLS, w.dc - c0);
+    const T* a = static_cast<const T*>(w.a.p) + (h / w.a.group) * w.a.head;
+    const T* b = static_cast<const T*>(w.b.p) + (h / w.b.group) * w.b.head;
+    const T* c = static_cast<const T*>(w.c.p) + (h / w.c.group) * w.c.head + c0;
+    const T* x = w.dots ? static_cast<const T*>(w.x.p) + (h / w.x.group) * w.x.head + c0 : nullptr;
+    const int64_t slot0 = first / kLinSpan + n;
+    const int64_t state0 = ((int64_t)n * w.H + h) * da * w.dc;
+    auto at_state = [&](int r, int cc) { return state0 + (int64_t)r * w.s_r + (int64_t)(c0 + cc) * w.s_c; };
+
+    for (int e = tid; e < da * COLS; e += THREADS) {
+        // (neighbouring threads along the dimension that is contiguous in memory)
+        const int r = w.s_c == 1 ? e / COLS : e % da, cc = w.s_c == 1 ? e % COLS : e / da;
+        S[r * COLS + cc] = w.s_in && cc < cols ? w.s_in[at_state(r, cc)] : 0.f;
+    }
+    __syncthreads();
+
+    // the inner product with, or a copy of, the state at a span's end (every thread)
+    auto at_span_end = [&](int64_t slot) {
+        float* dst = w.spans + ((slot * w.H + h) * blocks + blk) * (int64_t)(da * COLS);
+        if (!w.rev) {
+            for (int e = tid; e < da * COLS; e += THREADS) dst[e] = S[e];
+        } else {
+            float sum = 0.f;
+            for (int e = tid; e < da * COLS; e += THREADS) sum = fmaf(S[e], dst[e], sum);
+            for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+            if (lane == 0) red[warp] = sum;
+            __syncthreads();
+            if (tid == 0) {
+                float s = 0.f;
+                for (int i = 0; i < THREADS / 32; ++i) s += red[i];
+                w.anchors[(slot * w.H + h) * blocks + blk] = s;
+            }
+        }
+    };
+
+    const int chunks = (len + CH - 1) / CH;
+    for (int step = 0; step < chunks; ++step) {
+        const int ch = w.rev ? chunks - 1 - step : step;
+        const int t0 = ch * CH, L = min(CH, len - t0);
+        if (w.rev && w.spans && (step == 0 || t0 % kLinSpan + CH == kLinSpan)) at_span_end(slot0 + t0 / kLinSpan);
+        for (int e = tid; e < CH * da; e += THREADS) {
+            const int i = e / da, r = e % da;
+            const int64_t t = first + t0 + i;
+            As[i * lda + r] = i < L ? mix::ld(a + t * w.a.tok + r) : 0.f;
+            Bs[i * lda + r] = i < L ? mix::ld(b + t * w.b.tok + r) : 0.f;
+        }
+        for (int e = tid; e < CH * COLS; e += THREADS) {
+            const int i = e / COLS, cc = e % COLS;
+            Cs[e] = i < L && cc < cols ? mix::ld(c + (first + t0 + i) * w.c.tok + cc) : 0.f;
+        }
+        if (warp == 0) {                               // prefix sums of the log decays
+            double s = lane < L ? lin::log2_decay(w.g[(first + t0 + lane) * w.g_tok + h * w.g_head]) : 0.0;
+            for (int m = 1; m < 32; m <<= 1) {
+                const double y = __shfl_up_sync(0xffffffffu, s, m);
+                if (lane >= m) s += y;
+            }
+            const double end = __shfl_sync(0xffffffffu, s, 31);
+            const float before = lin::exp2_of(s), behind = lin::exp2_of(end - s);
+            G[lane] = s;
+            rowf[lane] = w.s_inter * (w.rev ? behind : before);
+            colf[lane] = w.s_state * (w.rev ? before : behind);
+            if (lane == 0) whole_s = lin::exp2_of(end);
+        }
+        __syncthreads();
+        for (int e = tid; e < CH * CH; e += THREADS) {
+            const int i = e / CH, j = e % CH;
+            if (w.rev ? j < i : j > i) continue;
+            float s = 0.f;
+            for (int r = 0; r < da; ++r) s = fmaf(As[i * lda + r], Bs[j * lda + r], s);
+            P[i * (CH + 1) + j] = w.s_intra * s * lin::exp2_of(w.rev ? G[j] - G[i] : G[i] - G[j]);
+        }
+        __syncthreads();
+        for (int i = warp; i < L; i += THREADS / 32) { // a warp a row, a lane a column
+            float s = 0.f, f = 0.f;
+            for (int r = 0; r < da; ++r) s = fmaf(As[i * lda + r], S[r * COLS + lane], s);
+            const int j0 = w.rev ? i + 1 : 0, j1 = w.rev ? L : i;
+            for (int j = j0; j < j1; ++j) f = fmaf(P[i * (CH + 1) + j], Cs[j * COLS + lane], f);
+            s = fmaf(rowf[i], s, f);
+            const int64_t t = first + t0 + i;
+            if (w.dots) {
+                float d = lane < cols ? mix::ld(x + t * w.x.tok + lane) * s : 0.f;
+                for (int m = 16; m > 0; m >>= 1) d += __shfl_xor_sync(0xffffffffu, d, m);
+                if (lane == 0) w.dots[((int64_t)blk * w.H + h) * w.rows() + t] = d;
+            }
+            s = fmaf(P[i * (CH + 1) + i], Cs[i * COLS + lane], s);
+            if (lane < cols) {
+                const int64_t at = (t * w.H + h) * w.dc + c0 + lane;
+                if (w.out_f32) static_cast<float*>(w.out)[at] = s;
+                else mix::st(static_cast<T*>(w.out) + at, s);
+            }
+        }
+        __syncthreads();
+        const float whole = whole_s;
+        for (int e = tid; e < da * COLS; e += THREADS) {
+            const int r = e / COLS, cc = e % COLS;
+            float s = whole * S[e];
+            for (int j = 0; j < L; ++j) s = fmaf(Bs[j * lda + r], colf[j] * Cs[j * COLS + cc], s);
+            S[e] = s;
+        }
+        __syncthreads();
+        if (!w.rev && w.spans && (step == chunks - 1 || (t0 + CH) % kLinSpan == 0)) at_span_end(slot0 + t0 / kLinSpan);
+    }
+    if (w.s_out)
+        for (int e = tid; e < da * COLS; e += THREADS) {
+            const int r = w.s_c == 1 ? e / COLS : e % da, cc = w.s_c == 1 ? e % COLS : e / da;
+            if (cc < cols) w.s_out[at_state(r, cc)] = S[r * COLS + cc];
+        }
+}
+
+// One block for each (span slot, head): sums from the span's end, in 64 bits.
+constexpr int DG_THREADS = 256, DG_PER = kLinSpan / DG_THREADS;
+__global__ void __launch_bounds__(DG_THREADS) lin_dg_kernel(const LinDg a) {
+    __shared__ double part[DG_THREADS / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int h = blockIdx.x % a.H;
+    const int64_t slot = blockIdx.x / a.H;
+    // the sequence whose slots the slot is one of: the last that begins at or before it
+    int n = 0, top = (int)min(slot, (int64_t)a.N() - 1), len;
+    int64_t first;
+    while (n < top) {
+        const int mid = (n + top + 1) >> 1;
+        lin::sequence(a.cu, a.T, mid, first, len);
+        if (first / kLinSpan + mid <= slot) n = mid; else top = mid - 1;
+    }
+    lin::sequence(a.cu, a.T, n, first, len);
+    const int64_t at = (slot - (first / kLinSpan + n)) * kLinSpan;
+    if (at < 0 || at >= len) {
+        if (a.per_head && tid == 0) a.part[slot * a.H + h] = 0.0;
+        return;
+    }
+    const int L = (int)min((int64_t)kLinSpan, len - at);
+    double v[DG_PER], sum = 0.0;                       // this thread's tokens, summed from their end
+    for (int u = DG_PER - 1; u >= 0; --u) {
+        const int i = tid * DG_PER + u;
+        if (i < L) {
+            const int64_t t = (int64_t)h * a.rows() + first + at + i;
+            for (int k = 0; k < a.blocks; ++k) {
+                const int64_t e = t + (int64_t)k * a.H * a.rows();
+                sum += (double)a.plus[e] - (double)a.minus[e];
+            }
+        }
+        v[u] = sum;
+    }
+    double s = sum;                                    // of the threads from this one on
+    for (int m = 1; m < 32; m <<= 1) {
+        const double y = __shfl_down_sync(0xffffffffu, s, m);
+        if (lane + m < 32) s += y;
+    }
+    if (lane == 0) part[warp] = s;
+    __syncthreads();
+    double behind = s - sum;
+    for (int i = warp + 1; i < DG_THREADS / 32; ++i) behind += part[i];
+    for (int k = 0; k < a.anchor_blocks; ++k) behind += (double)a.anchors[(slot * a.H + h) * a.anchor_blocks + k];
+    if (!a.per_head) {
+        for (int u = 0; u < DG_PER; ++u) {
+            const int i = tid * DG_PER + u;
+            if (i < L) a.dg[(first + at + i) * a.H + h] = (float)(v[u] + behind);
+        }
+        return;
+    }
+    double all = 0.0;
+    for (int u = 0; u < DG_PER; ++u)
+        if (tid * DG_PER + u < L) all += v[u] + behind;
+    for (int m = 16; m > 0; m >>= 1) all += __shfl_xor_sync(0xffffffffu, all, m);
+    __syncthreads();
+    if (lane == 0) part[warp] = all;
+    __syncthreads();
+    if (tid == 0) {
+        double t = 0.0;
+        for (int i = 0; i < DG_THREADS / 32; ++i) t += part[i];
+        a.part[slot * a.H + h] = t;
+    }
+}
+
+__global__ void lin_dg_sum_kernel(const double* part, float* dg, int64_t slots, int H) {
+    const int h = blockIdx.x, lane = threadIdx.x;
+    double s = 0.0;
+    for (int64_t i = lane; i < slots; i += 32) s += part[i * H + h];
+    for (int m = 16; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+    if (lane == 0) dg[h] = (float)s;
+}
+
+template <typename T>
+__global__ void lin_group_sum_kernel(const float* part, T* out, int64_t n, int group, int d) {
+    for (int64_t e = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; e < n; e += (int64_t)gridDim.x * blockDim.x) {
+        const int64_t head = e / d;
+        const float* p = part + head * group * d + e % d;
+        float s = 0.f;
+        for (int i = 0; i < group; ++i) s += p[(int64_t)i * d];
+        mix::st(out + e, s);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_lin_walk_generic(const LinWalk& w, cudaStream_t s) {
+    const int64_t units = (int64_t)w.N() * w.H * lin_blocks(w.dc, false);
+    if (units == 0) return cudaSuccess;
+    const size_t smem = sizeof(float) * ((size_t)w.da * COLS + 2 * (size_t)CH * (w.da | 1) + CH * COLS + CH * (CH + 1));
+    auto kernel = w.bf16 ? lin_walk_kernel<bf16> : lin_walk_kernel<float>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<(unsigned)units, THREADS, smem, s>>>(w);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_lin_dg(const LinDg& a, cudaStream_t s) {
+    const int64_t slots = lin_span_slots(a.rows(), a.N());
+    lin_dg_kernel<<<(unsigned)(slots * a.H), DG_THREADS, 0, s>>>(a);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || !a.per_head) return e;
+    lin_dg_sum_kernel<<<a.H, 32, 0, s>>>(a.part, a.dg, slots, a.H);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_lin_group_sum(const float* part, void* out, int bf16_out, int64_t rows, int Hk, int group, int d, cudaStream_t s) {
+    const int64_t n = rows * Hk * d;
+    if (n == 0) return cudaSuccess;
+    const unsigned blocks = (unsigned)((n + 255) / 256 < 65536 ? (n + 255) / 256 : 65536);
+    if (bf16_out) lin_group_sum_kernel<<<blocks, 256, 0, s>>>(part, static_cast<bf16*>(out), n, group, d);
+    else lin_group_sum_kernel<<<blocks, 256, 0, s>>>(part, static_cast<float*>(out), n, group, d);
+    return cudaGetLastError();
+}
+
+}  // namespace gdn

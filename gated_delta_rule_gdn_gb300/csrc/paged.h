@@ -1,0 +1,55 @@
+// Requests of the paged key-value cache: appending to it and attention over it, already validated by paged_api.cu.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <cstddef>
+#include <cstdint>
+
+namespace gdn {
+
+// Keys, or values: [pages][slots][heads][d] with strides in elements, the channels contiguous.
+struct PagedSide {
+    void* p;
+    int64_t page, slot, head;
+};
+// Token t of sequence n lies in slot t % page_size of page table[n * table_ld + t / page_size].  An entry outside [0, n_pages)
+// is no page: nothing is written there, and attention passes over its keys.
+struct PagedCache {
+    PagedSide k, v;
+    const int32_t* table;
+    int64_t table_ld;
+    int max_pages, page_size, n_pages;
+    const int32_t* lengths;     // tokens of each sequence, the call's new ones among them
+    int N, Hk, d;
+    int bf16;
+};
+
+struct PagedAppendArgs {
+    PagedCache c;
+    const void *k, *v, *q;      // [n_tokens, heads, d] with strides; q or nullptr
+    int64_t k_tok, k_head, v_tok, v_head, q_tok, q_head;
+    int Hq;
+    int64_t n_tokens;
+    const int32_t* cu;          // [N + 1] offsets of each sequence's new tokens, or nullptr: one each
+    const float *cos, *sin;     // [n_pos, rot / 2]
+    int n_pos, rot, interleaved;
+    void* q_out;                // [n_tokens, Hq, d] contiguous
+};
+cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t s);
+
+struct PagedAttnArgs {
+    PagedCache c;
+    const void* q;              // [N, Hq, d] with strides
+    int64_t q_tok, q_head;
+    int Hq;
+    float scale;
+    void* o;                    // [N, Hq, d] contiguous
+    float* lse;                 // [N, Hq] or nullptr
+    int splits;                 // parts that a sequence's tokens are divided into at most (paged_attn_splits)
+    void* ws;
+};
+int paged_attn_splits(const PagedAttnArgs& a);
+size_t paged_attn_workspace_bytes(const PagedAttnArgs& a);
+cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t s);
+
+}  // namespace gdn

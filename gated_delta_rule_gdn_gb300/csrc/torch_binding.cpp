@@ -1,4 +1,4 @@
-// Python binding of the operators around the delta rule (module _native): checks torch tensors, allocates outputs and
+// Python binding of the operators around and beside the delta rule (module _native): checks torch tensors, allocates outputs and
 // workspaces through torch, and calls the C ABI on torch's current stream.
 //
 // Marshalling only, like _binding.py, but without its interpreter time: a decode step's kernel takes 1.6 us, its checks in
@@ -15,8 +15,10 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cmath>
 #include <optional>
 #include <string>
+#include <utility>
 #include <vector>
 
 #include "../../include/gdn.h"
@@ -28,7 +30,8 @@ namespace {
 #define GDN_ENTRIES(F)                                                                                          \
     F(glr_scan_fwd) F(glr_scan_bwd) F(glr_step) F(glr_workspace_size) F(gdn_qk_norm_fwd) F(gdn_qk_norm_bwd)      \
     F(gdn_qk_norm_workspace_size) F(gdn_short_conv_fwd) F(gdn_short_conv_bwd) F(gdn_short_conv_step)             \
-    F(gdn_short_conv_workspace_size)
+    F(gdn_short_conv_workspace_size) F(lin_chunk_fwd) F(lin_chunk_bwd) F(lin_recurrent_step) F(lin_workspace_size) F(paged_append)      \
+    F(paged_attn_step) F(paged_attn_workspace_size)
 #define GDN_DECLARE(name) decltype(&::name) p_##name = nullptr;
 GDN_ENTRIES(GDN_DECLARE)
 PyObject* g_check = nullptr;       // _binding._check: raises GdnError for a status
@@ -609,6 +612,267 @@ GDN_ENTRY(py_gdn_short_conv_step) {
     GDN_END
 }
 
+// ---------------------------------------------------------------------------------------------- linear attention
+
+float number(PyObject* o, double otherwise) {
+    if (!o) return (float)otherwise;
+    const double x = PyFloat_AsDouble(o);
+    if (x == -1.0 && PyErr_Occurred()) throw Raised{};
+    return (float)x;
+}
+
+// A [..., heads, d] tensor of tokens with its strides.
+struct Heads { void* ptr = nullptr; int64_t tok = 0, head = 0; };
+Heads heads(PyObject* o, const char* name, at::IntArrayRef shape, at::ScalarType type, const at::Tensor& like) {
+    const at::Tensor& t = tensor(o, name);
+    same(t, name, shape, type, like);
+    Heads h;
+    h.ptr = t.data_ptr();
+    h.head = head_spacing(t, name, h.tok);
+    return h;
+}
+
+// q, k, v and g of the lin_ entries; v is [..., H, d_v] of `dim` dimensions.
+struct Lin {
+    Heads q, k, v;
+    float* g;
+    bool g_per_head;
+    int Hk, H, dk, dv;
+    float scale;
+    gdn_dtype dt;
+    std::vector<int64_t> q_shape;
+    Lin(const at::Tensor& vt, PyObject* qo, PyObject* ko, PyObject* vo, PyObject* go, PyObject* scale_o) {
+        const at::Tensor& qt = tensor(qo, "q");
+        const at::Tensor& gt = tensor(go, "g");
+        const int64_t dim = vt.dim();
+        if (qt.dim() != dim) value_error("q must have " + std::to_string(dim) + " dimensions (got " + text(qt.sizes()) + ")");
+        dt = dtype_of(vt, "v");
+        q_shape.assign(vt.sizes().begin(), vt.sizes().end());
+        q_shape[dim - 2] = qt.size(-2);
+        q_shape[dim - 1] = qt.size(-1);
+        Hk = to_int(qt.size(-2), "H_k");
+        dk = to_int(qt.size(-1), "d_k");
+        H = to_int(vt.size(-2), "H");
+        dv = to_int(vt.size(-1), "d_v");
+        v = heads(vo, "v", vt.sizes(), vt.scalar_type(), vt);
+        q = heads(qo, "q", q_shape, vt.scalar_type(), vt);
+        k = heads(ko, "k", q_shape, vt.scalar_type(), vt);
+        g_per_head = gt.dim() == 1 && dim > 2;
+        if (g_per_head) g = dense_f32(go, "g", {(int64_t)H}, vt);
+        else g = dense_f32(go, "g", vt.sizes().slice(0, dim - 1), vt);
+        scale = number(scale_o, 1.0 / std::sqrt((double)(dk > 0 ? dk : 1)));
+    }
+};
+
+gdn_algo algo_of(PyObject* o) {
+    if (!o) return GDN_ALGO_AUTO;
+    if (!PyUnicode_Check(o)) raise(PyExc_TypeError, "algo must be text");
+    for (const auto& [name, value] : {std::pair{"auto", GDN_ALGO_AUTO}, std::pair{"generic", GDN_ALGO_GENERIC}, std::pair{"tcgen05", GDN_ALGO_TCGEN05}})
+        if (PyUnicode_CompareWithASCIIString(o, name) == 0) return value;
+    value_error("algo must be 'auto', 'generic' or 'tcgen05'");
+}
+
+GDN_ENTRY(py_lin_chunk_fwd) {
+    GDN_BEGIN
+    static const Signature sig("lin_chunk_fwd", 4, {"q", "k", "v", "g", "scale", "initial_state", "output_final_state", "cu_seqlens",
+        "algo", "o", "final_state", "workspace", "stream"});
+    Args a(sig, args, nargs, kwnames);
+    const at::Tensor& v = first(a.v[2], "v", 4);
+    const Lin in(v, a.v[0], a.v[1], a.v[2], a.v[3], a.v[4]);
+    const int64_t B = v.size(0), T = v.size(1);
+    const Sequences s = sequences(a.v[7], B, v);
+    const int64_t shape[4] = {s.N, in.H, in.dk, in.dv};
+    const float* h0 = dense_f32(a.v[5], "initial_state", shape, v);
+    const int b = to_int(B, "B"), t = to_int(T, "T");
+    const gdn_algo algo = algo_of(a.v[8]);
+    size_t need = 0;
+    check(p_lin_workspace_size(0, b, t, in.Hk, in.H, in.dk, in.dv, s.n, &need));
+    const OnStream on(a.v[12], v);
+    at::Tensor o, hT;
+    void* op = output(a.v[9], "o", v.sizes(), v.scalar_type(), v, o);
+    if (a.v[10] || truth(a.v[6])) output(a.v[10], "final_state", shape, at::kFloat, v, hT);
+    const Workspace ws = workspace(a.v[11], need, v);
+    launch([&] {
+        return p_lin_chunk_fwd(in.q.ptr, in.k.ptr, in.v.ptr, in.g, in.g_per_head, in.scale, h0, f32(hT), s.cu, s.n, op, b, t, in.Hk, in.H,
+                               in.dk, in.dv, in.q.tok, in.q.head, in.k.tok, in.k.head, in.v.tok, in.v.head, in.dt, algo, ws.ptr,
+                               ws.bytes, on.handle);
+    });
+    return tuple_of({o, hT});
+    GDN_END
+}
+
+GDN_ENTRY(py_lin_chunk_bwd) {
+    GDN_BEGIN
+    static const Signature sig("lin_chunk_bwd", 5, {"q", "k", "v", "g", "d_o", "scale", "initial_state", "d_final_state", "cu_seqlens",
+        "algo", "workspace", "stream"});
+    Args a(sig, args, nargs, kwnames);
+    const at::Tensor& v = first(a.v[2], "v", 4);
+    const Lin in(v, a.v[0], a.v[1], a.v[2], a.v[3], a.v[5]);
+    const int64_t B = v.size(0), T = v.size(1);
+    const Sequences s = sequences(a.v[8], B, v);
+    const int64_t shape[4] = {s.N, in.H, in.dk, in.dv};
+    tensor(a.v[4], "d_o");
+    const void* dO = dense(a.v[4], "d_o", v.sizes(), v.scalar_type(), v);
+    const float* h0 = dense_f32(a.v[6], "initial_state", shape, v);
+    const float* dhT = dense_f32(a.v[7], "d_final_state", shape, v);
+    const int b = to_int(B, "B"), t = to_int(T, "T");
+    const gdn_algo algo = algo_of(a.v[9]);
+    size_t need = 0;
+    check(p_lin_workspace_size(1, b, t, in.Hk, in.H, in.dk, in.dv, s.n, &need));
+    const OnStream on(a.v[11], v);
+    at::Tensor dq = empty(in.q_shape, v.scalar_type(), v), dk = empty(in.q_shape, v.scalar_type(), v);
+    at::Tensor dv = empty(v.sizes(), v.scalar_type(), v), dg, dh0;
+    if (in.g_per_head) dg = empty({(int64_t)in.H}, at::kFloat, v);
+    else dg = empty(v.sizes().slice(0, 3), at::kFloat, v);
+    if (a.v[6]) dh0 = empty(shape, at::kFloat, v);
+    const Workspace ws = workspace(a.v[10], need, v);
+    launch([&] {
+        return p_lin_chunk_bwd(in.q.ptr, in.k.ptr, in.v.ptr, in.g, in.g_per_head, in.scale, h0, dO, dhT, s.cu, s.n, ptr_of(dq), ptr_of(dk),
+                               ptr_of(dv), f32(dg), f32(dh0), b, t, in.Hk, in.H, in.dk, in.dv, in.q.tok, in.q.head, in.k.tok, in.k.head,
+                               in.v.tok, in.v.head, in.dt, algo, ws.ptr, ws.bytes, on.handle);
+    });
+    return tuple_of({dq, dk, dv, dg, dh0});
+    GDN_END
+}
+
+GDN_ENTRY(py_lin_recurrent_step) {
+    GDN_BEGIN
+    static const Signature sig("lin_recurrent_step", 5, {"q", "k", "v", "g", "state", "scale", "state_out", "o", "stream"});
+    Args a(sig, args, nargs, kwnames);
+    const at::Tensor& v = first(a.v[2], "v", 3);
+    const Lin in(v, a.v[0], a.v[1], a.v[2], a.v[3], a.v[5]);
+    const int64_t shape[4] = {v.size(0), in.H, in.dk, in.dv};
+    tensor(a.v[4], "state");
+    float* h = dense_f32(a.v[4], "state", shape, v);
+    float* h_out = a.v[6] ? dense_f32(a.v[6], "state_out", shape, v) : h;
+    const int n = to_int(v.size(0), "N");
+    const OnStream on(a.v[8], v);
+    at::Tensor o;
+    void* op = output(a.v[7], "o", v.sizes(), v.scalar_type(), v, o);
+    launch([&] {
+        return p_lin_recurrent_step(in.q.ptr, in.k.ptr, in.v.ptr, in.g, in.g_per_head, in.scale, h, h_out, op, n, in.Hk, in.H, in.dk, in.dv,
+                                    in.q.tok, in.q.head, in.k.tok, in.k.head, in.v.tok, in.v.head, in.dt, on.handle);
+    });
+    return wrap(o);
+    GDN_END
+}
+
+// --------------------------------------------------------------------------------------------------- paged cache
+
+gdn_paged_side paged_side(const at::Tensor& t, const char* name) {
+    const int64_t d = t.size(3);
+    if (d > 1 && t.stride(3) != 1) value_error(std::string(name) + " must have contiguous channels (strides " + text(t.strides()) + ")");
+    gdn_paged_side s;
+    s.data = t.data_ptr();
+    // (a dimension of one has a stride of no meaning)
+    s.page_stride = t.size(0) > 1 ? t.stride(0) : d;
+    s.slot_stride = t.size(1) > 1 ? t.stride(1) : d;
+    s.head_stride = t.size(2) > 1 ? t.stride(2) : d;
+    return s;
+}
+
+gdn_paged_cache paged_cache(const at::Tensor& like, PyObject* ko, PyObject* vo, PyObject* to, PyObject* lo) {
+    const at::Tensor& k = tensor(ko, "k_cache");
+    const at::Tensor& v = tensor(vo, "v_cache");
+    const at::Tensor& table = tensor(to, "block_table");
+    const at::Tensor& lengths = tensor(lo, "lengths");
+    if (k.dim() != 4) value_error("k_cache must be [n_pages, page_size, H_k, d] (got " + text(k.sizes()) + ")");
+    same(k, "k_cache", k.sizes(), like.scalar_type(), like);
+    same(v, "v_cache", k.sizes(), like.scalar_type(), like);
+    if (lengths.dim() != 1 || lengths.scalar_type() != at::kInt || lengths.device() != like.device() || !lengths.is_contiguous())
+        value_error("lengths must be a contiguous int32 vector on " + like.device().str());
+    if (table.dim() != 2 || table.scalar_type() != at::kInt || table.device() != like.device() || table.size(0) != lengths.size(0) ||
+        (table.size(1) > 1 && table.stride(1) != 1))
+        value_error("block_table must be int32 of shape (" + std::to_string(lengths.size(0)) + ", max_pages) with contiguous rows on " +
+                    like.device().str() + " (got " + text(table.scalar_type()) + " " + text(table.sizes()) + ")");
+    gdn_paged_cache c{};
+    c.k = paged_side(k, "k_cache");
+    c.v = paged_side(v, "v_cache");
+    c.block_table = table.numel() ? table.data_ptr<int32_t>() : nullptr;
+    c.lengths = lengths.data_ptr<int32_t>();
+    c.table_stride = table.size(0) > 1 ? table.stride(0) : table.size(1);
+    c.N = to_int(lengths.size(0), "N");
+    c.max_pages = to_int(table.size(1), "max_pages");
+    c.n_pages = to_int(k.size(0), "n_pages");
+    c.page_size = to_int(k.size(1), "page_size");
+    c.H_k = to_int(k.size(2), "H_k");
+    c.d = to_int(k.size(3), "d");
+    c.dtype = dtype_of(k, "k_cache");
+    return c;
+}
+
+GDN_ENTRY(py_paged_append) {
+    GDN_BEGIN
+    static const Signature sig("paged_append", 6, {"k", "v", "k_cache", "v_cache", "block_table", "lengths", "q", "cu_seqlens", "cos",
+        "sin", "interleaved", "q_out", "stream"});
+    Args a(sig, args, nargs, kwnames);
+    const at::Tensor& k = first(a.v[0], "k", 3);
+    const gdn_paged_cache c = paged_cache(k, a.v[2], a.v[3], a.v[4], a.v[5]);
+    const int64_t n = k.size(0), shape[3] = {n, c.H_k, c.d};
+    const Heads kh = heads(a.v[0], "k", shape, k.scalar_type(), k), vh = heads(a.v[1], "v", shape, k.scalar_type(), k);
+    Heads qh;
+    int64_t q_shape[3] = {n, 0, c.d};
+    if (a.v[6]) {
+        const at::Tensor& q = tensor(a.v[6], "q");
+        if (q.dim() != 3) value_error("q must have 3 dimensions (got " + text(q.sizes()) + ")");
+        q_shape[1] = q.size(1);
+        qh = heads(a.v[6], "q", q_shape, k.scalar_type(), k);
+    } else if (a.v[11]) {
+        value_error("q_out is given without q");
+    }
+    const Sequences s = sequences(a.v[7], c.N, k);
+    if (s.cu && s.n != c.N)
+        value_error("cu_seqlens must have one offset more than lengths (got " + std::to_string(s.n + 1) + " for " + std::to_string(c.N) +
+                    " sequences)");
+    int64_t n_pos = 0, half = 0;
+    const float *cos = nullptr, *sin = nullptr;
+    if (!a.v[8] != !a.v[9]) value_error("cos and sin go together");
+    if (a.v[8]) {
+        const at::Tensor& t = tensor(a.v[8], "cos");
+        if (t.dim() != 2) value_error("cos must be [positions, rotary_dim / 2] (got " + text(t.sizes()) + ")");
+        n_pos = t.size(0);
+        half = t.size(1);
+        cos = dense_f32(a.v[8], "cos", t.sizes(), k);
+        sin = dense_f32(a.v[9], "sin", t.sizes(), k);
+    }
+    const int np = to_int(n_pos, "positions"), rot = to_int(2 * half, "rotary_dim"), hq = to_int(q_shape[1], "H_q");
+    const bool interleaved = truth(a.v[10]);
+    const OnStream on(a.v[12], k);
+    at::Tensor qo;
+    void* qp = a.v[6] ? output(a.v[11], "q_out", q_shape, k.scalar_type(), k, qo) : nullptr;
+    launch([&] {
+        return p_paged_append(kh.ptr, vh.ptr, qh.ptr, &c, s.cu, cos, sin, np, rot, interleaved, qp, n, hq, kh.tok, kh.head, vh.tok, vh.head,
+                              qh.tok, qh.head, on.handle);
+    });
+    return wrap(qo);
+    GDN_END
+}
+
+GDN_ENTRY(py_paged_attn_step) {
+    GDN_BEGIN
+    static const Signature sig("paged_attn_step", 5, {"q", "k_cache", "v_cache", "block_table", "lengths", "scale", "o", "output_lse",
+        "workspace", "stream"});
+    Args a(sig, args, nargs, kwnames);
+    const at::Tensor& q = first(a.v[0], "q", 3);
+    const gdn_paged_cache c = paged_cache(q, a.v[1], a.v[2], a.v[3], a.v[4]);
+    const int64_t shape[3] = {c.N, q.size(1), c.d};
+    const Heads qh = heads(a.v[0], "q", shape, q.scalar_type(), q);
+    const int hq = to_int(q.size(1), "H_q");
+    const float scale = number(a.v[5], 1.0 / std::sqrt((double)c.d));
+    size_t need = 0;
+    check(p_paged_attn_workspace_size(c.N, hq, c.H_k, c.d, c.max_pages, c.page_size, &need));
+    const bool with_lse = truth(a.v[7]);
+    const OnStream on(a.v[9], q);
+    at::Tensor o, lse;
+    void* op = output(a.v[6], "o", shape, q.scalar_type(), q, o);
+    if (with_lse) lse = empty({(int64_t)c.N, (int64_t)hq}, at::kFloat, q);
+    const Workspace ws = workspace(a.v[8], need, q);
+    launch([&] { return p_paged_attn_step(qh.ptr, &c, scale, op, f32(lse), hq, qh.tok, qh.head, ws.ptr, ws.bytes, on.handle); });
+    if (with_lse) return tuple_of({o, lse});
+    return wrap(o);
+    GDN_END
+}
+
 // ------------------------------------------------------------------------------------------------------- module
 
 // (row stride) of a [..., D] tensor, (token stride, head stride) of a [..., H, d] one: what the entries pass on
@@ -700,6 +964,41 @@ PyMethodDef methods[] = {
         "gdn_short_conv_step(x, state, weight, bias=None, activation='silu', state_out=None, y=None, stream=None)\n--\n\n"
         "One decode token of the short convolution for N sequences (C ABI gdn_short_conv_step); returns y [N, D].\n\n"
         "state [N, W - 1, D] in x's type moves up by the token in place, or is kept when state_out is given."),
+    GDN_METHOD(lin_chunk_fwd,
+        "lin_chunk_fwd(q, k, v, g, scale=None, initial_state=None, output_final_state=False, cu_seqlens=None, algo='auto', o=None, "
+        "final_state=None, workspace=None, stream=None)\n--\n\n"
+        "Linear attention with a decay for each head, S_t = exp(g_t) S_{t-1} + k_t v_t^T, o_t = scale S_t^T q_t, over whole\n"
+        "sequences (C ABI lin_chunk_fwd).\n\n"
+        "q, k [B, T, H_k, d_k] and v [B, T, H, d_v] in bf16 or fp32, H a multiple of H_k; g fp32, log decays [B, T, H] or [H];\n"
+        "states [N, H, d_k, d_v] fp32; scale d_k ** -0.5.  Packed sequences: cu_seqlens (int32, B = 1).  Returns (o in v's type,\n"
+        "final_state or None)."),
+    GDN_METHOD(lin_chunk_bwd,
+        "lin_chunk_bwd(q, k, v, g, d_o, scale=None, initial_state=None, d_final_state=None, cu_seqlens=None, algo='auto', "
+        "workspace=None, stream=None)\n--\n\n"
+        "Gradients of <d_o, o> + <d_final_state, final_state> through lin_chunk_fwd (C ABI lin_chunk_bwd).\n\n"
+        "Returns (dq, dk, dv, dg, d_initial_state or None); token gradients in their tensor's type, dg (of g's shape) and\n"
+        "d_initial_state fp32.  A key head's dq and dk sum those of its value heads."),
+    GDN_METHOD(lin_recurrent_step,
+        "lin_recurrent_step(q, k, v, g, state, scale=None, state_out=None, o=None, stream=None)\n--\n\n"
+        "One decode token of linear attention for N sequences (C ABI lin_recurrent_step); returns o [N, H, d_v].\n\n"
+        "q, k [N, H_k, d_k], v [N, H, d_v], g [N, H] or [H].  state [N, H, d_k, d_v] fp32 is updated in place, or kept when\n"
+        "state_out is given, which then takes the new state."),
+    GDN_METHOD(paged_append,
+        "paged_append(k, v, k_cache, v_cache, block_table, lengths, q=None, cu_seqlens=None, cos=None, sin=None, interleaved=False, "
+        "q_out=None, stream=None)\n--\n\n"
+        "Write new tokens' keys and values into a paged cache, keys (and q) turned by their position on the way (C ABI\n"
+        "paged_append).\n\n"
+        "k, v [n, H_k, d], q [n, H_q, d]; k_cache, v_cache [n_pages, page_size, H_k, d] at any strides with contiguous channels;\n"
+        "block_table [N, max_pages] and lengths [N] int32, the lengths with the new tokens.  One token for each sequence, or\n"
+        "cu_seqlens [N + 1].  cos, sin [positions, rotary_dim / 2] fp32, pairs as in gdn_qk_norm_fwd.  Returns the turned q,\n"
+        "contiguous, or None."),
+    GDN_METHOD(paged_attn_step,
+        "paged_attn_step(q, k_cache, v_cache, block_table, lengths, scale=None, o=None, output_lse=False, workspace=None, "
+        "stream=None)\n--\n\n"
+        "Softmax attention of one new token for each sequence over a paged cache (C ABI paged_attn_step); returns o [N, H_q, d],\n"
+        "and with output_lse the log of the softmax's sum [N, H_q] fp32.\n\n"
+        "q [N, H_q, d], H_q a multiple of H_k; the cache as in paged_append; scale d ** -0.5.  A sequence of length 0 has o = 0\n"
+        "and lse = -inf."),
     GDN_METHOD(spacing, "spacing(t, heads=False)\n--\n\nThe strides that the entries pass on for a strided tensor."),
     {"init", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_init)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};

@@ -651,6 +651,123 @@ gdn_status gdn_short_conv_step(const void* x, const float* weight, const float* 
                                const void* state, void* state_out, void* y, int N, int D, int W, int64_t ld_x,
                                gdn_dtype dtype, void* stream);
 
+/* ======================================================================================
+ * Token mixers beside the delta rule, for the other layers of a hybrid model: linear
+ * attention with a decay for each head, and softmax attention over a paged cache (appending
+ * to it, and one new token for each sequence).  The conventions of the section above hold:
+ * inputs may lie in a wider tensor (token and head strides in elements), outputs are
+ * contiguous, gradients of tokens have their tensor's type, and results are the same from
+ * run to run.
+ * ====================================================================================== */
+
+/*
+ * lin_chunk_fwd -- linear attention with a decay for each head, chunkwise: training and prefill.
+ *
+ *     S_t = exp(g_t) S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t
+ *
+ * (the delta rule without its correction: nothing is erased but by the decay).
+ *   q, k     [B, T, H_k, d_k] dtype;  v [B, T, H, d_v] dtype, each with token and head strides;
+ *            value head h reads key head h / (H / H_k), H a multiple of H_k
+ *   g        log decays <= 0, fp32: [B, T, H], or [H] with g_per_head nonzero; -inf forgets
+ *            everything before the token (any below -693 do)
+ *   initial_state  [N, H, d_k, d_v] fp32, or NULL for zeros;  final_state the same, or NULL
+ *   o        [B, T, H, d_v] dtype (output)
+ *   sizes    1 <= d_k, d_v <= 256
+ *   algo     GDN_ALGO_AUTO, GDN_ALGO_GENERIC (fp32 arithmetic, any type and size) or
+ *            GDN_ALGO_TCGEN05 (tensor cores; GDN_ERR_UNSUPPORTED where the request does not fit it)
+ *   workspace  lin_workspace_size(0, ...) bytes
+ */
+gdn_status lin_chunk_fwd(const void* q, const void* k, const void* v, const float* g, int g_per_head, float scale,
+                         const float* initial_state, float* final_state, const int32_t* cu_seqlens, int n_seqs, void* o,
+                         int B, int T, int H_k, int H, int d_k, int d_v, int64_t q_token_stride, int64_t q_head_stride,
+                         int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
+                         gdn_dtype dtype, gdn_algo algo, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * lin_chunk_bwd -- gradients of L = sum <grad_o, o> + sum <grad_final_state, final state> through
+ * lin_chunk_fwd, from the forward's inputs.
+ *   grad_o            [B, T, H, d_v] dtype, contiguous;  grad_final_state [N, H, d_k, d_v] fp32 or NULL (zero)
+ *   grad_q, grad_k    [B, T, H_k, d_k] dtype (a key head sums its value heads' parts, in order);
+ *   grad_v            [B, T, H, d_v] dtype
+ *   grad_g            fp32, the shape of g (with g_per_head the sum over all tokens, in a fixed order)
+ *   grad_initial_state  [N, H, d_k, d_v] fp32, or NULL
+ *   workspace         lin_workspace_size(1, ...) bytes
+ */
+gdn_status lin_chunk_bwd(const void* q, const void* k, const void* v, const float* g, int g_per_head, float scale,
+                         const float* initial_state, const void* grad_o, const float* grad_final_state,
+                         const int32_t* cu_seqlens, int n_seqs, void* grad_q, void* grad_k, void* grad_v, float* grad_g,
+                         float* grad_initial_state, int B, int T, int H_k, int H, int d_k, int d_v, int64_t q_token_stride,
+                         int64_t q_head_stride, int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
+                         int64_t v_head_stride, gdn_dtype dtype, gdn_algo algo, void* workspace, size_t workspace_bytes,
+                         void* stream);
+
+/* Workspace bytes of lin_chunk_fwd (backward = 0) or lin_chunk_bwd; n_seqs is 0 without cu_seqlens. */
+gdn_status lin_workspace_size(int backward, int B, int T, int H_k, int H, int d_k, int d_v, int n_seqs, size_t* bytes);
+
+/*
+ * lin_recurrent_step -- one decode token of the same for N sequences.
+ *   q, k [N, H_k, d_k], v [N, H, d_v] with strides over sequences and heads;  g [N, H] (or [H] with g_per_head) fp32
+ *   state, state_out  [N, H, d_k, d_v] fp32; state_out may be state (updated in place) or a buffer of its own
+ *   o [N, H, d_v] dtype
+ */
+gdn_status lin_recurrent_step(const void* q, const void* k, const void* v, const float* g, int g_per_head, float scale,
+                              const float* state, float* state_out, void* o, int N, int H_k, int H, int d_k, int d_v,
+                              int64_t q_token_stride, int64_t q_head_stride, int64_t k_token_stride, int64_t k_head_stride,
+                              int64_t v_token_stride, int64_t v_head_stride, gdn_dtype dtype, void* stream);
+
+/*
+ * A paged key-value cache.  Token t of sequence n lies in slot t % page_size of page
+ * block_table[n, t / page_size]; a page is [page_size, H_k, d] channels of either side, at any strides (page, slot
+ * and head strides in elements, the channels contiguous), so that the two sides may share an allocation.  Entries of
+ * the table outside [0, n_pages) are no pages: nothing is written there and their keys take no part.  Two sequences may
+ * share pages that are only read; a slot that one call writes twice holds either value.
+ *   lengths  [N] int32 device: tokens of each sequence, the new ones of this step included, so that one array serves
+ *            the append and the attention of every layer of a step (attention takes at most max_pages * page_size, and
+ *            nothing of a sequence whose length is 0 or less)
+ */
+typedef struct gdn_paged_side {
+    void* data;
+    int64_t page_stride, slot_stride, head_stride;
+} gdn_paged_side;
+typedef struct gdn_paged_cache {
+    gdn_paged_side k, v;            /* [n_pages, page_size, H_k, d] dtype */
+    const int32_t* block_table;     /* [N, max_pages] device, rows table_stride apart */
+    const int32_t* lengths;         /* [N] device */
+    int64_t table_stride;
+    int N, max_pages, n_pages, page_size, H_k, d;
+    gdn_dtype dtype;
+} gdn_paged_cache;
+
+/*
+ * paged_append -- write new tokens' keys and values behind those that the cache has, the keys (and q, into q_out)
+ * turned by the rotation of gdn_qk_norm_fwd at each token's position in its sequence.
+ *   k, v [n_tokens, H_k, d], q [n_tokens, H_q, d] or NULL: dtype, with token and head strides
+ *   cu_seqlens  NULL: one new token for each sequence (n_tokens = N).  Otherwise int32 device array [N + 1] of offsets:
+ *               sequence n has tokens cu[n] .. cu[n + 1] - 1, at positions lengths[n] - (cu[n + 1] - cu[n]) and on.
+ *               Tokens behind the last offset are passed over (q_out keeps its rows there).
+ *   cos, sin    [n_pos, rotary_dim / 2] fp32; positions are clamped into [0, n_pos); not read when rotary_dim is 0
+ *   q_out       [n_tokens, H_q, d] contiguous, dtype
+ * A token whose position has no page is not written.
+ */
+gdn_status paged_append(const void* k, const void* v, const void* q, const gdn_paged_cache* cache, const int32_t* cu_seqlens,
+                        const float* cos, const float* sin, int n_pos, int rotary_dim, int interleaved, void* q_out,
+                        int64_t n_tokens, int H_q, int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
+                        int64_t v_head_stride, int64_t q_token_stride, int64_t q_head_stride, void* stream);
+
+/*
+ * paged_attn_step -- softmax attention of one new token for each sequence over the cache:
+ *     o = sum_j p_j v_j,   p = softmax_j(scale q . k_j),   j over the sequence's tokens.
+ * Query head h reads key head h / (H_q / H_k).  A sequence without tokens has o = 0 and lse = -inf.
+ *   q [N, H_q, d] dtype, with strides over sequences and heads;  o [N, H_q, d] dtype
+ *   lse         [N, H_q] fp32, or NULL: log of the sum of exp(scale q . k_j)
+ *   workspace   paged_attn_workspace_size bytes (the parts of long sequences)
+ */
+gdn_status paged_attn_step(const void* q, const gdn_paged_cache* cache, float scale, void* o, float* lse, int H_q,
+                           int64_t q_token_stride, int64_t q_head_stride, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of paged_attn_step. */
+gdn_status paged_attn_workspace_size(int N, int H_q, int H_k, int d, int max_pages, int page_size, size_t* bytes);
+
 /* Message for the calling thread's last non-OK status ("" if none). */
 const char* gdn_last_error(void);
 
