@@ -95,6 +95,9 @@ bool make_map_f32_rows(CUtensorMap* m, const float* base, long rows, int H, int 
 // box_rows sets its height.
 bool make_map_rows(CUtensorMap* m, const void* base, long rows, int H, int d, bool f32, int box_d = 0,
                    int box_rows = 64);
+// The same swizzled box, of box_rows rows, over a bf16 tensor whose heads and rows lie at any strides (multiples of 16 bytes).
+bool make_map_strided(CUtensorMap* m, const void* base, int64_t rows, int H, int d, int64_t row_stride, int64_t head_stride,
+                      int box_rows);
 bool device_is_sm100_family();
 
 // Decode step (recurrent_step.cu).

@@ -36,18 +36,19 @@ struct LinWalk {
     const int32_t* cu;
     int n_seqs, B, T, H;
     int bf16;
-    // Backward, the parts of the decays' gradient: dots[block][h][token] = x_i . out_i over the block's columns of c, without
-    // the pair (i, i).  x has dc columns.
+    // Backward, the parts of the decays' gradient, each [block of columns][h][token] (x has dc columns):
     LinTok x;
-    float* dots;            // or nullptr
-    // States at the ends of spans of kLinSpan tokens, [span slot][h][block][da][block's columns]: the forward walk writes
-    // them, the reverse one writes anchors[span slot][h][block], the inner product of its state with them.
+    float* dots;            // x_i . (s_inter a_i S), or nullptr
+    float* pair_dots;       // x_i . (the sum over j) without j = i (the generic walk), or nullptr
+    // States at the starts of spans of kLinSpan tokens, [span slot][h][block][da][block's columns]: the forward walk writes
+    // them, the reverse one writes anchors[span slot][h][block], e^(G_end) times the inner product with its own state behind
+    // the span's first chunk.
     float* spans;
     float* anchors;
     __host__ __device__ int N() const { return cu ? n_seqs : B; }
     __host__ __device__ int64_t rows() const { return (int64_t)B * T; }
 };
-constexpr int kLinSpan = 1024;
+constexpr int kLinSpan = 256, kLinGenericChunk = 32, kLinChunk = 128;
 // The span slots of a call: those of sequence n begin at first_token / kLinSpan + n.
 inline int64_t lin_span_slots(int64_t rows, int64_t N) { return rows / kLinSpan + N + 1; }
 // Columns of c that a block of threads takes (the generic walk, the tensor-core one), for dots and anchors.
@@ -58,12 +59,23 @@ inline size_t lin_span_floats(int da, int dc, bool tensor) {
 }
 
 cudaError_t launch_lin_walk_generic(const LinWalk& w, cudaStream_t s);
+// The tensor-core walk: whether it takes the request, and with `pairs` (dv's walk, with x = v) the part of the decays'
+// gradient that pairs of tokens of one chunk have, pairs[block][h][token]: the sum over keys before the token minus the sum
+// over queries behind it.  Its dots are those of the state's part alone.
+bool lin_tensor_fits(const LinWalk& w);
+cudaError_t launch_lin_walk_tensor(const LinWalk& w, float* pairs, cudaStream_t s);
+cudaError_t lin_read_and_clear_status(unsigned* value, bool clear);
 
-// dg from the walks' dots and anchors: dg_t = <D, S> at its span's end + sum over the span's tokens i >= t of (q_i . dq_i -
-// k_i . dk_i).  With per_head, dg is [H], the sum over all tokens, by way of `part` [span slots][H].
+// dg from the walks' parts.  With S_in the state entering a token's chunk and D_out the gradient of the state leaving it,
+//     dg_t = sum over pairs j < t <= i of the chunk  +  sum_{i >= t} plus_i  +  sum_{j < t} minus_j  +  e^(G_end) <D_out, S_in>
+// where plus_i = q_i . (the part of dq_i that S_in has), minus_j = k_j . (the part of dk_j that D_out has), and the pairs are
+// sum_{i >= t} (pairs_i - pairs_minus_i), i over the chunk, of the sums over keys before i and over queries behind i.  No two
+// of the four cancel.  The last is an inner product at a span's first chunk (anchors) and goes on from chunk to chunk by
+//     <D, S> at their border = the former's minus and last = the latter's plus and last.
+// With per_head, dg is [H], the sum over all tokens, by way of `part` [span slots][H].
 struct LinDg {
-    const float *plus, *minus, *anchors;
-    int blocks, anchor_blocks;
+    const float *plus, *minus, *pairs, *pairs_minus, *anchors;
+    int blocks, pair_blocks, anchor_blocks, chunk;     // (pairs_minus nullptr: in pairs)
     float* dg;
     int per_head;
     double* part;

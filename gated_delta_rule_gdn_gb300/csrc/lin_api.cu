@@ -37,7 +37,6 @@ gdn_status check_sizes(const char* fn, const Sizes& z, gdn_dtype dtype, gdn_algo
         if (z.n_seqs < 1) return fail(GDN_ERR_INVALID_ARG, "%s: cu_seqlens needs n_seqs >= 1 (got %d)", fn, z.n_seqs);
         if (!aligned(z.cu, 4)) return fail(GDN_ERR_INVALID_ARG, "%s: cu_seqlens is not 4-byte aligned", fn);
     }
-    if (algo == GDN_ALGO_TCGEN05) return fail(GDN_ERR_UNSUPPORTED, "%s: the tensor-core path does not take this request", fn);
     const int64_t most = (int64_t(1) << 31) - 1;       // blocks of a launch
     if ((int64_t)z.N() > most / (8 * (int64_t)z.H) || gdn::lin_span_slots(z.rows(), z.N()) > most / z.H)
         return fail(GDN_ERR_UNSUPPORTED, "%s: %d sequences of %d heads need more than 2^31 blocks", fn, z.N(), z.H);
@@ -68,9 +67,17 @@ void state(LinWalk& w, const float* in, float* out, int rows_step, int cols_step
     w.s_in = in; w.s_out = out; w.s_r = rows_step; w.s_c = cols_step;
 }
 
+gdn_status choose(const char* fn, gdn_algo algo, bool fits, bool& tensor) {
+    if (algo == GDN_ALGO_TCGEN05 && !fits)
+        return fail(GDN_ERR_UNSUPPORTED, "%s: the tensor-core path takes bf16, head sizes up to 128 in steps of 8, and rows, heads and "
+                    "outputs on 16-byte boundaries", fn);
+    tensor = fits && algo != GDN_ALGO_GENERIC;
+    return GDN_OK;
+}
+
 // Parts of the backward's workspace, each a multiple of 256 bytes (for either walk: which one it is goes by the buffers too).
 struct BwdParts {
-    size_t plus, minus, spans, anchors, part, group, bytes;
+    size_t plus, minus, pairs, spans, anchors, part, group, bytes;
     explicit BwdParts(const Sizes& z) {
         size_t at = 0;
         auto take = [&](size_t n) {
@@ -83,8 +90,12 @@ struct BwdParts {
         const size_t span = gdn::lin_span_floats(z.dv, z.dk, false), tc = gdn::lin_span_floats(z.dv, z.dk, true);
         plus = take(4 * blocks * heads * (size_t)z.rows());
         minus = take(4 * blocks * heads * (size_t)z.rows());
+        // (the generic walks have two arrays of pairs, over the blocks of d_k; the tensor-core ones one, over those of d_v)
+        const size_t tc_pairs = (size_t)gdn::lin_blocks(z.dv, true);
+        pairs = take(4 * (2 * blocks > tc_pairs ? 2 * blocks : tc_pairs) * heads * (size_t)z.rows());
         spans = take(4 * slots * heads * (span > tc ? span : tc));
-        anchors = take(4 * slots * heads * blocks);
+        const size_t tc_blocks = 4 * (size_t)gdn::lin_blocks(z.dk, true);
+        anchors = take(4 * slots * heads * (blocks > tc_blocks ? blocks : tc_blocks));
         part = take(8 * slots * heads);
         group = take(z.group() > 1 ? 4 * (size_t)z.rows() * heads * (size_t)z.dk : 0);
         bytes = at;
@@ -134,9 +145,11 @@ gdn_status lin_chunk_fwd(const void* q, const void* k, const void* v, const floa
     state(w, initial_state, final_state, d_v, 1);
     w.out = o;
     w.out_f32 = dtype == GDN_F32;
+    bool tensor = false;
+    GDN_TRY(choose(fn, algo, gdn::lin_tensor_fits(w), tensor));
     Workspace ws;
     GDN_TRY(ws.get(fn, workspace, workspace_bytes, 0, static_cast<cudaStream_t>(stream)));
-    return finish(fn, gdn::launch_lin_walk_generic(w, ws.s), ws);
+    return finish(fn, tensor ? gdn::launch_lin_walk_tensor(w, nullptr, ws.s) : gdn::launch_lin_walk_generic(w, ws.s), ws);
 }
 
 gdn_status lin_chunk_bwd(const void* q, const void* k, const void* v, const float* g, int g_per_head, float scale,
@@ -176,46 +189,73 @@ gdn_status lin_chunk_bwd(const void* q, const void* k, const void* v, const floa
     char* base = static_cast<char*>(ws.ptr);
     auto part = [&](size_t at) { return reinterpret_cast<float*>(base + at); };
 
-    // dq, with the states at the spans' ends on the way
-    LinWalk w = walk(z, to, tv, tk, d_v, d_k, g, g_per_head, dtype);
-    w.s_intra = w.s_inter = scale;
-    w.s_state = 1.f;
-    state(w, initial_state, nullptr, 1, d_v);
-    w.out = group > 1 ? part(parts.group) : grad_q;
-    w.out_f32 = group > 1 || dtype == GDN_F32;
-    w.x = tq;
-    w.dots = part(parts.plus);
-    w.spans = part(parts.spans);
-    cudaError_t e = gdn::launch_lin_walk_generic(w, ws.s);
-    if (e == cudaSuccess && group > 1)
-        e = gdn::launch_lin_group_sum(part(parts.group), grad_q, w.bf16, z.rows(), H_k, group, d_k, ws.s);
+    float* pairs = part(parts.pairs);
+    float* pairs_minus = pairs + (int64_t)gdn::lin_blocks(d_k, false) * H * z.rows();
+    // dq, with the states at the spans' starts on the way
+    LinWalk wq = walk(z, to, tv, tk, d_v, d_k, g, g_per_head, dtype);
+    wq.s_intra = wq.s_inter = scale;
+    wq.s_state = 1.f;
+    state(wq, initial_state, nullptr, 1, d_v);
+    wq.out = group > 1 ? part(parts.group) : grad_q;
+    wq.out_f32 = group > 1 || dtype == GDN_F32;
+    wq.x = tq;
+    wq.dots = part(parts.plus);
+    wq.pair_dots = pairs;
+    wq.spans = part(parts.spans);
     // dk, from the last token to the first, with the states' inner products
-    w = walk(z, tv, to, tq, d_v, d_k, g, g_per_head, dtype);
-    w.rev = 1;
-    w.s_intra = w.s_state = scale;
-    w.s_inter = 1.f;
-    state(w, grad_final_state, nullptr, 1, d_v);
-    w.out = group > 1 ? part(parts.group) : grad_k;
-    w.out_f32 = group > 1 || dtype == GDN_F32;
-    w.x = tk;
-    w.dots = part(parts.minus);
-    w.spans = part(parts.spans);
-    w.anchors = part(parts.anchors);
-    if (e == cudaSuccess) e = gdn::launch_lin_walk_generic(w, ws.s);
-    if (e == cudaSuccess && group > 1)
-        e = gdn::launch_lin_group_sum(part(parts.group), grad_k, w.bf16, z.rows(), H_k, group, d_k, ws.s);
-    const int blocks = gdn::lin_blocks(d_k, false);
+    LinWalk wk = walk(z, tv, to, tq, d_v, d_k, g, g_per_head, dtype);
+    wk.rev = 1;
+    wk.s_intra = wk.s_state = scale;
+    wk.s_inter = 1.f;
+    state(wk, grad_final_state, nullptr, 1, d_v);
+    wk.out = group > 1 ? part(parts.group) : grad_k;
+    wk.out_f32 = group > 1 || dtype == GDN_F32;
+    wk.x = tk;
+    wk.dots = part(parts.minus);
+    wk.pair_dots = pairs_minus;
+    wk.spans = part(parts.spans);
+    wk.anchors = part(parts.anchors);
     // dv, and the gradient of the initial state
-    w = walk(z, tk, tq, to, d_k, d_v, g, g_per_head, dtype);
-    w.rev = 1;
-    w.s_intra = w.s_state = scale;
-    w.s_inter = 1.f;
-    state(w, grad_final_state, grad_initial_state, d_v, 1);
-    w.out = grad_v;
-    w.out_f32 = dtype == GDN_F32;
-    if (e == cudaSuccess) e = gdn::launch_lin_walk_generic(w, ws.s);
-    gdn::LinDg d{part(parts.plus), part(parts.minus), part(parts.anchors), blocks, blocks, grad_g, g_per_head != 0,
-                 reinterpret_cast<double*>(base + parts.part), z.cu, z.n_seqs, B, T, H};
+    LinWalk wv = walk(z, tk, tq, to, d_k, d_v, g, g_per_head, dtype);
+    wv.rev = 1;
+    wv.s_intra = wv.s_state = scale;
+    wv.s_inter = 1.f;
+    state(wv, grad_final_state, grad_initial_state, d_v, 1);
+    wv.out = grad_v;
+    wv.out_f32 = dtype == GDN_F32;
+    wv.x = tv;
+    bool tensor = false;
+    if (T > 0)
+        GDN_TRY(choose(fn, algo, gdn::lin_tensor_fits(wq) && gdn::lin_tensor_fits(wk) && gdn::lin_tensor_fits(wv) &&
+                       aligned(grad_q, 16) && aligned(grad_k, 16), tensor));
+    auto run = [&](const LinWalk& w, float* sums) {
+        return tensor ? gdn::launch_lin_walk_tensor(w, sums, ws.s) : gdn::launch_lin_walk_generic(w, ws.s);
+    };
+    cudaError_t e = run(wq, nullptr);
+    if (e == cudaSuccess && group > 1)
+        e = gdn::launch_lin_group_sum(part(parts.group), grad_q, wq.bf16, z.rows(), H_k, group, d_k, ws.s);
+    if (e == cudaSuccess) e = run(wk, nullptr);
+    if (e == cudaSuccess && group > 1)
+        e = gdn::launch_lin_group_sum(part(parts.group), grad_k, wk.bf16, z.rows(), H_k, group, d_k, ws.s);
+    if (e == cudaSuccess) e = run(wv, tensor ? pairs : nullptr);
+    gdn::LinDg d{};
+    d.plus = part(parts.plus);
+    d.minus = part(parts.minus);
+    d.pairs = pairs;
+    d.pairs_minus = tensor ? nullptr : pairs_minus;
+    d.anchors = part(parts.anchors);
+    d.blocks = gdn::lin_blocks(d_k, tensor);
+    d.pair_blocks = tensor ? gdn::lin_blocks(d_v, true) : d.blocks;
+    d.chunk = tensor ? gdn::kLinChunk : gdn::kLinGenericChunk;
+    d.anchor_blocks = tensor ? 4 * d.blocks : d.blocks;
+    d.dg = grad_g;
+    d.per_head = g_per_head != 0;
+    d.part = reinterpret_cast<double*>(base + parts.part);
+    d.cu = z.cu;
+    d.n_seqs = z.n_seqs;
+    d.B = B;
+    d.T = T;
+    d.H = H;
     if (e == cudaSuccess) e = gdn::launch_lin_dg(d, ws.s);
     return finish(fn, e, ws);
 }

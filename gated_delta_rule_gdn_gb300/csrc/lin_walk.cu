@@ -13,7 +13,7 @@ namespace gdn {
 namespace {
 
 using mix::bf16;
-constexpr int CH = 32, COLS = kLinGenericCols, THREADS = 256;
+constexpr int CH = kLinGenericChunk, COLS = kLinGenericCols, THREADS = 256;
 
 template <typename T>
 __global__ void __launch_bounds__(THREADS) lin_walk_kernel(const LinWalk w) {
@@ -51,30 +51,15 @@ __global__ void __launch_bounds__(THREADS) lin_walk_kernel(const LinWalk w) {
     }
     __syncthreads();
 
-    // the inner product with, or a copy of, the state at a span's end (every thread)
-    auto at_span_end = [&](int64_t slot) {
-        float* dst = w.spans + ((slot * w.H + h) * blocks + blk) * (int64_t)(da * COLS);
-        if (!w.rev) {
-            for (int e = tid; e < da * COLS; e += THREADS) dst[e] = S[e];
-        } else {
-            float sum = 0.f;
-            for (int e = tid; e < da * COLS; e += THREADS) sum = fmaf(S[e], dst[e], sum);
-            for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-            if (lane == 0) red[warp] = sum;
-            __syncthreads();
-            if (tid == 0) {
-                float s = 0.f;
-                for (int i = 0; i < THREADS / 32; ++i) s += red[i];
-                w.anchors[(slot * w.H + h) * blocks + blk] = s;
-            }
-        }
-    };
-
     const int chunks = (len + CH - 1) / CH;
     for (int step = 0; step < chunks; ++step) {
         const int ch = w.rev ? chunks - 1 - step : step;
         const int t0 = ch * CH, L = min(CH, len - t0);
-        if (w.rev && w.spans && (step == 0 || t0 % kLinSpan + CH == kLinSpan)) at_span_end(slot0 + t0 / kLinSpan);
+        // a span's first chunk: the state goes out, or is multiplied with the one that did
+        const bool starts_span = w.spans && t0 % kLinSpan == 0;
+        const int64_t span = ((slot0 + t0 / kLinSpan) * w.H + h) * blocks + blk;
+        if (starts_span && !w.rev)
+            for (int e = tid; e < da * COLS; e += THREADS) w.spans[span * (da * COLS) + e] = S[e];
         for (int e = tid; e < CH * da; e += THREADS) {
             const int i = e / da, r = e % da;
             const int64_t t = first + t0 + i;
@@ -112,13 +97,21 @@ __global__ void __launch_bounds__(THREADS) lin_walk_kernel(const LinWalk w) {
             for (int r = 0; r < da; ++r) s = fmaf(As[i * lda + r], S[r * COLS + lane], s);
             const int j0 = w.rev ? i + 1 : 0, j1 = w.rev ? L : i;
             for (int j = j0; j < j1; ++j) f = fmaf(P[i * (CH + 1) + j], Cs[j * COLS + lane], f);
-            s = fmaf(rowf[i], s, f);
+            s *= rowf[i];
             const int64_t t = first + t0 + i;
             if (w.dots) {
-                float d = lane < cols ? mix::ld(x + t * w.x.tok + lane) * s : 0.f;
-                for (int m = 16; m > 0; m >>= 1) d += __shfl_xor_sync(0xffffffffu, d, m);
-                if (lane == 0) w.dots[((int64_t)blk * w.H + h) * w.rows() + t] = d;
+                const float xi = lane < cols ? mix::ld(x + t * w.x.tok + lane) : 0.f;
+                float d = lane < cols ? xi * s : 0.f, p = lane < cols ? xi * f : 0.f;
+                for (int m = 16; m > 0; m >>= 1) {
+                    d += __shfl_xor_sync(0xffffffffu, d, m);
+                    p += __shfl_xor_sync(0xffffffffu, p, m);
+                }
+                if (lane == 0) {
+                    w.dots[((int64_t)blk * w.H + h) * w.rows() + t] = d;
+                    w.pair_dots[((int64_t)blk * w.H + h) * w.rows() + t] = p;
+                }
             }
+            s += f;
             s = fmaf(P[i * (CH + 1) + i], Cs[i * COLS + lane], s);
             if (lane < cols) {
                 const int64_t at = (t * w.H + h) * w.dc + c0 + lane;
@@ -126,8 +119,20 @@ __global__ void __launch_bounds__(THREADS) lin_walk_kernel(const LinWalk w) {
                 else mix::st(static_cast<T*>(w.out) + at, s);
             }
         }
-        __syncthreads();
         const float whole = whole_s;
+        if (starts_span && w.rev) {
+            float sum = 0.f;
+            for (int e = tid; e < da * COLS; e += THREADS) sum = fmaf(S[e], w.spans[span * (da * COLS) + e], sum);
+            for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+            if (lane == 0) red[warp] = sum;
+            __syncthreads();
+            if (tid == 0) {
+                float s = 0.f;
+                for (int i = 0; i < THREADS / 32; ++i) s += red[i];
+                w.anchors[span] = whole * s;
+            }
+        }
+        __syncthreads();
         for (int e = tid; e < da * COLS; e += THREADS) {
             const int r = e / COLS, cc = e % COLS;
             float s = whole * S[e];
@@ -135,7 +140,6 @@ __global__ void __launch_bounds__(THREADS) lin_walk_kernel(const LinWalk w) {
             S[e] = s;
         }
         __syncthreads();
-        if (!w.rev && w.spans && (step == chunks - 1 || (t0 + CH) % kLinSpan == 0)) at_span_end(slot0 + t0 / kLinSpan);
     }
     if (w.s_out)
         for (int e = tid; e < da * COLS; e += THREADS) {
@@ -144,10 +148,10 @@ __global__ void __launch_bounds__(THREADS) lin_walk_kernel(const LinWalk w) {
         }
 }
 
-// One block for each (span slot, head): sums from the span's end, in 64 bits.
-constexpr int DG_THREADS = 256, DG_PER = kLinSpan / DG_THREADS;
-__global__ void __launch_bounds__(DG_THREADS) lin_dg_kernel(const LinDg a) {
-    __shared__ double part[DG_THREADS / 32];
+// One block for each (span slot, head), a thread a token; sums in 64 bits.
+constexpr int DG_WARPS = kLinSpan / 32;
+__global__ void __launch_bounds__(kLinSpan) lin_dg_kernel(const LinDg a) {
+    __shared__ double plus_s[DG_WARPS], minus_s[DG_WARPS], pairs_s[DG_WARPS];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int h = blockIdx.x % a.H;
     const int64_t slot = blockIdx.x / a.H;
@@ -165,46 +169,53 @@ __global__ void __launch_bounds__(DG_THREADS) lin_dg_kernel(const LinDg a) {
         if (a.per_head && tid == 0) a.part[slot * a.H + h] = 0.0;
         return;
     }
-    const int L = (int)min((int64_t)kLinSpan, len - at);
-    double v[DG_PER], sum = 0.0;                       // this thread's tokens, summed from their end
-    for (int u = DG_PER - 1; u >= 0; --u) {
-        const int i = tid * DG_PER + u;
-        if (i < L) {
-            const int64_t t = (int64_t)h * a.rows() + first + at + i;
-            for (int k = 0; k < a.blocks; ++k) {
-                const int64_t e = t + (int64_t)k * a.H * a.rows();
-                sum += (double)a.plus[e] - (double)a.minus[e];
-            }
+    const bool in = at + tid < len;
+    double plus = 0.0, minus = 0.0, pairs = 0.0;
+    if (in) {
+        const int64_t t = (int64_t)h * a.rows() + first + at + tid, step = (int64_t)a.H * a.rows();
+        for (int k = 0; k < a.blocks; ++k) {
+            plus += (double)a.plus[t + k * step];
+            minus += (double)a.minus[t + k * step];
         }
-        v[u] = sum;
+        for (int k = 0; k < a.pair_blocks; ++k) pairs += (double)a.pairs[t + k * step] - (a.pairs_minus ? (double)a.pairs_minus[t + k * step] : 0.0);
     }
-    double s = sum;                                    // of the threads from this one on
+    double behind = plus, behind_pairs = pairs, before = minus;       // from this token on; up to it
     for (int m = 1; m < 32; m <<= 1) {
-        const double y = __shfl_down_sync(0xffffffffu, s, m);
-        if (lane + m < 32) s += y;
-    }
-    if (lane == 0) part[warp] = s;
-    __syncthreads();
-    double behind = s - sum;
-    for (int i = warp + 1; i < DG_THREADS / 32; ++i) behind += part[i];
-    for (int k = 0; k < a.anchor_blocks; ++k) behind += (double)a.anchors[(slot * a.H + h) * a.anchor_blocks + k];
-    if (!a.per_head) {
-        for (int u = 0; u < DG_PER; ++u) {
-            const int i = tid * DG_PER + u;
-            if (i < L) a.dg[(first + at + i) * a.H + h] = (float)(v[u] + behind);
+        const double x = __shfl_down_sync(0xffffffffu, behind, m), y = __shfl_down_sync(0xffffffffu, behind_pairs, m);
+        const double z = __shfl_up_sync(0xffffffffu, before, m);
+        if (lane + m < 32) {
+            behind += x;
+            behind_pairs += y;
         }
+        if (lane >= m) before += z;
+    }
+    if (lane == 0) {
+        plus_s[warp] = behind;
+        pairs_s[warp] = behind_pairs;
+    }
+    if (lane == 31) minus_s[warp] = before;
+    before = __shfl_up_sync(0xffffffffu, before, 1);
+    if (lane == 0) before = 0.0;
+    __syncthreads();
+    const int per = a.chunk / 32, chunk = warp / per;                // warps of a chunk
+    double dg = behind + behind_pairs + before;
+    for (int i = warp + 1; i < (chunk + 1) * per; ++i) dg += plus_s[i] + pairs_s[i];
+    for (int i = chunk * per; i < warp; ++i) dg += minus_s[i];
+    for (int k = 0; k < a.anchor_blocks; ++k) dg += (double)a.anchors[(slot * a.H + h) * a.anchor_blocks + k];
+    for (int i = 0; i < chunk * per; ++i) dg += minus_s[i];
+    for (int i = per; i < (chunk + 1) * per; ++i) dg -= plus_s[i];
+    if (!a.per_head) {
+        if (in) a.dg[(first + at + tid) * a.H + h] = (float)dg;
         return;
     }
-    double all = 0.0;
-    for (int u = 0; u < DG_PER; ++u)
-        if (tid * DG_PER + u < L) all += v[u] + behind;
+    double all = in ? dg : 0.0;
     for (int m = 16; m > 0; m >>= 1) all += __shfl_xor_sync(0xffffffffu, all, m);
     __syncthreads();
-    if (lane == 0) part[warp] = all;
+    if (lane == 0) plus_s[warp] = all;
     __syncthreads();
     if (tid == 0) {
         double t = 0.0;
-        for (int i = 0; i < DG_THREADS / 32; ++i) t += part[i];
+        for (int i = 0; i < DG_WARPS; ++i) t += plus_s[i];
         a.part[slot * a.H + h] = t;
     }
 }
@@ -243,7 +254,7 @@ cudaError_t launch_lin_walk_generic(const LinWalk& w, cudaStream_t s) {
 
 cudaError_t launch_lin_dg(const LinDg& a, cudaStream_t s) {
     const int64_t slots = lin_span_slots(a.rows(), a.N());
-    lin_dg_kernel<<<(unsigned)(slots * a.H), DG_THREADS, 0, s>>>(a);
+    lin_dg_kernel<<<(unsigned)(slots * a.H), kLinSpan, 0, s>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !a.per_head) return e;
     lin_dg_sum_kernel<<<a.H, 32, 0, s>>>(a.part, a.dg, slots, a.H);

@@ -54,6 +54,20 @@ bool make_map_rows(CUtensorMap* m, const void* base, long rows, int H, int d, bo
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// [rows][H][d] bf16 tensor with strides in elements, box 64 d-elements x 1 head x box_rows rows, 128-byte swizzle
+bool make_map_strided(CUtensorMap* m, const void* base, int64_t rows, int H, int d, int64_t row_stride, int64_t head_stride,
+                      int box_rows) {
+    auto enc = get_encode();
+    if (!enc || row_stride % 8 != 0 || head_stride % 8 != 0 || box_rows < 1 || box_rows > 256) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)H, (cuuint64_t)rows};
+    cuuint64_t strides[2] = {(cuuint64_t)head_stride * 2, (cuuint64_t)row_stride * 2};
+    cuuint32_t box[3] = {64, 1, (cuuint32_t)box_rows};
+    cuuint32_t es[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool make_map_f32_rows(CUtensorMap* m, const float* base, long rows, int H, int d) {
     auto enc = get_encode();
     if (!enc || d > 256) return false;
