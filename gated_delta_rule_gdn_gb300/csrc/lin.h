@@ -59,9 +59,9 @@ inline size_t lin_span_floats(int da, int dc, bool tensor) {
 }
 
 cudaError_t launch_lin_walk_generic(const LinWalk& w, cudaStream_t s);
-// The tensor-core walk: whether it takes the request, and with `pairs` (dv's walk, with x = v) the part of the decays'
-// gradient that pairs of tokens of one chunk have, pairs[block][h][token]: the sum over keys before the token minus the sum
-// over queries behind it.  Its dots are those of the state's part alone.
+// The tensor-core walk: whether it takes the request, and with `pairs` (dv's walk, with x = v) the sums over pairs of tokens of
+// a chunk, pairs[block][5][h][token]: for a query those over the keys before it among the chunk's 32 first, second, ... (up to
+// its own 32), then for a key minus the sum over the queries behind it.
 bool lin_tensor_fits(const LinWalk& w);
 cudaError_t launch_lin_walk_tensor(const LinWalk& w, float* pairs, cudaStream_t s);
 cudaError_t lin_read_and_clear_status(unsigned* value, bool clear);
@@ -78,7 +78,7 @@ struct LinDg {
     int blocks, pair_blocks, anchor_blocks, chunk;     // (pairs_minus nullptr: in pairs)
     float* dg;
     int per_head;
-    double* part;
+    float* part;
     const int32_t* cu;
     int n_seqs, B, T, H;
     __host__ __device__ int N() const { return cu ? n_seqs : B; }

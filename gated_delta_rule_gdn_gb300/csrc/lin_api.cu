@@ -90,13 +90,13 @@ struct BwdParts {
         const size_t span = gdn::lin_span_floats(z.dv, z.dk, false), tc = gdn::lin_span_floats(z.dv, z.dk, true);
         plus = take(4 * blocks * heads * (size_t)z.rows());
         minus = take(4 * blocks * heads * (size_t)z.rows());
-        // (the generic walks have two arrays of pairs, over the blocks of d_k; the tensor-core ones one, over those of d_v)
-        const size_t tc_pairs = (size_t)gdn::lin_blocks(z.dv, true);
+        // (the generic walks have two arrays of pairs, over the blocks of d_k; the tensor-core ones five, over those of d_v)
+        const size_t tc_pairs = 5 * (size_t)gdn::lin_blocks(z.dv, true);
         pairs = take(4 * (2 * blocks > tc_pairs ? 2 * blocks : tc_pairs) * heads * (size_t)z.rows());
         spans = take(4 * slots * heads * (span > tc ? span : tc));
-        const size_t tc_blocks = 4 * (size_t)gdn::lin_blocks(z.dk, true);
+        const size_t tc_blocks = 8 * (size_t)gdn::lin_blocks(z.dk, true);
         anchors = take(4 * slots * heads * (blocks > tc_blocks ? blocks : tc_blocks));
-        part = take(8 * slots * heads);
+        part = take(4 * slots * heads);
         group = take(z.group() > 1 ? 4 * (size_t)z.rows() * heads * (size_t)z.dk : 0);
         bytes = at;
     }
@@ -247,10 +247,10 @@ gdn_status lin_chunk_bwd(const void* q, const void* k, const void* v, const floa
     d.blocks = gdn::lin_blocks(d_k, tensor);
     d.pair_blocks = tensor ? gdn::lin_blocks(d_v, true) : d.blocks;
     d.chunk = tensor ? gdn::kLinChunk : gdn::kLinGenericChunk;
-    d.anchor_blocks = tensor ? 4 * d.blocks : d.blocks;
+    d.anchor_blocks = tensor ? 8 * d.blocks : d.blocks;
     d.dg = grad_g;
     d.per_head = g_per_head != 0;
-    d.part = reinterpret_cast<double*>(base + parts.part);
+    d.part = part(parts.part);
     d.cu = z.cu;
     d.n_seqs = z.n_seqs;
     d.B = B;

@@ -7,16 +7,17 @@
 // Four products of 128 rows, so that each fills the 128 lanes of a tensor-core instruction; the state's own change does not
 // depend on the state, so nothing but the fp32 update e^(G_end) S + dS is serial.
 //
-//   warps 0-3   scores: raw out of tensor memory, times decays, as bf16 back into tensor memory (the first operand of P C);
-//               the outputs' epilogue
-//   warps 4-7   state: in registers, a row a thread; scaled values and the state as operands in shared memory
-//   warp 8      tensor copies: two stages of (A, B, C)
-//   warp 9      issues the products
-//   warp 10     prefix sums of the decays
+//   warps 0-7    scores and outputs, four warps a chunk in turn: raw out of tensor memory, times decays, as bf16 back into
+//                tensor memory (the first operand of P C); the outputs' epilogue
+//   warps 8-15   state, 32 columns a warpgroup: in registers, a row a thread; scaled values and the state as operands in
+//                shared memory
+//   warp 16      tensor copies: two stages of (A, B, C)
+//   warp 17      issues the products
+//   warp 18      decays: prefix sums, column factors
 //
-// A block of 32 x 32 scores off the diagonal takes its decays as a product of two factors of at most one, e^(G_i - G_r) for
-// the row and e^(G_r - G_j) for the column with r the row block's first (rev: last) token: one exponential for each of the
-// block's columns in place of 32.  G is kept as the sum of two floats.
+// The decays of a 32 x 32 block of scores off the diagonal are products of factors of at most one, e^(G_i - R_I) of the row (R the
+// first token of its row block, E the last of a column block), e^(R_I - E_J) of the block and e^(E_J - G_j) of the column: one
+// exponential for a column instead of 32 (rev: the other way round).  G is kept as the sum of two floats.
 //
 // Roundings: P and (without dots) the state as an operand go once to bf16, as the result does; scaled values always, and
 // the state where an fp32 result comes of it, are the sum of two bf16 numbers (2^-18), in two products, the smaller first (the
@@ -38,33 +39,35 @@ using mix::bf16;
 __device__ unsigned g_lin_status;
 __device__ __forceinline__ void report(unsigned bit) { atomicOr(&g_lin_status, bit); }
 
-constexpr int CK = kLinChunk, NB = kLinCols;                    // tokens of a chunk, columns of c
+constexpr int CK = kLinChunk, NB = kLinCols;              // tokens of a chunk, columns of c
 constexpr uint64_t kWait = 2000000000ull;
-constexpr int THREADS = 384;
+constexpr int THREADS = 640;
 
 // What a walk does besides: nothing, inner products of its rows with x (SPLIT: the state is exact enough for them), or the
 // sums over pairs of tokens (PAIRS).
 enum Kind { PLAIN, SPLIT, PAIRS };
 
 struct Bars {
-    uint64_t full[2], empty[2], raw_full, raw_free, ds_full, ds_free, s_ready, s_read, p_ready[2], o_full, o_free, vhat, gate_full,
-        gate_empty, x_full, x_empty, sums_full, sums_read;
+    uint64_t full[2], full_c[2], empty[2], empty_c[2], gate_empty[2], raw_full[2], p_ready[2], o_full[2], o_free[2];
+    uint64_t raw_free, ds_full, ds_free, s_ready, vhat, x_full, x_empty;
+    uint32_t flags[2][2][4];                              // rows of C that are not finite, by chunk and half of the columns
     uint32_t tmem;
-    uint32_t flags[2][4];                                 // rows of C that are not finite, by chunk
 };
 
 template <Kind KIND>
 struct Map {                                              // shared memory
     static constexpr uint32_t STAGE = 81920, A = 0, B = 32768, C = 65536;
-    static constexpr uint32_t S = 2 * STAGE, V = S + (KIND == SPLIT ? 32768 : 16384), X = V + 32768;
-    static constexpr uint32_t GH = X + (KIND == PAIRS ? 16384 : 0), GL = GH + 512, W = GL + 512, BARS = W + 1280;
+    static constexpr uint32_t S = 2 * STAGE, V = S + (KIND == SPLIT ? 32768 : 16384), X = V + 32768;   // (PLAIN: outputs turn there)
+    // two buffers of each: G rounded, what the rounding left (bf16), column factors
+    static constexpr uint32_t GH = X + (KIND == SPLIT ? 0 : 16384), CF = GH + 1024, GL = CF + 1024, BARS = GL + 512;
     static constexpr uint32_t BYTES = BARS + sizeof(Bars);
-    // tensor memory columns
-    static constexpr uint32_t RAW = 0, P = 128, RAW2 = 192, DS = KIND == PAIRS ? 320 : 256, OI = KIND == PAIRS ? 384 : 320,
-                              OA = KIND == PAIRS ? 448 : 384;
+    // tensor memory columns.  Where the second scores of PAIRS do not take the room, scores have two buffers, P lies in the
+    // first half of its scores and P C in the second, A S has two buffers, and the two parts of the state's change lie side by side.
+    static constexpr bool TIGHT = KIND == PAIRS;
+    static constexpr uint32_t RAW = 0, RAW2 = 128, P = TIGHT ? 256 : 0, OA = TIGHT ? 384 : 64, DS = TIGHT ? 320 : 256, OI = TIGHT ? 448 : 384;
+    static constexpr uint32_t RING = TIGHT ? 0 : 128, OI_RING = TIGHT ? 0 : 64;      // from a buffer to the next
 };
 static_assert(Map<SPLIT>::BYTES <= 232448 && Map<PAIRS>::BYTES <= 232448, "shared memory of a block");
-static_assert(Map<PAIRS>::OA + 64 <= 512, "tensor memory");
 
 struct LinMaps { CUtensorMap a, b, c, x; };
 
@@ -75,6 +78,55 @@ __device__ __forceinline__ uint32_t bf2(float x, float y) {
 __device__ __forceinline__ float low(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 __device__ __forceinline__ float finite_or_0(float x) { return fabsf(x) < INFINITY ? x : 0.f; }
+__device__ __forceinline__ float ex2(float x) {           // 2^x to 2^-22; 0 below 2^-126
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// the larger magnitude of each half (and a sign of no meaning), NaN if either is
+__device__ __forceinline__ uint32_t most(uint32_t a, uint32_t w) {
+    uint32_t r;
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(w));
+    return r;
+}
+__device__ __forceinline__ uint32_t mul_bf(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t fma_bf(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t r;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    return r;
+}
+// two at a time
+struct F2 { float x, y; };
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 d;
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 d;
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tadd.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 d;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 z, x, y, z;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+// One lane of a converged warp.  (Products issued from a branch that the compiler knows to be one lane's take their operands
+// from the warp's registers, one in 33 to 64 cycles as the tensor cores take them; behind `lane == 0` inside the loop 70 to 150.)
+__device__ __forceinline__ bool elected() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e != 0;
+}
 // Column sums of a 32 x 32 block, a row a lane: lane l gets that of column l.
 __device__ __forceinline__ float column_sums(float (&v)[32], int lane) {
 #pragma unroll
@@ -97,10 +149,11 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
         return;
     }
     Bars& S = *reinterpret_cast<Bars*>(smem + M::BARS);
-    float* Gh = reinterpret_cast<float*>(smem + M::GH);
-    float* Gl = reinterpret_cast<float*>(smem + M::GL);
+    auto Gh = [&](int c) { return reinterpret_cast<float*>(smem + M::GH) + (c & 1) * CK; };
+    auto Gl = [&](int c) { return reinterpret_cast<bf16*>(smem + M::GL) + (c & 1) * CK; };
+    auto Cf = [&](int c) { return reinterpret_cast<float*>(smem + M::CF) + (c & 1) * CK; };
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int blocks = (w.dc + NB - 1) / NB;
     const int64_t unit = blockIdx.x;
     const int blk = (int)(unit % blocks), h = (int)(unit / blocks % w.H);
@@ -108,40 +161,38 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
     int64_t first;
     int len;
     lin::sequence(w.cu, w.T, n, first, len);
-    const int chunks = (len + CK - 1) / CK;
+    const int chunks = __shfl_sync(0xffffffffu, (len + CK - 1) / CK, 0);
     const int c0 = blk * NB, cols = min(NB, w.dc - c0);
 
-    if (warp == 9) {
+    if (warp == 17) {
         tmem_alloc(&S.tmem, 512);
         tmem_relinquish();
     }
     if (tid == 0) {
         for (int s = 0; s < 2; ++s) {
-            mbar_init(&S.full[s], 1);
+            mbar_init(&S.full[s], 2);                     // A and B, and the decays
+            mbar_init(&S.full_c[s], 1);
             mbar_init(&S.empty[s], 1);
+            mbar_init(&S.empty_c[s], KIND == PLAIN ? 1 : 4);
+            mbar_init(&S.gate_empty[s], 12);
+            mbar_init(&S.raw_full[s], 1);
             mbar_init(&S.p_ready[s], 4);
+            mbar_init(&S.o_full[s], 1);
+            mbar_init(&S.o_free[s], 4);
         }
-        mbar_init(&S.raw_full, 1);
         mbar_init(&S.raw_free, 4);
         mbar_init(&S.ds_full, 1);
-        mbar_init(&S.ds_free, 4);
-        mbar_init(&S.s_ready, 4);
-        mbar_init(&S.s_read, 1);
-        mbar_init(&S.o_full, 1);
-        mbar_init(&S.o_free, 4);
-        mbar_init(&S.vhat, 4);
-        mbar_init(&S.gate_full, 1);
-        mbar_init(&S.gate_empty, 8);
+        mbar_init(&S.ds_free, 8);
+        mbar_init(&S.s_ready, 8);
+        mbar_init(&S.vhat, 8);
         mbar_init(&S.x_full, 1);
         mbar_init(&S.x_empty, 1);
-        mbar_init(&S.sums_full, 4);
-        mbar_init(&S.sums_read, 4);
         fence_mbar_init();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = S.tmem;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, S.tmem, 0);
     bool ok = true;
     // chunk of a step, in the walk's direction, and how many of its tokens there are
     auto chunk_of = [&](int c) { return REV ? chunks - 1 - c : c; };
@@ -158,235 +209,249 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
         return ok;
     };
 
-    if (warp < 4) {
+    if (warp < 8) {
         // ------------------------------------------------------------------------------------- scores and outputs
-        const int row = 32 * warp + lane;
-        const uint32_t lanes = tmem + ((uint32_t)(32 * warp) << 16);
-        // column factors of this warp's blocks off the diagonal, and with PAIRS its column sums: 32 floats a block
-        constexpr int FIRST[2][4] = {{0, 32, 96, 192}, {0, 128, 224, 288}};
-        float* W = reinterpret_cast<float*>(smem + M::W) + FIRST[REV ? 1 : 0][warp];
-        const int J0 = REV ? warp : 0, J1 = REV ? 4 : warp + 1;
-        float inter = 0.f;                                // s_inter e^(G_i), or e^(G_end - G_i), of the last two chunks
-        float inter_before = 0.f;
-        {   // the blocks on the other side of the diagonal stay zero
-            uint32_t zero[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) zero[i] = 0u;
-            for (int J = 0; J < 4; ++J)
-                if (J < J0 || J >= J1) {
-                    tmem_st16(lanes + M::P + 16 * J, zero);
-                    if (KIND != PAIRS) tmem_st16(lanes + M::P + 64 + 16 * J, zero);
-                }
-            tmem_st_wait();
-        }
-        auto scores = [&](int c) {
-            const int L = rows_of(c);
-            const uint32_t p = lanes + M::P + (KIND == PAIRS ? 0 : (c & 1) * 64);
-            if (!wait(&S.gate_full, c, 1u)) return;
-            const float gh = Gh[row], gl = Gl[row];
-            const int r = REV ? 32 * warp + 31 : 32 * warp;
-            const float rh = Gh[r], rl = Gl[r], eh = Gh[CK - 1], el = Gl[CK - 1];
-            inter_before = inter;
-            inter = w.s_inter * (REV ? exp2f((eh - gh) + (el - gl)) : exp2f(gh + gl));
-            const float u = w.s_intra * (REV ? exp2f((rh - gh) + (rl - gl)) : exp2f((gh - rh) + (gl - rl)));
-            if (KIND == PAIRS && c > 0 && !wait(&S.sums_read, c - 1, 1u << 17)) return;
-            for (int J = J0; J < J1; ++J)
-                if (J != warp) {
-                    const int j = 32 * J + lane;
-                    W[32 * (J - J0) + lane] = REV ? exp2f((Gh[j] - rh) + (Gl[j] - rl)) : exp2f((rh - Gh[j]) + (rl - Gl[j]));
-                }
-            __syncwarp();
-            if (!wait(&S.raw_full, c, 2u)) return;
+        const int I = warp & 3, row = 32 * I + lane;
+        const uint32_t lanes = tmem + ((uint32_t)(32 * I) << 16);
+        const int J0 = REV ? I : 0, J1 = REV ? 4 : I + 1;
+        const bf16* xp = static_cast<const bf16*>(w.x.p) + (h / w.x.group) * w.x.head + c0;
+        float* pair_at = KIND == PAIRS ? pairs + ((int64_t)blk * 5 * w.H + h) * w.rows() + first : nullptr;
+        const int64_t pair_step = (int64_t)w.H * w.rows();
+        for (int c = warp >> 2; c < chunks; c += 2) {
+            const int L = rows_of(c), s = c & 1;
+            const int64_t t0 = (int64_t)chunk_of(c) * CK;
+            const uint32_t raw = lanes + M::RAW + s * M::RING, p = lanes + M::P + s * M::RING;
+            if (!wait(&S.full[s], c >> 1, 1u)) break;
+            const float *gh = Gh(c), *cf = Cf(c);
+            const bf16* gl = Gl(c);
+            const float ih = gh[row], il = __bfloat162float(gl[row]);
+            const int r = 32 * I + (REV ? 31 : 0);
+            const float rh = gh[r], rl = __bfloat162float(gl[r]);
+            const float f_inter = w.s_inter * (REV ? ex2((gh[CK - 1] - ih) + (__bfloat162float(gl[CK - 1]) - il)) : ex2(ih + il));
+            const float u = w.s_intra * (REV ? ex2((rh - ih) + (rl - il)) : ex2((ih - rh) + (il - rl)));
+            if (!wait(&S.raw_full[s], c >> 1, 2u)) break;
             tc_fence_after();
-            float sum = 0.f, other = 0.f;                 // over the pairs of row i (PAIRS): those off the diagonal
+            float sum = 0.f;                              // over the pairs of row i that are off the diagonal (PAIRS)
 #pragma unroll 1
             for (int J = J0; J < J1; ++J) {
-                uint32_t x[2][16], y[2][16];
-                tmem_ld16(lanes + M::RAW + 32 * J, x[0]);
-                tmem_ld16(lanes + M::RAW + 32 * J + 16, x[1]);
-                if (KIND == PAIRS) {
-                    tmem_ld16(lanes + M::RAW2 + 32 * J, y[0]);
-                    tmem_ld16(lanes + M::RAW2 + 32 * J + 16, y[1]);
-                }
-                float f[32];
-                if (J == warp) {
+                uint32_t xr[2][16];
+                tmem_ld16(raw + 32 * J, xr[0]);
+                tmem_ld16(raw + 32 * J + 16, xr[1]);
+                float x[32];
+                if (J == I) {
+                    // on the diagonal an exponential each; what is outside the triangle is left out, not multiplied by nothing
+                    float f[32];
 #pragma unroll
                     for (int j = 0; j < 32; j += 4) {
-                        const float4 a = *reinterpret_cast<const float4*>(Gh + 32 * J + j);
-                        const float4 b = *reinterpret_cast<const float4*>(Gl + 32 * J + j);
-                        const float ah[4] = {a.x, a.y, a.z, a.w}, bl[4] = {b.x, b.y, b.z, b.w};
+                        const float4 a = *reinterpret_cast<const float4*>(gh + 32 * J + j);
+                        const uint2 b = *reinterpret_cast<const uint2*>(gl + 32 * J + j);
+                        const F2 h0{a.x, a.y}, h1{a.z, a.w}, l0{low(b.x), high(b.x)}, l1{low(b.y), high(b.y)}, m1{-1.f, -1.f};
+                        const F2 e0 = REV ? add2(add2(h0, F2{-ih, -ih}), add2(l0, F2{-il, -il})) : add2(fma2(h0, m1, F2{ih, ih}), fma2(l0, m1, F2{il, il}));
+                        const F2 e1 = REV ? add2(add2(h1, F2{-ih, -ih}), add2(l1, F2{-il, -il})) : add2(fma2(h1, m1, F2{ih, ih}), fma2(l1, m1, F2{il, il}));
+                        f[j] = ex2(e0.x);
+                        f[j + 1] = ex2(e0.y);
+                        f[j + 2] = ex2(e1.x);
+                        f[j + 3] = ex2(e1.y);
+                    }
+                    tmem_ld_wait();
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const bool in = REV ? j + i >= lane && 32 * J + j + i < L : j + i <= lane;
-                            const float e = REV ? (ah[i] - gh) + (bl[i] - gl) : (gh - ah[i]) + (gl - bl[i]);
-                            f[j + i] = in ? w.s_intra * exp2f(e) : 0.f;
-                        }
+                    for (int j = 0; j < 32; j += 2) {
+                        const F2 v = mul2(mul2(F2{f[j], f[j + 1]}, F2{w.s_intra, w.s_intra}),
+                                          F2{__uint_as_float(xr[j >> 4][j & 15]), __uint_as_float(xr[j >> 4][(j & 15) + 1])});
+                        x[j] = (REV ? j >= lane : j <= lane) ? v.x : 0.f;
+                        x[j + 1] = (REV ? j + 1 >= lane : j + 1 <= lane) ? v.y : 0.f;
                     }
                 } else {
+                    const int e = REV ? 32 * J : 32 * J + 31;
+                    const float f = u * (REV ? ex2((gh[e] - rh) + (__bfloat162float(gl[e]) - rl)) : ex2((rh - gh[e]) + (rl - __bfloat162float(gl[e]))));
+                    tmem_ld_wait();
 #pragma unroll
                     for (int j = 0; j < 32; j += 4) {
-                        const float4 a = *reinterpret_cast<const float4*>(W + 32 * (J - J0) + j);
-                        f[j] = u * a.x;
-                        f[j + 1] = u * a.y;
-                        f[j + 2] = u * a.z;
-                        f[j + 3] = u * a.w;
+                        const float4 a = *reinterpret_cast<const float4*>(cf + 32 * J + j);
+                        const F2 v0 = mul2(mul2(F2{a.x, a.y}, F2{f, f}), F2{__uint_as_float(xr[j >> 4][j & 15]), __uint_as_float(xr[j >> 4][(j & 15) + 1])});
+                        const F2 v1 = mul2(mul2(F2{a.z, a.w}, F2{f, f}), F2{__uint_as_float(xr[j >> 4][(j & 15) + 2]), __uint_as_float(xr[j >> 4][(j & 15) + 3])});
+                        x[j] = v0.x;
+                        x[j + 1] = v0.y;
+                        x[j + 2] = v1.x;
+                        x[j + 3] = v1.y;
                     }
                 }
-                tmem_ld_wait();
+                if (REV && L < CK)                        // tokens behind the sequence
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) x[j] = 32 * J + j < L ? x[j] : 0.f;
                 uint32_t q[16];
-                // a score outside the triangle (or, rev, behind the sequence) is left out, not multiplied by nothing
 #pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    const bool in = (J != warp || (REV ? j >= lane : j <= lane)) && (!REV || 32 * J + j < L);
-                    const float s = __uint_as_float(x[j >> 4][j & 15]) * f[j];
-                    f[j] = in ? s : 0.f;
+                for (int j = 0; j < 32; j += 2) q[j >> 1] = bf2(x[j], x[j + 1]);
+                if (KIND == PAIRS && J == J0 && c > 0) {  // the product before, and its outputs, have read P
+                    if (!wait(&S.o_free[s ^ 1], (c - 1) >> 1, 4u)) break;
+                    tc_fence_after();
                 }
-#pragma unroll
-                for (int j = 0; j < 32; j += 2) q[j >> 1] = bf2(f[j], f[j + 1]);
                 tmem_st16(p + 16 * J, q);
                 if (KIND == PAIRS) {
+                    uint32_t y[2][16];
+                    tmem_ld16(lanes + M::RAW2 + 32 * J, y[0]);
+                    tmem_ld16(lanes + M::RAW2 + 32 * J + 16, y[1]);
+                    tmem_ld_wait();
 #pragma unroll
                     for (int j = 0; j < 32; ++j) {
-                        const bool in = (J != warp || j != lane) && row < L && f[j] != 0.f;
-                        f[j] = in ? f[j] * __uint_as_float(y[j >> 4][j & 15]) : 0.f;
-                        sum += f[j];
+                        const bool in = (J != I || j != lane) && row < L && x[j] != 0.f;
+                        x[j] = in ? x[j] * __uint_as_float(y[j >> 4][j & 15]) : 0.f;
+                        sum += x[j];
                     }
-                    const float s = column_sums(f, lane);
-                    __syncwarp();
-                    W[32 * (J - J0) + lane] = s;          // (the block's factors have been read)
+                    // a row of this walk is a key, a column a query behind it: the query's sum over the keys of this warp
+                    const float v = column_sums(x, lane);
+                    if (32 * J + lane < L) pair_at[I * pair_step + t0 + 32 * J + lane] = v;
                 }
             }
+            if (!ok) break;
+            {   // the blocks on the other side of the diagonal
+                uint32_t zero[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) zero[i] = 0u;
+                for (int J = REV ? 0 : J1; J < (REV ? J0 : 4); ++J) tmem_st16(p + 16 * J, zero);
+            }
             tc_fence_before();
-            arrive(&S.gate_empty);
-            arrive(&S.raw_free);
+            arrive(&S.gate_empty[s]);
+            if (KIND == PAIRS) arrive(&S.raw_free);
             tmem_st_wait();
             tc_fence_before();
-            arrive(&S.p_ready[KIND == PAIRS ? 0 : c & 1]);
-            if (KIND == PAIRS) {
-                // row i of this walk is a key: its sum over the queries behind it; the sums over the keys before a query are
-                // the column sums of the warps up to its own (the walk is a reverse one)
-                arrive(&S.sums_full);
-                if (!wait(&S.sums_full, c, 1u << 18)) return;
-                const float* all = reinterpret_cast<const float*>(smem + M::W);
-                for (int v = 0; v <= warp; ++v) other += all[FIRST[1][v] + 32 * (warp - v) + lane];
-                if (row < L)
-                    pairs[((int64_t)blk * w.H + h) * w.rows() + first + (int64_t)chunk_of(c) * CK + row] = other - sum;
-                arrive(&S.sums_read);
-            }
-        };
-        auto outputs = [&](int c, float f) {
-            const int L = rows_of(c);
-            const int64_t t = first + (int64_t)chunk_of(c) * CK + row;
+            arrive(&S.p_ready[s]);
             const bool in = row < L;
-            uint4 xr[8];
-            if (KIND == SPLIT) {
-                const bf16* x = static_cast<const bf16*>(w.x.p) + t * w.x.tok + (h / w.x.group) * w.x.head + c0;
+            const int64_t t = first + t0 + row;
+            if (KIND == PAIRS && in) pair_at[4 * pair_step + t0 + row] = -sum;
+
+            // rows of the outputs go, and rows of x come, several lanes a row (a lane a row would touch 32 lines an access):
+            // turned in shared memory of the warp's own, 32 rows of 64 bytes, or in the chunk's C tile, which has been read
+            // when the outputs are there, of 128
+            constexpr int Q = KIND == PLAIN ? 4 : 8, RPA = 32 / Q;                // pieces of a row, rows of an access
+            const uint32_t turn = KIND == PLAIN ? base + M::X + warp * 2048 : base + s * M::STAGE + M::C + I * 4096;
+            const int rq = lane / Q, q = lane % Q;
+            auto at_row = [&](int r, int i) { return turn + r * (16 * Q) + ((i ^ (KIND == PLAIN ? (r >> 1) & 3 : r & 7)) << 4); };
+            uint4 xv[8];
+            if (KIND == SPLIT)
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    xr[i] = in && 8 * i < cols ? *reinterpret_cast<const uint4*>(x + 8 * i) : make_uint4(0, 0, 0, 0);
-            }
-            if (!wait(&S.o_full, c, 4u)) return;
+                for (int i = 0; i < 8; ++i) {
+                    const int r = RPA * i + rq;
+                    xv[i] = 32 * I + r < L && 8 * q < cols
+                                ? *reinterpret_cast<const uint4*>(xp + (first + t0 + 32 * I + r) * w.x.tok + 8 * q)
+                                : make_uint4(0, 0, 0, 0);
+                }
+            if (!wait(&S.o_full[s], c >> 1, 8u)) break;
             tc_fence_after();
-            uint32_t flags[4], any = 0;
+            if (KIND == SPLIT) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) any |= flags[i] = S.flags[c & 1][i];
-            float o[64], dot = 0.f;
+                for (int i = 0; i < 8; ++i) sts128(at_row(RPA * i + rq, q), xv[i].x, xv[i].y, xv[i].z, xv[i].w);
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) xv[i] = lds128(at_row(lane, i));
+                __syncwarp();
+            }
+            uint32_t any = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) any |= S.flags[s][i >> 2][i & 3];
+            F2 dot{0.f, 0.f};
 #pragma unroll
             for (int i = 0; i < 64; i += 16) {
                 uint32_t a[16], b[16];
-                tmem_ld16(lanes + M::OI + i, a);
-                tmem_ld16(lanes + M::OA + i, b);
+                tmem_ld16(lanes + M::OI + s * M::OI_RING + i, a);
+                tmem_ld16(lanes + M::OA + s * M::RING + i, b);
                 tmem_ld_wait();
+                float o[16];
 #pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                    const float s = f * __uint_as_float(a[k]);
+                for (int k = 0; k < 16; k += 2) {
+                    const F2 g{__uint_as_float(a[k]), __uint_as_float(a[k + 1])};
                     if (KIND == SPLIT) {
-                        const uint4& v = xr[(i + k) >> 3];
-                        const int e = (i + k) & 7;
-                        const uint32_t word = e < 2 ? v.x : e < 4 ? v.y : e < 6 ? v.z : v.w;
-                        dot = fmaf(e & 1 ? high(word) : low(word), s, dot);
+                        const uint4& v = xv[(i + k) >> 3];
+                        const int e = (k & 7) >> 1;
+                        const uint32_t word = e == 0 ? v.x : e == 1 ? v.y : e == 2 ? v.z : v.w;
+                        dot = fma2(F2{low(word), high(word)}, g, dot);
                     }
-                    o[i + k] = s + __uint_as_float(b[k]);
+                    const F2 v = fma2(F2{f_inter, f_inter}, g, F2{__uint_as_float(b[k]), __uint_as_float(b[k + 1])});
+                    o[k] = v.x;
+                    o[k + 1] = v.y;
+                }
+                if (any)                                  // rows of C that are not finite: into the rows that see them
+#pragma unroll 1
+                    for (int j = 0; j < CK; ++j) {
+                        if (!((S.flags[s][i >> 5][j >> 5] >> (j & 31)) & 1)) continue;
+                        uint32_t pj[16];
+                        tmem_ld16(p + j / 32 * 16, pj);
+                        tmem_ld_wait();
+                        uint32_t word = 0;
+#pragma unroll
+                        for (int k = 0; k < 16; ++k)
+                            if (k == (j & 31) / 2) word = pj[k];
+                        const float pv = j & 1 ? high(word) : low(word);
+                        const bf16* cj = static_cast<const bf16*>(w.c.p) + (h / w.c.group) * w.c.head + c0 + (first + t0 + j) * w.c.tok;
+                        if (REV ? row <= j : row >= j)
+#pragma unroll
+                            for (int k = 0; k < 16; ++k)
+                                if (i + k < cols) o[k] = fmaf(pv, __bfloat162float(cj[i + k]), o[k]);
+                    }
+                if (i == 48) {
+                    tc_fence_before();
+                    arrive(&S.o_free[s]);
+                }
+                const bool wide = KIND != PLAIN && w.out_f32;                     // (forward outputs are bf16)
+                if (wide) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        sts128(at_row(lane, (i & 16 ? 4 : 0) + k), __float_as_uint(o[4 * k]), __float_as_uint(o[4 * k + 1]),
+                               __float_as_uint(o[4 * k + 2]), __float_as_uint(o[4 * k + 3]));
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        sts128(at_row(lane, ((i >> 3) & (Q - 1)) + k), bf2(o[8 * k], o[8 * k + 1]), bf2(o[8 * k + 2], o[8 * k + 3]),
+                               bf2(o[8 * k + 4], o[8 * k + 5]), bf2(o[8 * k + 6], o[8 * k + 7]));
+                }
+                if (wide || KIND == PLAIN ? i & 16 : i == 48) {                   // the rows are full
+                    __syncwarp();
+#pragma unroll
+                    for (int k = 0; k < Q; ++k) {
+                        const int r = RPA * k + rq, col = wide ? i - 16 + 4 * q : (KIND == PLAIN ? i - 16 : 0) + 8 * q;
+                        const uint4 v = lds128(at_row(r, q));
+                        const int64_t to = ((first + t0 + 32 * I + r) * w.H + h) * w.dc + c0 + col;
+                        if (32 * I + r < L && col < cols) {
+                            if (wide) *reinterpret_cast<uint4*>(static_cast<float*>(w.out) + to) = v;
+                            else *reinterpret_cast<uint4*>(static_cast<bf16*>(w.out) + to) = v;
+                        }
+                    }
+                    __syncwarp();
                 }
             }
-            if (any) {
-                // rows of C that are not finite: into the rows that see them
-                const bf16* cp = static_cast<const bf16*>(w.c.p) + (h / w.c.group) * w.c.head + c0;
-                for (int j = 0; j < CK; ++j) {
-                    if (!((flags[j >> 5] >> (j & 31)) & 1)) continue;
-                    uint32_t pj[16];
-                    tmem_ld16(lanes + M::P + (KIND == PAIRS ? 0 : (c & 1) * 64) + j / 32 * 16, pj);
-                    tmem_ld_wait();
-                    uint32_t word = 0;
-#pragma unroll
-                    for (int k = 0; k < 16; ++k)
-                        if (k == (j & 31) / 2) word = pj[k];
-                    const float p = j & 1 ? high(word) : low(word);
-                    const bf16* cj = cp + (first + (int64_t)chunk_of(c) * CK + j) * w.c.tok;
-                    if (REV ? row <= j : row >= j) {
-#pragma unroll
-                        for (int k = 0; k < 64; ++k)
-                            if (k < cols) o[k] = fmaf(p, __bfloat162float(cj[k]), o[k]);
-                    }
-                }
+            if (KIND != PLAIN) {
+                fence_async_smem();                       // (the next tile comes by another way)
+                arrive(&S.empty_c[s]);
             }
-            tc_fence_before();
-            arrive(&S.o_free);
-            if (!in) return;
-            if (KIND == SPLIT) w.dots[((int64_t)blk * w.H + h) * w.rows() + t] = dot;
-            const int64_t at = (t * w.H + h) * w.dc + c0;
-            if (w.out_f32) {
-                float4* dst = reinterpret_cast<float4*>(static_cast<float*>(w.out) + at);
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (4 * i < cols) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-            } else {
-                uint4* dst = reinterpret_cast<uint4*>(static_cast<bf16*>(w.out) + at);
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (8 * i < cols)
-                        dst[i] = make_uint4(bf2(o[8 * i], o[8 * i + 1]), bf2(o[8 * i + 2], o[8 * i + 3]),
-                                            bf2(o[8 * i + 4], o[8 * i + 5]), bf2(o[8 * i + 6], o[8 * i + 7]));
-            }
-        };
-        if (KIND == PAIRS) {                              // one buffer of P: its product first
-            for (int c = 0; c < chunks && ok; ++c) {
-                scores(c);
-                if (ok) outputs(c, inter);
-            }
-        } else {                                          // the scores of the next chunk while this one's products run
-            if (chunks > 0) scores(0);
-            for (int c = 0; c < chunks && ok; ++c) {
-                if (c + 1 < chunks) scores(c + 1);
-                if (ok) outputs(c, c + 1 < chunks ? inter_before : inter);
-            }
+            if (KIND == SPLIT && in) w.dots[((int64_t)blk * w.H + h) * w.rows() + t] = f_inter * (dot.x + dot.y);
         }
-    } else if (warp < 8) {
+    } else if (warp < 16) {
         // ------------------------------------------------------------------------------------------------- state
-        const int row = tid - 128;                        // of the state, and of the chunk's tokens
+        const int row = tid & 127, half = (warp - 8) >> 2, k0 = 32 * half;      // row of the state, and of the chunk's tokens
         const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-        float st[64];
-        {
-            const int64_t at = ((int64_t)n * w.H + h) * w.da * w.dc + (int64_t)row * w.s_r + (int64_t)c0 * w.s_c;
+        float st[32];
+        const int64_t state_at = ((int64_t)n * w.H + h) * w.da * w.dc + (int64_t)row * w.s_r + (int64_t)(c0 + k0) * w.s_c;
 #pragma unroll
-            for (int i = 0; i < 64; ++i) st[i] = w.s_in && row < w.da && i < cols ? w.s_in[at + (int64_t)i * w.s_c] : 0.f;
-        }
+        for (int i = 0; i < 32; ++i) st[i] = w.s_in && row < w.da && k0 + i < cols ? w.s_in[state_at + (int64_t)i * w.s_c] : 0.f;
         const int64_t slot0 = first / kLinSpan + n;
         // [span slot][h][block][row][column]
         auto span_at = [&](int ch) {
-            return w.spans + ((((slot0 + ch / (kLinSpan / CK)) * w.H + h) * blocks + blk) * 128 + row) * (int64_t)NB;
+            return w.spans + ((((slot0 + ch / (kLinSpan / CK)) * w.H + h) * blocks + blk) * 128 + row) * (int64_t)NB + k0;
         };
         auto operand = [&] {                              // S as an operand: rows of 64 columns, 128-byte swizzle
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < 4; ++i) {
                 uint32_t hi[4], lo[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const float a = st[8 * i + 2 * k], b = st[8 * i + 2 * k + 1];
                     hi[k] = bf2(a, b);
-                    if (KIND == SPLIT) lo[k] = bf2(finite_or_0(a - low(hi[k])), finite_or_0(b - high(hi[k])));
+                    if (KIND == SPLIT) {
+                        const F2 l = add2(F2{a, b}, F2{-low(hi[k]), -high(hi[k])});
+                        lo[k] = bf2(l.x, l.y);
+                    }
                 }
-                const uint32_t at = row * 128 + ((i ^ (row & 7)) << 4);
+                const uint32_t at = row * 128 + (((4 * half + i) ^ (row & 7)) << 4);
                 sts128(base + M::S + at, hi[0], hi[1], hi[2], hi[3]);
                 if (KIND == SPLIT) sts128(base + M::S + 16384 + at, lo[0], lo[1], lo[2], lo[3]);
             }
@@ -401,17 +466,18 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
             if (starts_span && !REV) {                    // a span's first chunk: the state goes out
                 float4* dst = reinterpret_cast<float4*>(span_at(ch));
 #pragma unroll
-                for (int i = 0; i < 16; ++i) dst[i] = make_float4(st[4 * i], st[4 * i + 1], st[4 * i + 2], st[4 * i + 3]);
+                for (int i = 0; i < 8; ++i) dst[i] = make_float4(st[4 * i], st[4 * i + 1], st[4 * i + 2], st[4 * i + 3]);
             }
-            if (!wait(&S.gate_full, c, 8u)) break;
-            const float gh = Gh[row], gl = Gl[row], eh = Gh[CK - 1], el = Gl[CK - 1];
-            arrive(&S.gate_empty);
+            if (!wait(&S.full[s], c >> 1, 32u)) break;
+            const float gh = Gh(c)[row], gl = __bfloat162float(Gl(c)[row]), eh = Gh(c)[CK - 1], el = __bfloat162float(Gl(c)[CK - 1]);
+            arrive(&S.gate_empty[s]);
             const float whole = exp2f(eh + el);
+            const float f = w.s_state * (REV ? exp2f(gh + gl) : exp2f((eh - gh) + (el - gl)));
             if (starts_span && REV) {                     // or is multiplied with the one that did
                 const float4* src = reinterpret_cast<const float4*>(span_at(ch));
                 float sum = 0.f;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
+                for (int i = 0; i < 8; ++i) {
                     const float4 x = src[i];
                     sum = fmaf(st[4 * i], x.x, sum);
                     sum = fmaf(st[4 * i + 1], x.y, sum);
@@ -420,193 +486,261 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
                 }
                 for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
                 if (lane == 0)
-                    w.anchors[(((slot0 + ch / (kLinSpan / CK)) * w.H + h) * blocks + blk) * 4 + (warp & 3)] = whole * sum;
+                    w.anchors[(((slot0 + ch / (kLinSpan / CK)) * w.H + h) * blocks + blk) * 8 + (warp - 8)] = whole * sum;
             }
-            const float f = w.s_state * (REV ? exp2f(gh + gl) : exp2f((eh - gh) + (el - gl)));
-            if (!wait(&S.full[s], c >> 1, 16u)) break;
-            float nf = 0.f;                               // stays 0 unless an element is not finite
+            if (!wait(&S.full_c[s], c >> 1, 16u)) break;
+            uint32_t top = 0;                             // the largest magnitudes
+            const bool in = row < L;
+            uint4 cv[4];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint32_t at = row * 128 + ((i ^ (row & 7)) << 4);
-                const uint4 v = lds128(tile + M::C + at);
-                const uint32_t word[4] = {v.x, v.y, v.z, v.w};
+            for (int i = 0; i < 4; ++i) cv[i] = lds128(tile + M::C + row * 128 + (((4 * half + i) ^ (row & 7)) << 4));
+            if (L < CK && !in)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) cv[i] = make_uint4(0, 0, 0, 0);
+            // f as the sum of two bf16 numbers f1 + f2: c f1 rounds to the first operand, what the rounding left has no more
+            // than eight bits and is exact, and c f2 joins it
+            const uint32_t f1 = bf2(f, f), f2 = bf2(f - low(f1), f - low(f1));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t at = row * 128 + (((4 * half + i) ^ (row & 7)) << 4);
+                const uint32_t word[4] = {cv[i].x, cv[i].y, cv[i].z, cv[i].w};
                 uint32_t hi[4], lo[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    float a = low(word[k]), b = high(word[k]);
-                    if (row < L) nf = fmaf(a, 0.f, fmaf(b, 0.f, nf));
-                    a = row < L ? f * a : 0.f;
-                    b = row < L ? f * b : 0.f;
-                    hi[k] = bf2(a, b);
-                    lo[k] = bf2(a - low(hi[k]), b - high(hi[k]));
+                    top = most(top, word[k]);
+                    hi[k] = mul_bf(word[k], f1);
+                    lo[k] = fma_bf(word[k], f2, fma_bf(word[k], f1, hi[k] ^ 0x80008000u));
                 }
                 sts128(base + M::V + at, hi[0], hi[1], hi[2], hi[3]);
                 sts128(base + M::V + 16384 + at, lo[0], lo[1], lo[2], lo[3]);
             }
-            const bool odd = !(nf == 0.f);
-            if (odd || row >= L) {                        // rare: a row to be passed over, or tokens of the next sequence (their
+            const bool odd = (top & 0x7F80u) == 0x7F80u || (top & 0x7F800000u) == 0x7F800000u;
+            if (odd || !in) {                             // rare: a row to be passed over, or tokens of the next sequence (their
                                                           // scores, which may be under way, are left out in any case)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) sts128(tile + M::C + row * 128 + i * 16, 0, 0, 0, 0);
-                if (row >= L)
+                for (int i = 0; i < 4; ++i) sts128(tile + M::C + row * 128 + (((4 * half + i) ^ (row & 7)) << 4), 0, 0, 0, 0);
+                if (!in)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) sts128(tile + M::B + (i >> 3) * 16384 + row * 128 + (i & 7) * 16, 0, 0, 0, 0);
+                    for (int i = 0; i < 8; ++i) sts128(tile + M::B + half * 16384 + row * 128 + i * 16, 0, 0, 0, 0);
                 if (odd)                                  // (the rest of an infinity is no number)
 #pragma unroll 1
-                    for (int i = 0; i < 8; ++i) {
-                        const uint32_t at = base + M::V + row * 128 + i * 16;
-                        const uint4 lo = lds128(at + 16384);
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t at = base + M::V + 16384 + row * 128 + (((4 * half + i) ^ (row & 7)) << 4);
+                        const uint4 lo = lds128(at);
                         const uint32_t word[4] = {lo.x, lo.y, lo.z, lo.w};
                         uint32_t z[4];
 #pragma unroll
                         for (int k = 0; k < 4; ++k) z[k] = bf2(finite_or_0(low(word[k])), finite_or_0(high(word[k])));
-                        sts128(at + 16384, z[0], z[1], z[2], z[3]);
+                        sts128(at, z[0], z[1], z[2], z[3]);
                     }
             }
-            const unsigned bits = __ballot_sync(0xffffffffu, odd && row < L);
-            if (lane == 0) S.flags[c & 1][warp & 3] = bits;
+            const unsigned bits = __ballot_sync(0xffffffffu, odd && in);
+            if (lane == 0) S.flags[s][half][warp & 3] = bits;
             fence_async_smem();
             arrive(&S.vhat);
-            if (!wait(&S.ds_full, c, 32u)) break;
+            if (!wait(&S.ds_full, c, 64u)) break;
             tc_fence_after();
-#pragma unroll
-            for (int i = 0; i < 64; i += 32) {
-                uint32_t a[2][16];
-                tmem_ld16(lanes + M::DS + i, a[0]);
-                tmem_ld16(lanes + M::DS + i + 16, a[1]);
+            {
+                uint32_t a[2][16], b[2][16];
+                tmem_ld16(lanes + M::DS + k0, a[0]);
+                tmem_ld16(lanes + M::DS + k0 + 16, a[1]);
+                if (KIND != PAIRS) {
+                    tmem_ld16(lanes + M::DS + 64 + k0, b[0]);
+                    tmem_ld16(lanes + M::DS + 64 + k0 + 16, b[1]);
+                }
                 tmem_ld_wait();
+                tc_fence_before();
+                arrive(&S.ds_free);
+                if (KIND != PAIRS)
 #pragma unroll
-                for (int k = 0; k < 32; ++k) st[i + k] = fmaf(whole, st[i + k], __uint_as_float(a[k >> 4][k & 15]));
-            }
-            tc_fence_before();
-            arrive(&S.ds_free);
-            if (c + 1 < chunks) {
-                if (!wait(&S.s_read, c, 64u)) break;
-                operand();
-            }
-        }
-        if (ok && w.s_out && row < w.da) {
-            const int64_t at = ((int64_t)n * w.H + h) * w.da * w.dc + (int64_t)row * w.s_r + (int64_t)c0 * w.s_c;
+                    for (int k = 0; k < 32; k += 2) {
+                        const F2 v = add2(F2{__uint_as_float(a[k >> 4][k & 15]), __uint_as_float(a[k >> 4][(k & 15) + 1])},
+                                          F2{__uint_as_float(b[k >> 4][k & 15]), __uint_as_float(b[k >> 4][(k & 15) + 1])});
+                        a[k >> 4][k & 15] = __float_as_uint(v.x);
+                        a[k >> 4][(k & 15) + 1] = __float_as_uint(v.y);
+                    }
 #pragma unroll
-            for (int i = 0; i < 64; ++i)
-                if (i < cols) w.s_out[at + (int64_t)i * w.s_c] = st[i];
+                for (int k = 0; k < 32; k += 2) {
+                    const F2 v = fma2(F2{whole, whole}, F2{st[k], st[k + 1]},
+                                      F2{__uint_as_float(a[k >> 4][k & 15]), __uint_as_float(a[k >> 4][(k & 15) + 1])});
+                    st[k] = v.x;
+                    st[k + 1] = v.y;
+                }
+            }
+            if (c + 1 < chunks) operand();
         }
-    } else if (warp == 8) {
+        if (ok && w.s_out && row < w.da)
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (k0 + i < cols) w.s_out[state_at + (int64_t)i * w.s_c] = st[i];
+    } else if (warp == 16) {
         // ------------------------------------------------------------------------------------------- tensor copies
         if (lane == 0 && chunks > 0) {
             prefetch_tmap(&maps.a);
             prefetch_tmap(&maps.b);
             prefetch_tmap(&maps.c);
             const int ha = h / w.a.group, hb = h / w.b.group, hc = h / w.c.group, hx = KIND == PAIRS ? h / w.x.group : 0;
-            int issued = 0, issued_x = 0;
-            uint64_t t_last = globaltimer_ns();
-            while (issued < chunks || (KIND == PAIRS && issued_x < chunks)) {
+            int issued = 0, issued_c = 0, issued_x = 0;
+            uint64_t last = globaltimer_ns();
+            // each stream is refilled as soon as what reads its buffer is done: polled, so that none waits behind another
+            while (issued < chunks || issued_c < chunks || (KIND == PAIRS && issued_x < chunks)) {
                 bool progress = false;
-                if (issued < chunks) {
-                    const int c = issued, s = c & 1;
-                    if (c < 2 || mbar_test(&S.empty[s], ((c >> 1) + 1) & 1)) {
-                        const int t = (int)(first + (int64_t)chunk_of(c) * CK);
-                        uint8_t* tile = smem + s * M::STAGE;
-                        mbar_arrive_expect_tx(&S.full[s], M::STAGE);
-                        for (int i = 0; i < 2; ++i) {
-                            tma_load_3d(tile + M::A + 16384 * i, &maps.a, &S.full[s], 64 * i, ha, t);
-                            tma_load_3d(tile + M::B + 16384 * i, &maps.b, &S.full[s], 64 * i, hb, t);
-                        }
-                        tma_load_3d(tile + M::C, &maps.c, &S.full[s], c0, hc, t);
-                        ++issued;
-                        progress = true;
+                if (issued < chunks && (issued < 2 || mbar_test(&S.empty[issued & 1], ((issued >> 1) + 1) & 1))) {
+                    const int s = issued & 1, t = (int)(first + (int64_t)chunk_of(issued) * CK);
+                    uint8_t* tile = smem + s * M::STAGE;
+                    mbar_arrive_expect_tx(&S.full[s], 65536);
+                    for (int i = 0; i < 2; ++i) {
+                        tma_load_3d(tile + M::A + 16384 * i, &maps.a, &S.full[s], 64 * i, ha, t);
+                        tma_load_3d(tile + M::B + 16384 * i, &maps.b, &S.full[s], 64 * i, hb, t);
                     }
+                    ++issued;
+                    progress = true;
+                }
+                if (issued_c < chunks && (issued_c < 2 || mbar_test(&S.empty_c[issued_c & 1], ((issued_c >> 1) + 1) & 1))) {
+                    const int s = issued_c & 1;
+                    mbar_arrive_expect_tx(&S.full_c[s], 16384);
+                    tma_load_3d(smem + s * M::STAGE + M::C, &maps.c, &S.full_c[s], c0, hc, (int)(first + (int64_t)chunk_of(issued_c) * CK));
+                    ++issued_c;
+                    progress = true;
                 }
                 if (KIND == PAIRS && issued_x < chunks && (issued_x < 1 || mbar_test(&S.x_empty, (issued_x - 1) & 1))) {
-                    const int t = (int)(first + (int64_t)chunk_of(issued_x) * CK);
                     mbar_arrive_expect_tx(&S.x_full, 16384);
-                    tma_load_3d(smem + M::X, &maps.x, &S.x_full, c0, hx, t);
+                    tma_load_3d(smem + M::X, &maps.x, &S.x_full, c0, hx, (int)(first + (int64_t)chunk_of(issued_x) * CK));
                     ++issued_x;
                     progress = true;
                 }
-                if (progress) t_last = globaltimer_ns();
-                else if (globaltimer_ns() - t_last > kWait) {
-                    report(128u);
+                if (progress) {
+                    last = globaltimer_ns();
+                } else if (globaltimer_ns() - last > kWait) {
+                    report(256u);
                     break;
                 }
             }
             // what was asked for has landed before the block leaves
             for (int c = issued > 2 ? issued - 2 : 0; c < issued; ++c) mbar_wait(&S.full[c & 1], (c >> 1) & 1, kWait);
-            if (KIND == PAIRS && issued_x > 0) mbar_wait(&S.x_full, (issued_x - 1) & 1, kWait);
+            for (int c = issued_c > 2 ? issued_c - 2 : 0; c < issued_c; ++c) mbar_wait(&S.full_c[c & 1], (c >> 1) & 1, kWait);
+            if (issued_x > 0) mbar_wait(&S.x_full, (issued_x - 1) & 1, kWait);
         }
-    } else if (warp == 9) {
+    } else if (warp == 17) {
         // ------------------------------------------------------------------------------------------------ products
-        if (lane == 0 && chunks > 0) {
-            auto until = [&](uint64_t* bar, int phase, unsigned bit) {
-                if (!ok) return false;
-                ok = mbar_wait(bar, phase & 1, kWait);
-                if (!ok) report(bit);
-                return ok;
-            };
+        if (chunks > 0) {
             constexpr uint32_t id_raw = idesc_f16(128, 128, true, false, false);   // A (K-major) x B (K-major)
-            constexpr uint32_t id_ds = idesc_f16(128, 64, true, true, true);       // B^T (MN-major) x scaled C (MN-major)
+            constexpr uint32_t id_ds = idesc_f16(128, KIND == PAIRS ? 64 : 128, true, true, true);   // B^T (MN-major) x scaled C (MN-major)
             constexpr uint32_t id_oi = idesc_f16(128, 64, true, false, true);      // A (K-major) x S (MN-major); P (TMEM) x C
-            const int ksteps = (w.da + 15) / 16;
-            auto scores = [&](int c) {
-                const uint32_t tile = base + (c & 1) * M::STAGE;
-                const uint64_t a = sdesc(tile + M::A, 16, 1024), b = sdesc(tile + M::B, 16, 1024);
-                for (int k = 0; k < ksteps; ++k)
-                    mma_f16(tmem + M::RAW, a + (k >> 2) * 1024 + (k & 3) * 2, b + (k >> 2) * 1024 + (k & 3) * 2, id_raw, k > 0);
-                if (KIND != PAIRS) mma_commit(&S.raw_full);
+            const bool wide = w.da > 64;                  // (the second half of the channels is all zeros else)
+            const uint64_t v = sdesc(base + M::V, 16384, 1024), so = sdesc(base + M::S, 16384, 1024);
+            const uint64_t a0 = sdesc(base + M::A, 16, 1024), b0 = sdesc(base + M::B, 16, 1024);
+            const uint64_t bt0 = sdesc(base + M::B, 16384, 1024), c0d = sdesc(base + M::C, 16384, 1024);
+            constexpr uint64_t NEXT = M::STAGE / 16;      // (descriptors count in 16 bytes)
+            auto scores = [&](int c) {                    // raw = A B^T
+                const uint64_t a = a0 + (c & 1) * NEXT, b = b0 + (c & 1) * NEXT;
+                const uint32_t d = tmem + M::RAW + (c & 1) * M::RING;
+                if (elected()) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) mma_f16(d, a + k * 2, b + k * 2, id_raw, k > 0);
+                    if (wide)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) mma_f16(d, a + 1024 + k * 2, b + 1024 + k * 2, id_raw, 1u);
+                    if (KIND != PAIRS) mma_commit(&S.raw_full[c & 1]);
+                }
+                __syncwarp();
             };
-            if (until(&S.full[0], 0, 256u)) {
+            auto inter = [&](int c) {                     // A S
+                const int freed = c - (KIND == PAIRS ? 1 : 2);
+                if (!wait(&S.s_ready, c, 1u << 14) || (freed >= 0 && !wait(&S.o_free[freed & 1], freed >> 1, 1u << 15))) return;
                 tc_fence_after();
-                if (KIND != PAIRS) scores(0);
+                const uint64_t a = a0 + (c & 1) * NEXT;
+                const uint32_t d = tmem + M::OI + (c & 1) * M::OI_RING;
+                if (elected()) {
+#pragma unroll
+                    for (int part = KIND == SPLIT ? 1 : 0; part >= 0; --part) {
+                        const uint32_t on = KIND == SPLIT && part == 0;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) mma_f16(d, a + k * 2, so + part * 1024 + k * 128, id_oi, on || k > 0);
+                        if (wide)
+#pragma unroll
+                            for (int k = 4; k < 8; ++k) mma_f16(d, a + 1024 + (k - 4) * 2, so + part * 1024 + k * 128, id_oi, 1u);
+                    }
+                }
+                __syncwarp();
+            };
+            if (KIND != PAIRS && wait(&S.full[0], 0, 512u)) {
+                tc_fence_after();
+                scores(0);
             }
             for (int c = 0; c < chunks && ok; ++c) {
                 const int s = c & 1;
-                const uint32_t tile = base + s * M::STAGE;
                 if (KIND == PAIRS) {
-                    if (!until(&S.full[s], c >> 1, 256u) || (c > 0 && !until(&S.raw_free, c - 1, 512u))) break;
+                    if (!wait(&S.full[s], c >> 1, 512u) || (c > 0 && !wait(&S.raw_free, c - 1, 1u << 10))) break;
                     tc_fence_after();
                     scores(c);
                 }
-                if (!until(&S.vhat, c, 1u << 10) || (c > 0 && !until(&S.ds_free, c - 1, 1u << 11))) break;
+                inter(c);
+                if (!ok || !wait(&S.vhat, c, 1u << 11) || (c > 0 && !wait(&S.ds_free, c - 1, 1u << 12))) break;
                 tc_fence_after();
-                const uint64_t bt = sdesc(tile + M::B, 16384, 1024), v = sdesc(base + M::V, 16384, 1024);
+                if (elected()) {
+                    const uint64_t bt = bt0 + s * NEXT;
+                    if (KIND == PAIRS)
 #pragma unroll
-                for (int k = 0; k < 8; ++k) mma_f16(tmem + M::DS, bt + k * 128, v + 1024 + k * 128, id_ds, k > 0);
+                        for (int k = 0; k < 8; ++k) mma_f16(tmem + M::DS, bt + k * 128, v + 1024 + k * 128, id_ds, k > 0);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) mma_f16(tmem + M::DS, bt + k * 128, v + k * 128, id_ds, 1u);
-                mma_commit(&S.ds_full);
-                if (KIND == PAIRS) {                      // raw2 = X C^T (behind vhat: rows of C that are not finite are out)
-                    if (!until(&S.x_full, c, 1u << 12)) break;
-                    tc_fence_after();
-                    const uint64_t x = sdesc(base + M::X, 16, 1024), ct = sdesc(tile + M::C, 16, 1024);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) mma_f16(tmem + M::RAW2, x + k * 2, ct + k * 2, id_raw, k > 0);
-                    mma_commit(&S.raw_full);
-                    mma_commit(&S.x_empty);
-                } else if (c + 1 < chunks) {
-                    if (!until(&S.full[s ^ 1], (c + 1) >> 1, 256u) || !until(&S.raw_free, c, 512u)) break;
-                    tc_fence_after();
-                    scores(c + 1);
+                    for (int k = 0; k < 8; ++k) mma_f16(tmem + M::DS, bt + k * 128, v + k * 128, id_ds, KIND == PAIRS || k > 0);
+                    mma_commit(&S.ds_full);               // (of both products: the state's operand has been read too)
+                    mma_commit(&S.empty[s]);
                 }
-                if (!until(&S.s_ready, c, 1u << 13) || (c > 0 && !until(&S.o_free, c - 1, 1u << 14))) break;
-                tc_fence_after();
-                const uint64_t a = sdesc(tile + M::A, 16, 1024), so = sdesc(base + M::S, 16384, 1024);
-                if (KIND == SPLIT)
-                    for (int k = 0; k < ksteps; ++k)
-                        mma_f16(tmem + M::OI, a + (k >> 2) * 1024 + (k & 3) * 2, so + 1024 + k * 128, id_oi, k > 0);
-                for (int k = 0; k < ksteps; ++k)
-                    mma_f16(tmem + M::OI, a + (k >> 2) * 1024 + (k & 3) * 2, so + k * 128, id_oi, KIND == SPLIT || k > 0);
-                mma_commit(&S.s_read);
-                if (!until(&S.p_ready[KIND == PAIRS ? 0 : s], KIND == PAIRS ? c : c >> 1, 1u << 15)) break;
-                tc_fence_after();
-                const uint64_t cm = sdesc(tile + M::C, 16384, 1024);
-                const uint32_t p = tmem + M::P + (KIND == PAIRS ? 0 : s * 64);
+                __syncwarp();
+                if (KIND == PAIRS) {                      // raw2 = X C^T (behind vhat: rows of C that are not finite are out)
+                    if (!wait(&S.x_full, c, 1u << 13)) break;
+                    tc_fence_after();
+                    if (elected()) {
+                        const uint64_t x = sdesc(base + M::X, 16, 1024), ct = sdesc(base + s * M::STAGE + M::C, 16, 1024);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) mma_f16_ts(tmem + M::OA, p + 8 * k, cm + k * 128, id_oi, k > 0);
-                mma_commit(&S.o_full);
-                mma_commit(&S.empty[s]);
+                        for (int k = 0; k < 4; ++k) mma_f16(tmem + M::RAW2, x + k * 2, ct + k * 2, id_raw, k > 0);
+                        mma_commit(&S.raw_full[s]);
+                        mma_commit(&S.x_empty);
+                    }
+                    __syncwarp();
+                }
+                // the next scores and P C, whichever can go first; the scores go into the place of P and P C of the chunk before
+                bool next = KIND == PAIRS || c + 1 == chunks, product = false;
+                for (uint64_t t0 = 0; !(next && product);) {
+                    bool progress = false;
+                    if (!next && __all_sync(0xffffffffu, mbar_test(&S.full[s ^ 1], ((c + 1) >> 1) & 1)) &&
+                        (c == 0 || __all_sync(0xffffffffu, mbar_test(&S.o_free[s ^ 1], ((c - 1) >> 1) & 1)))) {
+                        tc_fence_after();
+                        scores(c + 1);
+                        next = progress = true;
+                    }
+                    if (!product && __all_sync(0xffffffffu, mbar_test(&S.p_ready[s], (c >> 1) & 1))) {
+                        tc_fence_after();
+                        if (elected()) {                  // P C
+                            const uint64_t cm = c0d + s * NEXT;
+                            const uint32_t p = tmem + M::P + s * M::RING;
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) mma_f16_ts(tmem + M::OA + s * M::RING, p + 8 * k, cm + k * 128, id_oi, k > 0);
+                            mma_commit(&S.o_full[s]);
+                            if (KIND == PLAIN) mma_commit(&S.empty_c[s]);
+                        }
+                        __syncwarp();
+                        product = progress = true;
+                    }
+                    if (progress) {
+                        t0 = 0;
+                    } else {
+                        const uint64_t now = globaltimer_ns();
+                        if (t0 == 0) t0 = now;
+                        ok = __all_sync(0xffffffffu, now - t0 <= kWait);
+                        if (!ok) {
+                            if (lane == 0) report(1u << 16);
+                            break;
+                        }
+                    }
+                }
             }
+            // every product has completed before the block leaves
+            if (ok) mbar_wait(&S.o_full[(chunks - 1) & 1], ((chunks - 1) >> 1) & 1, kWait);
         }
-    } else if (warp == 10) {
+    } else if (warp == 18) {
         // ------------------------------------------------------------------------------------------------- decays
         auto fetch = [&](int c, float (&g)[4]) {
             const int L = c < chunks ? rows_of(c) : 0;
@@ -619,35 +753,37 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
         float g[4];
         fetch(0, g);
         for (int c = 0; c < chunks; ++c) {
-            double s[4], sum = 0.0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s[i] = sum += lin::log2_decay(g[i]);
-            fetch(c + 1, g);
-            double all = sum;
-            for (int m = 1; m < 32; m <<= 1) {
-                const double y = __shfl_up_sync(0xffffffffu, all, m);
-                if (lane >= m) all += y;
-            }
-            if (c > 0 && !wait(&S.gate_empty, c - 1, 1u << 16)) break;
-            float hi[4], lo[4];
+            lin::Log2 x[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const double x = (all - sum) + s[i];
-                hi[i] = (float)x;
-                lo[i] = (float)(x - (double)hi[i]);
+                const lin::Log2 y = lin::log2_decay(g[i]);
+                x[i] = i > 0 ? lin::add(x[i - 1], y) : y;
             }
-            reinterpret_cast<float4*>(Gh)[lane] = make_float4(hi[0], hi[1], hi[2], hi[3]);
-            reinterpret_cast<float4*>(Gl)[lane] = make_float4(lo[0], lo[1], lo[2], lo[3]);
-            arrive(&S.gate_full);
+            fetch(c + 1, g);
+            const lin::Log2 all = lin::prefix(x[3], lane);
+            lin::Log2 before{__shfl_up_sync(0xffffffffu, all.hi, 1), __shfl_up_sync(0xffffffffu, all.lo, 1)};
+            if (lane > 0)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[i] = lin::add(before, x[i]);
+            // the first, or last, token of the column block (eight lanes)
+            const int at = REV ? lane & 24 : lane | 7;
+            const lin::Log2 ref{__shfl_sync(0xffffffffu, x[REV ? 0 : 3].hi, at), __shfl_sync(0xffffffffu, x[REV ? 0 : 3].lo, at)};
+            float cf[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) cf[i] = ex2(REV ? lin::minus(x[i], ref) : lin::minus(ref, x[i]));
+            const uint32_t lo[2] = {bf2(x[0].lo, x[1].lo), bf2(x[2].lo, x[3].lo)};
+            if (c > 1 && !wait(&S.gate_empty[c & 1], (c >> 1) + 1, 1u << 17)) break;
+            reinterpret_cast<float4*>(Gh(c))[lane] = make_float4(x[0].hi, x[1].hi, x[2].hi, x[3].hi);
+            reinterpret_cast<float4*>(Cf(c))[lane] = make_float4(cf[0], cf[1], cf[2], cf[3]);
+            reinterpret_cast<uint2*>(Gl(c))[lane] = make_uint2(lo[0], lo[1]);
+            arrive(&S.full[c & 1]);
         }
     }
-    // every product has completed: the last chunk's are behind o_full (a walk that gave up waits as long as its waits)
-    if (warp == 9 && lane == 0 && chunks > 0 && ok) mbar_wait(&S.o_full, (chunks - 1) & 1, kWait);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     __syncwarp();
-    if (warp == 9) tmem_dealloc(tmem, 512);
+    if (warp == 17) tmem_dealloc(tmem, 512);
 }
 
 // [tokens, heads, d] bf16 with strides: boxes of 64 channels x 1 head x 128 tokens

@@ -39,15 +39,32 @@ __device__ __forceinline__ int by_length(const int32_t* cu, int n_seqs, int T, i
     return hit ? __ffs(hit) - 1 : rank;
 }
 
+// Log decays and their prefix sums are sums of two floats, hi + lo, so that differences within a chunk are exact to far below
+// fp32's roundoff (a single float would be off by 2^-24 of the chunk's whole decay, so by 1e-5 and more next to strong decays;
+// 64-bit arithmetic has a sixty-fourth of the rate here: a chunk's 128 prefix sums took longer than its products).
+struct Log2 { float hi, lo; };
+__device__ __forceinline__ Log2 add(Log2 a, Log2 b) {     // the sum's rounding error, then both joined anew
+    const float s = __fadd_rn(a.hi, b.hi), t = __fsub_rn(s, a.hi);
+    const float e = __fadd_rn(__fadd_rn(__fsub_rn(a.hi, __fsub_rn(s, t)), __fsub_rn(b.hi, t)), __fadd_rn(a.lo, b.lo));
+    const float hi = __fadd_rn(s, e);
+    return {hi, __fsub_rn(e, __fsub_rn(hi, s))};
+}
+__device__ __forceinline__ float minus(Log2 a, Log2 b) { return (a.hi - b.hi) + (a.lo - b.lo); }
 // A log decay in base 2.  Below -1000 (2^-1000 is 0 in fp32 many times over) and at -inf it is -1000: sums of them stay finite,
 // so that differences within a chunk do too.  A NaN stays one.
-__device__ __forceinline__ double log2_decay(float g) {
-    const double x = (double)g * 1.4426950408889634074;
-    return x < -1000.0 ? -1000.0 : x;
+__device__ __forceinline__ Log2 log2_decay(float g) {
+    constexpr float L = 1.44269502162933349609f, M = 1.92596299112661746888e-8f;     // log2(e) rounded, and the rest
+    const float x = __fmul_rn(g, L);
+    return x < -1000.f ? Log2{-1000.f, 0.f} : Log2{x, fmaf(g, L, -x) + __fmul_rn(g, M)};
 }
-// 2^x for x <= 0 given as a double (a difference of prefix sums, exact to far below fp32's roundoff; in fp32 the sums themselves
-// would be off by 2^-24 of the chunk's whole decay, so by 1e-5 and more next to strong decays)
-__device__ __forceinline__ float exp2_of(double x) { return exp2f((float)x); }
+// Sums over the lanes up to this one.
+__device__ __forceinline__ Log2 prefix(Log2 a, int lane) {
+    for (int m = 1; m < 32; m <<= 1) {
+        const Log2 b{__shfl_up_sync(0xffffffffu, a.hi, m), __shfl_up_sync(0xffffffffu, a.lo, m)};
+        if (lane >= m) a = add(a, b);
+    }
+    return a;
+}
 
 }  // namespace lin
 }  // namespace gdn

@@ -24,7 +24,7 @@ __global__ void __launch_bounds__(THREADS) lin_walk_kernel(const LinWalk w) {
     float* Bs = As + CH * lda;                         // [CH][lda]
     float* Cs = Bs + CH * lda;                         // [CH][COLS]
     float* P = Cs + CH * COLS;                         // [CH][CH + 1]
-    __shared__ double G[CH];
+    __shared__ lin::Log2 G[CH];
     __shared__ float rowf[CH], colf[CH], whole_s, red[THREADS / 32];
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -71,17 +71,13 @@ __global__ void __launch_bounds__(THREADS) lin_walk_kernel(const LinWalk w) {
             Cs[e] = i < L && cc < cols ? mix::ld(c + (first + t0 + i) * w.c.tok + cc) : 0.f;
         }
         if (warp == 0) {                               // prefix sums of the log decays
-            double s = lane < L ? lin::log2_decay(w.g[(first + t0 + lane) * w.g_tok + h * w.g_head]) : 0.0;
-            for (int m = 1; m < 32; m <<= 1) {
-                const double y = __shfl_up_sync(0xffffffffu, s, m);
-                if (lane >= m) s += y;
-            }
-            const double end = __shfl_sync(0xffffffffu, s, 31);
-            const float before = lin::exp2_of(s), behind = lin::exp2_of(end - s);
+            const lin::Log2 s = lin::prefix(lane < L ? lin::log2_decay(w.g[(first + t0 + lane) * w.g_tok + h * w.g_head]) : lin::Log2{0.f, 0.f}, lane);
+            const lin::Log2 end{__shfl_sync(0xffffffffu, s.hi, 31), __shfl_sync(0xffffffffu, s.lo, 31)};
+            const float before = exp2f(s.hi + s.lo), behind = exp2f(lin::minus(end, s));
             G[lane] = s;
             rowf[lane] = w.s_inter * (w.rev ? behind : before);
             colf[lane] = w.s_state * (w.rev ? before : behind);
-            if (lane == 0) whole_s = lin::exp2_of(end);
+            if (lane == 0) whole_s = exp2f(end.hi + end.lo);
         }
         __syncthreads();
         for (int e = tid; e < CH * CH; e += THREADS) {
@@ -89,7 +85,7 @@ __global__ void __launch_bounds__(THREADS) lin_walk_kernel(const LinWalk w) {
             if (w.rev ? j < i : j > i) continue;
             float s = 0.f;
             for (int r = 0; r < da; ++r) s = fmaf(As[i * lda + r], Bs[j * lda + r], s);
-            P[i * (CH + 1) + j] = w.s_intra * s * lin::exp2_of(w.rev ? G[j] - G[i] : G[i] - G[j]);
+            P[i * (CH + 1) + j] = w.s_intra * s * exp2f(w.rev ? lin::minus(G[j], G[i]) : lin::minus(G[i], G[j]));
         }
         __syncthreads();
         for (int i = warp; i < L; i += THREADS / 32) { // a warp a row, a lane a column
@@ -148,10 +144,10 @@ __global__ void __launch_bounds__(THREADS) lin_walk_kernel(const LinWalk w) {
         }
 }
 
-// One block for each (span slot, head), a thread a token; sums in 64 bits.
+// One block for each (span slot, head), a thread a token: sums of at most kLinSpan terms.
 constexpr int DG_WARPS = kLinSpan / 32;
 __global__ void __launch_bounds__(kLinSpan) lin_dg_kernel(const LinDg a) {
-    __shared__ double plus_s[DG_WARPS], minus_s[DG_WARPS], pairs_s[DG_WARPS];
+    __shared__ float plus_s[DG_WARPS], minus_s[DG_WARPS], pairs_s[DG_WARPS];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int h = blockIdx.x % a.H;
     const int64_t slot = blockIdx.x / a.H;
@@ -166,23 +162,32 @@ __global__ void __launch_bounds__(kLinSpan) lin_dg_kernel(const LinDg a) {
     lin::sequence(a.cu, a.T, n, first, len);
     const int64_t at = (slot - (first / kLinSpan + n)) * kLinSpan;
     if (at < 0 || at >= len) {
-        if (a.per_head && tid == 0) a.part[slot * a.H + h] = 0.0;
+        if (a.per_head && tid == 0) a.part[slot * a.H + h] = 0.f;
         return;
     }
     const bool in = at + tid < len;
-    double plus = 0.0, minus = 0.0, pairs = 0.0;
+    float plus = 0.f, minus = 0.f, pairs = 0.f;
     if (in) {
         const int64_t t = (int64_t)h * a.rows() + first + at + tid, step = (int64_t)a.H * a.rows();
         for (int k = 0; k < a.blocks; ++k) {
-            plus += (double)a.plus[t + k * step];
-            minus += (double)a.minus[t + k * step];
+            plus += a.plus[t + k * step];
+            minus += a.minus[t + k * step];
         }
-        for (int k = 0; k < a.pair_blocks; ++k) pairs += (double)a.pairs[t + k * step] - (a.pairs_minus ? (double)a.pairs_minus[t + k * step] : 0.0);
+        if (a.pairs_minus) {
+            for (int k = 0; k < a.pair_blocks; ++k) pairs += a.pairs[t + k * step] - a.pairs_minus[t + k * step];
+        } else {                                       // (sums over keys of a query come by 32 keys of the chunk)
+            const int own = tid % kLinChunk / 32;
+            for (int k = 0; k < a.pair_blocks; ++k) {
+                const float* p = a.pairs + t + 5 * k * step;
+                pairs += p[4 * step];
+                for (int i = 0; i <= own; ++i) pairs += p[i * step];
+            }
+        }
     }
-    double behind = plus, behind_pairs = pairs, before = minus;       // from this token on; up to it
+    float behind = plus, behind_pairs = pairs, before = minus;       // from this token on; up to it
     for (int m = 1; m < 32; m <<= 1) {
-        const double x = __shfl_down_sync(0xffffffffu, behind, m), y = __shfl_down_sync(0xffffffffu, behind_pairs, m);
-        const double z = __shfl_up_sync(0xffffffffu, before, m);
+        const float x = __shfl_down_sync(0xffffffffu, behind, m), y = __shfl_down_sync(0xffffffffu, behind_pairs, m);
+        const float z = __shfl_up_sync(0xffffffffu, before, m);
         if (lane + m < 32) {
             behind += x;
             behind_pairs += y;
@@ -195,35 +200,35 @@ __global__ void __launch_bounds__(kLinSpan) lin_dg_kernel(const LinDg a) {
     }
     if (lane == 31) minus_s[warp] = before;
     before = __shfl_up_sync(0xffffffffu, before, 1);
-    if (lane == 0) before = 0.0;
+    if (lane == 0) before = 0.f;
     __syncthreads();
     const int per = a.chunk / 32, chunk = warp / per;                // warps of a chunk
-    double dg = behind + behind_pairs + before;
+    float dg = behind + behind_pairs + before;
     for (int i = warp + 1; i < (chunk + 1) * per; ++i) dg += plus_s[i] + pairs_s[i];
     for (int i = chunk * per; i < warp; ++i) dg += minus_s[i];
-    for (int k = 0; k < a.anchor_blocks; ++k) dg += (double)a.anchors[(slot * a.H + h) * a.anchor_blocks + k];
+    for (int k = 0; k < a.anchor_blocks; ++k) dg += a.anchors[(slot * a.H + h) * a.anchor_blocks + k];
     for (int i = 0; i < chunk * per; ++i) dg += minus_s[i];
     for (int i = per; i < (chunk + 1) * per; ++i) dg -= plus_s[i];
     if (!a.per_head) {
-        if (in) a.dg[(first + at + tid) * a.H + h] = (float)dg;
+        if (in) a.dg[(first + at + tid) * a.H + h] = dg;
         return;
     }
-    double all = in ? dg : 0.0;
+    float all = in ? dg : 0.f;
     for (int m = 16; m > 0; m >>= 1) all += __shfl_xor_sync(0xffffffffu, all, m);
     __syncthreads();
     if (lane == 0) plus_s[warp] = all;
     __syncthreads();
     if (tid == 0) {
-        double t = 0.0;
+        float t = 0.f;
         for (int i = 0; i < DG_WARPS; ++i) t += plus_s[i];
         a.part[slot * a.H + h] = t;
     }
 }
 
-__global__ void lin_dg_sum_kernel(const double* part, float* dg, int64_t slots, int H) {
+__global__ void lin_dg_sum_kernel(const float* part, float* dg, int64_t slots, int H) {
     const int h = blockIdx.x, lane = threadIdx.x;
     double s = 0.0;
-    for (int64_t i = lane; i < slots; i += 32) s += part[i * H + h];
+    for (int64_t i = lane; i < slots; i += 32) s += (double)part[i * H + h];
     for (int m = 16; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
     if (lane == 0) dg[h] = (float)s;
 }
