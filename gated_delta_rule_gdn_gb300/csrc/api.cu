@@ -568,7 +568,7 @@ gdn_status gdn_test_inject(int what) {
 const char* gdn_last_error(void) { return g_last_error.c_str(); }
 
 gdn_status gdn_device_status(int clear) {
-    unsigned tp = 0, gt = 0, bw = 0, d2 = 0, lr = 0, lb = 0, la = 0;
+    unsigned tp = 0, gt = 0, bw = 0, d2 = 0, lr = 0, lb = 0, la = 0, lp = 0;
     cudaError_t e = gdn::tp_read_and_clear_status(&tp, clear != 0);
     if (e == cudaSuccess) e = gdn::gt_read_and_clear_status(&gt, clear != 0);
     if (e == cudaSuccess) e = gdn::d256_read_and_clear_status(&d2, clear != 0);
@@ -578,6 +578,8 @@ gdn_status gdn_device_status(int clear) {
     if (e == cudaSuccess) e = gdn::glr_bwd_read_and_clear_status(&lb, clear != 0);
     lr |= lb;
     if (e == cudaSuccess) e = gdn::lin_read_and_clear_status(&la, clear != 0);
+    if (e == cudaSuccess) e = gdn::lin_pairs_read_and_clear_status(&lp, clear != 0);
+    la |= lp << 20;
     if (e != cudaSuccess) return cuda_fail(e, "gdn_device_status");
     const unsigned nf = gdn::kStatusNonfinite;
     if (((tp | gt) & ~nf) != 0 || bw != 0 || lr != 0 || la != 0)

@@ -45,12 +45,17 @@ struct LinWalk {
     // the span's first chunk.
     float* spans;
     float* anchors;
+    // Segments of a walk on the tensor cores (0: none), [segment slot][h][block][128][kLinCols] states, first of each segment from
+    // nothing, then entering it, and [segment slot][h] what each keeps of the state entering it.
+    int seg_chunks;
+    float *seg_states, *seg_kept;
     __host__ __device__ int N() const { return cu ? n_seqs : B; }
     __host__ __device__ int64_t rows() const { return (int64_t)B * T; }
 };
 constexpr int kLinSpan = 256, kLinGenericChunk = 32, kLinChunk = 128;
 // The span slots of a call: those of sequence n begin at first_token / kLinSpan + n.
-inline int64_t lin_span_slots(int64_t rows, int64_t N) { return rows / kLinSpan + N + 1; }
+inline int64_t lin_slots(int64_t rows, int64_t N, int64_t size) { return rows / size + N + 1; }
+inline int64_t lin_span_slots(int64_t rows, int64_t N) { return lin_slots(rows, N, kLinSpan); }
 // Columns of c that a block of threads takes (the generic walk, the tensor-core one), for dots and anchors.
 constexpr int kLinGenericCols = 32, kLinCols = 64;
 inline int lin_blocks(int dc, bool tensor) { return (dc + (tensor ? kLinCols : kLinGenericCols) - 1) / (tensor ? kLinCols : kLinGenericCols); }
@@ -59,11 +64,28 @@ inline size_t lin_span_floats(int da, int dc, bool tensor) {
 }
 
 cudaError_t launch_lin_walk_generic(const LinWalk& w, cudaStream_t s);
-// The tensor-core walk: whether it takes the request, and with `pairs` (dv's walk, with x = v) the sums over pairs of tokens of
-// a chunk, pairs[block][5][h][token]: for a query those over the keys before it among the chunk's 32 first, second, ... (up to
-// its own 32), then for a key minus the sum over the queries behind it.
+// The tensor-core walk: whether it takes the request, the chunks of its segments (0: none), and the walk; its dots are those of
+// the state's part alone.
 bool lin_tensor_fits(const LinWalk& w);
-cudaError_t launch_lin_walk_tensor(const LinWalk& w, float* pairs, cudaStream_t s);
+int lin_segment_chunks(int64_t rows, int64_t N, int H, int dc);
+cudaError_t launch_lin_walk_tensor(const LinWalk& w, cudaStream_t s);
+cudaError_t launch_lin_segments(const LinWalk& w, cudaStream_t s);
+// What the pairs of tokens of a chunk have of the decays' gradient, pairs[h][token]: the sum over the keys before the token
+// minus the sum over the queries behind it, of scale e^(G_i - G_j) (q_i . k_j) (dO_i . v_j).
+struct LinPairs {
+    LinTok q, k, v, o;
+    int dk, dv;
+    float scale;
+    const float* g;
+    int64_t g_tok, g_head;
+    const int32_t* cu;
+    int n_seqs, B, T, H;
+    float* pairs;
+    __host__ __device__ int N() const { return cu ? n_seqs : B; }
+    __host__ __device__ int64_t rows() const { return (int64_t)B * T; }
+};
+cudaError_t launch_lin_pairs(const LinPairs& a, cudaStream_t s);
+cudaError_t lin_pairs_read_and_clear_status(unsigned* value, bool clear);
 cudaError_t lin_read_and_clear_status(unsigned* value, bool clear);
 
 // dg from the walks' parts.  With S_in the state entering a token's chunk and D_out the gradient of the state leaving it,

@@ -38,7 +38,7 @@ gdn_status check_sizes(const char* fn, const Sizes& z, gdn_dtype dtype, gdn_algo
         if (!aligned(z.cu, 4)) return fail(GDN_ERR_INVALID_ARG, "%s: cu_seqlens is not 4-byte aligned", fn);
     }
     const int64_t most = (int64_t(1) << 31) - 1;       // blocks of a launch
-    if ((int64_t)z.N() > most / (8 * (int64_t)z.H) || gdn::lin_span_slots(z.rows(), z.N()) > most / z.H)
+    if ((int64_t)z.N() > most / (8 * (int64_t)z.H) || gdn::lin_slots(z.rows(), z.N(), gdn::kLinChunk) > most / z.H)
         return fail(GDN_ERR_UNSUPPORTED, "%s: %d sequences of %d heads need more than 2^31 blocks", fn, z.N(), z.H);
     if (z.rows() * z.H > (int64_t(1) << 40) / 256)
         return fail(GDN_ERR_UNSUPPORTED, "%s: tokens times heads is more than 2^32", fn);
@@ -75,11 +75,39 @@ gdn_status choose(const char* fn, gdn_algo algo, bool fits, bool& tensor) {
     return GDN_OK;
 }
 
+// Segments of the walks on the tensor cores, one set of states for all walks of a call (they come one after another).
+struct Segments {
+    int fwd, bwd;                                          // chunks of a segment: of walks whose columns are d_v, and d_k
+    size_t states, kept, bytes;
+    Segments(const Sizes& z, bool backward) {
+        fwd = gdn::lin_segment_chunks(z.rows(), z.N(), z.H, z.dv);
+        bwd = backward ? gdn::lin_segment_chunks(z.rows(), z.N(), z.H, z.dk) : 0;
+        states = kept = 0;
+        for (int i = 0; i < 2; ++i) {
+            const int chunks = i ? bwd : fwd;
+            if (chunks == 0) continue;
+            const size_t slots = (size_t)gdn::lin_slots(z.rows(), z.N(), (int64_t)chunks * gdn::kLinChunk) * z.H;
+            const size_t n = 4 * slots * 128 * gdn::kLinCols * gdn::lin_blocks(i ? z.dk : z.dv, true), m = 4 * slots;
+            states = n > states ? n : states;
+            kept = m > kept ? m : kept;
+        }
+        kept = (kept + 255) / 256 * 256;
+        bytes = states + kept;
+    }
+    void put(LinWalk& w, void* base, bool tensor, int chunks) const {
+        if (!tensor || chunks == 0) return;
+        w.seg_chunks = chunks;
+        w.seg_states = static_cast<float*>(base);
+        w.seg_kept = reinterpret_cast<float*>(static_cast<char*>(base) + states);
+    }
+};
+
 // Parts of the backward's workspace, each a multiple of 256 bytes (for either walk: which one it is goes by the buffers too).
 struct BwdParts {
     size_t plus, minus, pairs, spans, anchors, part, group, bytes;
-    explicit BwdParts(const Sizes& z) {
-        size_t at = 0;
+    Segments segments;
+    explicit BwdParts(const Sizes& z) : segments(z, true) {
+        size_t at = segments.bytes;
         auto take = [&](size_t n) {
             const size_t here = at;
             at += (n + 255) / 256 * 256;
@@ -90,9 +118,7 @@ struct BwdParts {
         const size_t span = gdn::lin_span_floats(z.dv, z.dk, false), tc = gdn::lin_span_floats(z.dv, z.dk, true);
         plus = take(4 * blocks * heads * (size_t)z.rows());
         minus = take(4 * blocks * heads * (size_t)z.rows());
-        // (the generic walks have two arrays of pairs, over the blocks of d_k; the tensor-core ones five, over those of d_v)
-        const size_t tc_pairs = 5 * (size_t)gdn::lin_blocks(z.dv, true);
-        pairs = take(4 * (2 * blocks > tc_pairs ? 2 * blocks : tc_pairs) * heads * (size_t)z.rows());
+        pairs = take(4 * 2 * blocks * heads * (size_t)z.rows());     // (the tensor cores' are one array, the generic walks' two a block)
         spans = take(4 * slots * heads * (span > tc ? span : tc));
         const size_t tc_blocks = 8 * (size_t)gdn::lin_blocks(z.dk, true);
         anchors = take(4 * slots * heads * (blocks > tc_blocks ? blocks : tc_blocks));
@@ -112,7 +138,7 @@ gdn_status lin_workspace_size(int backward, int B, int T, int H_k, int H, int d_
     if (n_seqs < 0) return fail(GDN_ERR_INVALID_ARG, "%s: n_seqs must be >= 0 (got %d)", fn, n_seqs);
     const Sizes z{B, T, H_k, H, d_k, d_v, n_seqs > 0 ? reinterpret_cast<const int32_t*>(uintptr_t(1) << 20) : nullptr, n_seqs};
     GDN_TRY(check_sizes(fn, z, GDN_F32, GDN_ALGO_AUTO));
-    *bytes = backward ? BwdParts(z).bytes : 0;
+    *bytes = backward ? BwdParts(z).bytes : Segments(z, false).bytes;
     return ok();
 }
 
@@ -148,8 +174,10 @@ gdn_status lin_chunk_fwd(const void* q, const void* k, const void* v, const floa
     bool tensor = false;
     GDN_TRY(choose(fn, algo, gdn::lin_tensor_fits(w), tensor));
     Workspace ws;
-    GDN_TRY(ws.get(fn, workspace, workspace_bytes, 0, static_cast<cudaStream_t>(stream)));
-    return finish(fn, tensor ? gdn::launch_lin_walk_tensor(w, nullptr, ws.s) : gdn::launch_lin_walk_generic(w, ws.s), ws);
+    const Segments segments(z, false);
+    GDN_TRY(ws.get(fn, workspace, workspace_bytes, tensor ? segments.bytes : 0, static_cast<cudaStream_t>(stream)));
+    segments.put(w, ws.ptr, tensor, segments.fwd);
+    return finish(fn, tensor ? gdn::launch_lin_walk_tensor(w, ws.s) : gdn::launch_lin_walk_generic(w, ws.s), ws);
 }
 
 gdn_status lin_chunk_bwd(const void* q, const void* k, const void* v, const float* g, int g_per_head, float scale,
@@ -223,21 +251,23 @@ gdn_status lin_chunk_bwd(const void* q, const void* k, const void* v, const floa
     state(wv, grad_final_state, grad_initial_state, d_v, 1);
     wv.out = grad_v;
     wv.out_f32 = dtype == GDN_F32;
-    wv.x = tv;
     bool tensor = false;
     if (T > 0)
         GDN_TRY(choose(fn, algo, gdn::lin_tensor_fits(wq) && gdn::lin_tensor_fits(wk) && gdn::lin_tensor_fits(wv) &&
                        aligned(grad_q, 16) && aligned(grad_k, 16), tensor));
-    auto run = [&](const LinWalk& w, float* sums) {
-        return tensor ? gdn::launch_lin_walk_tensor(w, sums, ws.s) : gdn::launch_lin_walk_generic(w, ws.s);
-    };
-    cudaError_t e = run(wq, nullptr);
+    parts.segments.put(wq, base, tensor, parts.segments.bwd);
+    parts.segments.put(wk, base, tensor, parts.segments.bwd);
+    parts.segments.put(wv, base, tensor, parts.segments.fwd);
+    auto run = [&](const LinWalk& w) { return tensor ? gdn::launch_lin_walk_tensor(w, ws.s) : gdn::launch_lin_walk_generic(w, ws.s); };
+    cudaError_t e = run(wq);
     if (e == cudaSuccess && group > 1)
         e = gdn::launch_lin_group_sum(part(parts.group), grad_q, wq.bf16, z.rows(), H_k, group, d_k, ws.s);
-    if (e == cudaSuccess) e = run(wk, nullptr);
+    if (e == cudaSuccess) e = run(wk);
     if (e == cudaSuccess && group > 1)
         e = gdn::launch_lin_group_sum(part(parts.group), grad_k, wk.bf16, z.rows(), H_k, group, d_k, ws.s);
-    if (e == cudaSuccess) e = run(wv, tensor ? pairs : nullptr);
+    if (e == cudaSuccess) e = run(wv);
+    if (tensor && e == cudaSuccess)
+        e = gdn::launch_lin_pairs({tq, tk, tv, to, d_k, d_v, scale, g, wq.g_tok, wq.g_head, z.cu, z.n_seqs, B, T, H, pairs}, ws.s);
     gdn::LinDg d{};
     d.plus = part(parts.plus);
     d.minus = part(parts.minus);
@@ -245,7 +275,7 @@ gdn_status lin_chunk_bwd(const void* q, const void* k, const void* v, const floa
     d.pairs_minus = tensor ? nullptr : pairs_minus;
     d.anchors = part(parts.anchors);
     d.blocks = gdn::lin_blocks(d_k, tensor);
-    d.pair_blocks = tensor ? gdn::lin_blocks(d_v, true) : d.blocks;
+    d.pair_blocks = tensor ? 1 : d.blocks;
     d.chunk = tensor ? gdn::kLinChunk : gdn::kLinGenericChunk;
     d.anchor_blocks = tensor ? 8 * d.blocks : d.blocks;
     d.dg = grad_g;

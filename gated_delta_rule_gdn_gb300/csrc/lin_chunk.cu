@@ -7,6 +7,9 @@
 // Four products of 128 rows, so that each fills the 128 lanes of a tensor-core instruction; the state's own change does not
 // depend on the state, so nothing but the fp32 update e^(G_end) S + dS is serial.
 //
+// Where there are few sequences and heads, a walk is divided into segments: a first pass takes the state of each from nothing
+// (STATE), a second joins them in order (lin_segments_kernel), and the walk proper starts each segment from its own state.
+//
 //   warps 0-7    scores and outputs, four warps a chunk in turn: raw out of tensor memory, times decays, as bf16 back into
 //                tensor memory (the first operand of P C); the outputs' epilogue
 //   warps 8-15   state, 32 columns a warpgroup: in registers, a row a thread; scaled values and the state as operands in
@@ -26,30 +29,24 @@
 // A row of C that is not finite would reach the tokens before it as 0 times that; it is taken out of P C (not out of the
 // state) and added to the rows that see it.
 
-#include "internal.h"
-#include "lin_common.cuh"
-#include "tc_common.cuh"
+#include "lin_tile.cuh"
 
 namespace gdn {
 namespace {
 
-using namespace tc;
-using mix::bf16;
-
 __device__ unsigned g_lin_status;
 __device__ __forceinline__ void report(unsigned bit) { atomicOr(&g_lin_status, bit); }
 
-constexpr int CK = kLinChunk, NB = kLinCols;              // tokens of a chunk, columns of c
-constexpr uint64_t kWait = 2000000000ull;
+constexpr int NB = kLinCols;                              // columns of c
 constexpr int THREADS = 640;
 
-// What a walk does besides: nothing, inner products of its rows with x (SPLIT: the state is exact enough for them), or the
-// sums over pairs of tokens (PAIRS).
-enum Kind { PLAIN, SPLIT, PAIRS };
+// A walk; one that also takes inner products of its rows with x, for which the state as an operand is exact enough (SPLIT); or
+// the state alone (STATE), of a segment from nothing.
+enum Kind { PLAIN, SPLIT, STATE };
 
 struct Bars {
     uint64_t full[2], full_c[2], empty[2], empty_c[2], gate_empty[2], raw_full[2], p_ready[2], o_full[2], o_free[2];
-    uint64_t raw_free, ds_full, ds_free, s_ready, vhat, x_full, x_empty;
+    uint64_t ds_full, ds_free, s_ready, vhat;
     uint32_t flags[2][2][4];                              // rows of C that are not finite, by chunk and half of the columns
     uint32_t tmem;
 };
@@ -57,32 +54,18 @@ struct Bars {
 template <Kind KIND>
 struct Map {                                              // shared memory
     static constexpr uint32_t STAGE = 81920, A = 0, B = 32768, C = 65536;
-    static constexpr uint32_t S = 2 * STAGE, V = S + (KIND == SPLIT ? 32768 : 16384), X = V + 32768;   // (PLAIN: outputs turn there)
+    static constexpr uint32_t S = 2 * STAGE, V = S + (KIND == SPLIT ? 32768 : 16384), TURN = V + 32768;      // (where outputs turn)
     // two buffers of each: G rounded, what the rounding left (bf16), column factors
-    static constexpr uint32_t GH = X + (KIND == SPLIT ? 0 : 16384), CF = GH + 1024, GL = CF + 1024, BARS = GL + 512;
+    static constexpr uint32_t GH = TURN + (KIND == PLAIN ? 16384 : 0), CF = GH + 1024, GL = CF + 1024, BARS = GL + 512;
     static constexpr uint32_t BYTES = BARS + sizeof(Bars);
-    // tensor memory columns.  Where the second scores of PAIRS do not take the room, scores have two buffers, P lies in the
-    // first half of its scores and P C in the second, A S has two buffers, and the two parts of the state's change lie side by side.
-    static constexpr bool TIGHT = KIND == PAIRS;
-    static constexpr uint32_t RAW = 0, RAW2 = 128, P = TIGHT ? 256 : 0, OA = TIGHT ? 384 : 64, DS = TIGHT ? 320 : 256, OI = TIGHT ? 448 : 384;
-    static constexpr uint32_t RING = TIGHT ? 0 : 128, OI_RING = TIGHT ? 0 : 64;      // from a buffer to the next
+    // Tensor memory columns: two buffers of scores, P in the first half of its scores and P C in the second; the two parts of
+    // the state's change side by side; two buffers of A S.
+    static constexpr uint32_t RAW = 0, P = 0, OA = 64, RING = 128, DS = 256, OI = 384, OI_RING = 64;
 };
-static_assert(Map<SPLIT>::BYTES <= 232448 && Map<PAIRS>::BYTES <= 232448, "shared memory of a block");
+static_assert(Map<SPLIT>::BYTES <= 232448 && Map<PLAIN>::BYTES <= 232448, "shared memory of a block");
 
-struct LinMaps { CUtensorMap a, b, c, x; };
+struct LinMaps { CUtensorMap a, b, c; };
 
-__device__ __forceinline__ uint32_t bf2(float x, float y) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ float low(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
-__device__ __forceinline__ float finite_or_0(float x) { return fabsf(x) < INFINITY ? x : 0.f; }
-__device__ __forceinline__ float ex2(float x) {           // 2^x to 2^-22; 0 below 2^-126
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 // the larger magnitude of each half (and a sign of no meaning), NaN if either is
 __device__ __forceinline__ uint32_t most(uint32_t a, uint32_t w) {
     uint32_t r;
@@ -99,48 +82,8 @@ __device__ __forceinline__ uint32_t fma_bf(uint32_t a, uint32_t b, uint32_t c) {
     asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
     return r;
 }
-// two at a time
-struct F2 { float x, y; };
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-    F2 d;
-    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
-        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return d;
-}
-__device__ __forceinline__ F2 add2(F2 a, F2 b) {
-    F2 d;
-    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tadd.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
-        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return d;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-    F2 d;
-    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
-        "fma.rn.f32x2 z, x, y, z;\n\tmov.b64 {%0, %1}, z;\n\t}"
-        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return d;
-}
-// One lane of a converged warp.  (Products issued from a branch that the compiler knows to be one lane's take their operands
-// from the warp's registers, one in 33 to 64 cycles as the tensor cores take them; behind `lane == 0` inside the loop 70 to 150.)
-__device__ __forceinline__ bool elected() {
-    uint32_t e;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
-    return e != 0;
-}
-// Column sums of a 32 x 32 block, a row a lane: lane l gets that of column l.
-__device__ __forceinline__ float column_sums(float (&v)[32], int lane) {
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1)
-#pragma unroll
-        for (int k = 0; k < s; ++k) {
-            const float send = lane & s ? v[k] : v[k + s], keep = lane & s ? v[k + s] : v[k];
-            v[k] = keep + __shfl_xor_sync(0xffffffffu, send, s);
-        }
-    return v[0];
-}
-
 template <bool REV, Kind KIND>
-__global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_constant__ LinMaps maps, const LinWalk w, float* pairs) {
+__global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_constant__ LinMaps maps, const LinWalk w) {
     using M = Map<KIND>;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t base = smem_u32(smem);
@@ -157,11 +100,22 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
     const int blocks = (w.dc + NB - 1) / NB;
     const int64_t unit = blockIdx.x;
     const int blk = (int)(unit % blocks), h = (int)(unit / blocks % w.H);
-    const int n = lin::by_length(w.cu, w.n_seqs, w.T, (int)(unit / blocks / w.H));
+    const int64_t slot = unit / blocks / w.H;             // a sequence, or a segment of one
+    int n = 0, len, base_chunk = 0, count;
     int64_t first;
-    int len;
-    lin::sequence(w.cu, w.T, n, first, len);
-    const int chunks = __shfl_sync(0xffffffffu, (len + CK - 1) / CK, 0);
+    if (w.seg_chunks > 0) {
+        n = lin::slot_sequence(w.cu, w.N(), w.T, w.seg_chunks * CK, slot);
+        lin::sequence(w.cu, w.T, n, first, len);
+        const int64_t at = (slot - (first / (w.seg_chunks * CK) + n)) * w.seg_chunks;
+        if (at < 0 || at * CK >= len) return;             // (a slot of no segment)
+        base_chunk = (int)at;
+        count = min(w.seg_chunks, (len + CK - 1) / CK - base_chunk);
+    } else {
+        n = lin::by_length(w.cu, w.n_seqs, w.T, (int)slot);
+        lin::sequence(w.cu, w.T, n, first, len);
+        count = (len + CK - 1) / CK;
+    }
+    const int chunks = __shfl_sync(0xffffffffu, count, 0);
     const int c0 = blk * NB, cols = min(NB, w.dc - c0);
 
     if (warp == 17) {
@@ -173,20 +127,17 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
             mbar_init(&S.full[s], 2);                     // A and B, and the decays
             mbar_init(&S.full_c[s], 1);
             mbar_init(&S.empty[s], 1);
-            mbar_init(&S.empty_c[s], KIND == PLAIN ? 1 : 4);
-            mbar_init(&S.gate_empty[s], 12);
+            mbar_init(&S.empty_c[s], KIND == SPLIT ? 4 : 1);
+            mbar_init(&S.gate_empty[s], KIND == STATE ? 8 : 12);
             mbar_init(&S.raw_full[s], 1);
             mbar_init(&S.p_ready[s], 4);
             mbar_init(&S.o_full[s], 1);
             mbar_init(&S.o_free[s], 4);
         }
-        mbar_init(&S.raw_free, 4);
         mbar_init(&S.ds_full, 1);
         mbar_init(&S.ds_free, 8);
         mbar_init(&S.s_ready, 8);
         mbar_init(&S.vhat, 8);
-        mbar_init(&S.x_full, 1);
-        mbar_init(&S.x_empty, 1);
         fence_mbar_init();
     }
     tc_fence_before();
@@ -195,7 +146,7 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
     const uint32_t tmem = __shfl_sync(0xffffffffu, S.tmem, 0);
     bool ok = true;
     // chunk of a step, in the walk's direction, and how many of its tokens there are
-    auto chunk_of = [&](int c) { return REV ? chunks - 1 - c : c; };
+    auto chunk_of = [&](int c) { return base_chunk + (REV ? chunks - 1 - c : c); };
     auto rows_of = [&](int c) { return min(CK, len - chunk_of(c) * CK); };
     auto arrive = [&](uint64_t* bar) {
         __syncwarp();
@@ -209,14 +160,14 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
         return ok;
     };
 
-    if (warp < 8) {
+    if (warp < 8 && KIND == STATE) {
+        // (nothing to score)
+    } else if (warp < 8) {
         // ------------------------------------------------------------------------------------- scores and outputs
         const int I = warp & 3, row = 32 * I + lane;
         const uint32_t lanes = tmem + ((uint32_t)(32 * I) << 16);
         const int J0 = REV ? I : 0, J1 = REV ? 4 : I + 1;
         const bf16* xp = static_cast<const bf16*>(w.x.p) + (h / w.x.group) * w.x.head + c0;
-        float* pair_at = KIND == PAIRS ? pairs + ((int64_t)blk * 5 * w.H + h) * w.rows() + first : nullptr;
-        const int64_t pair_step = (int64_t)w.H * w.rows();
         for (int c = warp >> 2; c < chunks; c += 2) {
             const int L = rows_of(c), s = c & 1;
             const int64_t t0 = (int64_t)chunk_of(c) * CK;
@@ -231,7 +182,6 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
             const float u = w.s_intra * (REV ? ex2((rh - ih) + (rl - il)) : ex2((ih - rh) + (il - rl)));
             if (!wait(&S.raw_full[s], c >> 1, 2u)) break;
             tc_fence_after();
-            float sum = 0.f;                              // over the pairs of row i that are off the diagonal (PAIRS)
 #pragma unroll 1
             for (int J = J0; J < J1; ++J) {
                 uint32_t xr[2][16];
@@ -282,28 +232,8 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
                 uint32_t q[16];
 #pragma unroll
                 for (int j = 0; j < 32; j += 2) q[j >> 1] = bf2(x[j], x[j + 1]);
-                if (KIND == PAIRS && J == J0 && c > 0) {  // the product before, and its outputs, have read P
-                    if (!wait(&S.o_free[s ^ 1], (c - 1) >> 1, 4u)) break;
-                    tc_fence_after();
-                }
                 tmem_st16(p + 16 * J, q);
-                if (KIND == PAIRS) {
-                    uint32_t y[2][16];
-                    tmem_ld16(lanes + M::RAW2 + 32 * J, y[0]);
-                    tmem_ld16(lanes + M::RAW2 + 32 * J + 16, y[1]);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        const bool in = (J != I || j != lane) && row < L && x[j] != 0.f;
-                        x[j] = in ? x[j] * __uint_as_float(y[j >> 4][j & 15]) : 0.f;
-                        sum += x[j];
-                    }
-                    // a row of this walk is a key, a column a query behind it: the query's sum over the keys of this warp
-                    const float v = column_sums(x, lane);
-                    if (32 * J + lane < L) pair_at[I * pair_step + t0 + 32 * J + lane] = v;
-                }
             }
-            if (!ok) break;
             {   // the blocks on the other side of the diagonal
                 uint32_t zero[16];
 #pragma unroll
@@ -312,19 +242,17 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
             }
             tc_fence_before();
             arrive(&S.gate_empty[s]);
-            if (KIND == PAIRS) arrive(&S.raw_free);
             tmem_st_wait();
             tc_fence_before();
             arrive(&S.p_ready[s]);
             const bool in = row < L;
             const int64_t t = first + t0 + row;
-            if (KIND == PAIRS && in) pair_at[4 * pair_step + t0 + row] = -sum;
 
             // rows of the outputs go, and rows of x come, several lanes a row (a lane a row would touch 32 lines an access):
             // turned in shared memory of the warp's own, 32 rows of 64 bytes, or in the chunk's C tile, which has been read
             // when the outputs are there, of 128
             constexpr int Q = KIND == PLAIN ? 4 : 8, RPA = 32 / Q;                // pieces of a row, rows of an access
-            const uint32_t turn = KIND == PLAIN ? base + M::X + warp * 2048 : base + s * M::STAGE + M::C + I * 4096;
+            const uint32_t turn = KIND == PLAIN ? base + M::TURN + warp * 2048 : base + s * M::STAGE + M::C + I * 4096;
             const int rq = lane / Q, q = lane % Q;
             auto at_row = [&](int r, int i) { return turn + r * (16 * Q) + ((i ^ (KIND == PLAIN ? (r >> 1) & 3 : r & 7)) << 4); };
             uint4 xv[8];
@@ -431,10 +359,24 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
         const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
         float st[32];
         const int64_t state_at = ((int64_t)n * w.H + h) * w.da * w.dc + (int64_t)row * w.s_r + (int64_t)(c0 + k0) * w.s_c;
+        // [slot][h][block][row][column], of segments and of spans
+        float* seg_at = w.seg_states + ((slot * w.H + h) * blocks + blk) * (128 * NB) + row * NB + k0;
+        if (w.seg_chunks > 0 && KIND != STATE) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) st[i] = w.s_in && row < w.da && k0 + i < cols ? w.s_in[state_at + (int64_t)i * w.s_c] : 0.f;
+            for (int i = 0; i < 32; i += 4) {
+                const float4 v = *reinterpret_cast<const float4*>(seg_at + i);
+                st[i] = v.x;
+                st[i + 1] = v.y;
+                st[i + 2] = v.z;
+                st[i + 3] = v.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                st[i] = KIND != STATE && w.s_in && row < w.da && k0 + i < cols ? w.s_in[state_at + (int64_t)i * w.s_c] : 0.f;
+        }
+        float kept = 1.f;                                 // of what enters, behind the last token (STATE)
         const int64_t slot0 = first / kLinSpan + n;
-        // [span slot][h][block][row][column]
         auto span_at = [&](int ch) {
             return w.spans + ((((slot0 + ch / (kLinSpan / CK)) * w.H + h) * blocks + blk) * 128 + row) * (int64_t)NB + k0;
         };
@@ -458,7 +400,7 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
             fence_async_smem();
             arrive(&S.s_ready);
         };
-        if (chunks > 0) operand();
+        if (KIND != STATE && chunks > 0) operand();
         for (int c = 0; c < chunks; ++c) {
             const int s = c & 1, L = rows_of(c), ch = chunk_of(c);
             const uint32_t tile = base + s * M::STAGE;
@@ -472,6 +414,7 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
             const float gh = Gh(c)[row], gl = __bfloat162float(Gl(c)[row]), eh = Gh(c)[CK - 1], el = __bfloat162float(Gl(c)[CK - 1]);
             arrive(&S.gate_empty[s]);
             const float whole = exp2f(eh + el);
+            kept *= whole;
             const float f = w.s_state * (REV ? exp2f(gh + gl) : exp2f((eh - gh) + (el - gl)));
             if (starts_span && REV) {                     // or is multiplied with the one that did
                 const float4* src = reinterpret_cast<const float4*>(span_at(ch));
@@ -544,21 +487,18 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
                 uint32_t a[2][16], b[2][16];
                 tmem_ld16(lanes + M::DS + k0, a[0]);
                 tmem_ld16(lanes + M::DS + k0 + 16, a[1]);
-                if (KIND != PAIRS) {
-                    tmem_ld16(lanes + M::DS + 64 + k0, b[0]);
-                    tmem_ld16(lanes + M::DS + 64 + k0 + 16, b[1]);
-                }
+                tmem_ld16(lanes + M::DS + 64 + k0, b[0]);
+                tmem_ld16(lanes + M::DS + 64 + k0 + 16, b[1]);
                 tmem_ld_wait();
                 tc_fence_before();
                 arrive(&S.ds_free);
-                if (KIND != PAIRS)
 #pragma unroll
-                    for (int k = 0; k < 32; k += 2) {
-                        const F2 v = add2(F2{__uint_as_float(a[k >> 4][k & 15]), __uint_as_float(a[k >> 4][(k & 15) + 1])},
-                                          F2{__uint_as_float(b[k >> 4][k & 15]), __uint_as_float(b[k >> 4][(k & 15) + 1])});
-                        a[k >> 4][k & 15] = __float_as_uint(v.x);
-                        a[k >> 4][(k & 15) + 1] = __float_as_uint(v.y);
-                    }
+                for (int k = 0; k < 32; k += 2) {
+                    const F2 v = add2(F2{__uint_as_float(a[k >> 4][k & 15]), __uint_as_float(a[k >> 4][(k & 15) + 1])},
+                                      F2{__uint_as_float(b[k >> 4][k & 15]), __uint_as_float(b[k >> 4][(k & 15) + 1])});
+                    a[k >> 4][k & 15] = __float_as_uint(v.x);
+                    a[k >> 4][(k & 15) + 1] = __float_as_uint(v.y);
+                }
 #pragma unroll
                 for (int k = 0; k < 32; k += 2) {
                     const F2 v = fma2(F2{whole, whole}, F2{st[k], st[k + 1]},
@@ -567,9 +507,13 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
                     st[k + 1] = v.y;
                 }
             }
-            if (c + 1 < chunks) operand();
+            if (KIND != STATE && c + 1 < chunks) operand();
         }
-        if (ok && w.s_out && row < w.da)
+        if (KIND == STATE) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) *reinterpret_cast<float4*>(seg_at + i) = make_float4(st[i], st[i + 1], st[i + 2], st[i + 3]);
+            if (tid == 256 && blk == 0) w.seg_kept[slot * w.H + h] = kept;
+        } else if (ok && w.s_out && w.seg_chunks == 0 && row < w.da)
 #pragma unroll
             for (int i = 0; i < 32; ++i)
                 if (k0 + i < cols) w.s_out[state_at + (int64_t)i * w.s_c] = st[i];
@@ -579,18 +523,18 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
             prefetch_tmap(&maps.a);
             prefetch_tmap(&maps.b);
             prefetch_tmap(&maps.c);
-            const int ha = h / w.a.group, hb = h / w.b.group, hc = h / w.c.group, hx = KIND == PAIRS ? h / w.x.group : 0;
-            int issued = 0, issued_c = 0, issued_x = 0;
+            const int ha = h / w.a.group, hb = h / w.b.group, hc = h / w.c.group;
+            int issued = 0, issued_c = 0;
             uint64_t last = globaltimer_ns();
             // each stream is refilled as soon as what reads its buffer is done: polled, so that none waits behind another
-            while (issued < chunks || issued_c < chunks || (KIND == PAIRS && issued_x < chunks)) {
+            while (issued < chunks || issued_c < chunks) {
                 bool progress = false;
                 if (issued < chunks && (issued < 2 || mbar_test(&S.empty[issued & 1], ((issued >> 1) + 1) & 1))) {
                     const int s = issued & 1, t = (int)(first + (int64_t)chunk_of(issued) * CK);
                     uint8_t* tile = smem + s * M::STAGE;
-                    mbar_arrive_expect_tx(&S.full[s], 65536);
+                    mbar_arrive_expect_tx(&S.full[s], KIND == STATE ? 32768 : 65536);
                     for (int i = 0; i < 2; ++i) {
-                        tma_load_3d(tile + M::A + 16384 * i, &maps.a, &S.full[s], 64 * i, ha, t);
+                        if (KIND != STATE) tma_load_3d(tile + M::A + 16384 * i, &maps.a, &S.full[s], 64 * i, ha, t);
                         tma_load_3d(tile + M::B + 16384 * i, &maps.b, &S.full[s], 64 * i, hb, t);
                     }
                     ++issued;
@@ -603,12 +547,6 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
                     ++issued_c;
                     progress = true;
                 }
-                if (KIND == PAIRS && issued_x < chunks && (issued_x < 1 || mbar_test(&S.x_empty, (issued_x - 1) & 1))) {
-                    mbar_arrive_expect_tx(&S.x_full, 16384);
-                    tma_load_3d(smem + M::X, &maps.x, &S.x_full, c0, hx, (int)(first + (int64_t)chunk_of(issued_x) * CK));
-                    ++issued_x;
-                    progress = true;
-                }
                 if (progress) {
                     last = globaltimer_ns();
                 } else if (globaltimer_ns() - last > kWait) {
@@ -619,13 +557,12 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
             // what was asked for has landed before the block leaves
             for (int c = issued > 2 ? issued - 2 : 0; c < issued; ++c) mbar_wait(&S.full[c & 1], (c >> 1) & 1, kWait);
             for (int c = issued_c > 2 ? issued_c - 2 : 0; c < issued_c; ++c) mbar_wait(&S.full_c[c & 1], (c >> 1) & 1, kWait);
-            if (issued_x > 0) mbar_wait(&S.x_full, (issued_x - 1) & 1, kWait);
         }
     } else if (warp == 17) {
         // ------------------------------------------------------------------------------------------------ products
         if (chunks > 0) {
             constexpr uint32_t id_raw = idesc_f16(128, 128, true, false, false);   // A (K-major) x B (K-major)
-            constexpr uint32_t id_ds = idesc_f16(128, KIND == PAIRS ? 64 : 128, true, true, true);   // B^T (MN-major) x scaled C (MN-major)
+            constexpr uint32_t id_ds = idesc_f16(128, 128, true, true, true);      // B^T (MN-major) x scaled C (MN-major)
             constexpr uint32_t id_oi = idesc_f16(128, 64, true, false, true);      // A (K-major) x S (MN-major); P (TMEM) x C
             const bool wide = w.da > 64;                  // (the second half of the channels is all zeros else)
             const uint64_t v = sdesc(base + M::V, 16384, 1024), so = sdesc(base + M::S, 16384, 1024);
@@ -641,13 +578,12 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
                     if (wide)
 #pragma unroll
                         for (int k = 0; k < 4; ++k) mma_f16(d, a + 1024 + k * 2, b + 1024 + k * 2, id_raw, 1u);
-                    if (KIND != PAIRS) mma_commit(&S.raw_full[c & 1]);
+                    mma_commit(&S.raw_full[c & 1]);
                 }
                 __syncwarp();
             };
             auto inter = [&](int c) {                     // A S
-                const int freed = c - (KIND == PAIRS ? 1 : 2);
-                if (!wait(&S.s_ready, c, 1u << 14) || (freed >= 0 && !wait(&S.o_free[freed & 1], freed >> 1, 1u << 15))) return;
+                if (!wait(&S.s_ready, c, 1u << 14) || (c > 1 && !wait(&S.o_free[c & 1], (c >> 1) - 1, 1u << 15))) return;
                 tc_fence_after();
                 const uint64_t a = a0 + (c & 1) * NEXT;
                 const uint32_t d = tmem + M::OI + (c & 1) * M::OI_RING;
@@ -664,45 +600,26 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
                 }
                 __syncwarp();
             };
-            if (KIND != PAIRS && wait(&S.full[0], 0, 512u)) {
+            if (KIND != STATE && wait(&S.full[0], 0, 512u)) {
                 tc_fence_after();
                 scores(0);
             }
             for (int c = 0; c < chunks && ok; ++c) {
                 const int s = c & 1;
-                if (KIND == PAIRS) {
-                    if (!wait(&S.full[s], c >> 1, 512u) || (c > 0 && !wait(&S.raw_free, c - 1, 1u << 10))) break;
-                    tc_fence_after();
-                    scores(c);
-                }
-                inter(c);
+                if (KIND != STATE) inter(c);
                 if (!ok || !wait(&S.vhat, c, 1u << 11) || (c > 0 && !wait(&S.ds_free, c - 1, 1u << 12))) break;
                 tc_fence_after();
                 if (elected()) {
                     const uint64_t bt = bt0 + s * NEXT;
-                    if (KIND == PAIRS)
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) mma_f16(tmem + M::DS, bt + k * 128, v + 1024 + k * 128, id_ds, k > 0);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) mma_f16(tmem + M::DS, bt + k * 128, v + k * 128, id_ds, KIND == PAIRS || k > 0);
+                    for (int k = 0; k < 8; ++k) mma_f16(tmem + M::DS, bt + k * 128, v + k * 128, id_ds, k > 0);
+                    if (KIND == STATE) mma_commit(&S.empty_c[s]);
                     mma_commit(&S.ds_full);               // (of both products: the state's operand has been read too)
                     mma_commit(&S.empty[s]);
                 }
                 __syncwarp();
-                if (KIND == PAIRS) {                      // raw2 = X C^T (behind vhat: rows of C that are not finite are out)
-                    if (!wait(&S.x_full, c, 1u << 13)) break;
-                    tc_fence_after();
-                    if (elected()) {
-                        const uint64_t x = sdesc(base + M::X, 16, 1024), ct = sdesc(base + s * M::STAGE + M::C, 16, 1024);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) mma_f16(tmem + M::RAW2, x + k * 2, ct + k * 2, id_raw, k > 0);
-                        mma_commit(&S.raw_full[s]);
-                        mma_commit(&S.x_empty);
-                    }
-                    __syncwarp();
-                }
                 // the next scores and P C, whichever can go first; the scores go into the place of P and P C of the chunk before
-                bool next = KIND == PAIRS || c + 1 == chunks, product = false;
+                bool next = KIND == STATE || c + 1 == chunks, product = KIND == STATE;
                 for (uint64_t t0 = 0; !(next && product);) {
                     bool progress = false;
                     if (!next && __all_sync(0xffffffffu, mbar_test(&S.full[s ^ 1], ((c + 1) >> 1) & 1)) &&
@@ -738,7 +655,8 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
                 }
             }
             // every product has completed before the block leaves
-            if (ok) mbar_wait(&S.o_full[(chunks - 1) & 1], ((chunks - 1) >> 1) & 1, kWait);
+            if (ok && KIND == STATE) mbar_wait(&S.ds_full, (chunks - 1) & 1, kWait);
+            else if (ok) mbar_wait(&S.o_full[(chunks - 1) & 1], ((chunks - 1) >> 1) & 1, kWait);
         }
     } else if (warp == 18) {
         // ------------------------------------------------------------------------------------------------- decays
@@ -786,11 +704,6 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
     if (warp == 17) tmem_dealloc(tmem, 512);
 }
 
-// [tokens, heads, d] bf16 with strides: boxes of 64 channels x 1 head x 128 tokens
-bool token_map(CUtensorMap* m, const LinTok& t, int d, int heads, int64_t rows) {
-    return make_map_strided(m, t.p, rows, heads, d, t.tok, t.head, CK);
-}
-
 }  // namespace
 
 bool lin_tensor_fits(const LinWalk& w) {
@@ -799,26 +712,39 @@ bool lin_tensor_fits(const LinWalk& w) {
            (uintptr_t)w.out % 16 == 0 && device_is_sm100_family();
 }
 
-cudaError_t launch_lin_walk_tensor(const LinWalk& w, float* pairs, cudaStream_t s) {
-    const int64_t units = (int64_t)w.N() * w.H * lin_blocks(w.dc, true);
+// Chunks of a segment: 0 where there are blocks enough without (all sequences whole), else so many that the segments fill the
+// card, but no fewer than 8 (a segment's state has to come and go besides).
+int lin_segment_chunks(int64_t rows, int64_t N, int H, int dc) {
+    const int64_t units = N * H * lin_blocks(dc, true), chunks = (rows + CK - 1) / CK;
+    if (units >= 96 || chunks < 32) return 0;
+    const int64_t total = chunks * H * lin_blocks(dc, true);                     // chunks of all walks
+    const int64_t each = (total + 151) / 152;
+    return (int)(each < 8 ? 8 : each);
+}
+
+cudaError_t launch_lin_walk_tensor(const LinWalk& given, cudaStream_t s) {
+    LinWalk w = given;
+    const int blocks = lin_blocks(w.dc, true);
+    const int64_t slots = w.seg_chunks > 0 ? lin_slots(w.rows(), w.N(), w.seg_chunks * CK) : w.N();
+    const int64_t units = slots * w.H * blocks;
     if (units == 0) return cudaSuccess;
     LinMaps maps{};
-    const int64_t rows = w.rows() > 0 ? w.rows() : 1;
-    if (w.rows() > 0) {
-        if (!token_map(&maps.a, w.a, w.da, w.H / w.a.group, rows) || !token_map(&maps.b, w.b, w.da, w.H / w.b.group, rows) ||
-            !token_map(&maps.c, w.c, w.dc, w.H / w.c.group, rows))
-            return cudaErrorInvalidValue;
-        if (pairs && !token_map(&maps.x, w.x, w.dc, w.H / w.x.group, rows)) return cudaErrorInvalidValue;
-    }
+    if (w.rows() > 0 && (!token_map(&maps.a, w.a, w.da, w.H / w.a.group, w.rows()) || !token_map(&maps.b, w.b, w.da, w.H / w.b.group, w.rows()) ||
+                         !token_map(&maps.c, w.c, w.dc, w.H / w.c.group, w.rows())))
+        return cudaErrorInvalidValue;
     auto start = [&](auto kernel, uint32_t smem) -> cudaError_t {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
-        kernel<<<(unsigned)units, THREADS, smem, s>>>(maps, w, pairs);
+        kernel<<<(unsigned)units, THREADS, smem, s>>>(maps, w);
         return cudaGetLastError();
     };
-    if (pairs) return start(lin_chunk_kernel<true, PAIRS>, Map<PAIRS>::BYTES);
+    if (w.seg_chunks > 0) {
+        cudaError_t e = w.rev ? start(lin_chunk_kernel<true, STATE>, Map<STATE>::BYTES) : start(lin_chunk_kernel<false, STATE>, Map<STATE>::BYTES);
+        if (e == cudaSuccess) e = launch_lin_segments(w, s);
+        if (e != cudaSuccess) return e;
+    }
     if (w.dots) return w.rev ? start(lin_chunk_kernel<true, SPLIT>, Map<SPLIT>::BYTES) : start(lin_chunk_kernel<false, SPLIT>, Map<SPLIT>::BYTES);
-    return start(lin_chunk_kernel<false, PLAIN>, Map<PLAIN>::BYTES);
+    return w.rev ? start(lin_chunk_kernel<true, PLAIN>, Map<PLAIN>::BYTES) : start(lin_chunk_kernel<false, PLAIN>, Map<PLAIN>::BYTES);
 }
 
 cudaError_t lin_read_and_clear_status(unsigned* value, bool clear) {

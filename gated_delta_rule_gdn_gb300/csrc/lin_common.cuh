@@ -19,6 +19,19 @@ __device__ __forceinline__ void sequence(const int32_t* cu, int T, int n, int64_
     }
 }
 
+// The sequence that a slot of spans or segments of `size` tokens is one of (those of sequence n begin at first / size + n): the
+// last that begins at or before it.
+__device__ __forceinline__ int slot_sequence(const int32_t* cu, int N, int T, int size, int64_t slot) {
+    int n = 0, top = (int)min(slot, (int64_t)N - 1), len;
+    int64_t first;
+    while (n < top) {
+        const int mid = (n + top + 1) >> 1;
+        sequence(cu, T, mid, first, len);
+        if (first / size + mid <= slot) n = mid; else top = mid - 1;
+    }
+    return n;
+}
+
 // Rank in the launch -> sequence: packed sequences longest first, so that the longest walks do not start last (all lanes of a
 // warp call it; up to 32 sequences, as many as the lanes).
 __device__ __forceinline__ int by_length(const int32_t* cu, int n_seqs, int T, int rank) {

@@ -151,14 +151,9 @@ __global__ void __launch_bounds__(kLinSpan) lin_dg_kernel(const LinDg a) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int h = blockIdx.x % a.H;
     const int64_t slot = blockIdx.x / a.H;
-    // the sequence whose slots the slot is one of: the last that begins at or before it
-    int n = 0, top = (int)min(slot, (int64_t)a.N() - 1), len;
+    const int n = lin::slot_sequence(a.cu, a.N(), a.T, kLinSpan, slot);
     int64_t first;
-    while (n < top) {
-        const int mid = (n + top + 1) >> 1;
-        lin::sequence(a.cu, a.T, mid, first, len);
-        if (first / kLinSpan + mid <= slot) n = mid; else top = mid - 1;
-    }
+    int len;
     lin::sequence(a.cu, a.T, n, first, len);
     const int64_t at = (slot - (first / kLinSpan + n)) * kLinSpan;
     if (at < 0 || at >= len) {
@@ -173,16 +168,7 @@ __global__ void __launch_bounds__(kLinSpan) lin_dg_kernel(const LinDg a) {
             plus += a.plus[t + k * step];
             minus += a.minus[t + k * step];
         }
-        if (a.pairs_minus) {
-            for (int k = 0; k < a.pair_blocks; ++k) pairs += a.pairs[t + k * step] - a.pairs_minus[t + k * step];
-        } else {                                       // (sums over keys of a query come by 32 keys of the chunk)
-            const int own = tid % kLinChunk / 32;
-            for (int k = 0; k < a.pair_blocks; ++k) {
-                const float* p = a.pairs + t + 5 * k * step;
-                pairs += p[4 * step];
-                for (int i = 0; i <= own; ++i) pairs += p[i * step];
-            }
-        }
+        for (int k = 0; k < a.pair_blocks; ++k) pairs += a.pairs[t + k * step] - (a.pairs_minus ? a.pairs_minus[t + k * step] : 0.f);
     }
     float behind = plus, behind_pairs = pairs, before = minus;       // from this token on; up to it
     for (int m = 1; m < 32; m <<= 1) {
@@ -233,15 +219,65 @@ __global__ void lin_dg_sum_kernel(const float* part, float* dg, int64_t slots, i
     if (lane == 0) dg[h] = (float)s;
 }
 
-template <typename T>
-__global__ void lin_group_sum_kernel(const float* part, T* out, int64_t n, int group, int d) {
-    for (int64_t e = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; e < n; e += (int64_t)gridDim.x * blockDim.x) {
-        const int64_t head = e / d;
-        const float* p = part + head * group * d + e % d;
-        float s = 0.f;
-        for (int i = 0; i < group; ++i) s += p[(int64_t)i * d];
-        mix::st(out + e, s);
+// V elements a thread; d is a multiple of V.
+template <typename T, int V>
+__global__ void __launch_bounds__(256) lin_group_sum_kernel(const float* part, T* out, int64_t heads, int group, int d) {
+    const int per = d / V;
+    for (int64_t head = (int64_t)blockIdx.x * blockDim.y + threadIdx.y; head < heads; head += (int64_t)gridDim.x * blockDim.y)
+        for (int i = threadIdx.x; i < per; i += blockDim.x) {
+            const float* p = part + head * group * d + i * V;
+            mix::Vec<float, V> s, x;
+            s.load(p);
+            for (int k = 1; k < group; ++k) {
+                x.load(p + (int64_t)k * d);
+#pragma unroll
+                for (int u = 0; u < V; ++u) s.e[u] += x.e[u];
+            }
+            mix::Vec<T, V> y;
+#pragma unroll
+            for (int u = 0; u < V; ++u) y.set(u, s.e[u]);
+            y.store(out + head * d + i * V);
+        }
+}
+
+// The states entering the segments of a sequence: four elements of a block's [128][kLinCols] a thread, segment after segment in
+// the walk's direction.
+__global__ void __launch_bounds__(256) lin_segments_kernel(const LinWalk w) {
+    constexpr int PER = 128 * kLinCols / 1024;             // blocks of threads for a state
+    const int blocks = (w.dc + kLinCols - 1) / kLinCols;
+    const int part = blockIdx.x % PER;
+    const int64_t unit = blockIdx.x / PER;
+    const int blk = (int)(unit % blocks), h = (int)(unit / blocks % w.H), n = (int)(unit / blocks / w.H);
+    int64_t first;
+    int len;
+    lin::sequence(w.cu, w.T, n, first, len);
+    const int size = w.seg_chunks * kLinChunk, segs = (len + size - 1) / size;
+    const int64_t slot0 = first / size + n;
+    const int e = part * 1024 + threadIdx.x * 4, row = e / kLinCols, col = e % kLinCols, c = blk * kLinCols + col;
+    const int64_t at = ((int64_t)n * w.H + h) * w.da * w.dc + (int64_t)row * w.s_r;
+    float s[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[i] = w.s_in && row < w.da && c + i < w.dc ? w.s_in[at + (int64_t)(c + i) * w.s_c] : 0.f;
+    const int64_t step = (int64_t)w.H * blocks * (128 * kLinCols);
+    float* p = w.seg_states + ((slot0 * w.H + h) * blocks + blk) * (128 * kLinCols) + e;
+    if (w.rev) p += (segs - 1) * step;
+    float4 x = segs > 0 ? *reinterpret_cast<const float4*>(p) : make_float4(0, 0, 0, 0);
+    for (int k = 0; k < segs; ++k) {
+        float* next = p + (w.rev ? -step : step);
+        const float4 y = k + 1 < segs ? *reinterpret_cast<const float4*>(next) : make_float4(0, 0, 0, 0);
+        const float kept = w.seg_kept[(slot0 + (w.rev ? segs - 1 - k : k)) * w.H + h];
+        *reinterpret_cast<float4*>(p) = make_float4(s[0], s[1], s[2], s[3]);
+        s[0] = fmaf(kept, s[0], x.x);
+        s[1] = fmaf(kept, s[1], x.y);
+        s[2] = fmaf(kept, s[2], x.z);
+        s[3] = fmaf(kept, s[3], x.w);
+        x = y;
+        p = next;
     }
+    if (w.s_out)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (row < w.da && c + i < w.dc) w.s_out[at + (int64_t)(c + i) * w.s_c] = s[i];
 }
 
 }  // namespace
@@ -267,11 +303,24 @@ cudaError_t launch_lin_dg(const LinDg& a, cudaStream_t s) {
 }
 
 cudaError_t launch_lin_group_sum(const float* part, void* out, int bf16_out, int64_t rows, int Hk, int group, int d, cudaStream_t s) {
-    const int64_t n = rows * Hk * d;
-    if (n == 0) return cudaSuccess;
-    const unsigned blocks = (unsigned)((n + 255) / 256 < 65536 ? (n + 255) / 256 : 65536);
-    if (bf16_out) lin_group_sum_kernel<<<blocks, 256, 0, s>>>(part, static_cast<bf16*>(out), n, group, d);
-    else lin_group_sum_kernel<<<blocks, 256, 0, s>>>(part, static_cast<float*>(out), n, group, d);
+    const int64_t heads = rows * Hk;
+    if (heads == 0) return cudaSuccess;
+    auto start = [&](auto kernel, auto* to, int V) {
+        int x = 8;
+        while (x < 32 && x * V < d) x *= 2;
+        const int y = 256 / x;
+        const int64_t blocks = (heads + y - 1) / y;
+        kernel<<<(unsigned)(blocks < 152 * 64 ? blocks : 152 * 64), dim3(x, y), 0, s>>>(part, to, heads, group, d);
+        return cudaGetLastError();
+    };
+    const bool vec = d % 4 == 0 && (uintptr_t)part % 16 == 0 && (uintptr_t)out % 16 == 0;
+    if (bf16_out) return vec ? start(lin_group_sum_kernel<bf16, 4>, static_cast<bf16*>(out), 4) : start(lin_group_sum_kernel<bf16, 1>, static_cast<bf16*>(out), 1);
+    return vec ? start(lin_group_sum_kernel<float, 4>, static_cast<float*>(out), 4) : start(lin_group_sum_kernel<float, 1>, static_cast<float*>(out), 1);
+}
+
+cudaError_t launch_lin_segments(const LinWalk& w, cudaStream_t s) {
+    const int64_t blocks = (int64_t)w.N() * w.H * lin_blocks(w.dc, true) * (128 * kLinCols / 1024);
+    lin_segments_kernel<<<(unsigned)blocks, 256, 0, s>>>(w);
     return cudaGetLastError();
 }
 

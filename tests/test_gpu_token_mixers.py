@@ -164,6 +164,8 @@ TENSOR = [
     (1, 900, 1, 2, 32, 128, [0, 128, 256, 900], "resets", "dense"),
     (1, 2200, 1, 1, 128, 128, [0, 1024, 1024, 1030, 2200], "head", "dense"),         # past a span of 1024 tokens
     (2, 1153, 1, 1, 64, 64, None, "head", "dense"),
+    (1, 4500, 1, 1, 64, 72, None, "head", "dense"),                                  # few walks and long ones: in segments
+    (1, 4400, 1, 2, 24, 64, [0, 1, 1100, 1100, 3300, 4400], "token", "rows"),
 ]
 
 
