@@ -45,7 +45,7 @@ struct LinWalk {
     // the span's first chunk.
     float* spans;
     float* anchors;
-    // Segments of a walk on the tensor cores (0: none), [segment slot][h][block][128][kLinCols] states, first of each segment from
+    // Segments of a walk on the tensor cores (0: none), [segment slot][h][block] states of 128 x kLinCols, first of each segment from
     // nothing, then entering it, and [segment slot][h] what each keeps of the state entering it.
     int seg_chunks;
     float *seg_states, *seg_kept;

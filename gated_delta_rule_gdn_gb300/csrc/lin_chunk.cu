@@ -359,12 +359,13 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
         const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
         float st[32];
         const int64_t state_at = ((int64_t)n * w.H + h) * w.da * w.dc + (int64_t)row * w.s_r + (int64_t)(c0 + k0) * w.s_c;
-        // [slot][h][block][row][column], of segments and of spans
-        float* seg_at = w.seg_states + ((slot * w.H + h) * blocks + blk) * (128 * NB) + row * NB + k0;
+        // [slot][h][block][columns by four][row][4], of segments and of spans: the rows of a warp side by side
+        auto quad = [&](float* state, int i) { return reinterpret_cast<float4*>(state + (int64_t)((k0 + i) / 4 * 128 + row) * 4); };
+        float* seg_at = w.seg_states + ((slot * w.H + h) * blocks + blk) * (128 * NB);
         if (w.seg_chunks > 0 && KIND != STATE) {
 #pragma unroll
             for (int i = 0; i < 32; i += 4) {
-                const float4 v = *reinterpret_cast<const float4*>(seg_at + i);
+                const float4 v = *quad(seg_at, i);
                 st[i] = v.x;
                 st[i + 1] = v.y;
                 st[i + 2] = v.z;
@@ -378,7 +379,7 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
         float kept = 1.f;                                 // of what enters, behind the last token (STATE)
         const int64_t slot0 = first / kLinSpan + n;
         auto span_at = [&](int ch) {
-            return w.spans + ((((slot0 + ch / (kLinSpan / CK)) * w.H + h) * blocks + blk) * 128 + row) * (int64_t)NB + k0;
+            return w.spans + (((slot0 + ch / (kLinSpan / CK)) * w.H + h) * blocks + blk) * (int64_t)(128 * NB);
         };
         auto operand = [&] {                              // S as an operand: rows of 64 columns, 128-byte swizzle
 #pragma unroll
@@ -406,9 +407,9 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
             const uint32_t tile = base + s * M::STAGE;
             const bool starts_span = KIND == SPLIT && w.spans && ch % (kLinSpan / CK) == 0;
             if (starts_span && !REV) {                    // a span's first chunk: the state goes out
-                float4* dst = reinterpret_cast<float4*>(span_at(ch));
+                float* dst = span_at(ch);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) dst[i] = make_float4(st[4 * i], st[4 * i + 1], st[4 * i + 2], st[4 * i + 3]);
+                for (int i = 0; i < 8; ++i) *quad(dst, 4 * i) = make_float4(st[4 * i], st[4 * i + 1], st[4 * i + 2], st[4 * i + 3]);
             }
             if (!wait(&S.full[s], c >> 1, 32u)) break;
             const float gh = Gh(c)[row], gl = __bfloat162float(Gl(c)[row]), eh = Gh(c)[CK - 1], el = __bfloat162float(Gl(c)[CK - 1]);
@@ -417,11 +418,11 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
             kept *= whole;
             const float f = w.s_state * (REV ? exp2f(gh + gl) : exp2f((eh - gh) + (el - gl)));
             if (starts_span && REV) {                     // or is multiplied with the one that did
-                const float4* src = reinterpret_cast<const float4*>(span_at(ch));
+                float* src = span_at(ch);
                 float sum = 0.f;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float4 x = src[i];
+                    const float4 x = *quad(src, 4 * i);
                     sum = fmaf(st[4 * i], x.x, sum);
                     sum = fmaf(st[4 * i + 1], x.y, sum);
                     sum = fmaf(st[4 * i + 2], x.z, sum);
@@ -511,7 +512,7 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
         }
         if (KIND == STATE) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) *reinterpret_cast<float4*>(seg_at + i) = make_float4(st[i], st[i + 1], st[i + 2], st[i + 3]);
+            for (int i = 0; i < 32; i += 4) *quad(seg_at, i) = make_float4(st[i], st[i + 1], st[i + 2], st[i + 3]);
             if (tid == 256 && blk == 0) w.seg_kept[slot * w.H + h] = kept;
         } else if (ok && w.s_out && w.seg_chunks == 0 && row < w.da)
 #pragma unroll

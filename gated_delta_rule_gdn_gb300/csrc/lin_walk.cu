@@ -240,8 +240,8 @@ __global__ void __launch_bounds__(256) lin_group_sum_kernel(const float* part, T
         }
 }
 
-// The states entering the segments of a sequence: four elements of a block's [128][kLinCols] a thread, segment after segment in
-// the walk's direction.
+// The states entering the segments of a sequence: four columns of a row of a block's state a thread, segment after segment in the
+// walk's direction.
 __global__ void __launch_bounds__(256) lin_segments_kernel(const LinWalk w) {
     constexpr int PER = 128 * kLinCols / 1024;             // blocks of threads for a state
     const int blocks = (w.dc + kLinCols - 1) / kLinCols;
@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(256) lin_segments_kernel(const LinWalk w) {
     lin::sequence(w.cu, w.T, n, first, len);
     const int size = w.seg_chunks * kLinChunk, segs = (len + size - 1) / size;
     const int64_t slot0 = first / size + n;
-    const int e = part * 1024 + threadIdx.x * 4, row = e / kLinCols, col = e % kLinCols, c = blk * kLinCols + col;
+    const int e = part * 1024 + threadIdx.x * 4, row = e / 4 % 128, c = blk * kLinCols + e / 512 * 4;
     const int64_t at = ((int64_t)n * w.H + h) * w.da * w.dc + (int64_t)row * w.s_r;
     float s[4];
 #pragma unroll
