@@ -51,6 +51,11 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ float ex2(float x) {                    // 2^x to 2^-22; 0 below 2^-126
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 // two floats as bf16 pairs: the values rounded, and what the rounding left
 __device__ __forceinline__ void halves(float x, float y, uint32_t& hi, uint32_t& lo) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
@@ -89,19 +94,19 @@ struct Ring {
 };
 
 template <int D, int STAGES>
-__global__ void __launch_bounds__(THREADS) paged_attn_mma_kernel(const PagedAttnArgs a) {
+__global__ void __launch_bounds__(THREADS, D == 64 ? 4 : D == 128 ? 3 : 1) paged_attn_mma_kernel(const PagedAttnArgs a) {
     using R = Ring<D, STAGES>;
     extern __shared__ __align__(16) char ring[];
     __shared__ float top_s[WARPS][16], sum_s[WARPS][16];
     const PagedCache& c = a.c;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int group = a.Hq / c.Hk, tiles = (group + 15) / 16;
-    int64_t unit = blockIdx.x;
-    const int split = (int)(unit % a.splits);
-    unit /= a.splits;
+    int64_t unit = blockIdx.x;                         // (key heads first: their rows lie side by side)
+    const int hk = (int)(unit % c.Hk);
+    unit /= c.Hk;
     const int tile = (int)(unit % tiles);
     unit /= tiles;
-    const int hk = (int)(unit % c.Hk), n = (int)(unit / c.Hk);
+    const int split = (int)(unit % a.splits), n = (int)(unit / a.splits);
     const int len = sequence_tokens(c, n), per = part_tokens(len, a.splits);
     const int t0 = split * per, t1 = min(len, t0 + per), parts = (len + per - 1) / per;
     mix::let_next();
@@ -124,26 +129,34 @@ __global__ void __launch_bounds__(THREADS) paged_attn_mma_kernel(const PagedAttn
     const uint32_t base = smem_at(ring) + warp * R::WARP;
     const bf16* kp = static_cast<const bf16*>(c.k.p) + hk * c.k.head;
     const bf16* vp = static_cast<const bf16*>(c.v.p) + hk * c.v.head;
-    // lane l (and l + 16): the page of token l of a run, -1 where there is none
+    // lane l (and l + 16): where token l of a run lies, in 16 bytes from the first key (value), and whether it does
+    struct Where { uint32_t k, v; bool in; };
     auto look_up = [&](int run) {
         const int t = t0 + (warp + run * WARPS) * RUN + (lane & 15);
-        int page = -1;
-        if (run < mine && t < t1) page = c.table[n * c.table_ld + t / c.page_size];
-        return page >= 0 && page < c.n_pages ? page : -1;
+        Where at{0, 0, false};
+        if (run < mine && t < t1) {
+            const int page = c.table[n * c.table_ld + t / c.page_size], slot = t % c.page_size;
+            at.in = page >= 0 && page < c.n_pages;
+            if (at.in) {
+                at.k = (uint32_t)((page * c.k.page + slot * c.k.slot) / 8);
+                at.v = (uint32_t)((page * c.v.page + slot * c.v.slot) / 8);
+            }
+        }
+        return at;
     };
-    auto fill = [&](int run, int page) {
+    auto fill = [&](int run, const Where& at, unsigned in) {
         if (run < mine) {
-            const int slot = (t0 + (warp + run * WARPS) * RUN + (lane & 15)) % c.page_size;
-            const uint32_t dst = base + (run % STAGES) * R::STAGE;
             constexpr int PER = D / 8, EACH = RUN * PER / 32;      // 16-byte pieces of a row; those of a lane
+            const int col = lane % PER;
+            const uint32_t dst = base + (run % STAGES) * R::STAGE + lane / PER * R::ROW + col * 16;
+            const bool wide = col * 8 < c.d;
 #pragma unroll
             for (int u = 0; u < EACH; ++u) {
-                const int e = u * 32 + lane, r = e / PER, at = e % PER;
-                const int64_t pg = __shfl_sync(0xffffffffu, page, r);
-                const int sl = __shfl_sync(0xffffffffu, slot, r);
-                const bool in = pg >= 0 && at * 8 < c.d;
-                copy16(dst + r * R::ROW + at * 16, in ? kp + pg * c.k.page + sl * c.k.slot + at * 8 : kp, in);
-                copy16(dst + (RUN + r) * R::ROW + at * 16, in ? vp + pg * c.v.page + sl * c.v.slot + at * 8 : vp, in);
+                const int r = u * (32 / PER) + lane / PER;
+                const uint32_t ko = __shfl_sync(0xffffffffu, at.k, r), vo = __shfl_sync(0xffffffffu, at.v, r);
+                const bool have = wide && (in >> r) & 1;
+                copy16(dst + u * (32 / PER) * R::ROW, kp + (have ? (uint64_t)ko * 8 + col * 8 : 0), have);
+                copy16(dst + (RUN + u * (32 / PER)) * R::ROW, vp + (have ? (uint64_t)vo * 8 + col * 8 : 0), have);
             }
         }
         mix::copies_close();
@@ -156,13 +169,13 @@ __global__ void __launch_bounds__(THREADS) paged_attn_mma_kernel(const PagedAttn
         for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
     // which tokens of a run are there: a bit each, in the order of the runs (STAGES runs are on their way)
     unsigned there[STAGES];
-    int page = look_up(0);
+    Where at = look_up(0);
 #pragma unroll
     for (int s = 0; s < STAGES - 1; ++s) {
-        const int ahead = look_up(s + 1);
-        there[s] = __ballot_sync(0xffffffffu, page >= 0) & 0xFFFFu;
-        fill(s, page);
-        page = ahead;
+        const Where ahead = look_up(s + 1);
+        there[s] = __ballot_sync(0xffffffffu, at.in) & 0xFFFFu;
+        fill(s, at, there[s]);
+        at = ahead;
     }
     const float scale = a.scale * LOG2E;
     for (int run0 = 0; run0 < mine; run0 += STAGES)
@@ -174,10 +187,10 @@ __global__ void __launch_bounds__(THREADS) paged_attn_mma_kernel(const PagedAttn
             __syncwarp();                                          // (every lane's copies have landed, and the stage filled next is read)
             constexpr int LAST = STAGES - 1;
             {
-                const int ahead = look_up(run + STAGES);
-                there[(st + LAST) % STAGES] = __ballot_sync(0xffffffffu, page >= 0) & 0xFFFFu;
-                fill(run + LAST, page);
-                page = ahead;
+                const Where ahead = look_up(run + STAGES);
+                there[(st + LAST) % STAGES] = __ballot_sync(0xffffffffu, at.in) & 0xFFFFu;
+                fill(run + LAST, at, there[(st + LAST) % STAGES]);
+                at = ahead;
             }
             const uint32_t ks = base + st * R::STAGE, vs = ks + RUN * R::ROW;
             float x[2][4] = {};                                    // heads lane / 4 and + 8, tokens 8 i + lane % 4 * 2 and + 1
@@ -194,7 +207,8 @@ __global__ void __launch_bounds__(THREADS) paged_attn_mma_kernel(const PagedAttn
             for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    x[i][j] = (live >> (8 * i + lane % 4 * 2 + (j & 1))) & 1 ? x[i][j] * scale : -INFINITY;
+                    x[i][j] *= scale;
+                    if (live != 0xFFFFu && !((live >> (8 * i + lane % 4 * 2 + (j & 1))) & 1)) x[i][j] = -INFINITY;
                     most[j >> 1] = fmaxf(most[j >> 1], x[i][j]);
                 }
             bool more = false;
@@ -223,7 +237,7 @@ __global__ void __launch_bounds__(THREADS) paged_attn_mma_kernel(const PagedAttn
             for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    x[i][j] = exp2f(x[i][j] - zero[j >> 1]);
+                    x[i][j] = ex2(x[i][j] - zero[j >> 1]);
                     sum[j >> 1] += x[i][j];
                 }
             uint32_t hi[4], lo[4];
@@ -293,12 +307,12 @@ __global__ void __launch_bounds__(THREADS) paged_attn_generic_kernel(const Paged
     const PagedCache& c = a.c;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int group = a.Hq / c.Hk, tiles = (group + HEADS - 1) / HEADS;
-    int64_t unit = blockIdx.x;
-    const int split = (int)(unit % a.splits);
-    unit /= a.splits;
+    int64_t unit = blockIdx.x;                         // (key heads first: their rows lie side by side)
+    const int hk = (int)(unit % c.Hk);
+    unit /= c.Hk;
     const int tile = (int)(unit % tiles);
     unit /= tiles;
-    const int hk = (int)(unit % c.Hk), n = (int)(unit / c.Hk);
+    const int split = (int)(unit % a.splits), n = (int)(unit / a.splits);
     const int len = sequence_tokens(c, n), per = part_tokens(len, a.splits);
     const int t0 = split * per, t1 = min(len, t0 + per), parts = (len + per - 1) / per;
     mix::let_next();
@@ -392,34 +406,50 @@ __global__ void __launch_bounds__(THREADS) paged_attn_generic_kernel(const Paged
     }
 }
 
-// Joins the parts of each (sequence, query head) that has more than one: a warp each.
+// Joins the parts of each (sequence, query head) that has more than one: a block each, its warps take parts in turn.
 template <typename T>
 __global__ void __launch_bounds__(THREADS) paged_attn_join_kernel(const PagedAttnArgs a) {
+    __shared__ float tops_s[1024], sums_s[1024], joint[WARPS][256], total_s[WARPS];
     const PagedCache& c = a.c;
-    const int lane = threadIdx.x & 31;
-    const int64_t row = (int64_t)blockIdx.x * WARPS + (threadIdx.x >> 5);
-    const bool have = row < (int64_t)c.N * a.Hq;
-    const int n = have ? (int)(row / a.Hq) : 0, hq = (int)(row % a.Hq);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int n = blockIdx.x / a.Hq, hq = blockIdx.x % a.Hq;
     const int len = sequence_tokens(c, n), per = part_tokens(len, a.splits), parts = (len + per - 1) / per;
     mix::wait_behind();
-    if (!have || parts <= 1) return;
+    if (parts <= 1) return;
     const float* sums = Part{a, n, hq, 0, parts}.sums();
     const float* tops = Part{a, n, hq, 0, parts}.tops();
-    float top = -INFINITY, total = 0.f, o[8] = {};
-    for (int s = lane; s < parts; s += 32) top = fmaxf(top, tops[2 * s]);
+    float top = -INFINITY;
+    for (int s = tid; s < parts; s += THREADS) {
+        const float2 t = *reinterpret_cast<const float2*>(tops + 2 * s);
+        tops_s[s] = t.x;
+        sums_s[s] = t.y;
+    }
+    __syncthreads();
+    for (int s = lane; s < parts; s += 32) top = fmaxf(top, tops_s[s]);
     for (int m = 16; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
-    for (int s = 0; s < parts; ++s) {
-        const float f = tops[2 * s] == top ? 1.f : exp2f(tops[2 * s] - top);
-        total = fmaf(f, tops[2 * s + 1], total);
+    float total = 0.f, o[8] = {};
+#pragma unroll 2
+    for (int s = warp; s < parts; s += WARPS) {
+        const float f = tops_s[s] == top ? 1.f : exp2f(tops_s[s] - top);
+        total = fmaf(f, sums_s[s], total);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             if (lane + 32 * i < c.d) o[i] = fmaf(f, sums[(int64_t)s * c.d + lane + 32 * i], o[i]);
     }
-    const Part part{a, n, hq, 0, 1};
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (lane + 32 * i < c.d) part.put<T>(lane + 32 * i, o[i], total);
-    if (lane == 0) part.close(top, total);
+    for (int i = 0; i < 8; ++i) joint[warp][lane + 32 * i] = o[i];
+    if (lane == 0) total_s[warp] = total;
+    __syncthreads();
+    total = 0.f;
+    for (int w = 0; w < WARPS; ++w) total += total_s[w];
+    const Part part{a, n, hq, 0, 1};
+    for (int i = tid; i < c.d; i += THREADS) {
+        float s = 0.f;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) s += joint[w][i];
+        part.put<T>(i, s, total);
+    }
+    if (tid == 0) part.close(top, total);
 }
 
 template <int D, int STAGES>
@@ -434,7 +464,9 @@ cudaError_t start_mma(const PagedAttnArgs& a, unsigned blocks, cudaStream_t s) {
 
 bool vector_rows(const PagedAttnArgs& a) {
     auto fits = [](const PagedSide& x) { return (uintptr_t)x.p % 16 == 0 && x.page % 8 == 0 && x.slot % 8 == 0 && x.head % 8 == 0; };
-    return a.c.bf16 && a.c.d % 8 == 0 && fits(a.c.k) && fits(a.c.v) && (uintptr_t)a.q % 4 == 0 && a.q_tok % 2 == 0 && a.q_head % 2 == 0;
+    // (a row's place is counted in 16 bytes and 32 bits)
+    auto near = [&](const PagedSide& x) { return (a.c.n_pages * x.page + a.c.page_size * x.slot) / 8 < (int64_t(1) << 32); };
+    return a.c.bf16 && near(a.c.k) && near(a.c.v) && a.c.d % 8 == 0 && fits(a.c.k) && fits(a.c.v) && (uintptr_t)a.q % 4 == 0 && a.q_tok % 2 == 0 && a.q_head % 2 == 0;
 }
 
 }  // namespace
@@ -461,8 +493,8 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t s) {
     cudaError_t e;
     if (vector_rows(a)) {
         const unsigned blocks = (unsigned)((int64_t)a.c.N * a.c.Hk * ((group + 15) / 16) * a.splits);
-        if (a.c.d <= 64) e = start_mma<64, 4>(a, blocks, s);
-        else if (a.c.d <= 128) e = start_mma<128, 3>(a, blocks, s);
+        if (a.c.d <= 64) e = start_mma<64, 3>(a, blocks, s);
+        else if (a.c.d <= 128) e = start_mma<128, 2>(a, blocks, s);
         else e = start_mma<256, 3>(a, blocks, s);
     } else {
         const unsigned blocks = (unsigned)((int64_t)a.c.N * a.c.Hk * ((group + HEADS - 1) / HEADS) * a.splits);
@@ -471,7 +503,7 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t s) {
         e = cudaGetLastError();
     }
     if (e != cudaSuccess || a.splits <= 1) return e;
-    const unsigned blocks = (unsigned)(((int64_t)a.c.N * a.Hq + WARPS - 1) / WARPS);
+    const unsigned blocks = (unsigned)((int64_t)a.c.N * a.Hq);
     return a.c.bf16 ? mix::launch_behind(paged_attn_join_kernel<bf16>, blocks, THREADS, 0, true, s, a)
                     : mix::launch_behind(paged_attn_join_kernel<float>, blocks, THREADS, 0, true, s, a);
 }
