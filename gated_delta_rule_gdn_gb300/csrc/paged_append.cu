@@ -1,9 +1,11 @@
 // Appending keys and values to a paged cache, with the position rotation of keys (and queries) on the way.
 //
-// One block takes one new token: all its key, value and query heads, in vectors of 16 bytes (a rotated item is the two vectors
-// whose channels turn with one another, or one vector of interleaved pairs).  Each value is read and written once, so the bound
-// is memory, or for a decode step the chain from the length over the table to the store, which is one look-up for the block
-// while its inputs are on the way.
+// One block takes one new token.  A thread keeps one place in the head (two vectors of 16 bytes that turn with one another, one of
+// interleaved pairs, or one that is copied) and its angles, and takes that place of every few heads; so the angles are read once
+// for all of them.  Each value is read and written once, which is the bound where there are many tokens (with the angles read
+// for each head and divisions for each item, instructions were: 107 us for 16,384 tokens
+// of 48 heads, 80 now, 12 small blocks an SM; with 6 of twice the threads 97); a decode step waits for
+// the chain from the length over the table to the store.
 
 #include "mixer_common.cuh"
 #include "paged.h"
@@ -16,8 +18,7 @@ using mix::bf16;
 // The sequence of token t, the last n with cu[n] <= t, 32 candidates at a time (all lanes of a warp call it), with its offsets and
 // its length, which are read beside the last candidates.
 struct Place { int n, first, end, length; };
-__device__ __forceinline__ Place place_of(const int32_t* cu, const int32_t* lengths, int N, int64_t t) {
-    const int lane = threadIdx.x & 31;
+__device__ __forceinline__ Place place_of(const int32_t* cu, const int32_t* lengths, int N, int64_t t, int lane) {
     int lo = 0, n = N;
     while (n > 32) {
         const int step = (n + 31) / 32, at = lane * step;
@@ -32,61 +33,31 @@ __device__ __forceinline__ Place place_of(const int32_t* cu, const int32_t* leng
     return {lo + hit, __shfl_sync(0xffffffffu, first, hit), __shfl_sync(0xffffffffu, end, hit), __shfl_sync(0xffffffffu, length, hit)};
 }
 
+// N angles' cosines or sines, 16 or 8 bytes an access where N allows (a place's angles begin on such a boundary).
+template <int N>
+__device__ __forceinline__ void angles(const float* p, float* d) {
+    if constexpr (N == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(p);
+        d[0] = x.x; d[1] = x.y; d[2] = x.z; d[3] = x.w;
+    } else if constexpr (N == 2) {
+        const float2 x = *reinterpret_cast<const float2*>(p);
+        d[0] = x.x; d[1] = x.y;
+    } else if constexpr (N == 1) {
+        d[0] = *p;
+    }
+}
+
+// blockDim.x threads for the places of a head, blockDim.y heads at a time.
 template <typename T, int V>
-__global__ void __launch_bounds__(256, 4) paged_append_kernel(const PagedAppendArgs a) {
+__global__ void __launch_bounds__(128, 12) paged_append_kernel(const PagedAppendArgs a) {
     using Vec = mix::Vec<T, V>;
     const PagedCache& c = a.c;
     const int64_t t = blockIdx.x;
-    const T* k = static_cast<const T*>(a.k) + t * a.k_tok;
-    const T* v = static_cast<const T*>(a.v) + t * a.v_tok;
-    const T* q = static_cast<const T*>(a.q) + t * a.q_tok;
-    T* qo = static_cast<T*>(a.q_out) + t * a.Hq * c.d;
-
-    // items of a head that turns: two vectors that turn with one another (half layout) or one of pairs, then those that are
-    // copied; then the items of the values
-    const int half = a.rot / 2, turned = a.interleaved ? (V == 1 ? half : a.rot / V) : half / V;
-    const int per_turned = turned + (c.d - a.rot) / V, per_copied = c.d / V;
-    const int heads = c.Hk + (a.q ? a.Hq : 0), all_turned = heads * per_turned, items = all_turned + c.Hk * per_copied;
-    struct Item {
-        Vec x, y;
-        int h, at;                                         // head (keys, queries, then values), channel
-        int pair;                                          // the index of its first angle, or -1
-    };
-    auto read = [&](int e, Item& it) {
-        if (e >= items) {
-            it.h = -1;
-            return;
-        }
-        const T* src;
-        if (e >= all_turned) {
-            const int i = e - all_turned;
-            it.h = heads + i / per_copied;
-            it.at = i % per_copied * V;
-            it.pair = -1;
-            src = v + (it.h - heads) * a.v_head;
-        } else {
-            const int i = e % per_turned;
-            it.h = e / per_turned;
-            src = it.h < c.Hk ? k + it.h * a.k_head : q + (it.h - c.Hk) * a.q_head;
-            it.pair = i >= turned ? -1 : a.interleaved ? (V == 1 ? i : i * V / 2) : i * V;
-            it.at = i >= turned ? a.rot + (i - turned) * V : a.interleaved ? 2 * it.pair : it.pair;
-        }
-        it.x.load(src + it.at);
-        if (it.pair >= 0) {
-            if (!a.interleaved) it.y.load(src + half + it.at);
-            else if (V == 1) it.y.load(src + it.at + 1);
-        }
-    };
-    constexpr int AT_ONCE = 3;                             // items of a thread on their way while the slot is looked up
-    Item it[AT_ONCE];
-    const int tid = threadIdx.x;
-#pragma unroll
-    for (int u = 0; u < AT_ONCE; ++u) read(tid + u * blockDim.x, it[u]);
-
+    const int tx = threadIdx.x, ty = threadIdx.y;
     int n = (int)t;
     int64_t pos;
     if (a.cu) {
-        const Place at = place_of(a.cu, c.lengths, c.N, t);
+        const Place at = place_of(a.cu, c.lengths, c.N, t, (ty * blockDim.x + tx) & 31);
         if (t < at.first || t >= at.end) return;           // a row behind the last sequence
         n = at.n;
         pos = at.length - (at.end - t);
@@ -101,40 +72,70 @@ __global__ void __launch_bounds__(256, 4) paged_append_kernel(const PagedAppendA
             v_at = page * c.v.page + pos % c.page_size * c.v.slot;
         }
     }
+    const int half = a.rot / 2;
     const int64_t turn = min(max(pos, (int64_t)0), (int64_t)a.n_pos - 1) * half;
-    const float* cs = a.cos + turn;
-    const float* sn = a.sin + turn;
-    auto write = [&](Item& i) {
-        if (i.h < 0 || (k_at < 0 && (i.h < c.Hk || i.h >= heads))) return;
-        T* dst = i.h >= heads ? static_cast<T*>(c.v.p) + v_at + (i.h - heads) * c.v.head
-                 : i.h < c.Hk ? static_cast<T*>(c.k.p) + k_at + i.h * c.k.head
-                              : qo + (int64_t)(i.h - c.Hk) * c.d;
-        if (i.pair >= 0 && (!a.interleaved || V == 1)) {
-#pragma unroll
-            for (int u = 0; u < V; ++u) {
-                const float cc = cs[i.pair + u], ss = sn[i.pair + u], p = i.x.get(u), r = i.y.get(u);
-                i.x.set(u, p * cc - r * ss);
-                i.y.set(u, r * cc + p * ss);
+    const T* k = static_cast<const T*>(a.k) + t * a.k_tok;
+    const T* v = static_cast<const T*>(a.v) + t * a.v_tok;
+    const T* q = static_cast<const T*>(a.q) + t * a.q_tok;
+    T* kc = static_cast<T*>(c.k.p) + k_at;
+    T* vc = static_cast<T*>(c.v.p) + v_at;
+    T* qo = static_cast<T*>(a.q_out) + t * a.Hq * c.d;
+
+    // places of a head that turns: two vectors (half layout, and single elements) or one of pairs, then those that are copied
+    const bool pairs = a.interleaved && V > 1;
+    const int turned = pairs ? a.rot / V : half / V, per_turned = turned + (c.d - a.rot) / V;
+    const int keys = k_at < 0 ? c.Hk : 0, turning = c.Hk + (a.q ? a.Hq : 0);     // heads: keys (if there is a slot), queries
+    for (int i = tx; i < per_turned; i += blockDim.x) {
+        const bool turns = i < turned;
+        const int at = !turns ? a.rot + (i - turned) * V : a.interleaved && V == 1 ? 2 * i : i * V;
+        const int other = a.interleaved ? at + 1 : half + at;
+        float cs[V], sn[V];
+        if (turns) {
+            const float* cp = a.cos + turn + (pairs ? at / 2 : i * V);
+            const float* sp = a.sin + turn + (pairs ? at / 2 : i * V);
+            angles<V / 2>(cp, cs);                         // (pairs have half as many angles as channels)
+            angles<V / 2>(sp, sn);
+            if (!pairs) {
+                angles<V - V / 2>(cp + V / 2, cs + V / 2);
+                angles<V - V / 2>(sp + V / 2, sn + V / 2);
             }
-            i.y.store(dst + (a.interleaved ? i.at + 1 : half + i.at));
-        } else if constexpr (V > 1) {
-            if (i.pair >= 0)
-#pragma unroll
-                for (int u = 0; u < V; u += 2) {
-                    const float cc = cs[i.pair + u / 2], ss = sn[i.pair + u / 2], p = i.x.get(u), r = i.x.get(u + 1);
-                    i.x.set(u, p * cc - r * ss);
-                    i.x.set(u + 1, r * cc + p * ss);
-                }
         }
-        i.x.store(dst + i.at);
-    };
-    for (int e = tid; e < items; e += AT_ONCE * blockDim.x) {
-        if (e != tid)
+#pragma unroll 1
+        for (int h = keys + ty; h < turning; h += blockDim.y) {
+            const bool key = h < c.Hk;
+            const T* src = key ? k + h * a.k_head : q + (h - c.Hk) * a.q_head;
+            T* dst = key ? kc + h * c.k.head : qo + (int64_t)(h - c.Hk) * c.d;
+            Vec x, y;
+            x.load(src + at);
+            if (turns && !pairs) {
+                y.load(src + other);
 #pragma unroll
-            for (int u = 0; u < AT_ONCE; ++u) read(e + u * blockDim.x, it[u]);
+                for (int u = 0; u < V; ++u) {
+                    const float p = x.get(u), r = y.get(u);
+                    x.set(u, p * cs[u] - r * sn[u]);
+                    y.set(u, r * cs[u] + p * sn[u]);
+                }
+                y.store(dst + other);
+            } else if (turns) {
+                if constexpr (V > 1)
 #pragma unroll
-        for (int u = 0; u < AT_ONCE; ++u) write(it[u]);
+                    for (int u = 0; u < V; u += 2) {
+                        const float p = x.get(u), r = x.get(u + 1);
+                        x.set(u, p * cs[u / 2] - r * sn[u / 2]);
+                        x.set(u + 1, r * cs[u / 2] + p * sn[u / 2]);
+                    }
+            }
+            x.store(dst + at);
+        }
     }
+    if (k_at < 0) return;
+    for (int i = tx; i < c.d / V; i += blockDim.x)
+#pragma unroll 1
+        for (int h = ty; h < c.Hk; h += blockDim.y) {
+            Vec x;
+            x.load(v + h * a.v_head + i * V);
+            x.store(vc + h * c.v.head + i * V);
+        }
 }
 
 template <typename T>
@@ -144,14 +145,17 @@ cudaError_t typed(const PagedAppendArgs& a, cudaStream_t s) {
     auto fits = [](const void* p, int64_t x, int64_t y, int64_t z) {
         return (uintptr_t)p % 16 == 0 && x % V == 0 && y % V == 0 && z % V == 0;
     };
-    const bool vec = c.d % V == 0 && a.rot % V == 0 && (a.interleaved || a.rot / 2 % V == 0) &&
+    const bool vec = c.d % V == 0 && a.rot % V == 0 && (a.interleaved || a.rot / 2 % V == 0) && fits(a.cos, 0, 0, 0) && fits(a.sin, 0, 0, 0) &&
                      fits(a.k, a.k_tok, a.k_head, 0) && fits(a.v, a.v_tok, a.v_head, 0) &&
                      (!a.q || (fits(a.q, a.q_tok, a.q_head, 0) && fits(a.q_out, 0, 0, 0))) &&
                      fits(c.k.p, c.k.page, c.k.slot, c.k.head) && fits(c.v.p, c.v.page, c.v.slot, c.v.head);
-    const int64_t items = (int64_t)(2 * c.Hk + (a.q ? a.Hq : 0)) * c.d / (vec ? V : 1);
-    const int threads = items > 192 ? 256 : items > 96 ? 128 : items > 48 ? 64 : 32;
-    if (vec) paged_append_kernel<T, V><<<(unsigned)a.n_tokens, threads, 0, s>>>(a);
-    else paged_append_kernel<T, 1><<<(unsigned)a.n_tokens, threads, 0, s>>>(a);
+    const int heads = c.Hk + (a.q ? a.Hq : 0), places = (c.d - (vec && a.interleaved ? 0 : a.rot / 2)) / (vec ? V : 1);
+    int x = 1, y = 128;                                    // as many threads a head as it has places, and no more heads than there are
+    while (x < places && x < 32) x *= 2;
+    y /= x;
+    while (y / 2 >= heads && x * y > 32) y /= 2;
+    if (vec) paged_append_kernel<T, V><<<(unsigned)a.n_tokens, dim3(x, y), 0, s>>>(a);
+    else paged_append_kernel<T, 1><<<(unsigned)a.n_tokens, dim3(x, y), 0, s>>>(a);
     return cudaGetLastError();
 }
 
