@@ -372,9 +372,20 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
                 st[i + 3] = v.w;
             }
         } else {
+            const bool in = KIND != STATE && w.s_in && row < w.da;
+            if (w.s_c == 1 && (uintptr_t)w.s_in % 16 == 0) {  // (d_v goes in steps of 8)
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-                st[i] = KIND != STATE && w.s_in && row < w.da && k0 + i < cols ? w.s_in[state_at + (int64_t)i * w.s_c] : 0.f;
+                for (int i = 0; i < 32; i += 4) {
+                    const float4 v = in && k0 + i < cols ? *reinterpret_cast<const float4*>(w.s_in + state_at + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    st[i] = v.x;
+                    st[i + 1] = v.y;
+                    st[i + 2] = v.z;
+                    st[i + 3] = v.w;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) st[i] = in && k0 + i < cols ? w.s_in[state_at + (int64_t)i * w.s_c] : 0.f;
+            }
         }
         float kept = 1.f;                                 // of what enters, behind the last token (STATE)
         const int64_t slot0 = first / kLinSpan + n;
@@ -514,10 +525,17 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
 #pragma unroll
             for (int i = 0; i < 32; i += 4) *quad(seg_at, i) = make_float4(st[i], st[i + 1], st[i + 2], st[i + 3]);
             if (tid == 256 && blk == 0) w.seg_kept[slot * w.H + h] = kept;
-        } else if (ok && w.s_out && w.seg_chunks == 0 && row < w.da)
+        } else if (ok && w.s_out && w.seg_chunks == 0 && row < w.da) {
+            if (w.s_c == 1 && (uintptr_t)w.s_out % 16 == 0) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-                if (k0 + i < cols) w.s_out[state_at + (int64_t)i * w.s_c] = st[i];
+                for (int i = 0; i < 32; i += 4)
+                    if (k0 + i < cols) *reinterpret_cast<float4*>(w.s_out + state_at + i) = make_float4(st[i], st[i + 1], st[i + 2], st[i + 3]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (k0 + i < cols) w.s_out[state_at + (int64_t)i * w.s_c] = st[i];
+            }
+        }
     } else if (warp == 16) {
         // ------------------------------------------------------------------------------------------- tensor copies
         if (lane == 0 && chunks > 0) {

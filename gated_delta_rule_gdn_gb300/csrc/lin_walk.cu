@@ -2,9 +2,10 @@
 // tokens), and the sums behind the walks of the backward pass.
 //
 // One block of threads walks one (sequence, value head, 32 columns of c) in chunks of 32 tokens, with the state in shared
-// memory.  A chunk: the 32 x 32 triangle of decayed products a_i . b_j, the outputs (row i: a_i S and the triangle's row), then
-// the state.  The triangle is a loop bound, not a factor, so a value that is not a number reaches no token it should not.
-// It is bound by shared-memory reads (two to three for each multiply-add of the triangle).
+// memory.  Half of its warps bring the next chunk's rows (and the prefix sums of its decays) while the others work: the 32 x 32
+// triangle of decayed products a_i . b_j, the outputs (row i: a_i S and the triangle's row), then the state.  A thread takes
+// four rows at a time, so that a value read from shared memory serves four multiply-adds; those reads are the bound.  The
+// triangle is a loop bound, not a factor, so a value that is not a number reaches no token it should not.
 
 #include "internal.h"
 #include "lin_common.cuh"
@@ -13,19 +14,38 @@ namespace gdn {
 namespace {
 
 using mix::bf16;
-constexpr int CH = kLinGenericChunk, COLS = kLinGenericCols, THREADS = 256;
+constexpr int CH = kLinGenericChunk, COLS = kLinGenericCols, WORK = 256, THREADS = 2 * WORK, WARPS = WORK / 32;
+
+// A chunk's rows in fp32, tokens behind the sequence as zeros, and its decays.
+struct GenericTile {
+    float *A, *B, *C, *X;                              // [CH][lda] twice, [CH][COLS] twice
+    lin::Log2* G;
+    float *rowf, *colf, *whole;
+};
+__host__ __device__ inline int generic_lda(int da) { return da | 1; }       // (odd: rows read at one column hit different banks)
+__host__ __device__ inline size_t generic_tile_floats(int da) { return 2 * (size_t)CH * generic_lda(da) + 2 * CH * COLS + 4 * CH + 2; }
 
 template <typename T>
-__global__ void __launch_bounds__(THREADS) lin_walk_kernel(const LinWalk w) {
+__global__ void __launch_bounds__(THREADS, 2) lin_walk_kernel(const LinWalk w) {
     extern __shared__ float sh[];
-    const int da = w.da, lda = da | 1;                 // (odd: rows read at one column hit different banks)
+    const int da = w.da, lda = generic_lda(da);
     float* S = sh;                                     // [da][COLS]
-    float* As = S + da * COLS;                         // [CH][lda]
-    float* Bs = As + CH * lda;                         // [CH][lda]
-    float* Cs = Bs + CH * lda;                         // [CH][COLS]
-    float* P = Cs + CH * COLS;                         // [CH][CH + 1]
-    __shared__ lin::Log2 G[CH];
-    __shared__ float rowf[CH], colf[CH], whole_s, red[THREADS / 32];
+    float* P = S + da * COLS;                          // [CH][CH + 1], G_i - G_j decays and all
+    float* tiles = P + CH * (CH + 1);
+    auto tile = [&](int k) {
+        GenericTile t;
+        float* p = tiles + (k & 1) * (generic_tile_floats(da) + 1) / 2 * 2;
+        t.G = reinterpret_cast<lin::Log2*>(p);
+        t.rowf = p + 2 * CH;
+        t.colf = t.rowf + CH;
+        t.whole = t.colf + CH;
+        t.A = t.whole + 2;
+        t.B = t.A + CH * lda;
+        t.C = t.B + CH * lda;
+        t.X = t.C + CH * COLS;
+        return t;
+    };
+    __shared__ float red[WARPS];
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int blocks = (w.dc + COLS - 1) / COLS;
@@ -49,91 +69,123 @@ __global__ void __launch_bounds__(THREADS) lin_walk_kernel(const LinWalk w) {
         const int r = w.s_c == 1 ? e / COLS : e % da, cc = w.s_c == 1 ? e % COLS : e / da;
         S[r * COLS + cc] = w.s_in && cc < cols ? w.s_in[at_state(r, cc)] : 0.f;
     }
-    __syncthreads();
 
     const int chunks = (len + CH - 1) / CH;
-    for (int step = 0; step < chunks; ++step) {
-        const int ch = w.rev ? chunks - 1 - step : step;
-        const int t0 = ch * CH, L = min(CH, len - t0);
-        // a span's first chunk: the state goes out, or is multiplied with the one that did
-        const bool starts_span = w.spans && t0 % kLinSpan == 0;
-        const int64_t span = ((slot0 + t0 / kLinSpan) * w.H + h) * blocks + blk;
-        if (starts_span && !w.rev)
-            for (int e = tid; e < da * COLS; e += THREADS) w.spans[span * (da * COLS) + e] = S[e];
-        for (int e = tid; e < CH * da; e += THREADS) {
-            const int i = e / da, r = e % da;
-            const int64_t t = first + t0 + i;
-            As[i * lda + r] = i < L ? mix::ld(a + t * w.a.tok + r) : 0.f;
-            Bs[i * lda + r] = i < L ? mix::ld(b + t * w.b.tok + r) : 0.f;
-        }
-        for (int e = tid; e < CH * COLS; e += THREADS) {
-            const int i = e / COLS, cc = e % COLS;
-            Cs[e] = i < L && cc < cols ? mix::ld(c + (first + t0 + i) * w.c.tok + cc) : 0.f;
-        }
-        if (warp == 0) {                               // prefix sums of the log decays
+    auto start_of = [&](int step) { return (w.rev ? chunks - 1 - step : step) * CH; };
+    // a chunk's rows by one half of the warps, a warp a row
+    auto bring = [&](int step) {
+        const GenericTile t = tile(step);
+        const int t0 = start_of(step), L = min(CH, len - t0), wp = warp & (WARPS - 1);
+        if (wp == WARPS - 1) {                         // prefix sums of the log decays
             const lin::Log2 s = lin::prefix(lane < L ? lin::log2_decay(w.g[(first + t0 + lane) * w.g_tok + h * w.g_head]) : lin::Log2{0.f, 0.f}, lane);
             const lin::Log2 end{__shfl_sync(0xffffffffu, s.hi, 31), __shfl_sync(0xffffffffu, s.lo, 31)};
             const float before = exp2f(s.hi + s.lo), behind = exp2f(lin::minus(end, s));
-            G[lane] = s;
-            rowf[lane] = w.s_inter * (w.rev ? behind : before);
-            colf[lane] = w.s_state * (w.rev ? before : behind);
-            if (lane == 0) whole_s = exp2f(end.hi + end.lo);
+            t.G[lane] = s;
+            t.rowf[lane] = w.s_inter * (w.rev ? behind : before);
+            t.colf[lane] = w.s_state * (w.rev ? before : behind);
+            if (lane == 0) *t.whole = exp2f(end.hi + end.lo);
         }
-        __syncthreads();
-        for (int e = tid; e < CH * CH; e += THREADS) {
-            const int i = e / CH, j = e % CH;
-            if (w.rev ? j < i : j > i) continue;
-            float s = 0.f;
-            for (int r = 0; r < da; ++r) s = fmaf(As[i * lda + r], Bs[j * lda + r], s);
-            P[i * (CH + 1) + j] = w.s_intra * s * exp2f(w.rev ? lin::minus(G[j], G[i]) : lin::minus(G[i], G[j]));
+#pragma unroll 4
+        for (int i = wp; i < CH; i += WARPS) {
+            const int64_t row = first + t0 + i;
+            const bool in = i < L;
+            for (int r = lane; r < da; r += 32) {
+                t.A[i * lda + r] = in ? mix::ld(a + row * w.a.tok + r) : 0.f;
+                t.B[i * lda + r] = in ? mix::ld(b + row * w.b.tok + r) : 0.f;
+            }
+            t.C[i * COLS + lane] = in && lane < cols ? mix::ld(c + row * w.c.tok + lane) : 0.f;
+            if (x) t.X[i * COLS + lane] = in && lane < cols ? mix::ld(x + row * w.x.tok + lane) : 0.f;
         }
-        __syncthreads();
-        for (int i = warp; i < L; i += THREADS / 32) { // a warp a row, a lane a column
-            float s = 0.f, f = 0.f;
-            for (int r = 0; r < da; ++r) s = fmaf(As[i * lda + r], S[r * COLS + lane], s);
-            const int j0 = w.rev ? i + 1 : 0, j1 = w.rev ? L : i;
-            for (int j = j0; j < j1; ++j) f = fmaf(P[i * (CH + 1) + j], Cs[j * COLS + lane], f);
-            s *= rowf[i];
-            const int64_t t = first + t0 + i;
-            if (w.dots) {
-                const float xi = lane < cols ? mix::ld(x + t * w.x.tok + lane) : 0.f;
-                float d = lane < cols ? xi * s : 0.f, p = lane < cols ? xi * f : 0.f;
-                for (int m = 16; m > 0; m >>= 1) {
-                    d += __shfl_xor_sync(0xffffffffu, d, m);
-                    p += __shfl_xor_sync(0xffffffffu, p, m);
+    };
+    if (warp >= WARPS && chunks > 0) bring(0);
+    __syncthreads();
+
+    constexpr int R = CH / WARPS;                      // rows of a warp
+    auto work_sync = [] { asm volatile("bar.sync 1, 256;" ::: "memory"); };
+    for (int step = 0; step < chunks; ++step) {
+        if (warp >= WARPS) {
+            if (step + 1 < chunks) bring(step + 1);
+        } else {
+            const GenericTile t = tile(step);
+            const int t0 = start_of(step), L = min(CH, len - t0);
+            // a span's first chunk: the state goes out, or is multiplied with the one that did
+            const bool starts_span = w.spans && t0 % kLinSpan == 0;
+            const int64_t span = ((slot0 + t0 / kLinSpan) * w.H + h) * blocks + blk;
+            if (starts_span && !w.rev)
+                for (int e = tid; e < da * COLS; e += WORK) w.spans[span * (da * COLS) + e] = S[e];
+            float s[R] = {}, f[R] = {};
+            for (int r = 0; r < da; ++r) {             // row i = warp + k WARPS, column j = lane
+                const float y = t.B[lane * lda + r];
+#pragma unroll
+                for (int k = 0; k < R; ++k) s[k] = fmaf(t.A[(warp + k * WARPS) * lda + r], y, s[k]);
+            }
+#pragma unroll
+            for (int k = 0; k < R; ++k) {
+                const int i = warp + k * WARPS;
+                const bool pair = w.rev ? lane >= i : lane <= i;
+                if (pair) P[i * (CH + 1) + lane] = w.s_intra * s[k] * exp2f(w.rev ? lin::minus(t.G[lane], t.G[i]) : lin::minus(t.G[i], t.G[lane]));
+                s[k] = 0.f;
+            }
+            __syncwarp();                              // (a warp reads its own rows of P)
+            for (int r = 0; r < da; ++r) {             // a warp its rows, a lane a column
+                const float y = S[r * COLS + lane];
+#pragma unroll
+                for (int k = 0; k < R; ++k) s[k] = fmaf(t.A[(warp + k * WARPS) * lda + r], y, s[k]);
+            }
+#pragma unroll
+            for (int k = 0; k < R; ++k) {
+                const int i = warp + k * WARPS, j0 = w.rev ? i + 1 : 0, j1 = w.rev ? L : i;
+                for (int j = j0; j < j1; ++j) f[k] = fmaf(P[i * (CH + 1) + j], t.C[j * COLS + lane], f[k]);
+            }
+#pragma unroll
+            for (int k = 0; k < R; ++k) {
+                const int i = warp + k * WARPS;
+                if (i >= L) continue;
+                const int64_t row = first + t0 + i;
+                float y = s[k] * t.rowf[i];
+                if (w.dots) {
+                    const float xi = t.X[i * COLS + lane];
+                    float d = lane < cols ? xi * y : 0.f, p = lane < cols ? xi * f[k] : 0.f;
+                    for (int m = 16; m > 0; m >>= 1) {
+                        d += __shfl_xor_sync(0xffffffffu, d, m);
+                        p += __shfl_xor_sync(0xffffffffu, p, m);
+                    }
+                    if (lane == 0) {
+                        w.dots[((int64_t)blk * w.H + h) * w.rows() + row] = d;
+                        w.pair_dots[((int64_t)blk * w.H + h) * w.rows() + row] = p;
+                    }
                 }
-                if (lane == 0) {
-                    w.dots[((int64_t)blk * w.H + h) * w.rows() + t] = d;
-                    w.pair_dots[((int64_t)blk * w.H + h) * w.rows() + t] = p;
+                y = fmaf(P[i * (CH + 1) + i], t.C[i * COLS + lane], y + f[k]);
+                if (lane < cols) {
+                    const int64_t at = (row * w.H + h) * w.dc + c0 + lane;
+                    if (w.out_f32) static_cast<float*>(w.out)[at] = y;
+                    else mix::st(static_cast<T*>(w.out) + at, y);
                 }
             }
-            s += f;
-            s = fmaf(P[i * (CH + 1) + i], Cs[i * COLS + lane], s);
-            if (lane < cols) {
-                const int64_t at = (t * w.H + h) * w.dc + c0 + lane;
-                if (w.out_f32) static_cast<float*>(w.out)[at] = s;
-                else mix::st(static_cast<T*>(w.out) + at, s);
+            const float whole = *t.whole;
+            if (starts_span && w.rev) {
+                float sum = 0.f;
+                for (int e = tid; e < da * COLS; e += WORK) sum = fmaf(S[e], w.spans[span * (da * COLS) + e], sum);
+                for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+                if (lane == 0) red[warp] = sum;
             }
-        }
-        const float whole = whole_s;
-        if (starts_span && w.rev) {
-            float sum = 0.f;
-            for (int e = tid; e < da * COLS; e += THREADS) sum = fmaf(S[e], w.spans[span * (da * COLS) + e], sum);
-            for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-            if (lane == 0) red[warp] = sum;
-            __syncthreads();
-            if (tid == 0) {
-                float s = 0.f;
-                for (int i = 0; i < THREADS / 32; ++i) s += red[i];
-                w.anchors[span] = whole * s;
+            work_sync();                               // every row has read the state
+            if (starts_span && w.rev && tid == 0) {
+                float sum = 0.f;
+                for (int i = 0; i < WARPS; ++i) sum += red[i];
+                w.anchors[span] = whole * sum;
             }
-        }
-        __syncthreads();
-        for (int e = tid; e < da * COLS; e += THREADS) {
-            const int r = e / COLS, cc = e % COLS;
-            float s = whole * S[e];
-            for (int j = 0; j < L; ++j) s = fmaf(Bs[j * lda + r], colf[j] * Cs[j * COLS + cc], s);
-            S[e] = s;
+            for (int r0 = warp; r0 < da; r0 += R * WARPS) {                     // rows r0 + k WARPS of the state, a lane a column
+                float u[R] = {};
+                for (int j = 0; j < L; ++j) {
+                    const float y = t.colf[j] * t.C[j * COLS + lane];
+#pragma unroll
+                    for (int k = 0; k < R; ++k) u[k] = fmaf(t.B[j * lda + min(r0 + k * WARPS, da - 1)], y, u[k]);
+                }
+#pragma unroll
+                for (int k = 0; k < R; ++k)
+                    if (r0 + k * WARPS < da) S[(r0 + k * WARPS) * COLS + lane] = fmaf(whole, S[(r0 + k * WARPS) * COLS + lane], u[k]);
+            }
         }
         __syncthreads();
     }
@@ -285,7 +337,7 @@ __global__ void __launch_bounds__(256) lin_segments_kernel(const LinWalk w) {
 cudaError_t launch_lin_walk_generic(const LinWalk& w, cudaStream_t s) {
     const int64_t units = (int64_t)w.N() * w.H * lin_blocks(w.dc, false);
     if (units == 0) return cudaSuccess;
-    const size_t smem = sizeof(float) * ((size_t)w.da * COLS + 2 * (size_t)CH * (w.da | 1) + CH * COLS + CH * (CH + 1));
+    const size_t smem = sizeof(float) * ((size_t)w.da * COLS + CH * (CH + 1) + 2 * ((generic_tile_floats(w.da) + 1) / 2 * 2));
     auto kernel = w.bf16 ? lin_walk_kernel<bf16> : lin_walk_kernel<float>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;

@@ -22,6 +22,7 @@ namespace {
 using mix::bf16;
 constexpr int WARPS = 4, THREADS = 32 * WARPS, RUN = 16;
 constexpr float LOG2E = 1.4426950408889634f;
+constexpr int kMaxParts = 1024;
 
 // Tokens of one part of a sequence of `len`: a multiple of 64, at least 128
 __host__ __device__ inline int part_tokens(int len, int splits) {
@@ -406,49 +407,51 @@ __global__ void __launch_bounds__(THREADS) paged_attn_generic_kernel(const Paged
     }
 }
 
-// Joins the parts of each (sequence, query head) that has more than one: a block each, its warps take parts in turn.
+// Joins the parts of each (sequence, query head) that has more than one: a block each, a channel a thread.
 template <typename T>
 __global__ void __launch_bounds__(THREADS) paged_attn_join_kernel(const PagedAttnArgs a) {
-    __shared__ float tops_s[1024], sums_s[1024], joint[WARPS][256], total_s[WARPS];
+    __shared__ float tops_s[kMaxParts], sums_s[kMaxParts];
     const PagedCache& c = a.c;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31;
     const int n = blockIdx.x / a.Hq, hq = blockIdx.x % a.Hq;
     const int len = sequence_tokens(c, n), per = part_tokens(len, a.splits), parts = (len + per - 1) / per;
     mix::wait_behind();
     if (parts <= 1) return;
     const float* sums = Part{a, n, hq, 0, parts}.sums();
     const float* tops = Part{a, n, hq, 0, parts}.tops();
-    float top = -INFINITY;
     for (int s = tid; s < parts; s += THREADS) {
         const float2 t = *reinterpret_cast<const float2*>(tops + 2 * s);
         tops_s[s] = t.x;
         sums_s[s] = t.y;
     }
     __syncthreads();
+    float top = -INFINITY;
     for (int s = lane; s < parts; s += 32) top = fmaxf(top, tops_s[s]);
     for (int m = 16; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
-    float total = 0.f, o[8] = {};
-#pragma unroll 2
-    for (int s = warp; s < parts; s += WARPS) {
-        const float f = tops_s[s] == top ? 1.f : exp2f(tops_s[s] - top);
-        total = fmaf(f, sums_s[s], total);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (lane + 32 * i < c.d) o[i] = fmaf(f, sums[(int64_t)s * c.d + lane + 32 * i], o[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) joint[warp][lane + 32 * i] = o[i];
-    if (lane == 0) total_s[warp] = total;
     __syncthreads();
-    total = 0.f;
-    for (int w = 0; w < WARPS; ++w) total += total_s[w];
-    const Part part{a, n, hq, 0, 1};
-    for (int i = tid; i < c.d; i += THREADS) {
-        float s = 0.f;
+    for (int s = tid; s < parts; s += THREADS) tops_s[s] = tops_s[s] == top ? 1.f : exp2f(tops_s[s] - top);
+    __syncthreads();
+    float total = 0.f, o[2] = {0.f, 0.f};
+    const bool in[2] = {tid < c.d, tid + THREADS < c.d};
+    for (int s0 = 0; s0 < parts; s0 += 8) {                        // eight parts' reads on their way
+        float x[8][2];
 #pragma unroll
-        for (int w = 0; w < WARPS; ++w) s += joint[w][i];
-        part.put<T>(i, s, total);
+        for (int u = 0; u < 8; ++u)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) x[u][i] = s0 + u < parts && in[i] ? sums[(int64_t)(s0 + u) * c.d + tid + i * THREADS] : 0.f;
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            if (s0 + u < parts) {
+                const float f = tops_s[s0 + u];
+                total = fmaf(f, sums_s[s0 + u], total);
+                o[0] = fmaf(f, x[u][0], o[0]);
+                o[1] = fmaf(f, x[u][1], o[1]);
+            }
     }
+    const Part part{a, n, hq, 0, 1};
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        if (in[i]) part.put<T>(tid + i * THREADS, o[i], total);
     if (tid == 0) part.close(top, total);
 }
 
@@ -480,7 +483,7 @@ int paged_attn_splits(const PagedAttnArgs& a) {
     const int64_t least = (most + 2047) / 2048, fill = 304 / (units > 0 ? units : 1), top = (most + 127) / 128;
     int64_t s = least > fill ? least : fill;
     if (s > top) s = top;
-    return (int)(s < 1 ? 1 : s > 1024 ? 1024 : s);
+    return (int)(s < 1 ? 1 : s > kMaxParts ? kMaxParts : s);
 }
 
 size_t paged_attn_workspace_bytes(const PagedAttnArgs& a) {
