@@ -3,8 +3,8 @@
 //
 // One block of threads walks one (sequence, value head, 32 columns of c) in chunks of 32 tokens, with the state in shared
 // memory.  Half of its warps bring the next chunk's rows (and the prefix sums of its decays) while the others work: the 32 x 32
-// triangle of decayed products a_i . b_j, the outputs (row i: a_i S and the triangle's row), then the state.  A thread takes
-// four rows at a time, so that a value read from shared memory serves four multiply-adds; those reads are the bound.  The
+// triangle of decayed products a_i . b_j, the outputs (row i: a_i S and the triangle's row), then the state.  Bound by reads of
+// shared memory, so a thread takes four rows at a time, and four channels an access.  The
 // triangle is a loop bound, not a factor, so a value that is not a number reaches no token it should not.
 
 #include "internal.h"
@@ -18,34 +18,38 @@ constexpr int CH = kLinGenericChunk, COLS = kLinGenericCols, WORK = 256, THREADS
 
 // A chunk's rows in fp32, tokens behind the sequence as zeros, and its decays.
 struct GenericTile {
-    float *A, *B, *C, *X;                              // [CH][lda] twice, [CH][COLS] twice
+    float *A, *B, *C, *X;                              // [CH][lda] twice (zeros up to a step of four channels), [CH][COLS] twice
     lin::Log2* G;
     float *rowf, *colf, *whole;
 };
-__host__ __device__ inline int generic_lda(int da) { return da | 1; }       // (odd: rows read at one column hit different banks)
-__host__ __device__ inline size_t generic_tile_floats(int da) { return 2 * (size_t)CH * generic_lda(da) + 2 * CH * COLS + 4 * CH + 2; }
+__host__ __device__ inline int four(int n) { return (n + 3) & ~3; }
+// 4 more than a multiple of 32: 16-byte reads of eight rows at one column hit different banks
+__host__ __device__ inline int generic_lda(int da) { return (four(da) + 27) / 32 * 32 + 4; }
+__host__ __device__ inline size_t generic_tile_floats(int da) { return 2 * (size_t)CH * generic_lda(da) + 2 * CH * COLS + 4 * CH + 4; }
+constexpr int PLD = CH + 4;                            // row of the triangle
 
 template <typename T>
 __global__ void __launch_bounds__(THREADS, 2) lin_walk_kernel(const LinWalk w) {
-    extern __shared__ float sh[];
-    const int da = w.da, lda = generic_lda(da);
-    float* S = sh;                                     // [da][COLS]
-    float* P = S + da * COLS;                          // [CH][CH + 1], G_i - G_j decays and all
-    float* tiles = P + CH * (CH + 1);
+    extern __shared__ __align__(16) float sh[];
+    const int da = w.da, da4 = four(da), lda = generic_lda(da);
+    float* S = sh;                                     // [da4][COLS]
+    float* P = S + da4 * COLS;                         // [CH][PLD], decays and all
+    float* tiles = P + CH * PLD;
     auto tile = [&](int k) {
         GenericTile t;
-        float* p = tiles + (k & 1) * (generic_tile_floats(da) + 1) / 2 * 2;
+        float* p = tiles + (k & 1) * generic_tile_floats(da);
         t.G = reinterpret_cast<lin::Log2*>(p);
         t.rowf = p + 2 * CH;
         t.colf = t.rowf + CH;
         t.whole = t.colf + CH;
-        t.A = t.whole + 2;
+        t.A = t.whole + 4;
         t.B = t.A + CH * lda;
         t.C = t.B + CH * lda;
         t.X = t.C + CH * COLS;
         return t;
     };
     __shared__ float red[WARPS];
+    constexpr int R = CH / WARPS;                      // rows of a warp
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int blocks = (w.dc + COLS - 1) / COLS;
@@ -64,6 +68,7 @@ __global__ void __launch_bounds__(THREADS, 2) lin_walk_kernel(const LinWalk w) {
     const int64_t state0 = ((int64_t)n * w.H + h) * da * w.dc;
     auto at_state = [&](int r, int cc) { return state0 + (int64_t)r * w.s_r + (int64_t)(c0 + cc) * w.s_c; };
 
+    for (int e = da * COLS + tid; e < da4 * COLS; e += THREADS) S[e] = 0.f;
     for (int e = tid; e < da * COLS; e += THREADS) {
         // (neighbouring threads along the dimension that is contiguous in memory)
         const int r = w.s_c == 1 ? e / COLS : e % da, cc = w.s_c == 1 ? e % COLS : e / da;
@@ -85,22 +90,37 @@ __global__ void __launch_bounds__(THREADS, 2) lin_walk_kernel(const LinWalk w) {
             t.colf[lane] = w.s_state * (w.rev ? before : behind);
             if (lane == 0) *t.whole = exp2f(end.hi + end.lo);
         }
-#pragma unroll 4
-        for (int i = wp; i < CH; i += WARPS) {
-            const int64_t row = first + t0 + i;
-            const bool in = i < L;
-            for (int r = lane; r < da; r += 32) {
-                t.A[i * lda + r] = in ? mix::ld(a + row * w.a.tok + r) : 0.f;
-                t.B[i * lda + r] = in ? mix::ld(b + row * w.b.tok + r) : 0.f;
+        const int64_t row = first + t0;                // (all of a lane's rows are on their way before the first is put down)
+        float y[R], z[R];
+        for (int r = lane; r < da4; r += 32) {
+#pragma unroll
+            for (int k = 0; k < R; ++k) {
+                const int i = r < da ? wp + k * WARPS : CH;
+                y[k] = i < L ? mix::ld(a + (row + i) * w.a.tok + r) : 0.f;
+                z[k] = i < L ? mix::ld(b + (row + i) * w.b.tok + r) : 0.f;
             }
-            t.C[i * COLS + lane] = in && lane < cols ? mix::ld(c + row * w.c.tok + lane) : 0.f;
-            if (x) t.X[i * COLS + lane] = in && lane < cols ? mix::ld(x + row * w.x.tok + lane) : 0.f;
+#pragma unroll
+            for (int k = 0; k < R; ++k) {
+                t.A[(wp + k * WARPS) * lda + r] = y[k];
+                t.B[(wp + k * WARPS) * lda + r] = z[k];
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            const int i = wp + k * WARPS;
+            const bool in = i < L && lane < cols;
+            y[k] = in ? mix::ld(c + (row + i) * w.c.tok + lane) : 0.f;
+            z[k] = in && x ? mix::ld(x + (row + i) * w.x.tok + lane) : 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            t.C[(wp + k * WARPS) * COLS + lane] = y[k];
+            t.X[(wp + k * WARPS) * COLS + lane] = z[k];
         }
     };
     if (warp >= WARPS && chunks > 0) bring(0);
     __syncthreads();
 
-    constexpr int R = CH / WARPS;                      // rows of a warp
     auto work_sync = [] { asm volatile("bar.sync 1, 256;" ::: "memory"); };
     for (int step = 0; step < chunks; ++step) {
         if (warp >= WARPS) {
@@ -114,28 +134,44 @@ __global__ void __launch_bounds__(THREADS, 2) lin_walk_kernel(const LinWalk w) {
             if (starts_span && !w.rev)
                 for (int e = tid; e < da * COLS; e += WORK) w.spans[span * (da * COLS) + e] = S[e];
             float s[R] = {}, f[R] = {};
-            for (int r = 0; r < da; ++r) {             // row i = warp + k WARPS, column j = lane
-                const float y = t.B[lane * lda + r];
+            auto at4 = [](const float* p) { return *reinterpret_cast<const float4*>(p); };
+#pragma unroll 2
+            for (int r = 0; r < da4; r += 4) {         // row i = warp + k WARPS, column j = lane
+                const float4 y = at4(t.B + lane * lda + r);
 #pragma unroll
-                for (int k = 0; k < R; ++k) s[k] = fmaf(t.A[(warp + k * WARPS) * lda + r], y, s[k]);
+                for (int k = 0; k < R; ++k) {
+                    const float4 u = at4(t.A + (warp + k * WARPS) * lda + r);
+                    s[k] = fmaf(u.w, y.w, fmaf(u.z, y.z, fmaf(u.y, y.y, fmaf(u.x, y.x, s[k]))));
+                }
             }
 #pragma unroll
             for (int k = 0; k < R; ++k) {
                 const int i = warp + k * WARPS;
                 const bool pair = w.rev ? lane >= i : lane <= i;
-                if (pair) P[i * (CH + 1) + lane] = w.s_intra * s[k] * exp2f(w.rev ? lin::minus(t.G[lane], t.G[i]) : lin::minus(t.G[i], t.G[lane]));
+                if (pair) P[i * PLD + lane] = w.s_intra * s[k] * exp2f(w.rev ? lin::minus(t.G[lane], t.G[i]) : lin::minus(t.G[i], t.G[lane]));
                 s[k] = 0.f;
             }
             __syncwarp();                              // (a warp reads its own rows of P)
-            for (int r = 0; r < da; ++r) {             // a warp its rows, a lane a column
-                const float y = S[r * COLS + lane];
+#pragma unroll 2
+            for (int r = 0; r < da4; r += 4) {         // a warp its rows, a lane a column
+                const float y[4] = {S[r * COLS + lane], S[(r + 1) * COLS + lane], S[(r + 2) * COLS + lane], S[(r + 3) * COLS + lane]};
 #pragma unroll
-                for (int k = 0; k < R; ++k) s[k] = fmaf(t.A[(warp + k * WARPS) * lda + r], y, s[k]);
+                for (int k = 0; k < R; ++k) {
+                    const float4 u = at4(t.A + (warp + k * WARPS) * lda + r);
+                    s[k] = fmaf(u.w, y[3], fmaf(u.z, y[2], fmaf(u.y, y[1], fmaf(u.x, y[0], s[k]))));
+                }
             }
 #pragma unroll
             for (int k = 0; k < R; ++k) {
-                const int i = warp + k * WARPS, j0 = w.rev ? i + 1 : 0, j1 = w.rev ? L : i;
-                for (int j = j0; j < j1; ++j) f[k] = fmaf(P[i * (CH + 1) + j], t.C[j * COLS + lane], f[k]);
+                const int i = warp + k * WARPS, j1 = w.rev ? L : i;
+                int j = w.rev ? i + 1 : 0;
+                for (; j < j1 && (j & 3); ++j) f[k] = fmaf(P[i * PLD + j], t.C[j * COLS + lane], f[k]);
+                for (; j + 4 <= j1; j += 4) {
+                    const float4 u = at4(P + i * PLD + j);
+                    const float* y = t.C + j * COLS + lane;
+                    f[k] = fmaf(u.w, y[3 * COLS], fmaf(u.z, y[2 * COLS], fmaf(u.y, y[COLS], fmaf(u.x, y[0], f[k]))));
+                }
+                for (; j < j1; ++j) f[k] = fmaf(P[i * PLD + j], t.C[j * COLS + lane], f[k]);
             }
 #pragma unroll
             for (int k = 0; k < R; ++k) {
@@ -155,7 +191,7 @@ __global__ void __launch_bounds__(THREADS, 2) lin_walk_kernel(const LinWalk w) {
                         w.pair_dots[((int64_t)blk * w.H + h) * w.rows() + row] = p;
                     }
                 }
-                y = fmaf(P[i * (CH + 1) + i], t.C[i * COLS + lane], y + f[k]);
+                y = fmaf(P[i * PLD + i], t.C[i * COLS + lane], y + f[k]);
                 if (lane < cols) {
                     const int64_t at = (row * w.H + h) * w.dc + c0 + lane;
                     if (w.out_f32) static_cast<float*>(w.out)[at] = y;
@@ -175,16 +211,24 @@ __global__ void __launch_bounds__(THREADS, 2) lin_walk_kernel(const LinWalk w) {
                 for (int i = 0; i < WARPS; ++i) sum += red[i];
                 w.anchors[span] = whole * sum;
             }
-            for (int r0 = warp; r0 < da; r0 += R * WARPS) {                     // rows r0 + k WARPS of the state, a lane a column
-                float u[R] = {};
-                for (int j = 0; j < L; ++j) {
-                    const float y = t.colf[j] * t.C[j * COLS + lane];
+            for (int r = 4 * warp; r < da4; r += 4 * WARPS) {                   // four rows of the state, a lane a column
+                float u[4] = {};
+#pragma unroll 2
+                for (int j = 0; j < L; j += 4) {       // (tokens behind the sequence are zeros)
+                    const float4 f4 = at4(t.colf + j);
+                    const float ff[4] = {f4.x, f4.y, f4.z, f4.w};
 #pragma unroll
-                    for (int k = 0; k < R; ++k) u[k] = fmaf(t.B[j * lda + min(r0 + k * WARPS, da - 1)], y, u[k]);
+                    for (int q = 0; q < 4; ++q) {
+                        const float y = ff[q] * t.C[(j + q) * COLS + lane];
+                        const float4 x4 = at4(t.B + (j + q) * lda + r);
+                        u[0] = fmaf(x4.x, y, u[0]);
+                        u[1] = fmaf(x4.y, y, u[1]);
+                        u[2] = fmaf(x4.z, y, u[2]);
+                        u[3] = fmaf(x4.w, y, u[3]);
+                    }
                 }
 #pragma unroll
-                for (int k = 0; k < R; ++k)
-                    if (r0 + k * WARPS < da) S[(r0 + k * WARPS) * COLS + lane] = fmaf(whole, S[(r0 + k * WARPS) * COLS + lane], u[k]);
+                for (int q = 0; q < 4; ++q) S[(r + q) * COLS + lane] = fmaf(whole, S[(r + q) * COLS + lane], u[q]);
             }
         }
         __syncthreads();
@@ -337,7 +381,7 @@ __global__ void __launch_bounds__(256) lin_segments_kernel(const LinWalk w) {
 cudaError_t launch_lin_walk_generic(const LinWalk& w, cudaStream_t s) {
     const int64_t units = (int64_t)w.N() * w.H * lin_blocks(w.dc, false);
     if (units == 0) return cudaSuccess;
-    const size_t smem = sizeof(float) * ((size_t)w.da * COLS + CH * (CH + 1) + 2 * ((generic_tile_floats(w.da) + 1) / 2 * 2));
+    const size_t smem = sizeof(float) * ((size_t)four(w.da) * COLS + CH * PLD + 2 * generic_tile_floats(w.da));
     auto kernel = w.bf16 ? lin_walk_kernel<bf16> : lin_walk_kernel<float>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
