@@ -67,7 +67,7 @@ cudaError_t launch_lin_walk_generic(const LinWalk& w, cudaStream_t s);
 // The tensor-core walk: whether it takes the request, the chunks of its segments (0: none), and the walk; its dots are those of
 // the state's part alone.
 bool lin_tensor_fits(const LinWalk& w);
-int lin_segment_chunks(int64_t rows, int64_t N, int H, int dc);
+int lin_segment_chunks(int64_t rows, int64_t N, bool packed, int H, int dc);
 cudaError_t launch_lin_walk_tensor(const LinWalk& w, cudaStream_t s);
 cudaError_t launch_lin_segments(const LinWalk& w, cudaStream_t s);
 // What the pairs of tokens of a chunk have of the decays' gradient, pairs[h][token]: the sum over the keys before the token

@@ -69,8 +69,8 @@ void state(LinWalk& w, const float* in, float* out, int rows_step, int cols_step
 
 gdn_status choose(const char* fn, gdn_algo algo, bool fits, bool& tensor) {
     if (algo == GDN_ALGO_TCGEN05 && !fits)
-        return fail(GDN_ERR_UNSUPPORTED, "%s: the tensor-core path takes bf16, head sizes up to 128 in steps of 8, and rows, heads and "
-                    "outputs on 16-byte boundaries", fn);
+        return fail(GDN_ERR_UNSUPPORTED, "%s: the tensor-core path takes bf16, d_k up to 128, d_v up to 256 (128 backward) in steps of 8, and "
+                    "rows, heads and outputs on 16-byte boundaries", fn);
     tensor = fits && algo != GDN_ALGO_GENERIC;
     return GDN_OK;
 }
@@ -80,8 +80,8 @@ struct Segments {
     int fwd, bwd;                                          // chunks of a segment: of walks whose columns are d_v, and d_k
     size_t states, kept, bytes;
     Segments(const Sizes& z, bool backward) {
-        fwd = gdn::lin_segment_chunks(z.rows(), z.N(), z.H, z.dv);
-        bwd = backward ? gdn::lin_segment_chunks(z.rows(), z.N(), z.H, z.dk) : 0;
+        fwd = gdn::lin_segment_chunks(z.rows(), z.N(), z.cu != nullptr, z.H, z.dv);
+        bwd = backward ? gdn::lin_segment_chunks(z.rows(), z.N(), z.cu != nullptr, z.H, z.dk) : 0;
         states = kept = 0;
         for (int i = 0; i < 2; ++i) {
             const int chunks = i ? bwd : fwd;

@@ -1,4 +1,4 @@
-// Linear attention with a decay for each head on the tensor cores: the walk of lin.h for bf16 tokens, head sizes up to 128.
+// Linear attention with a decay for each head on the tensor cores: the walk of lin.h for bf16 tokens, head sizes up to 128 (d_v of the forward up to 256).
 //
 // One block walks one (sequence, value head, 64 columns of c) in chunks of 128 tokens.  With A, B [128, d] and C [128, 64] the
 // tiles of a chunk, G the prefix sums of its log decays and S the fp32 state [d, 64]:
@@ -102,6 +102,7 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
     const int blk = (int)(unit % blocks), h = (int)(unit / blocks % w.H);
     const int64_t slot = unit / blocks / w.H;             // a sequence, or a segment of one
     int n = 0, len, base_chunk = 0, count;
+    bool last = true;                                     // in the walk's direction
     int64_t first;
     if (w.seg_chunks > 0) {
         n = lin::slot_sequence(w.cu, w.N(), w.T, w.seg_chunks * CK, slot);
@@ -110,6 +111,8 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
         if (at < 0 || at * CK >= len) return;             // (a slot of no segment)
         base_chunk = (int)at;
         count = min(w.seg_chunks, (len + CK - 1) / CK - base_chunk);
+        last = REV ? base_chunk == 0 : base_chunk + count == (len + CK - 1) / CK;
+        if (KIND == STATE && last) return;                // (no segment enters behind it)
     } else {
         n = lin::by_length(w.cu, w.n_seqs, w.T, (int)slot);
         lin::sequence(w.cu, w.T, n, first, len);
@@ -525,7 +528,7 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
 #pragma unroll
             for (int i = 0; i < 32; i += 4) *quad(seg_at, i) = make_float4(st[i], st[i + 1], st[i + 2], st[i + 3]);
             if (tid == 256 && blk == 0) w.seg_kept[slot * w.H + h] = kept;
-        } else if (ok && w.s_out && w.seg_chunks == 0 && row < w.da) {
+        } else if (ok && w.s_out && last && row < w.da) {
             if (w.s_c == 1 && (uintptr_t)w.s_out % 16 == 0) {
 #pragma unroll
                 for (int i = 0; i < 32; i += 4)
@@ -727,15 +730,17 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
 
 bool lin_tensor_fits(const LinWalk& w) {
     auto fits = [](const LinTok& t) { return (uintptr_t)t.p % 16 == 0 && t.tok % 8 == 0 && t.head % 8 == 0; };
-    return w.bf16 && w.da <= 128 && w.dc <= 128 && w.dc % 8 == 0 && fits(w.a) && fits(w.b) && fits(w.c) && (!w.x.p || fits(w.x)) &&
+    return w.bf16 && w.da <= 128 && w.dc <= 256 && w.dc % 8 == 0 && fits(w.a) && fits(w.b) && fits(w.c) && (!w.x.p || fits(w.x)) &&
            (uintptr_t)w.out % 16 == 0 && device_is_sm100_family();
 }
 
 // Chunks of a segment: 0 where there are blocks enough without (all sequences whole), else so many that the segments fill the
-// card, but no fewer than 8 (a segment's state has to come and go besides).
-int lin_segment_chunks(int64_t rows, int64_t N, int H, int dc) {
+// card, but no fewer than 8 (a segment's state has to come and go besides).  Packed sequences may be of any lengths, so that two
+// blocks an SM are enough there, for what one long sequence among them takes; those that are no longer than a segment cost
+// nothing more.  (5 sequences of 391 to 13,636 tokens, 16 heads of 128: forward 222 us whole, 179 in segments.)
+int lin_segment_chunks(int64_t rows, int64_t N, bool packed, int H, int dc) {
     const int64_t units = N * H * lin_blocks(dc, true), chunks = (rows + CK - 1) / CK;
-    if (units >= 96 || chunks < 32) return 0;
+    if (units >= (packed ? 304 : 96) || chunks < 32) return 0;
     const int64_t total = chunks * H * lin_blocks(dc, true);                     // chunks of all walks
     const int64_t each = (total + 151) / 152;
     return (int)(each < 8 ? 8 : each);

@@ -357,11 +357,11 @@ __global__ void __launch_bounds__(256) lin_segments_kernel(const LinWalk w) {
     const int64_t step = (int64_t)w.H * blocks * (128 * kLinCols);
     float* p = w.seg_states + ((slot0 * w.H + h) * blocks + blk) * (128 * kLinCols) + e;
     if (w.rev) p += (segs - 1) * step;
-    float4 x = segs > 0 ? *reinterpret_cast<const float4*>(p) : make_float4(0, 0, 0, 0);
-    for (int k = 0; k < segs; ++k) {
+    float4 x = segs > 1 ? *reinterpret_cast<const float4*>(p) : make_float4(0, 0, 0, 0);
+    for (int k = 0; k < segs; ++k) {                       // (the last has none of its own: the walk takes it to the end)
         float* next = p + (w.rev ? -step : step);
-        const float4 y = k + 1 < segs ? *reinterpret_cast<const float4*>(next) : make_float4(0, 0, 0, 0);
-        const float kept = w.seg_kept[(slot0 + (w.rev ? segs - 1 - k : k)) * w.H + h];
+        const float4 y = k + 2 < segs ? *reinterpret_cast<const float4*>(next) : make_float4(0, 0, 0, 0);
+        const float kept = k + 1 < segs ? w.seg_kept[(slot0 + (w.rev ? segs - 1 - k : k)) * w.H + h] : 0.f;
         *reinterpret_cast<float4*>(p) = make_float4(s[0], s[1], s[2], s[3]);
         s[0] = fmaf(kept, s[0], x.x);
         s[1] = fmaf(kept, s[1], x.y);
@@ -370,7 +370,7 @@ __global__ void __launch_bounds__(256) lin_segments_kernel(const LinWalk w) {
         x = y;
         p = next;
     }
-    if (w.s_out)
+    if (w.s_out && segs == 0)                              // (no tokens: no walk either)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             if (row < w.da && c + i < w.dc) w.s_out[at + (int64_t)(c + i) * w.s_c] = s[i];

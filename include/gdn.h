@@ -674,7 +674,8 @@ gdn_status gdn_short_conv_step(const void* x, const float* weight, const float* 
  *   o        [B, T, H, d_v] dtype (output)
  *   sizes    1 <= d_k, d_v <= 256
  *   algo     GDN_ALGO_AUTO, GDN_ALGO_GENERIC (fp32 arithmetic, any type and size) or
- *            GDN_ALGO_TCGEN05 (tensor cores; GDN_ERR_UNSUPPORTED where the request does not fit it)
+ *            GDN_ALGO_TCGEN05 (tensor cores: bf16, d_k up to 128, d_v up to 256 (backward 128) in
+ *            steps of 8, rows and heads on 16-byte boundaries; else GDN_ERR_UNSUPPORTED)
  *   workspace  lin_workspace_size(0, ...) bytes
  */
 gdn_status lin_chunk_fwd(const void* q, const void* k, const void* v, const float* g, int g_per_head, float scale,

@@ -166,6 +166,7 @@ TENSOR = [
     (2, 1153, 1, 1, 64, 64, None, "head", "dense"),
     (1, 4500, 1, 1, 64, 72, None, "head", "dense"),                                  # few walks and long ones: in segments
     (1, 4400, 1, 2, 24, 64, [0, 1, 1100, 1100, 3300, 4400], "token", "rows"),
+    (1, 5000, 1, 1, 64, 64, [0, 0, 300, 4900, 5000], "token", "dense"),
 ]
 
 
@@ -175,6 +176,12 @@ def test_linear_attention_tensor_cores(case, h0):
     B, T, Hk, H, dk, dv, cu, gate, layout = TENSOR[case]
     x, kw, gen, N = lin_case(50 + case, B, T, Hk, H, dk, dv, BF, cu, gate, h0, layout)
     lin_check(x, kw, gen, N, "tcgen05")
+
+
+@pytest.mark.parametrize("T", [1, 300, 4200])
+def test_linear_attention_tensor_cores_with_wide_values(T):
+    x, kw, gen, N = lin_case(90, 1, T, 1, 1, 64, 200, BF)
+    lin_check(x, kw, gen, N, "tcgen05", backward=False)
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
