@@ -46,13 +46,13 @@ struct LinWalk {
     float* spans;
     float* anchors;
     // Segments of a walk on the tensor cores (0: none), [segment slot][h][block] states of 128 x kLinCols, first of each segment from
-    // nothing, then entering it, and [segment slot][h] what each keeps of the state entering it.
+    // nothing, then entering it, and [segment slot][h] the log (base 2) of what each keeps of the state entering it.
     int seg_chunks;
     float *seg_states, *seg_kept;
     __host__ __device__ int N() const { return cu ? n_seqs : B; }
     __host__ __device__ int64_t rows() const { return (int64_t)B * T; }
 };
-constexpr int kLinSpan = 256, kLinGenericChunk = 32, kLinChunk = 128;
+constexpr int kLinSpan = 128, kLinGenericChunk = 32, kLinChunk = 128;
 // The span slots of a call: those of sequence n begin at first_token / kLinSpan + n.
 inline int64_t lin_slots(int64_t rows, int64_t N, int64_t size) { return rows / size + N + 1; }
 inline int64_t lin_span_slots(int64_t rows, int64_t N) { return lin_slots(rows, N, kLinSpan); }

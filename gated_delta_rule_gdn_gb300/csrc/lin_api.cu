@@ -67,11 +67,14 @@ void state(LinWalk& w, const float* in, float* out, int rows_step, int cols_step
     w.s_in = in; w.s_out = out; w.s_r = rows_step; w.s_c = cols_step;
 }
 
-gdn_status choose(const char* fn, gdn_algo algo, bool fits, bool& tensor) {
+// The tensor cores, where the request fits them and sequences are long enough: a few tokens are one step of the generic walk, which
+// is as fast (6 us for one token of 16 heads either way) and rounds no scores (a single one rounded to bf16 has nothing beside it
+// that it would average out with).
+gdn_status choose(const char* fn, gdn_algo algo, const Sizes& z, bool fits, bool& tensor) {
     if (algo == GDN_ALGO_TCGEN05 && !fits)
         return fail(GDN_ERR_UNSUPPORTED, "%s: the tensor-core path takes bf16, d_k up to 128, d_v up to 256 (128 backward) in steps of 8, and "
                     "rows, heads and outputs on 16-byte boundaries", fn);
-    tensor = fits && algo != GDN_ALGO_GENERIC;
+    tensor = fits && algo != GDN_ALGO_GENERIC && (algo == GDN_ALGO_TCGEN05 || z.rows() >= 16 * (int64_t)z.N());
     return GDN_OK;
 }
 
@@ -172,7 +175,7 @@ gdn_status lin_chunk_fwd(const void* q, const void* k, const void* v, const floa
     w.out = o;
     w.out_f32 = dtype == GDN_F32;
     bool tensor = false;
-    GDN_TRY(choose(fn, algo, gdn::lin_tensor_fits(w), tensor));
+    GDN_TRY(choose(fn, algo, z, gdn::lin_tensor_fits(w), tensor));
     Workspace ws;
     const Segments segments(z, false);
     GDN_TRY(ws.get(fn, workspace, workspace_bytes, tensor ? segments.bytes : 0, static_cast<cudaStream_t>(stream)));
@@ -253,7 +256,7 @@ gdn_status lin_chunk_bwd(const void* q, const void* k, const void* v, const floa
     wv.out_f32 = dtype == GDN_F32;
     bool tensor = false;
     if (T > 0)
-        GDN_TRY(choose(fn, algo, gdn::lin_tensor_fits(wq) && gdn::lin_tensor_fits(wk) && gdn::lin_tensor_fits(wv) &&
+        GDN_TRY(choose(fn, algo, z, gdn::lin_tensor_fits(wq) && gdn::lin_tensor_fits(wk) && gdn::lin_tensor_fits(wv) &&
                        aligned(grad_q, 16) && aligned(grad_k, 16), tensor));
     parts.segments.put(wq, base, tensor, parts.segments.bwd);
     parts.segments.put(wk, base, tensor, parts.segments.bwd);

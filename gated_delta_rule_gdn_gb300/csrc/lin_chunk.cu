@@ -48,6 +48,7 @@ struct Bars {
     uint64_t full[2], full_c[2], empty[2], empty_c[2], gate_empty[2], raw_full[2], p_ready[2], o_full[2], o_free[2];
     uint64_t ds_full, ds_free, s_ready, vhat;
     uint32_t flags[2][2][4];                              // rows of C that are not finite, by chunk and half of the columns
+    lin::Keep keep[2];                                    // of a chunk's whole decay
     uint32_t tmem;
 };
 
@@ -390,7 +391,7 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
                 for (int i = 0; i < 32; ++i) st[i] = in && k0 + i < cols ? w.s_in[state_at + (int64_t)i * w.s_c] : 0.f;
             }
         }
-        float kept = 1.f;                                 // of what enters, behind the last token (STATE)
+        lin::Log2 kept{0.f, 0.f};                         // the log of what is kept of what enters (STATE)
         const int64_t slot0 = first / kLinSpan + n;
         auto span_at = [&](int ch) {
             return w.spans + (((slot0 + ch / (kLinSpan / CK)) * w.H + h) * blocks + blk) * (int64_t)(128 * NB);
@@ -427,9 +428,9 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
             }
             if (!wait(&S.full[s], c >> 1, 32u)) break;
             const float gh = Gh(c)[row], gl = __bfloat162float(Gl(c)[row]), eh = Gh(c)[CK - 1], el = __bfloat162float(Gl(c)[CK - 1]);
+            const lin::Keep keep = S.keep[s];
             arrive(&S.gate_empty[s]);
-            const float whole = exp2f(eh + el);
-            kept *= whole;
+            if (KIND == STATE) kept = lin::add(kept, {eh, el});
             const float f = w.s_state * (REV ? exp2f(gh + gl) : exp2f((eh - gh) + (el - gl)));
             if (starts_span && REV) {                     // or is multiplied with the one that did
                 float* src = span_at(ch);
@@ -444,7 +445,7 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
                 }
                 for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
                 if (lane == 0)
-                    w.anchors[(((slot0 + ch / (kLinSpan / CK)) * w.H + h) * blocks + blk) * 8 + (warp - 8)] = whole * sum;
+                    w.anchors[(((slot0 + ch / (kLinSpan / CK)) * w.H + h) * blocks + blk) * 8 + (warp - 8)] = keep.hi * sum;
             }
             if (!wait(&S.full_c[s], c >> 1, 16u)) break;
             uint32_t top = 0;                             // the largest magnitudes
@@ -457,7 +458,9 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
                 for (int i = 0; i < 4; ++i) cv[i] = make_uint4(0, 0, 0, 0);
             // f as the sum of two bf16 numbers f1 + f2: c f1 rounds to the first operand, what the rounding left has no more
             // than eight bits and is exact, and c f2 joins it
-            const uint32_t f1 = bf2(f, f), f2 = bf2(f - low(f1), f - low(f1));
+            const uint32_t f1 = bf2(f, f);
+            const float f_rest = f - low(f1);
+            const uint32_t f2 = bf2(f_rest, f_rest);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const uint32_t at = row * 128 + (((4 * half + i) ^ (row & 7)) << 4);
@@ -467,7 +470,13 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
                 for (int k = 0; k < 4; ++k) {
                     top = most(top, word[k]);
                     hi[k] = mul_bf(word[k], f1);
-                    lo[k] = fma_bf(word[k], f2, fma_bf(word[k], f1, hi[k] ^ 0x80008000u));
+                    const uint32_t rest = fma_bf(word[k], f1, hi[k] ^ 0x80008000u);
+                    if (KIND == SPLIT) {                  // (f2 has eight bits too; the decays' gradient wants more)
+                        const F2 l = fma2(F2{low(word[k]), high(word[k])}, F2{f_rest, f_rest}, F2{low(rest), high(rest)});
+                        lo[k] = bf2(l.x, l.y);
+                    } else {
+                        lo[k] = fma_bf(word[k], f2, rest);
+                    }
                 }
                 sts128(base + M::V + at, hi[0], hi[1], hi[2], hi[3]);
                 sts128(base + M::V + 16384 + at, lo[0], lo[1], lo[2], lo[3]);
@@ -516,10 +525,11 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
                 }
 #pragma unroll
                 for (int k = 0; k < 32; k += 2) {
-                    const F2 v = fma2(F2{whole, whole}, F2{st[k], st[k + 1]},
-                                      F2{__uint_as_float(a[k >> 4][k & 15]), __uint_as_float(a[k >> 4][(k & 15) + 1])});
-                    st[k] = v.x;
-                    st[k + 1] = v.y;
+                    const F2 old{st[k], st[k + 1]};
+                    const F2 v = fma2(F2{keep.lo, keep.lo}, old, F2{__uint_as_float(a[k >> 4][k & 15]), __uint_as_float(a[k >> 4][(k & 15) + 1])});
+                    const F2 now = fma2(F2{keep.hi, keep.hi}, old, v);
+                    st[k] = now.x;
+                    st[k + 1] = now.y;
                 }
             }
             if (KIND != STATE && c + 1 < chunks) operand();
@@ -527,7 +537,7 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
         if (KIND == STATE) {
 #pragma unroll
             for (int i = 0; i < 32; i += 4) *quad(seg_at, i) = make_float4(st[i], st[i + 1], st[i + 2], st[i + 3]);
-            if (tid == 256 && blk == 0) w.seg_kept[slot * w.H + h] = kept;
+            if (tid == 256 && blk == 0) w.seg_kept[slot * w.H + h] = kept.hi;
         } else if (ok && w.s_out && last && row < w.da) {
             if (w.s_c == 1 && (uintptr_t)w.s_out % 16 == 0) {
 #pragma unroll
@@ -712,10 +722,12 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
 #pragma unroll
             for (int i = 0; i < 4; ++i) cf[i] = ex2(REV ? lin::minus(x[i], ref) : lin::minus(ref, x[i]));
             const uint32_t lo[2] = {bf2(x[0].lo, x[1].lo), bf2(x[2].lo, x[3].lo)};
+            const lin::Keep keep = lin::keep_of({__shfl_sync(0xffffffffu, x[3].hi, 31), __shfl_sync(0xffffffffu, x[3].lo, 31)});
             if (c > 1 && !wait(&S.gate_empty[c & 1], (c >> 1) + 1, 1u << 17)) break;
             reinterpret_cast<float4*>(Gh(c))[lane] = make_float4(x[0].hi, x[1].hi, x[2].hi, x[3].hi);
             reinterpret_cast<float4*>(Cf(c))[lane] = make_float4(cf[0], cf[1], cf[2], cf[3]);
             reinterpret_cast<uint2*>(Gl(c))[lane] = make_uint2(lo[0], lo[1]);
+            if (lane == 0) S.keep[c & 1] = keep;
             arrive(&S.full[c & 1]);
         }
     }

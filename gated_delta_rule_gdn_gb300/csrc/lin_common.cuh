@@ -70,6 +70,16 @@ __device__ __forceinline__ Log2 log2_decay(float g) {
     const float x = __fmul_rn(g, L);
     return x < -1000.f ? Log2{-1000.f, 0.f} : Log2{x, fmaf(g, L, -x) + __fmul_rn(g, M)};
 }
+// 2^x of a chunk's whole decay as the sum of two floats (below a half the second is 0), so that what a rounded factor is off by
+// does not grow with the chunks of a long memory: 65,536 tokens with a decay of 1e-5 each would be off by 1e-5 and more.
+struct Keep { float hi, lo; };
+__device__ __forceinline__ Keep keep_of(Log2 x) {
+    const float y = x.hi + x.lo, whole = exp2f(y);
+    if (!(whole >= 0.5f)) return {whole, 0.f};
+    const float rest = expm1f(0.69314718055994531f * y), hi = __fadd_rn(1.f, rest);
+    return {hi, __fsub_rn(rest, __fsub_rn(hi, 1.f))};
+}
+__device__ __forceinline__ float keep(const Keep& k, float s, float add) { return fmaf(k.hi, s, fmaf(k.lo, s, add)); }
 // Sums over the lanes up to this one.
 __device__ __forceinline__ Log2 prefix(Log2 a, int lane) {
     for (int m = 1; m < 32; m <<= 1) {

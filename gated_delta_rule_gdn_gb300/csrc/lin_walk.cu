@@ -20,7 +20,8 @@ constexpr int CH = kLinGenericChunk, COLS = kLinGenericCols, WORK = 256, THREADS
 struct GenericTile {
     float *A, *B, *C, *X;                              // [CH][lda] twice (zeros up to a step of four channels), [CH][COLS] twice
     lin::Log2* G;
-    float *rowf, *colf, *whole;
+    float *rowf, *colf;
+    lin::Keep* keep;
 };
 __host__ __device__ inline int four(int n) { return (n + 3) & ~3; }
 // 4 more than a multiple of 32: 16-byte reads of eight rows at one column hit different banks
@@ -41,8 +42,8 @@ __global__ void __launch_bounds__(THREADS, 2) lin_walk_kernel(const LinWalk w) {
         t.G = reinterpret_cast<lin::Log2*>(p);
         t.rowf = p + 2 * CH;
         t.colf = t.rowf + CH;
-        t.whole = t.colf + CH;
-        t.A = t.whole + 4;
+        t.keep = reinterpret_cast<lin::Keep*>(t.colf + CH);          // (two words)
+        t.A = t.colf + CH + 4;
         t.B = t.A + CH * lda;
         t.C = t.B + CH * lda;
         t.X = t.C + CH * COLS;
@@ -88,7 +89,7 @@ __global__ void __launch_bounds__(THREADS, 2) lin_walk_kernel(const LinWalk w) {
             t.G[lane] = s;
             t.rowf[lane] = w.s_inter * (w.rev ? behind : before);
             t.colf[lane] = w.s_state * (w.rev ? before : behind);
-            if (lane == 0) *t.whole = exp2f(end.hi + end.lo);
+            if (lane == 0) *t.keep = lin::keep_of(end);
         }
         const int64_t row = first + t0;                // (all of a lane's rows are on their way before the first is put down)
         float y[R], z[R];
@@ -198,7 +199,7 @@ __global__ void __launch_bounds__(THREADS, 2) lin_walk_kernel(const LinWalk w) {
                     else mix::st(static_cast<T*>(w.out) + at, y);
                 }
             }
-            const float whole = *t.whole;
+            const lin::Keep kept = *t.keep;
             if (starts_span && w.rev) {
                 float sum = 0.f;
                 for (int e = tid; e < da * COLS; e += WORK) sum = fmaf(S[e], w.spans[span * (da * COLS) + e], sum);
@@ -209,7 +210,7 @@ __global__ void __launch_bounds__(THREADS, 2) lin_walk_kernel(const LinWalk w) {
             if (starts_span && w.rev && tid == 0) {
                 float sum = 0.f;
                 for (int i = 0; i < WARPS; ++i) sum += red[i];
-                w.anchors[span] = whole * sum;
+                w.anchors[span] = kept.hi * sum;
             }
             for (int r = 4 * warp; r < da4; r += 4 * WARPS) {                   // four rows of the state, a lane a column
                 float u[4] = {};
@@ -228,7 +229,7 @@ __global__ void __launch_bounds__(THREADS, 2) lin_walk_kernel(const LinWalk w) {
                     }
                 }
 #pragma unroll
-                for (int q = 0; q < 4; ++q) S[(r + q) * COLS + lane] = fmaf(whole, S[(r + q) * COLS + lane], u[q]);
+                for (int q = 0; q < 4; ++q) S[(r + q) * COLS + lane] = lin::keep(kept, S[(r + q) * COLS + lane], u[q]);
             }
         }
         __syncthreads();
@@ -361,12 +362,12 @@ __global__ void __launch_bounds__(256) lin_segments_kernel(const LinWalk w) {
     for (int k = 0; k < segs; ++k) {                       // (the last has none of its own: the walk takes it to the end)
         float* next = p + (w.rev ? -step : step);
         const float4 y = k + 2 < segs ? *reinterpret_cast<const float4*>(next) : make_float4(0, 0, 0, 0);
-        const float kept = k + 1 < segs ? w.seg_kept[(slot0 + (w.rev ? segs - 1 - k : k)) * w.H + h] : 0.f;
+        const lin::Keep kept = lin::keep_of({k + 1 < segs ? w.seg_kept[(slot0 + (w.rev ? segs - 1 - k : k)) * w.H + h] : 0.f, 0.f});
         *reinterpret_cast<float4*>(p) = make_float4(s[0], s[1], s[2], s[3]);
-        s[0] = fmaf(kept, s[0], x.x);
-        s[1] = fmaf(kept, s[1], x.y);
-        s[2] = fmaf(kept, s[2], x.z);
-        s[3] = fmaf(kept, s[3], x.w);
+        s[0] = lin::keep(kept, s[0], x.x);
+        s[1] = lin::keep(kept, s[1], x.y);
+        s[2] = lin::keep(kept, s[2], x.z);
+        s[3] = lin::keep(kept, s[3], x.w);
         x = y;
         p = next;
     }
