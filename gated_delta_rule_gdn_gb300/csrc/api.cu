@@ -559,7 +559,7 @@ gdn_status gdn_chunk_bwd_workspace_size(int per_channel, int B, int T, int H, in
 
 gdn_status gdn_test_inject(int what) {
     if (what != 0 && what != GDN_TEST_BWD_RECORD_STALL && what != GDN_TEST_FWD_RECORD_STALL &&
-        what != GDN_TEST_FWD_ONE_STAGE && what != GDN_TEST_GLR_STALL)
+        what != GDN_TEST_FWD_ONE_STAGE && what != GDN_TEST_GLR_STALL && what != GDN_TEST_LIN_STALL)
         return fail(GDN_ERR_INVALID_ARG, "gdn_test_inject: unknown injection %d", what);
     g_test_injection = what;
     return ok();

@@ -49,6 +49,7 @@ struct LinWalk {
     // nothing, then entering it, and [segment slot][h] the log (base 2) of what each keeps of the state entering it.
     int seg_chunks;
     float *seg_states, *seg_kept;
+    int test_stall;         // test of the bounded waits: the copies of c are left out
     __host__ __device__ int N() const { return cu ? n_seqs : B; }
     __host__ __device__ int64_t rows() const { return (int64_t)B * T; }
 };

@@ -67,9 +67,11 @@ void state(LinWalk& w, const float* in, float* out, int rows_step, int cols_step
     w.s_in = in; w.s_out = out; w.s_r = rows_step; w.s_c = cols_step;
 }
 
-// The tensor cores, where the request fits them and sequences are long enough: a few tokens are one step of the generic walk, which
-// is as fast (6 us for one token of 16 heads either way) and rounds no scores (a single one rounded to bf16 has nothing beside it
-// that it would average out with).
+// The tensor cores, where the request fits them and sequences have at least 16 tokens on average.  They are the faster ones at any
+// length, but round the scores to bf16, and a score among few has nothing beside it that its rounding would average out with (the
+// queries' gradient of one token and four heads that share it was off by 5e-3 of its size); the generic walk rounds none, and is
+// near for so few (forward, 16 heads of 128: one token 11.5 against 9.0 us; 16 tokens 13.2 against 9.1, 128 tokens 41.7 against
+// 8.2; 256 sequences of 8 tokens 854 against 478).
 gdn_status choose(const char* fn, gdn_algo algo, const Sizes& z, bool fits, bool& tensor) {
     if (algo == GDN_ALGO_TCGEN05 && !fits)
         return fail(GDN_ERR_UNSUPPORTED, "%s: the tensor-core path takes bf16, d_k up to 128, d_v up to 256 (128 backward) in steps of 8, and "
@@ -180,6 +182,7 @@ gdn_status lin_chunk_fwd(const void* q, const void* k, const void* v, const floa
     const Segments segments(z, false);
     GDN_TRY(ws.get(fn, workspace, workspace_bytes, tensor ? segments.bytes : 0, static_cast<cudaStream_t>(stream)));
     segments.put(w, ws.ptr, tensor, segments.fwd);
+    w.test_stall = tensor && gdn::take_test_injection(GDN_TEST_LIN_STALL);
     return finish(fn, tensor ? gdn::launch_lin_walk_tensor(w, ws.s) : gdn::launch_lin_walk_generic(w, ws.s), ws);
 }
 

@@ -556,7 +556,7 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
             prefetch_tmap(&maps.b);
             prefetch_tmap(&maps.c);
             const int ha = h / w.a.group, hb = h / w.b.group, hc = h / w.c.group;
-            int issued = 0, issued_c = 0;
+            int issued = 0, issued_c = w.test_stall ? chunks : 0;
             uint64_t last = globaltimer_ns();
             // each stream is refilled as soon as what reads its buffer is done: polled, so that none waits behind another
             while (issued < chunks || issued_c < chunks) {
@@ -588,7 +588,7 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
             }
             // what was asked for has landed before the block leaves
             for (int c = issued > 2 ? issued - 2 : 0; c < issued; ++c) mbar_wait(&S.full[c & 1], (c >> 1) & 1, kWait);
-            for (int c = issued_c > 2 ? issued_c - 2 : 0; c < issued_c; ++c) mbar_wait(&S.full_c[c & 1], (c >> 1) & 1, kWait);
+            for (int c = issued_c > 2 ? issued_c - 2 : 0; c < issued_c && !w.test_stall; ++c) mbar_wait(&S.full_c[c & 1], (c >> 1) & 1, kWait);
         }
     } else if (warp == 17) {
         // ------------------------------------------------------------------------------------------------ products

@@ -488,6 +488,11 @@ gdn_status gdn_chunk_bwd_workspace_size(int per_channel, int B, int T, int H, in
  * gdn_device_status reports GDN_ERR_TIMEOUT and that call's outputs are unspecified.
  */
 #define GDN_TEST_GLR_STALL 4
+/*
+ * GDN_TEST_LIN_STALL: the next lin_chunk_fwd on the tensor cores leaves out the copies of its values, so that its bounded waits
+ * give up (after 2 s), gdn_device_status reports GDN_ERR_TIMEOUT and that call's outputs are unspecified.
+ */
+#define GDN_TEST_LIN_STALL 5
 gdn_status gdn_test_inject(int what);
 
 /* ======================================================================================

@@ -136,7 +136,7 @@ GENERIC = [
     (1, 300, 2, 2, 64, 100, BF, [0, 0, 1, 33, 33, 290, 300], "token", "heads"),
     (1, 200, 1, 2, 24, 8, F32, [0, 64, 200], "resets", "dense"),
     (1, 129, 1, 1, 32, 32, F32, None, "strong", "dense"),
-    (1, 2100, 1, 2, 16, 40, F32, [0, 1024, 1024, 1030, 2100], "token", "dense"),     # past a span of 1024 tokens
+    (1, 2100, 1, 2, 16, 40, F32, [0, 1024, 1024, 1030, 2100], "token", "dense"),     # many chunks, and a border on one
     (2, 1025, 1, 1, 8, 8, F32, None, "head", "dense"),
 ]
 
@@ -162,7 +162,7 @@ TENSOR = [
     (1, 400, 1, 1, 96, 104, None, "resets", "rows"),
     (1, 700, 2, 2, 128, 128, [0, 0, 1, 130, 130, 386, 640, 700], "token", "dense"),
     (1, 900, 1, 2, 32, 128, [0, 128, 256, 900], "resets", "dense"),
-    (1, 2200, 1, 1, 128, 128, [0, 1024, 1024, 1030, 2200], "head", "dense"),         # past a span of 1024 tokens
+    (1, 2200, 1, 1, 128, 128, [0, 1024, 1024, 1030, 2200], "head", "dense"),         # many chunks, and a border on one
     (2, 1153, 1, 1, 64, 64, None, "head", "dense"),
     (1, 4500, 1, 1, 64, 72, None, "head", "dense"),                                  # few walks and long ones: in segments
     (1, 4400, 1, 2, 24, 64, [0, 1, 1100, 1100, 3300, 4400], "token", "rows"),

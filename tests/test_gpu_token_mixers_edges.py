@@ -168,6 +168,19 @@ def test_tensor_cores_and_generic_kernel_agree_past_where_walks_are_divided():
             near(p, f64(r), name, 2.0 ** -15 if wide else 2.0 ** -6, 2.0 ** -13 if wide else 2.0 ** -5)
 
 
+def test_waits_that_run_out_are_reported_and_leave_the_context_usable():
+    x, kw, gen, N = lin_case(17, 1, 300, 1, 1, 64, 64, BF)
+    want, _ = gdn.lin_chunk_fwd(x["q"], x["k"], x["v"], x["g"], algo="tcgen05", **kw)
+    lib = gdn.load()
+    assert lib.gdn_test_inject(5) == 0
+    gdn.lin_chunk_fwd(x["q"], x["k"], x["v"], x["g"], algo="tcgen05", **kw)
+    torch.cuda.synchronize()
+    assert gdn.device_status() == 4                  # GDN_ERR_TIMEOUT, and cleared
+    assert gdn.device_status() == 0
+    again, _ = gdn.lin_chunk_fwd(x["q"], x["k"], x["v"], x["g"], algo="tcgen05", **kw)
+    assert torch.equal(want, again)
+
+
 # ------------------------------------------------------------------------------------------------------ paged cache
 
 def test_append_and_attention_in_a_graph_on_another_stream():
