@@ -50,9 +50,12 @@ struct LinWalk {
     int seg_chunks;
     float *seg_states, *seg_kept;
     int test_stall;         // test of the bounded waits: the copies of c are left out
+    int wait_first;         // the kernel before it has to be complete (walks on the tensor cores are launched before it is)
     __host__ __device__ int N() const { return cu ? n_seqs : B; }
     __host__ __device__ int64_t rows() const { return (int64_t)B * T; }
 };
+// A span is a chunk of the tensor cores, so that no inner product is carried from one to the next there, where each adds its rounding;
+// the price is 512 bytes of states a token and head (128 x 128) to write and to read.
 constexpr int kLinSpan = 128, kLinGenericChunk = 32, kLinChunk = 128;
 // The span slots of a call: those of sequence n begin at first_token / kLinSpan + n.
 inline int64_t lin_slots(int64_t rows, int64_t N, int64_t size) { return rows / size + N + 1; }
@@ -69,7 +72,9 @@ cudaError_t launch_lin_walk_generic(const LinWalk& w, cudaStream_t s);
 // the state's part alone.
 bool lin_tensor_fits(const LinWalk& w);
 int lin_segment_chunks(int64_t rows, int64_t N, bool packed, int H, int dc);
-cudaError_t launch_lin_walk_tensor(const LinWalk& w, cudaStream_t s);
+// behind: launched while the stream's last kernel still runs (one of this operator, which does not complete before those before it).  A walk that reads nothing of what came before runs at once on the SMs that are free; with spans, or in
+// segments, it waits.
+cudaError_t launch_lin_walk_tensor(const LinWalk& w, bool behind, cudaStream_t s);
 cudaError_t launch_lin_segments(const LinWalk& w, cudaStream_t s);
 // What the pairs of tokens of a chunk have of the decays' gradient, pairs[h][token]: the sum over the keys before the token
 // minus the sum over the queries behind it, of scale e^(G_i - G_j) (q_i . k_j) (dO_i . v_j).

@@ -183,7 +183,7 @@ gdn_status lin_chunk_fwd(const void* q, const void* k, const void* v, const floa
     GDN_TRY(ws.get(fn, workspace, workspace_bytes, tensor ? segments.bytes : 0, static_cast<cudaStream_t>(stream)));
     segments.put(w, ws.ptr, tensor, segments.fwd);
     w.test_stall = tensor && gdn::take_test_injection(GDN_TEST_LIN_STALL);
-    return finish(fn, tensor ? gdn::launch_lin_walk_tensor(w, ws.s) : gdn::launch_lin_walk_generic(w, ws.s), ws);
+    return finish(fn, tensor ? gdn::launch_lin_walk_tensor(w, false, ws.s) : gdn::launch_lin_walk_generic(w, ws.s), ws);
 }
 
 gdn_status lin_chunk_bwd(const void* q, const void* k, const void* v, const float* g, int g_per_head, float scale,
@@ -264,14 +264,16 @@ gdn_status lin_chunk_bwd(const void* q, const void* k, const void* v, const floa
     parts.segments.put(wq, base, tensor, parts.segments.bwd);
     parts.segments.put(wk, base, tensor, parts.segments.bwd);
     parts.segments.put(wv, base, tensor, parts.segments.fwd);
-    auto run = [&](const LinWalk& w) { return tensor ? gdn::launch_lin_walk_tensor(w, ws.s) : gdn::launch_lin_walk_generic(w, ws.s); };
-    cudaError_t e = run(wq);
+    auto run = [&](const LinWalk& w, bool behind) {
+        return tensor ? gdn::launch_lin_walk_tensor(w, behind, ws.s) : gdn::launch_lin_walk_generic(w, ws.s);
+    };
+    cudaError_t e = run(wq, false);
     if (e == cudaSuccess && group > 1)
         e = gdn::launch_lin_group_sum(part(parts.group), grad_q, wq.bf16, z.rows(), H_k, group, d_k, ws.s);
-    if (e == cudaSuccess) e = run(wk);
+    if (e == cudaSuccess) e = run(wk, group == 1);         // (else in the place that the sum over the group still reads)
     if (e == cudaSuccess && group > 1)
         e = gdn::launch_lin_group_sum(part(parts.group), grad_k, wk.bf16, z.rows(), H_k, group, d_k, ws.s);
-    if (e == cudaSuccess) e = run(wv);
+    if (e == cudaSuccess) e = run(wv, true);
     if (tensor && e == cudaSuccess)
         e = gdn::launch_lin_pairs({tq, tk, tv, to, d_k, d_v, scale, g, wq.g_tok, wq.g_head, z.cu, z.n_seqs, B, T, H, pairs}, ws.s);
     gdn::LinDg d{};

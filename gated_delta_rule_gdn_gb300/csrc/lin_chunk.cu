@@ -28,6 +28,17 @@
 //
 // A row of C that is not finite would reach the tokens before it as 0 times that; it is taken out of P C (not out of the
 // state) and added to the rows that see it.
+//
+// Bound by shared memory: a chunk's operands and what is turned on the way are 336 KB of reads and writes (SPLIT 464), so 2.6 and 3.6
+// thousand cycles at 128 bytes a cycle, of the 3.6 and 5.6 that it takes; 128 walks fill 128 of 152 SMs.  B4, T 4096, 16 heads of 128:
+// forward 71 us (57 % of the copy rate), dq 105, dk 110, dv 71.  Not kept: four warps a role instead of eight (137 us forward),
+// products from a branch of one lane instead of an elected one (70 to 150 cycles each, not 33 to 64), decays in 64 bits.
+//
+// The kernels of a call are launched before the one before them has completed, and wait only where they read what it wrote: the walk
+// of dv runs beside that of dk, the sums of pairs beside both, on the SMs that they leave (backward of B4, T 4096, 8 heads: 326 us one
+// after another, 251 so; of 1000 tokens, 16 heads: 112 and 82; B4, T 4096, 16 heads: 391 and 372).
+
+#include <cmath>
 
 #include "lin_tile.cuh"
 
@@ -88,8 +99,10 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
     using M = Map<KIND>;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t base = smem_u32(smem);
+    mix::let_next();
     if (base & 1023u) {                                   // (the tiles' swizzle goes by address)
         if (threadIdx.x == 0) report(1u << 19);
+        last_behind();
         return;
     }
     Bars& S = *reinterpret_cast<Bars*>(smem + M::BARS);
@@ -109,11 +122,17 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
         n = lin::slot_sequence(w.cu, w.N(), w.T, w.seg_chunks * CK, slot);
         lin::sequence(w.cu, w.T, n, first, len);
         const int64_t at = (slot - (first / (w.seg_chunks * CK) + n)) * w.seg_chunks;
-        if (at < 0 || at * CK >= len) return;             // (a slot of no segment)
+        if (at < 0 || at * CK >= len) {                   // (a slot of no segment)
+            last_behind();
+            return;
+        }
         base_chunk = (int)at;
         count = min(w.seg_chunks, (len + CK - 1) / CK - base_chunk);
         last = REV ? base_chunk == 0 : base_chunk + count == (len + CK - 1) / CK;
-        if (KIND == STATE && last) return;                // (no segment enters behind it)
+        if (KIND == STATE && last) {                      // (no segment enters behind it)
+            last_behind();
+            return;
+        }
     } else {
         n = lin::by_length(w.cu, w.n_seqs, w.T, (int)slot);
         lin::sequence(w.cu, w.T, n, first, len);
@@ -144,6 +163,7 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
         mbar_init(&S.vhat, 8);
         fence_mbar_init();
     }
+    if (w.wait_first) mix::wait_behind();                 // (before any wait that is counted)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -535,6 +555,7 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
             if (KIND != STATE && c + 1 < chunks) operand();
         }
         if (KIND == STATE) {
+            mix::wait_behind();                           // (the walk before it enters its segments from the same states)
 #pragma unroll
             for (int i = 0; i < 32; i += 4) *quad(seg_at, i) = make_float4(st[i], st[i + 1], st[i + 2], st[i + 3]);
             if (tid == 256 && blk == 0) w.seg_kept[slot * w.H + h] = kept.hi;
@@ -736,6 +757,7 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
     tc_fence_after();
     __syncwarp();
     if (warp == 17) tmem_dealloc(tmem, 512);
+    last_behind();
 }
 
 }  // namespace
@@ -746,19 +768,41 @@ bool lin_tensor_fits(const LinWalk& w) {
            (uintptr_t)w.out % 16 == 0 && device_is_sm100_family();
 }
 
-// Chunks of a segment: 0 where there are blocks enough without (all sequences whole), else so many that the segments fill the
-// card, but no fewer than 8 (a segment's state has to come and go besides).  Packed sequences may be of any lengths, so that two
-// blocks an SM are enough there, for what one long sequence among them takes; those that are no longer than a segment cost
-// nothing more.  (5 sequences of 391 to 13,636 tokens, 16 heads of 128: forward 222 us whole, 179 in segments.)
+// Chunks of a segment, or 0: all sequences whole.  A chunk takes a walk 2 us and a first pass 1.1, a block 5 us besides, what joins the
+// segments and the two launches 12; 152 blocks run at once.  Whole, a walk takes as long as its longest sequence (forward, one of
+// 4096 tokens, 4 heads of 128: 64 us, 30 in segments of 4 chunks; of 65,536 tokens, 16 heads: 934 and 398 in segments of 57; two of
+// 2048 tokens, 16 heads: 37 and 50).
+//
+// Of packed sequences the lengths are not known here; the longest is taken to have half of the tokens, and segments are short
+// enough to be spread in two or three rounds over the card whatever the lengths (5 sequences, 32,768 tokens, 16 heads, forward and
+// backward, one kernel after another: of even lengths 205 and 1025 us whole, 237 and 1006 in segments of 20 chunks; 391 to 13,636
+// tokens 207 and 1092, 245 and 1031; one of 30,000 and four short ones 435 and 2138, 237 and 1025).
 int lin_segment_chunks(int64_t rows, int64_t N, bool packed, int H, int dc) {
-    const int64_t units = N * H * lin_blocks(dc, true), chunks = (rows + CK - 1) / CK;
-    if (units >= (packed ? 304 : 96) || chunks < 32) return 0;
-    const int64_t total = chunks * H * lin_blocks(dc, true);                     // chunks of all walks
-    const int64_t each = (total + 151) / 152;
-    return (int)(each < 8 ? 8 : each);
+    if (N < 1 || rows < 1) return 0;
+    const int64_t walks = (int64_t)H * lin_blocks(dc, true);
+    constexpr double WALK = 2, STATE = 1.1, BLOCK = 5, JOIN = 12, SMS = 152;
+    auto rounds = [&](int64_t blocks) { return (double)((blocks + 151) / 152); };
+    if (packed && N > 1) {
+        const double chunks = (double)((rows + CK - 1) / CK), each_sm = chunks * walks / SMS;
+        const double each = each_sm / 2.5 < 8 ? 8 : ceil(each_sm / 2.5);
+        const double whole = WALK * (each_sm > chunks / 2 ? each_sm : chunks / 2) + BLOCK;
+        return (WALK + STATE) * (each_sm + each / 2) + 2 * BLOCK + JOIN < whole && 2 * each <= chunks ? (int)each : 0;
+    }
+    const int64_t chunks = (rows / N + CK - 1) / CK;
+    double best = rounds(N * walks) * (WALK * chunks + BLOCK);
+    int best_each = 0;
+    for (int64_t n = 2; n <= 64 && 4 * n <= chunks; ++n) {
+        const int64_t each = (chunks + n - 1) / n;
+        const double cost = rounds(N * walks * n) * (WALK * each + BLOCK) + rounds(N * walks * (n - 1)) * (STATE * each + BLOCK) + JOIN;
+        if (cost < best) {
+            best = cost;
+            best_each = (int)each;
+        }
+    }
+    return best_each;
 }
 
-cudaError_t launch_lin_walk_tensor(const LinWalk& given, cudaStream_t s) {
+cudaError_t launch_lin_walk_tensor(const LinWalk& given, bool behind, cudaStream_t s) {
     LinWalk w = given;
     const int blocks = lin_blocks(w.dc, true);
     const int64_t slots = w.seg_chunks > 0 ? lin_slots(w.rows(), w.N(), w.seg_chunks * CK) : w.N();
@@ -768,19 +812,22 @@ cudaError_t launch_lin_walk_tensor(const LinWalk& given, cudaStream_t s) {
     if (w.rows() > 0 && (!token_map(&maps.a, w.a, w.da, w.H / w.a.group, w.rows()) || !token_map(&maps.b, w.b, w.da, w.H / w.b.group, w.rows()) ||
                          !token_map(&maps.c, w.c, w.dc, w.H / w.c.group, w.rows())))
         return cudaErrorInvalidValue;
-    auto start = [&](auto kernel, uint32_t smem) -> cudaError_t {
+    auto start = [&](auto kernel, uint32_t smem, bool early) -> cudaError_t {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
-        kernel<<<(unsigned)units, THREADS, smem, s>>>(maps, w);
-        return cudaGetLastError();
+        return mix::launch_behind(kernel, dim3((unsigned)units), THREADS, smem, early, s, maps, w);
     };
     if (w.seg_chunks > 0) {
-        cudaError_t e = w.rev ? start(lin_chunk_kernel<true, STATE>, Map<STATE>::BYTES) : start(lin_chunk_kernel<false, STATE>, Map<STATE>::BYTES);
+        w.wait_first = 0;
+        cudaError_t e = w.rev ? start(lin_chunk_kernel<true, STATE>, Map<STATE>::BYTES, behind) : start(lin_chunk_kernel<false, STATE>, Map<STATE>::BYTES, behind);
         if (e == cudaSuccess) e = launch_lin_segments(w, s);
         if (e != cudaSuccess) return e;
+        behind = true;
     }
-    if (w.dots) return w.rev ? start(lin_chunk_kernel<true, SPLIT>, Map<SPLIT>::BYTES) : start(lin_chunk_kernel<false, SPLIT>, Map<SPLIT>::BYTES);
-    return w.rev ? start(lin_chunk_kernel<true, PLAIN>, Map<PLAIN>::BYTES) : start(lin_chunk_kernel<false, PLAIN>, Map<PLAIN>::BYTES);
+    w.wait_first = behind && (w.spans || w.seg_chunks > 0);
+    if (w.dots)
+        return w.rev ? start(lin_chunk_kernel<true, SPLIT>, Map<SPLIT>::BYTES, behind) : start(lin_chunk_kernel<false, SPLIT>, Map<SPLIT>::BYTES, behind);
+    return w.rev ? start(lin_chunk_kernel<true, PLAIN>, Map<PLAIN>::BYTES, behind) : start(lin_chunk_kernel<false, PLAIN>, Map<PLAIN>::BYTES, behind);
 }
 
 cudaError_t lin_read_and_clear_status(unsigned* value, bool clear) {

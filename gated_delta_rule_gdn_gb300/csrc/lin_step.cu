@@ -4,6 +4,7 @@
 // A block takes some columns of one (sequence, head): all its threads hold V columns of every RG-th row between the read and
 // the write, eight rows' reads in flight, and the rows' parts of o are joined in shared memory.  The columns of a head are
 // spread over blocks of 32 where that many heads do not fill the card, else one block takes 128.
+// (256 sequences of 32 heads of 128: 158 us, the copy rate; one sequence of 16: 4.1 us, the call.)
 
 #include "lin_common.cuh"
 

@@ -11,6 +11,8 @@
 // with the values (one would add an error as large as the result's own rounding; the second product is hidden behind memory).
 // A group has at most 16 rows, an eighth of what the block-wide tensor instructions take, and the products are a tenth of what
 // even these warp-wide ones can do beside the bytes, so it is the loads that shape the kernel.
+// (256 sequences of up to 8192 tokens, 32 heads over 8 of 128: 650 us, 97 % of the copy rate for the tokens there are; two stages
+// and three blocks an SM, or three and two, are the same there.)
 // Anything else: a warp a token at a time, lanes along the channels, fp32.
 
 #include "mixer_common.cuh"
@@ -474,7 +476,8 @@ bool vector_rows(const PagedAttnArgs& a) {
 
 }  // namespace
 
-// As many parts as give two blocks an SM (of 152) with full sequences, none smaller than 128 tokens or (where there are blocks
+// As many parts as give two blocks an SM (of 152) with full sequences (one sequence of 32,768 tokens, 32 heads over 8: 34.9 us; for the
+// three that fit an SM 36.9, the join takes longer), none smaller than 128 tokens or (where there are blocks
 // enough without, so that long sequences of a ragged batch do not run last and alone) larger than 2048.
 int paged_attn_splits(const PagedAttnArgs& a) {
     const int64_t most = (int64_t)a.c.max_pages * a.c.page_size;

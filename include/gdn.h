@@ -682,6 +682,7 @@ gdn_status gdn_short_conv_step(const void* x, const float* weight, const float* 
  *            GDN_ALGO_TCGEN05 (tensor cores: bf16, d_k up to 128, d_v up to 256 (backward 128) in
  *            steps of 8, rows and heads on 16-byte boundaries; else GDN_ERR_UNSUPPORTED)
  *   workspace  lin_workspace_size(0, ...) bytes
+ * The bounded waits of the tensor-core kernels are reported by gdn_device_status.
  */
 gdn_status lin_chunk_fwd(const void* q, const void* k, const void* v, const float* g, int g_per_head, float scale,
                          const float* initial_state, float* final_state, const int32_t* cu_seqlens, int n_seqs, void* o,
@@ -695,7 +696,8 @@ gdn_status lin_chunk_fwd(const void* q, const void* k, const void* v, const floa
  *   grad_o            [B, T, H, d_v] dtype, contiguous;  grad_final_state [N, H, d_k, d_v] fp32 or NULL (zero)
  *   grad_q, grad_k    [B, T, H_k, d_k] dtype (a key head sums its value heads' parts, in order);
  *   grad_v            [B, T, H, d_v] dtype
- *   grad_g            fp32, the shape of g (with g_per_head the sum over all tokens, in a fixed order)
+ *   grad_g            fp32, the shape of g (with g_per_head the sum over all tokens, in a fixed order); an input that is
+ *                     not a number can make those of all tokens of its chunk (of 128) not numbers
  *   grad_initial_state  [N, H, d_k, d_v] fp32, or NULL
  *   workspace         lin_workspace_size(1, ...) bytes
  */
