@@ -45,12 +45,12 @@ struct LinWalk {
     // the span's first chunk.
     float* spans;
     float* anchors;
-    // Segments of a walk on the tensor cores (0: none), [segment slot][h][block] states of 128 x kLinCols, first of each segment from
-    // nothing, then entering it, and [segment slot][h] the log (base 2) of what each keeps of the state entering it.
+    // Segments of a walk (0: none) of seg_chunks kLinChunk tokens: [segment slot][h][block] states (128 x kLinCols on the tensor cores,
+    // else da x kLinGenericCols), first of each segment from nothing, then entering it, and [segment slot][h] the log (base 2) of what each keeps of the state entering it.
     int seg_chunks;
     float *seg_states, *seg_kept;
     int test_stall;         // test of the bounded waits: the copies of c are left out
-    int wait_first;         // the kernel before it has to be complete (walks on the tensor cores are launched before it is)
+    int wait_first;         // the kernel before it has to be complete (walks are launched before it is)
     __host__ __device__ int N() const { return cu ? n_seqs : B; }
     __host__ __device__ int64_t rows() const { return (int64_t)B * T; }
 };
@@ -67,14 +67,14 @@ inline size_t lin_span_floats(int da, int dc, bool tensor) {
     return tensor ? (size_t)128 * kLinCols * lin_blocks(dc, true) : (size_t)da * kLinGenericCols * lin_blocks(dc, false);
 }
 
-cudaError_t launch_lin_walk_generic(const LinWalk& w, cudaStream_t s);
-// The tensor-core walk: whether it takes the request, the chunks of its segments (0: none), and the walk; its dots are those of
-// the state's part alone.
+// The tensor-core walk and the generic one: whether the former takes the request, chunks of kLinChunk tokens of a segment of either
+// (0: none), and the walks.  The former's dots are those of the state's part alone.
 bool lin_tensor_fits(const LinWalk& w);
-int lin_segment_chunks(int64_t rows, int64_t N, bool packed, int H, int dc);
+int lin_segment_chunks(int64_t rows, int64_t N, bool packed, int H, int dc, bool tensor);
 // behind: launched while the stream's last kernel still runs (one of this operator, which does not complete before those before it).  A walk that reads nothing of what came before runs at once on the SMs that are free; with spans, or in
 // segments, it waits.
 cudaError_t launch_lin_walk_tensor(const LinWalk& w, bool behind, cudaStream_t s);
+cudaError_t launch_lin_walk_generic(const LinWalk& w, bool behind, cudaStream_t s);
 cudaError_t launch_lin_segments(const LinWalk& w, cudaStream_t s);
 // What the pairs of tokens of a chunk have of the decays' gradient, pairs[h][token]: the sum over the keys before the token
 // minus the sum over the queries behind it, of scale e^(G_i - G_j) (q_i . k_j) (dO_i . v_j).

@@ -80,28 +80,30 @@ gdn_status choose(const char* fn, gdn_algo algo, const Sizes& z, bool fits, bool
     return GDN_OK;
 }
 
-// Segments of the walks on the tensor cores, one set of states for all walks of a call (they come one after another).
+// Segments of the walks, one set of states for all walks of a call (they come one after another) and for either kind of walk.
 struct Segments {
-    int fwd, bwd;                                          // chunks of a segment: of walks whose columns are d_v, and d_k
+    int fwd[2], bwd[2];                                    // chunks of a segment (generic, tensor cores): columns of d_v, and d_k
     size_t states, kept, bytes;
     Segments(const Sizes& z, bool backward) {
-        fwd = gdn::lin_segment_chunks(z.rows(), z.N(), z.cu != nullptr, z.H, z.dv);
-        bwd = backward ? gdn::lin_segment_chunks(z.rows(), z.N(), z.cu != nullptr, z.H, z.dk) : 0;
         states = kept = 0;
-        for (int i = 0; i < 2; ++i) {
-            const int chunks = i ? bwd : fwd;
-            if (chunks == 0) continue;
-            const size_t slots = (size_t)gdn::lin_slots(z.rows(), z.N(), (int64_t)chunks * gdn::kLinChunk) * z.H;
-            const size_t n = 4 * slots * 128 * gdn::kLinCols * gdn::lin_blocks(i ? z.dk : z.dv, true), m = 4 * slots;
-            states = n > states ? n : states;
-            kept = m > kept ? m : kept;
-        }
+        for (int tensor = 0; tensor < 2; ++tensor)
+            for (int i = 0; i < 2; ++i) {
+                const int da = i ? z.dv : z.dk, dc = i ? z.dk : z.dv;
+                const int chunks = i && !backward ? 0 : gdn::lin_segment_chunks(z.rows(), z.N(), z.cu != nullptr, z.H, dc, tensor);
+                (i ? bwd : fwd)[tensor] = chunks;
+                if (chunks == 0) continue;
+                const size_t slots = (size_t)gdn::lin_slots(z.rows(), z.N(), (int64_t)chunks * gdn::kLinChunk) * z.H;
+                const size_t n = 4 * slots * gdn::lin_span_floats(da, dc, tensor), m = 4 * slots;
+                states = n > states ? n : states;
+                kept = m > kept ? m : kept;
+            }
+        states = (states + 255) / 256 * 256;
         kept = (kept + 255) / 256 * 256;
         bytes = states + kept;
     }
-    void put(LinWalk& w, void* base, bool tensor, int chunks) const {
-        if (!tensor || chunks == 0) return;
-        w.seg_chunks = chunks;
+    void put(LinWalk& w, void* base, bool tensor, const int (&chunks)[2]) const {
+        if (chunks[tensor] == 0) return;
+        w.seg_chunks = chunks[tensor];
         w.seg_states = static_cast<float*>(base);
         w.seg_kept = reinterpret_cast<float*>(static_cast<char*>(base) + states);
     }
@@ -180,10 +182,10 @@ gdn_status lin_chunk_fwd(const void* q, const void* k, const void* v, const floa
     GDN_TRY(choose(fn, algo, z, gdn::lin_tensor_fits(w), tensor));
     Workspace ws;
     const Segments segments(z, false);
-    GDN_TRY(ws.get(fn, workspace, workspace_bytes, tensor ? segments.bytes : 0, static_cast<cudaStream_t>(stream)));
+    GDN_TRY(ws.get(fn, workspace, workspace_bytes, segments.fwd[tensor] ? segments.bytes : 0, static_cast<cudaStream_t>(stream)));
     segments.put(w, ws.ptr, tensor, segments.fwd);
     w.test_stall = tensor && gdn::take_test_injection(GDN_TEST_LIN_STALL);
-    return finish(fn, tensor ? gdn::launch_lin_walk_tensor(w, false, ws.s) : gdn::launch_lin_walk_generic(w, ws.s), ws);
+    return finish(fn, tensor ? gdn::launch_lin_walk_tensor(w, false, ws.s) : gdn::launch_lin_walk_generic(w, false, ws.s), ws);
 }
 
 gdn_status lin_chunk_bwd(const void* q, const void* k, const void* v, const float* g, int g_per_head, float scale,
@@ -265,7 +267,7 @@ gdn_status lin_chunk_bwd(const void* q, const void* k, const void* v, const floa
     parts.segments.put(wk, base, tensor, parts.segments.bwd);
     parts.segments.put(wv, base, tensor, parts.segments.fwd);
     auto run = [&](const LinWalk& w, bool behind) {
-        return tensor ? gdn::launch_lin_walk_tensor(w, behind, ws.s) : gdn::launch_lin_walk_generic(w, ws.s);
+        return tensor ? gdn::launch_lin_walk_tensor(w, behind, ws.s) : gdn::launch_lin_walk_generic(w, behind, ws.s);
     };
     cudaError_t e = run(wq, false);
     if (e == cudaSuccess && group > 1)

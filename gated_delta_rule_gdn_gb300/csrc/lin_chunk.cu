@@ -777,21 +777,24 @@ bool lin_tensor_fits(const LinWalk& w) {
 // enough to be spread in two or three rounds over the card whatever the lengths (5 sequences, 32,768 tokens, 16 heads, forward and
 // backward, one kernel after another: of even lengths 205 and 1025 us whole, 237 and 1006 in segments of 20 chunks; 391 to 13,636
 // tokens 207 and 1092, 245 and 1031; one of 30,000 and four short ones 435 and 2138, 237 and 1025).
-int lin_segment_chunks(int64_t rows, int64_t N, bool packed, int H, int dc) {
+//
+// The generic walk, whose chunk of 128 tokens takes 36 us of 128 channels and whose first pass two fifths of that, goes by the same rule.
+int lin_segment_chunks(int64_t rows, int64_t N, bool packed, int H, int dc, bool tensor) {
     if (N < 1 || rows < 1) return 0;
-    const int64_t walks = (int64_t)H * lin_blocks(dc, true);
-    constexpr double WALK = 2, STATE = 1.1, BLOCK = 5, JOIN = 12, SMS = 152;
+    const int64_t walks = (int64_t)H * lin_blocks(dc, tensor);
+    const double WALK = tensor ? 2 : 36, STATE = tensor ? 1.1 : 15, BLOCK = 5, JOIN = 12, SMS = 152;
+    const int least = tensor ? 4 : 1;                     // chunks of a segment
     auto rounds = [&](int64_t blocks) { return (double)((blocks + 151) / 152); };
     if (packed && N > 1) {
         const double chunks = (double)((rows + CK - 1) / CK), each_sm = chunks * walks / SMS;
-        const double each = each_sm / 2.5 < 8 ? 8 : ceil(each_sm / 2.5);
+        const double each = each_sm / 2.5 < 2 * least ? 2 * least : ceil(each_sm / 2.5);
         const double whole = WALK * (each_sm > chunks / 2 ? each_sm : chunks / 2) + BLOCK;
         return (WALK + STATE) * (each_sm + each / 2) + 2 * BLOCK + JOIN < whole && 2 * each <= chunks ? (int)each : 0;
     }
     const int64_t chunks = (rows / N + CK - 1) / CK;
     double best = rounds(N * walks) * (WALK * chunks + BLOCK);
     int best_each = 0;
-    for (int64_t n = 2; n <= 64 && 4 * n <= chunks; ++n) {
+    for (int64_t n = 2; n <= 64 && least * n <= chunks; ++n) {
         const int64_t each = (chunks + n - 1) / n;
         const double cost = rounds(N * walks * n) * (WALK * each + BLOCK) + rounds(N * walks * (n - 1)) * (STATE * each + BLOCK) + JOIN;
         if (cost < best) {

@@ -7,6 +7,12 @@
 namespace gdn {
 namespace lin {
 
+// At the end of a kernel that was launched before the one before it had completed: the grid does not complete before that one, so
+// that what waits for this kernel waits for both.  One block holds it; the others leave their SMs.
+__device__ __forceinline__ void last_behind() {
+    if (blockIdx.x == 0) mix::wait_behind();
+}
+
 // First token row and length of sequence n; malformed offsets are clamped into the tokens.
 __device__ __forceinline__ void sequence(const int32_t* cu, int T, int n, int64_t& first, int& len) {
     if (cu) {

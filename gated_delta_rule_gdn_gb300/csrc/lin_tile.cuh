@@ -13,12 +13,7 @@ using mix::bf16;
 
 constexpr int CK = kLinChunk;                             // tokens of a chunk
 constexpr uint64_t kWait = 2000000000ull;
-
-// At the end of a kernel that was launched before the one before it had completed: the grid does not complete before that one, so
-// that what waits for this kernel waits for both.  One block holds it; the others leave their SMs.
-__device__ __forceinline__ void last_behind() {
-    if (blockIdx.x == 0) mix::wait_behind();
-}
+using lin::last_behind;
 
 __device__ __forceinline__ uint32_t bf2(float x, float y) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);

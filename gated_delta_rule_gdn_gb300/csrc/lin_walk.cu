@@ -30,8 +30,11 @@ __host__ __device__ inline int generic_lda(int da) { return (four(da) + 27) / 32
 __host__ __device__ inline size_t generic_tile_floats(int da) { return 2 * (size_t)CH * generic_lda(da) + 2 * CH * COLS + 4 * CH + 4; }
 constexpr int PLD = CH + 4;                            // row of the triangle
 
-template <typename T>
+// STATE: the state alone, of a segment from nothing.
+template <typename T, bool STATE>
 __global__ void __launch_bounds__(THREADS, 2) lin_walk_kernel(const LinWalk w) {
+    mix::let_next();
+    if (w.wait_first) mix::wait_behind();
     extern __shared__ __align__(16) float sh[];
     const int da = w.da, da4 = four(da), lda = generic_lda(da);
     float* S = sh;                                     // [da4][COLS]
@@ -57,10 +60,29 @@ __global__ void __launch_bounds__(THREADS, 2) lin_walk_kernel(const LinWalk w) {
     const int blocks = (w.dc + COLS - 1) / COLS;
     const int64_t unit = blockIdx.x;
     const int blk = (int)(unit % blocks), h = (int)(unit / blocks % w.H);
-    const int n = lin::by_length(w.cu, w.n_seqs, w.T, (int)(unit / blocks / w.H));
+    const int64_t slot = unit / blocks / w.H;          // a sequence, or a segment of one
     int64_t first;
-    int len;
-    lin::sequence(w.cu, w.T, n, first, len);
+    int n, len, base = 0, chunks;                      // base: the segment's first token
+    bool last = true;                                  // in the walk's direction
+    if (w.seg_chunks > 0) {
+        const int size = w.seg_chunks * kLinChunk;
+        n = lin::slot_sequence(w.cu, w.N(), w.T, size, slot);
+        lin::sequence(w.cu, w.T, n, first, len);
+        const int64_t at = (slot - (first / size + n)) * size;
+        if (at >= 0 && at < len) {
+            base = (int)at;
+            last = w.rev ? at == 0 : at + size >= len;
+        }
+        if (at < 0 || at >= len || (STATE && last)) {  // (no segment; or none enters behind it)
+            lin::last_behind();
+            return;
+        }
+        chunks = (min(size, len - base) + CH - 1) / CH;
+    } else {
+        n = lin::by_length(w.cu, w.n_seqs, w.T, (int)slot);
+        lin::sequence(w.cu, w.T, n, first, len);
+        chunks = (len + CH - 1) / CH;
+    }
     const int c0 = blk * COLS, cols = min(COLS, w.dc - c0);
     const T* a = static_cast<const T*>(w.a.p) + (h / w.a.group) * w.a.head;
     const T* b = static_cast<const T*>(w.b.p) + (h / w.b.group) * w.b.head;
@@ -70,15 +92,20 @@ __global__ void __launch_bounds__(THREADS, 2) lin_walk_kernel(const LinWalk w) {
     const int64_t state0 = ((int64_t)n * w.H + h) * da * w.dc;
     auto at_state = [&](int r, int cc) { return state0 + (int64_t)r * w.s_r + (int64_t)(c0 + cc) * w.s_c; };
 
+    float* seg_at = w.seg_states + ((slot * w.H + h) * blocks + blk) * ((int64_t)da * COLS);
     for (int e = da * COLS + tid; e < da4 * COLS; e += THREADS) S[e] = 0.f;
     for (int e = tid; e < da * COLS; e += THREADS) {
+        if (STATE || w.seg_chunks > 0) {
+            S[e] = STATE ? 0.f : seg_at[e];
+            continue;
+        }
         // (neighbouring threads along the dimension that is contiguous in memory)
         const int r = w.s_c == 1 ? e / COLS : e % da, cc = w.s_c == 1 ? e % COLS : e / da;
         S[r * COLS + cc] = w.s_in && cc < cols ? w.s_in[at_state(r, cc)] : 0.f;
     }
 
-    const int chunks = (len + CH - 1) / CH;
-    auto start_of = [&](int step) { return (w.rev ? chunks - 1 - step : step) * CH; };
+    lin::Log2 all{0.f, 0.f};                           // the log of what is kept of what enters (STATE)
+    auto start_of = [&](int step) { return base + (w.rev ? chunks - 1 - step : step) * CH; };
     // a chunk's rows by one half of the warps, a warp a row
     auto bring = [&](int step) {
         const GenericTile t = tile(step);
@@ -98,12 +125,12 @@ __global__ void __launch_bounds__(THREADS, 2) lin_walk_kernel(const LinWalk w) {
 #pragma unroll
             for (int k = 0; k < R; ++k) {
                 const int i = r < da ? wp + k * WARPS : CH;
-                y[k] = i < L ? mix::ld(a + (row + i) * w.a.tok + r) : 0.f;
+                y[k] = !STATE && i < L ? mix::ld(a + (row + i) * w.a.tok + r) : 0.f;
                 z[k] = i < L ? mix::ld(b + (row + i) * w.b.tok + r) : 0.f;
             }
 #pragma unroll
             for (int k = 0; k < R; ++k) {
-                t.A[(wp + k * WARPS) * lda + r] = y[k];
+                if (!STATE) t.A[(wp + k * WARPS) * lda + r] = y[k];
                 t.B[(wp + k * WARPS) * lda + r] = z[k];
             }
         }
@@ -112,12 +139,12 @@ __global__ void __launch_bounds__(THREADS, 2) lin_walk_kernel(const LinWalk w) {
             const int i = wp + k * WARPS;
             const bool in = i < L && lane < cols;
             y[k] = in ? mix::ld(c + (row + i) * w.c.tok + lane) : 0.f;
-            z[k] = in && x ? mix::ld(x + (row + i) * w.x.tok + lane) : 0.f;
+            z[k] = !STATE && in && x ? mix::ld(x + (row + i) * w.x.tok + lane) : 0.f;
         }
 #pragma unroll
         for (int k = 0; k < R; ++k) {
             t.C[(wp + k * WARPS) * COLS + lane] = y[k];
-            t.X[(wp + k * WARPS) * COLS + lane] = z[k];
+            if (!STATE) t.X[(wp + k * WARPS) * COLS + lane] = z[k];
         }
     };
     if (warp >= WARPS && chunks > 0) bring(0);
@@ -131,74 +158,78 @@ __global__ void __launch_bounds__(THREADS, 2) lin_walk_kernel(const LinWalk w) {
             const GenericTile t = tile(step);
             const int t0 = start_of(step), L = min(CH, len - t0);
             // a span's first chunk: the state goes out, or is multiplied with the one that did
-            const bool starts_span = w.spans && t0 % kLinSpan == 0;
+            const bool starts_span = !STATE && w.spans && t0 % kLinSpan == 0;
             const int64_t span = ((slot0 + t0 / kLinSpan) * w.H + h) * blocks + blk;
             if (starts_span && !w.rev)
                 for (int e = tid; e < da * COLS; e += WORK) w.spans[span * (da * COLS) + e] = S[e];
             float s[R] = {}, f[R] = {};
             auto at4 = [](const float* p) { return *reinterpret_cast<const float4*>(p); };
+            if (!STATE) {
 #pragma unroll 2
-            for (int r = 0; r < da4; r += 4) {         // row i = warp + k WARPS, column j = lane
-                const float4 y = at4(t.B + lane * lda + r);
+                for (int r = 0; r < da4; r += 4) {         // row i = warp + k WARPS, column j = lane
+                    const float4 y = at4(t.B + lane * lda + r);
 #pragma unroll
-                for (int k = 0; k < R; ++k) {
-                    const float4 u = at4(t.A + (warp + k * WARPS) * lda + r);
-                    s[k] = fmaf(u.w, y.w, fmaf(u.z, y.z, fmaf(u.y, y.y, fmaf(u.x, y.x, s[k]))));
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < R; ++k) {
-                const int i = warp + k * WARPS;
-                const bool pair = w.rev ? lane >= i : lane <= i;
-                if (pair) P[i * PLD + lane] = w.s_intra * s[k] * exp2f(w.rev ? lin::minus(t.G[lane], t.G[i]) : lin::minus(t.G[i], t.G[lane]));
-                s[k] = 0.f;
-            }
-            __syncwarp();                              // (a warp reads its own rows of P)
-#pragma unroll 2
-            for (int r = 0; r < da4; r += 4) {         // a warp its rows, a lane a column
-                const float y[4] = {S[r * COLS + lane], S[(r + 1) * COLS + lane], S[(r + 2) * COLS + lane], S[(r + 3) * COLS + lane]};
-#pragma unroll
-                for (int k = 0; k < R; ++k) {
-                    const float4 u = at4(t.A + (warp + k * WARPS) * lda + r);
-                    s[k] = fmaf(u.w, y[3], fmaf(u.z, y[2], fmaf(u.y, y[1], fmaf(u.x, y[0], s[k]))));
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < R; ++k) {
-                const int i = warp + k * WARPS, j1 = w.rev ? L : i;
-                int j = w.rev ? i + 1 : 0;
-                for (; j < j1 && (j & 3); ++j) f[k] = fmaf(P[i * PLD + j], t.C[j * COLS + lane], f[k]);
-                for (; j + 4 <= j1; j += 4) {
-                    const float4 u = at4(P + i * PLD + j);
-                    const float* y = t.C + j * COLS + lane;
-                    f[k] = fmaf(u.w, y[3 * COLS], fmaf(u.z, y[2 * COLS], fmaf(u.y, y[COLS], fmaf(u.x, y[0], f[k]))));
-                }
-                for (; j < j1; ++j) f[k] = fmaf(P[i * PLD + j], t.C[j * COLS + lane], f[k]);
-            }
-#pragma unroll
-            for (int k = 0; k < R; ++k) {
-                const int i = warp + k * WARPS;
-                if (i >= L) continue;
-                const int64_t row = first + t0 + i;
-                float y = s[k] * t.rowf[i];
-                if (w.dots) {
-                    const float xi = t.X[i * COLS + lane];
-                    float d = lane < cols ? xi * y : 0.f, p = lane < cols ? xi * f[k] : 0.f;
-                    for (int m = 16; m > 0; m >>= 1) {
-                        d += __shfl_xor_sync(0xffffffffu, d, m);
-                        p += __shfl_xor_sync(0xffffffffu, p, m);
-                    }
-                    if (lane == 0) {
-                        w.dots[((int64_t)blk * w.H + h) * w.rows() + row] = d;
-                        w.pair_dots[((int64_t)blk * w.H + h) * w.rows() + row] = p;
+                    for (int k = 0; k < R; ++k) {
+                        const float4 u = at4(t.A + (warp + k * WARPS) * lda + r);
+                        s[k] = fmaf(u.w, y.w, fmaf(u.z, y.z, fmaf(u.y, y.y, fmaf(u.x, y.x, s[k]))));
                     }
                 }
-                y = fmaf(P[i * PLD + i], t.C[i * COLS + lane], y + f[k]);
-                if (lane < cols) {
-                    const int64_t at = (row * w.H + h) * w.dc + c0 + lane;
-                    if (w.out_f32) static_cast<float*>(w.out)[at] = y;
-                    else mix::st(static_cast<T*>(w.out) + at, y);
+#pragma unroll
+                for (int k = 0; k < R; ++k) {
+                    const int i = warp + k * WARPS;
+                    const bool pair = w.rev ? lane >= i : lane <= i;
+                    if (pair) P[i * PLD + lane] = w.s_intra * s[k] * exp2f(w.rev ? lin::minus(t.G[lane], t.G[i]) : lin::minus(t.G[i], t.G[lane]));
+                    s[k] = 0.f;
                 }
+                __syncwarp();                              // (a warp reads its own rows of P)
+#pragma unroll 2
+                for (int r = 0; r < da4; r += 4) {         // a warp its rows, a lane a column
+                    const float y[4] = {S[r * COLS + lane], S[(r + 1) * COLS + lane], S[(r + 2) * COLS + lane], S[(r + 3) * COLS + lane]};
+#pragma unroll
+                    for (int k = 0; k < R; ++k) {
+                        const float4 u = at4(t.A + (warp + k * WARPS) * lda + r);
+                        s[k] = fmaf(u.w, y[3], fmaf(u.z, y[2], fmaf(u.y, y[1], fmaf(u.x, y[0], s[k]))));
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < R; ++k) {
+                    const int i = warp + k * WARPS, j1 = w.rev ? L : i;
+                    int j = w.rev ? i + 1 : 0;
+                    for (; j < j1 && (j & 3); ++j) f[k] = fmaf(P[i * PLD + j], t.C[j * COLS + lane], f[k]);
+                    for (; j + 4 <= j1; j += 4) {
+                        const float4 u = at4(P + i * PLD + j);
+                        const float* y = t.C + j * COLS + lane;
+                        f[k] = fmaf(u.w, y[3 * COLS], fmaf(u.z, y[2 * COLS], fmaf(u.y, y[COLS], fmaf(u.x, y[0], f[k]))));
+                    }
+                    for (; j < j1; ++j) f[k] = fmaf(P[i * PLD + j], t.C[j * COLS + lane], f[k]);
+                }
+#pragma unroll
+                for (int k = 0; k < R; ++k) {
+                    const int i = warp + k * WARPS;
+                    if (i >= L) continue;
+                    const int64_t row = first + t0 + i;
+                    float y = s[k] * t.rowf[i];
+                    if (w.dots) {
+                        const float xi = t.X[i * COLS + lane];
+                        float d = lane < cols ? xi * y : 0.f, p = lane < cols ? xi * f[k] : 0.f;
+                        for (int m = 16; m > 0; m >>= 1) {
+                            d += __shfl_xor_sync(0xffffffffu, d, m);
+                            p += __shfl_xor_sync(0xffffffffu, p, m);
+                        }
+                        if (lane == 0) {
+                            w.dots[((int64_t)blk * w.H + h) * w.rows() + row] = d;
+                            w.pair_dots[((int64_t)blk * w.H + h) * w.rows() + row] = p;
+                        }
+                    }
+                    y = fmaf(P[i * PLD + i], t.C[i * COLS + lane], y + f[k]);
+                    if (lane < cols) {
+                        const int64_t at = (row * w.H + h) * w.dc + c0 + lane;
+                        if (w.out_f32) static_cast<float*>(w.out)[at] = y;
+                        else mix::st(static_cast<T*>(w.out) + at, y);
+                    }
+                }
+            } else if (tid == 0) {
+                all = lin::add(all, t.G[CH - 1]);
             }
             const lin::Keep kept = *t.keep;
             if (starts_span && w.rev) {
@@ -235,11 +266,17 @@ __global__ void __launch_bounds__(THREADS, 2) lin_walk_kernel(const LinWalk w) {
         }
         __syncthreads();
     }
-    if (w.s_out)
+    if (STATE) {
+        mix::wait_behind();                            // (the walk before it enters its segments from the same states)
+        for (int e = tid; e < da * COLS; e += THREADS) seg_at[e] = S[e];
+        if (tid == 0 && blk == 0) w.seg_kept[slot * w.H + h] = all.hi;
+    } else if (w.s_out && last) {
         for (int e = tid; e < da * COLS; e += THREADS) {
             const int r = w.s_c == 1 ? e / COLS : e % da, cc = w.s_c == 1 ? e % COLS : e / da;
             if (cc < cols) w.s_out[at_state(r, cc)] = S[r * COLS + cc];
         }
+    }
+    lin::last_behind();
 }
 
 // One block for each (span slot, head), a thread a token: sums of at most kLinSpan terms.
@@ -338,8 +375,37 @@ __global__ void __launch_bounds__(256) lin_group_sum_kernel(const float* part, T
         }
 }
 
-// The states entering the segments of a sequence: four columns of a row of a block's state a thread, segment after segment in the
-// walk's direction.
+// The states entering the segments of a sequence, segment after segment in the walk's direction, an element of a block's state
+// [da][COLS] a thread.
+__global__ void __launch_bounds__(256) lin_generic_segments_kernel(const LinWalk w) {
+    const int blocks = (w.dc + COLS - 1) / COLS, elements = w.da * COLS, per = (elements + 255) / 256;
+    const int e = blockIdx.x % per * 256 + threadIdx.x;
+    const int64_t unit = blockIdx.x / per;
+    const int blk = (int)(unit % blocks), h = (int)(unit / blocks % w.H), n = (int)(unit / blocks / w.H);
+    int64_t first;
+    int len;
+    lin::sequence(w.cu, w.T, n, first, len);
+    const int size = w.seg_chunks * kLinChunk, segs = (len + size - 1) / size;
+    const int64_t slot0 = first / size + n;
+    const int r = e / COLS, c = blk * COLS + e % COLS;
+    const bool in = e < elements, inside = in && c < w.dc;
+    const int64_t at = ((int64_t)n * w.H + h) * w.da * w.dc + (int64_t)r * w.s_r + (int64_t)c * w.s_c;
+    float s = w.s_in && inside ? w.s_in[at] : 0.f;
+    mix::wait_behind();                                   // the segments' own states
+    mix::let_next();
+    for (int k = 0; k < segs && in; ++k) {                // (the last has none of its own: the walk takes it to the end)
+        const int64_t slot = slot0 + (w.rev ? segs - 1 - k : k);
+        float* p = w.seg_states + ((slot * w.H + h) * blocks + blk) * (int64_t)elements + e;
+        const bool own = k + 1 < segs;
+        const float x = own ? *p : 0.f;
+        const lin::Keep kept = lin::keep_of({own ? w.seg_kept[slot * w.H + h] : 0.f, 0.f});
+        *p = s;
+        s = lin::keep(kept, s, x);
+    }
+    if (w.s_out && segs == 0 && inside) w.s_out[at] = s;  // (no tokens: no walk either)
+}
+
+// The same for the tensor-core walk, four columns of a row of a block's state a thread.
 __global__ void __launch_bounds__(256) lin_segments_kernel(const LinWalk w) {
     constexpr int PER = 128 * kLinCols / 1024;             // blocks of threads for a state
     const int blocks = (w.dc + kLinCols - 1) / kLinCols;
@@ -382,15 +448,28 @@ __global__ void __launch_bounds__(256) lin_segments_kernel(const LinWalk w) {
 
 }  // namespace
 
-cudaError_t launch_lin_walk_generic(const LinWalk& w, cudaStream_t s) {
-    const int64_t units = (int64_t)w.N() * w.H * lin_blocks(w.dc, false);
+cudaError_t launch_lin_walk_generic(const LinWalk& given, bool behind, cudaStream_t s) {
+    LinWalk w = given;
+    const int64_t walks = (int64_t)w.H * lin_blocks(w.dc, false);
+    const int64_t units = walks * (w.seg_chunks > 0 ? lin_slots(w.rows(), w.N(), w.seg_chunks * kLinChunk) : w.N());
     if (units == 0) return cudaSuccess;
     const size_t smem = sizeof(float) * ((size_t)four(w.da) * COLS + CH * PLD + 2 * generic_tile_floats(w.da));
-    auto kernel = w.bf16 ? lin_walk_kernel<bf16> : lin_walk_kernel<float>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    kernel<<<(unsigned)units, THREADS, smem, s>>>(w);
-    return cudaGetLastError();
+    auto start = [&](auto kernel, bool early) -> cudaError_t {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+        return mix::launch_behind(kernel, dim3((unsigned)units), THREADS, smem, early, s, w);
+    };
+    if (w.seg_chunks > 0) {
+        w.wait_first = 0;
+        cudaError_t e = w.bf16 ? start(lin_walk_kernel<bf16, true>, behind) : start(lin_walk_kernel<float, true>, behind);
+        if (e != cudaSuccess) return e;
+        const int64_t blocks = (int64_t)w.N() * walks * ((w.da * COLS + 255) / 256);
+        e = mix::launch_behind(lin_generic_segments_kernel, dim3((unsigned)blocks), 256, 0, true, s, w);
+        if (e != cudaSuccess) return e;
+        behind = true;
+    }
+    w.wait_first = behind && (w.spans || w.seg_chunks > 0);
+    return w.bf16 ? start(lin_walk_kernel<bf16, false>, behind) : start(lin_walk_kernel<float, false>, behind);
 }
 
 cudaError_t launch_lin_dg(const LinDg& a, cudaStream_t s) {
