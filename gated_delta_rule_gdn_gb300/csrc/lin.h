@@ -70,7 +70,7 @@ inline size_t lin_span_floats(int da, int dc, bool tensor) {
 // The tensor-core walk and the generic one: whether the former takes the request, chunks of kLinChunk tokens of a segment of either
 // (0: none), and the walks.  The former's dots are those of the state's part alone.
 bool lin_tensor_fits(const LinWalk& w);
-int lin_segment_chunks(int64_t rows, int64_t N, bool packed, int H, int dc, bool tensor);
+int lin_segment_chunks(int64_t rows, int64_t N, bool packed, int H, int da, int dc, bool tensor);
 // behind: launched while the stream's last kernel still runs (one of this operator, which does not complete before those before it).  A walk that reads nothing of what came before runs at once on the SMs that are free; with spans, or in
 // segments, it waits.
 cudaError_t launch_lin_walk_tensor(const LinWalk& w, bool behind, cudaStream_t s);

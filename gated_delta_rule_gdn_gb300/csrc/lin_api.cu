@@ -89,7 +89,7 @@ struct Segments {
         for (int tensor = 0; tensor < 2; ++tensor)
             for (int i = 0; i < 2; ++i) {
                 const int da = i ? z.dv : z.dk, dc = i ? z.dk : z.dv;
-                const int chunks = i && !backward ? 0 : gdn::lin_segment_chunks(z.rows(), z.N(), z.cu != nullptr, z.H, dc, tensor);
+                const int chunks = i && !backward ? 0 : gdn::lin_segment_chunks(z.rows(), z.N(), z.cu != nullptr, z.H, da, dc, tensor);
                 (i ? bwd : fwd)[tensor] = chunks;
                 if (chunks == 0) continue;
                 const size_t slots = (size_t)gdn::lin_slots(z.rows(), z.N(), (int64_t)chunks * gdn::kLinChunk) * z.H;

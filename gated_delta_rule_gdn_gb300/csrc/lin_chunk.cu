@@ -778,13 +778,22 @@ bool lin_tensor_fits(const LinWalk& w) {
 // backward, one kernel after another: of even lengths 205 and 1025 us whole, 237 and 1006 in segments of 20 chunks; 391 to 13,636
 // tokens 207 and 1092, 245 and 1031; one of 30,000 and four short ones 435 and 2138, 237 and 1025).
 //
-// The generic walk, whose chunk of 128 tokens takes 36 us of 128 channels and whose first pass two fifths of that, goes by the same rule.
-int lin_segment_chunks(int64_t rows, int64_t N, bool packed, int H, int dc, bool tensor) {
+// The generic walk goes by the same rule with its own times: 11 us a chunk and 0.2 us a channel of a, two thirds of that for a first
+// pass, blocks that share an SM each at 0.82 of that (forward, fp32: one sequence of 1000 tokens, 16 heads of 128: 291 us whole, 184 in
+// segments of one chunk, 178 of two, 290 of four; two of 2048 tokens: 578 whole, 583 of two; two of 777 tokens, 3 heads of 40: 134
+// and 50 of one).
+int lin_segment_chunks(int64_t rows, int64_t N, bool packed, int H, int da, int dc, bool tensor) {
     if (N < 1 || rows < 1) return 0;
     const int64_t walks = (int64_t)H * lin_blocks(dc, tensor);
-    const double WALK = tensor ? 2 : 36, STATE = tensor ? 1.1 : 15, BLOCK = 5, JOIN = 12, SMS = 152;
+    constexpr double BLOCK = 5, JOIN = 12, SMS = 152;
+    const double WALK = tensor ? 2 : 11 + 0.195 * da, STATE = tensor ? 1.1 : 0.65 * WALK;
     const int least = tensor ? 4 : 1;                     // chunks of a segment
-    auto rounds = [&](int64_t blocks) { return (double)((blocks + 151) / 152); };
+    // blocks of `each` chunks: in rounds of one an SM, or the generic ones side by side
+    auto time = [&](int64_t blocks, int64_t each, double chunk) {
+        if (tensor) return (double)((blocks + 151) / 152) * (chunk * each + BLOCK);
+        const double full = blocks / SMS, slow = 0.45 + 0.82 * full;
+        return chunk * each * (slow > 1 ? slow : 1) + BLOCK * (full > 1 ? full : 1);
+    };
     if (packed && N > 1) {
         const double chunks = (double)((rows + CK - 1) / CK), each_sm = chunks * walks / SMS;
         const double each = each_sm / 2.5 < 2 * least ? 2 * least : ceil(each_sm / 2.5);
@@ -792,11 +801,11 @@ int lin_segment_chunks(int64_t rows, int64_t N, bool packed, int H, int dc, bool
         return (WALK + STATE) * (each_sm + each / 2) + 2 * BLOCK + JOIN < whole && 2 * each <= chunks ? (int)each : 0;
     }
     const int64_t chunks = (rows / N + CK - 1) / CK;
-    double best = rounds(N * walks) * (WALK * chunks + BLOCK);
+    double best = time(N * walks, chunks, WALK);
     int best_each = 0;
     for (int64_t n = 2; n <= 64 && least * n <= chunks; ++n) {
         const int64_t each = (chunks + n - 1) / n;
-        const double cost = rounds(N * walks * n) * (WALK * each + BLOCK) + rounds(N * walks * (n - 1)) * (STATE * each + BLOCK) + JOIN;
+        const double cost = time(N * walks * n, each, WALK) + time(N * walks * (n - 1), each, STATE) + JOIN;
         if (cost < best) {
             best = cost;
             best_each = (int)each;

@@ -138,6 +138,10 @@ GENERIC = [
     (1, 129, 1, 1, 32, 32, F32, None, "strong", "dense"),
     (1, 2100, 1, 2, 16, 40, F32, [0, 1024, 1024, 1030, 2100], "token", "dense"),     # many chunks, and a border on one
     (2, 1025, 1, 1, 8, 8, F32, None, "head", "dense"),
+    (1, 1000, 1, 2, 40, 72, F32, None, "resets", "dense"),                           # few walks and long ones: in segments
+    (2, 700, 2, 4, 64, 64, BF, None, "strong", "heads"),
+    (1, 1500, 1, 1, 256, 200, F32, [0, 0, 1100, 1100, 1500], "head", "rows"),
+    (1, 1300, 2, 2, 20, 256, F32, [0, 1, 1300], "token", "odd"),
 ]
 
 
