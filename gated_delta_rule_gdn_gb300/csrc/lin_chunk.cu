@@ -29,10 +29,11 @@
 // A row of C that is not finite would reach the tokens before it as 0 times that; it is taken out of P C (not out of the
 // state) and added to the rows that see it.
 //
-// Bound by shared memory: a chunk's operands and what is turned on the way are 336 KB of reads and writes (SPLIT 464), so 2.6 and 3.6
-// thousand cycles at 128 bytes a cycle, of the 3.6 and 5.6 that it takes; 128 walks fill 128 of 152 SMs.  B4, T 4096, 16 heads of 128:
-// forward 71 us (57 % of the copy rate), dq 105, dk 110, dv 71.  Not kept: four warps a role instead of eight (137 us forward),
-// products from a branch of one lane instead of an elected one (70 to 150 cycles each, not 33 to 64), decays in 64 bits.
+// Bound by shared memory first: a chunk's operands and what is turned on the way are 336 KB of reads and writes (SPLIT 464), so 1.3
+// and 1.8 us at 128 bytes a cycle, of the 2.2 and 3.9 that it takes; SPLIT moves the spans' states besides.  128 walks fill 128 of 152
+// SMs.  B4, T 4096, 16 heads of 128: forward 71 us (57 % of the copy rate), dq 126, dk 129, dv 73.  Not kept: four warps a role instead
+// of eight (137 us forward), products from a branch of one lane instead of an elected one (70 to 150 cycles each, not 33 to 64), decays
+// in 64 bits, the spans' states asked for a chunk ahead (backward of 65,536 tokens, 32 heads: 2.63 ms, 2.53 without).
 //
 // The kernels of a call are launched before the one before them has completed, and wait only where they read what it wrote: the walk
 // of dv runs beside that of dk, the sums of pairs beside both, on the SMs that they leave (backward of B4, T 4096, 8 heads: 326 us one

@@ -4,7 +4,7 @@
 // M_ij = scale e^(G_i - G_j) (q_i . k_j) (dO_i . v_j) of the pairs j < i in fp32, summed along its rows (a row a lane) and its
 // columns (over the lanes).  No chunk waits for another, so the bound is reading q, k, v and dO once; the two products share
 // 64 KB of tiles one after the other, so that two blocks and more fit an SM and one loads while the others sum (4 sequences of 4096
-// tokens, 16 heads of 128: 53 us, 40 at the copy rate; inside the walk of the values' gradient the sums took that from 71 to 180).
+// tokens, 16 heads of 128: 54 us, 40 at the copy rate; inside the walk of the values' gradient the sums took that from 71 to 180).
 
 #include "lin_tile.cuh"
 

@@ -5,7 +5,7 @@
 // memory.  Half of its warps bring the next chunk's rows (and the prefix sums of its decays) while the others work: the 32 x 32
 // triangle of decayed products a_i . b_j, the outputs (row i: a_i S and the triangle's row), then the state.  Bound by reads of
 // shared memory, so a thread takes four rows at a time, and four channels an access (2 sequences of 777 tokens, 3 heads of 40, fp32,
-// forward and backward: 1.30 ms a channel and a row at a time, 0.64 now; few walks, so what is left is one block's latency).  The
+// forward and backward: 1.30 ms a channel and a row at a time, 0.64 so, 0.18 in segments; what is left is one block's latency).  The
 // triangle is a loop bound, not a factor, so a value that is not a number reaches no token it should not.
 
 #include "internal.h"
