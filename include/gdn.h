@@ -696,8 +696,9 @@ gdn_status lin_chunk_fwd(const void* q, const void* k, const void* v, const floa
  *   grad_o            [B, T, H, d_v] dtype, contiguous;  grad_final_state [N, H, d_k, d_v] fp32 or NULL (zero)
  *   grad_q, grad_k    [B, T, H_k, d_k] dtype (a key head sums its value heads' parts, in order);
  *   grad_v            [B, T, H, d_v] dtype
- *   grad_g            fp32, the shape of g (with g_per_head the sum over all tokens, in a fixed order); an input that is
- *                     not a number can make those of all tokens of its chunk (of 128) not numbers
+ *   grad_g            fp32, the shape of g; with g_per_head the sum over all tokens, in a fixed order, good to fp32's
+ *                     roundoff of the parts' magnitudes (which the sum itself may be far below); an input that is not a
+ *                     number can make those of all tokens of its chunk (of 128) not numbers
  *   grad_initial_state  [N, H, d_k, d_v] fp32, or NULL
  *   workspace         lin_workspace_size(1, ...) bytes
  */
