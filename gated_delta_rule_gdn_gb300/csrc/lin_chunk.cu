@@ -59,7 +59,11 @@ enum Kind { PLAIN, SPLIT, STATE };
 struct Bars {
     uint64_t full[2], full_c[2], empty[2], empty_c[2], gate_empty[2], raw_full[2], p_ready[2], o_full[2], o_free[2];
     uint64_t ds_full, ds_free, s_ready, vhat;
-    uint32_t flags[2][2][4];                              // rows of C that are not finite, by chunk and half of the columns
+    // Rows of C that are not finite, by chunk, half of the columns and 32 rows.  Four chunks' places: those of chunk c + 4 are
+    // written behind ds_full of c + 2, whose product is issued behind the scores of c + 2 and so behind o_free of c, which the
+    // score warps signal when they have read theirs for the last time.  (Two places would not do: without SPLIT nothing holds the
+    // state warps back until the outputs of the chunk before last are done, and those take long beside such a row.)
+    uint32_t flags[4][2][4];
     lin::Keep keep[2];                                    // of a chunk's whole decay
     uint32_t tmem;
 };
@@ -301,7 +305,7 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
             }
             uint32_t any = 0;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) any |= S.flags[s][i >> 2][i & 3];
+            for (int i = 0; i < 8; ++i) any |= S.flags[c & 3][i >> 2][i & 3];
             F2 dot{0.f, 0.f};
 #pragma unroll
             for (int i = 0; i < 64; i += 16) {
@@ -326,7 +330,7 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
                 if (any)                                  // rows of C that are not finite: into the rows that see them
 #pragma unroll 1
                     for (int j = 0; j < CK; ++j) {
-                        if (!((S.flags[s][i >> 5][j >> 5] >> (j & 31)) & 1)) continue;
+                        if (!((S.flags[c & 3][i >> 5][j >> 5] >> (j & 31)) & 1)) continue;
                         uint32_t pj[16];
                         tmem_ld16(p + j / 32 * 16, pj);
                         tmem_ld_wait();
@@ -523,7 +527,7 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
                     }
             }
             const unsigned bits = __ballot_sync(0xffffffffu, odd && in);
-            if (lane == 0) S.flags[s][half][warp & 3] = bits;
+            if (lane == 0) S.flags[c & 3][half][warp & 3] = bits;
             fence_async_smem();
             arrive(&S.vhat);
             if (!wait(&S.ds_full, c, 64u)) break;
