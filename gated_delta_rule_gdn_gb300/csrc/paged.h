@@ -49,7 +49,17 @@ struct PagedAttnArgs {
     void* ws;
 };
 int paged_attn_splits(const PagedAttnArgs& a);
-size_t paged_attn_workspace_bytes(const PagedAttnArgs& a);
+// The workspace, where sequences have several parts: (maximum, sum) of each (sequence, query head, part), read as pairs and so
+// first, on the workspace's own alignment; then the parts' d channels, whose number may be odd.
+__host__ __device__ inline int64_t paged_attn_tops_at(const PagedAttnArgs& a, int n, int hq, int split) {      // in floats
+    return (((int64_t)n * a.Hq + hq) * a.splits + split) * 2;
+}
+__host__ __device__ inline int64_t paged_attn_sums_at(const PagedAttnArgs& a, int n, int hq, int split) {
+    return (int64_t)a.c.N * a.Hq * a.splits * 2 + (((int64_t)n * a.Hq + hq) * a.splits + split) * a.c.d;
+}
+inline size_t paged_attn_workspace_bytes(const PagedAttnArgs& a) {
+    return a.splits <= 1 ? 0 : sizeof(float) * (size_t)paged_attn_sums_at(a, a.c.N, 0, 0);
+}
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t s);
 
 }  // namespace gdn

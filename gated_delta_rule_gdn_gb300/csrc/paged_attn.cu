@@ -71,10 +71,8 @@ __device__ __forceinline__ void halves(float x, float y, uint32_t& hi, uint32_t&
 struct Part {
     const PagedAttnArgs& a;
     int n, hq, split, parts;
-    __device__ float* sums() const { return static_cast<float*>(a.ws) + (((int64_t)n * a.Hq + hq) * a.splits + split) * a.c.d; }
-    __device__ float* tops() const {
-        return static_cast<float*>(a.ws) + (int64_t)a.c.N * a.Hq * a.splits * a.c.d + (((int64_t)n * a.Hq + hq) * a.splits + split) * 2;
-    }
+    __device__ float* sums() const { return static_cast<float*>(a.ws) + paged_attn_sums_at(a, n, hq, split); }
+    __device__ float* tops() const { return static_cast<float*>(a.ws) + paged_attn_tops_at(a, n, hq, split); }
     template <typename T> __device__ void put(int i, float x, float total) const {
         if (parts > 1) sums()[i] = x;
         else mix::st(static_cast<T*>(a.o) + ((int64_t)n * a.Hq + hq) * a.c.d + i, total > 0.f || total != total ? x / total : 0.f);
@@ -487,11 +485,6 @@ int paged_attn_splits(const PagedAttnArgs& a) {
     int64_t s = least > fill ? least : fill;
     if (s > top) s = top;
     return (int)(s < 1 ? 1 : s > kMaxParts ? kMaxParts : s);
-}
-
-size_t paged_attn_workspace_bytes(const PagedAttnArgs& a) {
-    if (a.splits <= 1) return 0;
-    return (size_t)a.c.N * a.Hq * a.splits * (a.c.d + 2) * sizeof(float);
 }
 
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t s) {

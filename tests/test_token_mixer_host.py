@@ -1,0 +1,50 @@
+"""Host side of the token mixers beside the rule: where their kernels put and find things, at sizes that no test can run.  No GPU
+is needed."""
+import os
+import shutil
+import subprocess
+
+import pytest
+
+from gated_delta_rule_gdn_gb300 import build
+
+
+def compiled(d, text):
+    """A program around the headers that the kernels share; its arguments and results are whole numbers."""
+    (d / "main.cpp").write_text(text)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(build._nvcc())))
+    subprocess.run([shutil.which("g++") or "c++", "-std=c++17", "-fsanitize=undefined", "-fno-sanitize-recover", "-I", os.path.join(cuda, "include"), "-I", build.CSRC, "-I",
+                    build.INCLUDE, str(d / "main.cpp"), "-o", str(d / "run")], check=True)
+    return lambda *args: [int(v) for v in subprocess.run([str(d / "run"), *map(str, args)], check=True, capture_output=True,
+                                                         text=True).stdout.split()]
+
+
+@pytest.fixture(scope="module")
+def places(tmp_path_factory):
+    return compiled(tmp_path_factory.mktemp("places"), r'''
+#include "paged.h"
+#include <cstdio>
+#include <cstdlib>
+int main(int, char** v) {
+    gdn::PagedAttnArgs a{};
+    a.c.N = atoi(v[1]); a.Hq = atoi(v[2]); a.splits = atoi(v[3]); a.c.d = atoi(v[4]);
+    for (int n = 0; n < a.c.N; ++n)
+        for (int h = 0; h < a.Hq; ++h)
+            for (int s = 0; s < a.splits; ++s)
+                printf("%lld %lld\n", (long long)gdn::paged_attn_tops_at(a, n, h, s), (long long)gdn::paged_attn_sums_at(a, n, h, s));
+    printf("%zu\n", gdn::paged_attn_workspace_bytes(a));
+}
+''')
+
+
+@pytest.mark.parametrize("N,Hq,splits,d", [(1, 1, 3, 33), (1, 1, 1, 33), (3, 5, 7, 1), (2, 3, 2, 255), (1, 1, 5, 127), (2, 4, 3, 128)])
+def test_parts_of_the_attention_in_the_workspace(places, N, Hq, splits, d):
+    """Pairs lie on 8 bytes whatever the sizes, and no two pieces overlap."""
+    *at, size = places(N, Hq, splits, d)
+    if splits == 1:
+        assert size == 0
+        return
+    pairs, sums = at[::2], at[1::2]
+    assert all(p % 2 == 0 for p in pairs)
+    used = [e for p in pairs for e in range(p, p + 2)] + [e for s in sums for e in range(s, s + d)]
+    assert len(set(used)) == len(used) and min(used) == 0 and max(used) + 1 == size // 4 and size % 4 == 0
