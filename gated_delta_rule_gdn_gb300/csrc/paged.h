@@ -49,6 +49,17 @@ struct PagedAttnArgs {
     void* ws;
 };
 int paged_attn_splits(const PagedAttnArgs& a);
+// Tokens of one part of a sequence of `len` (2^31 - 256 at most, a multiple of 64 of at least 128), the parts that it has, no more than
+// `splits`, and where one begins (the end of the sequence where there is none).  Written so that no sum passes 31 bits.
+__host__ __device__ inline int paged_attn_part_tokens(int len, int splits) {
+    const int per = len / splits + (len % splits != 0);
+    return per <= 128 ? 128 : (per + 63) / 64 * 64;
+}
+__host__ __device__ inline int paged_attn_parts(int len, int per) { return len / per + (len % per != 0); }
+__host__ __device__ inline int paged_attn_part_begin(int len, int per, int split) {
+    const int64_t at = (int64_t)per * split;
+    return at < len ? (int)at : len;
+}
 // The workspace, where sequences have several parts: (maximum, sum) of each (sequence, query head, part), read as pairs and so
 // first, on the workspace's own alignment; then the parts' d channels, whose number may be odd.
 __host__ __device__ inline int64_t paged_attn_tops_at(const PagedAttnArgs& a, int n, int hq, int split) {      // in floats

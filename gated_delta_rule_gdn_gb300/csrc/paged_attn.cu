@@ -26,11 +26,6 @@ constexpr int WARPS = 4, THREADS = 32 * WARPS, RUN = 16;
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr int kMaxParts = 1024;
 
-// Tokens of one part of a sequence of `len`: a multiple of 64, at least 128
-__host__ __device__ inline int part_tokens(int len, int splits) {
-    const int per = (len + splits - 1) / splits;
-    return per <= 128 ? 128 : (per + 63) / 64 * 64;
-}
 __device__ __forceinline__ int sequence_tokens(const PagedCache& c, int n) {
     const int64_t most = (int64_t)c.max_pages * c.page_size;
     return (int)min(max((int64_t)c.lengths[n], (int64_t)0), min(most, (int64_t)0x7FFFFF00));
@@ -108,8 +103,8 @@ __global__ void __launch_bounds__(THREADS, D == 64 ? 4 : D == 128 ? 3 : 1) paged
     const int tile = (int)(unit % tiles);
     unit /= tiles;
     const int split = (int)(unit % a.splits), n = (int)(unit / a.splits);
-    const int len = sequence_tokens(c, n), per = part_tokens(len, a.splits);
-    const int t0 = split * per, t1 = min(len, t0 + per), parts = (len + per - 1) / per;
+    const int len = sequence_tokens(c, n), per = paged_attn_part_tokens(len, a.splits), parts = paged_attn_parts(len, per);
+    const int t0 = paged_attn_part_begin(len, per, split), t1 = paged_attn_part_begin(len, per, split + 1);
     mix::let_next();
     if (t0 >= t1 && split > 0) return;
     const int rows = min(16, group - tile * 16), hq0 = hk * group + tile * 16;
@@ -133,9 +128,10 @@ __global__ void __launch_bounds__(THREADS, D == 64 ? 4 : D == 128 ? 3 : 1) paged
     // lane l (and l + 16): where token l of a run lies, in 16 bytes from the first key (value), and whether it does
     struct Where { uint32_t k, v; bool in; };
     auto look_up = [&](int run) {
-        const int t = t0 + (warp + run * WARPS) * RUN + (lane & 15);
         Where at{0, 0, false};
-        if (run < mine && t < t1) {
+        if (run >= mine) return at;                                // (past the part, and maybe past 31 bits)
+        const int t = t0 + (warp + run * WARPS) * RUN + (lane & 15);
+        if (t < t1) {
             const int page = c.table[n * c.table_ld + t / c.page_size], slot = t % c.page_size;
             at.in = page >= 0 && page < c.n_pages;
             if (at.in) {
@@ -314,8 +310,8 @@ __global__ void __launch_bounds__(THREADS) paged_attn_generic_kernel(const Paged
     const int tile = (int)(unit % tiles);
     unit /= tiles;
     const int split = (int)(unit % a.splits), n = (int)(unit / a.splits);
-    const int len = sequence_tokens(c, n), per = part_tokens(len, a.splits);
-    const int t0 = split * per, t1 = min(len, t0 + per), parts = (len + per - 1) / per;
+    const int len = sequence_tokens(c, n), per = paged_attn_part_tokens(len, a.splits), parts = paged_attn_parts(len, per);
+    const int t0 = paged_attn_part_begin(len, per, split), t1 = paged_attn_part_begin(len, per, split + 1);
     mix::let_next();
     if (t0 >= t1 && split > 0) return;
     const int heads = min(HEADS, group - tile * HEADS), hq0 = hk * group + tile * HEADS;
@@ -414,7 +410,7 @@ __global__ void __launch_bounds__(THREADS) paged_attn_join_kernel(const PagedAtt
     const PagedCache& c = a.c;
     const int tid = threadIdx.x, lane = tid & 31;
     const int n = blockIdx.x / a.Hq, hq = blockIdx.x % a.Hq;
-    const int len = sequence_tokens(c, n), per = part_tokens(len, a.splits), parts = (len + per - 1) / per;
+    const int len = sequence_tokens(c, n), parts = paged_attn_parts(len, paged_attn_part_tokens(len, a.splits));
     mix::wait_behind();
     if (parts <= 1) return;
     const float* sums = Part{a, n, hq, 0, parts}.sums();

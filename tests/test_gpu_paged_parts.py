@@ -46,3 +46,32 @@ def test_parts_of_odd_sizes(dtype, N, Hq, Hk, d, page, max_pages, lengths):
     gen = torch.Generator().manual_seed(d)
     kc, vc, table = cache_case(gen, N, Hk, d, page, max_pages, dtype)
     check(draw(gen, N, Hq, d, dtype=dtype), kc, vc, table, lengths)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_the_longest_sequences(dtype):
+    """Nearly 2^31 tokens: one page of 2^20 again and again, and a last one whose last hundred tokens have half of the weight.
+
+    A lane adds up to 2^19 terms one after another in fp32, each time off by half a step of the sum: 2^-24 2^19 of it, and as much
+    for the weights' sum."""
+    page, d, repeats, more = 1 << 20, 8, 2046, (1 << 20) - 300
+    gen = torch.Generator().manual_seed(1)
+    kc, vc = draw(gen, 2, page, 1, d, dtype=dtype), draw(gen, 2, page, 1, d, dtype=dtype)
+    q = draw(gen, 1, 1, d, dtype=dtype)
+    tail = slice(more - 100, more)
+    unit = f64(q)[0, 0] / np.linalg.norm(f64(q))
+    kc[1, tail, 0] = torch.tensor(unit * (17 * d ** 0.5 / np.linalg.norm(f64(q)))).to(dtype).cuda()
+    vc[1, tail] = 4
+    kc[1, more:], vc[1, more:] = float("nan"), float("inf")
+    table = torch.zeros(1, repeats + 1, dtype=torch.int32, device="cuda")
+    table[0, -1] = 1
+    length = repeats * page + more
+    assert (1 << 31) - (1 << 21) < length <= (1 << 31) - 256
+    o, lse = gdn.paged_attn_step(q, kc, vc, table, offsets([length]), output_lse=True)
+    p = [np.exp(f64(kc)[i, :n, 0] @ f64(q)[0, 0] * d ** -0.5) for i, n in ((0, page), (1, more))]
+    total = repeats * p[0].sum() + p[1].sum()
+    ref = (repeats * (p[0] @ f64(vc)[0, :, 0]) + p[1] @ f64(vc)[1, :more, 0]) / total
+    share = p[1][-100:].sum() / total
+    assert 0.1 < share < 0.9
+    assert np.abs(f64(o)[0, 0] - ref).max() <= 2.0 ** -23 * 2 ** 19 * np.abs(ref).max() + 2.0 ** -8 * np.abs(ref).max()
+    assert np.abs(f64(lse)[0, 0] - np.log(total)) <= 2.0 ** -24 * 2 ** 19 + 2.0 ** -20

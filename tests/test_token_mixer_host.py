@@ -48,3 +48,31 @@ def test_parts_of_the_attention_in_the_workspace(places, N, Hq, splits, d):
     assert all(p % 2 == 0 for p in pairs)
     used = [e for p in pairs for e in range(p, p + 2)] + [e for s in sums for e in range(s, s + d)]
     assert len(set(used)) == len(used) and min(used) == 0 and max(used) + 1 == size // 4 and size % 4 == 0
+
+
+@pytest.fixture(scope="module")
+def parts(tmp_path_factory):
+    return compiled(tmp_path_factory.mktemp("parts"), r'''
+#include "paged.h"
+#include <cstdio>
+#include <cstdlib>
+int main(int, char** v) {
+    const int len = atoi(v[1]), splits = atoi(v[2]), per = gdn::paged_attn_part_tokens(len, splits);
+    printf("%d %d", per, gdn::paged_attn_parts(len, per));
+    for (int s = 0; s <= splits; ++s) printf(" %d", gdn::paged_attn_part_begin(len, per, s));
+}
+''')
+
+
+MOST = 0x7FFFFF00                       # tokens of a sequence that the entry takes
+
+
+@pytest.mark.parametrize("splits", [1, 2, 3, 7, 304, 1023, 1024])
+@pytest.mark.parametrize("length", [0, 1, 127, 128, 129, 8192, 100_003, (1 << 31) - (1 << 21) - 1, (1 << 31) - (1 << 21) + 1, MOST - 1023, MOST - 65536,
+                                    MOST - 1, MOST])
+def test_parts_of_a_sequence(parts, length, splits):
+    """They cover the sequence in order, whatever its length, and are no more than there are places for."""
+    per, count, *begin = parts(length, splits)
+    assert per >= 128 and per % 64 == 0 and (per == 128 or per - 64 < -(-length // splits))
+    assert count <= splits and count == -(-length // per)
+    assert begin == [min(length, s * per) for s in range(splits + 1)] and begin[-1] == length
