@@ -59,6 +59,8 @@ struct LinWalk {
 constexpr int kLinSpan = 128, kLinGenericChunk = 32, kLinChunk = 128;
 // The span slots of a call: those of sequence n begin at first_token / kLinSpan + n.
 inline int64_t lin_slots(int64_t rows, int64_t N, int64_t size) { return rows / size + N + 1; }
+// Segments of `size` tokens of a sequence of `len` (size + len may pass 31 bits).
+__host__ __device__ inline int lin_segments(int len, int size) { return len / size + (len % size != 0); }
 inline int64_t lin_span_slots(int64_t rows, int64_t N) { return lin_slots(rows, N, kLinSpan); }
 // Columns of c that a block of threads takes (the generic walk, the tensor-core one), for dots and anchors.
 constexpr int kLinGenericCols = 32, kLinCols = 64;

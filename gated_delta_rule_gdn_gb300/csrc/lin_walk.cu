@@ -385,7 +385,7 @@ __global__ void __launch_bounds__(256) lin_generic_segments_kernel(const LinWalk
     int64_t first;
     int len;
     lin::sequence(w.cu, w.T, n, first, len);
-    const int size = w.seg_chunks * kLinChunk, segs = (len + size - 1) / size;
+    const int size = w.seg_chunks * kLinChunk, segs = lin_segments(len, size);
     const int64_t slot0 = first / size + n;
     const int r = e / COLS, c = blk * COLS + e % COLS;
     const bool in = e < elements, inside = in && c < w.dc;
@@ -415,7 +415,7 @@ __global__ void __launch_bounds__(256) lin_segments_kernel(const LinWalk w) {
     int64_t first;
     int len;
     lin::sequence(w.cu, w.T, n, first, len);
-    const int size = w.seg_chunks * kLinChunk, segs = (len + size - 1) / size;
+    const int size = w.seg_chunks * kLinChunk, segs = lin_segments(len, size);
     const int64_t slot0 = first / size + n;
     const int e = part * 1024 + threadIdx.x * 4, row = e / 4 % 128, c = blk * kLinCols + e / 512 * 4;
     const int64_t at = ((int64_t)n * w.H + h) * w.da * w.dc + (int64_t)row * w.s_r;

@@ -76,3 +76,19 @@ def test_parts_of_a_sequence(parts, length, splits):
     assert per >= 128 and per % 64 == 0 and (per == 128 or per - 64 < -(-length // splits))
     assert count <= splits and count == -(-length // per)
     assert begin == [min(length, s * per) for s in range(splits + 1)] and begin[-1] == length
+
+
+@pytest.fixture(scope="module")
+def segments(tmp_path_factory):
+    return compiled(tmp_path_factory.mktemp("segments"), r'''
+#include "lin.h"
+#include <cstdio>
+#include <cstdlib>
+int main(int, char** v) { printf("%d\n", gdn::lin_segments(atoi(v[1]), atoi(v[2]))); }
+''')
+
+
+@pytest.mark.parametrize("size", [128, 512, 57 * 128, 1 << 20, 1 << 25, 1 << 30])
+@pytest.mark.parametrize("length", [0, 1, 127, 128, 129, 4096, (1 << 31) - 65536])
+def test_segments_of_a_sequence(segments, length, size):
+    assert segments(length, size) == [-(-length // size)]
