@@ -62,6 +62,12 @@ __device__ __forceinline__ void halves(float x, float y, uint32_t& hi, uint32_t&
     lo = *reinterpret_cast<const uint32_t*>(&l);
 }
 
+// two bf16 numbers, those that are infinite or no number as 0
+__device__ __forceinline__ uint32_t finite_or_0(uint32_t w) {
+    return (w & 0x7F80u) == 0x7F80u ? (w & 0x7F800000u) == 0x7F800000u ? 0u : w & 0xFFFF0000u
+                                    : (w & 0x7F800000u) == 0x7F800000u ? w & 0xFFFFu : w;
+}
+
 // What a block hands on: o (or a part's unscaled sum) of head `hq`, its maximum (base 2) and sum.
 struct Part {
     const PagedAttnArgs& a;
@@ -159,100 +165,117 @@ __global__ void __launch_bounds__(THREADS, D == 64 ? 4 : D == 128 ? 3 : 1) paged
         mix::copies_close();
     };
 
-    float o[D / 8][4], top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
+    // An infinite value is p infinities.  But the second of the two numbers that p is may be 0 or negative, and the sum of both
+    // products then no number; so where that is what came out, the warp takes its tokens once more, with values that are not
+    // finite left out of the second product.
+    float o[D / 8][4], top[2], sum[2];
+    for (bool apart = false;; apart = true) {
+        top[0] = top[1] = -INFINITY;
+        sum[0] = sum[1] = 0.f;
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i)
+        for (int i = 0; i < D / 8; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
-    // which tokens of a run are there: a bit each, in the order of the runs (STAGES runs are on their way)
-    unsigned there[STAGES];
-    Where at = look_up(0);
+            for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
+        // which tokens of a run are there: a bit each, in the order of the runs (STAGES runs are on their way)
+        unsigned there[STAGES];
+        Where at = look_up(0);
 #pragma unroll
-    for (int s = 0; s < STAGES - 1; ++s) {
-        const Where ahead = look_up(s + 1);
-        there[s] = __ballot_sync(0xffffffffu, at.in) & 0xFFFFu;
-        fill(s, at, there[s]);
-        at = ahead;
-    }
-    const float scale = a.scale * LOG2E;
-    for (int run0 = 0; run0 < mine; run0 += STAGES)
+        for (int s = 0; s < STAGES - 1; ++s) {
+            const Where ahead = look_up(s + 1);
+            there[s] = __ballot_sync(0xffffffffu, at.in) & 0xFFFFu;
+            fill(s, at, there[s]);
+            at = ahead;
+        }
+        const float scale = a.scale * LOG2E;
+        for (int run0 = 0; run0 < mine; run0 += STAGES)
 #pragma unroll
-        for (int st = 0; st < STAGES; ++st) {
-            const int run = run0 + st;
-            if (run >= mine) break;
-            mix::copies_wait<STAGES - 2>();
-            __syncwarp();                                          // (every lane's copies have landed, and the stage filled next is read)
-            constexpr int LAST = STAGES - 1;
-            {
-                const Where ahead = look_up(run + STAGES);
-                there[(st + LAST) % STAGES] = __ballot_sync(0xffffffffu, at.in) & 0xFFFFu;
-                fill(run + LAST, at, there[(st + LAST) % STAGES]);
-                at = ahead;
-            }
-            const uint32_t ks = base + st * R::STAGE, vs = ks + RUN * R::ROW;
-            float x[2][4] = {};                                    // heads lane / 4 and + 8, tokens 8 i + lane % 4 * 2 and + 1
-#pragma unroll
-            for (int s = 0; s < D / 16; ++s) {
-                uint32_t b[4];                                     // tokens 0-7 and 8-15, channels 0-7 and 8-15 of the step
-                ldsm4(b, ks + (lane % 8 + (lane >> 4) * 8) * R::ROW + s * 32 + ((lane >> 3) & 1) * 16);
-                mma16816(x[0], q[s], b[0], b[1]);
-                mma16816(x[1], q[s], b[2], b[3]);
-            }
-            const unsigned live = there[st];
-            float most[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    x[i][j] *= scale;
-                    if (live != 0xFFFFu && !((live >> (8 * i + lane % 4 * 2 + (j & 1))) & 1)) x[i][j] = -INFINITY;
-                    most[j >> 1] = fmaxf(most[j >> 1], x[i][j]);
+            for (int st = 0; st < STAGES; ++st) {
+                const int run = run0 + st;
+                if (run >= mine) break;
+                mix::copies_wait<STAGES - 2>();
+                __syncwarp();                                          // (every lane's copies have landed, and the stage filled next is read)
+                constexpr int LAST = STAGES - 1;
+                {
+                    const Where ahead = look_up(run + STAGES);
+                    there[(st + LAST) % STAGES] = __ballot_sync(0xffffffffu, at.in) & 0xFFFFu;
+                    fill(run + LAST, at, there[(st + LAST) % STAGES]);
+                    at = ahead;
                 }
-            bool more = false;
+                const uint32_t ks = base + st * R::STAGE, vs = ks + RUN * R::ROW;
+                float x[2][4] = {};                                    // heads lane / 4 and + 8, tokens 8 i + lane % 4 * 2 and + 1
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                most[r] = fmaxf(most[r], __shfl_xor_sync(0xffffffffu, most[r], 1));
-                most[r] = fmaxf(most[r], __shfl_xor_sync(0xffffffffu, most[r], 2));
-                more |= most[r] > top[r];
-            }
-            if (__any_sync(0xffffffffu, more)) {
-                float f[2];
+                for (int s = 0; s < D / 16; ++s) {
+                    uint32_t b[4];                                     // tokens 0-7 and 8-15, channels 0-7 and 8-15 of the step
+                    ldsm4(b, ks + (lane % 8 + (lane >> 4) * 8) * R::ROW + s * 32 + ((lane >> 3) & 1) * 16);
+                    mma16816(x[0], q[s], b[0], b[1]);
+                    mma16816(x[1], q[s], b[2], b[3]);
+                }
+                const unsigned live = there[st];
+                float most[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        x[i][j] *= scale;
+                        if (live != 0xFFFFu && !((live >> (8 * i + lane % 4 * 2 + (j & 1))) & 1)) x[i][j] = -INFINITY;
+                        most[j >> 1] = fmaxf(most[j >> 1], x[i][j]);
+                    }
+                bool more = false;
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    const float now = fmaxf(top[r], most[r]);
-                    f[r] = top[r] == now ? 1.f : exp2f(top[r] - now);
-                    top[r] = now;
-                    sum[r] *= f[r];
+                    most[r] = fmaxf(most[r], __shfl_xor_sync(0xffffffffu, most[r], 1));
+                    most[r] = fmaxf(most[r], __shfl_xor_sync(0xffffffffu, most[r], 2));
+                    more |= most[r] > top[r];
                 }
+                if (__any_sync(0xffffffffu, more)) {
+                    float f[2];
 #pragma unroll
-                for (int i = 0; i < D / 8; ++i)
+                    for (int r = 0; r < 2; ++r) {
+                        const float now = fmaxf(top[r], most[r]);
+                        f[r] = top[r] == now ? 1.f : exp2f(top[r] - now);
+                        top[r] = now;
+                        sum[r] *= f[r];
+                    }
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) o[i][j] *= f[j >> 1];
-            }
-            const float zero[2] = {top[0] == -INFINITY ? 0.f : top[0], top[1] == -INFINITY ? 0.f : top[1]};
+                    for (int i = 0; i < D / 8; ++i)
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    x[i][j] = ex2(x[i][j] - zero[j >> 1]);
-                    sum[j >> 1] += x[i][j];
+                        for (int j = 0; j < 4; ++j) o[i][j] *= f[j >> 1];
                 }
-            uint32_t hi[4], lo[4];
-            halves(x[0][0], x[0][1], hi[0], lo[0]);
-            halves(x[0][2], x[0][3], hi[1], lo[1]);
-            halves(x[1][0], x[1][1], hi[2], lo[2]);
-            halves(x[1][2], x[1][3], hi[3], lo[3]);
+                const float zero[2] = {top[0] == -INFINITY ? 0.f : top[0], top[1] == -INFINITY ? 0.f : top[1]};
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-                uint32_t b[4];                                     // tokens 0-7, 8-15 of channels 0-7, then of channels 8-15
-                ldsm4_t(b, vs + (lane % 16) * R::ROW + i * 32 + (lane >> 4) * 16);
-                mma16816(o[2 * i], hi, b[0], b[1]);
-                mma16816(o[2 * i], lo, b[0], b[1]);
-                mma16816(o[2 * i + 1], hi, b[2], b[3]);
-                mma16816(o[2 * i + 1], lo, b[2], b[3]);
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        x[i][j] = ex2(x[i][j] - zero[j >> 1]);
+                        sum[j >> 1] += x[i][j];
+                    }
+                uint32_t hi[4], lo[4];
+                halves(x[0][0], x[0][1], hi[0], lo[0]);
+                halves(x[0][2], x[0][3], hi[1], lo[1]);
+                halves(x[1][0], x[1][1], hi[2], lo[2]);
+                halves(x[1][2], x[1][3], hi[3], lo[3]);
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                    uint32_t b[4];                                     // tokens 0-7, 8-15 of channels 0-7, then of channels 8-15
+                    ldsm4_t(b, vs + (lane % 16) * R::ROW + i * 32 + (lane >> 4) * 16);
+                    mma16816(o[2 * i], hi, b[0], b[1]);
+                    mma16816(o[2 * i + 1], hi, b[2], b[3]);
+                    if (apart)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) b[k] = finite_or_0(b[k]);
+                    mma16816(o[2 * i], lo, b[0], b[1]);
+                    mma16816(o[2 * i + 1], lo, b[2], b[3]);
+                }
             }
-        }
-    mix::copies_wait<0>();
+        mix::copies_wait<0>();
+        bool nan = false;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) nan |= o[i][j] != o[i][j];
+        if (apart || !__any_sync(0xffffffffu, nan)) break;
+        __syncwarp();
+    }
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
         sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 1);

@@ -75,3 +75,41 @@ def test_the_longest_sequences(dtype):
     assert 0.1 < share < 0.9
     assert np.abs(f64(o)[0, 0] - ref).max() <= 2.0 ** -23 * 2 ** 19 * np.abs(ref).max() + 2.0 ** -8 * np.abs(ref).max()
     assert np.abs(f64(lse)[0, 0] - np.log(total)) <= 2.0 ** -24 * 2 ** 19 + 2.0 ** -20
+
+
+@pytest.mark.parametrize("dtype,layout,d,Hq,Hk", [(BF, "dense", 128, 8, 2), (BF, "together", 64, 2, 2), (BF, "dense", 256, 5, 1), (BF, "dense", 80, 20, 1),
+                                                  (BF, "odd", 64, 4, 2), (F32, "dense", 128, 4, 2)])
+@pytest.mark.parametrize("lengths", [[1, 17, 200], [1, 900, 3000]])
+def test_infinite_values_come_out_as_infinite(dtype, layout, d, Hq, Hk, lengths):
+    """On either kernel: an infinity of its sign in the channel that it is in, no number where both signs meet or one of the values
+    is none, and every other channel as ever."""
+    gen = torch.Generator().manual_seed(d + len(lengths))
+    page, max_pages = 16, 200
+    kc, vc, table = cache_case(gen, 3, Hk, d, page, max_pages, dtype, layout)
+    q, inf = draw(gen, 3, Hq, d, dtype=dtype), float("inf")
+    tab = f64(table).astype(int)
+    plain = gdn.paged_attn_step(q, kc, vc, table, offsets(lengths))
+
+    def put(n, t, channel, value):
+        vc[tab[n, t // page], t % page, :, channel] = value
+
+    put(0, 0, 1, inf)                                    # the only token of its sequence, so with p = 1
+    put(0, 0, d - 2, -inf)
+    for n in (1, 2):
+        last = lengths[n] - 1
+        put(n, 0, 0, inf)
+        put(n, last, 3, -inf)
+        put(n, last // 2, 5, inf)                        # twice the same sign
+        put(n, last // 2 + 1, 5, inf)
+        put(n, 2, d - 1, inf)                            # both
+        put(n, last, d - 1, -inf)
+        put(n, last // 3, 6, float("nan"))
+    o = gdn.paged_attn_step(q, kc, vc, table, offsets(lengths))
+    with np.errstate(invalid="ignore"):
+        ref, _ = R.attn(f64(q), f64(kc), f64(vc), tab, lengths, d ** -0.5)
+    x = f64(o)
+    assert not np.isfinite(ref[1:, :, [0, 3, 5, 6, d - 1]]).any()
+    assert np.array_equal(np.isnan(x), np.isnan(ref)) and np.array_equal(np.isposinf(x), np.isposinf(ref)) and np.array_equal(np.isneginf(x), np.isneginf(ref))
+    # (tokens in the order that they were taken in before, and a product left out only where it was of an infinity)
+    fin = torch.from_numpy(np.isfinite(ref)).cuda()
+    assert torch.equal(o[fin], plain[fin])
