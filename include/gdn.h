@@ -677,6 +677,8 @@ gdn_status gdn_short_conv_step(const void* x, const float* weight, const float* 
  *            everything before the token (any below -693 do)
  *   initial_state  [N, H, d_k, d_v] fp32, or NULL for zeros;  final_state the same, or NULL
  *   o        [B, T, H, d_v] dtype (output)
+ * An input that is not finite reaches what the formulas have it reach and nothing else, and makes that not finite.  An infinity may be
+ * a NaN there on either algo: decays and, on the tensor cores, scaled values and states are sums of two numbers of either sign.
  *   sizes    1 <= d_k, d_v <= 256
  *   algo     GDN_ALGO_AUTO, GDN_ALGO_GENERIC (fp32 arithmetic, any type and size) or
  *            GDN_ALGO_TCGEN05 (tensor cores: bf16, d_k up to 128, d_v up to 256 (backward 128) in
@@ -767,6 +769,7 @@ gdn_status paged_append(const void* k, const void* v, const void* q, const gdn_p
  * paged_attn_step -- softmax attention of one new token for each sequence over the cache:
  *     o = sum_j p_j v_j,   p = softmax_j(scale q . k_j),   j over the sequence's tokens.
  * Query head h reads key head h / (H_q / H_k).  A sequence without tokens has o = 0 and lse = -inf.
+ * An infinite value is infinite in o too (a NaN where its p is less than 2^-126, as in fp32's sum of products, or where both signs meet).
  *   q [N, H_q, d] dtype, with strides over sequences and heads;  o [N, H_q, d] dtype
  *   lse         [N, H_q] fp32, or NULL: log of the sum of exp(scale q . k_j)
  *   workspace   paged_attn_workspace_size bytes (the parts of long sequences)

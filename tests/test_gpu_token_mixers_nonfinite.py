@@ -72,3 +72,22 @@ def test_gradients_of_an_early_chunk_in_the_walk_of_the_values(algo, d, places):
     rel, el, parts = limits(algo, 700 + 64 + d)
     near(dv, want[2], "dv", 4 * rel, 4 * el, parts)
     near(dh0, want[4], "dh0", 4 * rel, 4 * el)
+
+
+@pytest.mark.parametrize("algo", ALGOS)
+@pytest.mark.parametrize("T", [700, 4500])                           # (one walk; segments)
+@pytest.mark.parametrize("which", ["q", "k", "v", "initial_state"])
+def test_infinite_inputs_reach_what_the_formula_has_them_reach(algo, T, which):
+    """Whatever becomes of an infinity on the way, the same results are finite as by the definition, and those are right."""
+    x, kw, gen, N = lin_case(40, 1, T, 1, 1, 64, 64)
+    x, kw = {n: t.clone() for n, t in x.items()}, dict(kw, initial_state=kw["initial_state"].clone())
+    if which == "initial_state":
+        kw[which][0, 0, 7, 50] = float("inf")
+    else:
+        x[which][0, 70, 0, 50] = -float("inf")
+    o, hT = gdn.lin_chunk_fwd(x["q"], x["k"], x["v"], x["g"], output_final_state=True, algo=algo, **kw)
+    with np.errstate(invalid="ignore"):
+        o_ref, h_ref, _ = R.lin_fwd(*(f64(x[n]) for n in "qkvg"), 64 ** -0.5, f64(kw["initial_state"]))
+    rel, el, parts = limits(algo, T + 128)
+    near(o, o_ref, "o", rel, el, parts)
+    near(hT, h_ref, "state", rel, el)
