@@ -15,6 +15,8 @@
 // and three blocks an SM, or three and two, are the same there.)
 // Anything else: a warp a token at a time, lanes along the channels, fp32.
 
+#include <type_traits>
+
 #include "mixer_common.cuh"
 #include "paged.h"
 
@@ -169,7 +171,7 @@ __global__ void __launch_bounds__(THREADS, D == 64 ? 4 : D == 128 ? 3 : 1) paged
     // products then no number; so where that is what came out, the warp takes its tokens once more, with values that are not
     // finite left out of the second product.
     float o[D / 8][4], top[2], sum[2];
-    for (bool apart = false;; apart = true) {
+    auto take = [&](auto apart) {
         top[0] = top[1] = -INFINITY;
         sum[0] = sum[1] = 0.f;
 #pragma unroll
@@ -260,7 +262,7 @@ __global__ void __launch_bounds__(THREADS, D == 64 ? 4 : D == 128 ? 3 : 1) paged
                     ldsm4_t(b, vs + (lane % 16) * R::ROW + i * 32 + (lane >> 4) * 16);
                     mma16816(o[2 * i], hi, b[0], b[1]);
                     mma16816(o[2 * i + 1], hi, b[2], b[3]);
-                    if (apart)
+                    if (apart.value)
 #pragma unroll
                         for (int k = 0; k < 4; ++k) b[k] = finite_or_0(b[k]);
                     mma16816(o[2 * i], lo, b[0], b[1]);
@@ -268,14 +270,15 @@ __global__ void __launch_bounds__(THREADS, D == 64 ? 4 : D == 128 ? 3 : 1) paged
                 }
             }
         mix::copies_wait<0>();
-        bool nan = false;
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) nan |= o[i][j] != o[i][j];
-        if (apart || !__any_sync(0xffffffffu, nan)) break;
         __syncwarp();
-    }
+    };
+    take(std::false_type{});
+    bool nan = false;
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) nan |= o[i][j] != o[i][j];
+    if (__any_sync(0xffffffffu, nan)) take(std::true_type{});
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
         sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 1);
