@@ -50,6 +50,7 @@ struct LinWalk {
     int seg_chunks;
     float *seg_states, *seg_kept;
     int test_stall;         // test of the bounded waits: the copies of c are left out
+    int fine;               // scaled values of the state as three bf16 numbers instead of two (walks that sum up a constant decay's gradient)
     int wait_first;         // the kernel before it has to be complete (walks are launched before it is)
     __host__ __device__ int N() const { return cu ? n_seqs : B; }
     __host__ __device__ int64_t rows() const { return (int64_t)B * T; }

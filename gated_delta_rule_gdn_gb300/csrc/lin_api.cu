@@ -263,6 +263,7 @@ gdn_status lin_chunk_bwd(const void* q, const void* k, const void* v, const floa
     if (T > 0)
         GDN_TRY(choose(fn, algo, z, gdn::lin_tensor_fits(wq) && gdn::lin_tensor_fits(wk) && gdn::lin_tensor_fits(wv) &&
                        aligned(grad_q, 16) && aligned(grad_k, 16), tensor));
+    wq.fine = wk.fine = g_per_head != 0;
     parts.segments.put(wq, base, tensor, parts.segments.bwd);
     parts.segments.put(wk, base, tensor, parts.segments.bwd);
     parts.segments.put(wv, base, tensor, parts.segments.fwd);

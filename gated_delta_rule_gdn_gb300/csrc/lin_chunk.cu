@@ -23,8 +23,12 @@
 // exponential for a column instead of 32 (rev: the other way round).  G is kept as the sum of two floats.
 //
 // Roundings: P and (without dots) the state as an operand go once to bf16, as the result does; scaled values always, and
-// the state where an fp32 result comes of it, are the sum of two bf16 numbers (2^-18), in two products, the smaller first (the
-// tensor cores' fp32 sums lose a little at every step, in proportion to the sum).
+// the state where an fp32 result comes of it, are the sum of two bf16 numbers (2^-17), in two products, the smaller first (the
+// tensor cores' fp32 sums lose a little at every step, in proportion to the sum).  That leaves a state off by 4e-6 of its size.  In
+// the walks behind the gradient of a constant decay (FINE), where the inner products of states enter for 128 tokens at once and
+// their sum may be far below them, scaled values are three bf16 numbers, the third in the place of the state's operand once A S
+// has read it: that gradient was off by up to 1.9e-5 of itself in 24 draws of B4, T 4096, 16 heads, and is by up to 3.6e-6; backward
+// 356 -> 383 us there.  In the other walks it would cost more than it gives (forward 71 -> 99 us).
 //
 // A row of C that is not finite would reach the tokens before it as 0 times that; it is taken out of P C (not out of the
 // state) and added to the rows that see it.
@@ -55,10 +59,11 @@ constexpr int THREADS = 640;
 // A walk; one that also takes inner products of its rows with x, for which the state as an operand is exact enough (SPLIT); or
 // the state alone (STATE), of a segment from nothing.
 enum Kind { PLAIN, SPLIT, STATE };
+// s_ready, s_read: the state's operand is written, and read by A S; vhat, third: the scaled values are
 
 struct Bars {
     uint64_t full[2], full_c[2], empty[2], empty_c[2], gate_empty[2], raw_full[2], p_ready[2], o_full[2], o_free[2];
-    uint64_t ds_full, ds_free, s_ready, vhat;
+    uint64_t ds_full, ds_free, s_ready, s_read, vhat, third;
     // Rows of C that are not finite, by chunk, half of the columns and 32 rows.  Four chunks' places: those of chunk c + 4 are
     // written behind ds_full of c + 2, whose product is issued behind the scores of c + 2 and so behind o_free of c, which the
     // score warps signal when they have read theirs for the last time.  (Two places would not do: without SPLIT nothing holds the
@@ -99,7 +104,7 @@ __device__ __forceinline__ uint32_t fma_bf(uint32_t a, uint32_t b, uint32_t c) {
     asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
     return r;
 }
-template <bool REV, Kind KIND>
+template <bool REV, Kind KIND, bool FINE>
 __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_constant__ LinMaps maps, const LinWalk w) {
     using M = Map<KIND>;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -165,7 +170,9 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
         mbar_init(&S.ds_full, 1);
         mbar_init(&S.ds_free, 8);
         mbar_init(&S.s_ready, 8);
+        mbar_init(&S.s_read, 1);
         mbar_init(&S.vhat, 8);
+        mbar_init(&S.third, 8);
         fence_mbar_init();
     }
     if (w.wait_first) mix::wait_behind();                 // (before any wait that is counted)
@@ -490,19 +497,24 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
             for (int i = 0; i < 4; ++i) {
                 const uint32_t at = row * 128 + (((4 * half + i) ^ (row & 7)) << 4);
                 const uint32_t word[4] = {cv[i].x, cv[i].y, cv[i].z, cv[i].w};
-                uint32_t hi[4], lo[4];
+                uint32_t hi[4], lo[4], third[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     top = most(top, word[k]);
                     hi[k] = mul_bf(word[k], f1);
                     const uint32_t rest = fma_bf(word[k], f1, hi[k] ^ 0x80008000u);
-                    if (KIND == SPLIT) {                  // (f2 has eight bits too; the decays' gradient wants more)
+                    if (KIND == SPLIT || FINE) {          // (f2 has eight bits too; the decays' gradient wants more)
                         const F2 l = fma2(F2{low(word[k]), high(word[k])}, F2{f_rest, f_rest}, F2{low(rest), high(rest)});
                         lo[k] = bf2(l.x, l.y);
+                        if (FINE) {
+                            const F2 left = add2(l, F2{-low(lo[k]), -high(lo[k])});
+                            third[k] = bf2(left.x, left.y);
+                        }
                     } else {
                         lo[k] = fma_bf(word[k], f2, rest);
                     }
                 }
+                if (FINE) cv[i] = make_uint4(third[0], third[1], third[2], third[3]);
                 sts128(base + M::V + at, hi[0], hi[1], hi[2], hi[3]);
                 sts128(base + M::V + 16384 + at, lo[0], lo[1], lo[2], lo[3]);
             }
@@ -525,11 +537,27 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
                         for (int k = 0; k < 4; ++k) z[k] = bf2(finite_or_0(low(word[k])), finite_or_0(high(word[k])));
                         sts128(at, z[0], z[1], z[2], z[3]);
                     }
+                if (FINE && odd)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t word[4] = {cv[i].x, cv[i].y, cv[i].z, cv[i].w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) word[k] = bf2(finite_or_0(low(word[k])), finite_or_0(high(word[k])));
+                        cv[i] = make_uint4(word[0], word[1], word[2], word[3]);
+                    }
             }
             const unsigned bits = __ballot_sync(0xffffffffu, odd && in);
             if (lane == 0) S.flags[c & 3][half][warp & 3] = bits;
             fence_async_smem();
             arrive(&S.vhat);
+            if (FINE) {                                   // the third part in the state's place, which A S has read
+                if (KIND != STATE && !wait(&S.s_read, c, 1u << 13)) break;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    sts128(base + M::S + row * 128 + (((4 * half + i) ^ (row & 7)) << 4), cv[i].x, cv[i].y, cv[i].z, cv[i].w);
+                fence_async_smem();
+                arrive(&S.third);
+            }
             if (!wait(&S.ds_full, c, 64u)) break;
             tc_fence_after();
             {
@@ -621,6 +649,7 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
         if (chunks > 0) {
             constexpr uint32_t id_raw = idesc_f16(128, 128, true, false, false);   // A (K-major) x B (K-major)
             constexpr uint32_t id_ds = idesc_f16(128, 128, true, true, true);      // B^T (MN-major) x scaled C (MN-major)
+            constexpr uint32_t id_third = idesc_f16(128, 64, true, true, true);
             constexpr uint32_t id_oi = idesc_f16(128, 64, true, false, true);      // A (K-major) x S (MN-major); P (TMEM) x C
             const bool wide = w.da > 64;                  // (the second half of the channels is all zeros else)
             const uint64_t v = sdesc(base + M::V, 16384, 1024), so = sdesc(base + M::S, 16384, 1024);
@@ -655,6 +684,7 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
 #pragma unroll
                             for (int k = 4; k < 8; ++k) mma_f16(d, a + 1024 + (k - 4) * 2, so + part * 1024 + k * 128, id_oi, 1u);
                     }
+                    if (FINE) mma_commit(&S.s_read);
                 }
                 __syncwarp();
             };
@@ -667,10 +697,21 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
                 if (KIND != STATE) inter(c);
                 if (!ok || !wait(&S.vhat, c, 1u << 11) || (c > 0 && !wait(&S.ds_free, c - 1, 1u << 12))) break;
                 tc_fence_after();
+                if (FINE) {
+                    const uint64_t bt = bt0 + s * NEXT;
+                    if (elected())
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) mma_f16(tmem + M::DS, bt + k * 128, v + k * 128, id_ds, k > 0);
+                    __syncwarp();
+                    if (!wait(&S.third, c, 1u << 18)) break;
+                    tc_fence_after();
+                }
                 if (elected()) {
                     const uint64_t bt = bt0 + s * NEXT;
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) mma_f16(tmem + M::DS, bt + k * 128, v + k * 128, id_ds, k > 0);
+                    for (int k = 0; k < 8; ++k)           // (the third part onto the second's)
+                        if (FINE) mma_f16(tmem + M::DS + 64, bt + k * 128, so + k * 128, id_third, 1u);
+                        else mma_f16(tmem + M::DS, bt + k * 128, v + k * 128, id_ds, k > 0);
                     if (KIND == STATE) mma_commit(&S.empty_c[s]);
                     mma_commit(&S.ds_full);               // (of both products: the state's operand has been read too)
                     mma_commit(&S.empty[s]);
@@ -836,15 +877,20 @@ cudaError_t launch_lin_walk_tensor(const LinWalk& given, bool behind, cudaStream
     };
     if (w.seg_chunks > 0) {
         w.wait_first = 0;
-        cudaError_t e = w.rev ? start(lin_chunk_kernel<true, STATE>, Map<STATE>::BYTES, behind) : start(lin_chunk_kernel<false, STATE>, Map<STATE>::BYTES, behind);
+        cudaError_t e = w.fine ? w.rev ? start(lin_chunk_kernel<true, STATE, true>, Map<STATE>::BYTES, behind)
+                                       : start(lin_chunk_kernel<false, STATE, true>, Map<STATE>::BYTES, behind)
+                               : w.rev ? start(lin_chunk_kernel<true, STATE, false>, Map<STATE>::BYTES, behind)
+                                       : start(lin_chunk_kernel<false, STATE, false>, Map<STATE>::BYTES, behind);
         if (e == cudaSuccess) e = launch_lin_segments(w, s);
         if (e != cudaSuccess) return e;
         behind = true;
     }
     w.wait_first = behind && (w.spans || w.seg_chunks > 0);
+    if (w.dots && w.fine)
+        return w.rev ? start(lin_chunk_kernel<true, SPLIT, true>, Map<SPLIT>::BYTES, behind) : start(lin_chunk_kernel<false, SPLIT, true>, Map<SPLIT>::BYTES, behind);
     if (w.dots)
-        return w.rev ? start(lin_chunk_kernel<true, SPLIT>, Map<SPLIT>::BYTES, behind) : start(lin_chunk_kernel<false, SPLIT>, Map<SPLIT>::BYTES, behind);
-    return w.rev ? start(lin_chunk_kernel<true, PLAIN>, Map<PLAIN>::BYTES, behind) : start(lin_chunk_kernel<false, PLAIN>, Map<PLAIN>::BYTES, behind);
+        return w.rev ? start(lin_chunk_kernel<true, SPLIT, false>, Map<SPLIT>::BYTES, behind) : start(lin_chunk_kernel<false, SPLIT, false>, Map<SPLIT>::BYTES, behind);
+    return w.rev ? start(lin_chunk_kernel<true, PLAIN, false>, Map<PLAIN>::BYTES, behind) : start(lin_chunk_kernel<false, PLAIN, false>, Map<PLAIN>::BYTES, behind);
 }
 
 cudaError_t lin_read_and_clear_status(unsigned* value, bool clear) {
