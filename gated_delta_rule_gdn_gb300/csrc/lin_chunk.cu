@@ -424,10 +424,9 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
             }
         }
         lin::Log2 kept{0.f, 0.f};                         // the log of what is kept of what enters (STATE)
+        static_assert(kLinSpan == CK, "a span is a chunk");
         const int64_t slot0 = first / kLinSpan + n;
-        auto span_at = [&](int ch) {
-            return w.spans + (((slot0 + ch / (kLinSpan / CK)) * w.H + h) * blocks + blk) * (int64_t)(128 * NB);
-        };
+        auto span_at = [&](int ch) { return w.spans + (((slot0 + ch) * w.H + h) * blocks + blk) * (int64_t)(128 * NB); };
         auto operand = [&] {                              // S as an operand: rows of 64 columns, 128-byte swizzle
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -452,8 +451,7 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
         for (int c = 0; c < chunks; ++c) {
             const int s = c & 1, L = rows_of(c), ch = chunk_of(c);
             const uint32_t tile = base + s * M::STAGE;
-            const bool starts_span = KIND == SPLIT && w.spans && ch % (kLinSpan / CK) == 0;
-            if (starts_span && !REV) {                    // a span's first chunk: the state goes out
+            if (KIND == SPLIT && !REV) {                  // the state goes out
                 float* dst = span_at(ch);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) *quad(dst, 4 * i) = make_float4(st[4 * i], st[4 * i + 1], st[4 * i + 2], st[4 * i + 3]);
@@ -464,7 +462,7 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
             arrive(&S.gate_empty[s]);
             if (KIND == STATE) kept = lin::add(kept, {eh, el});
             const float f = w.s_state * (REV ? exp2f(gh + gl) : exp2f((eh - gh) + (el - gl)));
-            if (starts_span && REV) {                     // or is multiplied with the one that did
+            if (KIND == SPLIT && REV) {                   // or is multiplied with the one that did
                 float* src = span_at(ch);
                 float sum = 0.f;
 #pragma unroll
@@ -477,7 +475,7 @@ __global__ void __launch_bounds__(THREADS, 1) lin_chunk_kernel(const __grid_cons
                 }
                 for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
                 if (lane == 0)
-                    w.anchors[(((slot0 + ch / (kLinSpan / CK)) * w.H + h) * blocks + blk) * 8 + (warp - 8)] = keep.hi * sum;
+                    w.anchors[(((slot0 + ch) * w.H + h) * blocks + blk) * 8 + (warp - 8)] = keep.hi * sum;
             }
             if (!wait(&S.full_c[s], c >> 1, 16u)) break;
             uint32_t top = 0;                             // the largest magnitudes

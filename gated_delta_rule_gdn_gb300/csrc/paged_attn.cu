@@ -5,7 +5,8 @@
 // Bound by reading every key and value once.  The tokens of a sequence are divided into parts (paged_attn_splits), a block of
 // four warps for each (sequence, key head, part), and a second kernel joins the parts of a sequence that has more than one.
 //
-// bf16, head sizes in steps of 16: a warp takes every fourth run of 16 tokens, with no barrier between warps: its own ring of
+// bf16, head sizes in steps of 8 (as 64, 128 or 256 channels, zeros behind the last), pages, slots and heads of the cache on 16 bytes, q
+// on 4, and places within 2^32 pieces of 16 bytes: a warp takes every fourth run of 16 tokens, with no barrier between warps: its own ring of
 // STAGES runs in shared memory, filled by 16-byte asynchronous copies (a lane looks up a token's page one run ahead), the
 // scores from m16n8k16 products with up to 16 heads of a group as rows, and p as the sum of two bf16 numbers for the product
 // with the values (one would add an error as large as the result's own rounding; the second product is hidden behind memory).
