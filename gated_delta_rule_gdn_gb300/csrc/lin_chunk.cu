@@ -33,15 +33,17 @@
 // A row of C that is not finite would reach the tokens before it as 0 times that; it is taken out of P C (not out of the
 // state) and added to the rows that see it.
 //
-// Bound by shared memory first: a chunk's operands and what is turned on the way are 336 KB of reads and writes (SPLIT 464), so 1.3
-// and 1.8 us at 128 bytes a cycle, of the 2.2 and 3.9 that it takes; SPLIT moves the spans' states besides.  128 walks fill 128 of 152
-// SMs.  B4, T 4096, 16 heads of 128: forward 71 us (57 % of the copy rate), dq 126, dk 129, dv 73.  Not kept: four warps a role instead
+// What bounds it: no unit alone.  A chunk's operands and what is turned on the way are 336 KB of reads and writes of shared memory (SPLIT
+// 464, FINE 528), so 1.3, 1.8 and 2.1 us at 128 bytes a cycle, of the 2.2, 3.9 and 4.4 that it takes; tensor pipe 38, 25 and 26 %, issue 44,
+// 41 and 40 %, DRAM 43, 44 and 39 %.  The rest is what the roles wait for one another; it has not been taken apart.  128 walks fill 128 of
+// 152 SMs.  B4, T 4096, 16 heads of 128: forward 71 us (58 % of the copy rate), dq 122, dk 130, dv 73 (FINE: dq 139, dk 145).  Not kept:
+// four warps a role instead
 // of eight (137 us forward), products from a branch of one lane instead of an elected one (70 to 150 cycles each, not 33 to 64), decays
 // in 64 bits, the spans' states asked for a chunk ahead (backward of 65,536 tokens, 32 heads: 2.63 ms, 2.53 without).
 //
 // The kernels of a call are launched before the one before them has completed, and wait only where they read what it wrote: the walk
-// of dv runs beside that of dk, the sums of pairs beside both, on the SMs that they leave (backward of B4, T 4096, 8 heads: 326 us one
-// after another, 251 so; of 1000 tokens, 16 heads: 112 and 82; B4, T 4096, 16 heads: 391 and 372).
+// of dv runs beside that of dk, the sums of pairs beside both, on the SMs that they leave (backward of B4, T 4096, 8 heads: 332 us one
+// after another, 253 so; of 1000 tokens, 16 heads: 114 and 82; B4, T 4096, 16 heads: 390 and 352, with a constant decay 411 and 380).
 
 #include <cmath>
 

@@ -998,7 +998,7 @@ PyMethodDef methods[] = {
         "Softmax attention of one new token for each sequence over a paged cache (C ABI paged_attn_step); returns o [N, H_q, d],\n"
         "and with output_lse the log of the softmax's sum [N, H_q] fp32.\n\n"
         "q [N, H_q, d], H_q a multiple of H_k; the cache as in paged_append; scale d ** -0.5.  A sequence of length 0 has o = 0\n"
-        "and lse = -inf."),
+        "and lse = -inf.  Work is divided by the table's width: cut it to the longest sequence, block_table[:, :pages]."),
     GDN_METHOD(spacing, "spacing(t, heads=False)\n--\n\nThe strides that the entries pass on for a strided tensor."),
     {"init", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_init)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};

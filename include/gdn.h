@@ -701,6 +701,7 @@ gdn_status lin_chunk_fwd(const void* q, const void* k, const void* v, const floa
  *   grad_g            fp32, the shape of g; with g_per_head the sum over all tokens, in a fixed order, good to fp32's
  *                     roundoff of the parts' magnitudes (which the sum itself may be far below); an input that is not a
  *                     number can make those of all tokens of its chunk (of 128) not numbers
+ *                     (seen on the tensor cores: 2^-21 of the sum of those magnitudes)
  *   grad_initial_state  [N, H, d_k, d_v] fp32, or NULL
  *   workspace         lin_workspace_size(1, ...) bytes
  */
@@ -773,6 +774,8 @@ gdn_status paged_append(const void* k, const void* v, const void* q, const gdn_p
  *   q [N, H_q, d] dtype, with strides over sequences and heads;  o [N, H_q, d] dtype
  *   lse         [N, H_q] fp32, or NULL: log of the sum of exp(scale q . k_j)
  *   workspace   paged_attn_workspace_size bytes (the parts of long sequences)
+ * The division of sequences into parts, and the workspace, go by max_pages * page_size: a table cut to the longest sequence's pages (its
+ * rows may lie further apart than max_pages) is the fast one.
  */
 gdn_status paged_attn_step(const void* q, const gdn_paged_cache* cache, float scale, void* o, float* lse, int H_q,
                            int64_t q_token_stride, int64_t q_head_stride, void* workspace, size_t workspace_bytes, void* stream);
