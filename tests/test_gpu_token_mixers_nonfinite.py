@@ -91,3 +91,23 @@ def test_infinite_inputs_reach_what_the_formula_has_them_reach(algo, T, which):
     rel, el, parts = limits(algo, T + 128)
     near(o, o_ref, "o", rel, el, parts)
     near(hT, h_ref, "state", rel, el)
+
+
+@pytest.mark.parametrize("algo", ALGOS)
+@pytest.mark.parametrize("gate", ["token", "head"])                  # (scaled values as two numbers; as three)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("which", ["q", "k"])
+@pytest.mark.parametrize("T", [700, 4400])                           # (one walk; segments)
+def test_gradients_beside_queries_and_keys_that_are_not_finite(algo, gate, d, which, T):
+    """A query reaches the keys' and values' gradients of the tokens before it, a key the queries' behind it and its own value's."""
+    x, kw, gen, N = lin_case(50 + d, 1, T, 1, 1, d, 64, gate=gate)
+    x = {n: t.clone() for n, t in x.items()}
+    places = [130, 300, 511]
+    bad_values(x[which], [T - 1 - t for t in places] if which == "q" else places, d)
+    do, dhT = draw(gen, 1, T, 1, 64, dtype=BF), draw(gen, N, 1, d, 64)
+    got = gdn.lin_chunk_bwd(x["q"], x["k"], x["v"], x["g"], do, d_final_state=dhT, algo=algo, **kw)
+    with np.errstate(invalid="ignore"):
+        want = R.lin_bwd(*(f64(x[n]) for n in "qkvg"), f64(do), d ** -0.5, f64(kw["initial_state"]), f64(dhT))
+    rel, el, parts = limits(algo, T + 64 + d)
+    for name, i, p in (("dq", 0, parts), ("dk", 1, parts), ("dv", 2, parts), ("dh0", 4, 0.0)):
+        near(got[i], want[i], name, 4 * rel, 4 * el, p)
